@@ -22,7 +22,8 @@
  *    optional device word `err` with atomicOr; read it after synchronising.
  *  - Outputs are never pre-cleared: cells a call does not define (scores
  *    beyond the causal boundary) keep whatever the caller put there.
- *  - fp16 values are passed as uint16_t bit patterns (IEEE binary16).
+ *  - fp16 values are passed as uint16_t bit patterns (IEEE binary16); where a
+ *    call takes several types, as void* beside a qsa_dtype.
  *  - No C++ exception crosses this boundary.
  */
 #ifndef QSA_H
@@ -47,8 +48,9 @@ typedef enum {
 /* Bits of the device error word. */
 #define QSA_DEVERR_BAD_ID 1u   /* an id < -1 or >= cache_cells was seen and treated as padding */
 #define QSA_DEVERR_TIMEOUT 2u  /* a bounded wait gave up; that launch's outputs are incomplete */
+#define QSA_DEVERR_NO_PAGES 4u /* qsa_page_update: a row did not get the pages, table columns or slots it asked for */
 
-typedef enum { QSA_F32 = 0, QSA_F16 = 1 } qsa_dtype;
+typedef enum { QSA_F32 = 0, QSA_F16 = 1, QSA_BF16 = 2 /* paged calls only */ } qsa_dtype;
 
 /*
  * qsa_prep -- "Round 36 Track C: qsa_prep Single-Barrier norm_rope & w == 128
@@ -296,6 +298,220 @@ qsa_status qsa_fill_ids_even(int ntok, int pos0, int width, int select, int32_t 
 qsa_status qsa_prep(const qsa_prep_args *args, void *stream);
 qsa_status qsa_score(const qsa_score_args *args, void *stream);
 qsa_status qsa_attn(const qsa_attn_args *args, void *stream);
+
+/*
+ * The paged cache.  Several sequences share one pool of pages, each page
+ * page_size cells of all KV heads, in the cache format of qsa_prep and
+ * qsa_attn:
+ *   kq, vq   int8 [n_layers, n_pages, page_size, n_kv_heads, head_dim]
+ *   ksc, vsc fp16 [n_layers, n_pages, page_size, n_kv_heads, 4]
+ * One layer of it is a qsa_attn cache of n_pages * page_size cells.  Cell c of
+ * row r (a sequence) is pool cell
+ *   page_table[r, c / page_size] * page_size + c % page_size
+ * for c < seq_lens[r]; page_table is int32 [rows, max_pages], seq_lens int32
+ * [rows].  A page may belong to several rows (a fork); the pages that no row
+ * holds are free.
+ * Supported: (head_dim 128, group 32) or (head_dim 256, group 64);
+ * page_size 16, 32, 64, 128 or 256; n_pages * page_size below 2^31.
+ * The page calls keep the whole state in the caller's device buffers and never
+ * synchronise, so a decode loop (update, prep, attention) can be captured in a
+ * graph.  The pages have no counterpart to these calls; they extend the path
+ * of the pages to many sequences.
+ */
+
+/*
+ * qsa_paged_prep -- the new tokens of any number of sequences: per-head RMS
+ * norm of queries and keys, rotation of both, and the quantised K/V rows
+ * written to their slots.
+ *
+ * For token t at position p = positions[t], each query and key head row x:
+ *   y = (x / sqrt(mean(x^2) + eps)) * w     with w = q_norm_w / k_norm_w;
+ *                                           a NULL weight leaves y = x
+ *   pairs (i, j), i < rope_dims/2: (i, i + rope_dims/2), or with interleaved
+ *   = 1 (2i, 2i + 1); a = p * inv_freq[i], exact to about 1e-7 at any p:
+ *     y'[i] = rope_mscale * (y[i] cos a - y[j] sin a)
+ *     y'[j] = rope_mscale * (y[j] cos a + y[i] sin a)
+ * dims from rope_dims on keep y.  q_out[t] = y' rounded to q_out_dtype.  Key
+ * rows y' and value rows v_in are quantised per group as in qsa_prep, s =
+ * fp16(max|.|/127), code = clamp(rint(./s), -127, 127), into pool cell
+ * slots[t].  A group that holds a NaN, or a value beyond 127 * 65504, gets a
+ * NaN or infinite scale, so that it reads back as NaN.
+ * slots[t] = -1 marks a padding token: nothing of it is read or written.
+ * Another slot outside [0, cache_cells) is treated so too and sets
+ * QSA_DEVERR_BAD_ID.  No two tokens may have the same slot.
+ *
+ * in_dtype (QSA_F32, QSA_F16 or QSA_BF16) is the type of q_in [ntok,
+ * n_q_heads, head_dim] and k_in, v_in [ntok, n_kv_heads, head_dim]; heads are
+ * contiguous, tokens are q_stride / k_stride / v_stride elements apart (so
+ * the three may be views of one projection).  q_norm_w, k_norm_w fp32
+ * [head_dim] or NULL; inv_freq fp32 [rope_dims/2] (non-negative and finite;
+ * a context stretched by any rule comes in here), NULL with rope_dims 0;
+ * positions, slots int32 [ntok], positions >= 0; q_out [ntok, n_q_heads,
+ * head_dim] in q_out_dtype (QSA_F16 or QSA_BF16).
+ * rope_dims is a multiple of head_dim/16 in [0, head_dim].  Inputs, weights,
+ * q_out, kq and vq 16-byte aligned, token strides multiples of 16 bytes; ksc,
+ * vsc 8-byte.  At most 32767 heads of each kind.
+ */
+typedef struct {
+    int ntok, n_q_heads, n_kv_heads, head_dim, group, rope_dims, interleaved, cache_cells;
+    int in_dtype, q_out_dtype;
+    float eps, rope_mscale;
+    const void *q_in, *k_in, *v_in;
+    int64_t q_stride, k_stride, v_stride;
+    const float *q_norm_w, *k_norm_w, *inv_freq;
+    const int32_t *positions, *slots;
+    void *q_out;
+    int8_t *kq, *vq;
+    uint16_t *ksc, *vsc;
+    unsigned int *err;
+} qsa_paged_prep_args;
+
+/*
+ * qsa_paged_gather -- cached rows read back as the values they stand for:
+ *   k_out[i, h, d] = ksc[c, h, d/group] * kq[c, h, d], v_out likewise,
+ * one rounding to out_dtype, for i < n_ids.  With page_table (then rows too),
+ * c is cell ids[i] of row rows[i]; without, c = ids[i] is a pool cell (as
+ * qsa_page_update's slots are).  ids[i] = -1 gives +0; an id < -1 or past the
+ * row's table or the pool, a row outside [0, n_rows) or a table entry outside
+ * the pool gives +0 and sets QSA_DEVERR_BAD_ID.
+ *
+ * kq, vq [cache_cells, n_kv_heads, head_dim] int8, ksc, vsc fp16 (one layer
+ * of the pool); ids, rows int32 [n_ids]; page_table int32 [n_rows,
+ * max_pages]; k_out, v_out [n_ids, n_kv_heads, head_dim] in out_dtype
+ * (QSA_F32, QSA_F16 or QSA_BF16).  page_size is read only with page_table.
+ * kq, vq, k_out, v_out 16-byte aligned; ksc, vsc 8-byte; the rest 4-byte.
+ */
+typedef struct {
+    int n_ids, n_kv_heads, head_dim, group, cache_cells, page_size, n_rows, max_pages;
+    int out_dtype;
+    const int8_t *kq, *vq;
+    const uint16_t *ksc, *vsc;
+    const int32_t *ids, *rows, *page_table;
+    void *k_out, *v_out;
+    unsigned int *err;
+} qsa_paged_gather_args;
+
+/*
+ * qsa_paged_attn -- attention of one new token per row of q over a whole
+ * paged sequence.  Row t attends to cells 0 .. seq_lens[t]-1 of table row
+ * rows[t] (rows NULL: table row t); several rows of q may read one sequence,
+ * each with its own length.  Query head h reads KV head h / (n_q_heads /
+ * n_kv_heads):
+ *   s_c = softmax_scale * sum_g ksc[c,g] * sum_{d in g} q[t,h,d] * kq[c,d]
+ *   w_c = exp(s_c - max s);  O = sum w_c v_c / sum w_c,  v_c = vsc * vq
+ *   out = O, or with a gate O / (1 + exp(-gate)), rounded to dtype
+ *   lse[t,h] = max s + log(sum w_c)   (natural logarithm; lse may be NULL)
+ * A row of length 0 gives out = +0 and lse = -inf.  A length below 0 or above
+ * max_pages * page_size is cut to that range, a table row outside [0, n_rows)
+ * counts as length 0, and a table entry outside the pool leaves its page's
+ * cells out; each of these sets QSA_DEVERR_BAD_ID.
+ *
+ * q, out [n_tokens, n_q_heads, head_dim] in dtype (QSA_F16 or QSA_BF16); gate
+ * NULL or fp32 of that shape; lse fp32 [n_tokens, n_q_heads]; seq_lens, rows
+ * int32 [n_tokens]; page_table int32 [n_rows, max_pages]; kq, vq, ksc, vsc one
+ * layer of the pool.  workspace: device scratch of at least
+ * qsa_paged_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim) bytes,
+ * 256-byte aligned, overwritten; two calls that share one must not run
+ * concurrently (graphs that replay on different streams need one each).
+ * The work is divided over the cached cells of all rows, so results do not
+ * depend on max_pages but their last bits may depend on the other rows'
+ * lengths.  Range: scores and sums are fp32; K scales of any fp16 value, V
+ * scales below 2^15.
+ * Supported: n_q_heads a multiple of n_kv_heads, 1..16 query heads per KV
+ * head.  q, out, kq, vq 16-byte aligned; ksc, vsc 8-byte; the rest 4-byte.
+ */
+typedef struct {
+    int n_tokens, n_q_heads, n_kv_heads, head_dim, group, page_size, n_pages, n_rows, max_pages;
+    int dtype;
+    const void *q;
+    const int8_t *kq, *vq;
+    const uint16_t *ksc, *vsc;
+    const int32_t *page_table, *seq_lens, *rows;
+    float softmax_scale;
+    const float *gate;
+    void *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    unsigned int *err;
+} qsa_paged_attn_args;
+
+/* Bytes of workspace qsa_paged_attn needs (0 on a shape it does not support);
+ * it depends on neither the batch nor the lengths. */
+size_t qsa_paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+
+/*
+ * qsa_page_update -- the batch's next page table: forks, reorders, frees and
+ * extends rows in one call.  New row r takes the pages of old row src[r]
+ * (src NULL: r itself; -1: none, an empty row), then grows by n_new[r] tokens:
+ *  - An old row that no new row takes is freed; one taken twice is forked.
+ *  - Pages: if n_new[r] > 0 and the last page is partly filled and held more
+ *    than once in the new table, the row gets a new page in its place and the
+ *    filled cells are copied there, in all layers.  Then as many new pages as
+ *    the row needs.  New pages are the pages that no new row holds, lowest
+ *    number first, dealt to the rows in order.
+ *  - Tokens: row r's new tokens are numbers off .. off + n_new[r] - 1 of the
+ *    packed batch, off = sum of n_new of the rows before; slots[i] and
+ *    positions[i] receive token i's pool cell and position.
+ *  - A row grows whole or not at all.  It stays at its old length, and its
+ *    tokens' slots and positions are -1, where its tokens do not fit into
+ *    max_pages pages or into the n_slots entries of slots, or where it needs
+ *    pages and the rows up to it have asked for more than were free.  Each
+ *    sets QSA_DEVERR_NO_PAGES.
+ * Outputs: page_table_out [rows, max_pages] (-1 behind a row's pages),
+ * seq_lens_out [rows], refs [n_pages] (how often a page is held: 0 = free),
+ * slots, positions [n_slots] (entries past the last token -1).
+ * src outside [-1, n_rows_in), a length outside [0, max_pages * page_size], a
+ * negative n_new and a table entry outside [0, n_pages) count as -1, the
+ * nearest length, 0 and no page; each sets QSA_DEVERR_BAD_ID.
+ * page_table_out and seq_lens_out may be page_table and seq_lens themselves
+ * where src is NULL (then n_rows_in = n_rows), and must not overlap them
+ * otherwise.  workspace: at least qsa_pages_workspace_bytes(n_rows, n_pages)
+ * bytes, 256-byte aligned, overwritten; not to be shared by concurrent calls.
+ * kq, vq, ksc, vsc: all layers of the pool.  kq, vq, ksc, vsc 16-byte
+ * aligned, the rest 4-byte.
+ */
+typedef struct {
+    int n_rows_in, n_rows, max_pages, n_layers, n_pages, page_size, n_kv_heads, head_dim, group, n_slots;
+    const int32_t *page_table, *seq_lens, *src, *n_new;
+    int8_t *kq, *vq;
+    uint16_t *ksc, *vsc;
+    int32_t *page_table_out, *seq_lens_out, *refs, *slots, *positions;
+    void *workspace;
+    size_t workspace_bytes;
+    unsigned int *err;
+} qsa_page_update_args;
+
+/*
+ * qsa_page_compact -- moves the held pages to the lowest page numbers.  With
+ * L the number of pages that some row holds: each held page below L stays,
+ * and the i-th free page below L receives the contents (all layers) of the
+ * i-th held page at or above L.  Outputs: page_table_out (the rows' pages by
+ * their new numbers, -1 behind them), refs [n_pages] by the new numbers,
+ * page_map [n_pages] (a page's new number; -1 for a free one) and n_live [1] =
+ * L.  Lengths do not change.  page_table_out may be page_table itself.
+ * Lengths and entries out of range are treated as in qsa_page_update.
+ * workspace and alignment as there.
+ */
+typedef struct {
+    int n_rows, max_pages, n_layers, n_pages, page_size, n_kv_heads, head_dim, group;
+    const int32_t *page_table, *seq_lens;
+    int8_t *kq, *vq;
+    uint16_t *ksc, *vsc;
+    int32_t *page_table_out, *refs, *page_map, *n_live;
+    void *workspace;
+    size_t workspace_bytes;
+    unsigned int *err;
+} qsa_page_compact_args;
+
+/* Bytes of workspace qsa_page_update and qsa_page_compact need (0 on bad input). */
+size_t qsa_pages_workspace_bytes(int n_rows, int n_pages);
+
+qsa_status qsa_paged_prep(const qsa_paged_prep_args *args, void *stream);
+qsa_status qsa_paged_gather(const qsa_paged_gather_args *args, void *stream);
+qsa_status qsa_paged_attn(const qsa_paged_attn_args *args, void *stream);
+qsa_status qsa_page_update(const qsa_page_update_args *args, void *stream);
+qsa_status qsa_page_compact(const qsa_page_compact_args *args, void *stream);
 
 /*
  * qsa_check_word -- the pages have no counterpart to this call; it serves the

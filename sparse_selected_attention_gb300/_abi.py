@@ -16,8 +16,8 @@ LIB_PATH = os.environ.get("QSA_LIB") or os.path.join(_HERE, "libqsa.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "qsa.h")
 
 QSA_OK, QSA_ERR_INVALID_ARG, QSA_ERR_UNSUPPORTED, QSA_ERR_CUDA = 0, 1, 2, 3
-QSA_DEVERR_BAD_ID, QSA_DEVERR_TIMEOUT = 1, 2
-QSA_F32, QSA_F16 = 0, 1
+QSA_DEVERR_BAD_ID, QSA_DEVERR_TIMEOUT, QSA_DEVERR_NO_PAGES = 1, 2, 4
+QSA_F32, QSA_F16, QSA_BF16 = 0, 1, 2
 QSA_SCORE_NOALLOC_MAX_TOKENS = 8192
 QSA_SELECT_MAX_CELLS = 32768
 
@@ -51,6 +51,46 @@ class AttnArgs(ctypes.Structure):
                 ("group", _c_int), ("cache_cells", _c_int), ("width", _c_int),
                 ("q", _vp), ("kq", _vp), ("vq", _vp), ("ksc", _vp), ("vsc", _vp), ("ids", _vp),
                 ("softmax_scale", _c_float), ("out", _vp), ("part", _vp), ("err", _vp), ("gate", _vp)]
+
+
+class PagedPrepArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("ntok", "n_q_heads", "n_kv_heads", "head_dim", "group", "rope_dims",
+                                       "interleaved", "cache_cells", "in_dtype", "q_out_dtype")]
+                + [("eps", _c_float), ("rope_mscale", _c_float)]
+                + [(n, _vp) for n in ("q_in", "k_in", "v_in")]
+                + [(n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride")]
+                + [(n, _vp) for n in ("q_norm_w", "k_norm_w", "inv_freq", "positions", "slots", "q_out",
+                                      "kq", "vq", "ksc", "vsc", "err")])
+
+
+class PagedGatherArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_ids", "n_kv_heads", "head_dim", "group", "cache_cells", "page_size",
+                                       "n_rows", "max_pages", "out_dtype")]
+                + [(n, _vp) for n in ("kq", "vq", "ksc", "vsc", "ids", "rows", "page_table", "k_out", "v_out", "err")])
+
+
+class PagedAttnArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "group", "page_size",
+                                       "n_pages", "n_rows", "max_pages", "dtype")]
+                + [(n, _vp) for n in ("q", "kq", "vq", "ksc", "vsc", "page_table", "seq_lens", "rows")]
+                + [("softmax_scale", _c_float)] + [(n, _vp) for n in ("gate", "out", "lse", "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t), ("err", _vp)])
+
+
+class PageUpdateArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_rows_in", "n_rows", "max_pages", "n_layers", "n_pages", "page_size",
+                                       "n_kv_heads", "head_dim", "group", "n_slots")]
+                + [(n, _vp) for n in ("page_table", "seq_lens", "src", "n_new", "kq", "vq", "ksc", "vsc",
+                                      "page_table_out", "seq_lens_out", "refs", "slots", "positions", "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t), ("err", _vp)])
+
+
+class PageCompactArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_rows", "max_pages", "n_layers", "n_pages", "page_size", "n_kv_heads",
+                                       "head_dim", "group")]
+                + [(n, _vp) for n in ("page_table", "seq_lens", "kq", "vq", "ksc", "vsc", "page_table_out", "refs",
+                                      "page_map", "n_live", "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t), ("err", _vp)])
 
 
 class QSAError(RuntimeError):
@@ -95,7 +135,10 @@ def lib() -> ctypes.CDLL:
 
 def _declare(L: ctypes.CDLL, path: str) -> None:
     for name, argt in (("qsa_prep", PrepArgs), ("qsa_score", ScoreArgs), ("qsa_attn", AttnArgs),
-                       ("qsa_score_noalloc", ScoreArgs), ("qsa_select", SelectArgs)):
+                       ("qsa_score_noalloc", ScoreArgs), ("qsa_select", SelectArgs),
+                       ("qsa_paged_prep", PagedPrepArgs), ("qsa_paged_gather", PagedGatherArgs),
+                       ("qsa_paged_attn", PagedAttnArgs), ("qsa_page_update", PageUpdateArgs),
+                       ("qsa_page_compact", PageCompactArgs)):
         f = getattr(L, name)
         f.argtypes = [ctypes.POINTER(argt), _vp]
         f.restype = _c_int
@@ -107,6 +150,10 @@ def _declare(L: ctypes.CDLL, path: str) -> None:
     L.qsa_check_word.restype = _c_int
     L.qsa_score_workspace_bytes.argtypes = [_c_int, _c_int]
     L.qsa_score_workspace_bytes.restype = ctypes.c_size_t
+    L.qsa_paged_attn_workspace_bytes.argtypes = [_c_int, _c_int, _c_int]
+    L.qsa_paged_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.qsa_pages_workspace_bytes.argtypes = [_c_int, _c_int]
+    L.qsa_pages_workspace_bytes.restype = ctypes.c_size_t
     L.qsa_status_str.argtypes = [_c_int]
     L.qsa_status_str.restype = ctypes.c_char_p
     L.qsa_last_error.argtypes = []

@@ -35,7 +35,8 @@ VARIANTS = {
     "wait0": (["-DQSA_WAIT_LIMIT=0"], "libqsa_wait0.so"),
     "check": (["-DQSA_CHECK=1"], "libqsa_check.so"),
 }
-SOURCES = ["api.cpp", "prep.cu", "score.cu", "select.cu", "attn.cu", "ids.cu"]
+SOURCES = ["api.cpp", "prep.cu", "score.cu", "select.cu", "attn.cu", "ids.cu",
+           "paged_prep.cu", "paged_attn.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

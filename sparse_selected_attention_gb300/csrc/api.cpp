@@ -29,6 +29,51 @@ bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 constexpr int kHeadDim = 128;
 constexpr int kGroup = 32;
 constexpr long long kMaxPos = 1ll << 29;  // positions stay exact in the rotation angle product
+constexpr long long kMaxInt = 0x7fffffffll;
+
+// A status with its text, passed through the checks the paged calls share.
+struct Fault {
+    qsa_status status;
+    const char *what;
+};
+constexpr Fault kFine{QSA_OK, nullptr};
+
+bool paged_shape(int head_dim, int group) { return (head_dim == 128 && group == 32) || (head_dim == 256 && group == 64); }
+bool paged_page(int page_size) { return page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0; }
+
+// The checks that qsa_page_update and qsa_page_compact share: the pool, the
+// tables, the workspace.
+template <class A>
+Fault check_pages(const A &a) {
+    if (!paged_shape(a.head_dim, a.group) || a.n_kv_heads < 1 || a.n_kv_heads > 65535 || !paged_page(a.page_size))
+        return {QSA_ERR_UNSUPPORTED,
+                "supported pools are (head_dim 128, group 32) or (head_dim 256, group 64), 1..65535 KV heads and "
+                "page_size 16, 32, 64, 128 or 256"};
+    if (a.n_rows < 0 || a.max_pages < 1 || a.n_layers < 1 || a.n_pages < 1)
+        return {QSA_ERR_INVALID_ARG, "negative n_rows, or max_pages, n_layers or n_pages below 1"};
+    if ((long long)a.n_pages * a.page_size > kMaxInt || (long long)a.max_pages * a.page_size > kMaxInt)
+        return {QSA_ERR_INVALID_ARG, "n_pages * page_size or max_pages * page_size beyond int32"};
+    if (!a.kq || !a.vq || !a.ksc || !a.vsc || !a.refs || !a.workspace || (a.n_rows && (!a.page_table_out)))
+        return {QSA_ERR_INVALID_ARG, "NULL buffer"};
+    if (a.workspace_bytes < qsa::pages_workspace_bytes(a.n_rows, a.n_pages))
+        return {QSA_ERR_INVALID_ARG, "workspace smaller than qsa_pages_workspace_bytes()"};
+    if (!aligned(a.kq, 16) || !aligned(a.vq, 16) || !aligned(a.ksc, 16) || !aligned(a.vsc, 16) ||
+        !aligned(a.workspace, 256) || !aligned(a.page_table, 4) || !aligned(a.seq_lens, 4) ||
+        !aligned(a.page_table_out, 4) || !aligned(a.refs, 4) || !aligned(a.err, 4))
+        return {QSA_ERR_INVALID_ARG, "misaligned buffer"};
+    return kFine;
+}
+
+qsa_status fail_in(const char *where, const Fault &f) {
+    std::snprintf(g_last_error, sizeof g_last_error, "%s: %s", where, f.what);
+    return f.status;
+}
+
+// Whether [a, a + na) and [b, b + nb) (bytes) share a byte.
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
 
 }  // namespace
 
@@ -217,7 +262,8 @@ qsa_status qsa_check_word(unsigned int *out) {
     unsigned int w = 0u;
     cudaError_t (*const readers[])(unsigned int *) = {qsa::take_check_word_attn, qsa::take_check_word_score,
                                                       qsa::take_check_word_prep, qsa::take_check_word_select,
-                                                      qsa::take_check_word_ids};
+                                                      qsa::take_check_word_ids,  qsa::take_check_word_paged_prep,
+                                                      qsa::take_check_word_paged_attn, qsa::take_check_word_pages};
     for (auto rd : readers) {
         unsigned int v = 0u;
         const cudaError_t e = rd(&v);
@@ -260,6 +306,159 @@ qsa_status qsa_score_noalloc(const qsa_score_args *a, void *stream) {
                        0,       a->max_ctas};
     cudaError_t e = qsa::launch_score_noalloc(L, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_score_noalloc");
+}
+
+size_t qsa_paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
+    if ((head_dim != 128 && head_dim != 256) || n_kv_heads < 1 || n_kv_heads > 65535 || n_q_heads < 1 ||
+        n_q_heads % n_kv_heads != 0 || n_q_heads / n_kv_heads > 16)
+        return 0;
+    return qsa::paged_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim);
+}
+
+size_t qsa_pages_workspace_bytes(int n_rows, int n_pages) {
+    if (n_rows < 0 || n_pages < 1) return 0;
+    return qsa::pages_workspace_bytes(n_rows, n_pages);
+}
+
+qsa_status qsa_paged_prep(const qsa_paged_prep_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: args is NULL");
+    if (!paged_shape(a->head_dim, a->group) || a->n_kv_heads < 1 || a->n_kv_heads > 32767 || a->n_q_heads < 1 ||
+        a->n_q_heads > 32767)
+        return fail(QSA_ERR_UNSUPPORTED,
+                    "qsa_paged_prep: supported shapes are (head_dim 128, group 32) or (head_dim 256, group 64), "
+                    "1..32767 heads");
+    if (a->rope_dims < 0 || a->rope_dims > a->head_dim || a->rope_dims % (a->head_dim / 16) != 0)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_prep: rope_dims must be a multiple of head_dim/16 in [0, head_dim]");
+    if (a->in_dtype != QSA_F32 && a->in_dtype != QSA_F16 && a->in_dtype != QSA_BF16)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: bad in_dtype");
+    if (a->q_out_dtype != QSA_F16 && a->q_out_dtype != QSA_BF16)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: q_out_dtype must be QSA_F16 or QSA_BF16");
+    if (a->interleaved != 0 && a->interleaved != 1)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: interleaved must be 0 or 1");
+    if (a->ntok < 0 || a->cache_cells < 1) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: negative ntok or empty cache");
+    if (!(a->eps >= 0.0f) || !std::isfinite(a->eps) || !std::isfinite(a->rope_mscale))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: eps must be finite >= 0 and rope_mscale finite");
+    const long long size = a->in_dtype == QSA_F32 ? 4 : 2, kv = (long long)a->n_kv_heads * a->head_dim;
+    if (a->ntok > 1 && (a->q_stride < (long long)a->n_q_heads * a->head_dim || a->k_stride < kv || a->v_stride < kv ||
+                        a->q_stride * size % 16 || a->k_stride * size % 16 || a->v_stride * size % 16))
+        return fail(QSA_ERR_INVALID_ARG,
+                    "qsa_paged_prep: token strides must hold a token's heads and be multiples of 16 bytes");
+    if (a->ntok == 0) return QSA_OK;
+    if (!a->q_in || !a->k_in || !a->v_in || !a->positions || !a->slots || !a->q_out || !a->kq || !a->vq || !a->ksc ||
+        !a->vsc || (a->rope_dims && !a->inv_freq))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: NULL buffer");
+    if (!aligned(a->q_in, 16) || !aligned(a->k_in, 16) || !aligned(a->v_in, 16) || !aligned(a->q_norm_w, 16) ||
+        !aligned(a->k_norm_w, 16) || !aligned(a->inv_freq, 4) || !aligned(a->positions, 4) || !aligned(a->slots, 4) ||
+        !aligned(a->q_out, 16) || !aligned(a->kq, 16) || !aligned(a->vq, 16) || !aligned(a->ksc, 8) ||
+        !aligned(a->vsc, 8) || !aligned(a->err, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_prep: misaligned buffer");
+    cudaError_t e = qsa::launch_paged_prep(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_paged_prep");
+}
+
+qsa_status qsa_paged_gather(const qsa_paged_gather_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: args is NULL");
+    if (!paged_shape(a->head_dim, a->group) || a->n_kv_heads < 1 || a->n_kv_heads > 65535)
+        return fail(QSA_ERR_UNSUPPORTED,
+                    "qsa_paged_gather: supported shapes are (head_dim 128, group 32) or (head_dim 256, group 64), "
+                    "1..65535 KV heads");
+    if (a->out_dtype != QSA_F32 && a->out_dtype != QSA_F16 && a->out_dtype != QSA_BF16)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: bad out_dtype");
+    if (a->n_ids < 0 || a->cache_cells < 1) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: negative n_ids or empty cache");
+    if (a->page_table) {
+        if (!paged_page(a->page_size))
+            return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_gather: page_size must be 16, 32, 64, 128 or 256");
+        if (a->n_rows < 1 || a->max_pages < 1 || (a->n_ids && !a->rows))
+            return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: a page table needs rows, n_rows and max_pages");
+    }
+    if ((long long)a->n_ids * a->n_kv_heads * (a->head_dim / 8) > kMaxInt * 256)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_gather: more than 2^31 blocks of output");
+    if (a->n_ids == 0) return QSA_OK;
+    if (!a->kq || !a->vq || !a->ksc || !a->vsc || !a->ids || !a->k_out || !a->v_out)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: NULL buffer");
+    if (!aligned(a->kq, 16) || !aligned(a->vq, 16) || !aligned(a->ksc, 8) || !aligned(a->vsc, 8) ||
+        !aligned(a->ids, 4) || !aligned(a->rows, 4) || !aligned(a->page_table, 4) || !aligned(a->k_out, 16) ||
+        !aligned(a->v_out, 16) || !aligned(a->err, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: misaligned buffer");
+    cudaError_t e = qsa::launch_paged_gather(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_paged_gather");
+}
+
+qsa_status qsa_paged_attn(const qsa_paged_attn_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: args is NULL");
+    if (!paged_shape(a->head_dim, a->group) || a->n_kv_heads < 1 || a->n_kv_heads > 65535 || a->n_q_heads < 1 ||
+        a->n_q_heads % a->n_kv_heads != 0 || a->n_q_heads / a->n_kv_heads > 16)
+        return fail(QSA_ERR_UNSUPPORTED,
+                    "qsa_paged_attn: supported shapes are (head_dim 128, group 32) or (head_dim 256, group 64), "
+                    "n_q_heads a multiple of n_kv_heads with at most 16 query heads per KV head");
+    if (!paged_page(a->page_size))
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_attn: page_size must be 16, 32, 64, 128 or 256");
+    if (a->dtype != QSA_F16 && a->dtype != QSA_BF16)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: dtype must be QSA_F16 or QSA_BF16");
+    if (a->n_tokens < 0 || a->n_pages < 1 || a->n_rows < 1 || a->max_pages < 1)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: negative n_tokens, or n_pages, n_rows or max_pages below 1");
+    if (!a->rows && a->n_rows < a->n_tokens)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: without rows the table needs a row per token");
+    if ((long long)a->n_pages * a->page_size > kMaxInt || (long long)a->max_pages * a->page_size > kMaxInt)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: n_pages * page_size or max_pages * page_size beyond int32");
+    if ((long long)a->n_tokens * a->n_kv_heads > kMaxInt)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_attn: n_tokens * n_kv_heads beyond int32");
+    if (!std::isfinite(a->softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: softmax_scale not finite");
+    if (a->n_tokens == 0) return QSA_OK;
+    if (!a->q || !a->kq || !a->vq || !a->ksc || !a->vsc || !a->page_table || !a->seq_lens || !a->out || !a->workspace)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: NULL buffer");
+    if (a->workspace_bytes < qsa_paged_attn_workspace_bytes(a->n_q_heads, a->n_kv_heads, a->head_dim))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: workspace smaller than qsa_paged_attn_workspace_bytes()");
+    if (!aligned(a->q, 16) || !aligned(a->kq, 16) || !aligned(a->vq, 16) || !aligned(a->ksc, 8) ||
+        !aligned(a->vsc, 8) || !aligned(a->page_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->rows, 4) ||
+        !aligned(a->gate, 4) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->workspace, 256) ||
+        !aligned(a->err, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: misaligned buffer");
+    cudaError_t e = qsa::launch_paged_attn(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_paged_attn");
+}
+
+qsa_status qsa_page_update(const qsa_page_update_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_page_update: args is NULL");
+    const Fault f = check_pages(*a);
+    if (f.status != QSA_OK) return fail_in("qsa_page_update", f);
+    if (a->n_rows_in < 0 || a->n_slots < 0) return fail(QSA_ERR_INVALID_ARG, "qsa_page_update: negative n_rows_in or n_slots");
+    if (!a->src && a->n_rows_in < a->n_rows)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_update: without src the old table needs every new row");
+    if ((a->n_rows && (!a->n_new || !a->seq_lens_out)) || (a->n_rows_in && (!a->page_table || !a->seq_lens)) ||
+        (a->n_slots && (!a->slots || !a->positions)))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_update: NULL buffer");
+    if (!aligned(a->src, 4) || !aligned(a->n_new, 4) || !aligned(a->seq_lens_out, 4) || !aligned(a->slots, 4) ||
+        !aligned(a->positions, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_update: misaligned buffer");
+    const size_t row = (size_t)a->max_pages * 4, tin = a->n_rows_in * row, tout = a->n_rows * row;
+    const bool same_table = a->page_table == a->page_table_out, same_lens = a->seq_lens == a->seq_lens_out;
+    if ((overlap(a->page_table, tin, a->page_table_out, tout) && (a->src || !same_table)) ||
+        (overlap(a->seq_lens, (size_t)a->n_rows_in * 4, a->seq_lens_out, (size_t)a->n_rows * 4) && (a->src || !same_lens)))
+        return fail(QSA_ERR_INVALID_ARG,
+                    "qsa_page_update: the new table and lengths may be the old ones only without src, and not overlap them otherwise");
+    cudaError_t e = qsa::launch_page_update(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_page_update");
+}
+
+qsa_status qsa_page_compact(const qsa_page_compact_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_page_compact: args is NULL");
+    const Fault f = check_pages(*a);
+    if (f.status != QSA_OK) return fail_in("qsa_page_compact", f);
+    if ((a->n_rows && (!a->page_table || !a->seq_lens)) || !a->page_map || !a->n_live)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_compact: NULL buffer");
+    if (!aligned(a->page_map, 4) || !aligned(a->n_live, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_compact: misaligned buffer");
+    const size_t bytes = (size_t)a->n_rows * a->max_pages * 4;
+    if (a->page_table != a->page_table_out && overlap(a->page_table, bytes, a->page_table_out, bytes))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_compact: page_table_out overlaps page_table without being it");
+    cudaError_t e = qsa::launch_page_compact(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_page_compact");
 }
 
 }  // extern "C"

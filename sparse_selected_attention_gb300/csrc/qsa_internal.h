@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "qsa.h"
+
 namespace qsa {
 
 struct PrepLaunch {
@@ -135,6 +137,14 @@ cudaError_t launch_attn(const AttnLaunch &a, cudaStream_t s);
 cudaError_t launch_select(const SelectLaunch &a, cudaStream_t s);
 // Decode windows (even = false) or evenly spaced causal lists (even = true).
 cudaError_t launch_fill_ids(const FillIdsLaunch &a, bool even, cudaStream_t s);
+// The paged cache's calls, on checked arguments.
+cudaError_t launch_paged_prep(const qsa_paged_prep_args &a, cudaStream_t s);
+cudaError_t launch_paged_gather(const qsa_paged_gather_args &a, cudaStream_t s);
+cudaError_t launch_paged_attn(const qsa_paged_attn_args &a, cudaStream_t s);
+cudaError_t launch_page_update(const qsa_page_update_args &a, cudaStream_t s);
+cudaError_t launch_page_compact(const qsa_page_compact_args &a, cudaStream_t s);
+size_t paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+size_t pages_workspace_bytes(int n_rows, int n_pages);
 
 #if QSA_CHECK
 // The QSA_CHECK build's per-file check words (check.cuh), read and cleared.
@@ -143,6 +153,9 @@ cudaError_t take_check_word_score(unsigned int *out);
 cudaError_t take_check_word_prep(unsigned int *out);
 cudaError_t take_check_word_select(unsigned int *out);
 cudaError_t take_check_word_ids(unsigned int *out);
+cudaError_t take_check_word_paged_prep(unsigned int *out);
+cudaError_t take_check_word_paged_attn(unsigned int *out);
+cudaError_t take_check_word_pages(unsigned int *out);
 #endif
 
 }  // namespace qsa

@@ -1,112 +1,767 @@
 // qsa_paged_attn: attention of one new token per row over a paged sequence.
+//
+//   s_c = scale * q . K_c,  O = sum_c 2^(s_c log2e - m) V_c / sum_c 2^(s_c log2e - m)
+//
+// One pass over the cache with a running maximum m and sum.  It is bound by
+// reading the cache: 2 D + 16 bytes per (cell, KV head) against 4 D flops per
+// query head, 23 flops per byte at 12 heads.
+//
+// Work.  A row's cells are taken in units of 32.  The units of all (row, KV
+// head) pairs, in that order, are cut into equal shares, one per CTA, so one
+// long row or a ragged batch fills the chip alike and the share does not
+// depend on the table's width.  A share that holds all of a pair writes its
+// output; a pair that spans CTAs leaves one partial per CTA in the workspace
+// (values, maximum, sum), and a second launch joins them.  Each CTA finds its
+// place by summing the rows' lengths itself, which costs one pass over
+// seq_lens and saves a launch.
+//
+// A unit.  The query heads of one KV head are the M side (padded to 16) of
+// m16n8k16 products, cells are N of Q.K and the contraction of P.V.  (tcgen05
+// would want the codes as fp16 in shared memory, a round trip of four bytes
+// per code; here they go from shared memory to fragments.)  Each warp streams
+// its units through a ring of two stages, each filled by two TMA boxes of 32
+// rows x 128 bytes (four of 16 rows where a page has 16) and eight-byte
+// cp.async for the scales.  The boxes carry the 128-byte swizzle, and cells
+// and dims are assigned to lanes so that every fragment read meets all banks
+// once (K: two passes):
+//   cell of column n of an 8-column tile: PERM[n] = 0 2 4 6 3 1 7 5
+//   K dims of lane (g, r), k-step (b, h): 32 b + 8 r + 4 h + {0, 2 | 1, 3}
+//   V dims of lane (g, r): 16 g .. 16 g + 15
+// Codes become fp16 integers by or-ing 0x6400 to the code + 128 (1024 + 128 +
+// code).  For K the 1152 stays: the accumulators start at -1152 * sum q, so
+// the products give q . code exactly, per scale group, and the group's scale
+// multiplies in fp32.  For V it is subtracted and the cell's scale multiplied
+// in fp16, under a power of two per warp that keeps small scales out of the
+// subnormals.
+//
+// With head_dim 256 two warps share a unit, each with 128 dims of K and V;
+// their partial scores meet in shared memory.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include "check.cuh"
 #include "qsa_internal.h"
+#include "tc_common.cuh"
 
 namespace qsa {
 namespace {
 
-constexpr int WARPS = 4;
-constexpr int MAX_PER = 16;  // query heads per KV head
+constexpr int DW = 128;   // dims a warp handles
+constexpr int UNIT = 32;  // cells of a warp step
+constexpr int NW = 4;     // warps per CTA
+constexpr int NS = 2;     // ring stages per warp
+constexpr int TILE = UNIT * DW;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float SLACK = 8.0f;  // weights stay below 2^8 of the running maximum's
+constexpr int MAX_CTAS = 152 * 3;
 
-__device__ __forceinline__ float load_q(const void *q, int dtype, size_t i) {
-    return dtype == QSA_F16 ? __half2float(static_cast<const __half *>(q)[i])
-                            : __bfloat162float(static_cast<const __nv_bfloat16 *>(q)[i]);
+// Fewest units of a share: finer ones would only add partials to join.
+constexpr int MIN_SHARE = 8;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+
+// Bytes 0 and 2 (or 1 and 3) of w, as fp16 1152 + code.
+__device__ __forceinline__ uint32_t even_codes(uint32_t w) { return (w & 0x00FF00FFu) ^ 0x64806480u; }
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u; }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1, float c0, float c1,
+                                         float c2, float c3) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
-// One block per (row, KV head); a warp takes every fourth cell, a lane
-// head_dim/32 dims of it, with one running maximum, sum and value row per
-// query head; the warps' states are joined at the end.
-template <int D>
-__global__ void __launch_bounds__(WARPS * 32) paged_attn_kernel(const qsa_paged_attn_args a) {
-    constexpr int N = D / 32;
-    __shared__ float so[WARPS][D], sm[WARPS], sl[WARPS];
-    wait_for_previous_grid();
-    allow_dependent_launch();
-    const int t = blockIdx.x / a.n_kv_heads, kvh = blockIdx.x % a.n_kv_heads;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = a.n_q_heads / a.n_kv_heads;
-    const int row = a.rows ? a.rows[t] : t;
-    int len = a.seq_lens[t];
-    bool bad = false;
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap *map, int x, int head, int cell, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(map), "r"(x), "r"(head), "r"(cell), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool pred) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(pred ? 8 : 0));
+}
+
+// Shared memory of a CTA.  After a segment the tiles hold the warps' values
+// for the merge.
+template <int S>
+struct Smem {
+    uint8_t tile[NW][NS][2][TILE];  // K, V; 1024-byte aligned
+    uint2 scale[NW][NS][2][UNIT];   // four fp16 per cell: ksc, vsc
+    uint4 q[S][8][32];              // Q fragments by k-step and lane
+    float bias[4][16];              // -1152 * sum of q over a scale group, per head (see stage_q)
+    float qinv[16];                 // 2^-e of a head's scaled query
+    float xch[S == 2 ? NW * 2 * 16 * 32 : 1];
+    float m[NW / S][16], l[NW / S][16], f[NW / S][16];
+    int v[NW / S];                  // the groups' V exponents
+    uint64_t bar[NW][NS];
+    long long scan[NW];
+    long long total, before;        // units of all rows; of the rows before `row`
+    int row;
+};
+
+struct Part {
+    int task, n;  // (row * n_kv_heads + KV head, CTAs that share it), task -1: none starts here
+};
+
+struct Work {
+    Part *part;  // [grid]
+    float *ml;   // [grid][2][per][2]
+    float *o;    // [grid][2][per][D]
+};
+__host__ __device__ inline Work carve(void *ws, int per) {
+    uint8_t *b = static_cast<uint8_t *>(ws);
+    Work w;
+    w.part = reinterpret_cast<Part *>(b);
+    b += ((size_t)MAX_CTAS * sizeof(Part) + 255) / 256 * 256;
+    w.ml = reinterpret_cast<float *>(b);
+    b += ((size_t)MAX_CTAS * 2 * per * 2 * sizeof(float) + 255) / 256 * 256;
+    w.o = reinterpret_cast<float *>(b);
+    return w;
+}
+
+// Row t's length, cut to its range, and its table row (0 with length 0 if it
+// is out of range).
+__device__ __forceinline__ int row_len(const qsa_paged_attn_args &a, int t, int &row, bool &bad) {
+    row = a.rows ? __ldg(a.rows + t) : t;
+    const int len = __ldg(a.seq_lens + t), most = a.max_pages * a.page_size;
     if (row < 0 || row >= a.n_rows) {
         bad = true;
-        len = 0;
+        row = 0;
+        return 0;
     }
-    const int most = a.max_pages * a.page_size;
-    if (len < 0 || len > most) {
-        bad = true;
-        len = len < 0 ? 0 : most;
+    bad |= len < 0 || len > most;
+    return min(max(len, 0), most);
+}
+__device__ __forceinline__ int units_of(int len) { return max((len + UNIT - 1) / UNIT, 1); }
+
+// Sums the rows' units and finds the row that holds unit share * blockIdx.x.
+// Each thread takes a run of rows.
+template <int S>
+__device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int &share) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = (a.n_tokens + NW * 32 - 1) / (NW * 32);
+    const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
+    bool bad = false;
+    long long mine = 0;
+    for (int t = t0; t < t1; ++t) {
+        int row;
+        mine += (long long)units_of(row_len(a, t, row, bad)) * a.n_kv_heads;
     }
-    for (int g = 0; g < per; ++g) {
-        const size_t qi = ((size_t)t * a.n_q_heads + kvh * per + g) * D + lane * N;
-        float q[N], o[N], m = -CUDART_INF_F, l = 0.0f;
+    if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+    long long s = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 31) sh.scan[warp] = s;
+    __syncthreads();
+    long long total = 0, before = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        if (w < warp) before += sh.scan[w];
+        total += sh.scan[w];
+    }
+    before += s - mine;
+    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    share = (int)max(per, (long long)MIN_SHARE);
+    const long long x0 = (long long)share * blockIdx.x;
+    if (x0 >= before && x0 < before + mine) {
+        for (int t = t0;; ++t) {
+            int row;
+            const long long u = (long long)units_of(row_len(a, t, row, bad)) * a.n_kv_heads;
+            if (x0 < before + u) {
+                sh.row = t;
+                sh.before = before;
+                break;
+            }
+            before += u;
+        }
+    }
+    if (tid == 0) sh.total = total;
+    __syncthreads();
+}
+
+// The query heads of (row t, KV head kvh) as A fragments in shared memory,
+// fp16, with the sums that undo the codes' 1152.  bf16 queries are scaled by
+// a power of two per head where they would leave the fp16 range; fp16 ones
+// are used as they are.  A negative softmax scale flips their sign.
+template <int S>
+__device__ __forceinline__ void stage_q(const qsa_paged_attn_args &a, Smem<S> &sh, int t, int kvh, int per) {
+    constexpr int D = DW * S, N = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int h = warp; h < 16; h += NW) {
+        float x[N];
+        uint16_t raw[N];
+        const size_t at = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + lane * N;
+        const bool have = h < per && QSA_IN(at + N - 1, (size_t)a.n_tokens * a.n_q_heads * D);
+        if constexpr (N == 4)
+            *reinterpret_cast<uint2 *>(raw) =
+                have ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at)) : make_uint2(0u, 0u);
+        else
+            *reinterpret_cast<uint4 *>(raw) = have ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at))
+                                                   : make_uint4(0u, 0u, 0u, 0u);
+        float top = 0.0f;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            q[e] = load_q(a.q, a.dtype, qi + e) * a.softmax_scale;
-            o[e] = 0.0f;
+            x[e] = a.dtype == QSA_F16 ? __half2float(__ushort_as_half(raw[e])) : __bfloat162float(__ushort_as_bfloat16(raw[e]));
+            top = fmaxf(top, fabsf(x[e]));
         }
-        for (int c = warp; c < len; c += WARPS) {
-            const int page = a.page_table[(size_t)row * a.max_pages + c / a.page_size];
-            if (page < 0 || page >= a.n_pages) {
-                bad = true;
-                continue;
-            }
-            const size_t cell = ((size_t)page * a.page_size + c % a.page_size) * a.n_kv_heads + kvh;
-            if (!QSA_IN(cell, (size_t)a.n_pages * a.page_size * a.n_kv_heads)) continue;
-            const float ks = __half2float(__ushort_as_half(a.ksc[cell * 4 + lane / 8]));
-            const float vs = __half2float(__ushort_as_half(a.vsc[cell * 4 + lane / 8]));
-            float s = 0.0f;
+        int ex = 0;
+        if (a.dtype != QSA_F16) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) s = fmaf(q[e], (float)a.kq[cell * D + lane * N + e], s);
-            s *= ks;
-#pragma unroll
-            for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-            const float mn = fmaxf(m, s), al = expf(m - mn), p = expf(s - mn);
-            m = mn;
-            l = l * al + p;
-#pragma unroll
-            for (int e = 0; e < N; ++e) o[e] = o[e] * al + p * vs * (float)a.vq[cell * D + lane * N + e];
+            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            ex = head_sum_exponent(top);
         }
-        __syncthreads();
+        const float f = (a.softmax_scale < 0.0f ? -1.0f : 1.0f) * exp2i(ex);
+        if (lane == 0) sh.qinv[h] = exp2i(-ex);
+        __half v[N];
+        float sum = 0.0f;
 #pragma unroll
-        for (int e = 0; e < N; ++e) so[warp][lane * N + e] = o[e];
-        if (lane == 0) {
-            sm[warp] = m;
-            sl[warp] = l;
+        for (int e = 0; e < N; ++e) {
+            v[e] = __float2half_rn(x[e] * f);
+            sum += __half2float(v[e]);
         }
-        __syncthreads();
-        float M = -CUDART_INF_F, L = 0.0f;
-        for (int w = 0; w < WARPS; ++w) M = fmaxf(M, sm[w]);
-        for (int w = 0; w < WARPS; ++w) L += M == -CUDART_INF_F ? 0.0f : sl[w] * expf(sm[w] - M);
-        for (int d = threadIdx.x; d < D; d += WARPS * 32) {
-            float r = 0.0f;
-            for (int w = 0; w < WARPS; ++w)
-                if (sm[w] != -CUDART_INF_F) r += expf(sm[w] - M) * so[w][d];
-            if (M != -CUDART_INF_F) r /= L;
-            const size_t i = ((size_t)t * a.n_q_heads + kvh * per + g) * D + d;
-            if (a.gate) r = r / (1.0f + expf(-a.gate[i]));
-            if (a.dtype == QSA_F16)
-                static_cast<__half *>(a.out)[i] = __float2half_rn(r);
-            else
-                static_cast<__nv_bfloat16 *>(a.out)[i] = __float2bfloat16_rn(r);
+        // A scale group is D/4 dims, eight lanes.
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if ((lane & 7) == 0) sh.bias[lane >> 3][h] = -1152.0f * sum;
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const int d = lane * N + e, half = d / DW, dl = d % DW;
+            const int ks = 2 * (dl >> 5) + ((dl >> 2) & 1), r = (dl >> 3) & 3;
+            uint32_t *dst = reinterpret_cast<uint32_t *>(&sh.q[half][ks][(h & 7) * 4 + r]) + (h >> 3);
+            dst[0] = h2u(__halves2half2(v[e], v[e + 2]));
+            dst[2] = h2u(__halves2half2(v[e + 1], v[e + 3]));
         }
-        if (threadIdx.x == 0 && a.lse)
-            a.lse[(size_t)t * a.n_q_heads + kvh * per + g] = M == -CUDART_INF_F ? M : M + logf(L);
     }
-    if (bad && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+}
+
+struct State {
+    float o[16][4];  // o[i][0..1]: head g, dims 16 (2r, 2r + 1) + i; o[i][2..3]: head g + 8
+    float m[2], l[2];
+    int v;  // values are in units of 2^v
+};
+
+// Column n of an 8-cell tile is cell PERM[n].
+__device__ __forceinline__ int perm_cell(int n) { return (0x57136420u >> (4 * n)) & 7; }
+
+// Folds one staged unit into the state.  vmask: the unit's valid cells.
+template <int S>
+__device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vmask, State &st, const float (&sl2)[2],
+                                             int half, int parity) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, r = lane & 3;
+    const uint8_t *K = sh.tile[warp][stage][0], *V = sh.tile[warp][stage][1];
+    const uint2 *KS = sh.scale[warp][stage][0];
+    const uint2 *VS = sh.scale[warp][stage][1];
+    const int kcell = perm_cell(g), c0 = perm_cell(2 * r), c1 = perm_cell(2 * r + 1);
+
+    // Scores: per 32-dim block two k-steps from -1152 sum q, then the scale.
+    float s[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+    constexpr int GB = S;  // 32-dim blocks per scale group
+#pragma unroll
+    for (int gr = 0; gr < 4 / S; ++gr) {
+        const int grp = (S == 2 ? 2 * half : 0) + gr;
+        const float b0 = sh.bias[grp][g], b1 = sh.bias[grp][g + 8];
+        float acc[4][4];
+#pragma unroll
+        for (int bb = 0; bb < GB; ++bb) {
+            const int b = gr * GB + bb;
+            const uint4 q0 = sh.q[S == 2 ? half : 0][2 * b][lane], q1 = sh.q[S == 2 ? half : 0][2 * b + 1][lane];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(K + (8 * j + kcell) * DW +
+                                                                 (((2 * b + (r >> 1)) ^ kcell) << 4) + ((r & 1) << 3));
+                if (bb == 0)
+                    mma16816(acc[j], q0, even_codes(w.x), odd_codes(w.x), b0, b0, b1, b1);
+                else
+                    mma16816(acc[j], q0, even_codes(w.x), odd_codes(w.x), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                mma16816(acc[j], q1, even_codes(w.y), odd_codes(w.y), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __half *k0 = reinterpret_cast<const __half *>(KS + 8 * j + c0);
+            const __half *k1 = reinterpret_cast<const __half *>(KS + 8 * j + c1);
+            const float f0 = __half2float(k0[grp]), f1 = __half2float(k1[grp]);
+            s[j][0] = fmaf(acc[j][0], f0, s[j][0]);
+            s[j][1] = fmaf(acc[j][1], f1, s[j][1]);
+            s[j][2] = fmaf(acc[j][2], f0, s[j][2]);
+            s[j][3] = fmaf(acc[j][3], f1, s[j][3]);
+        }
+    }
+    if constexpr (S == 2) {
+        // The partner's half of the contraction.  Two slots by parity: a slot
+        // is written again only after the partner has passed the next barrier.
+        float *mine = sh.xch + (warp * 2 + parity) * 16 * 32 + lane;
+        const float *other = sh.xch + ((warp ^ 1) * 2 + parity) * 16 * 32 + lane;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mine[i * 32] = s[i >> 2][i & 3];
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] += other[i * 32];
+    }
+    if (vmask != 0xffffffffu) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool v0 = (vmask >> (8 * j + c0)) & 1u, v1 = (vmask >> (8 * j + c1)) & 1u;
+            s[j][0] = v0 ? s[j][0] : -CUDART_INF_F;
+            s[j][1] = v1 ? s[j][1] : -CUDART_INF_F;
+            s[j][2] = v0 ? s[j][2] : -CUDART_INF_F;
+            s[j][3] = v1 ? s[j][3] : -CUDART_INF_F;
+        }
+    }
+
+    // The reference maximum moves only when a unit exceeds it by 2^SLACK, so
+    // the values are rarely rescaled.
+    float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+    float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+    mx0 = fmaxf(mx0, fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
+    mx1 = fmaxf(mx1, fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3])));
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+    }
+    mx0 *= sl2[0];
+    mx1 *= sl2[1];
+    const float mn0 = mx0 > st.m[0] + SLACK ? mx0 : st.m[0], mn1 = mx1 > st.m[1] + SLACK ? mx1 : st.m[1];
+    float al0 = ex2(st.m[0] - mn0), al1 = ex2(st.m[1] - mn1);
+    st.m[0] = mn0;
+    st.m[1] = mn1;
+    float ps0 = 0.0f, ps1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            s[j][e] = ex2(fmaf(s[j][e], sl2[0], -mn0));
+            s[j][e + 2] = ex2(fmaf(s[j][e + 2], sl2[1], -mn1));
+            ps0 += s[j][e];
+            ps1 += s[j][e + 2];
+        }
+    st.l[0] = fmaf(st.l[0], al0, ps0);
+    st.l[1] = fmaf(st.l[1], al1, ps1);
+
+    // The values' power of two: the largest V scale of the first unit, raised
+    // when a later scale would pass 2^8 of it (127 * 2^9 is the fp16 limit).
+    const uint2 own = VS[lane];
+    uint32_t top = __vmaxu2(own.x & 0x7FFF7FFFu, own.y & 0x7FFF7FFFu);
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
+    const int ve = min(max((int)(top >> 10) - 15, -14), 15);
+    if (ve >= st.v + 8) {
+        const float down = exp2i(max(st.v - ve, -126));
+        st.v = ve;
+        al0 *= down;
+        al1 *= down;
+    }
+    if (__any_sync(0xffffffffu, al0 != 1.0f || al1 != 1.0f)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            st.o[i][0] *= al0;
+            st.o[i][1] *= al0;
+            st.o[i][2] *= al1;
+            st.o[i][3] *= al1;
+        }
+    }
+    const __half2 vf = __float2half2_rn(exp2i(-max(st.v, -14)));
+
+    const int vg = S == 1 ? g >> 1 : 2 * half + (g >> 2);
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+        uint4 pa;
+        pa.x = h2u(__floats2half2_rn(s[2 * kk][0], s[2 * kk][1]));
+        pa.y = h2u(__floats2half2_rn(s[2 * kk][2], s[2 * kk][3]));
+        pa.z = h2u(__floats2half2_rn(s[2 * kk + 1][0], s[2 * kk + 1][1]));
+        pa.w = h2u(__floats2half2_rn(s[2 * kk + 1][2], s[2 * kk + 1][3]));
+        uint4 vd[4];
+        __half vs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int cell = 16 * kk + 8 * (e >> 1) + ((e & 1) ? c1 : c0);
+            vd[e] = *reinterpret_cast<const uint4 *>(V + cell * DW + ((g ^ (cell & 7)) << 4));
+            vs[e] = reinterpret_cast<const __half *>(VS + cell)[vg];
+        }
+        const __half2 f01 = __hmul2(__halves2half2(vs[0], vs[1]), vf), f89 = __hmul2(__halves2half2(vs[2], vs[3]), vf);
+        const __half2 off = u2h(0x64806480u);  // 1152
+        auto value = [&](uint32_t codes, __half2 f) { return h2u(__hmul2(__hsub2(u2h(codes), off), f)); };
+        const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&vd[0]), *w1 = reinterpret_cast<const uint32_t *>(&vd[1]);
+        const uint32_t *w8 = reinterpret_cast<const uint32_t *>(&vd[2]), *w9 = reinterpret_cast<const uint32_t *>(&vd[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            // Two cells' bytes side by side: (a0 a1 b0 b1), (a2 a3 b2 b3).
+            const uint32_t l0 = tc::prmt(w0[i], w1[i], 0x5410), h0 = tc::prmt(w0[i], w1[i], 0x7632);
+            const uint32_t l8 = tc::prmt(w8[i], w9[i], 0x5410), h8 = tc::prmt(w8[i], w9[i], 0x7632);
+            float(*o)[4] = st.o + 4 * i;
+            mma16816(o[0], pa, value(even_codes(l0), f01), value(even_codes(l8), f89), o[0][0], o[0][1], o[0][2], o[0][3]);
+            mma16816(o[1], pa, value(odd_codes(l0), f01), value(odd_codes(l8), f89), o[1][0], o[1][1], o[1][2], o[1][3]);
+            mma16816(o[2], pa, value(even_codes(h0), f01), value(even_codes(h8), f89), o[2][0], o[2][1], o[2][2], o[2][3]);
+            mma16816(o[3], pa, value(odd_codes(h0), f01), value(odd_codes(h8), f89), o[3][0], o[3][1], o[3][2], o[3][3]);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i, float x, float y) {
+    if (a.gate) {
+        x = x / (1.0f + expf(-__ldg(a.gate + i)));
+        y = y / (1.0f + expf(-__ldg(a.gate + i + 1)));
+    }
+    if (a.dtype == QSA_F16)
+        *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(x, y);
+    else
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(x, y);
+}
+
+template <int S>
+__global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
+    paged_attn_kernel(const qsa_paged_attn_args a, const __grid_constant__ CUtensorMap kmap,
+                      const __grid_constant__ CUtensorMap vmap) {
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Smem<S> &sh = *reinterpret_cast<Smem<S> *>(raw);
+    constexpr int D = DW * S, NP = NW / S;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, r = lane & 3;
+    const int pw = warp / S, half = warp % S;
+    const int per = a.n_q_heads / a.n_kv_heads, page_shift = 31 - __clz(a.page_size);
+    if (lane == 0) {
+        for (int i = 0; i < NS; ++i) tc::mbar_init(tc::smem_u32(&sh.bar[warp][i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    int share;
+    find_start<S>(a, sh, share);
+    const Work work = carve(a.workspace, per);
+    long long x = (long long)share * blockIdx.x;
+    const long long total = sh.total;
+    if (x >= total) {
+        if (tid == 0) work.part[blockIdx.x] = Part{-1, 0};
+        return;
+    }
+    int left = (int)min((long long)share, total - x);  // units of this share still to do
+    int t = sh.row, trow;
+    bool bad = false, dead = false;
+    int len = row_len(a, t, trow, bad);
+    int nu = units_of(len);
+    int kvh = (int)((x - sh.before) / nu), u0 = (int)((x - sh.before) % nu);
+    uint32_t phase = 0;   // parity of each stage's next completion, one bit per stage
+    uint32_t flying = 0;  // stages with copies in flight
+    Part part{-1, 0};
+    float sl2[2];
+
+    for (bool first = true; left > 0; first = false) {
+        // Segment: units u0 .. u1-1 of (t, kvh).
+        const int u1 = min(nu, u0 + left), n_units = u1 - u0;
+        stage_q<S>(a, sh, t, kvh, per);
+        const int n = n_units > pw ? (n_units - pw + NP - 1) / NP : 0;  // this group's units: u0 + pw + i NP
+        const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
+        auto page_id = [&](int i) -> int {
+            const int c = (u0 + pw + i * NP) * UNIT + lane;
+            return i < n && c < len && QSA_IN(c >> page_shift, a.max_pages) ? __ldg(tab + (c >> page_shift)) : -1;
+        };
+        // Starts the copies of unit i into its stage; returns its valid cells.
+        auto issue = [&](int i, int page) -> unsigned {
+            const int c = (u0 + pw + i * NP) * UNIT + lane;
+            const bool in = i < n && c < len;
+            const bool ok = in && page >= 0 && page < a.n_pages;
+            bad |= in && !ok;
+            const unsigned vmask = __ballot_sync(0xffffffffu, ok);
+            const int stage = i % NS;
+            const size_t cell = ok ? ((size_t)page << page_shift) + (c & (a.page_size - 1)) : 0;
+            const size_t si = (cell * a.n_kv_heads + kvh) * 4;
+            const bool sok = ok && QSA_IN(si + 3, (size_t)a.n_pages * a.page_size * a.n_kv_heads * 4);
+            cp_async8(tc::smem_u32(&sh.scale[warp][stage][0][lane]), a.ksc + (sok ? si : 0), sok);
+            cp_async8(tc::smem_u32(&sh.scale[warp][stage][1][lane]), a.vsc + (sok ? si : 0), sok);
+            asm volatile("cp.async.commit_group;\n" ::);
+            // A box starts on the first cell of a page or of a 32-cell part of one.
+            const int cell16 = __shfl_sync(0xffffffffu, (int)cell, 16);
+            if (vmask && !dead) flying |= 1u << stage;
+            if (lane == 0 && vmask && !dead) {
+                const uint32_t bar = tc::smem_u32(&sh.bar[warp][stage]);
+                const uint32_t k = tc::smem_u32(sh.tile[warp][stage][0]), v = tc::smem_u32(sh.tile[warp][stage][1]);
+                if (a.page_size >= UNIT) {
+                    expect_tx(bar, 2 * TILE);
+                    tma_box(k, &kmap, DW * half, kvh, (int)cell, bar);
+                    tma_box(v, &vmap, DW * half, kvh, (int)cell, bar);
+                } else {
+                    const bool lo = vmask & 0xFFFFu, hi = vmask >> 16;
+                    expect_tx(bar, (lo && hi ? 2 : 1) * TILE);
+                    if (lo) {
+                        tma_box(k, &kmap, DW * half, kvh, (int)cell, bar);
+                        tma_box(v, &vmap, DW * half, kvh, (int)cell, bar);
+                    }
+                    if (hi) {
+                        tma_box(k + TILE / 2, &kmap, DW * half, kvh, cell16, bar);
+                        tma_box(v + TILE / 2, &vmap, DW * half, kvh, cell16, bar);
+                    }
+                }
+            }
+            return vmask;
+        };
+        State st;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.0f;
+        st.m[0] = st.m[1] = -CUDART_INF_F;
+        st.l[0] = st.l[1] = 0.0f;
+        st.v = -64;  // below any scale's exponent: the first unit sets it
+        int next_page = page_id(1);
+        unsigned vmask = issue(0, page_id(0));
+        __syncthreads();  // the query fragments
+        // |scale| in base 2, floored at the smallest normal float: with scale
+        // 0 the weights are uniform and a masked -inf stays -inf.
+        sl2[0] = fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g], 1.17549435e-38f);
+        sl2[1] = fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g + 8], 1.17549435e-38f);
+        int nx = 0;
+        for (int i = 0; i < n; ++i) {
+            const unsigned vnext = issue(i + 1, next_page);  // empty past the last unit
+            next_page = page_id(i + 2);
+            asm volatile("cp.async.wait_group 1;\n" ::);
+            const int stage = i % NS;
+            if (vmask) {
+                if (!dead && !tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][stage]), (phase >> stage) & 1u, tc::WAIT_LIMIT)) {
+                    dead = true;
+                    if (lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_TIMEOUT);
+                }
+                dead = __any_sync(0xffffffffu, dead);
+                if (!dead) {
+                    phase ^= 1u << stage;
+                    flying &= ~(1u << stage);
+                }
+                __syncwarp();
+                compute_unit<S>(sh, stage, vmask, st, sl2, half, nx++ & 1);
+            }
+            __syncwarp();  // every lane has read the stage before it is filled again
+            vmask = vnext;
+        }
+        asm volatile("cp.async.wait_group 0;\n" ::);
+        if (flying) {  // after a time-out: copies in flight land before the tiles are used again or given up
+            for (int i = 0; i < NS; ++i)
+                if ((flying >> i) & 1u) tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][i]), (phase >> i) & 1u, tc::DRAIN_LIMIT);
+            flying = 0;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
+            st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
+        }
+        __syncthreads();  // all warps are done with the tiles and the fragments
+
+        // Join the groups' states.  Value (h, d) of group w sits at (16 w + h) D
+        // + (d ^ 4 x), x = 2 (d / 32) + (h & 1): the eight lanes that a 16-byte
+        // store serves at a time then hit eight different bank groups, and
+        // reads of consecutive d stay consecutive.
+        float *so = reinterpret_cast<float *>(sh.tile);
+        float *ow = so + pw * 16 * D + DW * half;
+        const int sw = 4 * ((2 * r + (g & 1)) & 7);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            // Columns 2r, 2r + 1 of a V tile are dims 32 r + i and 32 r + 16 + i.
+            const int d0 = (32 * r + i) ^ sw, d1 = (32 * r + 16 + i) ^ sw;
+            *reinterpret_cast<float4 *>(ow + g * D + d0) = make_float4(st.o[i][0], st.o[i + 1][0], st.o[i + 2][0], st.o[i + 3][0]);
+            *reinterpret_cast<float4 *>(ow + g * D + d1) = make_float4(st.o[i][1], st.o[i + 1][1], st.o[i + 2][1], st.o[i + 3][1]);
+            *reinterpret_cast<float4 *>(ow + (g + 8) * D + d0) =
+                make_float4(st.o[i][2], st.o[i + 1][2], st.o[i + 2][2], st.o[i + 3][2]);
+            *reinterpret_cast<float4 *>(ow + (g + 8) * D + d1) =
+                make_float4(st.o[i][3], st.o[i + 1][3], st.o[i + 2][3], st.o[i + 3][3]);
+        }
+        if (r == 0 && half == 0) {
+            sh.m[pw][g] = st.m[0];
+            sh.m[pw][g + 8] = st.m[1];
+            sh.l[pw][g] = st.l[0];
+            sh.l[pw][g + 8] = st.l[1];
+        }
+        if (lane == 0 && half == 0) sh.v[pw] = st.v;  // both halves see all four scale groups: the same
+        __syncthreads();
+        const bool whole = n_units == nu;
+        const int slot = !first || u0 == 0 ? 1 : 0;
+        const size_t at = (size_t)blockIdx.x * 2 + slot;
+        if (tid < 16) {
+            float M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NP; ++w) M = fmaxf(M, sh.m[w][tid]);
+            float f[NP];
+#pragma unroll
+            for (int w = 0; w < NP; ++w) {
+                f[w] = sh.m[w][tid] == -CUDART_INF_F ? 0.0f : exp2f(sh.m[w][tid] - M);
+                L += f[w] * sh.l[w][tid];
+            }
+            const float inv = whole ? (M == -CUDART_INF_F ? 0.0f : 1.0f / L) : 1.0f;
+#pragma unroll
+            for (int w = 0; w < NP; ++w) sh.f[w][tid] = f[w] * inv * (f[w] == 0.0f ? 0.0f : exp2i(sh.v[w]));
+            if (tid < per) {
+                if (whole) {
+                    if (a.lse) a.lse[(size_t)t * a.n_q_heads + kvh * per + tid] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+                } else {
+                    work.ml[(at * per + tid) * 2] = M;
+                    work.ml[(at * per + tid) * 2 + 1] = L;
+                }
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < per * (D / 2); i += NW * 32) {
+            const int h = i / (D / 2), d = 2 * (i % (D / 2));
+            const int pd = d ^ (4 * ((2 * (d >> 5) + (h & 1)) & 7));
+            float o0 = 0.0f, o1 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NP; ++w) {
+                const float f = sh.f[w][h];
+                const float2 o = *reinterpret_cast<const float2 *>(so + (w * 16 + h) * D + pd);
+                o0 = fmaf(f, o.x, o0);
+                o1 = fmaf(f, o.y, o1);
+            }
+            if (whole) {
+                const size_t oi = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + d;
+                if (QSA_IN(oi + 1, (size_t)a.n_tokens * a.n_q_heads * D)) store_out(a, oi, o0, o1);
+            } else {
+                *reinterpret_cast<float2 *>(work.o + (at * per + h) * D + d) = make_float2(o0, o1);
+            }
+        }
+        if (!whole && u0 == 0) part = Part{t * a.n_kv_heads + kvh, 1 + (nu - u1 + share - 1) / share};
+        left -= n_units;
+        u0 = 0;
+        if (left > 0 && ++kvh == a.n_kv_heads) {
+            kvh = 0;
+            len = row_len(a, ++t, trow, bad);
+            nu = units_of(len);
+        }
+        tc::fence_async_smem();  // the tiles are written by copies again
+        __syncthreads();
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+    if (tid == 0) work.part[blockIdx.x] = part;
+}
+
+// Joins the partials of the pair that starts in CTA blockIdx.x and spans
+// others: part p is slot 1 of that CTA, then slot 0 of the next ones.  One
+// block per (CTA, query head); G groups of threads take every G-th part.
+template <int S>
+__global__ void __launch_bounds__(512) paged_join_kernel(const qsa_paged_attn_args a) {
+    constexpr int D = DW * S, T2 = D / 2, G = 512 / T2;
+    __shared__ float w[MAX_CTAS], red[16], red2[16];
+    __shared__ float2 so[G][T2];
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    const int per = a.n_q_heads / a.n_kv_heads, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Work work = carve(a.workspace, per);
+    const Part part = work.part[blockIdx.x];
+    if (part.task < 0) return;
+    auto slot = [&](int p) { return (size_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0); };
+    float m = -CUDART_INF_F, l = 0.0f;
+    if (tid < part.n) {
+        m = work.ml[(slot(tid) * per + h) * 2];
+        l = work.ml[(slot(tid) * per + h) * 2 + 1];
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (lane == 0) red[warp] = M;
+    __syncthreads();
+    M = red[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) M = fmaxf(M, red[i]);
+    const float f = m == -CUDART_INF_F ? 0.0f : exp2f(m - M);
+    if (tid < part.n) w[tid] = f;
+    float L = f * l;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) red2[warp] = L;
+    __syncthreads();
+    L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) L += red2[i];
+    const int grp = tid / T2, d = 2 * (tid % T2);
+    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = grp; p < part.n; p += G) {
+        const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(p) * per + h) * D + d);
+        o.x = fmaf(w[p], v.x, o.x);
+        o.y = fmaf(w[p], v.y, o.y);
+    }
+    so[grp][tid % T2] = o;
+    __syncthreads();
+    if (grp) return;
+    o = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+        o.x += so[i][tid].x;
+        o.y += so[i][tid].y;
+    }
+    const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
+    const size_t row = (size_t)(part.task / a.n_kv_heads) * a.n_q_heads + (size_t)(part.task % a.n_kv_heads) * per + h;
+    if (tid == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+    if (QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) store_out(a, row * D + d, o.x * inv, o.y * inv);
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// Codes [cells, heads, D] in boxes of up to 32 cells x one head x 128 dims.
+cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t *codes) {
+    const EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads, (cuuint64_t)a.n_pages * a.page_size};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads * a.head_dim};
+    const cuuint32_t box[3] = {DW, 1, (cuuint32_t)(a.page_size < UNIT ? a.page_size : UNIT)}, ones[3] = {1, 1, 1};
+    const CUresult e = fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(codes), dims, strides, box, ones,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int S>
+cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
+    CUtensorMap kmap, vmap;
+    cudaError_t e = encode(kmap, a, a.kq);
+    if (e == cudaSuccess) e = encode(vmap, a, a.vq);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(paged_attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
+    if (e != cudaSuccess) return e;
+    // One share per resident CTA, or fewer where the table cannot hold as many units.
+    const long long most = (long long)a.n_tokens * a.n_kv_heads * (((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT);
+    const long long shares = (most + MIN_SHARE - 1) / MIN_SHARE, resident = 152 * (S == 1 ? 3 : 2);
+    const int grid = (int)(shares < resident ? shares : resident);
+    e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(paged_join_kernel<S>, dim3(grid, a.n_q_heads / a.n_kv_heads), dim3(512), 0, s, a);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace_bytes(int, int, int) { return 256; }
+size_t paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
+    const int per = n_q_heads / n_kv_heads;
+    const Work w = carve(nullptr, per);
+    return reinterpret_cast<uintptr_t>(w.o) + (size_t)MAX_CTAS * 2 * per * head_dim * sizeof(float);
+}
 
 cudaError_t launch_paged_attn(const qsa_paged_attn_args &a, cudaStream_t s) {
-    const dim3 grid(a.n_tokens * a.n_kv_heads), block(WARPS * 32);
-    return a.head_dim == 128 ? launch_dependent(paged_attn_kernel<128>, grid, block, 0, s, a)
-                             : launch_dependent(paged_attn_kernel<256>, grid, block, 0, s, a);
+    return a.head_dim == 128 ? launch<1>(a, s) : launch<2>(a, s);
 }
 
 }  // namespace qsa

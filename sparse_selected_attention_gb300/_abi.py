@@ -133,6 +133,20 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_packed = {}
+
+
+def packed(name: str):
+    """The release library's `name`, taking its argument struct as packed bytes."""
+    f = _packed.get(name)
+    if f is None:
+        f = lib()[name]  # a function object of its own: the attribute keeps its argtypes
+        f.argtypes = [ctypes.c_char_p, _vp]
+        f.restype = _c_int
+        _packed[name] = f
+    return f
+
+
 def _declare(L: ctypes.CDLL, path: str) -> None:
     for name, argt in (("qsa_prep", PrepArgs), ("qsa_score", ScoreArgs), ("qsa_attn", AttnArgs),
                        ("qsa_score_noalloc", ScoreArgs), ("qsa_select", SelectArgs),

@@ -188,7 +188,7 @@ def test_null_args_and_workspace_sizes(L):
         assert L.qsa_paged_attn_workspace_bytes(*bad) == 0
 
 
-def test_binding_refuses_cpu_tensors_and_shapes():
+def test_binding_refuses_cpu_tensors():
     import torch
 
     import sparse_selected_attention_gb300 as qsa
@@ -197,19 +197,21 @@ def test_binding_refuses_cpu_tensors_and_shapes():
     q = torch.zeros(2, 12, 128, dtype=torch.float16)
     tab, lens = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     ws = torch.zeros(1 << 20, dtype=torch.uint8)
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        qsa.qsa_paged_attn(q, kq, kq, ksc, ksc, tab, lens, q.clone(), ws)
-    with pytest.raises(ValueError, match="vq"):
-        qsa.qsa_paged_attn(q, kq, kq[:2], ksc, ksc, tab, lens, q.clone(), ws)
-    with pytest.raises(ValueError, match="seq_lens"):
-        qsa.qsa_paged_attn(q, kq, kq, ksc, ksc, tab, lens[:1], q.clone(), ws)
-    with pytest.raises(ValueError, match="float16 or bfloat16"):
-        qsa.qsa_paged_attn(q.float(), kq, kq, ksc, ksc, tab, lens, q.float(), ws)
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        qsa.qsa_paged_prep(q, q[:, :1], q[:, :1], lens, lens, kq, kq, ksc, ksc, q.clone())
-    with pytest.raises(ValueError, match="rows and page_table"):
-        qsa.qsa_paged_gather(kq, kq, ksc, ksc, lens, q[:, :1], q[:, :1], rows=lens)
-    with pytest.raises(ValueError, match="page_table"):
-        qsa.qsa_page_update(tab, lens, None, lens, kq, kq, ksc, ksc, tab[:, :1], lens, lens, lens, lens, ws)
-    with pytest.raises(ValueError, match="refs"):
-        qsa.qsa_page_compact(tab, lens, kq, kq, ksc, ksc, tab, lens, lens, lens, ws)
+    for call in (lambda: qsa.qsa_paged_attn(q, kq, kq, ksc, ksc, tab, lens, q.clone(), ws),
+                 lambda: qsa.qsa_paged_prep(q, q[:, :1], q[:, :1], lens, lens, kq, kq, ksc, ksc, q.clone()),
+                 lambda: qsa.qsa_paged_gather(kq, kq, ksc, ksc, lens, q[:, :1], q[:, :1]),
+                 lambda: qsa.qsa_page_update(tab, lens, None, lens, kq, kq, ksc, ksc, tab, lens, lens, lens, lens, ws),
+                 lambda: qsa.qsa_page_compact(tab, lens, kq, kq, ksc, ksc, tab, lens, lens, lens[:1], ws)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
+    with pytest.raises(AttributeError):
+        qsa.no_such_call
+
+
+def test_packed_arguments_are_the_structs():
+    """The bytes that the binding packs are the ctypes mirrors' bytes."""
+    from sparse_selected_attention_gb300 import paged
+    for cls, fmt in paged._FORMAT.items():
+        assert fmt.size == ctypes.sizeof(cls)
+        vals = [float(i) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(cls._fields_)]
+        assert bytes(cls(*vals)) == fmt.pack(*vals)

@@ -722,5 +722,62 @@ def test_binding_streams(cuda_device):
     qsa.qsa_paged_gather(*pd, ids, a, b, stream=side)
     side.synchronize()
     assert torch.equal(a[0], a[1]) and a.any()
-    with pytest.raises(ValueError, match="CUDA tensor"):
-        qsa.qsa_paged_gather(*pd, ids, a.cpu(), b)
+
+
+def test_binding_refuses(cuda_device):
+    """What only the binding can see: devices, dtypes, shapes, contiguity."""
+    z = lambda *v, t=torch.int32: torch.zeros(v, dtype=t, device="cuda")  # noqa: E731
+    kq, ksc = z(2, 4, 16, 1, 128, t=torch.int8), z(2, 4, 16, 1, 4, t=F16)
+    lay = (kq[0], kq[1], ksc[0], ksc[1])
+    q, tab, lens, ws = z(2, 12, 128, t=F16), z(2, 2), z(2), z(1 << 24, t=torch.uint8)
+
+    def refused(match, fn, *args, **kw):
+        with pytest.raises((ValueError, qsa.QSAError), match=match):
+            fn(*args, **kw)
+
+    attn = qsa.qsa_paged_attn
+    refused("CUDA tensor", attn, q, *lay, tab, lens, q.cpu(), ws)
+    refused("CUDA tensor", attn, q, *lay, tab, lens.cpu(), q, ws)
+    refused("vq must be", attn, q, lay[0], lay[1][:2], *lay[2:], tab, lens, q, ws)
+    refused("ksc must be", attn, q, *lay[:2], lay[2][..., :2], lay[3], tab, lens, q, ws)
+    refused("kq must be", attn, q, *[x.flatten(0, 1) for x in lay], tab, lens, q, ws)
+    refused("seq_lens must be", attn, q, *lay, tab, lens[:1], q, ws)
+    refused("seq_lens must be", attn, q, *lay, tab, lens.long(), q, ws)
+    refused("rows must be", attn, q, *lay, tab, lens, q, ws, rows=z(3))
+    refused("float16 or bfloat16", attn, q.float(), *lay, tab, lens, q.float(), ws)
+    refused("out must be", attn, q, *lay, tab, lens, q.to(BF16), ws)
+    refused("contiguous", attn, q.transpose(0, 1).contiguous().transpose(0, 1), *lay, tab, lens, q, ws)
+    refused("gate must be", attn, q, *lay, tab, lens, q, ws, gate=q)
+    refused("page_table must be", attn, q, *lay, tab[0], lens, q, ws)
+    refused("workspace", attn, q, *lay, tab, lens, q, ws.cpu())
+    refused("workspace smaller", attn, q, *lay, tab, lens, q, ws[:256])
+    refused("row per token", attn, q, *lay, tab[:1], lens, q, ws)
+    refused("err must be", attn, q, *lay, tab, lens, q, ws, err=torch.zeros(1, dtype=torch.int32))
+    prep = qsa.qsa_paged_prep
+    x = z(2, 14, 128, t=F16)
+    a = (x[:, :12], x[:, 12:13], x[:, 13:])
+    refused("k_in must be", prep, a[0], a[1].float(), a[2], lens, lens, *lay, q)
+    refused("k_in must be", prep, a[0], x[:, 11:13], a[2], lens, lens, *lay, q)
+    refused("contiguous", prep, x[:, ::2][:, :6], a[1], a[2], lens, lens, *lay, q[:, :6].contiguous())
+    refused("slots must be", prep, *a, lens, lens[:1], *lay, q)
+    refused("q_norm_w must be", prep, *a, lens, lens, *lay, q, q_norm_w=z(64, t=F32))
+    refused("inv_freq", prep, *a, lens, lens, *lay, q, inv_freq=z(2, 2, t=F32))
+    refused("rope_dims", prep, *a, lens, lens, *lay, q, inv_freq=z(3, t=F32))
+    refused("q_out", prep, *a, lens, lens, *lay, q.float())
+    refused("strides", prep, x[:1, :12].expand(2, 12, 128), a[1], a[2], lens, lens, *lay, q)
+    out = z(2, 1, 128, t=F32)
+    refused("go together", qsa.qsa_paged_gather, *lay, lens, out, out, rows=lens)
+    refused("v_out must be", qsa.qsa_paged_gather, *lay, lens, out, out.half())
+    refused("k_out must be", qsa.qsa_paged_gather, *lay, lens, z(2, 2, 128, t=F32), out)
+    pool = (kq, kq.clone(), ksc, ksc.clone())
+    upd = lambda **kw: {**dict(page_table=tab, seq_lens=lens, src=None, n_new=lens, page_table_out=z(2, 2), seq_lens_out=z(2),  # noqa: E731
+                               refs=z(4), slots=lens, positions=z(2), workspace=ws), **kw}
+    call = lambda kq=None, **kw: qsa.qsa_page_update(kq=pool[0], vq=pool[1], ksc=pool[2], vsc=pool[3], **upd(**kw))  # noqa: E731
+    refused("page_table_out must be", call, page_table_out=z(2, 3))
+    refused("refs must be", call, refs=z(5))
+    refused("positions must be", call, positions=z(3))
+    refused("src must be", call, src=z(3))
+    refused("may be the old ones only without src", call, src=lens, page_table_out=tab)
+    refused("may be the old ones only without src", call, src=lens, seq_lens_out=lens)
+    refused("page_map must be", qsa.qsa_page_compact, tab, lens, *pool, z(2, 2), z(4), z(3), z(1), ws)
+    refused("n_live must be", qsa.qsa_page_compact, tab, lens, *pool, z(2, 2), z(4), z(4), z(2), ws)

@@ -19,7 +19,8 @@ def use_library(monkeypatch):
     """Routes the binding's calls to a variant of the library."""
     def use(name):
         L = _abi.variant(name)
-        monkeypatch.setattr(qsa, "lib", lambda: L)
+        monkeypatch.setattr(_abi, "lib", lambda: L)
+        monkeypatch.setattr(_abi, "_packed", {})
         return L
     yield use
 

@@ -6,14 +6,16 @@
 // reading the cache: 2 D + 16 bytes per (cell, KV head) against 4 D flops per
 // query head, 23 flops per byte at 12 heads.
 //
-// Work.  A row's cells are taken in units of 32.  The units of all (row, KV
-// head) pairs, in that order, are cut into equal shares, one per CTA, so one
-// long row or a ragged batch fills the chip alike and the share does not
-// depend on the table's width.  A share that holds all of a pair writes its
-// output; a pair that spans CTAs leaves one partial per CTA in the workspace
-// (values, maximum, sum), and a second launch joins them.  Each CTA finds its
-// place by summing the rows' lengths itself, which costs one pass over
-// seq_lens and saves a launch.
+// Work.  A row's cells are taken in units of 32.  The units of all rows are
+// cut into equal shares, one per CTA of each KV head, so one long row or a
+// ragged batch fills the chip alike and the share does not depend on the
+// table's width.  The KV heads of a share are neighbouring CTAs: they walk the
+// same cells together, so that a cell's scales, eight bytes per head, come
+// from DRAM once for all heads of a 32-byte sector.  A share that holds all of
+// a row writes its output; a row that spans CTAs leaves one partial per CTA in
+// the workspace (values, maximum, sum), and a second launch joins them.  Each
+// CTA finds its place by summing the rows' lengths itself, which costs one
+// pass over seq_lens and saves a launch.
 //
 // A unit.  The query heads of one KV head are the M side (padded to 16) of
 // m16n8k16 products, cells are N of Q.K and the contraction of P.V.  (tcgen05
@@ -40,6 +42,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
+
+#include <algorithm>
 
 #include "check.cuh"
 #include "qsa_internal.h"
@@ -114,7 +118,7 @@ struct Smem {
 };
 
 struct Part {
-    int task, n;  // (row * n_kv_heads + KV head, CTAs that share it), task -1: none starts here
+    int row, n;  // the row that starts in this CTA and spans n CTAs of its KV head; row -1: none
 };
 
 struct Work {
@@ -148,10 +152,11 @@ __device__ __forceinline__ int row_len(const qsa_paged_attn_args &a, int t, int 
 }
 __device__ __forceinline__ int units_of(int len) { return max((len + UNIT - 1) / UNIT, 1); }
 
-// Sums the rows' units and finds the row that holds unit share * blockIdx.x.
+// Sums the rows' units and finds the row that holds unit share * range, of
+// `ranges` shares.
 // Each thread takes a run of rows.
 template <int S>
-__device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int &share) {
+__device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int &share) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (a.n_tokens + NW * 32 - 1) / (NW * 32);
     const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
@@ -159,7 +164,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     long long mine = 0;
     for (int t = t0; t < t1; ++t) {
         int row;
-        mine += (long long)units_of(row_len(a, t, row, bad)) * a.n_kv_heads;
+        mine += units_of(row_len(a, t, row, bad));
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     long long s = mine;
@@ -177,13 +182,13 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
         total += sh.scan[w];
     }
     before += s - mine;
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    const long long per = (total + ranges - 1) / ranges;
     share = (int)max(per, (long long)MIN_SHARE);
-    const long long x0 = (long long)share * blockIdx.x;
+    const long long x0 = (long long)share * range;
     if (x0 >= before && x0 < before + mine) {
         for (int t = t0;; ++t) {
             int row;
-            const long long u = (long long)units_of(row_len(a, t, row, bad)) * a.n_kv_heads;
+            const int u = units_of(row_len(a, t, row, bad));
             if (x0 < before + u) {
                 sh.row = t;
                 sh.before = before;
@@ -443,13 +448,14 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
     }
     wait_for_previous_grid();
     allow_dependent_launch();
+    const int kvh = blockIdx.x % a.n_kv_heads, range = blockIdx.x / a.n_kv_heads, ranges = gridDim.x / a.n_kv_heads;
     int share;
-    find_start<S>(a, sh, share);
+    find_start<S>(a, sh, range, ranges, share);
     const Work work = carve(a.workspace, per);
-    long long x = (long long)share * blockIdx.x;
+    const long long x = (long long)share * range;
     const long long total = sh.total;
     if (x >= total) {
-        if (tid == 0) work.part[blockIdx.x] = Part{-1, 0};
+        if (tid == 0 && ranges > 1) work.part[blockIdx.x] = Part{-1, 0};
         return;
     }
     int left = (int)min((long long)share, total - x);  // units of this share still to do
@@ -457,21 +463,21 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
     bool bad = false, dead = false;
     int len = row_len(a, t, trow, bad);
     int nu = units_of(len);
-    int kvh = (int)((x - sh.before) / nu), u0 = (int)((x - sh.before) % nu);
+    int u0 = (int)(x - sh.before);
     uint32_t phase = 0;   // parity of each stage's next completion, one bit per stage
     uint32_t flying = 0;  // stages with copies in flight
     Part part{-1, 0};
     float sl2[2];
 
     for (bool first = true; left > 0; first = false) {
-        // Segment: units u0 .. u1-1 of (t, kvh).
+        // Segment: units u0 .. u1-1 of row t.
         const int u1 = min(nu, u0 + left), n_units = u1 - u0;
         stage_q<S>(a, sh, t, kvh, per);
         const int n = n_units > pw ? (n_units - pw + NP - 1) / NP : 0;  // this group's units: u0 + pw + i NP
         const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
         auto page_id = [&](int i) -> int {
             const int c = (u0 + pw + i * NP) * UNIT + lane;
-            return i < n && c < len && QSA_IN(c >> page_shift, a.max_pages) ? __ldg(tab + (c >> page_shift)) : -1;
+            return i < n && (c >> page_shift) < a.max_pages ? __ldg(tab + (c >> page_shift)) : -1;
         };
         // Starts the copies of unit i into its stage; returns its valid cells.
         auto issue = [&](int i, int page) -> unsigned {
@@ -630,11 +636,10 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
                 *reinterpret_cast<float2 *>(work.o + (at * per + h) * D + d) = make_float2(o0, o1);
             }
         }
-        if (!whole && u0 == 0) part = Part{t * a.n_kv_heads + kvh, 1 + (nu - u1 + share - 1) / share};
+        if (!whole && u0 == 0) part = Part{t, 1 + (nu - u1 + share - 1) / share};
         left -= n_units;
         u0 = 0;
-        if (left > 0 && ++kvh == a.n_kv_heads) {
-            kvh = 0;
+        if (left > 0) {
             len = row_len(a, ++t, trow, bad);
             nu = units_of(len);
         }
@@ -642,12 +647,12 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
         __syncthreads();
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
-    if (tid == 0) work.part[blockIdx.x] = part;
+    if (tid == 0 && ranges > 1) work.part[blockIdx.x] = part;
 }
 
-// Joins the partials of the pair that starts in CTA blockIdx.x and spans
-// others: part p is slot 1 of that CTA, then slot 0 of the next ones.  One
-// block per (CTA, query head); G groups of threads take every G-th part.
+// Joins the partials of the row that starts in CTA blockIdx.x and spans
+// others: part p is slot 1 of that CTA, then slot 0 of the next ones of its KV
+// head.  One block per (CTA, query head); G groups of threads take every G-th part.
 template <int S>
 __global__ void __launch_bounds__(512) paged_join_kernel(const qsa_paged_attn_args a) {
     constexpr int D = DW * S, T2 = D / 2, G = 512 / T2;
@@ -658,8 +663,8 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const qsa_paged_attn_ar
     const int per = a.n_q_heads / a.n_kv_heads, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Work work = carve(a.workspace, per);
     const Part part = work.part[blockIdx.x];
-    if (part.task < 0) return;
-    auto slot = [&](int p) { return (size_t)(blockIdx.x + p) * 2 + (p == 0 ? 1 : 0); };
+    if (part.row < 0) return;
+    auto slot = [&](int p) { return (size_t)(blockIdx.x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0); };
     float m = -CUDART_INF_F, l = 0.0f;
     if (tid < part.n) {
         m = work.ml[(slot(tid) * per + h) * 2];
@@ -701,7 +706,7 @@ __global__ void __launch_bounds__(512) paged_join_kernel(const qsa_paged_attn_ar
         o.y += so[i][tid].y;
     }
     const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
-    const size_t row = (size_t)(part.task / a.n_kv_heads) * a.n_q_heads + (size_t)(part.task % a.n_kv_heads) * per + h;
+    const size_t row = (size_t)part.row * a.n_q_heads + (size_t)(blockIdx.x % a.n_kv_heads) * per + h;
     if (tid == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
     if (QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) store_out(a, row * D + d, o.x * inv, o.y * inv);
 }
@@ -743,12 +748,14 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
     if (e != cudaSuccess) return e;
-    // One share per resident CTA, or fewer where the table cannot hold as many units.
-    const long long most = (long long)a.n_tokens * a.n_kv_heads * (((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT);
-    const long long shares = (most + MIN_SHARE - 1) / MIN_SHARE, resident = 152 * (S == 1 ? 3 : 2);
-    const int grid = (int)(shares < resident ? shares : resident);
+    // A share per resident CTA, or fewer where the table cannot hold as many
+    // units.  With one share per KV head no row spans CTAs, and there may be
+    // more CTAs than the workspace has places for.
+    const long long most = (long long)a.n_tokens * (((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT);
+    const long long shares = (most + MIN_SHARE - 1) / MIN_SHARE, resident = std::max(152 * (S == 1 ? 3 : 2) / a.n_kv_heads, 1);
+    const int ranges = (int)(shares < resident ? shares : resident), grid = ranges * a.n_kv_heads;
     e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || ranges == 1) return e;
     return launch_dependent(paged_join_kernel<S>, dim3(grid, a.n_q_heads / a.n_kv_heads), dim3(512), 0, s, a);
 }
 

@@ -24,17 +24,17 @@
 // its units through a ring of two stages, each filled by two TMA boxes of 32
 // rows x 128 bytes (four of 16 rows where a page has 16) and eight-byte
 // cp.async for the scales.  The boxes carry the 128-byte swizzle, and cells
-// and dims are assigned to lanes so that every fragment read meets all banks
-// once (K: two passes):
-//   cell of column n of an 8-column tile: PERM[n] = 0 2 4 6 3 1 7 5
-//   K dims of lane (g, r), k-step (b, h): 32 b + 8 r + 4 h + {0, 2 | 1, 3}
-//   V dims of lane (g, r): 16 g .. 16 g + 15
+// and dims are assigned to lanes so that no fragment read meets a bank twice:
+//   lane (g, r) = (lane / 4, lane % 4) holds cells 4 r .. 4 r + 3 of each 16:
+//   column n of score tile j is cell 16 (j / 2) + 2 n + j % 2;
+//   K (eight bytes a read): dims 32 b + 8 r + 4 h + {0, 2 | 1, 3} of k-step (b, h);
+//   V (transposed 16 x 16 byte matrices): tile t holds dims 8 t .. 8 t + 7.
 // Codes become fp16 integers by or-ing 0x6400 to the code + 128 (1024 + 128 +
 // code).  For K the 1152 stays: the accumulators start at -1152 * sum q, so
 // the products give q . code exactly, per scale group, and the group's scale
-// multiplies in fp32.  For V it is subtracted and the cell's scale multiplied
-// in fp16, under a power of two per warp that keeps small scales out of the
-// subnormals.
+// multiplies in fp32.  For V it is subtracted, and the scales go to the
+// weights, a set of fp16 weights per scale group, under a power of two per
+// warp that keeps small scales out of the subnormals.
 //
 // With head_dim 256 two warps share a unit, each with 128 dims of K and V;
 // their partial scores meet in shared memory.
@@ -77,6 +77,22 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__
 __device__ __forceinline__ uint32_t even_codes(uint32_t w) { return (w & 0x00FF00FFu) ^ 0x64806480u; }
 __device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u; }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// 16 x 16 bytes of V, cells as rows, from cells 0-15 and 16-31: register 0 (1)
+// holds cells 4 r .. 4 r + 3 of dim g (g + 8), registers 2 and 3 the same of
+// cells 16 on.
+__device__ __forceinline__ void load_v(uint32_t (&w)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1, float c0, float c1,
                                          float c2, float c3) {
     asm volatile(
@@ -106,7 +122,7 @@ struct Smem {
     uint8_t tile[NW][NS][2][TILE];  // K, V; 1024-byte aligned
     uint2 scale[NW][NS][2][UNIT];   // four fp16 per cell: ksc, vsc
     uint4 q[S][8][32];              // Q fragments by k-step and lane
-    float bias[4][16];              // -1152 * sum of q over a scale group, per head (see stage_q)
+    float bias[4][8][4];            // -1152 * sum of q over a scale group, as accumulators: heads g, g, g + 8, g + 8
     float qinv[16];                 // 2^-e of a head's scaled query
     float xch[S == 2 ? NW * 2 * 16 * 32 : 1];
     float m[NW / S][16], l[NW / S][16], f[NW / S][16];
@@ -244,7 +260,8 @@ __device__ __forceinline__ void stage_q(const qsa_paged_attn_args &a, Smem<S> &s
         // A scale group is D/4 dims, eight lanes.
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if ((lane & 7) == 0) sh.bias[lane >> 3][h] = -1152.0f * sum;
+        if ((lane & 7) == 0)
+            *reinterpret_cast<float2 *>(&sh.bias[lane >> 3][h & 7][2 * (h >> 3)]) = make_float2(-1152.0f * sum, -1152.0f * sum);
 #pragma unroll
         for (int e = 0; e < N; e += 4) {
             const int d = lane * N + e, half = d / DW, dl = d % DW;
@@ -257,166 +274,183 @@ __device__ __forceinline__ void stage_q(const qsa_paged_attn_args &a, Smem<S> &s
 }
 
 struct State {
-    float o[16][4];  // o[i][0..1]: head g, dims 16 (2r, 2r + 1) + i; o[i][2..3]: head g + 8
+    float o[16][4];  // o[t][0..1]: head g, dims 8 t + 2 r, 8 t + 2 r + 1; o[t][2..3]: head g + 8
     float m[2], l[2];
     int v;  // values are in units of 2^v
 };
-
-// Column n of an 8-cell tile is cell PERM[n].
-__device__ __forceinline__ int perm_cell(int n) { return (0x57136420u >> (4 * n)) & 7; }
 
 // Folds one staged unit into the state.  vmask: the unit's valid cells.
 template <int S>
 __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vmask, State &st, const float (&sl2)[2],
                                              int half, int parity) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, r = lane & 3;
-    const uint8_t *K = sh.tile[warp][stage][0], *V = sh.tile[warp][stage][1];
-    const uint2 *KS = sh.scale[warp][stage][0];
-    const uint2 *VS = sh.scale[warp][stage][1];
-    const int kcell = perm_cell(g), c0 = perm_cell(2 * r), c1 = perm_cell(2 * r + 1);
+    constexpr int NG = 4 / S;  // scale groups of this warp's dims
+    // Row 2 g of K with the swizzle of its first 16 bytes for this lane, and row 2 g + 1.
+    const uint32_t kt = tc::smem_u32(sh.tile[warp][stage][0]) + 2 * g * DW + ((r & 1) << 3);
+    const uint32_t keven = kt + (((r >> 1) ^ ((2 * g) & 7)) << 4), kodd = kt + DW + (((r >> 1) ^ ((2 * g + 1) & 7)) << 4);
 
-    // Scores: per 32-dim block two k-steps from -1152 sum q, then the scale.
-    float s[4][4];
+    // Scores: per scale group S 32-dim blocks of two k-steps from -1152 sum q,
+    // then the scale.
+    float2 s[4][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
-    constexpr int GB = S;  // 32-dim blocks per scale group
+    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = make_float2(0.0f, 0.0f);
+    uint4 ks[2][2];  // scales of cells 16 kk + 4 r .. + 3
 #pragma unroll
-    for (int gr = 0; gr < 4 / S; ++gr) {
-        const int grp = (S == 2 ? 2 * half : 0) + gr;
-        const float b0 = sh.bias[grp][g], b1 = sh.bias[grp][g + 8];
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            ks[kk][i] = *reinterpret_cast<const uint4 *>(&sh.scale[warp][stage][0][16 * kk + 4 * r + 2 * i]);
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        const float4 bias = *reinterpret_cast<const float4 *>(sh.bias[(S == 2 ? 2 * half : 0) + gr][g]);
         float acc[4][4];
 #pragma unroll
-        for (int bb = 0; bb < GB; ++bb) {
-            const int b = gr * GB + bb;
+        for (int bb = 0; bb < S; ++bb) {
+            const int b = gr * S + bb;
             const uint4 q0 = sh.q[S == 2 ? half : 0][2 * b][lane], q1 = sh.q[S == 2 ? half : 0][2 * b + 1][lane];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(K + (8 * j + kcell) * DW +
-                                                                 (((2 * b + (r >> 1)) ^ kcell) << 4) + ((r & 1) << 3));
+                uint32_t w0, w1;
+                asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                             : "=r"(w0), "=r"(w1)
+                             : "r"((((j & 1) ? kodd : keven) ^ (b << 5)) + (j >> 1) * 16 * DW)
+                             : "memory");
                 if (bb == 0)
-                    mma16816(acc[j], q0, even_codes(w.x), odd_codes(w.x), b0, b0, b1, b1);
+                    mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), bias.x, bias.y, bias.z, bias.w);
                 else
-                    mma16816(acc[j], q0, even_codes(w.x), odd_codes(w.x), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                mma16816(acc[j], q1, even_codes(w.y), odd_codes(w.y), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                    mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                mma16816(acc[j], q1, even_codes(w1), odd_codes(w1), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
             }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const __half *k0 = reinterpret_cast<const __half *>(KS + 8 * j + c0);
-            const __half *k1 = reinterpret_cast<const __half *>(KS + 8 * j + c1);
-            const float f0 = __half2float(k0[grp]), f1 = __half2float(k1[grp]);
-            s[j][0] = fmaf(acc[j][0], f0, s[j][0]);
-            s[j][1] = fmaf(acc[j][1], f1, s[j][1]);
-            s[j][2] = fmaf(acc[j][2], f0, s[j][2]);
-            s[j][3] = fmaf(acc[j][3], f1, s[j][3]);
+            // Cells 4 r + j % 2 and two on: the first or second half of each 16 bytes.
+            const uint4 &lo = ks[j >> 1][0], &hi = ks[j >> 1][1];
+            const int word = S == 2 ? half : gr >> 1;
+            const uint32_t w0 = (j & 1) ? (word ? lo.w : lo.z) : (word ? lo.y : lo.x);
+            const uint32_t w1 = (j & 1) ? (word ? hi.w : hi.z) : (word ? hi.y : hi.x);
+            const float2 f = (gr & 1) ? make_float2(__high2float(u2h(w0)), __high2float(u2h(w1)))
+                                      : make_float2(__low2float(u2h(w0)), __low2float(u2h(w1)));
+            s[j][0] = __ffma2_rn(make_float2(acc[j][0], acc[j][1]), f, s[j][0]);
+            s[j][1] = __ffma2_rn(make_float2(acc[j][2], acc[j][3]), f, s[j][1]);
         }
     }
     if constexpr (S == 2) {
         // The partner's half of the contraction.  Two slots by parity: a slot
         // is written again only after the partner has passed the next barrier.
-        float *mine = sh.xch + (warp * 2 + parity) * 16 * 32 + lane;
-        const float *other = sh.xch + ((warp ^ 1) * 2 + parity) * 16 * 32 + lane;
+        float2 *mine = reinterpret_cast<float2 *>(sh.xch + (warp * 2 + parity) * 16 * 32) + lane;
+        const float2 *other = reinterpret_cast<const float2 *>(sh.xch + ((warp ^ 1) * 2 + parity) * 16 * 32) + lane;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mine[i * 32] = s[i >> 2][i & 3];
+        for (int i = 0; i < 8; ++i) mine[i * 32] = s[i >> 1][i & 1];
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i >> 2][i & 3] += other[i * 32];
+        for (int i = 0; i < 8; ++i) s[i >> 1][i & 1] = __fadd2_rn(s[i >> 1][i & 1], other[i * 32]);
     }
     if (vmask != 0xffffffffu) {
+        const unsigned mine = vmask >> (4 * r);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const bool v0 = (vmask >> (8 * j + c0)) & 1u, v1 = (vmask >> (8 * j + c1)) & 1u;
-            s[j][0] = v0 ? s[j][0] : -CUDART_INF_F;
-            s[j][1] = v1 ? s[j][1] : -CUDART_INF_F;
-            s[j][2] = v0 ? s[j][2] : -CUDART_INF_F;
-            s[j][3] = v1 ? s[j][3] : -CUDART_INF_F;
+            const int c = 16 * (j >> 1) + (j & 1);
+            if (!((mine >> c) & 1u)) s[j][0].x = s[j][1].x = -CUDART_INF_F;
+            if (!((mine >> (c + 2)) & 1u)) s[j][0].y = s[j][1].y = -CUDART_INF_F;
         }
     }
 
     // The reference maximum moves only when a unit exceeds it by 2^SLACK, so
     // the values are rarely rescaled.
-    float mx0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
-    float mx1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
-    mx0 = fmaxf(mx0, fmaxf(fmaxf(s[2][0], s[2][1]), fmaxf(s[3][0], s[3][1])));
-    mx1 = fmaxf(mx1, fmaxf(fmaxf(s[2][2], s[2][3]), fmaxf(s[3][2], s[3][3])));
+    float mx[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        mx[e] = max3(max3(s[0][e].x, s[0][e].y, s[1][e].x), s[1][e].y, s[2][e].x);
+        mx[e] = fmaxf(max3(mx[e], s[2][e].y, s[3][e].x), s[3][e].y);
+    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
     }
-    mx0 *= sl2[0];
-    mx1 *= sl2[1];
-    const float mn0 = mx0 > st.m[0] + SLACK ? mx0 : st.m[0], mn1 = mx1 > st.m[1] + SLACK ? mx1 : st.m[1];
-    float al0 = ex2(st.m[0] - mn0), al1 = ex2(st.m[1] - mn1);
-    st.m[0] = mn0;
-    st.m[1] = mn1;
-    float ps0 = 0.0f, ps1 = 0.0f;
+    float al[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int e = 0; e < 2; ++e) {
+        mx[e] *= sl2[e];
+        const float mn = mx[e] > st.m[e] + SLACK ? mx[e] : st.m[e];
+        al[e] = ex2(st.m[e] - mn);
+        st.m[e] = mn;
+    }
+    // Weights: in fp32 for the sum, rounded to fp16 for the products (each by
+    // at most 2^-11 of itself).  pa[kk] is the A fragment of cells 16 kk on.
+    uint32_t pa[2][4];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            s[j][e] = ex2(fmaf(s[j][e], sl2[0], -mn0));
-            s[j][e + 2] = ex2(fmaf(s[j][e + 2], sl2[1], -mn1));
-            ps0 += s[j][e];
-            ps1 += s[j][e + 2];
+    for (int e = 0; e < 2; ++e) {
+        const float2 f = make_float2(sl2[e], sl2[e]), m = make_float2(-st.m[e], -st.m[e]);
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float2 p = __ffma2_rn(s[j][e], f, m);
+            p = make_float2(ex2(p.x), ex2(p.y));
+            sum = __fadd2_rn(sum, p);
+            pa[j >> 1][2 * (j & 1) + e] = h2u(__floats2half2_rn(p.x, p.y));
         }
-    st.l[0] = fmaf(st.l[0], al0, ps0);
-    st.l[1] = fmaf(st.l[1], al1, ps1);
+        st.l[e] = fmaf(st.l[e], al[e], sum.x + sum.y);
+    }
 
     // The values' power of two: the largest V scale of the first unit, raised
-    // when a later scale would pass 2^8 of it (127 * 2^9 is the fp16 limit).
-    const uint2 own = VS[lane];
+    // when a later scale reaches 2^6 of it, so that weight (below 2^8) times
+    // scale stays in the fp16 range.
+    const uint2 own = sh.scale[warp][stage][1][lane];
     uint32_t top = __vmaxu2(own.x & 0x7FFF7FFFu, own.y & 0x7FFF7FFFu);
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     const int ve = min(max((int)(top >> 10) - 15, -14), 15);
-    if (ve >= st.v + 8) {
+    if (ve >= st.v + 6) {
         const float down = exp2i(max(st.v - ve, -126));
         st.v = ve;
-        al0 *= down;
-        al1 *= down;
+        al[0] *= down;
+        al[1] *= down;
     }
-    if (__any_sync(0xffffffffu, al0 != 1.0f || al1 != 1.0f)) {
+    if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            st.o[i][0] *= al0;
-            st.o[i][1] *= al0;
-            st.o[i][2] *= al1;
-            st.o[i][3] *= al1;
+            st.o[i][0] *= al[0];
+            st.o[i][1] *= al[0];
+            st.o[i][2] *= al[1];
+            st.o[i][3] *= al[1];
         }
     }
     const __half2 vf = __float2half2_rn(exp2i(-max(st.v, -14)));
 
-    const int vg = S == 1 ? g >> 1 : 2 * half + (g >> 2);
+    // Row `lane` of V, swizzled: chunk c is at vrow ^ 16 c.
+    const uint32_t vrow = tc::smem_u32(sh.tile[warp][stage][1]) + lane * DW + ((lane & 7) << 4);
+    uint4 vs[2][2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-        uint4 pa;
-        pa.x = h2u(__floats2half2_rn(s[2 * kk][0], s[2 * kk][1]));
-        pa.y = h2u(__floats2half2_rn(s[2 * kk][2], s[2 * kk][3]));
-        pa.z = h2u(__floats2half2_rn(s[2 * kk + 1][0], s[2 * kk + 1][1]));
-        pa.w = h2u(__floats2half2_rn(s[2 * kk + 1][2], s[2 * kk + 1][3]));
-        uint4 vd[4];
-        __half vs[4];
+    for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int cell = 16 * kk + 8 * (e >> 1) + ((e & 1) ? c1 : c0);
-            vd[e] = *reinterpret_cast<const uint4 *>(V + cell * DW + ((g ^ (cell & 7)) << 4));
-            vs[e] = reinterpret_cast<const __half *>(VS + cell)[vg];
+        for (int i = 0; i < 2; ++i)
+            vs[kk][i] = *reinterpret_cast<const uint4 *>(&sh.scale[warp][stage][1][16 * kk + 4 * r + 2 * i]);
+    const __half2 off = u2h(0x64806480u);  // 1152
+    auto even = [&](uint32_t w) { return h2u(__hsub2(u2h(even_codes(w)), off)); };
+    auto odd = [&](uint32_t w) { return h2u(__hsub2(u2h(odd_codes(w)), off)); };
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        uint4 a[2];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+            const uint4 &lo = vs[kk][0], &hi = vs[kk][1];
+            const int word = S == 2 ? half : gr >> 1;
+            const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
+            const __half2 f02 = __hmul2(u2h(word ? tc::prmt(lo.y, hi.y, sel) : tc::prmt(lo.x, hi.x, sel)), vf);
+            const __half2 f13 = __hmul2(u2h(word ? tc::prmt(lo.w, hi.w, sel) : tc::prmt(lo.z, hi.z, sel)), vf);
+            a[kk] = make_uint4(h2u(__hmul2(u2h(pa[kk][0]), f02)), h2u(__hmul2(u2h(pa[kk][1]), f02)),
+                               h2u(__hmul2(u2h(pa[kk][2]), f13)), h2u(__hmul2(u2h(pa[kk][3]), f13)));
         }
-        const __half2 f01 = __hmul2(__halves2half2(vs[0], vs[1]), vf), f89 = __hmul2(__halves2half2(vs[2], vs[3]), vf);
-        const __half2 off = u2h(0x64806480u);  // 1152
-        auto value = [&](uint32_t codes, __half2 f) { return h2u(__hmul2(__hsub2(u2h(codes), off), f)); };
-        const uint32_t *w0 = reinterpret_cast<const uint32_t *>(&vd[0]), *w1 = reinterpret_cast<const uint32_t *>(&vd[1]);
-        const uint32_t *w8 = reinterpret_cast<const uint32_t *>(&vd[2]), *w9 = reinterpret_cast<const uint32_t *>(&vd[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            // Two cells' bytes side by side: (a0 a1 b0 b1), (a2 a3 b2 b3).
-            const uint32_t l0 = tc::prmt(w0[i], w1[i], 0x5410), h0 = tc::prmt(w0[i], w1[i], 0x7632);
-            const uint32_t l8 = tc::prmt(w8[i], w9[i], 0x5410), h8 = tc::prmt(w8[i], w9[i], 0x7632);
-            float(*o)[4] = st.o + 4 * i;
-            mma16816(o[0], pa, value(even_codes(l0), f01), value(even_codes(l8), f89), o[0][0], o[0][1], o[0][2], o[0][3]);
-            mma16816(o[1], pa, value(odd_codes(l0), f01), value(odd_codes(l8), f89), o[1][0], o[1][1], o[1][2], o[1][3]);
-            mma16816(o[2], pa, value(even_codes(h0), f01), value(even_codes(h8), f89), o[2][0], o[2][1], o[2][2], o[2][3]);
-            mma16816(o[3], pa, value(odd_codes(h0), f01), value(odd_codes(h8), f89), o[3][0], o[3][1], o[3][2], o[3][3]);
+        for (int c = gr * 2 * S; c < (gr + 1) * 2 * S; ++c) {
+            uint32_t w[4];
+            load_v(w, vrow ^ (c << 4));
+            float(*o)[4] = st.o + 2 * c;
+            mma16816(o[0], a[0], even(w[0]), odd(w[0]), o[0][0], o[0][1], o[0][2], o[0][3]);
+            mma16816(o[1], a[0], even(w[1]), odd(w[1]), o[1][0], o[1][1], o[1][2], o[1][3]);
+            mma16816(o[0], a[1], even(w[2]), odd(w[2]), o[0][0], o[0][1], o[0][2], o[0][3]);
+            mma16816(o[1], a[1], even(w[3]), odd(w[3]), o[1][0], o[1][1], o[1][2], o[1][3]);
         }
     }
 }
@@ -567,22 +601,15 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
         __syncthreads();  // all warps are done with the tiles and the fragments
 
         // Join the groups' states.  Value (h, d) of group w sits at (16 w + h) D
-        // + (d ^ 4 x), x = 2 (d / 32) + (h & 1): the eight lanes that a 16-byte
-        // store serves at a time then hit eight different bank groups, and
-        // reads of consecutive d stay consecutive.
+        // + (d ^ 8 (h % 4)): the lanes of an 8-byte store then meet each bank
+        // once, and reads of consecutive d stay consecutive.
         float *so = reinterpret_cast<float *>(sh.tile);
         float *ow = so + pw * 16 * D + DW * half;
-        const int sw = 4 * ((2 * r + (g & 1)) & 7);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-            // Columns 2r, 2r + 1 of a V tile are dims 32 r + i and 32 r + 16 + i.
-            const int d0 = (32 * r + i) ^ sw, d1 = (32 * r + 16 + i) ^ sw;
-            *reinterpret_cast<float4 *>(ow + g * D + d0) = make_float4(st.o[i][0], st.o[i + 1][0], st.o[i + 2][0], st.o[i + 3][0]);
-            *reinterpret_cast<float4 *>(ow + g * D + d1) = make_float4(st.o[i][1], st.o[i + 1][1], st.o[i + 2][1], st.o[i + 3][1]);
-            *reinterpret_cast<float4 *>(ow + (g + 8) * D + d0) =
-                make_float4(st.o[i][2], st.o[i + 1][2], st.o[i + 2][2], st.o[i + 3][2]);
-            *reinterpret_cast<float4 *>(ow + (g + 8) * D + d1) =
-                make_float4(st.o[i][3], st.o[i + 1][3], st.o[i + 2][3], st.o[i + 3][3]);
+        for (int i = 0; i < 16; ++i) {
+            const int d = (8 * i + 2 * r) ^ (8 * (g & 3));
+            *reinterpret_cast<float2 *>(ow + g * D + d) = make_float2(st.o[i][0], st.o[i][1]);
+            *reinterpret_cast<float2 *>(ow + (g + 8) * D + d) = make_float2(st.o[i][2], st.o[i][3]);
         }
         if (r == 0 && half == 0) {
             sh.m[pw][g] = st.m[0];
@@ -620,7 +647,7 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
         __syncthreads();
         for (int i = tid; i < per * (D / 2); i += NW * 32) {
             const int h = i / (D / 2), d = 2 * (i % (D / 2));
-            const int pd = d ^ (4 * ((2 * (d >> 5) + (h & 1)) & 7));
+            const int pd = d ^ (8 * (h & 3));
             float o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
             for (int w = 0; w < NP; ++w) {

@@ -60,10 +60,13 @@ constexpr int TILE = UNIT * DW;
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float SLACK = 8.0f;  // weights stay below 2^8 of the running maximum's
-constexpr int MAX_CTAS = 152 * 3;
+constexpr int MAX_CTAS = 152 * 2;
 
 // Fewest units of a share: finer ones would only add partials to join.
 constexpr int MIN_SHARE = 8;
+// Rows of up to this many units are not shared out.
+constexpr int WHOLE = 16;
+static_assert(NS == 2, "the ring alternates between two stages");
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -74,8 +77,8 @@ __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<ui
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
 // Bytes 0 and 2 (or 1 and 3) of w, as fp16 1152 + code.
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) { return (w & 0x00FF00FFu) ^ 0x64806480u; }
-__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return ((w >> 8) & 0x00FF00FFu) ^ 0x64806480u; }
+__device__ __forceinline__ uint32_t even_codes(uint32_t w) { return tc::prmt(w ^ 0x80808080u, 0x64646464u, 0x4240); }
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return tc::prmt(w ^ 0x80808080u, 0x64646464u, 0x4341); }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -115,8 +118,7 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool pr
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(pred ? 8 : 0));
 }
 
-// Shared memory of a CTA.  After a segment the tiles hold the warps' values
-// for the merge.
+// Shared memory of a CTA.
 template <int S>
 struct Smem {
     uint8_t tile[NW][NS][2][TILE];  // K, V; 1024-byte aligned
@@ -124,7 +126,10 @@ struct Smem {
     uint4 q[S][8][32];              // Q fragments by k-step and lane
     float bias[4][8][4];            // -1152 * sum of q over a scale group, as accumulators: heads g, g, g + 8, g + 8
     float qinv[16];                 // 2^-e of a head's scaled query
-    float xch[S == 2 ? NW * 2 * 16 * 32 : 1];
+    union {
+        float o[NW / S][16][DW * S];   // the groups' values, at the end of a segment
+        float xch[NW][2][16 * 32];     // partial scores of a shared unit (head_dim 256), during one
+    };
     float m[NW / S][16], l[NW / S][16], f[NW / S][16];
     int v[NW / S];                  // the groups' V exponents
     uint64_t bar[NW][NS];
@@ -220,58 +225,75 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
 // The query heads of (row t, KV head kvh) as A fragments in shared memory,
 // fp16, with the sums that undo the codes' 1152.  bf16 queries are scaled by
 // a power of two per head where they would leave the fp16 range; fp16 ones
-// are used as they are.  A negative softmax scale flips their sign.
+// are used as they are.  A negative softmax scale flips their sign.  A warp
+// takes every NW-th head; the loads are apart from the rest, so that a
+// segment's can be in flight while the one before ends.
 template <int S>
-__device__ __forceinline__ void stage_q(const qsa_paged_attn_args &a, Smem<S> &sh, int t, int kvh, int per) {
-    constexpr int D = DW * S, N = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int h = warp; h < 16; h += NW) {
-        float x[N];
-        uint16_t raw[N];
-        const size_t at = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + lane * N;
-        const bool have = h < per && QSA_IN(at + N - 1, (size_t)a.n_tokens * a.n_q_heads * D);
-        if constexpr (N == 4)
-            *reinterpret_cast<uint2 *>(raw) =
-                have ? __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.q) + at)) : make_uint2(0u, 0u);
-        else
-            *reinterpret_cast<uint4 *>(raw) = have ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + at))
-                                                   : make_uint4(0u, 0u, 0u, 0u);
-        float top = 0.0f;
+struct Query {
+    static constexpr int D = DW * S, N = D / 32, H = 16 / NW;
+    uint32_t raw[H][N / 2];
+
+    __device__ __forceinline__ void load(const qsa_paged_attn_args &a, int t, int kvh, int per) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            x[e] = a.dtype == QSA_F16 ? __half2float(__ushort_as_half(raw[e])) : __bfloat162float(__ushort_as_bfloat16(raw[e]));
-            top = fmaxf(top, fabsf(x[e]));
-        }
-        int ex = 0;
-        if (a.dtype != QSA_F16) {
+        for (int i = 0; i < H; ++i) {
+            const int h = warp + i * NW;
+            const size_t at = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + lane * N;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            ex = head_sum_exponent(top);
-        }
-        const float f = (a.softmax_scale < 0.0f ? -1.0f : 1.0f) * exp2i(ex);
-        if (lane == 0) sh.qinv[h] = exp2i(-ex);
-        __half v[N];
-        float sum = 0.0f;
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-            v[e] = __float2half_rn(x[e] * f);
-            sum += __half2float(v[e]);
-        }
-        // A scale group is D/4 dims, eight lanes.
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if ((lane & 7) == 0)
-            *reinterpret_cast<float2 *>(&sh.bias[lane >> 3][h & 7][2 * (h >> 3)]) = make_float2(-1152.0f * sum, -1152.0f * sum);
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-            const int d = lane * N + e, half = d / DW, dl = d % DW;
-            const int ks = 2 * (dl >> 5) + ((dl >> 2) & 1), r = (dl >> 3) & 3;
-            uint32_t *dst = reinterpret_cast<uint32_t *>(&sh.q[half][ks][(h & 7) * 4 + r]) + (h >> 3);
-            dst[0] = h2u(__halves2half2(v[e], v[e + 2]));
-            dst[2] = h2u(__halves2half2(v[e + 1], v[e + 3]));
+            for (int e = 0; e < N / 2; ++e) raw[i][e] = 0u;
+            if (h < per && QSA_IN(at + N - 1, (size_t)a.n_tokens * a.n_q_heads * D)) {
+                const uint16_t *src = static_cast<const uint16_t *>(a.q) + at;
+                if constexpr (N == 4)
+                    *reinterpret_cast<uint2 *>(raw[i]) = __ldg(reinterpret_cast<const uint2 *>(src));
+                else
+                    *reinterpret_cast<uint4 *>(raw[i]) = __ldg(reinterpret_cast<const uint4 *>(src));
+            }
         }
     }
-}
+
+    __device__ __forceinline__ void store(const qsa_paged_attn_args &a, Smem<S> &sh) const {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const int h = warp + i * NW;
+            float x[N], top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const uint16_t v = (uint16_t)(raw[i][e / 2] >> (16 * (e & 1)));
+                x[e] = a.dtype == QSA_F16 ? __half2float(__ushort_as_half(v)) : __bfloat162float(__ushort_as_bfloat16(v));
+                top = fmaxf(top, fabsf(x[e]));
+            }
+            int ex = 0;
+            if (a.dtype != QSA_F16) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                ex = head_sum_exponent(top);
+            }
+            const float f = (a.softmax_scale < 0.0f ? -1.0f : 1.0f) * exp2i(ex);
+            if (lane == 0) sh.qinv[h] = exp2i(-ex);
+            __half v[N];
+            float sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                v[e] = __float2half_rn(x[e] * f);
+                sum += __half2float(v[e]);
+            }
+            // A scale group is D/4 dims, eight lanes.
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if ((lane & 7) == 0)
+                *reinterpret_cast<float2 *>(&sh.bias[lane >> 3][h & 7][2 * (h >> 3)]) = make_float2(-1152.0f * sum, -1152.0f * sum);
+#pragma unroll
+            for (int e = 0; e < N; e += 4) {
+                const int d = lane * N + e, half = d / DW, dl = d % DW;
+                const int ks = 2 * (dl >> 5) + ((dl >> 2) & 1), r = (dl >> 3) & 3;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(&sh.q[half][ks][(h & 7) * 4 + r]) + (h >> 3);
+                dst[0] = h2u(__halves2half2(v[e], v[e + 2]));
+                dst[2] = h2u(__halves2half2(v[e + 1], v[e + 3]));
+            }
+        }
+    }
+};
 
 struct State {
     float o[16][4];  // o[t][0..1]: head g, dims 8 t + 2 r, 8 t + 2 r + 1; o[t][2..3]: head g + 8
@@ -338,8 +360,8 @@ __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vm
     if constexpr (S == 2) {
         // The partner's half of the contraction.  Two slots by parity: a slot
         // is written again only after the partner has passed the next barrier.
-        float2 *mine = reinterpret_cast<float2 *>(sh.xch + (warp * 2 + parity) * 16 * 32) + lane;
-        const float2 *other = reinterpret_cast<const float2 *>(sh.xch + ((warp ^ 1) * 2 + parity) * 16 * 32) + lane;
+        float2 *mine = reinterpret_cast<float2 *>(sh.xch[warp][parity]) + lane;
+        const float2 *other = reinterpret_cast<const float2 *>(sh.xch[warp ^ 1][parity]) + lane;
 #pragma unroll
         for (int i = 0; i < 8; ++i) mine[i * 32] = s[i >> 1][i & 1];
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
@@ -466,10 +488,20 @@ __device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i
         *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(x, y);
 }
 
+// The units of a warp group in order, across rows: unit u of row t is the next
+// one whose copies start.  The row after, and the page of the next unit, are
+// loaded a step before they are needed.
+struct Feed {
+    int t, trow, len, u, end;  // units up to `end` of row t are this CTA's
+    int left;                  // its units in the rows after
+    int next_trow, next_len;
+    int page;                  // this lane's table entry for unit u
+};
+
 template <int S>
-__global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
+__global__ void __launch_bounds__(NW * 32, 2)
     paged_attn_kernel(const qsa_paged_attn_args a, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap) {
+                      const __grid_constant__ CUtensorMap vmap, int whole_rows) {
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<S> &sh = *reinterpret_cast<Smem<S> *>(raw);
     constexpr int D = DW * S, NP = NW / S;
@@ -483,54 +515,69 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
     wait_for_previous_grid();
     allow_dependent_launch();
     const int kvh = blockIdx.x % a.n_kv_heads, range = blockIdx.x / a.n_kv_heads, ranges = gridDim.x / a.n_kv_heads;
-    int share;
-    find_start<S>(a, sh, range, ranges, share);
     const Work work = carve(a.workspace, per);
-    const long long x = (long long)share * range;
-    const long long total = sh.total;
-    if (x >= total) {
-        if (tid == 0 && ranges > 1) work.part[blockIdx.x] = Part{-1, 0};
-        return;
+    // This CTA's units: `left` of them from unit u0 of row t on, or with
+    // whole_rows every ranges-th row from row `range`.
+    int share = 0, t = range, u0 = 0, left = 0x7fffffff;
+    const int step = whole_rows ? ranges : 1;
+    if (!whole_rows) {
+        find_start<S>(a, sh, range, ranges, share);
+        const long long x = (long long)share * range, total = sh.total;
+        if (x >= total) {
+            if (tid == 0) work.part[blockIdx.x] = Part{-1, 0};
+            return;
+        }
+        left = (int)min((long long)share, total - x);
+        t = sh.row;
+        u0 = (int)(x - sh.before);
     }
-    int left = (int)min((long long)share, total - x);  // units of this share still to do
-    int t = sh.row, trow;
     bool bad = false, dead = false;
-    int len = row_len(a, t, trow, bad);
-    int nu = units_of(len);
-    int u0 = (int)(x - sh.before);
     uint32_t phase = 0;   // parity of each stage's next completion, one bit per stage
     uint32_t flying = 0;  // stages with copies in flight
-    Part part{-1, 0};
-    float sl2[2];
-
-    for (bool first = true; left > 0; first = false) {
-        // Segment: units u0 .. u1-1 of row t.
-        const int u1 = min(nu, u0 + left), n_units = u1 - u0;
-        stage_q<S>(a, sh, t, kvh, per);
-        const int n = n_units > pw ? (n_units - pw + NP - 1) / NP : 0;  // this group's units: u0 + pw + i NP
-        const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
-        auto page_id = [&](int i) -> int {
-            const int c = (u0 + pw + i * NP) * UNIT + lane;
-            return i < n && (c >> page_shift) < a.max_pages ? __ldg(tab + (c >> page_shift)) : -1;
-        };
-        // Starts the copies of unit i into its stage; returns its valid cells.
-        auto issue = [&](int i, int page) -> unsigned {
-            const int c = (u0 + pw + i * NP) * UNIT + lane;
-            const bool in = i < n && c < len;
-            const bool ok = in && page >= 0 && page < a.n_pages;
-            bad |= in && !ok;
-            const unsigned vmask = __ballot_sync(0xffffffffu, ok);
-            const int stage = i % NS;
-            const size_t cell = ok ? ((size_t)page << page_shift) + (c & (a.page_size - 1)) : 0;
-            const size_t si = (cell * a.n_kv_heads + kvh) * 4;
-            const bool sok = ok && QSA_IN(si + 3, (size_t)a.n_pages * a.page_size * a.n_kv_heads * 4);
-            cp_async8(tc::smem_u32(&sh.scale[warp][stage][0][lane]), a.ksc + (sok ? si : 0), sok);
-            cp_async8(tc::smem_u32(&sh.scale[warp][stage][1][lane]), a.vsc + (sok ? si : 0), sok);
-            asm volatile("cp.async.commit_group;\n" ::);
-            // A box starts on the first cell of a page or of a 32-cell part of one.
-            const int cell16 = __shfl_sync(0xffffffffu, (int)cell, 16);
-            if (vmask && !dead) flying |= 1u << stage;
-            if (lane == 0 && vmask && !dead) {
+    Feed f;
+    f.t = t;
+    f.len = row_len(a, t, f.trow, bad);
+    int nu = units_of(f.len);
+    f.end = min(nu, u0 + left);
+    f.left = left - (f.end - u0);
+    f.u = u0 + pw;
+    f.next_len = f.next_trow = 0;
+    auto peek = [&] {
+        if (f.left > 0 && f.t + step < a.n_tokens) f.next_len = row_len(a, f.t + step, f.next_trow, bad);
+    };
+    // Moves on to the next row that has a unit for this group.
+    auto settle = [&] {
+        while (f.u >= f.end && f.left > 0 && f.t + step < a.n_tokens) {
+            f.t += step;
+            f.len = f.next_len;
+            f.trow = f.next_trow;
+            f.end = min(units_of(f.len), f.left);
+            f.left -= f.end;
+            f.u = pw;
+            peek();
+        }
+        const int j = (f.u * UNIT + lane) >> page_shift;
+        f.page = f.u < f.end && j < a.max_pages ? __ldg(a.page_table + (size_t)f.trow * a.max_pages + j) : -1;
+    };
+    // Starts the copies of unit f.u into a stage and moves on; returns the
+    // unit's valid cells (none past the last unit).
+    auto issue = [&](int stage) -> unsigned {
+        const int c = f.u * UNIT + lane;
+        const bool in = f.u < f.end && c < f.len;
+        const bool ok = in && f.page >= 0 && f.page < a.n_pages;
+        bad |= in && !ok;
+        const unsigned vmask = __ballot_sync(0xffffffffu, ok);
+        const size_t cell = ok ? ((size_t)f.page << page_shift) + (c & (a.page_size - 1)) : 0;
+        const size_t si = (cell * a.n_kv_heads + kvh) * 4;
+        const bool sok = ok && QSA_IN(si + 3, (size_t)a.n_pages * a.page_size * a.n_kv_heads * 4);
+        cp_async8(tc::smem_u32(&sh.scale[warp][stage][0][lane]), a.ksc + (sok ? si : 0), sok);
+        cp_async8(tc::smem_u32(&sh.scale[warp][stage][1][lane]), a.vsc + (sok ? si : 0), sok);
+        asm volatile("cp.async.commit_group;\n" ::);
+        // A box starts on the first cell of a page or of a 32-cell part of one.
+        const int cell16 = __shfl_sync(0xffffffffu, (int)cell, 16);
+        if (vmask && !dead) {
+            flying |= 1u << stage;
+            if (lane == 0) {
                 const uint32_t bar = tc::smem_u32(&sh.bar[warp][stage]);
                 const uint32_t k = tc::smem_u32(sh.tile[warp][stage][0]), v = tc::smem_u32(sh.tile[warp][stage][1]);
                 if (a.page_size >= UNIT) {
@@ -550,27 +597,42 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
                     }
                 }
             }
-            return vmask;
-        };
+        }
+        f.u += NP;
+        settle();
+        return vmask;
+    };
+
+    Query<S> q;
+    q.load(a, t, kvh, per);
+    peek();
+    settle();
+    q.store(a, sh);
+    int stage = 0, nx = 0;
+    unsigned vmask = 0;
+    bool ahead = false;  // the next unit's copies have been started
+    Part part{-1, 0};
+    __syncthreads();  // the query fragments
+
+    for (bool first = true;; first = false) {
+        // Segment: units u0 .. u1-1 of row t; this group's are u0 + pw, + NP ...
+        const int u1 = min(nu, u0 + left), n_units = u1 - u0;
+        const int n = n_units > pw ? (n_units - pw + NP - 1) / NP : 0;
+        // |scale| in base 2, floored at the smallest normal float: with scale
+        // 0 the weights are uniform and a masked -inf stays -inf.
+        const float sl2[2] = {fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g], 1.17549435e-38f),
+                              fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g + 8], 1.17549435e-38f)};
         State st;
 #pragma unroll
         for (int i = 0; i < 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.0f;
         st.m[0] = st.m[1] = -CUDART_INF_F;
         st.l[0] = st.l[1] = 0.0f;
         st.v = -64;  // below any scale's exponent: the first unit sets it
-        int next_page = page_id(1);
-        unsigned vmask = issue(0, page_id(0));
-        __syncthreads();  // the query fragments
-        // |scale| in base 2, floored at the smallest normal float: with scale
-        // 0 the weights are uniform and a masked -inf stays -inf.
-        sl2[0] = fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g], 1.17549435e-38f);
-        sl2[1] = fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g + 8], 1.17549435e-38f);
-        int nx = 0;
         for (int i = 0; i < n; ++i) {
-            const unsigned vnext = issue(i + 1, next_page);  // empty past the last unit
-            next_page = page_id(i + 2);
+            if (!ahead) vmask = issue(stage);
+            const unsigned vnext = issue(stage ^ 1);
+            ahead = true;
             asm volatile("cp.async.wait_group 1;\n" ::);
-            const int stage = i % NS;
             if (vmask) {
                 if (!dead && !tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][stage]), (phase >> stage) & 1u, tc::WAIT_LIMIT)) {
                     dead = true;
@@ -586,30 +648,27 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
             }
             __syncwarp();  // every lane has read the stage before it is filled again
             vmask = vnext;
-        }
-        asm volatile("cp.async.wait_group 0;\n" ::);
-        if (flying) {  // after a time-out: copies in flight land before the tiles are used again or given up
-            for (int i = 0; i < NS; ++i)
-                if ((flying >> i) & 1u) tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][i]), (phase >> i) & 1u, tc::DRAIN_LIMIT);
-            flying = 0;
+            stage ^= 1;
         }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
             st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
             st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
         }
-        __syncthreads();  // all warps are done with the tiles and the fragments
+        left -= n_units;
+        const int next = t + step;
+        const bool more = left > 0 && next < a.n_tokens;
+        if (more) q.load(a, next, kvh, per);
+        __syncthreads();  // all warps are done with the query, and with the values of the segment before
 
-        // Join the groups' states.  Value (h, d) of group w sits at (16 w + h) D
-        // + (d ^ 8 (h % 4)): the lanes of an 8-byte store then meet each bank
-        // once, and reads of consecutive d stay consecutive.
-        float *so = reinterpret_cast<float *>(sh.tile);
-        float *ow = so + pw * 16 * D + DW * half;
+        // Join the groups' states.  Value (h, d) of a group sits at d ^ 8 (h %
+        // 4) of its row: the lanes of an 8-byte store then meet each bank once,
+        // and reads of consecutive d stay consecutive.
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int d = (8 * i + 2 * r) ^ (8 * (g & 3));
-            *reinterpret_cast<float2 *>(ow + g * D + d) = make_float2(st.o[i][0], st.o[i][1]);
-            *reinterpret_cast<float2 *>(ow + (g + 8) * D + d) = make_float2(st.o[i][2], st.o[i][3]);
+            const int d = DW * half + ((8 * i + 2 * r) ^ (8 * (g & 3)));
+            *reinterpret_cast<float2 *>(&sh.o[pw][g][d]) = make_float2(st.o[i][0], st.o[i][1]);
+            *reinterpret_cast<float2 *>(&sh.o[pw][g + 8][d]) = make_float2(st.o[i][2], st.o[i][3]);
         }
         if (r == 0 && half == 0) {
             sh.m[pw][g] = st.m[0];
@@ -618,23 +677,22 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
             sh.l[pw][g + 8] = st.l[1];
         }
         if (lane == 0 && half == 0) sh.v[pw] = st.v;  // both halves see all four scale groups: the same
+        if (more) q.store(a, sh);
         __syncthreads();
         const bool whole = n_units == nu;
-        const int slot = !first || u0 == 0 ? 1 : 0;
-        const size_t at = (size_t)blockIdx.x * 2 + slot;
+        const size_t at = (size_t)blockIdx.x * 2 + (first && u0 > 0 ? 0 : 1);
         if (tid < 16) {
-            float M = -CUDART_INF_F, L = 0.0f;
+            float M = -CUDART_INF_F, L = 0.0f, w[NP];
 #pragma unroll
-            for (int w = 0; w < NP; ++w) M = fmaxf(M, sh.m[w][tid]);
-            float f[NP];
+            for (int p = 0; p < NP; ++p) M = fmaxf(M, sh.m[p][tid]);
 #pragma unroll
-            for (int w = 0; w < NP; ++w) {
-                f[w] = sh.m[w][tid] == -CUDART_INF_F ? 0.0f : exp2f(sh.m[w][tid] - M);
-                L += f[w] * sh.l[w][tid];
+            for (int p = 0; p < NP; ++p) {
+                w[p] = sh.m[p][tid] == -CUDART_INF_F ? 0.0f : exp2f(sh.m[p][tid] - M);
+                L += w[p] * sh.l[p][tid];
             }
             const float inv = whole ? (M == -CUDART_INF_F ? 0.0f : 1.0f / L) : 1.0f;
 #pragma unroll
-            for (int w = 0; w < NP; ++w) sh.f[w][tid] = f[w] * inv * (f[w] == 0.0f ? 0.0f : exp2i(sh.v[w]));
+            for (int p = 0; p < NP; ++p) sh.f[p][tid] = w[p] == 0.0f ? 0.0f : w[p] * inv * exp2i(sh.v[p]);
             if (tid < per) {
                 if (whole) {
                     if (a.lse) a.lse[(size_t)t * a.n_q_heads + kvh * per + tid] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
@@ -646,15 +704,14 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
         }
         __syncthreads();
         for (int i = tid; i < per * (D / 2); i += NW * 32) {
-            const int h = i / (D / 2), d = 2 * (i % (D / 2));
-            const int pd = d ^ (8 * (h & 3));
+            const int h = i / (D / 2), d = 2 * (i % (D / 2)), pd = d ^ (8 * (h & 3));
             float o0 = 0.0f, o1 = 0.0f;
 #pragma unroll
-            for (int w = 0; w < NP; ++w) {
-                const float f = sh.f[w][h];
-                const float2 o = *reinterpret_cast<const float2 *>(so + (w * 16 + h) * D + pd);
-                o0 = fmaf(f, o.x, o0);
-                o1 = fmaf(f, o.y, o1);
+            for (int p = 0; p < NP; ++p) {
+                const float w = sh.f[p][h];
+                const float2 o = *reinterpret_cast<const float2 *>(&sh.o[p][h][pd]);
+                o0 = fmaf(w, o.x, o0);
+                o1 = fmaf(w, o.y, o1);
             }
             if (whole) {
                 const size_t oi = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + d;
@@ -664,17 +721,20 @@ __global__ void __launch_bounds__(NW * 32, S == 1 ? 3 : 2)
             }
         }
         if (!whole && u0 == 0) part = Part{t, 1 + (nu - u1 + share - 1) / share};
-        left -= n_units;
+        if (!more) break;
+        t = next;
         u0 = 0;
-        if (left > 0) {
-            len = row_len(a, ++t, trow, bad);
-            nu = units_of(len);
-        }
-        tc::fence_async_smem();  // the tiles are written by copies again
-        __syncthreads();
+        int trow;
+        nu = units_of(row_len(a, t, trow, bad));
+        if constexpr (S == 2) __syncthreads();  // the scores' exchange takes the values' place
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::);
+    if (flying) {  // after a time-out: copies in flight land before this CTA's shared memory is given up
+        for (int i = 0; i < NS; ++i)
+            if ((flying >> i) & 1u) tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][i]), (phase >> i) & 1u, tc::DRAIN_LIMIT);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
-    if (tid == 0 && ranges > 1) work.part[blockIdx.x] = part;
+    if (tid == 0 && !whole_rows) work.part[blockIdx.x] = part;
 }
 
 // Joins the partials of the row that starts in CTA blockIdx.x and spans
@@ -775,14 +835,17 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
     if (e != cudaSuccess) return e;
-    // A share per resident CTA, or fewer where the table cannot hold as many
-    // units.  With one share per KV head no row spans CTAs, and there may be
-    // more CTAs than the workspace has places for.
-    const long long most = (long long)a.n_tokens * (((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT);
-    const long long shares = (most + MIN_SHARE - 1) / MIN_SHARE, resident = std::max(152 * (S == 1 ? 3 : 2) / a.n_kv_heads, 1);
-    const int ranges = (int)(shares < resident ? shares : resident), grid = ranges * a.n_kv_heads;
-    e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap);
-    if (e != cudaSuccess || ranges == 1) return e;
+    // A share per resident CTA.  Whole rows, and no join, where the table
+    // cannot hold longer ones than WHOLE units, or where there are as many KV
+    // heads as CTAs (then there may also be more CTAs than the workspace has
+    // places for).
+    const long long units = ((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT;
+    const int resident = std::max(152 * 2 / a.n_kv_heads, 1);
+    const bool whole = units <= WHOLE || resident == 1;
+    const long long most = whole ? a.n_tokens : (a.n_tokens * units + MIN_SHARE - 1) / MIN_SHARE;
+    const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
+    e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, whole ? 1 : 0);
+    if (e != cudaSuccess || whole) return e;
     return launch_dependent(paged_join_kernel<S>, dim3(grid, a.n_q_heads / a.n_kv_heads), dim3(512), 0, s, a);
 }
 

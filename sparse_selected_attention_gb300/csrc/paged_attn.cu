@@ -737,64 +737,78 @@ __global__ void __launch_bounds__(NW * 32, 2)
     if (tid == 0 && !whole_rows) work.part[blockIdx.x] = part;
 }
 
-// Joins the partials of the row that starts in CTA blockIdx.x and spans
-// others: part p is slot 1 of that CTA, then slot 0 of the next ones of its KV
-// head.  One block per (CTA, query head); G groups of threads take every G-th part.
-template <int S>
-__global__ void __launch_bounds__(512) paged_join_kernel(const qsa_paged_attn_args a) {
-    constexpr int D = DW * S, T2 = D / 2, G = 512 / T2;
-    __shared__ float w[MAX_CTAS], red[16], red2[16];
-    __shared__ float2 so[G][T2];
+// Joins the partials of rows that span CTAs.  Block x looks after the row that
+// starts in CTA x and continues in others, if there is one: part p is slot 1 of
+// that CTA, then slot 0 of the next ones of its KV head.  A warp takes 64 dims
+// of one query head and every G-th part; it works the weights out itself (a
+// few loads per lane), so there is nothing to wait for but the last sum.  Many
+// rows: HB heads and no split per block; few, whose parts are many: the block's
+// warps split the parts of one head.
+constexpr int JOIN_WARPS = 16;
+template <int S, int HB>
+__global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const qsa_paged_attn_args a) {
+    constexpr int D = DW * S, DC = D / 64, G = JOIN_WARPS / (HB * DC);
+    constexpr int LOADS = (MAX_CTAS + 31) / 32;
+    __shared__ float2 so[G > 1 ? JOIN_WARPS : 1][32];
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int per = a.n_q_heads / a.n_kv_heads, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = a.n_q_heads / a.n_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int h = blockIdx.y * HB + warp / (DC * G), dc = warp / G % DC, grp = warp % G;
     const Work work = carve(a.workspace, per);
     const Part part = work.part[blockIdx.x];
     if (part.row < 0) return;
     auto slot = [&](int p) { return (size_t)(blockIdx.x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0); };
-    float m = -CUDART_INF_F, l = 0.0f;
-    if (tid < part.n) {
-        m = work.ml[(slot(tid) * per + h) * 2];
-        l = work.ml[(slot(tid) * per + h) * 2 + 1];
+    const int n = h < per ? part.n : 0;
+    float w[LOADS], l[LOADS], M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+        const int p = i * 32 + lane;
+        w[i] = -CUDART_INF_F;
+        l[i] = 0.0f;
+        if (p < n) {
+            const float2 v = *reinterpret_cast<const float2 *>(work.ml + (slot(p) * per + h) * 2);
+            w[i] = v.x;
+            l[i] = v.y;
+        }
+        M = fmaxf(M, w[i]);
     }
-    float M = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (lane == 0) red[warp] = M;
-    __syncthreads();
-    M = red[0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) M = fmaxf(M, red[i]);
-    const float f = m == -CUDART_INF_F ? 0.0f : exp2f(m - M);
-    if (tid < part.n) w[tid] = f;
-    float L = f * l;
+    for (int i = 0; i < LOADS; ++i) {
+        w[i] = w[i] == -CUDART_INF_F ? 0.0f : exp2f(w[i] - M);
+        L += w[i] * l[i];
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) red2[warp] = L;
-    __syncthreads();
-    L = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) L += red2[i];
-    const int grp = tid / T2, d = 2 * (tid % T2);
+    const int d = dc * 64 + lane * 2;
     float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-    for (int p = grp; p < part.n; p += G) {
-        const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(p) * per + h) * D + d);
-        o.x = fmaf(w[p], v.x, o.x);
-        o.y = fmaf(w[p], v.y, o.y);
-    }
-    so[grp][tid % T2] = o;
-    __syncthreads();
-    if (grp) return;
-    o = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-        o.x += so[i][tid].x;
-        o.y += so[i][tid].y;
+    for (int i = 0; i < LOADS; ++i) {
+        if (i * 32 >= n) break;
+        const int top = min(n - i * 32, 32);
+#pragma unroll 4
+        for (int k = (grp - i * 32 % G + G) % G; k < top; k += G) {
+            const float f = __shfl_sync(0xffffffffu, w[i], k);
+            const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(i * 32 + k) * per + h) * D + d);
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+        }
     }
+    if constexpr (G > 1) {
+        so[warp][lane] = o;
+        __syncthreads();
+        if (grp) return;
+#pragma unroll
+        for (int i = 1; i < G; ++i) {
+            o.x += so[warp + i][lane].x;
+            o.y += so[warp + i][lane].y;
+        }
+    }
+    if (h >= per) return;
     const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
     const size_t row = (size_t)part.row * a.n_q_heads + (size_t)(blockIdx.x % a.n_kv_heads) * per + h;
-    if (tid == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+    if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
     if (QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) store_out(a, row * D + d, o.x * inv, o.y * inv);
 }
 
@@ -846,7 +860,13 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, whole ? 1 : 0);
     if (e != cudaSuccess || whole) return e;
-    return launch_dependent(paged_join_kernel<S>, dim3(grid, a.n_q_heads / a.n_kv_heads), dim3(512), 0, s, a);
+    // Fewer rows than half the SMs: their parts are many (a row of 30 K cells
+    // alone: 118), and a block's warps share them.
+    const int per = a.n_q_heads / a.n_kv_heads;
+    constexpr int HB = S == 1 ? 8 : 4;
+    if ((long long)a.n_tokens * a.n_kv_heads < 76)
+        return launch_dependent(paged_join_kernel<S, 1>, dim3(grid, per), dim3(JOIN_WARPS * 32), 0, s, a);
+    return launch_dependent(paged_join_kernel<S, HB>, dim3(grid, (per + HB - 1) / HB), dim3(JOIN_WARPS * 32), 0, s, a);
 }
 
 }  // namespace

@@ -328,7 +328,8 @@ qsa_status qsa_attn(const qsa_attn_args *args, void *stream);
  *   y = (x / sqrt(mean(x^2) + eps)) * w     with w = q_norm_w / k_norm_w;
  *                                           a NULL weight leaves y = x
  *   pairs (i, j), i < rope_dims/2: (i, i + rope_dims/2), or with interleaved
- *   = 1 (2i, 2i + 1); a = p * inv_freq[i], exact to about 1e-7 at any p:
+ *   = 1 (2i, 2i + 1); a = p * inv_freq[i]; cos a, sin a good to 1e-6
+ *   at any p:
  *     y'[i] = rope_mscale * (y[i] cos a - y[j] sin a)
  *     y'[j] = rope_mscale * (y[j] cos a + y[i] sin a)
  * dims from rope_dims on keep y.  q_out[t] = y' rounded to q_out_dtype.  Key
@@ -336,7 +337,7 @@ qsa_status qsa_attn(const qsa_attn_args *args, void *stream);
  * fp16(max|.|/127), code = clamp(rint(./s), -127, 127), into pool cell
  * slots[t].  A group that holds a NaN, or a value beyond 127 * 65504, gets a
  * NaN or infinite scale, so that it reads back as NaN.
- * slots[t] = -1 marks a padding token: nothing of it is read or written.
+ * slots[t] = -1 marks a padding token: nothing of it is written, q_out included.
  * Another slot outside [0, cache_cells) is treated so too and sets
  * QSA_DEVERR_BAD_ID.  No two tokens may have the same slot.
  *

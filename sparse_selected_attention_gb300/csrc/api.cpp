@@ -373,8 +373,8 @@ qsa_status qsa_paged_gather(const qsa_paged_gather_args *a, void *stream) {
         if (a->n_rows < 1 || a->max_pages < 1 || (a->n_ids && !a->rows))
             return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: a page table needs rows, n_rows and max_pages");
     }
-    if ((long long)a->n_ids * a->n_kv_heads * (a->head_dim / 8) > kMaxInt * 256)
-        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_gather: more than 2^31 blocks of output");
+    if ((long long)a->n_ids * a->n_kv_heads > (1ll << 40) / a->head_dim)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_gather: more than 2^40 values of output");
     if (a->n_ids == 0) return QSA_OK;
     if (!a->kq || !a->vq || !a->ksc || !a->vsc || !a->ids || !a->k_out || !a->v_out)
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: NULL buffer");

@@ -1,12 +1,12 @@
 // qsa_paged_prep and qsa_paged_gather: rows into and out of the paged cache.
 //
 // Prep: for each token, the query and key heads' RMS norm and rotation and the
-// K/V rows' int8 codes, written to the token's slot.  One block of four warps
-// per token and 16 of its head rows (query heads, then key, then value heads);
-// a warp takes four rows side by side, so that their loads and their sums of
-// squares are in flight together, and a lane holds head_dim/32 consecutive
-// elements.  The token's angles are computed once per block, one per thread,
-// while the rows are on their way.
+// K/V rows' int8 codes, written to the token's slot.  Its traffic is small
+// beside its arithmetic and latency (some 100 instructions per row of 256 to 512
+// bytes), so a warp works alone, without shared memory or barriers: it takes a
+// run of one token's rows (query heads, then key, then value heads), two at a
+// time with the next two on their way, and keeps the token's cosines and sines
+// in registers.  Few tokens are split over more warps, down to two rows each.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -16,9 +16,8 @@
 namespace qsa {
 namespace {
 
-constexpr int ROWS_PER_WARP = 4;
 constexpr int PREP_WARPS = 4;
-constexpr int ROWS_PER_BLOCK = ROWS_PER_WARP * PREP_WARPS;
+constexpr int BATCH = 2;  // rows worked on together, with as many on their way
 
 template <int BYTES>
 struct Words {
@@ -45,25 +44,22 @@ __device__ __forceinline__ void from_float(float v, __half &o) { o = __float2hal
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16 &o) { o = __float2bfloat16_rn(v); }
 
 template <int N, class T>
-__device__ __forceinline__ void load_elems(const T *p, float (&x)[N]) {
-    union {
-        Words<N * (int)sizeof(T)> w;
-        T e[N];
-    } u;
+union Raw {
+    Words<N * (int)sizeof(T)> w;
+    T e[N];
+    __device__ Raw() {}
+};
+
+template <int N, class T>
+__device__ __forceinline__ void load_raw(Raw<N, T> &u, const T *p) {
     const auto *src = reinterpret_cast<const decltype(u.w) *>(p);
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(u.w.w) / sizeof(u.w.w[0])); ++i) u.w.w[i] = __ldg(&src->w[i]);
-#pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = to_float(u.e[e]);
 }
 
 template <int N, class T>
 __device__ __forceinline__ void store_elems(T *p, const float (&x)[N]) {
-    union U {
-        Words<N * (int)sizeof(T)> w;
-        T e[N];
-        __device__ U() {}
-    } u;
+    Raw<N, T> u;
 #pragma unroll
     for (int e = 0; e < N; ++e) from_float(x[e], u.e[e]);
     *reinterpret_cast<decltype(u.w) *>(p) = u.w;
@@ -91,183 +87,298 @@ __device__ __forceinline__ float2 cos_sin_of(int p, float f, float m) {
         v = hi >> (sh - 64);
     else
         v = sh == 0 ? lo : (lo >> sh) | (hi << (64 - sh));
+    // The special-function unit's sine and cosine are off by 2^-21 in this range
+    // (as much as the angle's own rounding), a fraction of a query's fp16 or a
+    // key's int8 step; the accurate ones cost as much as a row.
     float s, c;
-    sincospif((float)(int32_t)(uint32_t)v * 4.656612873077393e-10f, &s, &c);  // 2^-31 half turns
+    __sincosf((float)(int32_t)(uint32_t)v * 1.4629180792671596e-09f, &s, &c);  // pi 2^-31
     return make_float2(c * m, p < 0 ? -s * m : s * m);
 }
 
-template <int D, class TI, class TO>
-__global__ void __launch_bounds__(PREP_WARPS * 32) paged_prep_kernel(const qsa_paged_prep_args a) {
+// The code of x under scale s (normal or subnormal fp16, inv = 1/s correctly
+// rounded), in the low byte: clamp(rint(x / s), -127, 127).  The quotient is
+// the correctly rounded one by P. Markstein's theorem ("Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): one
+// correction of x * inv by its exact remainder.  Adding 1.5 * 2^23 rounds it to
+// the nearest even integer, in the low mantissa bits.
+__device__ __forceinline__ uint32_t code_of(float x, float s, float inv) {
+    const float q = x * inv;
+    const float c = fminf(fmaxf(fmaf(fmaf(-q, s, x), inv, q), -127.0f), 127.0f);
+    return __float_as_uint(c + 12582912.0f);
+}
+
+struct PrepPlan {
+    int chunks, rows;  // runs per token, rows of a run (even)
+};
+
+template <int D, bool INTER, class TI, class TO>
+__global__ void __launch_bounds__(PREP_WARPS * 32) paged_prep_kernel(const qsa_paged_prep_args a, const PrepPlan plan) {
     constexpr int N = D / 32;  // elements per lane
-    __shared__ float2 cs[D / 2];
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, i0 = lane * N, half = a.rope_dims >> 1;
+    const long long task = (long long)blockIdx.x * PREP_WARPS + (threadIdx.x >> 5);
+    const int t = (int)(task / plan.chunks), chunk = (int)(task - (long long)t * plan.chunks);
+    if (t >= a.ntok) return;
+    const int hq = a.n_q_heads, hkv = a.n_kv_heads, nrows = hq + 2 * hkv;
+    const int r0 = chunk * plan.rows, r1 = min(r0 + plan.rows, nrows);
+    // The rows do not wait for the slot: a padding token's first ones are read
+    // too, and dropped.
     const int slot = __ldg(a.slots + t);
+    const int pos = __ldg(a.positions + t);
+    const TI *q = static_cast<const TI *>(a.q_in) + t * a.q_stride + i0;
+    const TI *k = static_cast<const TI *>(a.k_in) + t * a.k_stride + i0;
+    const TI *v = static_cast<const TI *>(a.v_in) + t * a.v_stride + i0;
+    Raw<N, TI> raw[BATCH];  // the next batch's rows, on their way
+    auto fetch = [&](int r) {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int row = min(r + j, nrows - 1);
+            load_raw(raw[j], row < hq ? q + row * D : row < hq + hkv ? k + (row - hq) * D : v + (row - hq - hkv) * D);
+        }
+    };
+    fetch(r0);
     if (slot < 0 || slot >= a.cache_cells) {
-        if (slot != -1 && threadIdx.x == 0 && blockIdx.y == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+        if (slot != -1 && lane == 0 && chunk == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
         return;
     }
-    const int hq = a.n_q_heads, hkv = a.n_kv_heads, nrows = hq + 2 * hkv;
-    const int row0 = blockIdx.y * ROWS_PER_BLOCK + warp * ROWS_PER_WARP;
-    float x[ROWS_PER_WARP][N];
-#pragma unroll
-    for (int j = 0; j < ROWS_PER_WARP; ++j) {
-        const int row = row0 + j;
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[j][e] = 0.0f;
-        if (row < nrows) {
-            const TI *src = row < hq         ? static_cast<const TI *>(a.q_in) + t * a.q_stride + row * D
-                            : row < hq + hkv ? static_cast<const TI *>(a.k_in) + t * a.k_stride + (row - hq) * D
-                                             : static_cast<const TI *>(a.v_in) + t * a.v_stride + (row - hq - hkv) * D;
-            load_elems<N>(src + lane * N, x[j]);
-        }
-    }
-    const int half = a.rope_dims >> 1;
-    if ((int)threadIdx.x < half)
-        cs[threadIdx.x] = cos_sin_of(__ldg(a.positions + t), __ldg(a.inv_freq + threadIdx.x), a.rope_mscale);
 
-    float ss[ROWS_PER_WARP];
+    // cos and sin of this lane's dims.  Interleaved: a pair's two dims are in
+    // one lane.  Halves: the partner dims are `sh` lanes away and turn by the
+    // same angles, so each of the two lanes works out half of them.
+    constexpr int NA = INTER ? N / 2 : N;
+    const bool turns = i0 < 2 * half, first = INTER || i0 < half;
+    const int sh = half / N, from = (first ? lane + sh : lane - sh) & 31;
+    float2 cs[NA];
+    if (half > 0 && r0 < hq + hkv) {
+        const int a0 = INTER ? i0 >> 1 : first ? i0 : i0 - half + N / 2;
+        float2 mine[N / 2];
 #pragma unroll
-    for (int j = 0; j < ROWS_PER_WARP; ++j) {
-        ss[j] = 0.0f;
+        for (int e = 0; e < N / 2; ++e)
+            mine[e] = cos_sin_of(pos, turns ? __ldg(a.inv_freq + a0 + e) : 0.0f, a.rope_mscale);
+        if constexpr (INTER) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) ss[j] = fmaf(x[j][e], x[j][e], ss[j]);
-    }
+            for (int e = 0; e < NA; ++e) cs[e] = mine[e];
+        } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int j = 0; j < ROWS_PER_WARP; ++j) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
-    __syncthreads();  // cs
-
-#pragma unroll
-    for (int j = 0; j < ROWS_PER_WARP; ++j) {
-        const int row = row0 + j;
-        if (row >= nrows) break;
-        const bool is_q = row < hq, is_v = row >= hq + hkv;
-        const float *w = is_q ? a.q_norm_w : is_v ? nullptr : a.k_norm_w;
-        if (w) {
-            float wv[N];
-            load_elems<N>(w + lane * N, wv);
-            const float rs = __frsqrt_rn(ss[j] * (1.0f / D) + a.eps);
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[j][e] = (rs * x[j][e]) * wv[e];
-        }
-        const int i0 = lane * N;
-        if (!is_v && half > 0) {
-            if (a.interleaved) {
-                if (i0 < 2 * half) {
-#pragma unroll
-                    for (int e = 0; e < N; e += 2) {
-                        const float2 c = cs[(i0 + e) >> 1];
-                        const float u = x[j][e], v = x[j][e + 1];
-                        x[j][e] = u * c.x - v * c.y;
-                        x[j][e + 1] = v * c.x + u * c.y;
-                    }
-                }
-            } else {
-                const int sh = half / N;  // lanes between partners
-                const bool first = i0 < half;
-                const int from = first ? lane + sh : lane - sh;
-#pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float o = __shfl_sync(0xffffffffu, x[j][e], from & 31);
-                    if (i0 < 2 * half) {
-                        const float2 c = cs[first ? i0 + e : i0 - half + e];
-                        x[j][e] = first ? x[j][e] * c.x - o * c.y : x[j][e] * c.x + o * c.y;
-                    }
-                }
+            for (int e = 0; e < N / 2; ++e) {
+                const float2 o = make_float2(__shfl_sync(0xffffffffu, mine[e].x, from), __shfl_sync(0xffffffffu, mine[e].y, from));
+                cs[e] = first ? mine[e] : o;
+                cs[e + N / 2] = first ? o : mine[e];
             }
         }
-        if (is_q) {
-            const size_t at = ((size_t)t * hq + row) * D;
-            if (QSA_IN(at + D - 1, (size_t)a.ntok * hq * D)) store_elems<N>(static_cast<TO *>(a.q_out) + at + i0, x[j]);
-            continue;
+    }
+
+    const float *w = nullptr;
+    float wv[N];
+    auto weights = [&](const float *wr) {  // once for a run's rows of one kind
+        if (w == wr) return;
+        Raw<N, float> u;
+        load_raw(u, wr + i0);
+#pragma unroll
+        for (int e = 0; e < N; ++e) wv[e] = u.e[e];
+        w = wr;
+    };
+    float x[BATCH][N], ss[BATCH];
+    auto squares = [&] {
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int e = 0; e < N; e += 2) s2 = __ffma2_rn(make_float2(x[j][e], x[j][e + 1]), make_float2(x[j][e], x[j][e + 1]), s2);
+            ss[j] = s2.x + s2.y;
         }
-        // The largest magnitude as an integer, so that a NaN is the largest.
-        uint32_t top = 0u;
 #pragma unroll
-        for (int e = 0; e < N; ++e) top = max(top, __float_as_uint(x[j][e]) & 0x7FFFFFFFu);
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const __half sch = __float2half_rn(__fdiv_rn(__uint_as_float(top), 127.0f));
-        const float sc = __half2float(sch);
-        const size_t cell = (size_t)slot * hkv + (row - hq - (is_v ? hkv : 0));
-        if (!QSA_IN(cell, (size_t)a.cache_cells * hkv)) continue;
-        uint32_t code[N / 4];
+            for (int j = 0; j < BATCH; ++j) ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], o);
+    };
+    auto norm = [&](int j) {
+        const float rs = rsqrtf(ss[j] * (1.0f / D) + a.eps);  // off by at most 2^-22
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            float c = 0.0f;
-            if (sc != 0.0f) c = fminf(fmaxf(rintf(__fdiv_rn(x[j][e], sc)), -127.0f), 127.0f);
-            const uint32_t b = (uint32_t)(uint8_t)(int8_t)(int)c << (8 * (e & 3));
-            code[e / 4] = (e & 3) ? code[e / 4] | b : b;
+        for (int e = 0; e < N; e += 2) {
+            float2 y = __fmul2_rn(make_float2(x[j][e], x[j][e + 1]), make_float2(rs, rs));
+            y = __fmul2_rn(y, make_float2(wv[e], wv[e + 1]));
+            x[j][e] = y.x;
+            x[j][e + 1] = y.y;
         }
-        int8_t *dst = (is_v ? a.vq : a.kq) + cell * D + i0;
-        if constexpr (N == 4)
-            *reinterpret_cast<uint32_t *>(dst) = code[0];
-        else
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
-        if ((lane & 7) == 0) (is_v ? a.vsc : a.ksc)[cell * 4 + (lane >> 3)] = __half_as_ushort(sch);
+    };
+    auto turn = [&](int j) {
+        if constexpr (INTER) {
+            if (turns) {
+#pragma unroll
+                for (int e = 0; e < N; e += 2) {
+                    const float y0 = x[j][e], y1 = x[j][e + 1];
+                    x[j][e] = y0 * cs[e / 2].x - y1 * cs[e / 2].y;
+                    x[j][e + 1] = y1 * cs[e / 2].x + y0 * cs[e / 2].y;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float o = __shfl_sync(0xffffffffu, x[j][e], from);
+                if (turns) x[j][e] = fmaf(x[j][e], cs[e].x, first ? -o * cs[e].y : o * cs[e].y);
+            }
+        }
+    };
+    auto take = [&](int r) {  // batch r's rows; the next one's loads start
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[j][e] = to_float(raw[j].e[e]);
+        if (r + BATCH < r1) fetch(r + BATCH);
+    };
+
+    // Query rows by whole batches, without the branches of the mixed ones below.
+    int r = r0;
+    TO *out = static_cast<TO *>(a.q_out) + (size_t)t * hq * D + i0;
+    if (a.q_norm_w && r + BATCH <= min(r1, hq)) weights(a.q_norm_w);
+    for (; r + BATCH <= min(r1, hq); r += BATCH) {
+        take(r);
+        if (a.q_norm_w) {
+            squares();
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) norm(j);
+        }
+        if (half > 0) {
+#pragma unroll
+            for (int j = 0; j < BATCH; ++j) turn(j);
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j)
+            if (QSA_IN(((size_t)t * hq + r + j) * D + D - 1, (size_t)a.ntok * hq * D)) store_elems<N>(out + (r + j) * D, x[j]);
+    }
+    for (; r < r1; r += BATCH) {
+        take(r);
+        if (r < hq + hkv) squares();
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            const int row = r + j;
+            if (row >= r1) break;
+            const bool is_q = row < hq, is_v = row >= hq + hkv;
+            if (!is_v) {
+                const float *wr = is_q ? a.q_norm_w : a.k_norm_w;
+                if (wr) {
+                    weights(wr);
+                    norm(j);
+                }
+                if (half > 0) turn(j);
+            }
+            if (is_q) {
+                if (QSA_IN(((size_t)t * hq + row) * D + D - 1, (size_t)a.ntok * hq * D)) store_elems<N>(out + row * D, x[j]);
+                continue;
+            }
+            // The largest magnitude as an integer, so that a NaN is the largest.
+            uint32_t top = 0u;
+#pragma unroll
+            for (int e = 0; e < N; ++e) top = max(top, __float_as_uint(x[j][e]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const __half sch = __float2half_rn(__fdiv_rn(__uint_as_float(top), 127.0f));
+            const float sc = __half2float(sch);
+            const size_t cell = (size_t)slot * hkv + (row - hq - (is_v ? hkv : 0));
+            if (!QSA_IN(cell, (size_t)a.cache_cells * hkv)) continue;
+            uint32_t code[N / 4];
+            const bool fine = sc > 0.0f && sc <= 65504.0f;
+            const float inv = fine ? __frcp_rn(sc) : 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; e += 4) {
+                uint32_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = fine ? code_of(x[j][e + i], sc, inv) : 0u;
+                code[e / 4] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+            }
+            int8_t *dst = (is_v ? a.vq : a.kq) + cell * D + i0;
+            if constexpr (N == 4)
+                *reinterpret_cast<uint32_t *>(dst) = code[0];
+            else
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(code[0], code[1]);
+            if ((lane & 7) == 0) (is_v ? a.vsc : a.ksc)[cell * 4 + (lane >> 3)] = __half_as_ushort(sch);
+        }
     }
 }
 
-// Gather: a thread takes eight dims of one (cell, KV head), of both K and V,
-// so that neighbouring threads read 8-byte and write 16-byte words of one row.
+// Gather: bound by its traffic, 2 (D + 8) bytes read and 2 D elements written
+// per (cell, KV head).  A thread takes sixteen dims of one (cell, KV head), of
+// both K and V, so that a warp reads and writes whole rows.  A block takes
+// ids_per_block whole ids, so that an item's id and place need 32-bit
+// arithmetic only.
 constexpr int GATHER_THREADS = 256;
 
+struct GatherPlan {
+    int per_id, ids_per_block;
+    uint32_t magic;  // ceil(2^32 / per_id): item * magic >> 32 is item / per_id for the at most 1024 items; 0 for one id
+};
+
 template <class T>
-__global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(const qsa_paged_gather_args a) {
+__global__ void __launch_bounds__(GATHER_THREADS) paged_gather_kernel(const qsa_paged_gather_args a, const GatherPlan g) {
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int per_row = a.head_dim / 8, per_id = a.n_kv_heads * per_row;
-    const long long i = (long long)blockIdx.x * GATHER_THREADS + threadIdx.x;
-    const long long id_i = i / per_id;
-    if (id_i >= a.n_ids) return;
-    const int in_id = (int)(i - id_i * per_id), h = in_id / per_row, d = (in_id - h * per_row) * 8;
-    long long cell = __ldg(a.ids + id_i);
-    bool bad = cell < -1;
-    if (cell >= 0 && a.page_table) {
-        const int row = __ldg(a.rows + id_i);
-        const long long page = cell / a.page_size;
-        if (row < 0 || row >= a.n_rows || page >= a.max_pages) {
+    const int per_row = a.head_dim / 16, shift = a.head_dim == 128 ? 3 : 4, page_shift = 31 - __clz(a.page_size | 1);
+    const long long id0 = (long long)blockIdx.x * g.ids_per_block;
+    const int items = (int)(a.n_ids - id0 < g.ids_per_block ? a.n_ids - id0 : g.ids_per_block) * g.per_id;
+    for (int it = threadIdx.x; it < items; it += GATHER_THREADS) {
+        const int id = (int)__umulhi((uint32_t)it, g.magic), in_id = it - id * g.per_id;
+        int cell = __ldg(a.ids + id0 + id);
+        bool bad = cell < -1;
+        if (cell >= 0 && a.page_table) {
+            const int row = __ldg(a.rows + id0 + id), page = cell >> page_shift, in_page = cell & (a.page_size - 1);
+            bad = row < 0 || row >= a.n_rows || page >= a.max_pages;
+            const int e = bad ? -1 : __ldg(a.page_table + (size_t)row * a.max_pages + page);
+            bad |= e < 0 || e > ((a.cache_cells - 1) >> page_shift);
+            cell = bad ? -1 : (e << page_shift) + in_page;
+        }
+        if (cell >= a.cache_cells) {
             bad = true;
             cell = -1;
-        } else {
-            const int e = __ldg(a.page_table + (size_t)row * a.max_pages + page);
-            cell = e < 0 ? -2 : (long long)e * a.page_size + cell % a.page_size;
-            bad = e < 0;
+        }
+        if (bad && in_id == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+        uint4 k = make_uint4(0u, 0u, 0u, 0u), v = k;
+        uint16_t ks = 0, vs = 0;
+        if (cell >= 0) {
+            const int h = in_id >> shift, c = in_id & (per_row - 1);
+            const size_t row = (size_t)cell * a.n_kv_heads + h;
+            k = __ldg(reinterpret_cast<const uint4 *>(a.kq + row * a.head_dim) + c);
+            v = __ldg(reinterpret_cast<const uint4 *>(a.vq + row * a.head_dim) + c);
+            ks = __ldg(a.ksc + row * 4 + (c >> (shift - 2)));
+            vs = __ldg(a.vsc + row * 4 + (c >> (shift - 2)));
+        }
+        const size_t at = (size_t)(id0 + id) * a.n_kv_heads * a.head_dim + in_id * 16;
+        if (!QSA_IN(at + 15, (size_t)a.n_ids * a.n_kv_heads * a.head_dim)) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float f = __half2float(__ushort_as_half(i ? vs : ks));
+            const uint32_t w[4] = {i ? v.x : k.x, i ? v.y : k.y, i ? v.z : k.z, i ? v.w : k.w};
+            T *dst = static_cast<T *>(i ? a.v_out : a.k_out) + at;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = (float)(int8_t)(w[2 * p + (e >> 2)] >> (8 * (e & 3))) * f;
+                store_elems<8>(dst + 8 * p, y);
+            }
         }
     }
-    bad |= cell >= a.cache_cells;
-    if (bad && in_id == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
-    float k[8], v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.0f;
-    if (cell >= 0 && cell < a.cache_cells) {
-        const size_t row = (size_t)cell * a.n_kv_heads + h;
-        const uint2 kw = __ldg(reinterpret_cast<const uint2 *>(a.kq + row * a.head_dim + d));
-        const uint2 vw = __ldg(reinterpret_cast<const uint2 *>(a.vq + row * a.head_dim + d));
-        const float ks = __half2float(__ushort_as_half(__ldg(a.ksc + row * 4 + d / a.group)));
-        const float vs = __half2float(__ushort_as_half(__ldg(a.vsc + row * 4 + d / a.group)));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            k[e] = (float)(int8_t)((e < 4 ? kw.x : kw.y) >> (8 * (e & 3))) * ks;
-            v[e] = (float)(int8_t)((e < 4 ? vw.x : vw.y) >> (8 * (e & 3))) * vs;
-        }
-    }
-    const size_t at = ((size_t)id_i * a.n_kv_heads + h) * a.head_dim + d;
-    if (!QSA_IN(at + 7, (size_t)a.n_ids * a.n_kv_heads * a.head_dim)) return;
-    store_elems<8>(static_cast<T *>(a.k_out) + at, k);
-    store_elems<8>(static_cast<T *>(a.v_out) + at, v);
+}
+
+template <int D, class TI, class TO>
+cudaError_t prep_run(const qsa_paged_prep_args &a, cudaStream_t s) {
+    // One run per token, or more while there are fewer runs than 24 warps per SM.
+    const int nrows = a.n_q_heads + 2 * a.n_kv_heads;
+    const long long want = (152 * 24 + a.ntok - 1) / a.ntok;
+    PrepPlan p;
+    p.rows = (int)((nrows + want - 1) / want);
+    p.rows += p.rows & 1;
+    p.chunks = (nrows + p.rows - 1) / p.rows;
+    const long long tasks = (long long)a.ntok * p.chunks;
+    const dim3 grid((unsigned)((tasks + PREP_WARPS - 1) / PREP_WARPS)), block(PREP_WARPS * 32);
+    return a.interleaved ? launch_dependent(paged_prep_kernel<D, true, TI, TO>, grid, block, 0, s, a, p)
+                         : launch_dependent(paged_prep_kernel<D, false, TI, TO>, grid, block, 0, s, a, p);
 }
 
 template <int D, class TI>
 cudaError_t prep_to(const qsa_paged_prep_args &a, cudaStream_t s) {
-    const int nrows = a.n_q_heads + 2 * a.n_kv_heads;
-    const dim3 grid(a.ntok, (nrows + ROWS_PER_BLOCK - 1) / ROWS_PER_BLOCK);
-    if (a.q_out_dtype == QSA_F16)
-        return launch_dependent(paged_prep_kernel<D, TI, __half>, grid, dim3(PREP_WARPS * 32), 0, s, a);
-    return launch_dependent(paged_prep_kernel<D, TI, __nv_bfloat16>, grid, dim3(PREP_WARPS * 32), 0, s, a);
+    return a.q_out_dtype == QSA_F16 ? prep_run<D, TI, __half>(a, s) : prep_run<D, TI, __nv_bfloat16>(a, s);
 }
 
 template <int D>
@@ -284,11 +395,17 @@ cudaError_t launch_paged_prep(const qsa_paged_prep_args &a, cudaStream_t s) {
 }
 
 cudaError_t launch_paged_gather(const qsa_paged_gather_args &a, cudaStream_t s) {
-    const long long n = (long long)a.n_ids * a.n_kv_heads * (a.head_dim / 8);
-    const dim3 grid((unsigned)((n + GATHER_THREADS - 1) / GATHER_THREADS)), block(GATHER_THREADS);
-    return a.out_dtype == QSA_F32   ? launch_dependent(paged_gather_kernel<float>, grid, block, 0, s, a)
-           : a.out_dtype == QSA_F16 ? launch_dependent(paged_gather_kernel<__half>, grid, block, 0, s, a)
-                                    : launch_dependent(paged_gather_kernel<__nv_bfloat16>, grid, block, 0, s, a);
+    GatherPlan g;
+    g.per_id = a.n_kv_heads * (a.head_dim / 16);
+    // Up to four rounds of a block's threads, fewer while that leaves SMs
+    // without blocks (321 cells: 5.3 us with three blocks, 2.1 us with one per id).
+    const int most = 4 * GATHER_THREADS / g.per_id, spread = (int)(((long long)a.n_ids + 607) / 608);
+    g.ids_per_block = spread < most ? spread : most < 1 ? 1 : most;
+    g.magic = g.ids_per_block == 1 ? 0u : (uint32_t)(((1ull << 32) + g.per_id - 1) / g.per_id);
+    const dim3 grid((unsigned)(((long long)a.n_ids + g.ids_per_block - 1) / g.ids_per_block)), block(GATHER_THREADS);
+    return a.out_dtype == QSA_F32   ? launch_dependent(paged_gather_kernel<float>, grid, block, 0, s, a, g)
+           : a.out_dtype == QSA_F16 ? launch_dependent(paged_gather_kernel<__half>, grid, block, 0, s, a, g)
+                                    : launch_dependent(paged_gather_kernel<__nv_bfloat16>, grid, block, 0, s, a, g);
 }
 
 }  // namespace qsa

@@ -1,15 +1,16 @@
 // qsa_page_update and qsa_page_compact: the paged cache's bookkeeping and the
 // page copies that it calls for.
 //
-// Each call is two launches.  The first, one cluster of eight blocks, works
-// out the new table: it counts how often each page is held, ranks the free
-// (or moved) pages by prefix sums, deals them out and leaves a list of copies
-// in the workspace.  Its phases are separated by the cluster's hardware
-// barrier, which also orders their global-memory traffic; a grid-wide form
-// would need one launch per phase, and the tables are small (a phase is a few
-// loads per thread).  The second launch runs over the whole chip and copies
-// the listed pages in 16-byte words; sources and targets are disjoint, so no
-// order among them matters.
+// Each call is two launches.  The first works out the new table: it counts how
+// often each page is held, ranks the free (or moved) pages by prefix sums,
+// deals them out and leaves a list of copies in the workspace.  It is bound by
+// the latency of its phases, a few dependent loads each, so it is one block
+// with the counts in shared memory while pool and table are small (SMALL_*),
+// and one cluster of eight blocks with the counts in the refs output above
+// that; the phases are separated by the block's or the cluster's hardware
+// barrier, where a grid-wide form would need one launch per phase.  The second
+// launch runs over the whole chip and copies the listed pages; sources and
+// targets are disjoint, so no order among them matters.
 //
 // All results are whole numbers and do not depend on the order of the atomic
 // counts.
@@ -21,10 +22,14 @@
 namespace qsa {
 namespace {
 
-constexpr int CTAS = 8;
+constexpr int CLUSTER = 8;
 constexpr int THREADS = 1024;
-constexpr int ALL = CTAS * THREADS;
-constexpr int SEG = 256;  // table columns a warp takes at a time
+constexpr int SEG = 128;  // table columns a warp takes at a time
+
+// One block up to this many pages (128 KB of counts) and table entries.  A
+// decode step of 64 rows over 1700 pages: one block X_ONE us, cluster X_CLU.
+constexpr int SMALL_PAGES = 32768;
+constexpr long long SMALL_ENTRIES = 65536;
 
 // One page copy: the first `cells` cells of page src go to page dst.
 struct Copy {
@@ -38,11 +43,11 @@ struct RowPlan {
     int keep, need;       // length before growing; pages asked for (-1: does not fit)
 };
 struct Header {
-    int n_copies, pad[3];
-    long long n_free_or_live, tokens;
-    long long part[CTAS][2];
+    int n_copies, n_live;
+    long long asked, tokens;       // pages asked for; tokens of the packed batch
+    int count[CLUSTER * THREADS / 32];  // a warp's count of its slice of the pool
 };
-constexpr size_t HEADER_BYTES = 256;
+constexpr size_t HEADER_BYTES = 2048;
 static_assert(sizeof(Header) <= HEADER_BYTES, "workspace header");
 
 struct Ws {
@@ -73,14 +78,52 @@ size_t ws_bytes(int n_rows, int n_pages) {
            align16(copies * sizeof(Copy));
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ unsigned cluster_rank() {
-    unsigned r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
+// The blocks that work on one table: CTAS of them, with counts in shared
+// memory (one) or in the refs output (a cluster).
+template <int CTAS>
+struct Team {
+    static constexpr int ALL = CTAS * THREADS, WARPS = ALL / 32;
+
+    static __device__ __forceinline__ int rank() {
+        if constexpr (CTAS == 1) return 0;
+        unsigned r;
+        asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+        return (int)r;
+    }
+    static __device__ __forceinline__ void sync() {
+        if constexpr (CTAS == 1)
+            __syncthreads();
+        else
+            asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
+    // A value that another block may have written in an earlier phase.
+    template <class T>
+    static __device__ __forceinline__ T peek(const T *p) {
+        if constexpr (CTAS == 1)
+            return *p;
+        else
+            return __ldcg(p);
+    }
+    // Slice of the pool that warp w counts and ranks: whole groups of 32 pages.
+    static __device__ __forceinline__ void slice(int w, int n_pages, int &p0, int &p1) {
+        const int per = ((n_pages + 31) / 32 + WARPS - 1) / WARPS * 32;
+        p0 = (int)min((long long)w * per, (long long)n_pages);
+        p1 = min(p0 + per, n_pages);
+    }
+    // Sum of the warps' counts, and of those before warp w.
+    static __device__ __forceinline__ void totals(const int *count, int w, int &before, int &total) {
+        const int lane = threadIdx.x & 31;
+        before = total = 0;
+#pragma unroll
+        for (int i = 0; i < WARPS / 32; ++i) {
+            const int v = peek(count + i * 32 + lane);
+            total += v;
+            before += i * 32 + lane < w ? v : 0;
+        }
+        before = __reduce_add_sync(0xffffffffu, before);
+        total = __reduce_add_sync(0xffffffffu, total);
+    }
+};
 
 // Exclusive prefix of v over the block (in thread order); total to all.
 __device__ __forceinline__ long long block_scan(long long v, long long &total, long long *tmp) {
@@ -94,18 +137,15 @@ __device__ __forceinline__ long long block_scan(long long v, long long &total, l
     __syncthreads();  // tmp may still be read from the scan before
     if (lane == 31) tmp[warp] = s;
     __syncthreads();
-    if (warp == 0) {
-        long long w = tmp[lane];
+    long long w = tmp[lane];  // every warp adds up the warps before it
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, w, o);
-            if (lane >= o) w += u;
-        }
-        tmp[lane] = w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += u;
     }
-    __syncthreads();
-    total = tmp[31];
-    return s - v + (warp ? tmp[warp - 1] : 0);
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const long long before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return s - v + (warp ? before : 0);
 }
 
 __device__ __forceinline__ void flag(unsigned int *err, unsigned bit) {
@@ -141,35 +181,52 @@ __device__ __forceinline__ int pages_of(long long cells, int page_size) {
 
 // Copies the kept entries to the new table (-1 behind them and for an entry
 // outside the pool) and counts them in refs, which is zero before.  A warp
-// takes SEG columns of a row at a time.
-template <bool WRITE>
-__device__ __forceinline__ void gather_and_count(const TableArgs &a, int rank) {
+// takes SEG columns of a row at a time, and BATCH of these items at once, so
+// that the chains of loads (source row, length, entries) of several rows are in
+// flight together.  With WRITE the rows' lengths go to their plans.
+template <int CTAS, bool WRITE>
+__device__ __forceinline__ void gather_and_count(const TableArgs &a, int *refs, RowPlan *rows, int warp) {
+    constexpr int BATCH = 4, E = SEG / 32, W = Team<CTAS>::WARPS;
     const int lane = threadIdx.x & 31;
     const int segs = (a.max_pages + SEG - 1) / SEG;
     const long long items = (long long)a.n_rows * segs;
-    for (long long it = rank * (THREADS / 32) + (threadIdx.x >> 5); it < items; it += ALL / 32) {
-        const int r = (int)(it / segs), j0 = (int)(it % segs) * SEG;
-        int from;
-        const int had = pages_of(row_keep(a, r, from), a.page_size);
-        int e[SEG / 32];
+    for (long long it0 = warp; it0 < items; it0 += W * BATCH) {
+        int row = 0, from = -1, had = 0;  // lane b's: item it0 + b W
+        if (lane < BATCH && it0 + lane * W < items) {
+            row = (int)(segs == 1 ? it0 + lane * W : (it0 + lane * W) / segs);
+            const int keep = row_keep(a, row, from);
+            had = pages_of(keep, a.page_size);
+            if (WRITE) rows[row].keep = keep;  // the same from each of a row's items
+        }
+        int e[BATCH][E];
 #pragma unroll
-        for (int i = 0; i < SEG / 32; ++i) {
-            const int j = j0 + i * 32 + lane;
-            e[i] = -1;
-            if (j < had && QSA_IN((size_t)from * a.max_pages + j, (size_t)a.n_rows_in * a.max_pages)) {
-                e[i] = a.table[(size_t)from * a.max_pages + j];
-                if (e[i] < 0 || e[i] >= a.n_pages) {
+        for (int b = 0; b < BATCH; ++b) {
+            const int f = __shfl_sync(0xffffffffu, from, b), n = __shfl_sync(0xffffffffu, had, b);
+            const int j0 = segs == 1 ? lane : (int)((it0 + b * W) % segs) * SEG + lane;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int j = j0 + i * 32;
+                e[b][i] = j < n && QSA_IN((size_t)f * a.max_pages + j, (size_t)a.n_rows_in * a.max_pages)
+                              ? a.table[(size_t)f * a.max_pages + j]
+                              : -1;
+                if (j < n && (e[b][i] < 0 || e[b][i] >= a.n_pages)) {
                     flag(a.err, QSA_DEVERR_BAD_ID);
-                    e[i] = -1;
+                    e[b][i] = -1;
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < SEG / 32; ++i) {
-            const int j = j0 + i * 32 + lane;
-            if (e[i] >= 0) atomicAdd(a.refs + e[i], 1);
-            if (WRITE && j < a.max_pages && QSA_IN((size_t)r * a.max_pages + j, (size_t)a.n_rows * a.max_pages))
-                a.table_out[(size_t)r * a.max_pages + j] = e[i];
+        for (int b = 0; b < BATCH; ++b) {
+            if (it0 + b * W >= items) break;
+            const int r = __shfl_sync(0xffffffffu, row, b);
+            const int j0 = segs == 1 ? lane : (int)((it0 + b * W) % segs) * SEG + lane;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const int j = j0 + i * 32;
+                if (e[b][i] >= 0) atomicAdd(refs + e[b][i], 1);
+                if (WRITE && j < a.max_pages && QSA_IN((size_t)r * a.max_pages + j, (size_t)a.n_rows * a.max_pages))
+                    a.table_out[(size_t)r * a.max_pages + j] = e[b][i];
+            }
         }
     }
 }
@@ -182,133 +239,147 @@ struct UpdateLaunch {
     void *ws;
 };
 
-__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) page_update_kernel(const UpdateLaunch a) {
+template <int CTAS>
+__global__ void __launch_bounds__(THREADS) page_update_kernel(const UpdateLaunch a) {
+    using T = Team<CTAS>;
+    extern __shared__ int counts[];
     __shared__ long long tmp[32];
+    __shared__ Header local;
     const TableArgs &t = a.t;
-    const int rank = (int)cluster_rank(), tid = threadIdx.x, gtid = rank * THREADS + tid;
+    const int rank = T::rank(), tid = threadIdx.x, gtid = rank * THREADS + tid, lane = tid & 31, warp = gtid >> 5;
     const Ws ws = carve(a.ws, t.n_rows, t.n_pages);
+    int *refs = CTAS == 1 ? counts : t.refs;
+    Header *h = CTAS == 1 ? &local : ws.h;
+    for (int p = gtid; CTAS == 1 && p < t.n_pages; p += T::ALL) refs[p] = 0;
     wait_for_previous_grid();
     allow_dependent_launch();
-    for (int p = gtid; p < t.n_pages; p += ALL) t.refs[p] = 0;
+    for (int p = gtid; CTAS > 1 && p < t.n_pages; p += T::ALL) refs[p] = 0;
     if (gtid == 0) ws.h->n_copies = 0;
-    cluster_sync();
-    gather_and_count<true>(t, rank);
-    cluster_sync();
+    T::sync();
+    gather_and_count<CTAS, true>(t, refs, ws.rows, warp);
+    T::sync();
 
-    // Block 0 plans the rows in order; the others count the free pages of
-    // their slices of the pool.
-    constexpr int SCAN = CTAS - 1;
-    const int per = (t.n_pages + SCAN - 1) / SCAN;
-    const int p0 = min((rank - 1) * per, t.n_pages), p1 = min(p0 + per, t.n_pages);
+    // Each warp counts the free pages of its slice, and block 0 plans the rows
+    // in order.
+    int p0, p1;
+    T::slice(warp, t.n_pages, p0, p1);
+    int n_mine = 0;
+    for (int p = p0 + lane; p - lane < p1; p += 32)
+        n_mine += __popc(__ballot_sync(0xffffffffu, p < p1 && T::peek(refs + p) == 0));
+    if (lane == 0) h->count[warp] = n_mine;
     if (rank == 0) {
         long long off0 = 0, need0 = 0;
         for (int base = 0; base < t.n_rows; base += THREADS) {
             const int r = base + tid;
-            int n = 0, keep = 0, need = 0;
+            int n = 0, keep = 0, need = 0, held = -1;
             if (r < t.n_rows) {
-                int from;
-                keep = row_keep(t, r, from);
+                keep = T::peek(&ws.rows[r].keep);
                 n = a.n_new[r];
                 if (n < 0) {
                     flag(t.err, QSA_DEVERR_BAD_ID);
                     n = 0;
                 }
+                if (n > 0 && keep % t.page_size) held = T::peek(t.table_out + (size_t)r * t.max_pages + keep / t.page_size);
             }
             long long total;
             const long long off = off0 + block_scan(n, total, tmp);
             off0 += total;
             if (n > 0) {
                 const long long want = ((long long)keep + n + t.page_size - 1) / t.page_size;
-                if (want > t.max_pages || off + n > a.n_slots) {
+                if (want > t.max_pages || off + n > a.n_slots)
                     need = -1;
-                } else {
-                    need = (int)want - pages_of(keep, t.page_size);
-                    if (keep % t.page_size) {
-                        const int held = __ldcg(t.table_out + (size_t)r * t.max_pages + keep / t.page_size);
-                        need += held >= 0 && __ldcg(t.refs + held) > 1;
-                    }
-                }
+                else
+                    need = (int)want - pages_of(keep, t.page_size) + (held >= 0 && T::peek(refs + held) > 1);
             }
-            const long long upto = need0 + block_scan(need > 0 ? need : 0, total, tmp) + (need > 0 ? need : 0);
+            const long long upto = need0 + block_scan(max(need, 0), total, tmp) + max(need, 0);
             need0 += total;
-            if (r < t.n_rows) ws.rows[r] = RowPlan{off, upto, keep, need};
+            if (r < t.n_rows) {
+                ws.rows[r].off = off;
+                ws.rows[r].upto = upto;
+                ws.rows[r].need = need;
+            }
         }
         if (tid == 0) {
-            ws.h->tokens = off0;
-            ws.h->part[0][0] = need0;
+            h->tokens = off0;
+            h->asked = need0;
         }
-    } else {
-        long long mine = 0, total;
-        for (int p = p0 + tid; p < p1; p += THREADS) mine += __ldcg(t.refs + p) == 0;
-        block_scan(mine, total, tmp);
-        if (tid == 0) ws.h->part[rank][0] = total;
     }
-    cluster_sync();
+    T::sync();
 
     // The free pages by rank, as far as they are asked for.
-    const long long asked = __ldcg(&ws.h->part[0][0]);
-    long long free_before = 0, n_free = 0;
-    for (int c = 1; c < CTAS; ++c) {
-        const long long v = __ldcg(&ws.h->part[c][0]);
-        n_free += v;
-        if (c < rank) free_before += v;
+    const long long asked = T::peek(&h->asked);
+    int before, n_free;
+    T::totals(h->count, warp, before, n_free);
+    for (int p = p0 + lane; p - lane < p1 && before < asked; p += 32) {
+        const bool is_free = p < p1 && T::peek(refs + p) == 0;
+        const unsigned m = __ballot_sync(0xffffffffu, is_free);
+        const int at = before + __popc(m & ((1u << lane) - 1));
+        if (is_free && at < asked) ws.list[at] = p;
+        before += __popc(m);
     }
-    if (rank > 0) {
-        for (int base = p0; base < p1 && free_before < asked; base += THREADS) {
-            const int p = base + tid;
-            const int is_free = p < p1 && __ldcg(t.refs + p) == 0;
-            long long total;
-            const long long at = free_before + block_scan(is_free, total, tmp);
-            if (is_free && at < asked) ws.list[at] = p;
-            free_before += total;
-        }
-    }
-    cluster_sync();
+    T::sync();
 
-    // Deal the pages out, a warp per row.
-    const int lane = tid & 31;
-    for (int r = gtid >> 5; r < t.n_rows; r += ALL / 32) {
-        const RowPlan pl{__ldcg(&ws.rows[r].off), __ldcg(&ws.rows[r].upto), __ldcg(&ws.rows[r].keep), __ldcg(&ws.rows[r].need)};
-        const int n = max(a.n_new[r], 0);
-        const bool ok = n > 0 && pl.need >= 0 && (pl.need == 0 || pl.upto <= n_free);
-        int32_t *row = t.table_out + (size_t)r * t.max_pages;
-        const int had = pages_of(pl.keep, t.page_size), tail = pl.keep % t.page_size;
-        if (n > 0 && !ok && lane == 0) flag(t.err, QSA_DEVERR_NO_PAGES);
-        if (ok) {
-            const int want = pages_of((long long)pl.keep + n, t.page_size);
-            const int copied = pl.need - (want - had);  // 1: the last page is copied first
-            const long long first = pl.upto - pl.need;
-            int last = tail ? __ldcg(row + had - 1) : -1;
-            if (copied) {
-                const int to = __ldcg(ws.list + first);
-                if (lane == 0) {
-                    ws.copies[atomicAdd(&ws.h->n_copies, 1)] = Copy{last, to, tail};
-                    atomicSub(t.refs + last, 1);
-                    t.refs[to] = 1;
-                    row[had - 1] = to;
+    // Deal the pages out: a lane per row works out what the row gets, and
+    // writes it where that is a few tokens; the warp writes the long ones.
+    for (int base = warp * 32; base < t.n_rows; base += T::WARPS * 32) {
+        const int r = base + lane;
+        int n = 0, keep = 0, had = 0, want = 0, copied = 0, last = -1;
+        long long off = 0, first = 0;
+        bool ok = false;
+        if (r < t.n_rows) {
+            n = max(a.n_new[r], 0);
+            keep = T::peek(&ws.rows[r].keep);
+            const int need = T::peek(&ws.rows[r].need);
+            off = T::peek(&ws.rows[r].off);
+            const long long upto = T::peek(&ws.rows[r].upto);
+            ok = n > 0 && need >= 0 && (need == 0 || upto <= n_free);
+            had = pages_of(keep, t.page_size);
+            if (n > 0 && !ok) flag(t.err, QSA_DEVERR_NO_PAGES);
+            a.lens_out[r] = keep + (ok ? n : 0);
+            if (ok) {
+                want = pages_of((long long)keep + n, t.page_size);
+                copied = need - (want - had);  // 1: the last page is copied first
+                first = upto - need;
+                int32_t *const slot = t.table_out + (size_t)r * t.max_pages + had - 1;
+                if (keep % t.page_size) last = T::peek(slot);
+                if (copied) {
+                    const int to = T::peek(ws.list + first);
+                    ws.copies[atomicAdd(&ws.h->n_copies, 1)] = Copy{last, to, keep % t.page_size};
+                    atomicSub(refs + last, 1);
+                    refs[to] = 1;
+                    *slot = last = to;
                 }
-                last = to;
+                first += copied;
             }
-            for (int j = had + lane; j < want; j += 32) {
-                const int p = __ldcg(ws.list + first + copied + (j - had));
-                row[j] = p;
-                t.refs[p] = 1;
-            }
-            // Token i of the row sits at position keep + i.
-            for (int i = lane; i < n; i += 32) {
-                const int pos = pl.keep + i, j = pos / t.page_size;
-                const int p = j < had ? last : __ldcg(ws.list + first + copied + (j - had));
-                if (!QSA_IN(pl.off + i, a.n_slots)) continue;
-                a.slots[pl.off + i] = p < 0 ? -1 : p * t.page_size + pos % t.page_size;
-                a.positions[pl.off + i] = pos;
-            }
-        } else {
-            for (long long i = pl.off + lane; i < pl.off + n && i < a.n_slots; i += 32) a.slots[i] = a.positions[i] = -1;
         }
-        __syncwarp();
-        if (lane == 0) a.lens_out[r] = pl.keep + (ok ? n : 0);
+        // Row rr's pages from index j0 and tokens from i0 on, every `step`-th.
+        auto write = [&](int rr, int n, int keep, int had, int want, int last, long long off, long long first, bool ok, int i0,
+                         int step) {
+            for (int j = had + i0; ok && j < want; j += step) {
+                const int p = T::peek(ws.list + first + (j - had));
+                t.table_out[(size_t)rr * t.max_pages + j] = p;
+                refs[p] = 1;
+            }
+            for (int i = i0; i < n && off + i < a.n_slots; i += step) {  // token i sits at position keep + i
+                const int pos = keep + i, j = pos / t.page_size;
+                const int p = !ok ? -1 : j < had ? last : T::peek(ws.list + first + (j - had));
+                a.slots[off + i] = p < 0 ? -1 : p * t.page_size + pos % t.page_size;
+                a.positions[off + i] = ok ? pos : -1;
+            }
+        };
+        if (n <= 8) write(r, n, keep, had, want, last, off, first, ok, 0, 1);
+        for (unsigned m = __ballot_sync(0xffffffffu, n > 8); m; m &= m - 1) {
+            const int b = __ffs(m) - 1;
+            write(base + b, __shfl_sync(0xffffffffu, n, b), __shfl_sync(0xffffffffu, keep, b), __shfl_sync(0xffffffffu, had, b),
+                  __shfl_sync(0xffffffffu, want, b), __shfl_sync(0xffffffffu, last, b), __shfl_sync(0xffffffffu, off, b),
+                  __shfl_sync(0xffffffffu, first, b), __shfl_sync(0xffffffffu, (int)ok, b), lane, 32);
+        }
     }
-    for (long long i = __ldcg(&ws.h->tokens) + gtid; i < a.n_slots; i += ALL) a.slots[i] = a.positions[i] = -1;
+    for (long long i = T::peek(&h->tokens) + gtid; i < a.n_slots; i += T::ALL) a.slots[i] = a.positions[i] = -1;
+    if constexpr (CTAS == 1) {
+        __syncthreads();
+        for (int p = tid; p < t.n_pages; p += THREADS) t.refs[p] = refs[p];
+    }
 }
 
 struct CompactLaunch {
@@ -317,94 +388,103 @@ struct CompactLaunch {
     void *ws;
 };
 
-__global__ void __cluster_dims__(CTAS, 1, 1) __launch_bounds__(THREADS) page_compact_kernel(const CompactLaunch a) {
-    __shared__ long long tmp[32];
+template <int CTAS>
+__global__ void __launch_bounds__(THREADS) page_compact_kernel(const CompactLaunch a) {
+    using T = Team<CTAS>;
+    extern __shared__ int counts[];
+    __shared__ Header local;
     const TableArgs &t = a.t;
-    const int rank = (int)cluster_rank(), tid = threadIdx.x, gtid = rank * THREADS + tid;
+    const int rank = T::rank(), tid = threadIdx.x, gtid = rank * THREADS + tid, lane = tid & 31, warp = gtid >> 5;
     const Ws ws = carve(a.ws, t.n_rows, t.n_pages);
+    int *refs = CTAS == 1 ? counts : t.refs;
+    Header *h = CTAS == 1 ? &local : ws.h;
+    for (int p = gtid; CTAS == 1 && p < t.n_pages; p += T::ALL) refs[p] = 0;
     wait_for_previous_grid();
     allow_dependent_launch();
-    for (int p = gtid; p < t.n_pages; p += ALL) t.refs[p] = 0;
-    cluster_sync();
-    gather_and_count<false>(t, rank);
-    cluster_sync();
+    for (int p = gtid; CTAS > 1 && p < t.n_pages; p += T::ALL) refs[p] = 0;
+    T::sync();
+    gather_and_count<CTAS, false>(t, refs, nullptr, warp);
+    T::sync();
 
     // L, the number of held pages.
-    const int per = (t.n_pages + CTAS - 1) / CTAS;
-    const int p0 = min(rank * per, t.n_pages), p1 = min(p0 + per, t.n_pages);
-    long long mine = 0, total;
-    for (int p = p0 + tid; p < p1; p += THREADS) mine += __ldcg(t.refs + p) > 0;
-    block_scan(mine, total, tmp);
-    if (tid == 0) ws.h->part[rank][0] = total;
-    cluster_sync();
-    int live = 0, live_before = 0;
-    for (int c = 0; c < CTAS; ++c) {
-        const int v = (int)__ldcg(&ws.h->part[c][0]);
-        live += v;
-        if (c < rank) live_before += v;
-    }
+    int p0, p1;
+    T::slice(warp, t.n_pages, p0, p1);
+    int n_mine = 0;
+    for (int p = p0 + lane; p - lane < p1; p += 32)
+        n_mine += __popc(__ballot_sync(0xffffffffu, p < p1 && T::peek(refs + p) > 0));
+    if (lane == 0) h->count[warp] = n_mine;
+    T::sync();
+    int before, live;
+    T::totals(h->count, warp, before, live);
 
     // Rank of each free page below L among the free, and of each held page at
     // or above L among the held: with b held pages before p, a hole p < L has
-    // rank p - b, a mover p >= L has rank b - (held pages below L).  The last
-    // is L less the number of holes, so a mover's rank from the end is
-    // (held pages from p on), and it needs no second count: movers are ranked
-    // from the last one, and the number of holes is known after this pass.
-    for (int base = p0; base < p1; base += THREADS) {
-        const int p = base + tid;
-        const int held = p < p1 && __ldcg(t.refs + p) > 0;
-        const int before = live_before + (int)block_scan(held, total, tmp);
+    // rank p - b, and a mover p >= L has L - 1 - b held pages after it, its
+    // rank from the end.  So one pass ranks both, and the movers are listed
+    // from the last one; there are as many of them as holes, L less the held
+    // pages before L.
+    for (int p = p0 + lane; p - lane < p1; p += 32) {
+        const bool held = p < p1 && T::peek(refs + p) > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, held);
+        const int b = before + __popc(m & ((1u << lane) - 1));
         if (p < p1) {
-            if (p < live && !held) ws.list[p - before] = p;
-            if (p >= live && held) ws.moved[live - 1 - before] = p;  // the last mover is entry 0
+            if (p < live && !held) ws.list[p - b] = p;
+            if (p >= live && held) ws.moved[live - 1 - b] = p;
             a.page_map[p] = held && p < live ? p : -1;
-            if (p == live) ws.h->n_free_or_live = p - before;  // holes below L = movers
-            if (p + 1 == t.n_pages && live == t.n_pages) ws.h->n_free_or_live = 0;
+            if (p == live) h->n_live = p - b;
+            if (p + 1 == t.n_pages && live == t.n_pages) h->n_live = 0;
         }
-        live_before += (int)total;
+        before += __popc(m);
     }
-    cluster_sync();
+    T::sync();
 
-    const int moves = (int)__ldcg(&ws.h->n_free_or_live);
-    for (int i = gtid; i < moves; i += ALL) {
-        const int to = __ldcg(ws.list + i), from = __ldcg(ws.moved + (moves - 1 - i));
+    const int moves = T::peek(&h->n_live);
+    for (int i = gtid; i < moves; i += T::ALL) {
+        const int to = T::peek(ws.list + i), from = T::peek(ws.moved + (moves - 1 - i));
         a.page_map[from] = to;
         ws.copies[i] = Copy{from, to, t.page_size};
-        t.refs[to] = __ldcg(t.refs + from);
-        t.refs[from] = 0;
+        refs[to] = T::peek(refs + from);
+        refs[from] = 0;
     }
     if (gtid == 0) {
         ws.h->n_copies = moves;
         *a.n_live = live;
     }
-    cluster_sync();
+    T::sync();
 
-    const int lane = tid & 31;
     const int segs = (t.max_pages + SEG - 1) / SEG;
     const long long items = (long long)t.n_rows * segs;
-    for (long long it = gtid >> 5; it < items; it += ALL / 32) {
-        const int r = (int)(it / segs), j0 = (int)(it % segs) * SEG;
+    for (long long it = warp; it < items; it += T::WARPS) {
+        const int r = (int)(segs == 1 ? it : it / segs), j0 = segs == 1 ? 0 : (int)(it % segs) * SEG;
         int from;
         const int had = pages_of(row_keep(t, r, from), t.page_size);
+        int e[SEG / 32];
 #pragma unroll
         for (int i = 0; i < SEG / 32; ++i) {
             const int j = j0 + i * 32 + lane;
-            if (j >= t.max_pages) continue;
-            int e = j < had ? t.table[(size_t)r * t.max_pages + j] : -1;
-            if (e >= t.n_pages) e = -1;
-            t.table_out[(size_t)r * t.max_pages + j] = e < 0 ? -1 : __ldcg(a.page_map + e);
+            e[i] = j < min(had, t.max_pages) ? t.table[(size_t)r * t.max_pages + j] : -1;
+        }
+#pragma unroll
+        for (int i = 0; i < SEG / 32; ++i) {
+            const int j = j0 + i * 32 + lane;
+            if (j < t.max_pages)
+                t.table_out[(size_t)r * t.max_pages + j] = e[i] < 0 || e[i] >= t.n_pages ? -1 : T::peek(a.page_map + e[i]);
         }
     }
+    if constexpr (CTAS == 1)
+        for (int p = tid; p < t.n_pages; p += THREADS) t.refs[p] = refs[p];
 }
 
-// The listed copies, all layers, codes and scales.  A block takes one piece
-// of PIECE bytes of one layer's copy at a time, in the order codes of K, codes
-// of V, scales of K, scales of V.
+// The listed copies, all layers, codes and scales: bound by reading and writing
+// them.  A block takes a run of cells of one layer's copy, of K or of V, at a
+// time: up to PIECE bytes of codes in 16-byte words, four per thread in flight,
+// and the same cells' scales in 8-byte words.
 constexpr int COPY_THREADS = 256;
-constexpr int PIECE = COPY_THREADS * 2 * 16;
+constexpr int PIECE = COPY_THREADS * 4 * 16;
 
 struct CopyLaunch {
     int n_layers, n_pages, page_size, code_row, scale_row, n_copies_max;  // bytes per cell
+    int piece_cells, pieces;                                            // cells of a piece, pieces of a page
     uint8_t *kq, *vq, *ksc, *vsc;
     void *ws;
     int n_rows;
@@ -414,52 +494,76 @@ __global__ void __launch_bounds__(COPY_THREADS) page_copy_kernel(const CopyLaunc
     wait_for_previous_grid();
     allow_dependent_launch();
     const Ws ws = carve(a.ws, a.n_rows, a.n_pages);
-    const int n = min(__ldcg(&ws.h->n_copies), a.n_copies_max);
+    const int n = min(__ldcg(&ws.h->n_copies), a.n_copies_max), tid = threadIdx.x;
     const size_t code_page = (size_t)a.page_size * a.code_row, scale_page = (size_t)a.page_size * a.scale_row;
-    const int code_pieces = (int)((code_page + PIECE - 1) / PIECE), scale_pieces = (int)((scale_page + PIECE - 1) / PIECE);
-    const int pieces = 2 * (code_pieces + scale_pieces);
-    const long long items = (long long)n * a.n_layers * pieces;
+    const int per_copy = 2 * a.pieces * a.n_layers;
+    const long long items = (long long)n * per_copy;
     for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int piece = (int)(it % pieces);
-        const long long cl = it / pieces;
-        const int layer = (int)(cl % a.n_layers);
-        const Copy c = ws.copies[cl / a.n_layers];
-        if (!QSA_IN(c.src, a.n_pages) || !QSA_IN(c.dst, a.n_pages) || !QSA_IN(c.cells, a.page_size + 1)) continue;
-        const bool code = piece < 2 * code_pieces;
-        const int local = code ? piece : piece - 2 * code_pieces, each = code ? code_pieces : scale_pieces;
-        const bool is_v = local >= each;
-        const size_t start = (size_t)(local - (is_v ? each : 0)) * PIECE;
-        const size_t page = code ? code_page : scale_page;
-        const size_t bytes = (size_t)c.cells * (code ? a.code_row : a.scale_row);
-        if (start >= bytes) continue;
-        uint8_t *base = (code ? (is_v ? a.vq : a.kq) : (is_v ? a.vsc : a.ksc)) + (size_t)layer * a.n_pages * page;
-        const uint8_t *src = base + (size_t)c.src * page + start;
-        uint8_t *dst = base + (size_t)c.dst * page + start;
-        const int len = (int)(bytes - start < PIECE ? bytes - start : PIECE);
-        uint4 v[PIECE / (COPY_THREADS * 16)];
+        const Copy c = ws.copies[it / per_copy];
+        const int in = (int)(it % per_copy), layer = in / (2 * a.pieces), part = in % (2 * a.pieces);
+        const bool is_v = part >= a.pieces;
+        const int c0 = (part - (is_v ? a.pieces : 0)) * a.piece_cells, cells = min(c.cells - c0, a.piece_cells);
+        if (cells <= 0 || !QSA_IN(c.src, a.n_pages) || !QSA_IN(c.dst, a.n_pages) || !QSA_IN(c.cells, a.page_size + 1)) continue;
+        const size_t from = (size_t)layer * a.n_pages + c.src, to = (size_t)layer * a.n_pages + c.dst;
+        uint8_t *codes = (is_v ? a.vq : a.kq) + (size_t)c0 * a.code_row, *scales = (is_v ? a.vsc : a.ksc) + (size_t)c0 * a.scale_row;
+        const uint4 *src = reinterpret_cast<const uint4 *>(codes + from * code_page);
+        uint4 *dst = reinterpret_cast<uint4 *>(codes + to * code_page);
+        const int n16 = cells * (a.code_row / 16), n8 = cells * (a.scale_row / 8);
+        const uint2 *ssrc = reinterpret_cast<const uint2 *>(scales + from * scale_page);
+        uint2 *sdst = reinterpret_cast<uint2 *>(scales + to * scale_page);
+        uint2 s = make_uint2(0u, 0u);
+        if (tid < n8) s = ssrc[tid];
+        for (int i = tid; i < n16; i += COPY_THREADS * 4) {
+            uint4 v[4];
 #pragma unroll
-        for (int k = 0; k < PIECE / (COPY_THREADS * 16); ++k) {
-            const int at = (k * COPY_THREADS + (int)threadIdx.x) * 16;
-            if (at + 16 <= len) v[k] = *reinterpret_cast<const uint4 *>(src + at);
-        }
+            for (int k = 0; k < 4; ++k)
+                if (i + k * COPY_THREADS < n16) v[k] = src[i + k * COPY_THREADS];
 #pragma unroll
-        for (int k = 0; k < PIECE / (COPY_THREADS * 16); ++k) {
-            const int at = (k * COPY_THREADS + (int)threadIdx.x) * 16;
-            if (at + 16 <= len) *reinterpret_cast<uint4 *>(dst + at) = v[k];
+            for (int k = 0; k < 4; ++k)
+                if (i + k * COPY_THREADS < n16) dst[i + k * COPY_THREADS] = v[k];
         }
-        // An odd number of cells of one KV head leaves eight bytes of scales.
-        if ((len & 15) && threadIdx.x == 0)
-            *reinterpret_cast<uint2 *>(dst + (len & ~15)) = *reinterpret_cast<const uint2 *>(src + (len & ~15));
+        if (tid < n8) sdst[tid] = s;
+        for (int i = tid + COPY_THREADS; i < n8; i += COPY_THREADS) sdst[i] = ssrc[i];
     }
 }
 
 template <class A>
-cudaError_t launch_copies(const A &a, cudaStream_t s) {
-    const CopyLaunch c{a.n_layers, a.n_pages, a.page_size, a.n_kv_heads * a.head_dim, a.n_kv_heads * 8,
-                       a.n_rows > a.n_pages ? a.n_rows : a.n_pages,
+cudaError_t launch_copies(const A &a, int n_copies_max, cudaStream_t s) {
+    const int code_row = a.n_kv_heads * a.head_dim;
+    int piece_cells = PIECE / code_row;
+    piece_cells = piece_cells < 1 ? 1 : piece_cells > a.page_size ? a.page_size : piece_cells;
+    const int pieces = (a.page_size + piece_cells - 1) / piece_cells;
+    const CopyLaunch c{a.n_layers, a.n_pages, a.page_size, code_row, a.n_kv_heads * 8, n_copies_max, piece_cells, pieces,
                        reinterpret_cast<uint8_t *>(a.kq), reinterpret_cast<uint8_t *>(a.vq),
                        reinterpret_cast<uint8_t *>(a.ksc), reinterpret_cast<uint8_t *>(a.vsc), a.workspace, a.n_rows};
-    return launch_dependent(page_copy_kernel, dim3(152 * 8), dim3(COPY_THREADS), 0, s, c);
+    const long long items = (long long)n_copies_max * 2 * pieces * a.n_layers;
+    const int blocks = (int)(items < 152 * 8 ? (items < 1 ? 1 : items) : 152 * 8);
+    return launch_dependent(page_copy_kernel, dim3(blocks), dim3(COPY_THREADS), 0, s, c);
+}
+
+// The table's launch: one block, or one cluster of eight.
+template <class L>
+cudaError_t launch_team(void (*one)(L), void (*cluster)(L), const L &l, cudaStream_t s) {
+    const bool small = l.t.n_pages <= SMALL_PAGES && (long long)l.t.n_rows * l.t.max_pages <= SMALL_ENTRIES;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(small ? 1 : CLUSTER);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = small ? (size_t)l.t.n_pages * sizeof(int) : 0;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CLUSTER;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = small ? 1 : 2;
+    if (cfg.dynamicSmemBytes > 40 * 1024) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, SMALL_PAGES * (int)sizeof(int));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaLaunchKernelEx(&cfg, small ? one : cluster, l);
 }
 
 }  // namespace
@@ -470,16 +574,16 @@ cudaError_t launch_page_update(const qsa_page_update_args &a, cudaStream_t s) {
     const UpdateLaunch u{{a.n_rows_in, a.n_rows, a.max_pages, a.n_pages, a.page_size, a.page_table, a.seq_lens, a.src,
                           a.page_table_out, a.refs, a.err},
                          a.n_new, a.seq_lens_out, a.slots, a.positions, a.n_slots, a.workspace};
-    const cudaError_t e = launch_dependent(page_update_kernel, dim3(CTAS), dim3(THREADS), 0, s, u);
-    return e != cudaSuccess ? e : launch_copies(a, s);
+    const cudaError_t e = launch_team(page_update_kernel<1>, page_update_kernel<CLUSTER>, u, s);
+    return e != cudaSuccess ? e : launch_copies(a, a.n_rows, s);  // a row copies at most one page
 }
 
 cudaError_t launch_page_compact(const qsa_page_compact_args &a, cudaStream_t s) {
     const CompactLaunch c{{a.n_rows, a.n_rows, a.max_pages, a.n_pages, a.page_size, a.page_table, a.seq_lens, nullptr,
                            a.page_table_out, a.refs, a.err},
                           a.page_map, a.n_live, a.workspace};
-    const cudaError_t e = launch_dependent(page_compact_kernel, dim3(CTAS), dim3(THREADS), 0, s, c);
-    return e != cudaSuccess ? e : launch_copies(a, s);
+    const cudaError_t e = launch_team(page_compact_kernel<1>, page_compact_kernel<CLUSTER>, c, s);
+    return e != cudaSuccess ? e : launch_copies(a, a.n_pages / 2, s);  // as many movers as holes
 }
 
 }  // namespace qsa

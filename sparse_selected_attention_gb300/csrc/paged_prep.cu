@@ -112,7 +112,7 @@ struct PrepPlan {
 };
 
 template <int D, bool INTER, class TI, class TO>
-__global__ void __launch_bounds__(PREP_WARPS * 32) paged_prep_kernel(const qsa_paged_prep_args a, const PrepPlan plan) {
+__global__ void __launch_bounds__(PREP_WARPS * 32, 7) paged_prep_kernel(const qsa_paged_prep_args a, const PrepPlan plan) {
     constexpr int N = D / 32;  // elements per lane
     wait_for_previous_grid();
     allow_dependent_launch();

@@ -17,8 +17,9 @@ from . import _abi
 
 F32, F16, BF16, I32, I8 = torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int8
 _CODE = {F32: _abi.QSA_F32, F16: _abi.QSA_F16, BF16: _abi.QSA_BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+# The raw handle of the current stream and the current device's number: what
+# torch.cuda.current_stream() and current_device() wrap, without their objects.
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _formats():
@@ -88,7 +89,7 @@ def _call(name, packed, dev, stream):
     else:
         raw = stream.cuda_stream
     fn = _abi.packed(name)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = fn(packed, raw)
     else:
         with torch.cuda.device(dev):

@@ -419,7 +419,7 @@ typedef struct {
  * lengths.  Range: scores and sums are fp32; K scales of any fp16 value, V
  * scales below 2^15.
  * Supported: n_q_heads a multiple of n_kv_heads, 1..16 query heads per KV
- * head.  q, out, kq, vq 16-byte aligned; ksc, vsc 8-byte; the rest 4-byte.
+ * head.  q, out, kq, vq 16-byte aligned; ksc, vsc, gate 8-byte; the rest 4-byte.
  */
 typedef struct {
     int n_tokens, n_q_heads, n_kv_heads, head_dim, group, page_size, n_pages, n_rows, max_pages;

@@ -414,7 +414,7 @@ qsa_status qsa_paged_attn(const qsa_paged_attn_args *a, void *stream) {
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: workspace smaller than qsa_paged_attn_workspace_bytes()");
     if (!aligned(a->q, 16) || !aligned(a->kq, 16) || !aligned(a->vq, 16) || !aligned(a->ksc, 8) ||
         !aligned(a->vsc, 8) || !aligned(a->page_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->rows, 4) ||
-        !aligned(a->gate, 4) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->workspace, 256) ||
+        !aligned(a->gate, 8) || !aligned(a->out, 16) || !aligned(a->lse, 4) || !aligned(a->workspace, 256) ||
         !aligned(a->err, 4))
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: misaligned buffer");
     cudaError_t e = qsa::launch_paged_attn(*a, static_cast<cudaStream_t>(stream));

@@ -6,24 +6,28 @@
 // reading the cache: 2 D + 16 bytes per (cell, KV head) against 4 D flops per
 // query head, 23 flops per byte at 12 heads.
 //
-// Work.  A row's cells are taken in units of 32.  The units of all rows are
-// cut into equal shares, one per CTA of each KV head, so one long row or a
-// ragged batch fills the chip alike and the share does not depend on the
-// table's width.  The KV heads of a share are neighbouring CTAs: they walk the
-// same cells together, so that a cell's scales, eight bytes per head, come
-// from DRAM once for all heads of a 32-byte sector.  A share that holds all of
-// a row writes its output; a row that spans CTAs leaves one partial per CTA in
-// the workspace (values, maximum, sum), and a second launch joins them.  Each
-// CTA finds its place by summing the rows' lengths itself, which costs one
-// pass over seq_lens and saves a launch.
+// Work.  A row's cells are taken in units (32 cells of 128 dims or 16 of 256:
+// 8 KB of codes).  The units of all rows are cut into equal shares, one per CTA
+// of each KV head, so one long row or a ragged batch fills the chip alike and
+// the share does not depend on the table's width.  The KV heads of a share are
+// neighbouring CTAs: they walk the same cells together, so that a cell's
+// scales, eight bytes per head, come from DRAM once for all heads of a 32-byte
+// sector.  A share that holds all of a row writes its output; a row that spans
+// CTAs leaves one partial per CTA in the workspace (values, maximum, sum), and
+// a second launch joins them.  Each CTA finds its place by summing the rows'
+// lengths itself, which costs one pass over seq_lens and saves a launch.
+// (Shares by warp instead of by CTA, without block barriers: 202 us for 61 rows
+// of up to 32 K cells where this takes 187, the partials being four times as
+// many.)
 //
 // A unit.  The query heads of one KV head are the M side (padded to 16) of
 // m16n8k16 products, cells are N of Q.K and the contraction of P.V.  (tcgen05
 // would want the codes as fp16 in shared memory, a round trip of four bytes
-// per code; here they go from shared memory to fragments.)  Each warp streams
-// its units through a ring of two stages, each filled by two TMA boxes of 32
-// rows x 128 bytes (four of 16 rows where a page has 16) and eight-byte
-// cp.async for the scales.  The boxes carry the 128-byte swizzle, and cells
+// per code; here they go from shared memory to fragments.)  The warps of a CTA
+// take a row's units in turn.  Each streams its units through a ring of two
+// stages, filled by TMA boxes of 32 or 16 rows x 128 bytes and eight-byte
+// cp.async for the scales; the next unit's copies are in flight while one is
+// computed, across rows too.  The boxes carry the 128-byte swizzle, and cells
 // and dims are assigned to lanes so that no fragment read meets a bank twice:
 //   lane (g, r) = (lane / 4, lane % 4) holds cells 4 r .. 4 r + 3 of each 16:
 //   column n of score tile j is cell 16 (j / 2) + 2 n + j % 2;
@@ -35,9 +39,6 @@
 // multiplies in fp32.  For V it is subtracted, and the scales go to the
 // weights, a set of fp16 weights per scale group, under a power of two per
 // warp that keeps small scales out of the subnormals.
-//
-// With head_dim 256 two warps share a unit, each with 128 dims of K and V;
-// their partial scores meet in shared memory.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,21 +53,26 @@
 namespace qsa {
 namespace {
 
-constexpr int DW = 128;   // dims a warp handles
-constexpr int UNIT = 32;  // cells of a warp step
-constexpr int NW = 4;     // warps per CTA
-constexpr int NS = 2;     // ring stages per warp
-constexpr int TILE = UNIT * DW;
+constexpr int NW = 4;           // warps per CTA
+constexpr int CTAS_PER_SM = 2;  // 255 registers a thread
+constexpr int MAX_CTAS = 152 * CTAS_PER_SM;
+constexpr int TILE = 4096;      // a unit's K or V codes
 constexpr float LN2 = 0.6931471805599453f;
 constexpr float LOG2E = 1.4426950408889634f;
-constexpr float SLACK = 8.0f;  // weights stay below 2^8 of the running maximum's
-constexpr int MAX_CTAS = 152 * 2;
+constexpr float SLACK = 8.0f;   // weights stay below 2^8 of the running maximum's
 
-// Fewest units of a share: finer ones would only add partials to join.
-constexpr int MIN_SHARE = 8;
+// Fewest units of a share, one per warp: finer ones would only add partials.
+constexpr int MIN_SHARE = NW;
 // Rows of up to this many units are not shared out.
-constexpr int WHOLE = 16;
-static_assert(NS == 2, "the ring alternates between two stages");
+constexpr int WHOLE = 4 * NW;
+
+// S = head_dim / 128.
+template <int S>
+struct Shape {
+    static constexpr int D = 128 * S, UNIT = 32 / S;  // cells of a unit
+    static constexpr int NJ = 4 / S, NK = 2 / S;      // score tiles of eight cells, halves of 16
+    static constexpr unsigned FULL = S == 1 ? 0xffffffffu : 0xffffu;
+};
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -86,9 +92,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// 16 x 16 bytes of V, cells as rows, from cells 0-15 and 16-31: register 0 (1)
-// holds cells 4 r .. 4 r + 3 of dim g (g + 8), registers 2 and 3 the same of
-// cells 16 on.
+// Two 16 x 16 byte matrices of V, cells as rows, from lanes 0-15's and lanes
+// 16-31's row addresses: registers 0 and 2 hold cells 4 r .. 4 r + 3 of dim g
+// of the first and the second, registers 1 and 3 those of dim g + 8.
 __device__ __forceinline__ void load_v(uint32_t (&w)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                  : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -121,20 +127,17 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool pr
 // Shared memory of a CTA.
 template <int S>
 struct Smem {
-    uint8_t tile[NW][NS][2][TILE];  // K, V; 1024-byte aligned
-    uint2 scale[NW][NS][2][UNIT];   // four fp16 per cell: ksc, vsc
-    uint4 q[S][8][32];              // Q fragments by k-step and lane
-    float bias[4][8][4];            // -1152 * sum of q over a scale group, as accumulators: heads g, g, g + 8, g + 8
-    float qinv[16];                 // 2^-e of a head's scaled query
-    union {
-        float o[NW / S][16][DW * S];   // the groups' values, at the end of a segment
-        float xch[NW][2][16 * 32];     // partial scores of a shared unit (head_dim 256), during one
-    };
-    float m[NW / S][16], l[NW / S][16], f[NW / S][16];
-    int v[NW / S];                  // the groups' V exponents
-    uint64_t bar[NW][NS];
+    uint8_t tile[NW][2][2][TILE];                  // stage, K or V: [S][UNIT][128] codes; 1024-byte aligned
+    uint2 scale[NW][2][2][Shape<S>::UNIT];         // four fp16 per cell
+    uint4 q[8 * S][32];                            // Q fragments by k-step and lane
+    float bias[4][8][4];                           // -1152 * sum of q over a scale group, as accumulators: heads g, g, g + 8, g + 8
+    float qinv[16];                                // 2^-e of a head's scaled query
+    float o[NW][16][128];                          // 128 dims of the warps' values, at the end of a segment
+    float m[NW][16], l[NW][16], f[NW][16];
+    int v[NW];                                     // the warps' V exponents
+    uint64_t bar[NW][2];
     long long scan[NW];
-    long long total, before;        // units of all rows; of the rows before `row`
+    long long total, before;                       // units of all rows; of the rows before `row`
     int row;
 };
 
@@ -171,7 +174,10 @@ __device__ __forceinline__ int row_len(const qsa_paged_attn_args &a, int t, int 
     bad |= len < 0 || len > most;
     return min(max(len, 0), most);
 }
-__device__ __forceinline__ int units_of(int len) { return max((len + UNIT - 1) / UNIT, 1); }
+template <int S>
+__device__ __forceinline__ int units_of(int len) {
+    return max((len + Shape<S>::UNIT - 1) / Shape<S>::UNIT, 1);
+}
 
 // Sums the rows' units and finds the row that holds unit share * range, of
 // `ranges` shares.
@@ -185,7 +191,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     long long mine = 0;
     for (int t = t0; t < t1; ++t) {
         int row;
-        mine += units_of(row_len(a, t, row, bad));
+        mine += units_of<S>(row_len(a, t, row, bad));
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     long long s = mine;
@@ -209,7 +215,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     if (x0 >= before && x0 < before + mine) {
         for (int t = t0;; ++t) {
             int row;
-            const int u = units_of(row_len(a, t, row, bad));
+            const int u = units_of<S>(row_len(a, t, row, bad));
             if (x0 < before + u) {
                 sh.row = t;
                 sh.before = before;
@@ -230,7 +236,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
 // segment's can be in flight while the one before ends.
 template <int S>
 struct Query {
-    static constexpr int D = DW * S, N = D / 32, H = 16 / NW;
+    static constexpr int D = Shape<S>::D, N = D / 32, H = 16 / NW;
     uint32_t raw[H][N / 2];
 
     __device__ __forceinline__ void load(const qsa_paged_attn_args &a, int t, int kvh, int per) {
@@ -285,9 +291,8 @@ struct Query {
                 *reinterpret_cast<float2 *>(&sh.bias[lane >> 3][h & 7][2 * (h >> 3)]) = make_float2(-1152.0f * sum, -1152.0f * sum);
 #pragma unroll
             for (int e = 0; e < N; e += 4) {
-                const int d = lane * N + e, half = d / DW, dl = d % DW;
-                const int ks = 2 * (dl >> 5) + ((dl >> 2) & 1), r = (dl >> 3) & 3;
-                uint32_t *dst = reinterpret_cast<uint32_t *>(&sh.q[half][ks][(h & 7) * 4 + r]) + (h >> 3);
+                const int d = lane * N + e, ks = 2 * (d >> 5) + ((d >> 2) & 1), r = (d >> 3) & 3;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(&sh.q[ks][(h & 7) * 4 + r]) + (h >> 3);
                 dst[0] = h2u(__halves2half2(v[e], v[e + 2]));
                 dst[2] = h2u(__halves2half2(v[e + 1], v[e + 3]));
             }
@@ -295,83 +300,71 @@ struct Query {
     }
 };
 
+template <int S>
 struct State {
-    float o[16][4];  // o[t][0..1]: head g, dims 8 t + 2 r, 8 t + 2 r + 1; o[t][2..3]: head g + 8
+    float o[16 * S][4];  // o[t][0..1]: head g, dims 8 t + 2 r, 8 t + 2 r + 1; o[t][2..3]: head g + 8
     float m[2], l[2];
     int v;  // values are in units of 2^v
 };
 
 // Folds one staged unit into the state.  vmask: the unit's valid cells.
 template <int S>
-__device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vmask, State &st, const float (&sl2)[2],
-                                             int half, int parity) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, r = lane & 3;
-    constexpr int NG = 4 / S;  // scale groups of this warp's dims
+__device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const uint2 *KS, const uint2 *VS, const uint4 (*q)[32],
+                                             const float (*bias)[8][4], unsigned vmask, State<S> &st, const float (&sl2)[2]) {
+    constexpr int NJ = Shape<S>::NJ, NK = Shape<S>::NK, UNIT = Shape<S>::UNIT;
+    const int lane = threadIdx.x & 31, g = lane >> 2, r = lane & 3;
     // Row 2 g of K with the swizzle of its first 16 bytes for this lane, and row 2 g + 1.
-    const uint32_t kt = tc::smem_u32(sh.tile[warp][stage][0]) + 2 * g * DW + ((r & 1) << 3);
-    const uint32_t keven = kt + (((r >> 1) ^ ((2 * g) & 7)) << 4), kodd = kt + DW + (((r >> 1) ^ ((2 * g + 1) & 7)) << 4);
+    const uint32_t kt = tc::smem_u32(K) + 2 * g * 128 + ((r & 1) << 3);
+    const uint32_t keven = kt + (((r >> 1) ^ ((2 * g) & 7)) << 4), kodd = kt + 128 + (((r >> 1) ^ ((2 * g + 1) & 7)) << 4);
 
     // Scores: per scale group S 32-dim blocks of two k-steps from -1152 sum q,
     // then the scale.
-    float2 s[4][2];
+    float2 s[NJ][2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = make_float2(0.0f, 0.0f);
-    uint4 ks[2][2];  // scales of cells 16 kk + 4 r .. + 3
+    for (int j = 0; j < NJ; ++j) s[j][0] = s[j][1] = make_float2(0.0f, 0.0f);
+    uint4 ks[NK][2];  // scales of cells 16 kk + 4 r .. + 3
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+    for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            ks[kk][i] = *reinterpret_cast<const uint4 *>(&sh.scale[warp][stage][0][16 * kk + 4 * r + 2 * i]);
+        for (int i = 0; i < 2; ++i) ks[kk][i] = *reinterpret_cast<const uint4 *>(KS + 16 * kk + 4 * r + 2 * i);
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-        const float4 bias = *reinterpret_cast<const float4 *>(sh.bias[(S == 2 ? 2 * half : 0) + gr][g]);
-        float acc[4][4];
+    for (int gr = 0; gr < 4; ++gr) {
+        const float4 c0 = *reinterpret_cast<const float4 *>(bias[gr][g]);
+        float acc[NJ][4];
 #pragma unroll
         for (int bb = 0; bb < S; ++bb) {
-            const int b = gr * S + bb;
-            const uint4 q0 = sh.q[S == 2 ? half : 0][2 * b][lane], q1 = sh.q[S == 2 ? half : 0][2 * b + 1][lane];
+            const int b = gr * S + bb, half = b >> 2, bh = b & 3;  // of all dims; of the 128 of a tile half
+            const uint4 q0 = q[2 * b][lane], q1 = q[2 * b + 1][lane];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < NJ; ++j) {
                 uint32_t w0, w1;
                 asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
                              : "=r"(w0), "=r"(w1)
-                             : "r"((((j & 1) ? kodd : keven) ^ (b << 5)) + (j >> 1) * 16 * DW)
+                             : "r"((((j & 1) ? kodd : keven) ^ (bh << 5)) + (j >> 1) * 16 * 128 + half * UNIT * 128)
                              : "memory");
                 if (bb == 0)
-                    mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), bias.x, bias.y, bias.z, bias.w);
+                    mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), c0.x, c0.y, c0.z, c0.w);
                 else
                     mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
                 mma16816(acc[j], q1, even_codes(w1), odd_codes(w1), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < NJ; ++j) {
             // Cells 4 r + j % 2 and two on: the first or second half of each 16 bytes.
             const uint4 &lo = ks[j >> 1][0], &hi = ks[j >> 1][1];
-            const int word = S == 2 ? half : gr >> 1;
-            const uint32_t w0 = (j & 1) ? (word ? lo.w : lo.z) : (word ? lo.y : lo.x);
-            const uint32_t w1 = (j & 1) ? (word ? hi.w : hi.z) : (word ? hi.y : hi.x);
+            const uint32_t w0 = (j & 1) ? (gr >> 1 ? lo.w : lo.z) : (gr >> 1 ? lo.y : lo.x);
+            const uint32_t w1 = (j & 1) ? (gr >> 1 ? hi.w : hi.z) : (gr >> 1 ? hi.y : hi.x);
             const float2 f = (gr & 1) ? make_float2(__high2float(u2h(w0)), __high2float(u2h(w1)))
                                       : make_float2(__low2float(u2h(w0)), __low2float(u2h(w1)));
             s[j][0] = __ffma2_rn(make_float2(acc[j][0], acc[j][1]), f, s[j][0]);
             s[j][1] = __ffma2_rn(make_float2(acc[j][2], acc[j][3]), f, s[j][1]);
         }
     }
-    if constexpr (S == 2) {
-        // The partner's half of the contraction.  Two slots by parity: a slot
-        // is written again only after the partner has passed the next barrier.
-        float2 *mine = reinterpret_cast<float2 *>(sh.xch[warp][parity]) + lane;
-        const float2 *other = reinterpret_cast<const float2 *>(sh.xch[warp ^ 1][parity]) + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mine[i * 32] = s[i >> 1][i & 1];
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i >> 1][i & 1] = __fadd2_rn(s[i >> 1][i & 1], other[i * 32]);
-    }
-    if (vmask != 0xffffffffu) {
+    if (vmask != Shape<S>::FULL) {
         const unsigned mine = vmask >> (4 * r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < NJ; ++j) {
             const int c = 16 * (j >> 1) + (j & 1);
             if (!((mine >> c) & 1u)) s[j][0].x = s[j][1].x = -CUDART_INF_F;
             if (!((mine >> (c + 2)) & 1u)) s[j][0].y = s[j][1].y = -CUDART_INF_F;
@@ -380,18 +373,21 @@ __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vm
 
     // The reference maximum moves only when a unit exceeds it by 2^SLACK, so
     // the values are rarely rescaled.
-    float mx[2];
+    float mx[2], al[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        mx[e] = max3(max3(s[0][e].x, s[0][e].y, s[1][e].x), s[1][e].y, s[2][e].x);
-        mx[e] = fmaxf(max3(mx[e], s[2][e].y, s[3][e].x), s[3][e].y);
+        mx[e] = max3(s[0][e].x, s[0][e].y, s[1][e].x);
+        mx[e] = fmaxf(mx[e], s[1][e].y);
+        if constexpr (NJ == 4) {
+            mx[e] = max3(mx[e], s[2][e].x, s[2][e].y);
+            mx[e] = max3(mx[e], s[3][e].x, s[3][e].y);
+        }
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
         mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
     }
-    float al[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         mx[e] *= sl2[e];
@@ -401,13 +397,13 @@ __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vm
     }
     // Weights: in fp32 for the sum, rounded to fp16 for the products (each by
     // at most 2^-11 of itself).  pa[kk] is the A fragment of cells 16 kk on.
-    uint32_t pa[2][4];
+    uint32_t pa[NK][4];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const float2 f = make_float2(sl2[e], sl2[e]), m = make_float2(-st.m[e], -st.m[e]);
         float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < NJ; ++j) {
             float2 p = __ffma2_rn(s[j][e], f, m);
             p = make_float2(ex2(p.x), ex2(p.y));
             sum = __fadd2_rn(sum, p);
@@ -419,7 +415,7 @@ __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vm
     // The values' power of two: the largest V scale of the first unit, raised
     // when a later scale reaches 2^6 of it, so that weight (below 2^8) times
     // scale stays in the fp16 range.
-    const uint2 own = sh.scale[warp][stage][1][lane];
+    const uint2 own = VS[lane % UNIT];
     uint32_t top = __vmaxu2(own.x & 0x7FFF7FFFu, own.y & 0x7FFF7FFFu);
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     const int ve = min(max((int)(top >> 10) - 15, -14), 15);
@@ -431,7 +427,7 @@ __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vm
     }
     if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 16 * S; ++i) {
             st.o[i][0] *= al[0];
             st.o[i][1] *= al[0];
             st.o[i][2] *= al[1];
@@ -440,55 +436,60 @@ __device__ __forceinline__ void compute_unit(Smem<S> &sh, int stage, unsigned vm
     }
     const __half2 vf = __float2half2_rn(exp2i(-max(st.v, -14)));
 
-    // Row `lane` of V, swizzled: chunk c is at vrow ^ 16 c.
-    const uint32_t vrow = tc::smem_u32(sh.tile[warp][stage][1]) + lane * DW + ((lane & 7) << 4);
-    uint4 vs[2][2];
+    // This lane's row address of V's matrices: 128 dims, cells 0-31 by lane; or
+    // cells 0-15 by lane % 16, lanes 16-31 sixteen dims on.
+    const uint32_t vrow = S == 1 ? V + lane * 128 + ((lane & 7) << 4) : V + (lane & 15) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
+    uint4 vs[NK][2];
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+    for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            vs[kk][i] = *reinterpret_cast<const uint4 *>(&sh.scale[warp][stage][1][16 * kk + 4 * r + 2 * i]);
+        for (int i = 0; i < 2; ++i) vs[kk][i] = *reinterpret_cast<const uint4 *>(VS + 16 * kk + 4 * r + 2 * i);
     const __half2 off = u2h(0x64806480u);  // 1152
     auto even = [&](uint32_t w) { return h2u(__hsub2(u2h(even_codes(w)), off)); };
     auto odd = [&](uint32_t w) { return h2u(__hsub2(u2h(odd_codes(w)), off)); };
+    auto pv = [&](float (&o)[4], const uint4 &p, uint32_t w) { mma16816(o, p, even(w), odd(w), o[0], o[1], o[2], o[3]); };
 #pragma unroll
-    for (int gr = 0; gr < NG; ++gr) {
-        uint4 a[2];
+    for (int gr = 0; gr < 4; ++gr) {
+        uint4 p[NK];
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
+        for (int kk = 0; kk < NK; ++kk) {
             const uint4 &lo = vs[kk][0], &hi = vs[kk][1];
-            const int word = S == 2 ? half : gr >> 1;
             const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
-            const __half2 f02 = __hmul2(u2h(word ? tc::prmt(lo.y, hi.y, sel) : tc::prmt(lo.x, hi.x, sel)), vf);
-            const __half2 f13 = __hmul2(u2h(word ? tc::prmt(lo.w, hi.w, sel) : tc::prmt(lo.z, hi.z, sel)), vf);
-            a[kk] = make_uint4(h2u(__hmul2(u2h(pa[kk][0]), f02)), h2u(__hmul2(u2h(pa[kk][1]), f02)),
+            const __half2 f02 = __hmul2(u2h(gr >> 1 ? tc::prmt(lo.y, hi.y, sel) : tc::prmt(lo.x, hi.x, sel)), vf);
+            const __half2 f13 = __hmul2(u2h(gr >> 1 ? tc::prmt(lo.w, hi.w, sel) : tc::prmt(lo.z, hi.z, sel)), vf);
+            p[kk] = make_uint4(h2u(__hmul2(u2h(pa[kk][0]), f02)), h2u(__hmul2(u2h(pa[kk][1]), f02)),
                                h2u(__hmul2(u2h(pa[kk][2]), f13)), h2u(__hmul2(u2h(pa[kk][3]), f13)));
         }
 #pragma unroll
-        for (int c = gr * 2 * S; c < (gr + 1) * 2 * S; ++c) {
+        for (int i = 0; i < 2; ++i) {
             uint32_t w[4];
-            load_v(w, vrow ^ (c << 4));
-            float(*o)[4] = st.o + 2 * c;
-            mma16816(o[0], a[0], even(w[0]), odd(w[0]), o[0][0], o[0][1], o[0][2], o[0][3]);
-            mma16816(o[1], a[0], even(w[1]), odd(w[1]), o[1][0], o[1][1], o[1][2], o[1][3]);
-            mma16816(o[0], a[1], even(w[2]), odd(w[2]), o[0][0], o[0][1], o[0][2], o[0][3]);
-            mma16816(o[1], a[1], even(w[3]), odd(w[3]), o[1][0], o[1][1], o[1][2], o[1][3]);
+            if constexpr (S == 1) {  // 16 dims of both halves of the cells
+                const int c = 2 * gr + i;
+                load_v(w, vrow ^ (c << 4));
+                pv(st.o[2 * c], p[0], w[0]);
+                pv(st.o[2 * c + 1], p[0], w[1]);
+                pv(st.o[2 * c], p[NK - 1], w[2]);
+                pv(st.o[2 * c + 1], p[NK - 1], w[3]);
+            } else {  // 32 dims
+                const int c = 2 * (gr & 1) + i, t = 16 * (gr >> 1) + 4 * c;
+                load_v(w, (vrow ^ (c << 5)) + (gr >> 1) * UNIT * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) pv(st.o[t + k], p[0], w[k]);
+            }
         }
     }
 }
 
-__device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i, float x, float y) {
-    if (a.gate) {
-        x = x / (1.0f + expf(-__ldg(a.gate + i)));
-        y = y / (1.0f + expf(-__ldg(a.gate + i + 1)));
-    }
+__device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i, float2 y) {
     if (a.dtype == QSA_F16)
-        *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(x, y);
+        *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(y.x, y.y);
     else
-        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(x, y);
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(y.x, y.y);
 }
+// y / (1 + exp(-gate)); each step off by a few 2^-23, and a gate far below 0 gives 0.
+__device__ __forceinline__ float gated(float y, float gate) { return __fdividef(y, 1.0f + ex2(-gate * LOG2E)); }
 
-// The units of a warp group in order, across rows: unit u of row t is the next
+// The units of a warp in order, across rows: unit u of row t is the next
 // one whose copies start.  The row after, and the page of the next unit, are
 // loaded a step before they are needed.
 struct Feed {
@@ -499,17 +500,17 @@ struct Feed {
 };
 
 template <int S>
-__global__ void __launch_bounds__(NW * 32, 2)
+__global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     paged_attn_kernel(const qsa_paged_attn_args a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, int whole_rows) {
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<S> &sh = *reinterpret_cast<Smem<S> *>(raw);
-    constexpr int D = DW * S, NP = NW / S;
+    constexpr int D = Shape<S>::D, UNIT = Shape<S>::UNIT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, r = lane & 3;
-    const int pw = warp / S, half = warp % S;
     const int per = a.n_q_heads / a.n_kv_heads, page_shift = 31 - __clz(a.page_size);
     if (lane == 0) {
-        for (int i = 0; i < NS; ++i) tc::mbar_init(tc::smem_u32(&sh.bar[warp][i]), 1);
+        tc::mbar_init(tc::smem_u32(&sh.bar[warp][0]), 1);
+        tc::mbar_init(tc::smem_u32(&sh.bar[warp][1]), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     wait_for_previous_grid();
@@ -537,68 +538,79 @@ __global__ void __launch_bounds__(NW * 32, 2)
     Feed f;
     f.t = t;
     f.len = row_len(a, t, f.trow, bad);
-    int nu = units_of(f.len);
+    int nu = units_of<S>(f.len);
     f.end = min(nu, u0 + left);
     f.left = left - (f.end - u0);
-    f.u = u0 + pw;
+    f.u = u0 + warp;
     f.next_len = f.next_trow = 0;
     auto peek = [&] {
         if (f.left > 0 && f.t + step < a.n_tokens) f.next_len = row_len(a, f.t + step, f.next_trow, bad);
     };
-    // Moves on to the next row that has a unit for this group.
+    // Moves on to the next row that has a unit for this warp.
     auto settle = [&] {
         while (f.u >= f.end && f.left > 0 && f.t + step < a.n_tokens) {
             f.t += step;
             f.len = f.next_len;
             f.trow = f.next_trow;
-            f.end = min(units_of(f.len), f.left);
+            f.end = min(units_of<S>(f.len), f.left);
             f.left -= f.end;
-            f.u = pw;
+            f.u = warp;
             peek();
         }
-        const int j = (f.u * UNIT + lane) >> page_shift;
+        const int j = (f.u * UNIT + lane % UNIT) >> page_shift;
         f.page = f.u < f.end && j < a.max_pages ? __ldg(a.page_table + (size_t)f.trow * a.max_pages + j) : -1;
     };
     // Starts the copies of unit f.u into a stage and moves on; returns the
     // unit's valid cells (none past the last unit).
     auto issue = [&](int stage) -> unsigned {
-        const int c = f.u * UNIT + lane;
+        const int c = f.u * UNIT + lane % UNIT;
         const bool in = f.u < f.end && c < f.len;
         const bool ok = in && f.page >= 0 && f.page < a.n_pages;
         bad |= in && !ok;
-        const unsigned vmask = __ballot_sync(0xffffffffu, ok);
+        const unsigned vmask = __ballot_sync(0xffffffffu, ok) & Shape<S>::FULL;
         const size_t cell = ok ? ((size_t)f.page << page_shift) + (c & (a.page_size - 1)) : 0;
         const size_t si = (cell * a.n_kv_heads + kvh) * 4;
         const bool sok = ok && QSA_IN(si + 3, (size_t)a.n_pages * a.page_size * a.n_kv_heads * 4);
-        cp_async8(tc::smem_u32(&sh.scale[warp][stage][0][lane]), a.ksc + (sok ? si : 0), sok);
-        cp_async8(tc::smem_u32(&sh.scale[warp][stage][1][lane]), a.vsc + (sok ? si : 0), sok);
+        if constexpr (S == 1) {
+            cp_async8(tc::smem_u32(&sh.scale[warp][stage][0][lane]), a.ksc + (sok ? si : 0), sok);
+            cp_async8(tc::smem_u32(&sh.scale[warp][stage][1][lane]), a.vsc + (sok ? si : 0), sok);
+        } else {  // lanes 0-15 K's, lanes 16-31 V's
+            cp_async8(tc::smem_u32(&sh.scale[warp][stage][lane >> 4][lane & 15]), (lane & 16 ? a.vsc : a.ksc) + (sok ? si : 0), sok);
+        }
         asm volatile("cp.async.commit_group;\n" ::);
-        // A box starts on the first cell of a page or of a 32-cell part of one.
+        // A box starts on the first cell of a page or of a unit in one.
         const int cell16 = __shfl_sync(0xffffffffu, (int)cell, 16);
         if (vmask && !dead) {
             flying |= 1u << stage;
             if (lane == 0) {
                 const uint32_t bar = tc::smem_u32(&sh.bar[warp][stage]);
-                const uint32_t k = tc::smem_u32(sh.tile[warp][stage][0]), v = tc::smem_u32(sh.tile[warp][stage][1]);
-                if (a.page_size >= UNIT) {
+                const uint32_t k = tc::smem_u32(sh.tile[warp][stage][0]), v = k + TILE;
+                if constexpr (S == 2) {
                     expect_tx(bar, 2 * TILE);
-                    tma_box(k, &kmap, DW * half, kvh, (int)cell, bar);
-                    tma_box(v, &vmap, DW * half, kvh, (int)cell, bar);
-                } else {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        tma_box(k + half * TILE / 2, &kmap, 128 * half, kvh, (int)cell, bar);
+                        tma_box(v + half * TILE / 2, &vmap, 128 * half, kvh, (int)cell, bar);
+                    }
+                } else if (a.page_size >= UNIT) {
+                    expect_tx(bar, 2 * TILE);
+                    tma_box(k, &kmap, 0, kvh, (int)cell, bar);
+                    tma_box(v, &vmap, 0, kvh, (int)cell, bar);
+                } else {  // two pages of 16 cells
                     const bool lo = vmask & 0xFFFFu, hi = vmask >> 16;
                     expect_tx(bar, (lo && hi ? 2 : 1) * TILE);
                     if (lo) {
-                        tma_box(k, &kmap, DW * half, kvh, (int)cell, bar);
-                        tma_box(v, &vmap, DW * half, kvh, (int)cell, bar);
+                        tma_box(k, &kmap, 0, kvh, (int)cell, bar);
+                        tma_box(v, &vmap, 0, kvh, (int)cell, bar);
                     }
                     if (hi) {
-                        tma_box(k + TILE / 2, &kmap, DW * half, kvh, cell16, bar);
-                        tma_box(v + TILE / 2, &vmap, DW * half, kvh, cell16, bar);
+                        tma_box(k + TILE / 2, &kmap, 0, kvh, cell16, bar);
+                        tma_box(v + TILE / 2, &vmap, 0, kvh, cell16, bar);
                     }
                 }
             }
         }
-        f.u += NP;
+        f.u += NW;
         settle();
         return vmask;
     };
@@ -608,23 +620,23 @@ __global__ void __launch_bounds__(NW * 32, 2)
     peek();
     settle();
     q.store(a, sh);
-    int stage = 0, nx = 0;
+    int stage = 0;
     unsigned vmask = 0;
     bool ahead = false;  // the next unit's copies have been started
     Part part{-1, 0};
     __syncthreads();  // the query fragments
 
     for (bool first = true;; first = false) {
-        // Segment: units u0 .. u1-1 of row t; this group's are u0 + pw, + NP ...
+        // Segment: units u0 .. u1-1 of row t; this warp's are u0 + warp, + NW ...
         const int u1 = min(nu, u0 + left), n_units = u1 - u0;
-        const int n = n_units > pw ? (n_units - pw + NP - 1) / NP : 0;
+        const int n = n_units > warp ? (n_units - warp + NW - 1) / NW : 0;
         // |scale| in base 2, floored at the smallest normal float: with scale
         // 0 the weights are uniform and a masked -inf stays -inf.
         const float sl2[2] = {fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g], 1.17549435e-38f),
                               fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g + 8], 1.17549435e-38f)};
-        State st;
+        State<S> st;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.0f;
+        for (int i = 0; i < 16 * S; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.0f;
         st.m[0] = st.m[1] = -CUDART_INF_F;
         st.l[0] = st.l[1] = 0.0f;
         st.v = -64;  // below any scale's exponent: the first unit sets it
@@ -644,7 +656,9 @@ __global__ void __launch_bounds__(NW * 32, 2)
                     flying &= ~(1u << stage);
                 }
                 __syncwarp();
-                compute_unit<S>(sh, stage, vmask, st, sl2, half, nx++ & 1);
+                const uint8_t *k = sh.tile[warp][stage][0];
+                compute_unit<S>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q, sh.bias, vmask, st,
+                                sl2);
             }
             __syncwarp();  // every lane has read the stage before it is filled again
             vmask = vnext;
@@ -660,64 +674,88 @@ __global__ void __launch_bounds__(NW * 32, 2)
         const bool more = left > 0 && next < a.n_tokens;
         if (more) q.load(a, next, kvh, per);
         __syncthreads();  // all warps are done with the query, and with the values of the segment before
-
-        // Join the groups' states.  Value (h, d) of a group sits at d ^ 8 (h %
-        // 4) of its row: the lanes of an 8-byte store then meet each bank once,
-        // and reads of consecutive d stay consecutive.
+        if (r == 0) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int d = DW * half + ((8 * i + 2 * r) ^ (8 * (g & 3)));
-            *reinterpret_cast<float2 *>(&sh.o[pw][g][d]) = make_float2(st.o[i][0], st.o[i][1]);
-            *reinterpret_cast<float2 *>(&sh.o[pw][g + 8][d]) = make_float2(st.o[i][2], st.o[i][3]);
+            for (int e = 0; e < 2; ++e) {
+                sh.m[warp][g + 8 * e] = st.m[e];
+                sh.l[warp][g + 8 * e] = st.l[e];
+            }
         }
-        if (r == 0 && half == 0) {
-            sh.m[pw][g] = st.m[0];
-            sh.m[pw][g + 8] = st.m[1];
-            sh.l[pw][g] = st.l[0];
-            sh.l[pw][g + 8] = st.l[1];
-        }
-        if (lane == 0 && half == 0) sh.v[pw] = st.v;  // both halves see all four scale groups: the same
+        if (lane == 0) sh.v[warp] = st.v;
         if (more) q.store(a, sh);
-        __syncthreads();
         const bool whole = n_units == nu;
         const size_t at = (size_t)blockIdx.x * 2 + (first && u0 > 0 ? 0 : 1);
-        if (tid < 16) {
-            float M = -CUDART_INF_F, L = 0.0f, w[NP];
+        // Join the warps' states, 128 dims at a time.
 #pragma unroll
-            for (int p = 0; p < NP; ++p) M = fmaxf(M, sh.m[p][tid]);
+        for (int half = 0; half < S; ++half) {
+            // Value (h, d) of a warp sits at d ^ 8 (h % 4) of its row: the lanes
+            // of an 8-byte store then meet each bank once, and reads of
+            // consecutive d stay consecutive.
+            if (half) __syncthreads();
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                w[p] = sh.m[p][tid] == -CUDART_INF_F ? 0.0f : exp2f(sh.m[p][tid] - M);
-                L += w[p] * sh.l[p][tid];
+            for (int i = 0; i < 16; ++i) {
+                const int d = (8 * i + 2 * r) ^ (8 * (g & 3));
+                *reinterpret_cast<float2 *>(&sh.o[warp][g][d]) = make_float2(st.o[16 * half + i][0], st.o[16 * half + i][1]);
+                *reinterpret_cast<float2 *>(&sh.o[warp][g + 8][d]) = make_float2(st.o[16 * half + i][2], st.o[16 * half + i][3]);
             }
-            const float inv = whole ? (M == -CUDART_INF_F ? 0.0f : 1.0f / L) : 1.0f;
+            __syncthreads();
+            if (half == 0) {
+                if (tid < 16) {
+                    float M = -CUDART_INF_F, L = 0.0f, w[NW];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) sh.f[p][tid] = w[p] == 0.0f ? 0.0f : w[p] * inv * exp2i(sh.v[p]);
-            if (tid < per) {
-                if (whole) {
-                    if (a.lse) a.lse[(size_t)t * a.n_q_heads + kvh * per + tid] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
-                } else {
-                    work.ml[(at * per + tid) * 2] = M;
-                    work.ml[(at * per + tid) * 2 + 1] = L;
+                    for (int p = 0; p < NW; ++p) M = fmaxf(M, sh.m[p][tid]);
+#pragma unroll
+                    for (int p = 0; p < NW; ++p) {
+                        w[p] = sh.m[p][tid] == -CUDART_INF_F ? 0.0f : exp2f(sh.m[p][tid] - M);
+                        L += w[p] * sh.l[p][tid];
+                    }
+                    const float inv = whole ? (M == -CUDART_INF_F ? 0.0f : 1.0f / L) : 1.0f;
+#pragma unroll
+                    for (int p = 0; p < NW; ++p) sh.f[p][tid] = w[p] == 0.0f ? 0.0f : w[p] * inv * exp2i(sh.v[p]);
+                    if (tid < per) {
+                        if (!whole)
+                            *reinterpret_cast<float2 *>(work.ml + (at * per + tid) * 2) = make_float2(M, L);
+                        else if (a.lse)
+                            a.lse[(size_t)t * a.n_q_heads + kvh * per + tid] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+                    }
                 }
+                __syncthreads();
             }
-        }
-        __syncthreads();
-        for (int i = tid; i < per * (D / 2); i += NW * 32) {
-            const int h = i / (D / 2), d = 2 * (i % (D / 2)), pd = d ^ (8 * (h & 3));
-            float o0 = 0.0f, o1 = 0.0f;
+            // A warp takes 64 dims of every other head, BATCH heads at a time
+            // with their gates on the way together.
+            constexpr int BATCH = 4;
+            const int d = 64 * (warp & 1) + 2 * lane, dd = 128 * half + d;
+            const size_t row0 = (size_t)t * a.n_q_heads + (size_t)kvh * per;
+            for (int h0 = warp >> 1; h0 < per; h0 += 2 * BATCH) {
+                float2 gate[BATCH], y[BATCH];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const float w = sh.f[p][h];
-                const float2 o = *reinterpret_cast<const float2 *>(&sh.o[p][h][pd]);
-                o0 = fmaf(w, o.x, o0);
-                o1 = fmaf(w, o.y, o1);
-            }
-            if (whole) {
-                const size_t oi = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + d;
-                if (QSA_IN(oi + 1, (size_t)a.n_tokens * a.n_q_heads * D)) store_out(a, oi, o0, o1);
-            } else {
-                *reinterpret_cast<float2 *>(work.o + (at * per + h) * D + d) = make_float2(o0, o1);
+                for (int k = 0; k < BATCH; ++k) {
+                    const int h = h0 + 2 * k;
+                    gate[k] = a.gate && whole && h < per && QSA_IN((row0 + h) * D + dd + 1, (size_t)a.n_tokens * a.n_q_heads * D)
+                                  ? __ldg(reinterpret_cast<const float2 *>(a.gate + (row0 + h) * D + dd))
+                                  : make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int h = min(h0 + 2 * k, per - 1), pd = d ^ (8 * (h & 3));
+                    y[k] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                    for (int p = 0; p < NW; ++p) {
+                        const float w = sh.f[p][h];
+                        y[k] = __ffma2_rn(*reinterpret_cast<const float2 *>(&sh.o[p][h][pd]), make_float2(w, w), y[k]);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < BATCH; ++k) {
+                    const int h = h0 + 2 * k;
+                    if (h >= per) break;
+                    if (!whole) {
+                        *reinterpret_cast<float2 *>(work.o + (at * per + h) * D + dd) = y[k];
+                    } else if (QSA_IN((row0 + h) * D + dd + 1, (size_t)a.n_tokens * a.n_q_heads * D)) {
+                        if (a.gate) y[k] = make_float2(gated(y[k].x, gate[k].x), gated(y[k].y, gate[k].y));
+                        store_out(a, (row0 + h) * D + dd, y[k]);
+                    }
+                }
             }
         }
         if (!whole && u0 == 0) part = Part{t, 1 + (nu - u1 + share - 1) / share};
@@ -725,12 +763,11 @@ __global__ void __launch_bounds__(NW * 32, 2)
         t = next;
         u0 = 0;
         int trow;
-        nu = units_of(row_len(a, t, trow, bad));
-        if constexpr (S == 2) __syncthreads();  // the scores' exchange takes the values' place
+        nu = units_of<S>(row_len(a, t, trow, bad));
     }
     asm volatile("cp.async.wait_group 0;\n" ::);
     if (flying) {  // after a time-out: copies in flight land before this CTA's shared memory is given up
-        for (int i = 0; i < NS; ++i)
+        for (int i = 0; i < 2; ++i)
             if ((flying >> i) & 1u) tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][i]), (phase >> i) & 1u, tc::DRAIN_LIMIT);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
@@ -747,7 +784,7 @@ __global__ void __launch_bounds__(NW * 32, 2)
 constexpr int JOIN_WARPS = 16;
 template <int S, int HB>
 __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const qsa_paged_attn_args a) {
-    constexpr int D = DW * S, DC = D / 64, G = JOIN_WARPS / (HB * DC);
+    constexpr int D = Shape<S>::D, DC = D / 64, G = JOIN_WARPS / (HB * DC);
     constexpr int LOADS = (MAX_CTAS + 31) / 32;
     __shared__ float2 so[G > 1 ? JOIN_WARPS : 1][32];
     wait_for_previous_grid();
@@ -809,7 +846,13 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const qsa_p
     const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
     const size_t row = (size_t)part.row * a.n_q_heads + (size_t)(blockIdx.x % a.n_kv_heads) * per + h;
     if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
-    if (QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) store_out(a, row * D + d, o.x * inv, o.y * inv);
+    if (!QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
+    o = make_float2(o.x * inv, o.y * inv);
+    if (a.gate) {
+        const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d));
+        o = make_float2(gated(o.x, gate.x), gated(o.y, gate.y));
+    }
+    store_out(a, row * D + d, o);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -828,13 +871,15 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// Codes [cells, heads, D] in boxes of up to 32 cells x one head x 128 dims.
+// Codes [cells, heads, D] in boxes of a unit's cells (or a page's, if fewer) x
+// one head x 128 dims.
+template <int S>
 cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t *codes) {
     const EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads, (cuuint64_t)a.n_pages * a.page_size};
     const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads * a.head_dim};
-    const cuuint32_t box[3] = {DW, 1, (cuuint32_t)(a.page_size < UNIT ? a.page_size : UNIT)}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {128, 1, (cuuint32_t)std::min(a.page_size, Shape<S>::UNIT)}, ones[3] = {1, 1, 1};
     const CUresult e = fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(codes), dims, strides, box, ones,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -843,9 +888,10 @@ cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t 
 
 template <int S>
 cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
+    constexpr int UNIT = Shape<S>::UNIT;
     CUtensorMap kmap, vmap;
-    cudaError_t e = encode(kmap, a, a.kq);
-    if (e == cudaSuccess) e = encode(vmap, a, a.vq);
+    cudaError_t e = encode<S>(kmap, a, a.kq);
+    if (e == cudaSuccess) e = encode<S>(vmap, a, a.vq);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(paged_attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
     if (e != cudaSuccess) return e;
@@ -854,7 +900,7 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     // heads as CTAs (then there may also be more CTAs than the workspace has
     // places for).
     const long long units = ((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT;
-    const int resident = std::max(152 * 2 / a.n_kv_heads, 1);
+    const int resident = std::max(MAX_CTAS / a.n_kv_heads, 1);
     const bool whole = units <= WHOLE || resident == 1;
     const long long most = whole ? a.n_tokens : (a.n_tokens * units + MIN_SHARE - 1) / MIN_SHARE;
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;

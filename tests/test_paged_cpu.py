@@ -152,7 +152,7 @@ COMPACT = dict(n_rows=2, max_pages=4, n_layers=1, n_pages=8, page_size=16, n_kv_
         (dict(n_pages=0), INV), (dict(max_pages=0), INV), (dict(rows=None, n_rows=2), INV),
         (dict(n_pages=1 << 28), INV), (dict(max_pages=1 << 28), INV), (dict(softmax_scale=float("inf")), INV),
         (dict(workspace_bytes=16), INV), (dict(workspace=FAKE + 16), INV), (dict(workspace=None), INV),
-        (dict(seq_lens=None), INV), (dict(q=FAKE + 4), INV), (dict(lse=FAKE + 2), INV), (dict(ksc=FAKE + 4), INV)]
+        (dict(seq_lens=None), INV), (dict(q=FAKE + 4), INV), (dict(lse=FAKE + 2), INV), (dict(gate=FAKE + 4), INV), (dict(ksc=FAKE + 4), INV)]
 ] + [
     ("qsa_page_update", _abi.PageUpdateArgs, UPDATE, kw, want) for kw, want in [
         (dict(page_size=24), UNS), (dict(head_dim=128, group=64), UNS), (dict(n_kv_heads=0), UNS), (dict(n_rows=-1), INV),

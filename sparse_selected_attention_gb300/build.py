@@ -36,7 +36,7 @@ VARIANTS = {
     "check": (["-DQSA_CHECK=1"], "libqsa_check.so"),
 }
 SOURCES = ["api.cpp", "prep.cu", "score.cu", "select.cu", "attn.cu", "ids.cu",
-           "paged_prep.cu", "paged_attn.cu", "pages.cu"]
+           "paged_prep.cu", "paged_attn.cu", "paged_group.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

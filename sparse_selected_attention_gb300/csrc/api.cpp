@@ -263,7 +263,8 @@ qsa_status qsa_check_word(unsigned int *out) {
     cudaError_t (*const readers[])(unsigned int *) = {qsa::take_check_word_attn, qsa::take_check_word_score,
                                                       qsa::take_check_word_prep, qsa::take_check_word_select,
                                                       qsa::take_check_word_ids,  qsa::take_check_word_paged_prep,
-                                                      qsa::take_check_word_paged_attn, qsa::take_check_word_pages};
+                                                      qsa::take_check_word_paged_attn, qsa::take_check_word_paged_group,
+                                                      qsa::take_check_word_pages};
     for (auto rd : readers) {
         unsigned int v = 0u;
         const cudaError_t e = rd(&v);

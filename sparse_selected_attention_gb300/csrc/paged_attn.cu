@@ -40,15 +40,10 @@
 // weights, a set of fp16 weights per scale group, under a power of two per
 // warp that keeps small scales out of the subnormals.
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <math_constants.h>
 
 #include <algorithm>
 
-#include "check.cuh"
-#include "qsa_internal.h"
-#include "tc_common.cuh"
+#include "paged_attn.cuh"
 
 namespace qsa {
 namespace {
@@ -57,10 +52,6 @@ constexpr int NW = 4;           // warps per CTA
 constexpr int CTAS_PER_SM = 2;  // 255 registers a thread
 constexpr int MAX_CTAS = 152 * CTAS_PER_SM;
 constexpr int TILE = 4096;      // a unit's K or V codes
-constexpr float LN2 = 0.6931471805599453f;
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float SLACK = 8.0f;   // weights stay below 2^8 of the running maximum's
-
 // Fewest units of a share, one per warp: finer ones would only add partials.
 constexpr int MIN_SHARE = NW;
 // Rows of up to this many units are not shared out.
@@ -74,23 +65,9 @@ struct Shape {
     static constexpr unsigned FULL = S == 1 ? 0xffffffffu : 0xffffu;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
-__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
-
 // Bytes 0 and 2 (or 1 and 3) of w, as fp16 1152 + code.
 __device__ __forceinline__ uint32_t even_codes(uint32_t w) { return tc::prmt(w ^ 0x80808080u, 0x64646464u, 0x4240); }
 __device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return tc::prmt(w ^ 0x80808080u, 0x64646464u, 0x4341); }
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
 
 // Two 16 x 16 byte matrices of V, cells as rows, from lanes 0-15's and lanes
 // 16-31's row addresses: registers 0 and 2 hold cells 4 r .. 4 r + 3 of dim g
@@ -141,49 +118,17 @@ struct Smem {
     int row;
 };
 
-struct Part {
-    int row, n;  // the row that starts in this CTA and spans n CTAs of its KV head; row -1: none
-};
-
-struct Work {
-    Part *part;  // [grid]
-    float *ml;   // [grid][2][per][2]
-    float *o;    // [grid][2][per][D]
-};
-__host__ __device__ inline Work carve(void *ws, int per) {
-    uint8_t *b = static_cast<uint8_t *>(ws);
-    Work w;
-    w.part = reinterpret_cast<Part *>(b);
-    b += ((size_t)MAX_CTAS * sizeof(Part) + 255) / 256 * 256;
-    w.ml = reinterpret_cast<float *>(b);
-    b += ((size_t)MAX_CTAS * 2 * per * 2 * sizeof(float) + 255) / 256 * 256;
-    w.o = reinterpret_cast<float *>(b);
-    return w;
-}
-
-// Row t's length, cut to its range, and its table row (0 with length 0 if it
-// is out of range).
-__device__ __forceinline__ int row_len(const qsa_paged_attn_args &a, int t, int &row, bool &bad) {
-    row = a.rows ? __ldg(a.rows + t) : t;
-    const int len = __ldg(a.seq_lens + t), most = a.max_pages * a.page_size;
-    if (row < 0 || row >= a.n_rows) {
-        bad = true;
-        row = 0;
-        return 0;
-    }
-    bad |= len < 0 || len > most;
-    return min(max(len, 0), most);
-}
+// Units of a row: one at least, so that an empty row's output is written; none
+// for a row of a group (block 0: there are no groups).
 template <int S>
-__device__ __forceinline__ int units_of(int len) {
-    return max((len + Shape<S>::UNIT - 1) / Shape<S>::UNIT, 1);
+__device__ __forceinline__ int row_units(const qsa_paged_attn_args &a, int t, int block, int len) {
+    return block && grouped(a, t, block) ? 0 : max((len + Shape<S>::UNIT - 1) / Shape<S>::UNIT, 1);
 }
-
 // Sums the rows' units and finds the row that holds unit share * range, of
 // `ranges` shares.
 // Each thread takes a run of rows.
 template <int S>
-__device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int &share) {
+__device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int block, int &share) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (a.n_tokens + NW * 32 - 1) / (NW * 32);
     const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
@@ -191,7 +136,8 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     long long mine = 0;
     for (int t = t0; t < t1; ++t) {
         int row;
-        mine += units_of<S>(row_len(a, t, row, bad));
+        const int len = row_len(a, t, row, bad);
+        mine += row_units<S>(a, t, block, len);
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     long long s = mine;
@@ -215,7 +161,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     if (x0 >= before && x0 < before + mine) {
         for (int t = t0;; ++t) {
             int row;
-            const int u = units_of<S>(row_len(a, t, row, bad));
+            const int len = row_len(a, t, row, bad), u = row_units<S>(a, t, block, len);
             if (x0 < before + u) {
                 sh.row = t;
                 sh.before = before;
@@ -480,15 +426,6 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     }
 }
 
-__device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i, float2 y) {
-    if (a.dtype == QSA_F16)
-        *reinterpret_cast<__half2 *>(static_cast<__half *>(a.out) + i) = __floats2half2_rn(y.x, y.y);
-    else
-        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(y.x, y.y);
-}
-// y / (1 + exp(-gate)); each step off by a few 2^-23, and a gate far below 0 gives 0.
-__device__ __forceinline__ float gated(float y, float gate) { return __fdividef(y, 1.0f + ex2(-gate * LOG2E)); }
-
 // The units of a warp in order, across rows: unit u of row t is the next
 // one whose copies start.  The row after, and the page of the next unit, are
 // loaded a step before they are needed.
@@ -502,7 +439,7 @@ struct Feed {
 template <int S>
 __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     paged_attn_kernel(const qsa_paged_attn_args a, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap, int whole_rows) {
+                      const __grid_constant__ CUtensorMap vmap, int whole_rows, int block) {
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<S> &sh = *reinterpret_cast<Smem<S> *>(raw);
     constexpr int D = Shape<S>::D, UNIT = Shape<S>::UNIT;
@@ -516,16 +453,16 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     wait_for_previous_grid();
     allow_dependent_launch();
     const int kvh = blockIdx.x % a.n_kv_heads, range = blockIdx.x / a.n_kv_heads, ranges = gridDim.x / a.n_kv_heads;
-    const Work work = carve(a.workspace, per);
+    const Work work(a.workspace, MAX_CTAS, per);
     // This CTA's units: `left` of them from unit u0 of row t on, or with
     // whole_rows every ranges-th row from row `range`.
     int share = 0, t = range, u0 = 0, left = 0x7fffffff;
     const int step = whole_rows ? ranges : 1;
     if (!whole_rows) {
-        find_start<S>(a, sh, range, ranges, share);
+        find_start<S>(a, sh, range, ranges, block, share);
         const long long x = (long long)share * range, total = sh.total;
         if (x >= total) {
-            if (tid == 0) work.part[blockIdx.x] = Part{-1, 0};
+            if (tid == 0) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
             return;
         }
         left = (int)min((long long)share, total - x);
@@ -538,7 +475,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     Feed f;
     f.t = t;
     f.len = row_len(a, t, f.trow, bad);
-    int nu = units_of<S>(f.len);
+    int nu = row_units<S>(a, t, block, f.len);
     f.end = min(nu, u0 + left);
     f.left = left - (f.end - u0);
     f.u = u0 + warp;
@@ -552,7 +489,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             f.t += step;
             f.len = f.next_len;
             f.trow = f.next_trow;
-            f.end = min(units_of<S>(f.len), f.left);
+            f.end = min(row_units<S>(a, f.t, block, f.len), f.left);
             f.left -= f.end;
             f.u = warp;
             peek();
@@ -623,7 +560,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     int stage = 0;
     unsigned vmask = 0;
     bool ahead = false;  // the next unit's copies have been started
-    Part part{-1, 0};
+    Part part{-1, 0, 0, 0};
     __syncthreads();  // the query fragments
 
     for (bool first = true;; first = false) {
@@ -670,7 +607,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
         }
         left -= n_units;
-        const int next = t + step;
+        int next = t + step;
+        while (block && left > 0 && next < a.n_tokens && grouped(a, next, block)) next += step;
         const bool more = left > 0 && next < a.n_tokens;
         if (more) q.load(a, next, kvh, per);
         __syncthreads();  // all warps are done with the query, and with the values of the segment before
@@ -758,12 +696,12 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
                 }
             }
         }
-        if (!whole && u0 == 0) part = Part{t, 1 + (nu - u1 + share - 1) / share};
+        if (!whole && u0 == 0) part = Part{t, 1 + (nu - u1 + share - 1) / share, 1, 0};
         if (!more) break;
         t = next;
         u0 = 0;
         int trow;
-        nu = units_of<S>(row_len(a, t, trow, bad));
+        nu = max((row_len(a, t, trow, bad) + UNIT - 1) / UNIT, 1);
     }
     asm volatile("cp.async.wait_group 0;\n" ::);
     if (flying) {  // after a time-out: copies in flight land before this CTA's shared memory is given up
@@ -772,87 +710,6 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     if (tid == 0 && !whole_rows) work.part[blockIdx.x] = part;
-}
-
-// Joins the partials of rows that span CTAs.  Block x looks after the row that
-// starts in CTA x and continues in others, if there is one: part p is slot 1 of
-// that CTA, then slot 0 of the next ones of its KV head.  A warp takes 64 dims
-// of one query head and every G-th part; it works the weights out itself (a
-// few loads per lane), so there is nothing to wait for but the last sum.  Many
-// rows: HB heads and no split per block; few, whose parts are many: the block's
-// warps split the parts of one head.
-constexpr int JOIN_WARPS = 16;
-template <int S, int HB>
-__global__ void __launch_bounds__(JOIN_WARPS * 32) paged_join_kernel(const qsa_paged_attn_args a) {
-    constexpr int D = Shape<S>::D, DC = D / 64, G = JOIN_WARPS / (HB * DC);
-    constexpr int LOADS = (MAX_CTAS + 31) / 32;
-    __shared__ float2 so[G > 1 ? JOIN_WARPS : 1][32];
-    wait_for_previous_grid();
-    allow_dependent_launch();
-    const int per = a.n_q_heads / a.n_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.y * HB + warp / (DC * G), dc = warp / G % DC, grp = warp % G;
-    const Work work = carve(a.workspace, per);
-    const Part part = work.part[blockIdx.x];
-    if (part.row < 0) return;
-    auto slot = [&](int p) { return (size_t)(blockIdx.x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0); };
-    const int n = h < per ? part.n : 0;
-    float w[LOADS], l[LOADS], M = -CUDART_INF_F, L = 0.0f;
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const int p = i * 32 + lane;
-        w[i] = -CUDART_INF_F;
-        l[i] = 0.0f;
-        if (p < n) {
-            const float2 v = *reinterpret_cast<const float2 *>(work.ml + (slot(p) * per + h) * 2);
-            w[i] = v.x;
-            l[i] = v.y;
-        }
-        M = fmaxf(M, w[i]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        w[i] = w[i] == -CUDART_INF_F ? 0.0f : exp2f(w[i] - M);
-        L += w[i] * l[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const int d = dc * 64 + lane * 2;
-    float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        if (i * 32 >= n) break;
-        const int top = min(n - i * 32, 32);
-#pragma unroll 4
-        for (int k = (grp - i * 32 % G + G) % G; k < top; k += G) {
-            const float f = __shfl_sync(0xffffffffu, w[i], k);
-            const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(i * 32 + k) * per + h) * D + d);
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-        }
-    }
-    if constexpr (G > 1) {
-        so[warp][lane] = o;
-        __syncthreads();
-        if (grp) return;
-#pragma unroll
-        for (int i = 1; i < G; ++i) {
-            o.x += so[warp + i][lane].x;
-            o.y += so[warp + i][lane].y;
-        }
-    }
-    if (h >= per) return;
-    const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
-    const size_t row = (size_t)part.row * a.n_q_heads + (size_t)(blockIdx.x % a.n_kv_heads) * per + h;
-    if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
-    if (!QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
-    o = make_float2(o.x * inv, o.y * inv);
-    if (a.gate) {
-        const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d));
-        o = make_float2(gated(o.x, gate.x), gated(o.y, gate.y));
-    }
-    store_out(a, row * D + d, o);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -904,23 +761,18 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const bool whole = units <= WHOLE || resident == 1;
     const long long most = whole ? a.n_tokens : (a.n_tokens * units + MIN_SHARE - 1) / MIN_SHARE;
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
-    e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, whole ? 1 : 0);
-    if (e != cudaSuccess || whole) return e;
-    // Fewer rows than half the SMs: their parts are many (a row of 30 K cells
-    // alone: 118), and a block's warps share them.
-    const int per = a.n_q_heads / a.n_kv_heads;
-    constexpr int HB = S == 1 ? 8 : 4;
-    if ((long long)a.n_tokens * a.n_kv_heads < 76)
-        return launch_dependent(paged_join_kernel<S, 1>, dim3(grid, per), dim3(JOIN_WARPS * 32), 0, s, a);
-    return launch_dependent(paged_join_kernel<S, HB>, dim3(grid, (per + HB - 1) / HB), dim3(JOIN_WARPS * 32), 0, s, a);
+    const int per = a.n_q_heads / a.n_kv_heads, block = a.rows && !whole ? group_block(per) : 0;
+    e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, whole ? 1 : 0, block);
+    if (e == cudaSuccess && !whole) e = launch_join<S>(a, a.workspace, MAX_CTAS, per, grid, s);
+    if (e == cudaSuccess && block)
+        e = launch_paged_group(a, static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), s);
+    return e;
 }
 
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
-    const int per = n_q_heads / n_kv_heads;
-    const Work w = carve(nullptr, per);
-    return reinterpret_cast<uintptr_t>(w.o) + (size_t)MAX_CTAS * 2 * per * head_dim * sizeof(float);
+    return Work::bytes(MAX_CTAS, n_q_heads / n_kv_heads, head_dim) + paged_group_workspace_bytes(head_dim);
 }
 
 cudaError_t launch_paged_attn(const qsa_paged_attn_args &a, cudaStream_t s) {

@@ -155,6 +155,7 @@ cudaError_t take_check_word_select(unsigned int *out);
 cudaError_t take_check_word_ids(unsigned int *out);
 cudaError_t take_check_word_paged_prep(unsigned int *out);
 cudaError_t take_check_word_paged_attn(unsigned int *out);
+cudaError_t take_check_word_paged_group(unsigned int *out);
 cudaError_t take_check_word_pages(unsigned int *out);
 #endif
 

@@ -236,7 +236,7 @@ def shuffled_table(lens, page, extra, rng, wide=None):
     return table, max(pages, 1)
 
 
-def check_attn(q, pool, table, lens, rows=None, scale=None, gate=None, otype=F16, lse=True, ws=None, what=""):
+def check_attn(q, pool, table, lens, rows=None, scale=None, gate=None, otype=F16, lse=True, ws=None, what="", grouped=False):
     """q float64 [T, H, D]; returns the output tensor and the error word."""
     T, H, D = q.shape
     hkv = pool[0].shape[2]
@@ -250,7 +250,7 @@ def check_attn(q, pool, table, lens, rows=None, scale=None, gate=None, otype=F16
                        softmax_scale=scale, gate=None if gate is None else dev(gate), lse=ls, err=err)
     torch.cuda.synchronize()
     ref, rlse, mag, flush, qk = po.attn(host(qd), *pool, table, lens, rows, scale, gate)
-    ds = 1152 * qk * 2.0 ** -21
+    ds = 1152 * qk * 2.0 ** -21 + (127 * qk * 2.0 ** -11 if grouped else 0.0)
     tol = HALF[otype] * np.abs(ref) + mag * (2.0 ** -10 + 2 * np.expm1(ds)[..., None] + 2.0 ** -16) + flush * 2.0 ** -24 + TINY[otype]
     got = host(out)
     bad = ~(np.abs(got - ref) <= tol)
@@ -305,8 +305,67 @@ def test_attn_draft_window_shares_a_sequence(cuda_device):
     lens = [base + 1 + i for i in range(8)] + [50, 99, 0]
     q = rng.standard_normal((11, 24, 256))
     gate = wl.gates_f32(11, seed=3, heads=24, head_dim=256)
-    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=BF16)
+    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=BF16, grouped=True)
     assert err == 0
+
+
+@pytest.mark.parametrize("d,hq,hkv,page,window,base", [
+    (128, 12, 1, 64, 8, 700), (256, 24, 2, 16, 8, 1300), (128, 32, 8, 32, 4, 500), (128, 4, 4, 16, 130, 63), (256, 16, 1, 256, 5, 1),
+    (128, 8, 1, 128, 16, 9000), (256, 6, 3, 64, 3, 64)])
+def test_attn_groups(cuda_device, d, hq, hkv, page, window, base):
+    """Windows of consecutive tokens of several sequences, which are taken
+    together: sizes below and past a group's, alone and beside single rows."""
+    rng = np.random.default_rng(window)
+    held = [base + window, 40, base // 2 + 3, 2 * base + window]
+    table, pages = shuffled_table(held, page, 2, rng)
+    pool = make_pool(pages, page, hkv, d, seed=22)
+    rows, lens = [], []
+    for s in (0, 1, 3, 2, 0):
+        n = window if s != 1 else 1
+        rows += [s] * n
+        lens += [max(held[s] - n + 1 + i, 0) for i in range(n)]
+    q = rng.standard_normal((len(rows), hq, d)) * 1.5
+    otype = F16 if hkv % 2 else BF16
+    gate = wl.gates_f32(len(rows), seed=4, heads=hq, head_dim=d) if hkv == 2 else None
+    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=otype, grouped=True)
+    assert err == 0
+
+
+def test_attn_group_lengths_and_scales(cuda_device):
+    """Rows of a group in any order of lengths, empty ones among them; wide K
+    and V scales, zero ones, a negative softmax scale; missing pages."""
+    rng = np.random.default_rng(23)
+    table, pages = shuffled_table([1000, 64], 32, 2, rng)
+    pool = make_pool(pages, 32, 2, 128, seed=23)
+    for i in (2, 3):
+        pool[i] = np.exp(wl.uniform(24 + i, 1, pool[i].shape, math.log(1e-5), math.log(0.5 if i == 2 else 100.0))).astype(np.float16)
+        pool[i][::3, ::2] = 0
+    rows = [0] * 7 + [1] * 5
+    lens = [1000, 0, 3, 129, 64, 999, 65, 0, 64, 1, 63, 33]
+    q = rng.standard_normal((12, 24, 128))
+    for scale in (None, -0.03, 0.0):
+        out, err = check_attn(q, pool, table, lens, rows=rows, scale=scale, otype=BF16, grouped=True)
+        assert err == 0 and not out[1].any() and not out[7].any()
+    check_attn(q * 1e8, pool, table, lens, rows=rows, scale=1e-10, otype=BF16, grouped=True)
+    table[0, 3], table[1, 1] = -4, pages
+    _, err = check_attn(q, pool, table, lens, rows=rows, grouped=True)
+    assert err == qsa.QSA_DEVERR_BAD_ID
+    out, err = check_attn(q, pool, table, lens, rows=[9] * 12, grouped=True)
+    assert err == qsa.QSA_DEVERR_BAD_ID and not out.any()
+
+
+def test_attn_many_groups(cuda_device):
+    """More groups than CTAs, and one group over the whole chip."""
+    rng = np.random.default_rng(25)
+    for seqs, window, lo, hi in ((90, 4, 1, 300), (1, 8, 20000, 20000), (5, 3, 2000, 4000)):
+        held = [int(v) + window for v in rng.integers(lo, hi + 1, seqs)]
+        table, pages = shuffled_table(held, 64, 1, rng)
+        pool = make_pool(pages, 64, 1, 128, seed=26)
+        rows = [s for s in range(seqs) for _ in range(window)]
+        lens = [held[s] - window + 1 + i for s in range(seqs) for i in range(window)]
+        q = rng.standard_normal((len(rows), 4, 128)) * 2
+        _, err = check_attn(q, pool, table, lens, rows=rows, grouped=True)
+        assert err == 0
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 1.0, 1e-30])

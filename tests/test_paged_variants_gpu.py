@@ -52,12 +52,15 @@ def every_call(d, hkv, per, page):
     out, lse = z(7, hq, d, t=BF16), z(7, hq, t=torch.float32)
     qsa.qsa_paged_attn(q[:7], *layer, tout, lout, out, z(qsa.qsa_paged_attn_workspace_bytes(hq, hkv, d), t=torch.uint8), lse=lse,
                        gate=torch.ones(7, hq, d, device="cuda"), err=err)
+    grp = z(7, hq, d, t=BF16)
+    qsa.qsa_paged_attn(q[:7], *layer, tout, i32(900, 701, 702, 703, 20, 0, 35), grp, z(qsa.qsa_paged_attn_workspace_bytes(hq, hkv, d), t=torch.uint8),
+                       rows=i32(0, 0, 0, 0, 2, 2, 2), err=z(1))
     ko, vo = z(70, hkv, d, t=F16), z(70, hkv, d, t=F16)
     qsa.qsa_paged_gather(*layer, slots, ko, vo, err=err)
     pmap, live, t2, r2 = z(pages), z(1), z(7, table.shape[1]), z(pages)
     qsa.qsa_page_compact(tout, lout, *pool, t2, r2, pmap, live, ws, err=err)
     torch.cuda.synchronize()
-    return [tout, lout, refs, slots, pos, q, out, lse, ko, vo, t2, r2, pmap, live, err] + pool
+    return [tout, lout, refs, slots, pos, q, out, lse, grp, ko, vo, t2, r2, pmap, live, err] + pool
 
 
 @pytest.mark.parametrize("d,hkv,per,page", [(128, 1, 12, 16), (128, 3, 5, 64), (256, 2, 12, 32)])
@@ -71,8 +74,8 @@ def test_check_build_same_bits(cuda_device, use_library, d, hkv, per, page):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), i
 
 
-@pytest.mark.parametrize("d,page", [(128, 64), (128, 16), (256, 32)])
-def test_attn_time_out(cuda_device, use_library, monkeypatch, d, page):
+@pytest.mark.parametrize("d,page,rows", [(128, 64, None), (128, 16, None), (256, 32, None), (128, 64, [0, 0, 0]), (256, 16, [0, 0, 0])])
+def test_attn_time_out(cuda_device, use_library, monkeypatch, d, page, rows):
     rng = np.random.default_rng(5)
     lens = [3000, 5, 400]
     table, pages = shuffled_table(lens, page, 1, rng)
@@ -82,8 +85,9 @@ def test_attn_time_out(cuda_device, use_library, monkeypatch, d, page):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     out = torch.zeros(3, 6, d, dtype=F16, device="cuda")
     ws = torch.empty(qsa.qsa_paged_attn_workspace_bytes(6, 1, d), dtype=torch.uint8, device="cuda")
-    qsa.qsa_paged_attn(dev(q.astype(np.float16)), *[dev(x) for x in pool], dev(table), i32(lens), out, ws, err=err)
+    qsa.qsa_paged_attn(dev(q.astype(np.float16)), *[dev(x) for x in pool], dev(table), i32(lens), out, ws, err=err,
+                       rows=None if rows is None else i32(rows))
     torch.cuda.synchronize()
     assert int(err.item()) == qsa.QSA_DEVERR_TIMEOUT
     monkeypatch.undo()
-    check_attn(q, pool, table, lens)
+    check_attn(q, pool, table, lens, rows=rows, grouped=rows is not None)

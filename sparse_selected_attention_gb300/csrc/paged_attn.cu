@@ -51,6 +51,7 @@ namespace {
 constexpr int NW = 4;           // warps per CTA
 constexpr int CTAS_PER_SM = 2;  // 255 registers a thread
 constexpr int MAX_CTAS = 152 * CTAS_PER_SM;
+static_assert(MAX_CTAS <= MAX_PARTS, "the join's room");
 constexpr int TILE = 4096;      // a unit's K or V codes
 // Fewest units of a share, one per warp: finer ones would only add partials.
 constexpr int MIN_SHARE = NW;
@@ -763,10 +764,12 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads, block = a.rows && !whole ? group_block(per) : 0;
     e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, whole ? 1 : 0, block);
-    if (e == cudaSuccess && !whole) e = launch_join<S>(a, a.workspace, MAX_CTAS, per, grid, s);
-    if (e == cudaSuccess && block)
-        e = launch_paged_group(a, static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), s);
-    return e;
+    if (e != cudaSuccess || whole) return e;
+    const Joined one{a.workspace, MAX_CTAS, per, grid};
+    Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};
+    if (block && (e = launch_paged_group(a, two.ws, two.ctas, s)) != cudaSuccess) return e;
+    if (!block) two.rows = 0;
+    return launch_join<S>(a, one, two, s);
 }
 
 }  // namespace

@@ -96,106 +96,143 @@ __device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i
 // y / (1 + exp(-gate)); each step off by a few 2^-23, and a gate far below 0 gives 0.
 __device__ __forceinline__ float gated(float y, float gate) { return __fdividef(y, 1.0f + ex2(-gate * LOG2E)); }
 
-// Joins the partials of rows that span CTAs.  Block x looks after the row that
-// starts in CTA x and continues in others, if there is one: part p is slot 1 of
-// that CTA, then slot 0 of the next ones of its KV head.  A warp takes 64 dims
-// of one query head and every G-th part; it works the weights out itself (a
-// few loads per lane), so there is nothing to wait for but the last sum.  Many
+// Joins the partials of rows that span CTAs, of one kernel or of both.  Part p
+// of the row that starts in CTA x is slot 1 of that CTA, then slot 0 of the
+// next ones of its KV head.  A block lists the CTAs in which such rows start,
+// and blocks go round over these and chunks of their heads.  A warp takes 64
+// dims of one head and every G-th part; it works the weights out itself (a few
+// loads per lane), so there is nothing to wait for but the last sum.  Many
 // rows: HB heads and no split per block; few, whose parts are many: the block's
 // warps split the parts of one head.
 constexpr int JOIN_WARPS = 16;
-constexpr int MAX_PARTS = 152 * 2;  // CTAs of either kernel
+constexpr int MAX_PARTS = 152 * 2;          // CTAs of paged_attn_kernel
+constexpr int MAX_GROUP_PARTS = 152;        // CTAs of paged_group_kernel
+struct Joined {  // a kernel's partials: where, room for how many CTAs and heads, CTAs launched
+    void *ws;
+    int cap, rows, ctas;
+};
 template <int S, int HB>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
-    paged_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, int rows) {
+    paged_join_kernel(const qsa_paged_attn_args a, const Joined one, const Joined two) {
     constexpr int D = 128 * S, DC = D / 64, G = JOIN_WARPS / (HB * DC);
     constexpr int LOADS = (MAX_PARTS + 31) / 32;
+    static_assert(MAX_PARTS + MAX_GROUP_PARTS <= JOIN_WARPS * 32, "a thread per CTA");
     __shared__ float2 so[G > 1 ? JOIN_WARPS : 1][32];
+    __shared__ int at[JOIN_WARPS * 32], found[2][JOIN_WARPS];
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int per = a.n_q_heads / a.n_kv_heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.y * HB + warp / (DC * G), dc = warp / G % DC, grp = warp % G;
-    const Work work(ws, ctas, rows);
-    const Part part = work.part[blockIdx.x];
-    if (part.row < 0) return;
-    auto slot = [&](int p) { return (size_t)(blockIdx.x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0); };
-    const int n = h < part.tokens * per ? part.n : 0;
-    float w[LOADS], l[LOADS], M = -CUDART_INF_F, L = 0.0f;
+    const int per = a.n_q_heads / a.n_kv_heads, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Work w1(one.ws, one.cap, one.rows), w2(two.ws, two.cap, two.rows);
+    const bool first = tid < one.ctas && w1.part[tid].row >= 0;
+    const bool second = tid >= one.ctas && tid - one.ctas < two.ctas && w2.part[tid - one.ctas].row >= 0;
+    const unsigned m1 = __ballot_sync(0xffffffffu, first), m2 = __ballot_sync(0xffffffffu, second);
+    if (lane == 0) {
+        found[0][warp] = __popc(m1);
+        found[1][warp] = __popc(m2);
+    }
+    __syncthreads();
+    int before1 = 0, before2 = 0, n1 = 0, n2 = 0;
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        const int p = i * 32 + lane;
-        w[i] = -CUDART_INF_F;
-        l[i] = 0.0f;
-        if (p < n) {
-            const float2 v = *reinterpret_cast<const float2 *>(work.ml + (slot(p) * rows + h) * 2);
+    for (int w = 0; w < JOIN_WARPS; ++w) {
+        before1 += w < warp ? found[0][w] : 0;
+        before2 += w < warp ? found[1][w] : 0;
+        n1 += found[0][w];
+        n2 += found[1][w];
+    }
+    if (first) at[before1 + __popc(m1 & ((1u << lane) - 1))] = tid;
+    if (second) at[n1 + before2 + __popc(m2 & ((1u << lane) - 1))] = tid - one.ctas;
+    __syncthreads();
+    const int chunks1 = (one.rows + HB - 1) / HB, chunks2 = (two.rows + HB - 1) / HB;
+    for (int it = blockIdx.x; it < n1 * chunks1 + n2 * chunks2; it += gridDim.x) {
+        const bool group = it >= n1 * chunks1;
+        const int in = group ? it - n1 * chunks1 : it, chunks = group ? chunks2 : chunks1, rows = group ? two.rows : one.rows;
+        const Work &work = group ? w2 : w1;
+        const int x = at[(group ? n1 : 0) + in / chunks], h0 = in % chunks * HB;
+        const int h = h0 + warp / (DC * G), dc = warp / G % DC, grp = warp % G;
+        const Part part = work.part[x];
+        if (h0 >= part.tokens * per) continue;  // the same in all warps
+        auto slot = [&](int p) { return (size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0); };
+        const int n = h < part.tokens * per ? part.n : 0;
+        float w[LOADS], l[LOADS], M = -CUDART_INF_F, L = 0.0f;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int p = i * 32 + lane;
+            float2 v = make_float2(-CUDART_INF_F, 0.0f);
+            if (p < n) v = *reinterpret_cast<const float2 *>(work.ml + (slot(p) * rows + h) * 2);
             w[i] = v.x;
             l[i] = v.y;
+            M = fmaxf(M, v.x);
         }
-        M = fmaxf(M, w[i]);
-    }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        w[i] = w[i] == -CUDART_INF_F ? 0.0f : exp2f(w[i] - M);
-        L += w[i] * l[i];
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const int d = dc * 64 + lane * 2;
-    float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < LOADS; ++i) {
-        if (i * 32 >= n) break;
-        const int top = min(n - i * 32, 32);
-#pragma unroll 4
-        for (int k = (grp - i * 32 % G + G) % G; k < top; k += G) {
-            const float f = __shfl_sync(0xffffffffu, w[i], k);
-            const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(i * 32 + k) * rows + h) * D + d);
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
+        for (int i = 0; i < LOADS; ++i) {
+            w[i] = w[i] == -CUDART_INF_F ? 0.0f : exp2f(w[i] - M);
+            L += w[i] * l[i];
         }
-    }
-    if constexpr (G > 1) {
-        so[warp][lane] = o;
-        __syncthreads();
-        if (grp) return;
 #pragma unroll
-        for (int i = 1; i < G; ++i) {
-            o.x += so[warp + i][lane].x;
-            o.y += so[warp + i][lane].y;
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        const int d = dc * 64 + lane * 2;
+        float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            if (i * 32 >= n) break;
+            const int top = min(n - i * 32, 32);
+#pragma unroll 8
+            for (int k = grp; k < top; k += G) {  // G divides 32
+                const float f = __shfl_sync(0xffffffffu, w[i], k);
+                const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(i * 32 + k) * rows + h) * D + d);
+                o.x = fmaf(f, v.x, o.x);
+                o.y = fmaf(f, v.y, o.y);
+            }
         }
+        if constexpr (G > 1) {
+            so[warp][lane] = o;
+            __syncthreads();
+            if (grp == 0) {
+#pragma unroll
+                for (int i = 1; i < G; ++i) {
+                    o.x += so[warp + i][lane].x;
+                    o.y += so[warp + i][lane].y;
+                }
+            }
+            __syncthreads();
+        }
+        if (grp || h >= part.tokens * per) continue;
+        const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
+        const size_t row = (size_t)(part.row + h / per) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + h % per;
+        if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+        if (!QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
+        o = make_float2(o.x * inv, o.y * inv);
+        if (a.gate) {
+            const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d));
+            o = make_float2(gated(o.x, gate.x), gated(o.y, gate.y));
+        }
+        store_out(a, row * D + d, o);
     }
-    if (h >= part.tokens * per) return;
-    const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
-    const size_t row = (size_t)(part.row + h / per) * a.n_q_heads + (size_t)(blockIdx.x % a.n_kv_heads) * per + h % per;
-    if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
-    if (!QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
-    o = make_float2(o.x * inv, o.y * inv);
-    if (a.gate) {
-        const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d));
-        o = make_float2(gated(o.x, gate.x), gated(o.y, gate.y));
-    }
-    store_out(a, row * D + d, o);
 }
 
-// `ctas` launched CTAs whose partials lie in ws (room for `cap` of them, `rows`
-// heads each).  Fewer pairs of a row and a KV head than half the SMs: their
-// parts are many (a row of 30 K cells alone: 118), and a block's warps share
-// them.
+// Fewer pairs of a row and a KV head than half the SMs: their parts are many (a
+// row of 30 K cells alone: 118), and a block's warps share them.
 template <int S>
-cudaError_t launch_join(const qsa_paged_attn_args &a, void *ws, int cap, int rows, int ctas, cudaStream_t s) {
+cudaError_t launch_join(const qsa_paged_attn_args &a, const Joined &one, const Joined &two, cudaStream_t s) {
     constexpr int HB = S == 1 ? 8 : 4;
     const dim3 block(JOIN_WARPS * 32);
-    if ((long long)a.n_tokens * a.n_kv_heads < 76)
-        return launch_dependent(paged_join_kernel<S, 1>, dim3(ctas, rows), block, 0, s, a, ws, cap, rows);
-    return launch_dependent(paged_join_kernel<S, HB>, dim3(ctas, (rows + HB - 1) / HB), block, 0, s, a, ws, cap, rows);
+    const long long most = (long long)a.n_tokens * a.n_kv_heads;
+    const bool few = most < 76;
+    // Rows that span CTAs: no more than there are, nor than one per CTA.
+    const int heads = one.rows > two.rows ? one.rows : two.rows;
+    const long long items = (most < one.ctas + two.ctas ? most : one.ctas + two.ctas) * (few ? heads : (heads + HB - 1) / HB);
+    const dim3 grid((unsigned)(items < 152 * 4 ? items : 152 * 4));
+    return few ? launch_dependent(paged_join_kernel<S, 1>, grid, block, 0, s, a, one, two)
+               : launch_dependent(paged_join_kernel<S, HB>, grid, block, 0, s, a, one, two);
 }
 
-// paged_group.cu: the groups, where a.rows is given; ws as Work of GROUP_ROWS rows.
 }  // namespace
 
 size_t paged_group_workspace_bytes(int head_dim);
-cudaError_t launch_paged_group(const qsa_paged_attn_args &a, void *ws, cudaStream_t s);
+// paged_group.cu: the groups, where a.rows is given.  ws as Work of GROUP_ROWS
+// rows; `ctas` receives how many leave partials there, to be joined.
+cudaError_t launch_paged_group(const qsa_paged_attn_args &a, void *ws, int &ctas, cudaStream_t s);
 
 }  // namespace qsa

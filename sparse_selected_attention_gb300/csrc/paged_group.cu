@@ -32,31 +32,60 @@ namespace {
 using namespace tc;
 
 constexpr int M = GROUP_ROWS, N = 64;  // heads and cells of a tile
-constexpr int CONVERTERS = 128;  // threads each for K and V
-constexpr int THREADS = 128 + 2 * CONVERTERS + 64;
+constexpr int SOFTMAX = 256;     // threads of the softmax, two for a head row
+constexpr int CONVERTERS = 256;  // threads that turn codes to halves
+constexpr int PRODUCTS = (SOFTMAX + CONVERTERS) / 32, LOADER = PRODUCTS + 1, WARPS = LOADER + 2;  // roles by warp, in this order
+constexpr int THREADS = 32 * WARPS;
+constexpr int STAGES = 2;        // tiles on their way
 constexpr int MIN_TILES = 6;     // of a share: a partial of 128 rows costs as much as some tiles
 
 template <int S>
 struct GroupShape {
     static constexpr int D = 128 * S;
-    static constexpr uint32_t TMEM_COLS = S == 1 ? 256 : 512, O_COL = 2 * N;  // S at 0 and N
+    static constexpr uint32_t TMEM_COLS = 512, Q_COL = 2 * N, O_COL = Q_COL + D / 2;  // S at 0 and N
+    static_assert(O_COL + D <= TMEM_COLS, "tensor memory");
     static constexpr uint32_t IDESC_S = idesc_f16(M, N, false, false), IDESC_O = idesc_f16(M, D, false, true);
+};
+
+// Zeros where not `have`.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src, bool have) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src), "r"(have ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES), "r"(have ? BYTES : 0)
+                     : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0u;
+}
+// The group that starts at a row t: its rows (0: none starts), and the shortest
+// and longest length.
+struct Group {
+    int rows, least, most, trow;
+    __device__ __forceinline__ int tiles() const { return rows ? max((most + N - 1) / N, 1) : 0; }
 };
 
 // Everything of shared memory; tiles of 64 halves (128 bytes) a row, 16-byte
 // unit u of row r at u ^ (r % 8).
 template <int S>
 struct GroupSmem {
-    uint8_t q[2 * S][M * 128];  // per 64 dims; from here on also the values at the end of a segment, fp32 [M][D]
-    uint8_t k[2 * S][N * 128];
-    uint8_t v[2 * S][N * 128];
-    uint8_t p[M * 128];
+    uint8_t k[2 * S][N * 128];  // per 64 dims; from here on also the values at the end of a segment, fp32 [M][D]
+    uint8_t v[2][2 * S][N * 128];
+    uint8_t p[2][M * 128];
+    alignas(16) int8_t codes[STAGES][2][N * 128 * S];  // K's and V's as they come
+    uint2 scales[STAGES][2][N];
+    bool there[STAGES][N];
     alignas(16) float kf[3][N], vb[3][N], vw[3][N];  // a cell's 2^-ek, -ev (-inf: not there), 2^ev
-    float qinv[M];                       // 2^-e of a head's scaled query
-    uint64_t k_full, v_full, s_full[2], p_full, pv_full, drain;
-    long long scan[THREADS / 32];
+    float top[2][2][M], l[2][M];         // the two halves' maxima (two buffers) and sums of a head row
+    uint64_t full[2][STAGES], empty[2][STAGES];  // K's and V's codes
+    uint64_t q_full, k_full, v_full[2], s_full[2], p_full[2], pv_full[2], drain;
+    long long scan[WARPS];
     long long before;  // tiles before the group at t, in which the CTA's share starts
     int t;
+    Group grp;
     int abort;
     uint32_t tmem;
 };
@@ -79,12 +108,7 @@ __device__ __forceinline__ uint32_t prod(uint32_t codes, __half2 f) {  // (1152 
     const uint32_t off = 0x64806480u;
     return h2u(__hmul2(__hsub2(u2h(codes), u2h(off)), f));
 }
-// The group that starts at row t, looked up by a warp: its rows (0: none
-// starts), and the shortest and longest length.
-struct Group {
-    int rows, least, most, trow;
-    __device__ __forceinline__ int tiles() const { return rows ? max((most + N - 1) / N, 1) : 0; }
-};
+// Looked up by a warp.
 __device__ __forceinline__ Group group_at(const qsa_paged_attn_args &a, int t, int block, bool &bad) {
     const int lane = threadIdx.x & 31, row = __ldg(a.rows + t);
     Group g{0, 0x7fffffff, 0, 0};
@@ -126,12 +150,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int kvh = blockIdx.x % a.n_kv_heads, range = blockIdx.x / a.n_kv_heads, ranges = gridDim.x / a.n_kv_heads;
     volatile int *abort = &sh.abort;
     if (tid == 0) {
-        mbar_init(smem_u32(&sh.s_full[0]), 1);
-        mbar_init(smem_u32(&sh.s_full[1]), 1);
-        mbar_init(smem_u32(&sh.k_full), CONVERTERS + 32);
-        mbar_init(smem_u32(&sh.v_full), CONVERTERS);
-        mbar_init(smem_u32(&sh.p_full), 128);
-        mbar_init(smem_u32(&sh.pv_full), 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_u32(&sh.s_full[b]), 1);
+            mbar_init(smem_u32(&sh.v_full[b]), CONVERTERS);
+            mbar_init(smem_u32(&sh.p_full[b]), SOFTMAX);
+            mbar_init(smem_u32(&sh.pv_full[b]), 1);
+        }
+        mbar_init(smem_u32(&sh.q_full), SOFTMAX);
+        for (int b = 0; b < 2 * STAGES; ++b) {
+            mbar_init(smem_u32(&sh.full[0][0] + b), b < STAGES ? 64 : 32);
+            mbar_init(smem_u32(&sh.empty[0][0] + b), CONVERTERS / 32);
+        }
+        mbar_init(smem_u32(&sh.k_full), CONVERTERS);
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -146,10 +176,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // thread of a row in which a group starts adds it up there.
     int share, left;
     {
-        constexpr int CHUNK = 384;  // a multiple of any block
+        constexpr int CHUNK = 512;  // a multiple of any block
         static_assert(CHUNK <= THREADS && CHUNK % M == 0, "a thread per row");
-        int *srow = reinterpret_cast<int *>(sh.q), *slen = srow + CHUNK;
-        auto tiles_from = [&](int base, int &n) -> int {  // of the group in which row base + tid starts
+        int *srow = reinterpret_cast<int *>(sh.k), *slen = srow + CHUNK;
+        auto group_from = [&](int base) -> Group {  // that starts in row base + tid
             const int t = base + tid;
             __syncthreads();
             if (tid < CHUNK && t < a.n_tokens) {
@@ -158,14 +188,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 slen[tid] = row_len(a, t, trow, bad);
             }
             __syncthreads();
-            n = 0;
-            if (tid >= CHUNK || t >= a.n_tokens || ((t & (block - 1)) && srow[tid - 1] == srow[tid])) return 0;
-            const int end = min(min(a.n_tokens - base, CHUNK), (tid | (block - 1)) + 1);
-            int most = 0, u = tid;
-            for (; u < end && srow[u] == srow[tid]; ++u) most = max(most, slen[u]);
-            if (u - tid < GROUP_MIN) return 0;
-            n = u - tid;
-            return max((most + N - 1) / N, 1);
+            Group g{0, 0x7fffffff, 0, 0};
+            if (tid >= CHUNK || t >= a.n_tokens || ((t & (block - 1)) && srow[tid - 1] == srow[tid])) return g;
+            const int end = min(min(a.n_tokens - base, CHUNK), (tid | (block - 1)) + 1), row = srow[tid];
+            int u = tid;
+            for (; u < end && srow[u] == row; ++u) {
+                g.least = min(g.least, slen[u]);
+                g.most = max(g.most, slen[u]);
+            }
+            if (u - tid >= GROUP_MIN) g.rows = u - tid;
+            g.trow = row >= 0 && row < a.n_rows ? row : 0;
+            return g;
         };
         auto block_sum = [&](int v, long long &before) -> long long {  // of THREADS values, and of those before
             long long sum = v;
@@ -178,20 +211,22 @@ __global__ void __launch_bounds__(THREADS, 1)
             __syncthreads();
             long long total = 0;
             before = sum - v;
-            for (int w = 0; w < THREADS / 32; ++w) {
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) {
                 if (w < warp) before += sh.scan[w];
                 total += sh.scan[w];
             }
             __syncthreads();
             return total;
         };
-        long long total = 0, before;
-        int n, tiles = 0;
+        long long total = 0, before = 0;
+        Group g;
         for (int base = 0; base < a.n_tokens; base += CHUNK) {
-            tiles = tiles_from(base, n);
-            total += block_sum(tiles, before);
+            g = group_from(base);
+            total += block_sum(g.tiles(), before);
         }
-        share = (int)max((total + ranges - 1) / ranges, (long long)MIN_TILES);
+        const long long each = total < 0x7fffffffll - MAX_GROUP_PARTS ? ((int)total + ranges - 1) / ranges : (total + ranges - 1) / ranges;
+        share = (int)max(each, (long long)MIN_TILES);
         const long long x = (long long)share * range;
         left = (int)max(min((long long)share, total - x), 0ll);
         if (left == 0) {  // the same in all threads
@@ -201,252 +236,295 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         long long done = 0;
         for (int base = 0; base < a.n_tokens; base += CHUNK) {
-            if (a.n_tokens > CHUNK) tiles = tiles_from(base, n);
-            const long long sum = block_sum(tiles, before);
-            if (x >= done + before && x < done + before + tiles) {
+            long long sum = total;  // of one chunk, g and before are still at hand
+            if (a.n_tokens > CHUNK) {
+                g = group_from(base);
+                sum = block_sum(g.tiles(), before);
+            }
+            if (x >= done + before && x < done + before + g.tiles()) {
                 sh.t = base + tid;
                 sh.before = done + before;
+                sh.grp = g;
             }
             done += sum;
             if (x < done) break;
         }
     }
-    if (warp == 12) tmem_alloc(smem_u32(&sh.tmem), G::TMEM_COLS);
+    if (warp == PRODUCTS) tmem_alloc(smem_u32(&sh.tmem), G::TMEM_COLS);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem;
     int t = sh.t;
-    Group grp = group_at(a, t, block, bad);
+    Group grp = sh.grp;
     int tokens = grp.rows, tiles = grp.tiles();
     int i0 = (int)((long long)share * range - sh.before);
     Part part{-1, 0, 0, 0};
     int k = 0;  // tiles done: the barriers' phases
-    bool ok = true, issued = false;
+    bool ok = true, issued = false;  // issued: products, by this thread
+    uint32_t segment = 0;
 
-    for (bool first = true;; first = false) {
+    for (bool first = true;; first = false, ++segment) {
         // Segment: tiles i0 .. i1-1 of the group of `tokens` rows at t.
         const int i1 = min(tiles, i0 + left), rows = tokens * per;
         const bool whole = i1 - i0 == tiles;
         const size_t at = (size_t)blockIdx.x * 2 + (first && i0 > 0 ? 0 : 1);
-        float *values = reinterpret_cast<float *>(sh.q);
+        float *values = reinterpret_cast<float *>(sh.k);
         auto head_row = [&](int m) -> size_t {  // of q: token t + m / per, head kvh per + m % per
             const int i = (int)((uint32_t)m * per_inv >> 16);  // m / per, m < 128
             return (size_t)(t + i) * a.n_q_heads + (size_t)kvh * per + (m - i * per);
         };
         const int trow = grp.trow, least = grp.least, most = grp.most;
 
-        // The queries: a warp takes every fourteenth head row, five in flight.
-        auto stage_q = [&] {
-            constexpr int E = 4 * S, QW = THREADS / 32, QB = 5;  // elements per lane; warps; rows in flight
-            for (int m0 = warp; m0 < M; m0 += QB * QW) {
-                uint32_t x[QB][E / 2];
-#pragma unroll
-                for (int b = 0; b < QB; ++b) {
-                    const int m = m0 + QW * b;
-                    const size_t at = head_row(m) * D + lane * E;
-#pragma unroll
-                    for (int e = 0; e < E / 2; ++e) x[b][e] = 0u;
-                    if (m < rows && QSA_IN(at + E - 1, (size_t)a.n_tokens * a.n_q_heads * D)) {
-                        const uint16_t *src = static_cast<const uint16_t *>(a.q) + at;
-                        if constexpr (S == 1)
-                            *reinterpret_cast<uint2 *>(x[b]) = __ldg(reinterpret_cast<const uint2 *>(src));
-                        else
-                            *reinterpret_cast<uint4 *>(x[b]) = __ldg(reinterpret_cast<const uint4 *>(src));
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < QB; ++b) {
-                    const int m = m0 + QW * b;
-                    if (m >= M) break;
-                    int ex = 0;
-                    if (a.dtype != QSA_F16) {  // bf16 under a power of two that keeps it in the fp16 range
-                        uint32_t top = 0u;
-#pragma unroll
-                        for (int e = 0; e < E / 2; ++e) top = __vmaxu2(top, x[b][e] & 0x7FFF7FFFu);
-                        top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-                        ex = head_sum_exponent(__uint_as_float(top << 16));
-                        const float f = exp2i(ex);
-#pragma unroll
-                        for (int e = 0; e < E / 2; ++e)
-                            x[b][e] = h2u(__floats2half2_rn(__uint_as_float(x[b][e] << 16) * f,
-                                                            __uint_as_float(x[b][e] & 0xFFFF0000u) * f));
-                    }
-                    if (lane == 0) sh.qinv[m] = exp2i(-ex);
-                    const int d = lane * E;
-                    uint8_t *dst = sh.q[d >> 6] + unit_off(m, (d & 63) >> 3) + 2 * (d & 7);
-                    if constexpr (S == 1)
-                        *reinterpret_cast<uint2 *>(dst) = *reinterpret_cast<const uint2 *>(x[b]);
-                    else
-                        *reinterpret_cast<uint4 *>(dst) = *reinterpret_cast<const uint4 *>(x[b]);
-                }
-            }
-            fence_async_smem();
-            asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");  // of all roles, each at its place
+        const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
+        auto page_of = [&](int i) {  // of cells 2 lane and 2 lane + 1 of tile i
+            const int j = (i * N + 2 * lane) >> page_shift;
+            return i < i1 && j < a.max_pages ? __ldg(tab + j) : -1;
+        };
+        auto cell_row = [&](int c, int page) -> long long {  // of the pool's (cell, KV head) rows; -1: none
+            const bool have = c < most && page >= 0 && page < a.n_pages;
+            bad |= c < most && !have;
+            const long long row = ((((long long)page << page_shift) + (c & (a.page_size - 1))) * a.n_kv_heads) + kvh;
+            return have && QSA_IN(row, (long long)a.n_pages * a.page_size * a.n_kv_heads) ? row : -1;
         };
 
-        if (warp >= 4 && warp < 12) {
-            // ---- loads and conversion: K (warps 4-7) or V ----
-            // Sixteen codes an item: CH lanes take a cell's row, so that a load
-            // reads whole rows, ITEMS cells per thread.
-            constexpr int CH = D / 16, ITEMS = N * CH / CONVERTERS, STEP = N / ITEMS;
-            const bool is_v = warp >= 8;
-            const int ct = (tid - 128) % CONVERTERS, ch = ct % CH, c0 = ct / CH;
-            const int8_t *codes = (is_v ? a.vq : a.kq) + 16 * ch;
-            const uint16_t *scales = is_v ? a.vsc : a.ksc;
-            uint8_t *dst = is_v ? sh.v[ch >> 2] : sh.k[ch >> 2];
+        constexpr int CH = D / 16;  // items of sixteen codes of a cell
+        if (warp >= LOADER) {
+            // ---- loads, a warp each for K (with the scales of both) and V ----
+            // A lane finds two neighbouring cells, which are of one page; all
+            // then copy, CH lanes to a cell's row.
+            constexpr int AT_ONCE = 32 / CH;
+            const int kind = warp - LOADER;
             const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
-            uint4 w[ITEMS];
-            uint2 sc[ITEMS];
-            auto page_of = [&](int i) {  // of cells 2 lane and 2 lane + 1 of tile i
+            auto page_of = [&](int i) {
                 const int j = (i * N + 2 * lane) >> page_shift;
                 return i < i1 && j < a.max_pages ? __ldg(tab + j) : -1;
             };
-            auto load = [&](int i, int pages) {
-#pragma unroll
-                for (int j = 0; j < ITEMS; ++j) {
-                    const int in = c0 + j * STEP, c = i * N + in, page = __shfl_sync(0xffffffffu, pages, in >> 1);
-                    const bool wanted = i < i1 && c < most;
-                    bool have = wanted && page >= 0 && page < a.n_pages;
-                    bad |= wanted && !have;
-                    const long long row = ((((long long)page << page_shift) + (c & (a.page_size - 1))) * a.n_kv_heads) + kvh;
-                    have = have && QSA_IN(row, (long long)a.n_pages * a.page_size * a.n_kv_heads);
-                    w[j] = have ? __ldg(reinterpret_cast<const uint4 *>(codes + row * D)) : make_uint4(0u, 0u, 0u, 0u);
-                    sc[j] = have ? __ldg(reinterpret_cast<const uint2 *>(scales + row * 4)) : make_uint2(0u, 0u);
-                }
-            };
-            int pages = page_of(i0);
-            load(i0, pages);
-            pages = page_of(i0 + 1);
-            stage_q();
+            // The lane's part of a copy: its cell of the pair, its codes.
+            const int8_t *codes = (kind ? a.vq : a.kq) + (size_t)(lane / CH & 1) * a.n_kv_heads * D + lane % CH * 16;
+            int page = page_of(i0);
             bool good = ok;
-            for (int i = i0; i < i1 && good; ++i, ++k) {
-                // Until the products with the tile before are done.
-                if (k > 0)
-                    good = is_v ? mbar_wait_or_abort(smem_u32(&sh.pv_full), (k - 1) & 1, abort)
-                                : mbar_wait_or_abort(smem_u32(&sh.s_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort);
+            for (int i = i0; i < i1; ++i, ++k) {
+                const int st = k % STAGES, c = i * N + 2 * lane;
+                // The pool's (cell, KV head) row of the first, and which are there.
+                const bool known = page >= 0 && page < a.n_pages;
+                bool have[2] = {known && c < most, known && c + 1 < most};
+                bad |= !known && c < most;
+                const long long row = ((((long long)page << page_shift) + (c & (a.page_size - 1))) * a.n_kv_heads) + kvh;
+                have[0] = have[0] && QSA_IN(row, (long long)a.n_pages * a.page_size * a.n_kv_heads);
+                have[1] = have[1] && QSA_IN(row + a.n_kv_heads, (long long)a.n_pages * a.page_size * a.n_kv_heads);
+                const unsigned m0 = __ballot_sync(0xffffffffu, have[0]), m1 = __ballot_sync(0xffffffffu, have[1]);
+                const unsigned mine = lane / CH & 1 ? m1 : m0;
+                page = page_of(i + 1);
+                if (k >= STAGES) good = mbar_wait_or_abort(smem_u32(&sh.empty[kind][st]), (k / STAGES - 1) & 1, abort);
                 good = __all_sync(0xffffffffu, good);
                 if (!good) break;
+                const long long off = row * D;
+#pragma unroll 8
+                for (int j = 0; j < N / AT_ONCE; ++j) {
+                    const int pair = j * AT_ONCE / 2 + lane / (2 * CH);
+                    const long long o = __shfl_sync(0xffffffffu, off, pair);
+                    const bool in = mine >> pair & 1u;
+                    cp_async<16>(sh.codes[st][kind] + j * 512 + 16 * lane, codes + (in ? o : 0), in);
+                }
+                const uint32_t bar = smem_u32(&sh.full[kind][st]);
+                if (kind == 0) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const size_t r = have[e] ? (row + e * a.n_kv_heads) * 4 : 0;
+                        cp_async<8>(&sh.scales[st][0][2 * lane + e], a.ksc + r, have[e]);
+                        cp_async<8>(&sh.scales[st][1][2 * lane + e], a.vsc + r, have[e]);
+                        sh.there[st][2 * lane + e] = have[e];
+                    }
+                    mbar_arrive(bar);
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+            }
+            ok = good;
+        } else if (warp >= SOFTMAX / 32 && warp < PRODUCTS) {
+            // ---- conversion ----
+            // A warp takes CELLS cells at a time and ITEMS times that of a
+            // tile: eight cells, so a lane makes the factor of one scale of K
+            // and one of V.
+            constexpr int CELLS = 32 / CH, ITEMS = N * CH / CONVERTERS, STEP = N / ITEMS;
+            static_assert(CELLS * ITEMS * 4 == 32, "a factor per lane");
+            const int ct = tid % CONVERTERS, ch = ct % CH, c0 = ct / CH;
+            const int fsub = (lane >> 2) % CELLS, fitem = (lane >> 2) / CELLS, fcell = (ct >> 5) * CELLS + fsub + fitem * STEP;
+            auto convert = [&](int kind, int k, uint32_t mine) {  // of the k-th tile; mine: the lane's factor
+                const int st = k % STAGES;
+                uint8_t *dst = kind ? sh.v[k & 1][ch >> 2] : sh.k[ch >> 2];
 #pragma unroll
                 for (int j = 0; j < ITEMS; ++j) {
-                    const int in = c0 + j * STEP, e = scale_exponent(sc[j]);
-                    const __half2 f = scaled(sc[j], ch / (CH / 4), e);
-                    const uint32_t x[4] = {w[j].x ^ 0x80808080u, w[j].y ^ 0x80808080u, w[j].z ^ 0x80808080u, w[j].w ^ 0x80808080u};
+                    const int in = c0 + j * STEP, odd = ch >> 2 & 1;  // 64 dims apart, lanes write units of other banks
+                    const uint4 w = *reinterpret_cast<const uint4 *>(sh.codes[st][kind] + in * D + 16 * ch);
+                    const __half2 f = u2h(__shfl_sync(0xffffffffu, mine, (j * CELLS + lane / CH) * 4 + ch / (CH / 4)));
+                    const uint32_t x[4] = {(odd ? w.z : w.x) ^ 0x80808080u, (odd ? w.w : w.y) ^ 0x80808080u,
+                                           (odd ? w.x : w.z) ^ 0x80808080u, (odd ? w.y : w.w) ^ 0x80808080u};
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
-                        *reinterpret_cast<uint4 *>(dst + unit_off(in, 2 * (ch & 3) + u)) =
+                        *reinterpret_cast<uint4 *>(dst + unit_off(in, 2 * (ch & 3) + (u ^ odd))) =
                             make_uint4(prod(prmt(x[2 * u], 0x64646464u, 0x4140), f), prod(prmt(x[2 * u], 0x64646464u, 0x4342), f),
                                        prod(prmt(x[2 * u + 1], 0x64646464u, 0x4140), f),
                                        prod(prmt(x[2 * u + 1], 0x64646464u, 0x4342), f));
                 }
                 fence_async_smem();
-                mbar_arrive(smem_u32(is_v ? &sh.v_full : &sh.k_full));
-                load(i + 1, pages);
-                pages = page_of(i + 2);
-            }
-            ok = good;
-        } else if (warp == 13) {
-            // ---- the cells' factors, two cells a lane ----
-            const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
-            uint2 ks[2], vs[2];
-            bool there[2];
-            auto load = [&](int i) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = i * N + 2 * lane + e, j = c >> page_shift;
-                    const int page = i < i1 && c < most && j < a.max_pages ? __ldg(tab + j) : -1;
-                    there[e] = page >= 0 && page < a.n_pages;
-                    const long long row = ((((long long)page << page_shift) + (c & (a.page_size - 1))) * a.n_kv_heads) + kvh;
-                    there[e] = there[e] && QSA_IN(row, (long long)a.n_pages * a.page_size * a.n_kv_heads);
-                    ks[e] = there[e] ? __ldg(reinterpret_cast<const uint2 *>(a.ksc + row * 4)) : make_uint2(0u, 0u);
-                    vs[e] = there[e] ? __ldg(reinterpret_cast<const uint2 *>(a.vsc + row * 4)) : make_uint2(0u, 0u);
-                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.empty[kind][st]));
             };
-            load(i0);
-            stage_q();
+            uint32_t vnext = 0u, vmine;  // V's factors of the tile whose K was converted, and of this
+            auto convert_k = [&](int k) {  // of the k-th tile
+                const int st = k % STAGES, b = k % 3;
+                bool good = mbar_wait_or_abort(smem_u32(&sh.full[0][st]), (k / STAGES) & 1, abort);
+                // Until the products with the tile before are done.  Then also
+                // the softmax of tile k - 3, as S k - 1 was issued after P k - 3 came.
+                if (k > 0) good = good && mbar_wait_or_abort(smem_u32(&sh.s_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort);
+                if (!__all_sync(0xffffffffu, good)) return false;
+                const uint2 ks = sh.scales[st][0][fcell], vs = sh.scales[st][1][fcell];
+                const int ek = scale_exponent(ks), ev = scale_exponent(vs);
+                vnext = h2u(scaled(vs, lane & 3, ev));
+                if ((lane & 3) == 0) {
+                    sh.kf[b][fcell] = exp2i(-ek);
+                    sh.vb[b][fcell] = sh.there[st][fcell] ? -(float)ev : -CUDART_INF_F;
+                    sh.vw[b][fcell] = exp2i(ev);
+                }
+                convert(0, k, h2u(scaled(ks, lane & 3, ek)));
+                mbar_arrive(smem_u32(&sh.k_full));
+                return true;
+            };
+            // K is a tile ahead of V.
             bool good = ok;
-            for (int i = i0; i < i1 && good; ++i, ++k) {
-                // Three buffers: with S k - 1, issued after P k - 3 came, the softmax of tile k - 3 is done.
-                if (k > 0) good = mbar_wait_or_abort(smem_u32(&sh.s_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort);
+            for (int i = i0 - 1; i < i1; ++i) {
+                vmine = vnext;
+                if (i + 1 < i1) good = good && convert_k(k + (i >= i0));
+                if (i < i0) continue;
+                if (!good) break;
+                good = mbar_wait_or_abort(smem_u32(&sh.full[1][k % STAGES]), (k / STAGES) & 1, abort);
+                if (k > 1) good = good && mbar_wait_or_abort(smem_u32(&sh.pv_full[k & 1]), ((k - 2) >> 1) & 1, abort);
                 good = __all_sync(0xffffffffu, good);
                 if (!good) break;
-                const int b = k % 3;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int ev = scale_exponent(vs[e]);
-                    sh.kf[b][2 * lane + e] = exp2i(-scale_exponent(ks[e]));
-                    sh.vb[b][2 * lane + e] = there[e] ? -(float)ev : -CUDART_INF_F;
-                    sh.vw[b][2 * lane + e] = exp2i(ev);
-                }
-                mbar_arrive(smem_u32(&sh.k_full));
-                load(i + 1);
+                convert(1, k, vmine);
+                mbar_arrive(smem_u32(&sh.v_full[k & 1]));
+                ++k;
             }
             ok = good;
-        } else if (warp == 12) {
+        } else if (warp == PRODUCTS) {
             // ---- products ----
-            stage_q();
+            // The whole warp goes through the loop, so that what the products
+            // need is the same in all lanes; one lane issues them.
+            const bool one = elect_one();
             bool good = ok;
-            if (lane == 0) {
-                auto issue_s = [&](int kk) {
-                    good = mbar_wait_or_abort(smem_u32(&sh.k_full), kk & 1, abort);
-                    if (!good) return;
-                    fence_after();
+            auto wait = [&](uint64_t &bar, int phase) {
+                good = good && __all_sync(0xffffffffu, mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort));
+            };
+            // Descriptors differ in their address field (16-byte units) only.
+            const uint64_t dk = sw128_kmajor(smem_u32(sh.k[0])), dp = sw128_kmajor(smem_u32(sh.p[0]));
+            // V transposed: 64 dims apart N * 128 bytes, eight cells 1024.
+            const uint64_t dv = smem_desc(smem_u32(sh.v[0][0]), N * 128, 1024, 2);
+            auto issue_s = [&](int kk) {
+                wait(sh.k_full, kk);
+                if (!good) return;
+                fence_after();
+                if (one) {
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ++ks)
-                        mma_f16(tmem + (kk & 1) * N, sw128_kmajor(smem_u32(sh.q[ks >> 2]) + (ks & 3) * 32),
-                                sw128_kmajor(smem_u32(sh.k[ks >> 2]) + (ks & 3) * 32), G::IDESC_S, ks ? 1u : 0u);
+                        mma_f16_ts(tmem + (kk & 1) * N, tmem + G::Q_COL + ks * 8, dk + (ks >> 2) * (N * 8) + (ks & 3) * 2,
+                                   G::IDESC_S, ks ? 1u : 0u);
                     mma_commit(smem_u32(&sh.s_full[kk & 1]));
-                    issued = true;
-                };
-                issue_s(k);
-                for (int i = i0; i < i1 && good; ++i, ++k) {
-                    // The buffer of S k + 1 was S k - 1's, whose P has come.
-                    if (i + 1 < i1) issue_s(k + 1);
-                    good = good && mbar_wait_or_abort(smem_u32(&sh.v_full), k & 1, abort) &&
-                           mbar_wait_or_abort(smem_u32(&sh.p_full), k & 1, abort);
-                    if (!good) break;
-                    fence_after();
-                    // V transposed: 64 dims apart N * 128 bytes, eight cells 1024.
-#pragma unroll
-                    for (int ks = 0; ks < N / 16; ++ks)
-                        mma_f16(tmem + G::O_COL, sw128_kmajor(smem_u32(sh.p) + ks * 32),
-                                smem_desc(smem_u32(sh.v[0]) + ks * 16 * 128, N * 128, 1024, 2), G::IDESC_O, i > i0 || ks ? 1u : 0u);
-                    mma_commit(smem_u32(&sh.pv_full));
                 }
-            }
-            k = __shfl_sync(0xffffffffu, k, 0);
-            ok = __shfl_sync(0xffffffffu, (int)good, 0);
-        } else {
-            // ---- softmax, a thread per head row ----
-            stage_q();
-            const int m = tid;
-            const bool mine = m < rows;
-            const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-            const float sl2 = a.softmax_scale * LOG2E * sh.qinv[m];
-            int len = 0, tr;
-            if (mine) len = row_len(a, t + (int)((uint32_t)m * per_inv >> 16), tr, bad);
-            float ref = -CUDART_INF_F, l = 0.0f;
-            bool good = ok;
+                issued |= one;
+                __syncwarp();
+            };
+            wait(sh.q_full, segment);
+            if (good) issue_s(k);
             for (int i = i0; i < i1 && good; ++i, ++k) {
-                good = __all_sync(0xffffffffu, mbar_wait_or_abort(smem_u32(&sh.s_full[k & 1]), (k >> 1) & 1, abort));
+                // The buffer of S k + 1 was S k - 1's, whose P has come.
+                if (i + 1 < i1) issue_s(k + 1);
+                wait(sh.v_full[k & 1], k >> 1);
+                wait(sh.p_full[k & 1], k >> 1);
                 if (!good) break;
                 fence_after();
-                float y[N];
-                {
-                    uint32_t v[N / 16][16];
+                if (one) {
 #pragma unroll
-                    for (int c = 0; c < N / 16; ++c) tmem_ld16(lane_base + (k & 1) * N + 16 * c, v[c]);
+                    for (int ks = 0; ks < N / 16; ++ks)
+                        mma_f16(tmem + G::O_COL, dp + (k & 1) * (M * 8) + ks * 2, dv + (k & 1) * (2 * S * N * 8) + ks * 16 * 8,
+                                G::IDESC_O, i > i0 || ks ? 1u : 0u);
+                    mma_commit(smem_u32(&sh.pv_full[k & 1]));
+                }
+                __syncwarp();
+            }
+            ok = good;
+        } else {
+            // ---- softmax: a head row is two threads', NH of a tile's cells each ----
+            constexpr int NH = N / 2, DH = D / 2;
+            const int m = tid & (M - 1), half = tid / M, j0 = half * NH;
+            const bool mine = m < rows;
+            const uint32_t lane_base = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+            int len = 0, tr;
+            if (mine) len = row_len(a, t + (int)((uint32_t)m * per_inv >> 16), tr, bad);
+            // Of the two warps that share their head rows.  Both come here once a
+            // tile whatever they waited for, and go on or stop together.
+            auto both = [&](bool good) {
+                int r;
+                asm volatile("{\n.reg .pred p, q;\nsetp.ne.s32 p, %1, 0;\nbar.red.and.pred q, %2, 64, p;\nselp.s32 %0, 1, 0, q;\n}\n"
+                             : "=r"(r)
+                             : "r"((int)good), "r"(1 + warp % 4)
+                             : "memory");
+                return r != 0;
+            };
+            bool good = ok;
+            // The queries to tensor memory; bf16 ones under a power of two per
+            // head row that keeps them in the fp16 range.
+            float sl2 = a.softmax_scale * LOG2E;
+            {
+                uint32_t x[DH / 32][16];
+                const size_t at = head_row(mine ? m : 0) * D + half * DH;
+                const bool in = mine && QSA_IN(at + DH - 1, (size_t)a.n_tokens * a.n_q_heads * D);
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + (in ? at : 0));
+#pragma unroll
+                for (int j = 0; j < DH / 8; ++j)
+                    *reinterpret_cast<uint4 *>(&x[j / 4][j % 4 * 4]) = in ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+                if (a.dtype != QSA_F16) {
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int j = 0; j < DH / 2; ++j) top = __vmaxu2(top, x[j / 16][j % 16] & 0x7FFF7FFFu);
+                    top = max(top & 0xFFFFu, top >> 16);
+                    sh.l[half][m] = __uint_as_float(top);
+                    good = both(good);
+                    top = max(top, __float_as_uint(sh.l[half ^ 1][m]));
+                    const int ex = head_sum_exponent(__uint_as_float(top << 16));
+                    const float f = exp2i(ex);
+                    sl2 *= exp2i(-ex);
+#pragma unroll
+                    for (int j = 0; j < DH / 2; ++j) {
+                        const uint32_t v = x[j / 16][j % 16];
+                        x[j / 16][j % 16] = h2u(__floats2half2_rn(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f));
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < DH / 32; ++c) tmem_st16(lane_base + G::Q_COL + half * (DH / 2) + 16 * c, x[c]);
+                tmem_wait_st();
+                fence_before();
+                mbar_arrive(smem_u32(&sh.q_full));
+            }
+            float ref = -CUDART_INF_F, l = 0.0f;
+            for (int i = i0; i < i1; ++i, ++k) {
+                good = __all_sync(0xffffffffu, good && mbar_wait_or_abort(smem_u32(&sh.s_full[k & 1]), (k >> 1) & 1, abort));
+                fence_after();
+                float y[NH];
+                {
+                    uint32_t v[NH / 16][16];
+#pragma unroll
+                    for (int c = 0; c < NH / 16; ++c) tmem_ld16(lane_base + (k & 1) * N + j0 + 16 * c, v[c]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
+                    for (int j = 0; j < NH; ++j) {
                         asm volatile("" : "+r"(v[j / 16][j % 16]));  // not before the wait
                         y[j] = __uint_as_float(v[j / 16][j % 16]);
                     }
                 }
-                const float *kf = sh.kf[k % 3], *vb = sh.vb[k % 3], *vw = sh.vw[k % 3];
-                float top = -CUDART_INF_F;
+                const float *kf = sh.kf[k % 3] + j0, *vb = sh.vb[k % 3] + j0, *vw = sh.vw[k % 3] + j0;
 #pragma unroll
-                for (int j = 0; j < N; j += 4) {
+                for (int j = 0; j < NH; j += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(kf + j), b = *reinterpret_cast<const float4 *>(vb + j);
                     float2 s0 = __fmul2_rn(make_float2(y[j], y[j + 1]), make_float2(f.x, f.y));
                     float2 s1 = __fmul2_rn(make_float2(y[j + 2], y[j + 3]), make_float2(f.z, f.w));
@@ -459,84 +537,99 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 if ((i + 1) * N > least) {  // some row ends in this tile
 #pragma unroll
-                    for (int j = 0; j < N; ++j)
-                        if (i * N + j >= len) y[j] = -CUDART_INF_F;
+                    for (int j = 0; j < NH; ++j)
+                        if (i * N + j0 + j >= len) y[j] = -CUDART_INF_F;
                 }
+                float top = -CUDART_INF_F;
 #pragma unroll
-                for (int j = 0; j < N; j += 2) top = max3(top, y[j], y[j + 1]);
+                for (int j = 0; j < NH; j += 2) top = max3(top, y[j], y[j + 1]);
+                sh.top[k & 1][half][m] = top;
+                good = both(good);
+                if (!good) break;
+                top = fmaxf(top, sh.top[k & 1][half ^ 1][m]);
                 // The reference moves only when a tile exceeds it by 2^SLACK.
                 const bool up = top > ref + SLACK;
                 const float alpha = up ? ex2(ref - top) : 1.0f;
                 ref = up ? top : ref;
                 l *= alpha;
-                // P's buffer and the values: the tile before must be done with them.
-                if (k > 0) good = __all_sync(0xffffffffu, mbar_wait_or_abort(smem_u32(&sh.pv_full), (k - 1) & 1, abort));
-                if (!good) break;
                 if (i > i0 && __any_sync(0xffffffffu, up)) {
+                    // The values so far: each of the two scales half of them.
+                    good = __all_sync(0xffffffffu, mbar_wait_or_abort(smem_u32(&sh.pv_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort));
                     fence_after();
-                    for (int c = 0; c < D / 16; ++c) {
+#pragma unroll 1
+                    for (int c = 0; c < DH / 16 && good; ++c) {
                         uint32_t v[16];
-                        tmem_ld16(lane_base + G::O_COL + 16 * c, v);
+                        tmem_ld16(lane_base + G::O_COL + half * DH + 16 * c, v);
                         tmem_wait_ld();
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             asm volatile("" : "+r"(v[j]));
                             v[j] = __float_as_uint(__uint_as_float(v[j]) * alpha);
                         }
-                        tmem_st16(lane_base + G::O_COL + 16 * c, v);
+                        tmem_st16(lane_base + G::O_COL + half * DH + 16 * c, v);
                     }
                     tmem_wait_st();
                 }
                 const float base = ref == -CUDART_INF_F ? 0.0f : -ref;
                 float2 sum = make_float2(0.0f, 0.0f);
+                uint32_t h[NH / 2];
 #pragma unroll
-                for (int u = 0; u < N / 8; ++u) {
-                    uint32_t h[4];
-#pragma unroll
-                    for (int j = 0; j < 4; j += 2) {
-                        const int c = 8 * u + 2 * j;
-                        const float4 f = *reinterpret_cast<const float4 *>(vw + c);
-                        float2 p0 = __fadd2_rn(make_float2(y[c], y[c + 1]), make_float2(base, base));
-                        float2 p1 = __fadd2_rn(make_float2(y[c + 2], y[c + 3]), make_float2(base, base));
-                        p0 = make_float2(ex2(p0.x), ex2(p0.y));
-                        p1 = make_float2(ex2(p1.x), ex2(p1.y));
-                        sum = __ffma2_rn(p0, make_float2(f.x, f.y), sum);
-                        sum = __ffma2_rn(p1, make_float2(f.z, f.w), sum);
-                        h[j] = h2u(__floats2half2_rn(p0.x, p0.y));
-                        h[j + 1] = h2u(__floats2half2_rn(p1.x, p1.y));
-                    }
-                    *reinterpret_cast<uint4 *>(sh.p + unit_off(m, u)) = make_uint4(h[0], h[1], h[2], h[3]);
+                for (int c = 0; c < NH; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(vw + c);
+                    float2 p0 = __fadd2_rn(make_float2(y[c], y[c + 1]), make_float2(base, base));
+                    float2 p1 = __fadd2_rn(make_float2(y[c + 2], y[c + 3]), make_float2(base, base));
+                    p0 = make_float2(ex2(p0.x), ex2(p0.y));
+                    p1 = make_float2(ex2(p1.x), ex2(p1.y));
+                    sum = __ffma2_rn(p0, make_float2(f.x, f.y), sum);
+                    sum = __ffma2_rn(p1, make_float2(f.z, f.w), sum);
+                    h[c / 2] = h2u(__floats2half2_rn(p0.x, p0.y));
+                    h[c / 2 + 1] = h2u(__floats2half2_rn(p1.x, p1.y));
                 }
                 l += sum.x + sum.y;
+                // P's buffer: the products with tile k - 2 must be done.
+                if (k > 1)
+                    good = __all_sync(0xffffffffu, good && mbar_wait_or_abort(smem_u32(&sh.pv_full[k & 1]), ((k - 2) >> 1) & 1, abort));
+                if (good) {
+#pragma unroll
+                    for (int u = 0; u < NH / 8; ++u)
+                        *reinterpret_cast<uint4 *>(sh.p[k & 1] + unit_off(m, half * (NH / 8) + u)) =
+                            make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
+                }
                 fence_async_smem();
                 fence_before();
-                mbar_arrive(smem_u32(&sh.p_full));
+                if (good) mbar_arrive(smem_u32(&sh.p_full[k & 1]));
             }
-            if (good && k > 0) good = __all_sync(0xffffffffu, mbar_wait_or_abort(smem_u32(&sh.pv_full), (k - 1) & 1, abort));
+            if (good && k > 0)
+                good = mbar_wait_or_abort(smem_u32(&sh.pv_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort);
+            good = __all_sync(0xffffffffu, good);
+            sh.l[half][m] = l;
+            good = both(good);
             if (good) {
                 // The values to shared memory, in place of the tiles (whose
                 // products are done): 16-byte unit c of row m at c ^ (m % 8).
                 fence_after();
+                l += sh.l[half ^ 1][m];
                 const bool none = ref == -CUDART_INF_F;
                 const float w = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
-                for (int c = 0; c < D / 16; c += 4) {
-                    uint32_t v[4][16];
+#pragma unroll 1
+                for (int c = 0; c < DH / 16; c += 2) {
+                    uint32_t v[2][16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld16(lane_base + G::O_COL + 16 * (c + i), v[i]);
+                    for (int i = 0; i < 2; ++i) tmem_ld16(lane_base + G::O_COL + half * DH + 16 * (c + i), v[i]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) asm volatile("" : "+r"(v[i][4 * j + e]));
-                            float *dst = values + m * D + 4 * ((4 * (c + i) + j) ^ (m & 7));
+                            float *dst = values + m * D + 4 * ((half * (DH / 4) + 4 * (c + i) + j) ^ (m & 7));
                             *reinterpret_cast<float4 *>(dst) =
                                 make_float4(__uint_as_float(v[i][4 * j]) * w, __uint_as_float(v[i][4 * j + 1]) * w,
                                             __uint_as_float(v[i][4 * j + 2]) * w, __uint_as_float(v[i][4 * j + 3]) * w);
                         }
                 }
-                if (mine) {
+                if (mine && half == 0) {
                     if (!whole)
                         *reinterpret_cast<float2 *>(work.ml + (at * M + m) * 2) = make_float2(ref, l);
                     else if (a.lse)
@@ -546,6 +639,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             ok = good;
         }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
         if (!__syncthreads_and(ok)) {
             ok = false;
             break;
@@ -595,7 +689,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok && a.err) atomicOr(a.err, QSA_DEVERR_TIMEOUT);
         work.part[blockIdx.x] = ok ? part : Part{-1, 0, 0, 0};
     }
-    if (warp == 12) {
+    if (warp == PRODUCTS) {
         fence_after();
         tmem_dealloc(tmem, G::TMEM_COLS);
     }

@@ -93,16 +93,6 @@ using namespace tc;
 // fp16 operands (both K-major), fp32 accumulation.
 constexpr uint32_t IDESC = idesc_f16(TM, TN, false, false);
 
-// D (tensor memory) (+)= A (tensor memory, lane = row, two fp16 of K per
-// 32-bit column) x B (shared-memory descriptor).
-__device__ __forceinline__ void mma_f16_ts(uint32_t dtmem, uint32_t atmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t acc) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(dtmem),
-        "r"(atmem), "l"(bdesc), "r"(idesc), "r"(acc));
-}
-
 // --- kernels ----------------------------------------------------------------
 
 // qbar = sum over heads, split into fp16 hi/lo rows; rows >= ntok are zero.

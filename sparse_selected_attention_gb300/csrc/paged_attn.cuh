@@ -56,21 +56,33 @@ struct Work {
     }
 };
 
-// Groups: a maximal run of rows of q with one table row, within an aligned block
-// of `block` rows, is taken by paged_group.cu if it has GROUP_MIN rows or more.
-constexpr int GROUP_MIN = 3;
+// Groups: of a run of rows of q with one table row (within aligned spans of
+// group_span rows, which bound the search for its start), every `block` rows from
+// its start on are taken together by paged_group.cu if they are GROUP_MIN or
+// more.  A pass for a group costs what 3.4 to 3.8 rows cost one by one (12
+// sequences of 6 K cells, 48/4 heads of 256 and 32/8 of 128: 117 and 125 us for
+// three rows each, 103 and 100 us one by one; eight rows: 99 and 118 us against 238
+// and 241).
+constexpr int GROUP_MIN = 4;
 constexpr int GROUP_ROWS = 128;  // heads of a group, all its rows' (the M of its products)
 __host__ __device__ inline int group_block(int per) {
     int b = 1;
     while (2 * b * per <= GROUP_ROWS) b *= 2;
     return b;
 }
+__device__ __forceinline__ int group_span(int block) { return block > 64 ? block : 64; }
+// The first row of the group that row t would belong to.
+__device__ __forceinline__ int group_start(const int32_t *rows, int t, int block) {
+    const int row = __ldg(rows + t);
+    int s = t;
+    while ((s & (group_span(block) - 1)) && __ldg(rows + s - 1) == row) --s;
+    return s + ((t - s) & -block);
+}
 // Whether row t belongs to a group.
 __device__ __forceinline__ bool grouped(const qsa_paged_attn_args &a, int t, int block) {
-    const int row = __ldg(a.rows + t);
-    int n = 1;
-    for (int u = t; n < GROUP_MIN && (u & (block - 1)) && __ldg(a.rows + u - 1) == row; --u) ++n;
-    for (int u = t + 1; n < GROUP_MIN && u < a.n_tokens && (u & (block - 1)) && __ldg(a.rows + u) == row; ++u) ++n;
+    const int first = group_start(a.rows, t, block), end = min(a.n_tokens, first + block), row = __ldg(a.rows + t);
+    int n = t - first + 1;
+    for (int u = t + 1; n < GROUP_MIN && u < end && (u & (group_span(block) - 1)) && __ldg(a.rows + u) == row; ++u) ++n;
     return n >= GROUP_MIN;
 }
 

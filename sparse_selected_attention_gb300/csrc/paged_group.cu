@@ -37,7 +37,7 @@ constexpr int CONVERTERS = 256;  // threads that turn codes to halves
 constexpr int PRODUCTS = (SOFTMAX + CONVERTERS) / 32, LOADER = PRODUCTS + 1, WARPS = LOADER + 2;  // roles by warp, in this order
 constexpr int THREADS = 32 * WARPS;
 constexpr int STAGES = 2;        // tiles on their way
-constexpr int MIN_TILES = 6;     // of a share: a partial of 128 rows costs as much as some tiles
+constexpr int MIN_TILES = 2;     // of a share
 
 template <int S>
 struct GroupShape {
@@ -112,8 +112,8 @@ __device__ __forceinline__ uint32_t prod(uint32_t codes, __half2 f) {  // (1152 
 __device__ __forceinline__ Group group_at(const qsa_paged_attn_args &a, int t, int block, bool &bad) {
     const int lane = threadIdx.x & 31, row = __ldg(a.rows + t);
     Group g{0, 0x7fffffff, 0, 0};
-    if ((t & (block - 1)) && __ldg(a.rows + t - 1) == row) return g;
-    const int end = min(a.n_tokens, (t | (block - 1)) + 1);
+    if (group_start(a.rows, t, block) != t) return g;
+    const int end = min(min(a.n_tokens, t + block), (t | (group_span(block) - 1)) + 1);
     int n = 0, least = 0x7fffffff, most = 0;
     for (bool more = true; more && t + n < end;) {
         const int u = t + n + lane;
@@ -189,9 +189,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncthreads();
             Group g{0, 0x7fffffff, 0, 0};
-            if (tid >= CHUNK || t >= a.n_tokens || ((t & (block - 1)) && srow[tid - 1] == srow[tid])) return g;
-            const int end = min(min(a.n_tokens - base, CHUNK), (tid | (block - 1)) + 1), row = srow[tid];
+            if (tid >= CHUNK || t >= a.n_tokens) return g;
+            const int row = srow[tid], span = group_span(block);
             int u = tid;
+            while ((u & (span - 1)) && srow[u - 1] == row) --u;
+            if ((tid - u) & (block - 1)) return g;
+            const int end = min(min(a.n_tokens - base, tid + block), (tid | (span - 1)) + 1);
+            u = tid;
             for (; u < end && srow[u] == row; ++u) {
                 g.least = min(g.least, slen[u]);
                 g.most = max(g.most, slen[u]);

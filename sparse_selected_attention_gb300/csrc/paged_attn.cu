@@ -55,7 +55,9 @@ static_assert(MAX_CTAS <= MAX_PARTS, "the join's room");
 constexpr int TILE = 4096;      // a unit's K or V codes
 // Fewest units of a share, one per warp: finer ones would only add partials.
 constexpr int MIN_SHARE = NW;
-// Rows of up to this many units are not shared out.
+// Rows of up to this many units are not shared out: of 64 rows of 40 cells, 48/4
+// heads of 256, a share would take four, one after the other (23 us; 12 with a
+// row to a CTA).
 constexpr int WHOLE = 4 * NW;
 
 // S = head_dim / 128.
@@ -127,7 +129,7 @@ __device__ __forceinline__ int row_units(const qsa_paged_attn_args &a, int t, in
 }
 // Sums the rows' units and finds the row that holds unit share * range, of
 // `ranges` shares.
-// Each thread takes a run of rows.
+// Each thread takes a run of rows.  share 0: no row has more than WHOLE units.
 template <int S>
 __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int block, int &share) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -135,10 +137,12 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
     bool bad = false;
     long long mine = 0;
+    int most = 0;
     for (int t = t0; t < t1; ++t) {
         int row;
-        const int len = row_len(a, t, row, bad);
-        mine += row_units<S>(a, t, block, len);
+        const int len = row_len(a, t, row, bad), u = row_units<S>(a, t, block, len);
+        mine += u;
+        most = max(most, u);
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     long long s = mine;
@@ -148,7 +152,10 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
         if (lane >= o) s += u;
     }
     if (lane == 31) sh.scan[warp] = s;
-    __syncthreads();
+    if (!__syncthreads_or(most > WHOLE)) {
+        share = 0;
+        return;
+    }
     long long total = 0, before = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
@@ -455,20 +462,27 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     allow_dependent_launch();
     const int kvh = blockIdx.x % a.n_kv_heads, range = blockIdx.x / a.n_kv_heads, ranges = gridDim.x / a.n_kv_heads;
     const Work work(a.workspace, MAX_CTAS, per);
-    // This CTA's units: `left` of them from unit u0 of row t on, or with
-    // whole_rows every ranges-th row from row `range`.
+    // This CTA's units: `left` of them from unit u0 of row t on, or of whole
+    // rows every ranges-th from row `range`.
     int share = 0, t = range, u0 = 0, left = 0x7fffffff;
-    const int step = whole_rows ? ranges : 1;
-    if (!whole_rows) {
-        find_start<S>(a, sh, range, ranges, block, share);
+    if (!whole_rows) find_start<S>(a, sh, range, ranges, block, share);
+    const int step = share ? 1 : ranges;
+    bool none = false;
+    if (share) {
         const long long x = (long long)share * range, total = sh.total;
-        if (x >= total) {
-            if (tid == 0) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
-            return;
+        none = x >= total;
+        if (!none) {
+            left = (int)min((long long)share, total - x);
+            t = sh.row;
+            u0 = (int)(x - sh.before);
         }
-        left = (int)min((long long)share, total - x);
-        t = sh.row;
-        u0 = (int)(x - sh.before);
+    } else {
+        while (block && t < a.n_tokens && grouped(a, t, block)) t += step;
+        none = t >= a.n_tokens;
+    }
+    if (none) {
+        if (tid == 0 && !whole_rows) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
+        return;
     }
     bool bad = false, dead = false;
     uint32_t phase = 0;   // parity of each stage's next completion, one bit per stage

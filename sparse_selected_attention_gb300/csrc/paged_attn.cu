@@ -349,9 +349,9 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
         al[e] = ex2(st.m[e] - mn);
         st.m[e] = mn;
     }
-    // Weights: in fp32 for the sum, rounded to fp16 for the products (each by
-    // at most 2^-11 of itself).  pa[kk] is the A fragment of cells 16 kk on.
-    uint32_t pa[NK][4];
+    // Weights, in fp32: weight times V scale is rounded to fp16, once (by at
+    // most 2^-11 of itself).
+    float2 w[NJ][2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const float2 f = make_float2(sl2[e], sl2[e]), m = make_float2(-st.m[e], -st.m[e]);
@@ -361,7 +361,7 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
             float2 p = __ffma2_rn(s[j][e], f, m);
             p = make_float2(ex2(p.x), ex2(p.y));
             sum = __fadd2_rn(sum, p);
-            pa[j >> 1][2 * (j & 1) + e] = h2u(__floats2half2_rn(p.x, p.y));
+            w[j][e] = p;
         }
         st.l[e] = fmaf(st.l[e], al[e], sum.x + sum.y);
     }
@@ -388,7 +388,11 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
             st.o[i][3] *= al[1];
         }
     }
-    const __half2 vf = __float2half2_rn(exp2i(-max(st.v, -14)));
+    const float vf = exp2i(-max(st.v, -14));
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) w[j][e] = __fmul2_rn(w[j][e], make_float2(vf, vf));
 
     // This lane's row address of V's matrices: 128 dims, cells 0-31 by lane; or
     // cells 0-15 by lane % 16, lanes 16-31 sixteen dims on.
@@ -408,27 +412,32 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) {
             const uint4 &lo = vs[kk][0], &hi = vs[kk][1];
-            const uint32_t sel = (gr & 1) ? 0x7632u : 0x5410u;
-            const __half2 f02 = __hmul2(u2h(gr >> 1 ? tc::prmt(lo.y, hi.y, sel) : tc::prmt(lo.x, hi.x, sel)), vf);
-            const __half2 f13 = __hmul2(u2h(gr >> 1 ? tc::prmt(lo.w, hi.w, sel) : tc::prmt(lo.z, hi.z, sel)), vf);
-            p[kk] = make_uint4(h2u(__hmul2(u2h(pa[kk][0]), f02)), h2u(__hmul2(u2h(pa[kk][1]), f02)),
-                               h2u(__hmul2(u2h(pa[kk][2]), f13)), h2u(__hmul2(u2h(pa[kk][3]), f13)));
+            const uint32_t l0 = gr >> 1 ? lo.y : lo.x, l1 = gr >> 1 ? lo.w : lo.z;  // cells 4 r and on
+            const uint32_t h0 = gr >> 1 ? hi.y : hi.x, h1 = gr >> 1 ? hi.w : hi.z;
+            auto scale = [&](uint32_t x) { return (gr & 1) ? __high2float(u2h(x)) : __low2float(u2h(x)); };
+            const float2 f02 = make_float2(scale(l0), scale(h0)), f13 = make_float2(scale(l1), scale(h1));
+            auto scaled = [&](float2 x, float2 f) {
+                const float2 y = __fmul2_rn(x, f);
+                return h2u(__floats2half2_rn(y.x, y.y));
+            };
+            p[kk] = make_uint4(scaled(w[2 * kk][0], f02), scaled(w[2 * kk][1], f02), scaled(w[2 * kk + 1][0], f13),
+                               scaled(w[2 * kk + 1][1], f13));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            uint32_t w[4];
+            uint32_t v[4];
             if constexpr (S == 1) {  // 16 dims of both halves of the cells
                 const int c = 2 * gr + i;
-                load_v(w, vrow ^ (c << 4));
-                pv(st.o[2 * c], p[0], w[0]);
-                pv(st.o[2 * c + 1], p[0], w[1]);
-                pv(st.o[2 * c], p[NK - 1], w[2]);
-                pv(st.o[2 * c + 1], p[NK - 1], w[3]);
+                load_v(v, vrow ^ (c << 4));
+                pv(st.o[2 * c], p[0], v[0]);
+                pv(st.o[2 * c + 1], p[0], v[1]);
+                pv(st.o[2 * c], p[NK - 1], v[2]);
+                pv(st.o[2 * c + 1], p[NK - 1], v[3]);
             } else {  // 32 dims
                 const int c = 2 * (gr & 1) + i, t = 16 * (gr >> 1) + 4 * c;
-                load_v(w, (vrow ^ (c << 5)) + (gr >> 1) * UNIT * 128);
+                load_v(v, (vrow ^ (c << 5)) + (gr >> 1) * UNIT * 128);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pv(st.o[t + k], p[0], w[k]);
+                for (int k = 0; k < 4; ++k) pv(st.o[t + k], p[0], v[k]);
             }
         }
     }

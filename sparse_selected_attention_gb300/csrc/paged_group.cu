@@ -42,7 +42,7 @@ constexpr int MIN_TILES = 2;     // of a share
 template <int S>
 struct GroupShape {
     static constexpr int D = 128 * S;
-    static constexpr uint32_t TMEM_COLS = 512, Q_COL = 2 * N, O_COL = Q_COL + D / 2;  // S at 0 and N
+    static constexpr uint32_t TMEM_COLS = 512, Q_COL = 2 * N, O_COL = Q_COL + D / 2;  // S at 0 and N, P in its place
     static_assert(O_COL + D <= TMEM_COLS, "tensor memory");
     static constexpr uint32_t IDESC_S = idesc_f16(M, N, false, false), IDESC_O = idesc_f16(M, D, false, true);
 };
@@ -72,9 +72,8 @@ struct Group {
 // unit u of row r at u ^ (r % 8).
 template <int S>
 struct GroupSmem {
-    uint8_t k[2 * S][N * 128];  // per 64 dims; from here on also the values at the end of a segment, fp32 [M][D]
+    uint8_t k[2][2 * S][N * 128];  // high and low part, per 64 dims; from here on also the values at the end of a segment, fp32 [M][D]
     uint8_t v[2][2 * S][N * 128];
-    uint8_t p[2][M * 128];
     alignas(16) int8_t codes[STAGES][2][N * 128 * S];  // K's and V's as they come
     uint2 scales[STAGES][2][N];
     bool there[STAGES][N];
@@ -103,10 +102,6 @@ __device__ __forceinline__ __half2 scaled(uint2 sc, int i, int e) {
     const uint32_t w = i >> 1 ? sc.y : sc.x;
     const float f = __half2float(__ushort_as_half((unsigned short)(i & 1 ? w >> 16 : w & 0xFFFFu)));
     return __float2half2_rn(f * exp2i(e));
-}
-__device__ __forceinline__ uint32_t prod(uint32_t codes, __half2 f) {  // (1152 + code) pairs to code * f
-    const uint32_t off = 0x64806480u;
-    return h2u(__hmul2(__hsub2(u2h(codes), u2h(off)), f));
 }
 // Looked up by a warp.
 __device__ __forceinline__ Group group_at(const qsa_paged_attn_args &a, int t, int block, bool &bad) {
@@ -169,6 +164,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     wait_for_previous_grid();
     allow_dependent_launch();
     const Work work(ws, MAX_GROUP_PARTS, M);
+    // Results in fp16 take weights in two parts (22 bits); bf16's own rounding,
+    // 2^-9, hides one of 11 bits.
+    const bool fine = a.dtype == QSA_F16;
     bool bad = false;
 
     // The groups' tiles, and where this CTA's share of them starts: rows and
@@ -356,7 +354,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int fsub = (lane >> 2) % CELLS, fitem = (lane >> 2) / CELLS, fcell = (ct >> 5) * CELLS + fsub + fitem * STEP;
             auto convert = [&](int kind, int k, uint32_t mine) {  // of the k-th tile; mine: the lane's factor
                 const int st = k % STAGES;
-                uint8_t *dst = kind ? sh.v[k & 1][ch >> 2] : sh.k[ch >> 2];
+                uint8_t *dst = kind ? sh.v[k & 1][ch >> 2] : sh.k[0][ch >> 2];
 #pragma unroll
                 for (int j = 0; j < ITEMS; ++j) {
                     const int in = c0 + j * STEP, odd = ch >> 2 & 1;  // 64 dims apart, lanes write units of other banks
@@ -365,11 +363,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const uint32_t x[4] = {(odd ? w.z : w.x) ^ 0x80808080u, (odd ? w.w : w.y) ^ 0x80808080u,
                                            (odd ? w.x : w.z) ^ 0x80808080u, (odd ? w.y : w.w) ^ 0x80808080u};
 #pragma unroll
-                    for (int u = 0; u < 2; ++u)
-                        *reinterpret_cast<uint4 *>(dst + unit_off(in, 2 * (ch & 3) + (u ^ odd))) =
-                            make_uint4(prod(prmt(x[2 * u], 0x64646464u, 0x4140), f), prod(prmt(x[2 * u], 0x64646464u, 0x4342), f),
-                                       prod(prmt(x[2 * u + 1], 0x64646464u, 0x4140), f),
-                                       prod(prmt(x[2 * u + 1], 0x64646464u, 0x4342), f));
+                    for (int u = 0; u < 2; ++u) {
+                        const int at = unit_off(in, 2 * (ch & 3) + (u ^ odd));
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __half2 c = __hsub2(u2h(prmt(x[2 * u + e / 2], 0x64646464u, e & 1 ? 0x4342 : 0x4140)), u2h(0x64806480u));
+                            const __half2 h = __hmul2(c, f);
+                            hi[e] = h2u(h);
+                            lo[e] = h2u(__hfma2(c, f, __hneg2(h)));
+                        }
+                        *reinterpret_cast<uint4 *>(dst + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (kind == 0) *reinterpret_cast<uint4 *>(dst + at + (sh.k[1][0] - sh.k[0][0])) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
@@ -421,17 +427,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 good = good && __all_sync(0xffffffffu, mbar_wait_or_abort(smem_u32(&bar), phase & 1, abort));
             };
             // Descriptors differ in their address field (16-byte units) only.
-            const uint64_t dk = sw128_kmajor(smem_u32(sh.k[0])), dp = sw128_kmajor(smem_u32(sh.p[0]));
+            const uint64_t dk = sw128_kmajor(smem_u32(sh.k[0][0]));
             // V transposed: 64 dims apart N * 128 bytes, eight cells 1024.
             const uint64_t dv = smem_desc(smem_u32(sh.v[0][0]), N * 128, 1024, 2);
             auto issue_s = [&](int kk) {
                 wait(sh.k_full, kk);
+                // The buffer holds P kk - 2.
+                if (kk > 1) wait(sh.pv_full[kk & 1], (kk - 2) >> 1);
                 if (!good) return;
                 fence_after();
                 if (one) {
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_f16_ts(tmem + (kk & 1) * N, tmem + G::Q_COL + ks * 8, dk + (ks >> 2) * (N * 8) + (ks & 3) * 2,
+                    for (int ks = 0; ks < D / 8; ++ks)  // high parts, then low parts
+                        mma_f16_ts(tmem + (kk & 1) * N, tmem + G::Q_COL + ks % (D / 16) * 8, dk + (ks >> 2) * (N * 8) + (ks & 3) * 2,
                                    G::IDESC_S, ks ? 1u : 0u);
                     mma_commit(smem_u32(&sh.s_full[kk & 1]));
                 }
@@ -441,7 +449,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             wait(sh.q_full, segment);
             if (good) issue_s(k);
             for (int i = i0; i < i1 && good; ++i, ++k) {
-                // The buffer of S k + 1 was S k - 1's, whose P has come.
                 if (i + 1 < i1) issue_s(k + 1);
                 wait(sh.v_full[k & 1], k >> 1);
                 wait(sh.p_full[k & 1], k >> 1);
@@ -449,9 +456,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 fence_after();
                 if (one) {
 #pragma unroll
-                    for (int ks = 0; ks < N / 16; ++ks)
-                        mma_f16(tmem + G::O_COL, dp + (k & 1) * (M * 8) + ks * 2, dv + (k & 1) * (2 * S * N * 8) + ks * 16 * 8,
-                                G::IDESC_O, i > i0 || ks ? 1u : 0u);
+                    for (int ks = 0; ks < N / 8; ++ks) {  // high parts, then low parts
+                        if (ks == N / 16 && !fine) break;
+                        mma_f16_ts(tmem + G::O_COL, tmem + (k & 1) * N + ks * 8, dv + (k & 1) * (2 * S * N * 8) + ks % (N / 16) * 16 * 8,
+                                   G::IDESC_O, i > i0 || ks ? 1u : 0u);
+                    }
                     mma_commit(smem_u32(&sh.pv_full[k & 1]));
                 }
                 __syncwarp();
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 const float base = ref == -CUDART_INF_F ? 0.0f : -ref;
                 float2 sum = make_float2(0.0f, 0.0f);
-                uint32_t h[NH / 2];
+                uint32_t h[NH / 2], low[NH / 2];
 #pragma unroll
                 for (int c = 0; c < NH; c += 4) {
                     const float4 f = *reinterpret_cast<const float4 *>(vw + c);
@@ -586,20 +595,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                     p1 = make_float2(ex2(p1.x), ex2(p1.y));
                     sum = __ffma2_rn(p0, make_float2(f.x, f.y), sum);
                     sum = __ffma2_rn(p1, make_float2(f.z, f.w), sum);
-                    h[c / 2] = h2u(__floats2half2_rn(p0.x, p0.y));
-                    h[c / 2 + 1] = h2u(__floats2half2_rn(p1.x, p1.y));
+                    const __half2 h0 = __floats2half2_rn(p0.x, p0.y), h1 = __floats2half2_rn(p1.x, p1.y);
+                    h[c / 2] = h2u(h0);
+                    h[c / 2 + 1] = h2u(h1);
+                    if (fine) {
+                        low[c / 2] = h2u(__floats2half2_rn(p0.x - __low2float(h0), p0.y - __high2float(h0)));
+                        low[c / 2 + 1] = h2u(__floats2half2_rn(p1.x - __low2float(h1), p1.y - __high2float(h1)));
+                    }
                 }
                 l += sum.x + sum.y;
-                // P's buffer: the products with tile k - 2 must be done.
-                if (k > 1)
-                    good = __all_sync(0xffffffffu, good && mbar_wait_or_abort(smem_u32(&sh.pv_full[k & 1]), ((k - 2) >> 1) & 1, abort));
-                if (good) {
-#pragma unroll
-                    for (int u = 0; u < NH / 8; ++u)
-                        *reinterpret_cast<uint4 *>(sh.p[k & 1] + unit_off(m, half * (NH / 8) + u)) =
-                            make_uint4(h[4 * u], h[4 * u + 1], h[4 * u + 2], h[4 * u + 3]);
-                }
-                fence_async_smem();
+                // P in the place of S: both halves of its cells have been read.
+                tmem_st16(lane_base + (k & 1) * N + half * (NH / 2), h);
+                if (fine) tmem_st16(lane_base + (k & 1) * N + N / 2 + half * (NH / 2), low);
+                tmem_wait_st();
                 fence_before();
                 if (good) mbar_arrive(smem_u32(&sh.p_full[k & 1]));
             }

@@ -51,14 +51,10 @@ namespace {
 constexpr int NW = 4;           // warps per CTA
 constexpr int CTAS_PER_SM = 2;  // 255 registers a thread
 constexpr int MAX_CTAS = 152 * CTAS_PER_SM;
-static_assert(MAX_CTAS <= MAX_PARTS, "the join's room");
+static_assert(MAX_CTAS <= MAX_PARTS && WHOLE == 4 * NW, "shared with the join and the groups");
 constexpr int TILE = 4096;      // a unit's K or V codes
 // Fewest units of a share, one per warp: finer ones would only add partials.
 constexpr int MIN_SHARE = NW;
-// Rows of up to this many units are not shared out: of 64 rows of 40 cells, 48/4
-// heads of 256, a share would take four, one after the other (23 us; 12 with a
-// row to a CTA).
-constexpr int WHOLE = 4 * NW;
 
 // S = head_dim / 128.
 template <int S>
@@ -116,33 +112,36 @@ struct Smem {
     float m[NW][16], l[NW][16], f[NW][16];
     int v[NW];                                     // the warps' V exponents
     uint64_t bar[NW][2];
-    long long scan[NW];
+    long long together[NW], scan[NW];
     long long total, before;                       // units of all rows; of the rows before `row`
     int row;
 };
 
-// Units of a row: one at least, so that an empty row's output is written; none
-// for a row of a group (block 0: there are no groups).
-template <int S>
-__device__ __forceinline__ int row_units(const qsa_paged_attn_args &a, int t, int block, int len) {
-    return block && grouped(a, t, block) ? 0 : max((len + Shape<S>::UNIT - 1) / Shape<S>::UNIT, 1);
-}
 // Sums the rows' units and finds the row that holds unit share * range, of
 // `ranges` shares.
-// Each thread takes a run of rows.  share 0: no row has more than WHOLE units.
+// Each thread takes a run of rows.  share 0: no row has more than WHOLE units,
+// and each is taken whole (64 rows of 40 cells in a wide table, 48/4 heads of 256:
+// 12 us; 23 us where a share took four of them, one after the other).  False: the
+// rows are taken by groups (block 0: there are none).
 template <int S>
-__device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int block, int &share) {
+__device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int block, int &share) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (a.n_tokens + NW * 32 - 1) / (NW * 32);
     const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
     bool bad = false;
-    long long mine = 0;
+    long long mine = 0, together = 0;
     int most = 0;
     for (int t = t0; t < t1; ++t) {
         int row;
-        const int len = row_len(a, t, row, bad), u = row_units<S>(a, t, block, len);
+        const int u = units_of<S>(row_len(a, t, row, bad));
         mine += u;
         most = max(most, u);
+        if (block && group_start(a.rows, t, block) == t) {
+            int longest = u;
+            const int end = group_end(a, t, block), same = __ldg(a.rows + t);
+            for (int i = t + 1; i < end && __ldg(a.rows + i) == same; ++i) longest = max(longest, units_of<S>(row_len(a, i, row, bad)));
+            together += longest;
+        }
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     long long s = mine;
@@ -151,17 +150,24 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
         const long long u = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += u;
     }
-    if (lane == 31) sh.scan[warp] = s;
-    if (!__syncthreads_or(most > WHOLE)) {
-        share = 0;
-        return;
+    if (block) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) together += __shfl_xor_sync(0xffffffffu, together, o);
     }
-    long long total = 0, before = 0;
+    if (lane == 31) {
+        sh.scan[warp] = s;
+        sh.together[warp] = together;
+    }
+    share = 0;
+    if (!__syncthreads_or(most > WHOLE)) return true;
+    long long total = 0, before = 0, groups = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         if (w < warp) before += sh.scan[w];
         total += sh.scan[w];
+        groups += sh.together[w];
     }
+    if (block && take_groups(a, total, groups, true)) return false;
     before += s - mine;
     const long long per = (total + ranges - 1) / ranges;
     share = (int)max(per, (long long)MIN_SHARE);
@@ -169,7 +175,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     if (x0 >= before && x0 < before + mine) {
         for (int t = t0;; ++t) {
             int row;
-            const int len = row_len(a, t, row, bad), u = row_units<S>(a, t, block, len);
+            const int u = units_of<S>(row_len(a, t, row, bad));
             if (x0 < before + u) {
                 sh.row = t;
                 sh.before = before;
@@ -180,6 +186,7 @@ __device__ __forceinline__ void find_start(const qsa_paged_attn_args &a, Smem<S>
     }
     if (tid == 0) sh.total = total;
     __syncthreads();
+    return true;
 }
 
 // The query heads of (row t, KV head kvh) as A fragments in shared memory,
@@ -261,8 +268,13 @@ struct State {
     int v;  // values are in units of 2^v
 };
 
-// Folds one staged unit into the state.  vmask: the unit's valid cells.
-template <int S>
+// Folds one staged unit into the state.  vmask: the unit's valid cells.  Scores
+// are summed over K's codes, EXACT, or over 1152 + codes from -1152 sum q, with
+// sixteen times the rounding: of rows of one or two cells, whose scores are the
+// results' logarithms, 1.2e-6 of them.  Long rows average it (2e-7), and exact codes
+// cost them 2.6 to 7% (61 rows, 48/4 heads of 128: 200 us, 195 us; 90 rows of 18 K
+// cells, one head of 256: 171 us, 159 us); so EXACT goes with short tables.
+template <int S, bool EXACT>
 __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const uint2 *KS, const uint2 *VS, const uint4 (*q)[32],
                                              const float (*bias)[8][4], unsigned vmask, State<S> &st, const float (&sl2)[2]) {
     constexpr int NJ = Shape<S>::NJ, NK = Shape<S>::NK, UNIT = Shape<S>::UNIT;
@@ -270,6 +282,12 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     // Row 2 g of K with the swizzle of its first 16 bytes for this lane, and row 2 g + 1.
     const uint32_t kt = tc::smem_u32(K) + 2 * g * 128 + ((r & 1) << 3);
     const uint32_t keven = kt + (((r >> 1) ^ ((2 * g) & 7)) << 4), kodd = kt + 128 + (((r >> 1) ^ ((2 * g + 1) & 7)) << 4);
+
+    const __half2 off = u2h(0x64806480u);  // 1152
+    auto even = [&](uint32_t w) { return h2u(__hsub2(u2h(even_codes(w)), off)); };
+    auto odd = [&](uint32_t w) { return h2u(__hsub2(u2h(odd_codes(w)), off)); };
+    auto k_even = [&](uint32_t w) { return EXACT ? even(w) : even_codes(w); };
+    auto k_odd = [&](uint32_t w) { return EXACT ? odd(w) : odd_codes(w); };
 
     // Scores: per scale group S 32-dim blocks of two k-steps from -1152 sum q,
     // then the scale.
@@ -283,7 +301,7 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
         for (int i = 0; i < 2; ++i) ks[kk][i] = *reinterpret_cast<const uint4 *>(KS + 16 * kk + 4 * r + 2 * i);
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
-        const float4 c0 = *reinterpret_cast<const float4 *>(bias[gr][g]);
+        const float4 c0 = EXACT ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : *reinterpret_cast<const float4 *>(bias[gr][g]);
         float acc[NJ][4];
 #pragma unroll
         for (int bb = 0; bb < S; ++bb) {
@@ -297,10 +315,10 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
                              : "r"((((j & 1) ? kodd : keven) ^ (bh << 5)) + (j >> 1) * 16 * 128 + half * UNIT * 128)
                              : "memory");
                 if (bb == 0)
-                    mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), c0.x, c0.y, c0.z, c0.w);
+                    mma16816(acc[j], q0, k_even(w0), k_odd(w0), c0.x, c0.y, c0.z, c0.w);
                 else
-                    mma16816(acc[j], q0, even_codes(w0), odd_codes(w0), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                mma16816(acc[j], q1, even_codes(w1), odd_codes(w1), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                    mma16816(acc[j], q0, k_even(w0), k_odd(w0), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                mma16816(acc[j], q1, k_even(w1), k_odd(w1), acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
             }
         }
 #pragma unroll
@@ -402,9 +420,6 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
         for (int i = 0; i < 2; ++i) vs[kk][i] = *reinterpret_cast<const uint4 *>(VS + 16 * kk + 4 * r + 2 * i);
-    const __half2 off = u2h(0x64806480u);  // 1152
-    auto even = [&](uint32_t w) { return h2u(__hsub2(u2h(even_codes(w)), off)); };
-    auto odd = [&](uint32_t w) { return h2u(__hsub2(u2h(odd_codes(w)), off)); };
     auto pv = [&](float (&o)[4], const uint4 &p, uint32_t w) { mma16816(o, p, even(w), odd(w), o[0], o[1], o[2], o[3]); };
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
@@ -453,10 +468,11 @@ struct Feed {
     int page;                  // this lane's table entry for unit u
 };
 
-template <int S>
+// WHOLE_ROWS: no row is shared out.
+template <int S, bool WHOLE_ROWS>
 __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     paged_attn_kernel(const qsa_paged_attn_args a, const __grid_constant__ CUtensorMap kmap,
-                      const __grid_constant__ CUtensorMap vmap, int whole_rows, int block) {
+                      const __grid_constant__ CUtensorMap vmap, int block) {
     extern __shared__ __align__(1024) uint8_t raw[];
     Smem<S> &sh = *reinterpret_cast<Smem<S> *>(raw);
     constexpr int D = Shape<S>::D, UNIT = Shape<S>::UNIT;
@@ -474,9 +490,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     // This CTA's units: `left` of them from unit u0 of row t on, or of whole
     // rows every ranges-th from row `range`.
     int share = 0, t = range, u0 = 0, left = 0x7fffffff;
-    if (!whole_rows) find_start<S>(a, sh, range, ranges, block, share);
+    bool none = !WHOLE_ROWS && !find_start<S>(a, sh, range, ranges, block, share);
     const int step = share ? 1 : ranges;
-    bool none = false;
     if (share) {
         const long long x = (long long)share * range, total = sh.total;
         none = x >= total;
@@ -486,11 +501,10 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             u0 = (int)(x - sh.before);
         }
     } else {
-        while (block && t < a.n_tokens && grouped(a, t, block)) t += step;
-        none = t >= a.n_tokens;
+        none |= t >= a.n_tokens;
     }
     if (none) {
-        if (tid == 0 && !whole_rows) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
+        if (tid == 0 && !WHOLE_ROWS) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
         return;
     }
     bool bad = false, dead = false;
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     Feed f;
     f.t = t;
     f.len = row_len(a, t, f.trow, bad);
-    int nu = row_units<S>(a, t, block, f.len);
+    int nu = units_of<S>(f.len);
     f.end = min(nu, u0 + left);
     f.left = left - (f.end - u0);
     f.u = u0 + warp;
@@ -513,7 +527,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             f.t += step;
             f.len = f.next_len;
             f.trow = f.next_trow;
-            f.end = min(row_units<S>(a, f.t, block, f.len), f.left);
+            f.end = min(units_of<S>(f.len), f.left);
             f.left -= f.end;
             f.u = warp;
             peek();
@@ -618,7 +632,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
                 }
                 __syncwarp();
                 const uint8_t *k = sh.tile[warp][stage][0];
-                compute_unit<S>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q, sh.bias, vmask, st,
+                compute_unit<S, WHOLE_ROWS>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q, sh.bias, vmask, st,
                                 sl2);
             }
             __syncwarp();  // every lane has read the stage before it is filled again
@@ -631,8 +645,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
         }
         left -= n_units;
-        int next = t + step;
-        while (block && left > 0 && next < a.n_tokens && grouped(a, next, block)) next += step;
+        const int next = t + step;
         const bool more = left > 0 && next < a.n_tokens;
         if (more) q.load(a, next, kvh, per);
         __syncthreads();  // all warps are done with the query, and with the values of the segment before
@@ -725,7 +738,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
         t = next;
         u0 = 0;
         int trow;
-        nu = max((row_len(a, t, trow, bad) + UNIT - 1) / UNIT, 1);
+        nu = units_of<S>(row_len(a, t, trow, bad));
     }
     asm volatile("cp.async.wait_group 0;\n" ::);
     if (flying) {  // after a time-out: copies in flight land before this CTA's shared memory is given up
@@ -733,7 +746,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             if ((flying >> i) & 1u) tc::mbar_wait_bounded(tc::smem_u32(&sh.bar[warp][i]), (phase >> i) & 1u, tc::DRAIN_LIMIT);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
-    if (tid == 0 && !whole_rows) work.part[blockIdx.x] = part;
+    if (tid == 0 && !WHOLE_ROWS) work.part[blockIdx.x] = part;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
@@ -774,8 +787,6 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     cudaError_t e = encode<S>(kmap, a, a.kq);
     if (e == cudaSuccess) e = encode<S>(vmap, a, a.vq);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(paged_attn_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
-    if (e != cudaSuccess) return e;
     // A share per resident CTA.  Whole rows, and no join, where the table
     // cannot hold longer ones than WHOLE units, or where there are as many KV
     // heads as CTAs (then there may also be more CTAs than the workspace has
@@ -786,7 +797,9 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const long long most = whole ? a.n_tokens : (a.n_tokens * units + MIN_SHARE - 1) / MIN_SHARE;
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads, block = a.rows && !whole ? group_block(per) : 0;
-    e = launch_dependent(paged_attn_kernel<S>, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, whole ? 1 : 0, block);
+    const auto kernel = whole ? paged_attn_kernel<S, true> : paged_attn_kernel<S, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
+    if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, block);
     if (e != cudaSuccess || whole) return e;
     const Joined one{a.workspace, MAX_CTAS, per, grid};
     Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};

@@ -56,14 +56,32 @@ struct Work {
     }
 };
 
-// Groups: of a run of rows of q with one table row (within aligned spans of
-// group_span rows, which bound the search for its start), every `block` rows from
-// its start on are taken together by paged_group.cu if they are GROUP_MIN or
-// more.  A pass for a group costs what 3.4 to 3.8 rows cost one by one (12
-// sequences of 6 K cells, 48/4 heads of 256 and 32/8 of 128: 117 and 125 us for
-// three rows each, 103 and 100 us one by one; eight rows: 99 and 118 us against 238
-// and 241).
-constexpr int GROUP_MIN = 4;
+// Groups: every `block` rows, counted from its start, of a run of rows of q with
+// one table row (within aligned spans of group_span rows, which bound the search
+// for the start).  Either paged_group.cu takes all rows of a call, by groups, or
+// paged_attn.cu, one by one: one of them alone, as a few rows of a kind would
+// still cost its whole latency (14 groups of four rows and three rows more, 2 K
+// cells, 8/2 heads of 256: 59 us by both, 44 us one by one).  Both decide it from
+// the lengths.
+constexpr int WHOLE = 16;  // rows of up to this many units are not shared out
+template <int S>
+__device__ __forceinline__ int units_of(int len) {  // one at least, so that an empty row's output is written
+    constexpr int UNIT = 32 / S;
+    return max((len + UNIT - 1) / UNIT, 1);
+}
+// alone: units of all rows; together: of the longest row of each group; longer:
+// some row has more than WHOLE.  A group costs what 3 to 3.6 rows cost, and some
+// microseconds more for a few long tiles than for many small units: groups where
+// they save 4096 units of a KV head (33 MB of codes).  One by one and by groups, us:
+//   48/4 heads of 256, 12 sequences: 3 rows of 6 K cells 103, 100; 4 131, 101; 8 241, 113
+//                                    4 rows of 1 K cells 44, 48; 8 69, 58
+//                      1 sequence:   8 rows of 1 K cells 23, 30; of 6 K 42, 35
+//   32/8 heads of 128, 12 sequences: 3 rows of 6 K cells 99, 117; 4 127, 120; 8 236, 120
+//                                    4 rows of 1 K cells 40, 44; 8 62, 46
+//                      1 sequence:   8 rows of 1 K cells 22, 22; of 6 K 36, 28
+__device__ __forceinline__ bool take_groups(const qsa_paged_attn_args &a, long long alone, long long together, bool longer) {
+    return longer && (2 * alone - 7 * together) * a.n_kv_heads > 2 * 4096;
+}
 constexpr int GROUP_ROWS = 128;  // heads of a group, all its rows' (the M of its products)
 __host__ __device__ inline int group_block(int per) {
     int b = 1;
@@ -78,12 +96,9 @@ __device__ __forceinline__ int group_start(const int32_t *rows, int t, int block
     while ((s & (group_span(block) - 1)) && __ldg(rows + s - 1) == row) --s;
     return s + ((t - s) & -block);
 }
-// Whether row t belongs to a group.
-__device__ __forceinline__ bool grouped(const qsa_paged_attn_args &a, int t, int block) {
-    const int first = group_start(a.rows, t, block), end = min(a.n_tokens, first + block), row = __ldg(a.rows + t);
-    int n = t - first + 1;
-    for (int u = t + 1; n < GROUP_MIN && u < end && (u & (group_span(block) - 1)) && __ldg(a.rows + u) == row; ++u) ++n;
-    return n >= GROUP_MIN;
+// The row after the last one that the group of t, its first, could have.
+__device__ __forceinline__ int group_end(const qsa_paged_attn_args &a, int t, int block) {
+    return min(min(a.n_tokens, t + block), (t | (group_span(block) - 1)) + 1);
 }
 
 // Row t's length, cut to its range, and its table row (0 with length 0 if it

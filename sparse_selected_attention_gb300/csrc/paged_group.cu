@@ -81,7 +81,7 @@ struct GroupSmem {
     float top[2][2][M], l[2][M];         // the two halves' maxima (two buffers) and sums of a head row
     uint64_t full[2][STAGES], empty[2][STAGES];  // K's and V's codes
     uint64_t q_full, k_full, v_full[2], s_full[2], p_full[2], pv_full[2], drain;
-    long long scan[WARPS];
+    long long scan[3][WARPS];
     long long before;  // tiles before the group at t, in which the CTA's share starts
     int t;
     Group grp;
@@ -108,7 +108,7 @@ __device__ __forceinline__ Group group_at(const qsa_paged_attn_args &a, int t, i
     const int lane = threadIdx.x & 31, row = __ldg(a.rows + t);
     Group g{0, 0x7fffffff, 0, 0};
     if (group_start(a.rows, t, block) != t) return g;
-    const int end = min(min(a.n_tokens, t + block), (t | (group_span(block) - 1)) + 1);
+    const int end = group_end(a, t, block);
     int n = 0, least = 0x7fffffff, most = 0;
     for (bool more = true; more && t + n < end;) {
         const int u = t + n + lane;
@@ -124,7 +124,6 @@ __device__ __forceinline__ Group group_at(const qsa_paged_attn_args &a, int t, i
         n += k;
         more = k == 32;
     }
-    if (n < GROUP_MIN) return g;
     g.rows = n;
     g.least = __reduce_min_sync(0xffffffffu, least);
     g.most = __reduce_max_sync(0xffffffffu, most);
@@ -192,41 +191,61 @@ __global__ void __launch_bounds__(THREADS, 1)
             int u = tid;
             while ((u & (span - 1)) && srow[u - 1] == row) --u;
             if ((tid - u) & (block - 1)) return g;
-            const int end = min(min(a.n_tokens - base, tid + block), (tid | (span - 1)) + 1);
+            const int end = min(group_end(a, t, block) - base, CHUNK);
             u = tid;
             for (; u < end && srow[u] == row; ++u) {
                 g.least = min(g.least, slen[u]);
                 g.most = max(g.most, slen[u]);
             }
-            if (u - tid >= GROUP_MIN) g.rows = u - tid;
+            g.rows = u - tid;
             g.trow = row >= 0 && row < a.n_rows ? row : 0;
             return g;
         };
-        auto block_sum = [&](int v, long long &before) -> long long {  // of THREADS values, and of those before
-            long long sum = v;
+        // Sums over the block: of tiles, with those before the thread's, and of
+        // the rows' and the groups' units.
+        struct Sums {
+            long long tiles, alone, together;
+        };
+        auto block_sum = [&](Sums v, long long &before) -> Sums {
+            long long sum = v.tiles;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long u = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += u;
+                v.alone += __shfl_xor_sync(0xffffffffu, v.alone, o);
+                v.together += __shfl_xor_sync(0xffffffffu, v.together, o);
             }
-            if (lane == 31) sh.scan[warp] = sum;
+            if (lane == 31) {
+                sh.scan[0][warp] = sum;
+                sh.scan[1][warp] = v.alone;
+                sh.scan[2][warp] = v.together;
+            }
             __syncthreads();
-            long long total = 0;
-            before = sum - v;
+            Sums total{0, 0, 0};
+            before = sum - v.tiles;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
-                if (w < warp) before += sh.scan[w];
-                total += sh.scan[w];
+                if (w < warp) before += sh.scan[0][w];
+                total.tiles += sh.scan[0][w];
+                total.alone += sh.scan[1][w];
+                total.together += sh.scan[2][w];
             }
             __syncthreads();
             return total;
         };
-        long long total = 0, before = 0;
+        long long total = 0, before = 0, alone = 0, together = 0;
+        int longer = 0;
         Group g;
         for (int base = 0; base < a.n_tokens; base += CHUNK) {
             g = group_from(base);
-            total += block_sum(g.tiles(), before);
+            const int u = tid < CHUNK && base + tid < a.n_tokens ? units_of<S>(slen[tid]) : 0;
+            longer |= u > WHOLE;
+            const Sums sums = block_sum(Sums{g.tiles(), u, g.rows ? units_of<S>(g.most) : 0}, before);
+            total += sums.tiles;
+            alone += sums.alone;
+            together += sums.together;
         }
+        if (!take_groups(a, alone, together, __syncthreads_or(longer))) total = 0;  // paged_attn.cu takes the rows
         const long long each = total < 0x7fffffffll - MAX_GROUP_PARTS ? ((int)total + ranges - 1) / ranges : (total + ranges - 1) / ranges;
         share = (int)max(each, (long long)MIN_TILES);
         const long long x = (long long)share * range;
@@ -241,7 +260,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             long long sum = total;  // of one chunk, g and before are still at hand
             if (a.n_tokens > CHUNK) {
                 g = group_from(base);
-                sum = block_sum(g.tiles(), before);
+                sum = block_sum(Sums{g.tiles(), 0, 0}, before).tiles;
             }
             if (x >= done + before && x < done + before + g.tiles()) {
                 sh.t = base + tid;
@@ -689,7 +708,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         } while (tiles == 0);
     }
 
-    // Products issued before a time-out are complete before tensor memory is freed.
+    // After a time-out: copies on their way land before the block ends, and
+    // products issued are complete before tensor memory is freed.
+    if (warp >= LOADER && !ok) {
+        for (int j = max(k - STAGES, 0); j < k; ++j)
+            mbar_wait_bounded(smem_u32(&sh.full[warp - LOADER][j % STAGES]), (j / STAGES) & 1, DRAIN_LIMIT);
+    }
     if (issued) {
         mma_commit(smem_u32(&sh.drain));
         if (!mbar_wait_bounded(smem_u32(&sh.drain), 0, DRAIN_LIMIT)) ok = false;

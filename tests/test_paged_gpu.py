@@ -236,7 +236,7 @@ def shuffled_table(lens, page, extra, rng, wide=None):
     return table, max(pages, 1)
 
 
-def check_attn(q, pool, table, lens, rows=None, scale=None, gate=None, otype=F16, lse=True, ws=None, what="", grouped=False):
+def check_attn(q, pool, table, lens, rows=None, scale=None, gate=None, otype=F16, lse=True, ws=None, what=""):
     """q float64 [T, H, D]; returns the output tensor and the error word."""
     T, H, D = q.shape
     hkv = pool[0].shape[2]
@@ -250,7 +250,7 @@ def check_attn(q, pool, table, lens, rows=None, scale=None, gate=None, otype=F16
                        softmax_scale=scale, gate=None if gate is None else dev(gate), lse=ls, err=err)
     torch.cuda.synchronize()
     ref, rlse, mag, flush, qk = po.attn(host(qd), *pool, table, lens, rows, scale, gate)
-    ds = 1152 * qk * 2.0 ** -21 + (127 * qk * 2.0 ** -11 if grouped else 0.0)
+    ds = 1152 * qk * 2.0 ** -21
     tol = HALF[otype] * np.abs(ref) + mag * (2.0 ** -10 + 2 * np.expm1(ds)[..., None] + 2.0 ** -16) + flush * 2.0 ** -24 + TINY[otype]
     got = host(out)
     bad = ~(np.abs(got - ref) <= tol)
@@ -305,7 +305,7 @@ def test_attn_draft_window_shares_a_sequence(cuda_device):
     lens = [base + 1 + i for i in range(8)] + [50, 99, 0]
     q = rng.standard_normal((11, 24, 256))
     gate = wl.gates_f32(11, seed=3, heads=24, head_dim=256)
-    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=BF16, grouped=True)
+    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=BF16)
     assert err == 0
 
 
@@ -327,7 +327,7 @@ def test_attn_groups(cuda_device, d, hq, hkv, page, window, base):
     q = rng.standard_normal((len(rows), hq, d)) * 1.5
     otype = F16 if hkv % 2 else BF16
     gate = wl.gates_f32(len(rows), seed=4, heads=hq, head_dim=d) if hkv == 2 else None
-    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=otype, grouped=True)
+    _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=otype)
     assert err == 0
 
 
@@ -344,13 +344,13 @@ def test_attn_group_lengths_and_scales(cuda_device):
     lens = [1000, 0, 3, 129, 64, 999, 65, 0, 64, 1, 63, 33]
     q = rng.standard_normal((12, 24, 128))
     for scale in (None, -0.03, 0.0):
-        out, err = check_attn(q, pool, table, lens, rows=rows, scale=scale, otype=BF16, grouped=True)
+        out, err = check_attn(q, pool, table, lens, rows=rows, scale=scale, otype=BF16)
         assert err == 0 and not out[1].any() and not out[7].any()
-    check_attn(q * 1e8, pool, table, lens, rows=rows, scale=1e-10, otype=BF16, grouped=True)
+    check_attn(q * 1e8, pool, table, lens, rows=rows, scale=1e-10, otype=BF16)
     table[0, 3], table[1, 1] = -4, pages
-    _, err = check_attn(q, pool, table, lens, rows=rows, grouped=True)
+    _, err = check_attn(q, pool, table, lens, rows=rows)
     assert err == qsa.QSA_DEVERR_BAD_ID
-    out, err = check_attn(q, pool, table, lens, rows=[9] * 12, grouped=True)
+    out, err = check_attn(q, pool, table, lens, rows=[9] * 12)
     assert err == qsa.QSA_DEVERR_BAD_ID and not out.any()
 
 
@@ -364,8 +364,94 @@ def test_attn_many_groups(cuda_device):
         rows = [s for s in range(seqs) for _ in range(window)]
         lens = [held[s] - window + 1 + i for s in range(seqs) for i in range(window)]
         q = rng.standard_normal((len(rows), 4, 128)) * 2
-        _, err = check_attn(q, pool, table, lens, rows=rows, grouped=True)
+        _, err = check_attn(q, pool, table, lens, rows=rows)
         assert err == 0
+
+
+def taken_together(rows, lens, hq, hkv, d):
+    """Whether the call's rows are taken by groups: the units of 32 (of 256
+    dims 16) cells that rows alone and the longest of each group have."""
+    unit, block = 32 if d == 128 else 16, 1
+    while 2 * block * (hq // hkv) <= 128:
+        block *= 2
+    units = [max(-(-n // unit), 1) for n in lens]
+    together, start = 0, 0
+    for t in range(len(rows)):
+        if t % max(block, 64) == 0 or rows[t] != rows[t - 1]:
+            start = t
+        if (t - start) % block == 0:
+            end = t
+            while end < len(rows) and end - t < block and rows[end] == rows[t] and (end == t or end % max(block, 64)):
+                end += 1
+            together += max(units[t:end])
+    return max(units) > 16 and (2 * sum(units) - 7 * together) * hkv > 8192
+
+
+@pytest.mark.parametrize("d,hq,hkv,page,windows,cells", [
+    (128, 8, 8, 64, [128], 600), (128, 12, 1, 64, [8], 30001), (256, 24, 2, 16, [8, 8, 1], 7900), (256, 16, 1, 256, [40], 2950),
+    (128, 32, 8, 32, [4, 5, 7, 1, 8, 2, 6, 9, 5, 4, 3, 6], 2000), (256, 6, 3, 64, [67], 700), (128, 15, 3, 128, [90, 1, 30], 1300),
+    (256, 8, 8, 32, [300, 210], 290), (128, 2, 2, 16, [512, 188], 1030)])
+def test_attn_rows_taken_together(cuda_device, d, hq, hkv, page, windows, cells):
+    """Windows of consecutive tokens of sequences, long enough to be taken by
+    groups: groups cut by a block, by a span and by the rows' end, heads that do
+    not fill a tile, shares that end inside a group; empty outputs' neighbours."""
+    rng = np.random.default_rng(len(windows) + d)
+    held = [cells - 3 * i for i in range(len(windows))]
+    table, pages = shuffled_table(held, page, 2, rng)
+    pool = make_pool(pages, page, hkv, d, seed=27)
+    rows = [s for s, n in enumerate(windows) for _ in range(n)]
+    lens = [max(held[s] - n + 1 + i, 0) for s, n in enumerate(windows) for i in range(n)]
+    assert taken_together(rows, lens, hq, hkv, d)
+    q = rng.standard_normal((len(rows), hq, d)) * 1.5
+    gate = wl.gates_f32(len(rows), seed=5, heads=hq, head_dim=d) if hkv == 2 else None
+    for otype in (F16, BF16):
+        _, err = check_attn(q, pool, table, lens, rows=rows, gate=gate, otype=otype)
+        assert err == 0
+
+
+def test_attn_together_lengths_and_scales(cuda_device):
+    """Rows taken together with any order of lengths, empty ones among them;
+    wide K and V scales, zero ones, a negative softmax scale; missing pages."""
+    rng = np.random.default_rng(28)
+    table, pages = shuffled_table([700, 64], 32, 2, rng)
+    pool = make_pool(pages, 32, 8, 128, seed=29)
+    for i in (2, 3):
+        pool[i] = np.exp(wl.uniform(30 + i, 1, pool[i].shape, math.log(1e-5), math.log(0.5 if i == 2 else 100.0))).astype(np.float16)
+        pool[i][::3, ::2] = 0
+    rows = [0] * 128 + [1] * 5
+    lens = [int(n) for n in rng.integers(0, 701, 128)] + [64, 1, 63, 33, 0]
+    lens[:9] = [700, 0, 3, 129, 64, 699, 65, 0, 1]
+    assert taken_together(rows, lens, 8, 8, 128)
+    q = rng.standard_normal((133, 8, 128))
+    for otype in (F16, BF16):
+        for scale in (None, -0.03, 0.0):
+            out, err = check_attn(q, pool, table, lens, rows=rows, scale=scale, otype=otype)
+            assert err == 0 and not out[1].any() and not out[7].any() and not out[132].any()
+    check_attn(q * 1e8, pool, table, lens, rows=rows, scale=1e-10, otype=BF16)
+    table[0, 3], table[1, 1] = -4, pages
+    _, err = check_attn(q, pool, table, lens, rows=rows)
+    assert err == qsa.QSA_DEVERR_BAD_ID
+
+
+def test_attn_together_repeats_its_bits(cuda_device):
+    """The same call twice, and captured and replayed, gives the same bits."""
+    rng = np.random.default_rng(31)
+    table, pages = shuffled_table([900], 64, 1, rng)
+    pd = [dev(x) for x in make_pool(pages, 64, 8, 128, seed=32)]
+    q = dev(rng.standard_normal((100, 8, 128)).astype(np.float16))
+    lens, rows = i32(list(range(801, 901))), i32([0] * 100)
+    ws = torch.empty(qsa.qsa_paged_attn_workspace_bytes(8, 8, 128), dtype=torch.uint8, device="cuda")
+    out = [torch.empty_like(q) for _ in range(3)]
+    for o in out[:2]:
+        qsa.qsa_paged_attn(q, *pd, dev(table), lens, o, ws, rows=rows)
+    td, g, s = dev(table), torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=s):
+        qsa.qsa_paged_attn(q, *pd, td, lens, out[2], ws, rows=rows)
+    for _ in range(2):
+        out[2].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 1.0, 1e-30])

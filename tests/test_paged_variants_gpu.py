@@ -90,4 +90,36 @@ def test_attn_time_out(cuda_device, use_library, monkeypatch, d, page, rows):
     torch.cuda.synchronize()
     assert int(err.item()) == qsa.QSA_DEVERR_TIMEOUT
     monkeypatch.undo()
-    check_attn(q, pool, table, lens, rows=rows, grouped=rows is not None)
+    check_attn(q, pool, table, lens, rows=rows)
+
+
+def together(d):
+    """Rows of one sequence that are taken by groups, few cells for many heads."""
+    rng = np.random.default_rng(6)
+    lens = [560 + i for i in range(64)]
+    table, pages = shuffled_table(lens[-1:], 32, 1, rng)
+    return rng.standard_normal((64, 16, d)), make_pool(pages, 32, 8, d, seed=42), table, lens, [0] * 64
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_check_build_rows_taken_together(cuda_device, use_library, d):
+    q, pool, table, lens, rows = together(d)
+    plain, _ = check_attn(q, pool, table, lens, rows=rows)
+    L = use_library("check")
+    word(L)
+    checked, _ = check_attn(q, pool, table, lens, rows=rows)
+    assert word(L) == 0 and torch.equal(plain, checked)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_time_out_of_rows_taken_together(cuda_device, use_library, monkeypatch, d):
+    q, pool, table, lens, rows = together(d)
+    use_library("wait0")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.zeros(64, 16, d, dtype=F16, device="cuda")
+    ws = torch.empty(qsa.qsa_paged_attn_workspace_bytes(16, 8, d), dtype=torch.uint8, device="cuda")
+    qsa.qsa_paged_attn(dev(q.astype(np.float16)), *[dev(x) for x in pool], dev(table), i32(lens), out, ws, err=err, rows=i32(rows))
+    torch.cuda.synchronize()
+    assert int(err.item()) == qsa.QSA_DEVERR_TIMEOUT
+    monkeypatch.undo()
+    check_attn(q, pool, table, lens, rows=rows)

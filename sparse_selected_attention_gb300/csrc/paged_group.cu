@@ -168,11 +168,69 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool fine = a.dtype == QSA_F16;
     bool bad = false;
 
-    // The groups' tiles, and where this CTA's share of them starts: rows and
-    // lengths go to shared memory a chunk of whole blocks at a time, and the
-    // thread of a row in which a group starts adds it up there.
-    int share, left;
-    {
+    // The groups' tiles, and the group in which this CTA's share of them starts.
+    int share = 0, left = 0, t = 0;
+    long long tiles_before = 0;
+    Group grp{0, 0, 0, 0};
+    auto take_share = [&](long long total) {  // false: nothing to do, the same in all threads
+        const long long each = total < 0x7fffffffll - MAX_GROUP_PARTS ? ((int)total + ranges - 1) / ranges : (total + ranges - 1) / ranges;
+        share = (int)max(each, (long long)MIN_TILES);
+        const long long x = (long long)share * range;
+        left = (int)max(min((long long)share, total - x), 0ll);
+        return left > 0;
+    };
+    bool any;
+    if (a.n_tokens <= 32) {
+        // Few rows: each warp works it out for itself, a lane per row (2 us
+        // less than by the block).
+        const bool in = lane < a.n_tokens;
+        int row = -1, len = 0, trow = 0;
+        if (in) {
+            row = __ldg(a.rows + lane);
+            len = row_len(a, lane, trow, bad);
+        }
+        const int prev = __shfl_up_sync(0xffffffffu, row, 1);
+        const unsigned upto = 0xffffffffu >> (31 - lane), runs = __ballot_sync(0xffffffffu, in && (lane == 0 || prev != row));
+        const int run = 31 - __clz(runs & upto);  // where the lane's starts
+        const bool starts = in && ((lane - run) & (block - 1)) == 0;
+        const unsigned groups = __ballot_sync(0xffffffffu, starts), after = groups & ~upto;
+        const int id = __popc(groups & upto);
+        Group g{(after ? __ffs(after) - 1 : a.n_tokens) - lane, len, len, trow};
+        struct {
+            long long tiles, alone, together;
+        } v{0, in ? units_of<S>(len) : 0, 0};
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {  // over the rest of the lane's group
+            const int least = __shfl_down_sync(0xffffffffu, g.least, o), most = __shfl_down_sync(0xffffffffu, g.most, o);
+            const int other = __shfl_down_sync(0xffffffffu, id, o);
+            if (lane + o < a.n_tokens && other == id) {
+                g.least = min(g.least, least);
+                g.most = max(g.most, most);
+            }
+        }
+        if (starts) {
+            v.tiles = g.tiles();
+            v.together = units_of<S>(g.most);
+        }
+        const bool longer = __any_sync(0xffffffffu, v.alone > WHOLE);
+        long long sum = v.tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+            v.alone += __shfl_xor_sync(0xffffffffu, v.alone, o);
+            v.together += __shfl_xor_sync(0xffffffffu, v.together, o);
+        }
+        any = take_groups(a, v.alone, v.together, longer) && take_share(__shfl_sync(0xffffffffu, sum, 31));
+        const long long x = (long long)share * range;
+        const unsigned here = __ballot_sync(0xffffffffu, any && starts && x >= sum - v.tiles && x < sum);
+        t = here ? __ffs(here) - 1 : 0;
+        tiles_before = __shfl_sync(0xffffffffu, sum - v.tiles, t);
+        grp = Group{__shfl_sync(0xffffffffu, g.rows, t), __shfl_sync(0xffffffffu, g.least, t), __shfl_sync(0xffffffffu, g.most, t),
+                    __shfl_sync(0xffffffffu, g.trow, t)};
+    } else {
+        // Rows and lengths go to shared memory a chunk of whole spans at a
+        // time, and the thread of a row in which a group starts adds it up there.
         constexpr int CHUNK = 512;  // a multiple of any block
         static_assert(CHUNK <= THREADS && CHUNK % M == 0, "a thread per row");
         int *srow = reinterpret_cast<int *>(sh.k), *slen = srow + CHUNK;
@@ -245,18 +303,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             alone += sums.alone;
             together += sums.together;
         }
-        if (!take_groups(a, alone, together, __syncthreads_or(longer))) total = 0;  // paged_attn.cu takes the rows
-        const long long each = total < 0x7fffffffll - MAX_GROUP_PARTS ? ((int)total + ranges - 1) / ranges : (total + ranges - 1) / ranges;
-        share = (int)max(each, (long long)MIN_TILES);
+        any = take_groups(a, alone, together, __syncthreads_or(longer)) && take_share(total);
         const long long x = (long long)share * range;
-        left = (int)max(min((long long)share, total - x), 0ll);
-        if (left == 0) {  // the same in all threads
-            if (tid == 0) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
-            if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
-            return;
-        }
         long long done = 0;
-        for (int base = 0; base < a.n_tokens; base += CHUNK) {
+        for (int base = 0; any && base < a.n_tokens; base += CHUNK) {
             long long sum = total;  // of one chunk, g and before are still at hand
             if (a.n_tokens > CHUNK) {
                 g = group_from(base);
@@ -271,15 +321,23 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (x < done) break;
         }
     }
+    if (!any) {  // the same in all threads; also where paged_attn.cu takes the rows
+        if (tid == 0) work.part[blockIdx.x] = Part{-1, 0, 0, 0};
+        if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+        return;
+    }
     if (warp == PRODUCTS) tmem_alloc(smem_u32(&sh.tmem), G::TMEM_COLS);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem;
-    int t = sh.t;
-    Group grp = sh.grp;
+    if (a.n_tokens > 32) {
+        t = sh.t;
+        tiles_before = sh.before;
+        grp = sh.grp;
+    }
     int tokens = grp.rows, tiles = grp.tiles();
-    int i0 = (int)((long long)share * range - sh.before);
+    int i0 = (int)((long long)share * range - tiles_before);
     Part part{-1, 0, 0, 0};
     int k = 0;  // tiles done: the barriers' phases
     bool ok = true, issued = false;  // issued: products, by this thread

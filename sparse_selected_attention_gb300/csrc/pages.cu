@@ -26,10 +26,14 @@ constexpr int CLUSTER = 8;
 constexpr int THREADS = 1024;
 constexpr int SEG = 128;  // table columns a warp takes at a time
 
-// One block up to this many pages (128 KB of counts) and table entries.  A
-// decode step of 64 rows over 1700 pages: one block X_ONE us, cluster X_CLU.
-constexpr int SMALL_PAGES = 32768;
-constexpr long long SMALL_ENTRIES = 65536;
+// One block up to this many pages (32 KB of counts) and table entries.  One block
+// and a cluster, us, of an update by a token a row and of a compaction:
+//   table 64 x 27, pool of 1700 pages: 8.0, 11.5; 9.4, 13.0
+//   table 64 x 64, pool of 4096:       8.8, 12.3; 11.5, 15.5
+//   table 256 x 64, pool of 16384:     14.2, 14.3; 32.2, 24.7
+//   table 1024 x 64, pool of 32768:    33.2, 19.8; 68.1, 29.7
+constexpr int SMALL_PAGES = 8192;
+constexpr long long SMALL_ENTRIES = 16384;
 
 // One page copy: the first `cells` cells of page src go to page dst.
 struct Copy {

@@ -396,7 +396,8 @@ typedef struct {
  * qsa_paged_attn -- attention of one new token per row of q over a whole
  * paged sequence.  Row t attends to cells 0 .. seq_lens[t]-1 of table row
  * rows[t] (rows NULL: table row t); several rows of q may read one sequence,
- * each with its own length.  Query head h reads KV head h / (n_q_heads /
+ * each with its own length (consecutive ones are read together where that
+ * saves time: tokens of a draft window or of a chunk).  Query head h reads KV head h / (n_q_heads /
  * n_kv_heads):
  *   s_c = softmax_scale * sum_g ksc[c,g] * sum_{d in g} q[t,h,d] * kq[c,d]
  *   w_c = exp(s_c - max s);  O = sum w_c v_c / sum w_c,  v_c = vsc * vq
@@ -414,9 +415,9 @@ typedef struct {
  * qsa_paged_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim) bytes,
  * 256-byte aligned, overwritten; two calls that share one must not run
  * concurrently (graphs that replay on different streams need one each).
- * The work is divided over the cached cells of all rows, so results do not
- * depend on max_pages but their last bits may depend on the other rows'
- * lengths.  Range: scores and sums are fp32; K scales of any fp16 value, V
+ * The work is divided over the cached cells of all rows, so the last bits of
+ * a row's results may depend on the other rows' lengths and on max_pages; the
+ * same call gives the same bits.  Range: scores and sums are fp32; K scales of any fp16 value, V
  * scales below 2^15.
  * Supported: n_q_heads a multiple of n_kv_heads, 1..16 query heads per KV
  * head.  q, out, kq, vq 16-byte aligned; ksc, vsc, gate 8-byte; the rest 4-byte.

@@ -1,29 +1,37 @@
 // qsa_paged_attn, rows that read one sequence together: the consecutive tokens
-// of a draft window, each with its own length.
+// of a draft window or of a chunk, each with its own length.
 //
 // Their heads, up to 128, are the M side of tcgen05 products over one pass of
 // the cache, so a cell's codes are read and converted once for all of them.
-// (Eight tokens x 12 heads over 30 K cells of 2 x 256 dims: row by row the
-// cache would be read, and its 2 x 15 M codes converted, eight times.)
+// (Eight tokens x 12 heads over 30 K cells of 2 x 256 dims, with the join:
+// 38 us; row by row, where the cache comes eight times from L2 and its 2 x 15 M
+// codes are converted eight times, 61 us.)
 //
-// A CTA takes tiles of 64 cells.  Warps 4-7 load a tile's K and warps 8-11 its
-// V (the next tile's loads are in flight meanwhile), convert the codes to fp16
-// and write them to shared memory as [64 cells][D], 64 dims to a 128-byte row
-// with the swizzle: K-major for S = Q K^T (128 x 64), and read transposed
-// (N-major) for O += P V (128 x D).  One thread of warp 12 issues the products.
-// Warps 0-3, a thread per head row, take S from tensor memory, do the softmax
-// and write P as fp16 to shared memory.  The roles hand tiles over by
-// mbarriers (warp 13 provides the cells' factors): S has two buffers, so the softmax of tile i runs beside the
-// conversions of K i + 1 and V i.  Tiles are shared out over the chip and joined
-// as in paged_attn.cu.  A tile is bound by the roles' latency, not by its
-// 2 x 128 x 64 x 256 products.
+// A CTA takes tiles of 64 cells; its warps have roles, which hand tiles over by
+// mbarriers:
+//   softmax (8 warps, two threads per head row, 32 cells each): the queries to
+//   tensor memory, then of each tile S from there, and the weights P back in
+//   its place, fp16, as the A operand of the next product;
+//   converters (8): codes to fp16 in shared memory, [64 cells][D], 64 dims to a
+//   128-byte row with the swizzle: K-major for S = Q K^T (128 x 64), read
+//   transposed (N-major) for O += P V (128 x D).  K is a tile ahead of V;
+//   products (1 warp, one thread issues);
+//   loads (1 warp each for K and V, up to two tiles ahead).
+// Tiles are shared out over the chip and joined as in paged_attn.cu.  A tile
+// takes 3.8 K cycles of the chain K converted - S - K converted, of which the
+// 32 products of S are 1.7 K; issue slots are used to a third and the tensor
+// pipe to a fifth, so the rest is the roles' latency.  (Dropped, each without
+// gain: K converted by halves of the dims beside the other half's products; TMA
+// boxes in place of cp.async; two warps each for the loads.  A bulk copy per
+// cell, 256 bytes each, took 70 cycles a copy: 53 us where cp.async took 35.)
 //
 // Scales.  K's are multiplied into the codes under a power of two per cell,
 // 2^ek, that the softmax undoes (codes x scales then use fp16's range whatever
-// the scales are); V's under 2^ev, so that a cell's largest scale is in [1, 2).
-// The softmax works on s - ev: P = 2^(s - ev - m) is the weight of the scaled
-// values, its running maximum m is one of weight x value, and the denominator
-// adds P 2^ev.
+// the scales are), in two fp16 parts that hold the 19-bit product exactly (one
+// part alone, each product off by up to 2^-11 of itself: 36 us).  V's are multiplied in under 2^ev, so that a cell's largest
+// scale is in [1, 2), and rounded to fp16.  The softmax works on s - ev: P =
+// 2^(s - ev - m) is the weight of the scaled values, its running maximum m is
+// one of weight x value, and the denominator adds P 2^ev, in fp32.
 #include "paged_attn.cuh"
 
 namespace qsa {
@@ -37,7 +45,9 @@ constexpr int CONVERTERS = 256;  // threads that turn codes to halves
 constexpr int PRODUCTS = (SOFTMAX + CONVERTERS) / 32, LOADER = PRODUCTS + 1, WARPS = LOADER + 2;  // roles by warp, in this order
 constexpr int THREADS = 32 * WARPS;
 constexpr int STAGES = 2;        // tiles on their way
-constexpr int MIN_TILES = 2;     // of a share
+// Of a share.  Eight rows of 2 K cells, 8/2 heads of 256: 20.5 us; shares of four
+// 23.1, of six 26.3.
+constexpr int MIN_TILES = 2;
 
 template <int S>
 struct GroupShape {
@@ -354,18 +364,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             return (size_t)(t + i) * a.n_q_heads + (size_t)kvh * per + (m - i * per);
         };
         const int trow = grp.trow, least = grp.least, most = grp.most;
-
-        const int32_t *tab = a.page_table + (size_t)trow * a.max_pages;
-        auto page_of = [&](int i) {  // of cells 2 lane and 2 lane + 1 of tile i
-            const int j = (i * N + 2 * lane) >> page_shift;
-            return i < i1 && j < a.max_pages ? __ldg(tab + j) : -1;
-        };
-        auto cell_row = [&](int c, int page) -> long long {  // of the pool's (cell, KV head) rows; -1: none
-            const bool have = c < most && page >= 0 && page < a.n_pages;
-            bad |= c < most && !have;
-            const long long row = ((((long long)page << page_shift) + (c & (a.page_size - 1))) * a.n_kv_heads) + kvh;
-            return have && QSA_IN(row, (long long)a.n_pages * a.page_size * a.n_kv_heads) ? row : -1;
-        };
 
         constexpr int CH = D / 16;  // items of sixteen codes of a cell
         if (warp >= LOADER) {

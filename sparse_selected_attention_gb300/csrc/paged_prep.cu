@@ -7,6 +7,10 @@
 // run of one token's rows (query heads, then key, then value heads), two at a
 // time with the next two on their way, and keeps the token's cosines and sines
 // in registers.  Few tokens are split over more warps, down to two rows each.
+// 1984 tokens of 12/1 heads of 128, with their gather: 7.0 us; 8191 of 24/2 heads of
+// 256, 230 MB with their gather: 50 us, 4.6 TB/s, with 57% of the issue slots
+// used.  (Rows fetched into L2 ahead, or fewer warps with more registers: 52 and
+// 53 us.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -302,7 +306,8 @@ __global__ void __launch_bounds__(PREP_WARPS * 32, 7) paged_prep_kernel(const qs
 // per (cell, KV head).  A thread takes sixteen dims of one (cell, KV head), of
 // both K and V, so that a warp reads and writes whole rows.  A block takes
 // ids_per_block whole ids, so that an item's id and place need 32-bit
-// arithmetic only.
+// arithmetic only.  240 K cells of 2 heads of 256 to bf16, 744 MB: 125 us, 5.95
+// TB/s.
 constexpr int GATHER_THREADS = 256;
 
 struct GatherPlan {

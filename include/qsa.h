@@ -313,6 +313,7 @@ qsa_status qsa_attn(const qsa_attn_args *args, void *stream);
  * holds are free.
  * Supported: (head_dim 128, group 32) or (head_dim 256, group 64);
  * page_size 16, 32, 64, 128 or 256; n_pages * page_size below 2^31.
+ * Outputs overlap neither each other nor the inputs, but where a call says so.
  * The page calls keep the whole state in the caller's device buffers and never
  * synchronise, so a decode loop (update, prep, attention) can be captured in a
  * graph.  The pages have no counterpart to these calls; they extend the path
@@ -397,8 +398,8 @@ typedef struct {
  * paged sequence.  Row t attends to cells 0 .. seq_lens[t]-1 of table row
  * rows[t] (rows NULL: table row t); several rows of q may read one sequence,
  * each with its own length (consecutive ones are read together where that
- * saves time: tokens of a draft window or of a chunk).  Query head h reads KV head h / (n_q_heads /
- * n_kv_heads):
+ * saves time: tokens of a draft window or of a chunk).  Query head h reads KV
+ * head h / (n_q_heads / n_kv_heads):
  *   s_c = softmax_scale * sum_g ksc[c,g] * sum_{d in g} q[t,h,d] * kq[c,d]
  *   w_c = exp(s_c - max s);  O = sum w_c v_c / sum w_c,  v_c = vsc * vq
  *   out = O, or with a gate O / (1 + exp(-gate)), rounded to dtype
@@ -419,8 +420,10 @@ typedef struct {
  * a row's results may depend on the other rows' lengths and on max_pages; the
  * same call gives the same bits.  Range: scores and sums are fp32; K scales of any fp16 value, V
  * scales below 2^15.
+ * An infinite or NaN V scale makes the dims it scales NaN or infinite in the
+ * rows that attend to its cell, and in no other.
  * Supported: n_q_heads a multiple of n_kv_heads, 1..16 query heads per KV
- * head.  q, out, kq, vq 16-byte aligned; ksc, vsc, gate 8-byte; the rest 4-byte.
+ * head; max_pages * page_size up to 2^30.  q, out, kq, vq 16-byte aligned; ksc, vsc, gate 8-byte; the rest 4-byte.
  */
 typedef struct {
     int n_tokens, n_q_heads, n_kv_heads, head_dim, group, page_size, n_pages, n_rows, max_pages;

@@ -405,6 +405,8 @@ qsa_status qsa_paged_attn(const qsa_paged_attn_args *a, void *stream) {
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: without rows the table needs a row per token");
     if ((long long)a->n_pages * a->page_size > kMaxInt || (long long)a->max_pages * a->page_size > kMaxInt)
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: n_pages * page_size or max_pages * page_size beyond int32");
+    if ((long long)a->max_pages * a->page_size > 1ll << 30)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_attn: rows of more than 2^30 cells");
     if ((long long)a->n_tokens * a->n_kv_heads > kMaxInt)
         return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_attn: n_tokens * n_kv_heads beyond int32");
     if (!std::isfinite(a->softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: softmax_scale not finite");

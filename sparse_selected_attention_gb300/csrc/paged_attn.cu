@@ -391,11 +391,11 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
         st.l[e] = fmaf(st.l[e], al[e], sum.x + sum.y);
     }
 
-    // The values' power of two: the largest V scale of the first unit, raised
+    // The values' power of two: the largest finite V scale of the first unit, raised
     // when a later scale reaches 2^6 of it, so that weight (below 2^8) times
     // scale stays in the fp16 range.
     const uint2 own = VS[lane % UNIT];
-    uint32_t top = __vmaxu2(own.x & 0x7FFF7FFFu, own.y & 0x7FFF7FFFu);
+    uint32_t top = __vmaxu2(finite2(own.x) & 0x7FFF7FFFu, finite2(own.y) & 0x7FFF7FFFu);
     top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
     const int ve = min(max((int)(top >> 10) - 15, -14), 15);
     if (ve >= st.v + 6) {

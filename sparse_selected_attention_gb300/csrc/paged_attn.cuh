@@ -30,6 +30,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
 
+// Two scales with an infinite or NaN one replaced by 0.
+__device__ __forceinline__ uint32_t finite2(uint32_t x) { return x & ~__vcmpgeu2(x & 0x7FFF7FFFu, 0x7C007C00u); }
+
 // The row of q (or, of a group, its first and the number of them) that starts in
 // a CTA's share and spans n CTAs of its KV head; row -1: none.
 struct Part {

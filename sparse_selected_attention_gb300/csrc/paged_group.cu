@@ -87,6 +87,7 @@ struct GroupSmem {
     alignas(16) int8_t codes[STAGES][2][N * 128 * S];  // K's and V's as they come
     uint2 scales[STAGES][2][N];
     bool there[STAGES][N];
+    alignas(16) uint32_t poison[3][CONVERTERS / 32];  // by converter warp: its lanes whose V scale is infinite or NaN
     alignas(16) float kf[3][N], vb[3][N], vw[3][N];  // a cell's 2^-ek, -ev (-inf: not there), 2^ev
     float top[2][2][M], l[2][M];         // the two halves' maxima (two buffers) and sums of a head row
     uint64_t full[2][STAGES], empty[2][STAGES];  // K's and V's codes
@@ -101,10 +102,10 @@ struct GroupSmem {
 
 __device__ __forceinline__ uint32_t unit_off(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
-// -floor(log2) of the largest |scale| of a cell, 0 where it is 0, infinite or NaN.
+// -floor(log2) of the largest finite |scale| of a cell, 0 where that is 0.
 __device__ __forceinline__ int scale_exponent(uint2 sc) {
-    const uint32_t m2 = __vmaxu2(sc.x & 0x7FFF7FFFu, sc.y & 0x7FFF7FFFu), m = max(m2 & 0xFFFFu, m2 >> 16);
-    if (m == 0u || m >= 0x7C00u) return 0;
+    const uint32_t m2 = __vmaxu2(finite2(sc.x) & 0x7FFF7FFFu, finite2(sc.y) & 0x7FFF7FFFu), m = max(m2 & 0xFFFFu, m2 >> 16);
+    if (m == 0u) return 0;
     return 127 - (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) >> 23);
 }
 // Scale i of a cell times 2^e, in both halves.
@@ -366,6 +367,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int trow = grp.trow, least = grp.least, most = grp.most;
 
         constexpr int CH = D / 16;  // items of sixteen codes of a cell
+        // A converter warp takes CELLS cells at a time and ITEMS times that of a
+        // tile: eight cells, so a lane makes the factor of one scale of K and
+        // one of V (scale lane % 4 of the warp's cell lane / 4).
+        constexpr int CELLS = 32 / CH, ITEMS = N * CH / CONVERTERS, STEP = N / ITEMS;
+        static_assert(CELLS * ITEMS * 4 == 32, "a factor per lane");
+        auto factor_cell = [](int converter, int lane) { return converter * CELLS + (lane >> 2) % CELLS + (lane >> 2) / CELLS * STEP; };
         if (warp >= LOADER) {
             // ---- loads, a warp each for K (with the scales of both) and V ----
             // A lane finds two neighbouring cells, which are of one page; all
@@ -420,13 +427,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = good;
         } else if (warp >= SOFTMAX / 32 && warp < PRODUCTS) {
             // ---- conversion ----
-            // A warp takes CELLS cells at a time and ITEMS times that of a
-            // tile: eight cells, so a lane makes the factor of one scale of K
-            // and one of V.
-            constexpr int CELLS = 32 / CH, ITEMS = N * CH / CONVERTERS, STEP = N / ITEMS;
-            static_assert(CELLS * ITEMS * 4 == 32, "a factor per lane");
             const int ct = tid % CONVERTERS, ch = ct % CH, c0 = ct / CH;
-            const int fsub = (lane >> 2) % CELLS, fitem = (lane >> 2) / CELLS, fcell = (ct >> 5) * CELLS + fsub + fitem * STEP;
+            const int fcell = factor_cell(ct >> 5, lane);
             auto convert = [&](int kind, int k, uint32_t mine) {  // of the k-th tile; mine: the lane's factor
                 const int st = k % STAGES;
                 uint8_t *dst = kind ? sh.v[k & 1][ch >> 2] : sh.k[0][ch >> 2];
@@ -466,7 +468,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!__all_sync(0xffffffffu, good)) return false;
                 const uint2 ks = sh.scales[st][0][fcell], vs = sh.scales[st][1][fcell];
                 const int ek = scale_exponent(ks), ev = scale_exponent(vs);
-                vnext = h2u(scaled(vs, lane & 3, ev));
+                // A V scale that is infinite or NaN counts as 0 here: times a
+                // weight of 0 it would reach rows that end before its cell.
+                vnext = h2u(scaled(make_uint2(finite2(vs.x), finite2(vs.y)), lane & 3, ev));
+                const uint32_t mine = lane & 2 ? vs.y : vs.x;
+                const unsigned poison = __ballot_sync(0xffffffffu, (mine >> (lane & 1 ? 16 : 0) & 0x7C00u) == 0x7C00u);
+                if (lane == 0) sh.poison[b][ct >> 5] = poison;
                 if ((lane & 3) == 0) {
                     sh.kf[b][fcell] = exp2i(-ek);
                     sh.vb[b][fcell] = sh.there[st][fcell] ? -(float)ev : -CUDART_INF_F;
@@ -595,6 +602,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_arrive(smem_u32(&sh.q_full));
             }
             float ref = -CUDART_INF_F, l = 0.0f;
+            uint32_t poison = 0u;  // quarters of the dims whose value is NaN: an infinite or NaN V scale was attended to
             for (int i = i0; i < i1; ++i, ++k) {
                 good = __all_sync(0xffffffffu, good && mbar_wait_or_abort(smem_u32(&sh.s_full[k & 1]), (k >> 1) & 1, abort));
                 fence_after();
@@ -623,7 +631,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     y[j + 2] = s1.x;
                     y[j + 3] = s1.y;
                 }
-                if ((i + 1) * N > least) {  // some row ends in this tile
+                const uint4 bad0 = *reinterpret_cast<const uint4 *>(sh.poison[k % 3]), bad1 = *reinterpret_cast<const uint4 *>(sh.poison[k % 3] + 4);
+                if (bad0.x | bad0.y | bad0.z | bad0.w | bad1.x | bad1.y | bad1.z | bad1.w) {
+                    for (int w = 0; w < CONVERTERS / 32; ++w)
+                        for (uint32_t bits = sh.poison[k % 3][w]; bits; bits &= bits - 1) {
+                            const int b = __ffs(bits) - 1;
+                            if (i * N + factor_cell(w, b) < len) poison |= 1u << (b & 3);
+                        }
+                }
+                if (i * N > least - N) {  // some row ends in this tile
 #pragma unroll
                     for (int j = 0; j < NH; ++j)
                         if (i * N + j0 + j >= len) y[j] = -CUDART_INF_F;
@@ -697,7 +713,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 fence_after();
                 l += sh.l[half ^ 1][m];
                 const bool none = ref == -CUDART_INF_F;
-                const float w = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
+                const float scale = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
 #pragma unroll 1
                 for (int c = 0; c < DH / 16; c += 2) {
                     uint32_t v[2][16];
@@ -710,6 +726,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int j = 0; j < 4; ++j) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) asm volatile("" : "+r"(v[i][4 * j + e]));
+                            const float w = poison >> ((half * DH + 16 * (c + i)) / (D / 4)) & 1u ? CUDART_NAN_F : scale;
                             float *dst = values + m * D + 4 * ((half * (DH / 4) + 4 * (c + i) + j) ^ (m & 7));
                             *reinterpret_cast<float4 *>(dst) =
                                 make_float4(__uint_as_float(v[i][4 * j]) * w, __uint_as_float(v[i][4 * j + 1]) * w,

@@ -565,11 +565,7 @@ cudaError_t launch_team(void (*one)(L), void (*cluster)(L), const L &l, cudaStre
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = small ? 1 : 2;
-    if (cfg.dynamicSmemBytes > 40 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, SMALL_PAGES * (int)sizeof(int));
-        if (e != cudaSuccess) return e;
-    }
+    static_assert(SMALL_PAGES * sizeof(int) <= 40 * 1024, "below the default limit, with the kernels' own");
     return cudaLaunchKernelEx(&cfg, small ? one : cluster, l);
 }
 

@@ -150,7 +150,8 @@ COMPACT = dict(n_rows=2, max_pages=4, n_layers=1, n_pages=8, page_size=16, n_kv_
         (dict(head_dim=192, group=48), UNS), (dict(n_q_heads=17), UNS), (dict(n_kv_heads=5), UNS), (dict(n_kv_heads=0), UNS),
         (dict(page_size=8), UNS), (dict(page_size=100), UNS), (dict(dtype=0), INV), (dict(n_tokens=-2), INV),
         (dict(n_pages=0), INV), (dict(max_pages=0), INV), (dict(rows=None, n_rows=2), INV),
-        (dict(n_pages=1 << 28), INV), (dict(max_pages=1 << 28), INV), (dict(softmax_scale=float("inf")), INV),
+        (dict(n_pages=1 << 28), INV), (dict(max_pages=1 << 28), INV), (dict(max_pages=(1 << 26) + 1, page_size=16), UNS),
+        (dict(softmax_scale=float("inf")), INV),
         (dict(workspace_bytes=16), INV), (dict(workspace=FAKE + 16), INV), (dict(workspace=None), INV),
         (dict(seq_lens=None), INV), (dict(q=FAKE + 4), INV), (dict(lse=FAKE + 2), INV), (dict(gate=FAKE + 4), INV), (dict(ksc=FAKE + 4), INV)]
 ] + [

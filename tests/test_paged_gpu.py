@@ -454,6 +454,72 @@ def test_attn_together_repeats_its_bits(cuda_device):
         assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
 
 
+@pytest.mark.parametrize("d,hq,hkv,n,base", [(128, 8, 8, 128, 600), (256, 16, 8, 64, 560), (128, 12, 1, 8, 700)])
+def test_attn_nan_and_inf_reach_only_their_rows(cuda_device, d, hq, hkv, n, base):
+    """A NaN or infinite scale of a window's later token: rows that end before
+    its cell are as without it, to the last bit where the division of work is
+    the same; a V scale makes its own dims of the others NaN or infinite, a K
+    scale a whole head of them."""
+    rng = np.random.default_rng(33)
+    table, pages = shuffled_table([base + n], 32, 1, rng)
+    pool = make_pool(pages, 32, hkv, d, seed=34)
+    rows, lens = [0] * n, [base + 1 + i for i in range(n)]
+    q = rng.standard_normal((n, hq, d))
+    per, cut = hq // hkv, n // 2
+    cell = base + cut  # of row cut's own token
+    page, at = table[0, cell // 32], cell % 32
+    # Two runs, each off by two roundings of at most 2^-11 of each term.
+    most = 2 * 2.0 ** -10 * float(np.abs(pool[1].astype(np.float64) * np.repeat(pool[3].astype(np.float64), d // 4, -1)).max())
+    for otype in (F16, BF16):
+        plain, _ = check_attn(q, pool, table, lens, rows=rows, otype=otype)
+        for value in (np.nan, np.inf, -np.inf):
+            bad = [x.copy() for x in pool]
+            bad[3][page, at, hkv - 1, 2] = value
+            bad[1][page, at, hkv - 1] = 3
+            out = torch.empty_like(plain)
+            ws = torch.empty(qsa.qsa_paged_attn_workspace_bytes(hq, hkv, d), dtype=torch.uint8, device="cuda")
+            args = (dev(table), i32(lens), out, ws)
+            qd = dev(q.astype(np.float32)).to(otype)
+            good = [x.copy() for x in bad]
+            good[3][page, at, hkv - 1, 2] = 0.01
+            qsa.qsa_paged_attn(qd, *[dev(x) for x in good], *args, rows=i32(rows))
+            want = out.clone()
+            qsa.qsa_paged_attn(qd, *[dev(x) for x in bad], *args, rows=i32(rows))
+            head, dims = slice((hkv - 1) * per, hq), slice(d // 2, 3 * d // 4)
+            assert not torch.isfinite(out[cut:, head, dims]).any()
+            assert torch.equal(out[:cut], want[:cut]) and torch.equal(out[:, :hq - per], want[:, :hq - per])
+            for part in (slice(0, d // 2), slice(3 * d // 4, d)):
+                assert torch.isfinite(out[cut:, head, part]).all()
+                assert torch.allclose(out[cut:, head, part].float(), want[cut:, head, part].float(), rtol=2.0 ** -7, atol=most)
+        bad = [x.copy() for x in pool]
+        bad[2][page, at, 0, 1] = np.nan
+        out = torch.empty_like(plain)
+        qsa.qsa_paged_attn(qd, *[dev(x) for x in bad], dev(table), i32(lens), out, ws, rows=i32(rows))
+        assert torch.equal(out[:cut], plain[:cut]) and torch.equal(out[:, per:], plain[:, per:])
+        assert torch.isnan(out[cut:, :per]).all()
+
+
+def test_attn_together_beyond_32_bit_offsets(cuda_device):
+    """Rows taken together whose pages start past 2^32 bytes of codes."""
+    page, d, hkv, n, held = 64, 256, 8, 64, 9
+    pages = (1 << 32) // (page * hkv * d) + 16
+    small = make_pool(held, page, hkv, d, seed=35)
+    big = [torch.zeros(pages, page, hkv, x.shape[3], dtype=dev(x).dtype, device="cuda") for x in small]
+    where = [pages - 1 - 2 * i if i % 2 else i for i in range(held)]
+    for t, x in zip(big, small):
+        t[where] = dev(x)
+    q = dev(np.random.default_rng(12).standard_normal((n, hkv * 2, d)).astype(np.float16))
+    lens = [held * page - n + 1 + i for i in range(n)]
+    assert taken_together([0] * n, lens, hkv * 2, hkv, d)
+    ws = torch.empty(qsa.qsa_paged_attn_workspace_bytes(hkv * 2, hkv, d), dtype=torch.uint8, device="cuda")
+    outs = []
+    for pool, tab in ((big, where), ([dev(x) for x in small], list(range(held)))):
+        out = torch.empty_like(q)
+        qsa.qsa_paged_attn(q, *pool, i32(tab).view(1, held), i32(lens), out, ws, rows=i32([0] * n))
+        outs.append(out)
+    assert torch.equal(*outs)
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.05, 1.0, 1e-30])
 def test_attn_scales_and_peaks(cuda_device, scale):
     """Uniform weights, reversed ones, and ones so peaked that nearly every

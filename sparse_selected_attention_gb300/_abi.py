@@ -147,6 +147,17 @@ def packed(name: str):
     return f
 
 
+_entries = {}
+
+
+def entry(name: str) -> int:
+    """The address of the release library's `name`."""
+    a = _entries.get(name)
+    if a is None:
+        a = _entries[name] = ctypes.cast(lib()[name], _vp).value
+    return a
+
+
 def _declare(L: ctypes.CDLL, path: str) -> None:
     for name, argt in (("qsa_prep", PrepArgs), ("qsa_score", ScoreArgs), ("qsa_attn", AttnArgs),
                        ("qsa_score_noalloc", ScoreArgs), ("qsa_select", SelectArgs),

@@ -14,13 +14,18 @@ built by build_all():
                    its buffer sets a device word (read by qsa_check_word)
                    and the access is skipped.
 and libqsa_l2probe.so, the benchmark's L2 gather-rate probe.
+
+_paged_binding.so, the paged calls' argument marshalling, is host code against
+the installed torch; it is given the library's entry points and links none.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -124,6 +129,28 @@ def build_host_sanitized(verbose: bool = False) -> str:
     return lib
 
 
+BINDING = os.path.join(PKG, "_paged_binding.so")
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """_paged_binding.so, for this interpreter and its torch."""
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    if force or _stale(BINDING, [src, os.path.join(INCLUDE, "qsa.h")]):
+        gxx = shutil.which("g++")
+        if not gxx:
+            raise RuntimeError("g++ not found")
+        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+        includes = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                    sysconfig.get_paths()["include"], os.path.join(cuda_home, "include")]
+        lib = os.path.join(torch, "lib")
+        tmp = BINDING + ".tmp"
+        _run([gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(x for i in includes for x in ("-I", i)), src, "-o", tmp,
+              "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], verbose)
+        os.replace(tmp, BINDING)
+    return BINDING
+
+
 PROBE_LIB = os.path.join(PKG, "libqsa_l2probe.so")
 
 
@@ -139,13 +166,14 @@ def build_probe(verbose: bool = False, force: bool = False) -> str:
 
 
 def build_all(verbose: bool = False, force: bool = False) -> list:
-    """Every variant (release first), the variants and the probe in parallel."""
-    out = [build(verbose=verbose, force=force)]
+    """Every variant (release first), the variants, the probe and the binding in parallel."""
     rest = [v for v in VARIANTS if v != "release"]
-    with ThreadPoolExecutor(max_workers=len(rest) + 1) as ex:
+    with ThreadPoolExecutor(max_workers=len(rest) + 2) as ex:
+        binding = ex.submit(build_binding, verbose=verbose, force=force)
+        out = [build(verbose=verbose, force=force)]
         futs = [ex.submit(build, verbose=verbose, force=force, variant=v) for v in rest]
         probe = ex.submit(build_probe, verbose=verbose, force=force)
-        out += [f.result() for f in futs] + [probe.result()]
+        out += [f.result() for f in futs] + [probe.result(), binding.result()]
     return out
 
 
@@ -155,3 +183,4 @@ if __name__ == "__main__":
         print("\n".join(build_all(verbose=v, force="--force" in sys.argv)))
     else:
         print(build(verbose=v, ptxas_info="--ptxas" in sys.argv, force="--force" in sys.argv))
+        print(build_binding(verbose=v, force="--force" in sys.argv))

@@ -1,11 +1,13 @@
 """Python binding of the paged cache's calls (include/qsa.h, "The paged cache").
 
 A decode step makes three of these calls and its kernels take some
-microseconds each, so the host's share is kept small: a tensor is checked with
-a handful of attribute reads, the argument struct is packed in one call, and
-the stream is read as a raw handle.  The checks are the C ABI's and the ones
-only Python can make (device, dtype, shape, contiguity): everything the kernels
-index by is a shape that was checked here.
+microseconds each, so the host's share is kept small: _paged_binding
+(csrc/paged_binding.cpp) checks and reads the tensors on torch's C++ side and
+makes the call.  Where it finds anything amiss it says so, and the functions
+below called _checked_* look again: they hold the checks with their words, and
+make the calls that need another device current.  The checks are the C ABI's
+and the ones only Python can make (device, dtype, shape, contiguity):
+everything the kernels index by is a shape that was checked here.
 """
 from __future__ import annotations
 
@@ -14,6 +16,12 @@ import struct
 import torch
 
 from . import _abi
+
+try:
+    from . import _paged_binding as _native
+except ImportError as e:
+    raise RuntimeError("_paged_binding.so is missing or of another torch: build it with "
+                       "`python -m sparse_selected_attention_gb300.build --all`") from e
 
 F32, F16, BF16, I32, I8 = torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int8
 _CODE = {F32: _abi.QSA_F32, F16: _abi.QSA_F16, BF16: _abi.QSA_BF16}
@@ -98,6 +106,13 @@ def _call(name, packed, dev, stream):
         _abi.check(status)
 
 
+def _again(status, checked, *args):
+    """After a call that did not go through: the library's status, or -1."""
+    if status > 0:
+        _abi.check(status)
+    checked(*args)
+
+
 def qsa_paged_prep(q_in, k_in, v_in, positions, slots, kq, vq, ksc, vsc, q_out, q_norm_w=None, k_norm_w=None,
                    inv_freq=None, interleaved=False, eps=1e-6, rope_mscale=1.0, err=None, stream=None):
     """New tokens of any sequences: q_out [T, Hq, D] (fp16 or bf16) <- the
@@ -109,6 +124,15 @@ def qsa_paged_prep(q_in, k_in, v_in, positions, slots, kq, vq, ksc, vsc, q_out, 
     [rope_dims/2] holds the rotation's frequencies (None: no rotation), paired
     in halves or interleaved; positions, slots int32 [T], a slot of -1 marks a
     padding token."""
+    status = _native.prep(_abi.entry("qsa_paged_prep"), q_in, k_in, v_in, positions, slots, kq, vq, ksc, vsc, q_out,
+                          q_norm_w, k_norm_w, inv_freq, interleaved, eps, rope_mscale, err, stream)
+    if status:
+        _again(status, _checked_prep, q_in, k_in, v_in, positions, slots, kq, vq, ksc, vsc, q_out, q_norm_w, k_norm_w, inv_freq,
+               interleaved, eps, rope_mscale, err, stream)
+
+
+def _checked_prep(q_in, k_in, v_in, positions, slots, kq, vq, ksc, vsc, q_out, q_norm_w, k_norm_w, inv_freq,
+                  interleaved, eps, rope_mscale, err, stream):
     T, H, D = q_in.shape
     dev, itype = q_in.get_device(), q_in.dtype
     hkv, d = kq.shape[-2:]
@@ -146,6 +170,13 @@ def qsa_paged_gather(kq, vq, ksc, vsc, ids, k_out, v_out, rows=None, page_table=
     cells ids [N] int32 as the values they stand for; -1 gives zeros.  With
     page_table [R, max_pages] int32 and rows [N] int32, ids[i] is a cell of
     sequence rows[i] and kq [pages, page, Hkv, D]; without, a pool cell."""
+    status = _native.gather(_abi.entry("qsa_paged_gather"), kq, vq, ksc, vsc, ids, k_out, v_out, rows, page_table,
+                            err, stream)
+    if status:
+        _again(status, _checked_gather, kq, vq, ksc, vsc, ids, k_out, v_out, rows, page_table, err, stream)
+
+
+def _checked_gather(kq, vq, ksc, vsc, ids, k_out, v_out, rows, page_table, err, stream):
     hkv, d = kq.shape[-2:]
     dev, otype = kq.get_device(), k_out.dtype
     cells = kq.numel() // max(hkv * d, 1)
@@ -185,6 +216,15 @@ def qsa_paged_attn(q, kq, vq, ksc, vsc, page_table, seq_lens, out, workspace, ro
     lse, if given, fp32 [T, Hq] receives the log of the softmax denominator.
     workspace is a uint8 CUDA tensor of at least
     qsa_paged_attn_workspace_bytes(Hq, Hkv, D) bytes."""
+    status = _native.attn(_abi.entry("qsa_paged_attn"), q, kq, vq, ksc, vsc, page_table, seq_lens, out, workspace,
+                          rows, softmax_scale, gate, lse, err, stream)
+    if status:
+        _again(status, _checked_attn, q, kq, vq, ksc, vsc, page_table, seq_lens, out, workspace, rows, softmax_scale, gate, lse, err,
+               stream)
+
+
+def _checked_attn(q, kq, vq, ksc, vsc, page_table, seq_lens, out, workspace, rows, softmax_scale, gate, lse, err,
+                  stream):
     T, H, D = q.shape
     dev, dtype = q.get_device(), q.dtype
     if dev < 0:
@@ -237,6 +277,15 @@ def qsa_page_update(page_table, seq_lens, src, n_new, kq, vq, ksc, vsc, page_tab
     past them and for a row that could not grow (QSA_DEVERR_NO_PAGES in err).
     All int32.  With src None the outputs may be the inputs.  workspace: uint8,
     qsa_pages_workspace_bytes(R, pages) bytes."""
+    status = _native.update(_abi.entry("qsa_page_update"), page_table, seq_lens, src, n_new, kq, vq, ksc, vsc,
+                            page_table_out, seq_lens_out, refs, slots, positions, workspace, err, stream)
+    if status:
+        _again(status, _checked_update, page_table, seq_lens, src, n_new, kq, vq, ksc, vsc, page_table_out, seq_lens_out, refs, slots,
+               positions, workspace, err, stream)
+
+
+def _checked_update(page_table, seq_lens, src, n_new, kq, vq, ksc, vsc, page_table_out, seq_lens_out, refs, slots,
+                    positions, workspace, err, stream):
     dev, (layers, pages, page, hkv, d) = _pool(kq, page_table)
     r_in, wide = page_table.shape
     r_out = n_new.numel()
@@ -260,6 +309,15 @@ def qsa_page_compact(page_table, seq_lens, kq, vq, ksc, vsc, page_table_out, ref
     refs [pages] by the new numbers, and the moved pages' contents in all
     layers.  All int32; page_table_out may be page_table.  workspace: uint8,
     qsa_pages_workspace_bytes(R, pages) bytes."""
+    status = _native.compact(_abi.entry("qsa_page_compact"), page_table, seq_lens, kq, vq, ksc, vsc, page_table_out,
+                             refs, page_map, n_live, workspace, err, stream)
+    if status:
+        _again(status, _checked_compact, page_table, seq_lens, kq, vq, ksc, vsc, page_table_out, refs, page_map, n_live, workspace, err,
+               stream)
+
+
+def _checked_compact(page_table, seq_lens, kq, vq, ksc, vsc, page_table_out, refs, page_map, n_live, workspace, err,
+                     stream):
     dev, (layers, pages, page, hkv, d) = _pool(kq, page_table)
     rows, wide = table = page_table.shape
     kv = _cache(kq, vq, ksc, vsc, dev)

@@ -992,3 +992,63 @@ def test_binding_refuses(cuda_device):
     refused("may be the old ones only without src", call, src=lens, seq_lens_out=lens)
     refused("page_map must be", qsa.qsa_page_compact, tab, lens, *pool, z(2, 2), z(4), z(3), z(1), ws)
     refused("n_live must be", qsa.qsa_page_compact, tab, lens, *pool, z(2, 2), z(4), z(4), z(2), ws)
+
+
+def test_binding_paths_agree(cuda_device, monkeypatch):
+    """A call that is as it should be goes through the compiled binding alone,
+    and does what the checked one does, to the bit."""
+    from sparse_selected_attention_gb300 import paged
+    rng = np.random.default_rng(36)
+    T, hq, hkv, d, page, pages = 5, 6, 2, 128, 16, 12
+    z = lambda *v, t=torch.int32: torch.zeros(v, dtype=t, device="cuda")  # noqa: E731
+    q, k, v = (dev(rng.standard_normal((T, h, d)).astype(np.float16)) for h in (hq, hkv, hkv))
+    w, freq = dev(rng.random(d).astype(np.float32)), dev(rng.random(d // 4).astype(np.float32))
+    gate = dev(rng.standard_normal((T, hq, d)).astype(np.float32))
+    first = [dev(x) for x in make_pool(pages, page, hkv, d, seed=37)]
+    table, lens = i32(3, 5, -1, 7, 1, 2).view(2, 3), i32(20, 40)
+    side = torch.cuda.Stream()
+
+    def everything(stream):
+        lay = [x.clone() for x in first]
+        qo, ko, vo, out, lse = torch.empty_like(q), *(torch.empty(T, hkv, d, device="cuda") for _ in range(2)), torch.empty_like(q), z(T, hq, t=F32)
+        to, lo, refs, sl, po_, tc, mp, nl, err = z(2, 3), z(2), z(pages), z(T), z(T), z(2, 3), z(pages), z(1), z(1)
+        wa, wp = (z(n, t=torch.uint8) for n in (qsa.qsa_paged_attn_workspace_bytes(hq, hkv, d), qsa.qsa_pages_workspace_bytes(2, pages)))
+        torch.cuda.synchronize()
+        kw = dict(err=err, stream=stream)
+        qsa.qsa_page_update(table, lens, i32(0, 1), i32(3, 2), *lay, to, lo, refs, sl, po_, wp, **kw)
+        qsa.qsa_paged_prep(q, k, v, po_, sl, *lay, qo, q_norm_w=w, k_norm_w=w, inv_freq=freq, interleaved=True, eps=1e-5, rope_mscale=0.5, **kw)
+        qsa.qsa_paged_gather(*lay, i32(0, 19, 39, -1, 2), ko, vo, rows=i32(0, 0, 1, 1, 1), page_table=to, **kw)
+        qsa.qsa_paged_attn(qo, *lay, to, i32(21, 22, 23, 41, 42), out, wa, rows=i32(0, 0, 0, 1, 1), softmax_scale=0.1, gate=gate, lse=lse, **kw)
+        qsa.qsa_page_compact(to, lo, *lay, tc, refs, mp, nl, wp, **kw)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return lay + [qo, ko, vo, out, lse, to, lo, refs, sl, po_, tc, mp, nl]
+
+    checked = {n: getattr(paged, "_checked_" + n) for n in ("prep", "gather", "attn", "update", "compact")}
+    with monkeypatch.context() as m:
+        for n in checked:
+            m.setattr(paged, "_checked_" + n, None)
+        a = [everything(s) for s in (None, side)]
+
+    class Never:
+        def __getattr__(self, name):
+            return lambda *args: -1
+    with monkeypatch.context() as m:
+        m.setattr(paged, "_native", Never())
+        a += [everything(s) for s in (None, side)]
+    for other in a[1:]:
+        for i, (x, y) in enumerate(zip(a[0], other)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), i
+
+
+def test_binding_says_what_the_library_says(cuda_device):
+    """A refusal by the library, through the compiled binding."""
+    pd = [dev(x) for x in make_pool(2, 16, 1, 128)]
+    ko, vo = (torch.empty(1, 1, 128, device="cuda") for _ in range(2))
+    shifted = torch.empty(129, device="cuda")[1:].view(1, 1, 128)
+    with pytest.raises(qsa.QSAError, match="qsa_paged_gather: misaligned"):
+        qsa.qsa_paged_gather(*pd, i32(0), shifted, vo)
+    with pytest.raises((ValueError, TypeError, AttributeError)):
+        qsa.qsa_paged_gather(*pd, [0], ko, vo)
+    with pytest.raises((ValueError, TypeError)):
+        qsa.qsa_paged_gather(*pd, i32(0).expand(2)[:1].to_sparse(), ko, vo)

@@ -21,6 +21,7 @@ def use_library(monkeypatch):
         L = _abi.variant(name)
         monkeypatch.setattr(_abi, "lib", lambda: L)
         monkeypatch.setattr(_abi, "_packed", {})
+        monkeypatch.setattr(_abi, "_entries", {})
         return L
     yield use
 

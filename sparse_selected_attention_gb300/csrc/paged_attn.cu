@@ -275,12 +275,15 @@ struct State {
     int v;  // values are in units of 2^v
 };
 
-// Folds one staged unit into the state.  vmask: the unit's valid cells.  Scores
-// are summed over K's codes, EXACT, or over 1152 + codes from -1152 sum q, with
-// sixteen times the rounding: of rows of one or two cells, whose scores are the
-// results' logarithms, 1.2e-6 of them.  Long rows average it (2e-7), and exact codes
-// cost them 2.6 to 7% (61 rows, 48/4 heads of 128: 200 us, 195 us; 90 rows of 18 K
-// cells, one head of 256: 171 us, 159 us); so EXACT goes with short tables.
+// Folds one staged unit into the state.  vmask: the unit's valid cells.  EXACT:
+// scores are summed over K's codes, not over 1152 + codes from -1152 sum q with
+// sixteen times the rounding, and the products weight x scale go in in two parts
+// of 11 bits, not in one.  Long rows average both (off by 2e-7 of lse, and by
+// 1.2 times the output's own rounding), and would pay 2.6 to 7% for exact codes
+// alone (61 rows, 48/4 heads of 128: 200 us, 195 us; 90 rows of 18 K cells, one
+// head of 256: 171 us, 159 us).  Of short ones, a few cells carry the result (1.2e-6
+// of lse, 1.5 times the output's rounding), and the time is latency: so EXACT
+// goes with short tables.
 template <int S, bool EXACT>
 __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const uint2 *KS, const uint2 *VS, const uint4 (*q)[32],
                                              const float (*bias)[8][4], unsigned vmask, State<S> &st, const float (&sl2)[2]) {
@@ -427,10 +430,13 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     for (int kk = 0; kk < NK; ++kk)
 #pragma unroll
         for (int i = 0; i < 2; ++i) vs[kk][i] = *reinterpret_cast<const uint4 *>(VS + 16 * kk + 4 * r + 2 * i);
-    auto pv = [&](float (&o)[4], const uint4 &p, uint32_t w) { mma16816(o, p, even(w), odd(w), o[0], o[1], o[2], o[3]); };
+    auto pv = [&](float (&o)[4], const uint4 &p, const uint4 &rest, uint32_t w) {
+        mma16816(o, p, even(w), odd(w), o[0], o[1], o[2], o[3]);
+        if constexpr (EXACT) mma16816(o, rest, even(w), odd(w), o[0], o[1], o[2], o[3]);
+    };
 #pragma unroll
     for (int gr = 0; gr < 4; ++gr) {
-        uint4 p[NK];
+        uint4 p[NK], rest[NK];
 #pragma unroll
         for (int kk = 0; kk < NK; ++kk) {
             const uint4 &lo = vs[kk][0], &hi = vs[kk][1];
@@ -438,12 +444,16 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
             const uint32_t h0 = gr >> 1 ? hi.y : hi.x, h1 = gr >> 1 ? hi.w : hi.z;
             auto scale = [&](uint32_t x) { return (gr & 1) ? __high2float(u2h(x)) : __low2float(u2h(x)); };
             const float2 f02 = make_float2(scale(l0), scale(h0)), f13 = make_float2(scale(l1), scale(h1));
-            auto scaled = [&](float2 x, float2 f) {
+            auto scaled = [&](float2 x, float2 f, uint32_t &high, uint32_t &low) {
                 const float2 y = __fmul2_rn(x, f);
-                return h2u(__floats2half2_rn(y.x, y.y));
+                const __half2 h = __floats2half2_rn(y.x, y.y);
+                high = h2u(h);
+                if constexpr (EXACT) low = h2u(__floats2half2_rn(y.x - __low2float(h), y.y - __high2float(h)));
             };
-            p[kk] = make_uint4(scaled(w[2 * kk][0], f02), scaled(w[2 * kk][1], f02), scaled(w[2 * kk + 1][0], f13),
-                               scaled(w[2 * kk + 1][1], f13));
+            scaled(w[2 * kk][0], f02, p[kk].x, rest[kk].x);
+            scaled(w[2 * kk][1], f02, p[kk].y, rest[kk].y);
+            scaled(w[2 * kk + 1][0], f13, p[kk].z, rest[kk].z);
+            scaled(w[2 * kk + 1][1], f13, p[kk].w, rest[kk].w);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -451,15 +461,15 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
             if constexpr (S == 1) {  // 16 dims of both halves of the cells
                 const int c = 2 * gr + i;
                 load_v(v, vrow ^ (c << 4));
-                pv(st.o[2 * c], p[0], v[0]);
-                pv(st.o[2 * c + 1], p[0], v[1]);
-                pv(st.o[2 * c], p[NK - 1], v[2]);
-                pv(st.o[2 * c + 1], p[NK - 1], v[3]);
+                pv(st.o[2 * c], p[0], rest[0], v[0]);
+                pv(st.o[2 * c + 1], p[0], rest[0], v[1]);
+                pv(st.o[2 * c], p[NK - 1], rest[NK - 1], v[2]);
+                pv(st.o[2 * c + 1], p[NK - 1], rest[NK - 1], v[3]);
             } else {  // 32 dims
                 const int c = 2 * (gr & 1) + i, t = 16 * (gr >> 1) + 4 * c;
                 load_v(v, (vrow ^ (c << 5)) + (gr >> 1) * UNIT * 128);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) pv(st.o[t + k], p[0], v[k]);
+                for (int k = 0; k < 4; ++k) pv(st.o[t + k], p[0], rest[0], v[k]);
             }
         }
     }
@@ -803,7 +813,7 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const bool whole = units <= WHOLE || resident == 1;
     const long long most = whole ? a.n_tokens : (a.n_tokens * units + MIN_SHARE - 1) / MIN_SHARE;
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, block = a.rows && !whole ? group_block(per) : 0;
+    const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups(a, units, group_block(per)) ? group_block(per) : 0;
     const auto kernel = whole ? paged_attn_kernel<S, true> : paged_attn_kernel<S, false>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, block);

@@ -85,6 +85,11 @@ __device__ __forceinline__ int units_of(int len) {  // one at least, so that an 
 __device__ __forceinline__ bool take_groups(const qsa_paged_attn_args &a, long long alone, long long together, bool longer) {
     return longer && (2 * alone - 7 * together) * a.n_kv_heads > 2 * 4096;
 }
+// Whether rows of up to `units` units could be: if not, the groups' launch is left out (2 us).
+inline bool may_take_groups(const qsa_paged_attn_args &a, long long units, int block) {
+    const long long groups = a.n_tokens < block ? 1 : a.n_tokens / block;
+    return a.rows && (2ll * a.n_tokens - 7 * groups) * units * a.n_kv_heads > 2 * 4096;
+}
 constexpr int GROUP_ROWS = 128;  // heads of a group, all its rows' (the M of its products)
 __host__ __device__ inline int group_block(int per) {
     int b = 1;

@@ -21,8 +21,8 @@
 // many.)  Consecutive rows of one sequence go to paged_group.cu where that saves
 // enough (take_groups).
 //
-// 61 rows of up to 32 K cells, 48/4 heads of 128, 1.1 GB: 196 us, 5.6 TB/s; the
-// same launch without the arithmetic 176 us.  A row of 321 cells alone: 7.3 us,
+// 61 rows of up to 32 K cells, 48/4 heads of 128, 1.1 GB: 197 us, 5.6 TB/s; the
+// same launch without the arithmetic 176 us.  A row of 321 cells alone: 8 us,
 // all of it latency.
 //
 // A unit.  The query heads of one KV head are the M side (padded to 16) of
@@ -119,9 +119,9 @@ struct Smem {
     float m[NW][16], l[NW][16], f[NW][16];
     int v[NW];                                     // the warps' V exponents
     uint64_t bar[NW][2];
-    long long together[NW], scan[NW];
+    long long together[NW], padded[NW], scan[NW];
     long long total, before;                       // units of all rows; of the rows before `row`
-    int row;
+    int row, left;                                 // the share's units
 };
 
 // Sums the rows' units and finds the row that holds unit share * range, of
@@ -136,12 +136,14 @@ __device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S>
     const int run = (a.n_tokens + NW * 32 - 1) / (NW * 32);
     const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
     bool bad = false;
-    long long mine = 0, together = 0;
+    long long mine = 0, padded = 0, together = 0;
     int most = 0;
+    auto pad = [](int u) { return (u + MIN_SHARE - 1) & -MIN_SHARE; };
     for (int t = t0; t < t1; ++t) {
         int row;
         const int u = units_of<S>(row_len(a, t, row, bad));
         mine += u;
+        padded += pad(u);
         most = max(most, u);
         if (block && group_start(a.rows, t, block) == t) {
             int longest = u;
@@ -151,11 +153,14 @@ __device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S>
         }
     }
     if (bad && blockIdx.x == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
-    long long s = mine;
+    long long s = mine, sp = padded;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
+        const long long u = __shfl_up_sync(0xffffffffu, s, o), up = __shfl_up_sync(0xffffffffu, sp, o);
+        if (lane >= o) {
+            s += u;
+            sp += up;
+        }
     }
     if (block) {
 #pragma unroll
@@ -163,32 +168,48 @@ __device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S>
     }
     if (lane == 31) {
         sh.scan[warp] = s;
+        sh.padded[warp] = sp;
         sh.together[warp] = together;
     }
     share = 0;
     if (!__syncthreads_or(most > WHOLE)) return true;
-    long long total = 0, before = 0, groups = 0;
+    long long total = 0, before = 0, groups = 0, total_padded = 0, before_padded = 0;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-        if (w < warp) before += sh.scan[w];
+        if (w < warp) {
+            before += sh.scan[w];
+            before_padded += sh.padded[w];
+        }
         total += sh.scan[w];
+        total_padded += sh.padded[w];
         groups += sh.together[w];
     }
     if (block && take_groups(a, total, groups, true)) return false;
     before += s - mine;
+    before_padded += sp - padded;
     const long long per = (total + ranges - 1) / ranges;
     share = (int)max(per, (long long)MIN_SHARE);
+    // Where CTAs are to spare, no share goes over a row's end: the rows' units
+    // count as padded to whole shares (four rows of 321 cells, 24/2 heads of 256:
+    // 13.0 us, 17.0 us without).
+    const bool aligned = share == MIN_SHARE && total_padded <= (long long)share * ranges;
+    if (aligned) {
+        total = total_padded;
+        before = before_padded;
+        mine = padded;
+    }
     const long long x0 = (long long)share * range;
     if (x0 >= before && x0 < before + mine) {
         for (int t = t0;; ++t) {
             int row;
-            const int u = units_of<S>(row_len(a, t, row, bad));
-            if (x0 < before + u) {
+            const int u = units_of<S>(row_len(a, t, row, bad)), v = aligned ? pad(u) : u;
+            if (x0 < before + v) {
                 sh.row = t;
                 sh.before = before;
+                sh.left = aligned ? (int)min((long long)share, before + u - x0) : (int)min((long long)share, total - x0);
                 break;
             }
-            before += u;
+            before += v;
         }
     }
     if (tid == 0) sh.total = total;
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
         const long long x = (long long)share * range, total = sh.total;
         none = x >= total;
         if (!none) {
-            left = (int)min((long long)share, total - x);
+            left = sh.left;
             t = sh.row;
             u0 = (int)(x - sh.before);
         }
@@ -811,7 +832,7 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const long long units = ((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT;
     const int resident = std::max(MAX_CTAS / a.n_kv_heads, 1);
     const bool whole = units <= WHOLE || resident == 1;
-    const long long most = whole ? a.n_tokens : (a.n_tokens * units + MIN_SHARE - 1) / MIN_SHARE;
+    const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups(a, units, group_block(per)) ? group_block(per) : 0;
     const auto kernel = whole ? paged_attn_kernel<S, true> : paged_attn_kernel<S, false>;

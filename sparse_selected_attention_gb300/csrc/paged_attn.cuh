@@ -134,7 +134,7 @@ __device__ __forceinline__ float gated(float y, float gate) { return __fdividef(
 // Joins the partials of rows that span CTAs, of one kernel or of both.  Part p
 // of the row that starts in CTA x is slot 1 of that CTA, then slot 0 of the
 // next ones of its KV head.  A block lists the CTAs in which such rows start,
-// and blocks go round over these and chunks of their heads.  A warp takes 64
+// and blocks go round over these and chunks of their heads.  A warp takes 32 V
 // dims of one head and every G-th part; it works the weights out itself (a few
 // loads per lane), so there is nothing to wait for but the last sum.  Many
 // rows: HB heads and no split per block; few, whose parts are many: the block's
@@ -149,10 +149,13 @@ struct Joined {  // a kernel's partials: where, room for how many CTAs and heads
 template <int S, int HB>
 __global__ void __launch_bounds__(JOIN_WARPS * 32)
     paged_join_kernel(const qsa_paged_attn_args a, const Joined one, const Joined two) {
-    constexpr int D = 128 * S, DC = D / 64, G = JOIN_WARPS / (HB * DC);
+    // Dims of a lane.  Few rows of 256: 4, for more loads at once (one of 321 cells 11.4
+    // us, 12.8 with 2; of 128 dims 10.6, 10.1).
+    constexpr int V = HB == 1 && S == 2 ? 4 : 2;
+    constexpr int D = 128 * S, DC = D / (32 * V), G = JOIN_WARPS / (HB * DC);
     constexpr int LOADS = (MAX_PARTS + 31) / 32;
     static_assert(MAX_PARTS + MAX_GROUP_PARTS <= JOIN_WARPS * 32, "a thread per CTA");
-    __shared__ float2 so[G > 1 ? JOIN_WARPS : 1][32];
+    __shared__ float2 so[G > 1 ? JOIN_WARPS : 1][V / 2][32];
     __shared__ int at[JOIN_WARPS * 32], found[2][JOIN_WARPS];
     wait_for_previous_grid();
     allow_dependent_launch();
@@ -207,8 +210,10 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        const int d = dc * 64 + lane * 2;
-        float2 o = make_float2(0.0f, 0.0f);
+        const int d = (dc * 32 + lane) * V;
+        float2 o[V / 2];
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) o[e] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
             if (i * 32 >= n) break;
@@ -216,20 +221,28 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
 #pragma unroll 8
             for (int k = grp; k < top; k += G) {  // G divides 32
                 const float f = __shfl_sync(0xffffffffu, w[i], k);
-                const float2 v = *reinterpret_cast<const float2 *>(work.o + (slot(i * 32 + k) * rows + h) * D + d);
-                o.x = fmaf(f, v.x, o.x);
-                o.y = fmaf(f, v.y, o.y);
+                const float *src = work.o + (slot(i * 32 + k) * rows + h) * D + d;
+                float2 v[V / 2];
+                if constexpr (V == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    v[0] = make_float2(x.x, x.y);
+                    v[1] = make_float2(x.z, x.w);
+                } else {
+                    v[0] = *reinterpret_cast<const float2 *>(src);
+                }
+#pragma unroll
+                for (int e = 0; e < V / 2; ++e) o[e] = __ffma2_rn(make_float2(f, f), v[e], o[e]);
             }
         }
         if constexpr (G > 1) {
-            so[warp][lane] = o;
+#pragma unroll
+            for (int e = 0; e < V / 2; ++e) so[warp][e][lane] = o[e];
             __syncthreads();
             if (grp == 0) {
 #pragma unroll
-                for (int i = 1; i < G; ++i) {
-                    o.x += so[warp + i][lane].x;
-                    o.y += so[warp + i][lane].y;
-                }
+                for (int i = 1; i < G; ++i)
+#pragma unroll
+                    for (int e = 0; e < V / 2; ++e) o[e] = __fadd2_rn(o[e], so[warp + i][e][lane]);
             }
             __syncthreads();
         }
@@ -237,13 +250,16 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
         const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
         const size_t row = (size_t)(part.row + h / per) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + h % per;
         if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
-        if (!QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
-        o = make_float2(o.x * inv, o.y * inv);
-        if (a.gate) {
-            const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d));
-            o = make_float2(gated(o.x, gate.x), gated(o.y, gate.y));
+        if (!QSA_IN(row * D + d + V - 1, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
+#pragma unroll
+        for (int e = 0; e < V / 2; ++e) {
+            float2 y = make_float2(o[e].x * inv, o[e].y * inv);
+            if (a.gate) {
+                const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d + 2 * e));
+                y = make_float2(gated(y.x, gate.x), gated(y.y, gate.y));
+            }
+            store_out(a, row * D + d + 2 * e, y);
         }
-        store_out(a, row * D + d, o);
     }
 }
 

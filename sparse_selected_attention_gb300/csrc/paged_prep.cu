@@ -306,9 +306,9 @@ __global__ void __launch_bounds__(PREP_WARPS * 32, 7) paged_prep_kernel(const qs
 // per (cell, KV head).  A thread takes sixteen dims of one (cell, KV head), of
 // both K and V, so that a warp reads and writes whole rows.  A block takes
 // ids_per_block whole ids, so that an item's id and place need 32-bit
-// arithmetic only.  240 K cells of 2 heads of 256 to bf16, 744 MB: 125 us, 5.95
-// TB/s.
-constexpr int GATHER_THREADS = 256;
+// arithmetic only.  240 K cells of 2 heads of 256 to bf16, 744 MB: 119 us, 6.3 TB/s
+// (256 threads a block 125 us, 64 119 us).
+constexpr int GATHER_THREADS = 128;
 
 struct GatherPlan {
     int per_id, ids_per_block;
@@ -402,10 +402,13 @@ cudaError_t launch_paged_prep(const qsa_paged_prep_args &a, cudaStream_t s) {
 cudaError_t launch_paged_gather(const qsa_paged_gather_args &a, cudaStream_t s) {
     GatherPlan g;
     g.per_id = a.n_kv_heads * (a.head_dim / 16);
-    // Up to four rounds of a block's threads, fewer while that leaves SMs
-    // without blocks (321 cells: 5.3 us with three blocks, 2.1 us with one per id).
-    const int most = 4 * GATHER_THREADS / g.per_id, spread = (int)(((long long)a.n_ids + 607) / 608);
-    g.ids_per_block = spread < most ? spread : most < 1 ? 1 : most;
+    // Up to four rounds of a block's threads (two 120 us, eight 128 us), fewer
+    // while that leaves blocks out (321 cells: 5.3 us with three blocks, 1.9 us
+    // with one per id); a power of two (14.5 K cells of 4 heads of 128: 9.3 us with
+    // 16 ids, 12.5 us with 12).
+    const int most = 4 * GATHER_THREADS / g.per_id;
+    g.ids_per_block = 1;
+    while (2 * g.ids_per_block <= most && (long long)g.ids_per_block * 1216 < a.n_ids) g.ids_per_block *= 2;
     g.magic = g.ids_per_block == 1 ? 0u : (uint32_t)(((1ull << 32) + g.per_id - 1) / g.per_id);
     const dim3 grid((unsigned)(((long long)a.n_ids + g.ids_per_block - 1) / g.ids_per_block)), block(GATHER_THREADS);
     return a.out_dtype == QSA_F32   ? launch_dependent(paged_gather_kernel<float>, grid, block, 0, s, a, g)

@@ -12,8 +12,8 @@
 // launch runs over the whole chip and copies the listed pages; sources and
 // targets are disjoint, so no order among them matters.
 //
-// A compaction that moves 1.04 GB takes 175 us (6.0 TB/s), a fork of 64 rows into
-// 256 with 192 page copies of 16 layers, 227 MB, 39 us, a decode step 8 us.
+// A compaction that moves 1.04 GB takes 164 us (6.3 TB/s), a fork of 64 rows into
+// 256 with its page copies of 16 layers, 227 MB, 36 us, a decode step 8 us.
 //
 // All results are whole numbers and do not depend on the order of the atomic
 // counts.
@@ -485,9 +485,11 @@ __global__ void __launch_bounds__(THREADS) page_compact_kernel(const CompactLaun
 // The listed copies, all layers, codes and scales: bound by reading and writing
 // them.  A block takes a run of cells of one layer's copy, of K or of V, at a
 // time: up to PIECE bytes of codes in 16-byte words, four per thread in flight,
-// and the same cells' scales in 8-byte words.
+// and the same cells' scales in 8-byte words.  Blocks: 32 per SM (8: 174 us, 16: 167
+// us, 32: 164 us for 1.04 GB), pieces of 32 KB (of 16: 36.6 us, of 32: 35.7 us for
+// half-filled pages).
 constexpr int COPY_THREADS = 256;
-constexpr int PIECE = COPY_THREADS * 4 * 16;
+constexpr int PIECE = COPY_THREADS * 8 * 16;
 
 struct CopyLaunch {
     int n_layers, n_pages, page_size, code_row, scale_row, n_copies_max;  // bytes per cell
@@ -544,7 +546,7 @@ cudaError_t launch_copies(const A &a, int n_copies_max, cudaStream_t s) {
                        reinterpret_cast<uint8_t *>(a.kq), reinterpret_cast<uint8_t *>(a.vq),
                        reinterpret_cast<uint8_t *>(a.ksc), reinterpret_cast<uint8_t *>(a.vsc), a.workspace, a.n_rows};
     const long long items = (long long)n_copies_max * 2 * pieces * a.n_layers;
-    const int blocks = (int)(items < 152 * 8 ? (items < 1 ? 1 : items) : 152 * 8);
+    const int blocks = (int)(items < 152 * 32 ? (items < 1 ? 1 : items) : 152 * 32);
     return launch_dependent(page_copy_kernel, dim3(blocks), dim3(COPY_THREADS), 0, s, c);
 }
 

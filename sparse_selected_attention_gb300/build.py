@@ -76,8 +76,8 @@ def lib_path(variant: str = "release") -> str:
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, variant: str = "release") -> str:
-    """Compile and link one variant; returns the library path.  Rebuilds only
-    stale parts."""
+    """Compile and link one variant (with the release one, the binding);
+    returns the library path.  Rebuilds only stale parts."""
     defines, libname = VARIANTS[variant]
     bdir = BUILD if variant == "release" else os.path.join(BUILD, variant)
     lib = os.path.join(PKG, libname)
@@ -94,8 +94,11 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, 
         if force or _stale(o, [s] + headers):
             extra = ["-Xptxas", "-v"] if (ptxas_info and src.endswith(".cu")) else []
             jobs.append([cc, *ARCH, *FLAGS, *defines, *extra, "-c", s, "-o", o])
-    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4)) + 1) as ex:
+        binding = ex.submit(build_binding, verbose, force) if variant == "release" else None
         results = list(ex.map(lambda c: _run(c, verbose), jobs))
+        if binding:
+            binding.result()
     if ptxas_info:
         for r in results:
             sys.stdout.write(r.stderr)
@@ -166,14 +169,13 @@ def build_probe(verbose: bool = False, force: bool = False) -> str:
 
 
 def build_all(verbose: bool = False, force: bool = False) -> list:
-    """Every variant (release first), the variants, the probe and the binding in parallel."""
+    """Every variant (release first), the variants and the probe in parallel."""
+    out = [build(verbose=verbose, force=force)]
     rest = [v for v in VARIANTS if v != "release"]
-    with ThreadPoolExecutor(max_workers=len(rest) + 2) as ex:
-        binding = ex.submit(build_binding, verbose=verbose, force=force)
-        out = [build(verbose=verbose, force=force)]
+    with ThreadPoolExecutor(max_workers=len(rest) + 1) as ex:
         futs = [ex.submit(build, verbose=verbose, force=force, variant=v) for v in rest]
         probe = ex.submit(build_probe, verbose=verbose, force=force)
-        out += [f.result() for f in futs] + [probe.result(), binding.result()]
+        out += [f.result() for f in futs] + [probe.result()]
     return out
 
 
@@ -183,4 +185,3 @@ if __name__ == "__main__":
         print("\n".join(build_all(verbose=v, force="--force" in sys.argv)))
     else:
         print(build(verbose=v, ptxas_info="--ptxas" in sys.argv, force="--force" in sys.argv))
-        print(build_binding(verbose=v, force="--force" in sys.argv))

@@ -1052,3 +1052,50 @@ def test_binding_says_what_the_library_says(cuda_device):
         qsa.qsa_paged_gather(*pd, [0], ko, vo)
     with pytest.raises((ValueError, TypeError)):
         qsa.qsa_paged_gather(*pd, i32(0).expand(2)[:1].to_sparse(), ko, vo)
+
+
+def test_two_calls_at_once(cuda_device):
+    """Calls on two streams, each with its own workspace and outputs, beside
+    one another: rows taken together, rows one by one, and a page table's
+    update, give the bits that they give alone."""
+    rng = np.random.default_rng(38)
+    jobs = []
+    for d, n, held in ((256, 64, 900), (128, 100, 900), (128, 0, 5000)):
+        table, pages = shuffled_table([held] * (1 if n else 6), 32, 4, rng)
+        pool = [dev(x) for x in make_pool(pages, 32, 8, d, seed=39)]
+        rows = [0] * n if n else list(range(6))
+        lens = [held - n + 1 + i for i in range(n)] if n else [held - 700 * i for i in range(6)]
+        assert taken_together(rows, lens, 16, 8, d) == bool(n)
+        q = dev(rng.standard_normal((len(rows), 16, d)).astype(np.float16))
+        jobs.append((q, pool, dev(table), i32(lens), i32(rows), d))
+
+    def state():
+        out = []
+        for q, pool, table, lens, rows, d in jobs:
+            ws = torch.empty(qsa.qsa_paged_attn_workspace_bytes(16, 8, d), dtype=torch.uint8, device="cuda")
+            r = table.shape[0]
+            up = [torch.zeros_like(table), i32([0] * r), torch.zeros(pool[0].shape[0], dtype=torch.int32, device="cuda"), i32([0] * r), i32([0] * r),
+                  torch.empty(qsa.qsa_pages_workspace_bytes(r, pool[0].shape[0]), dtype=torch.uint8, device="cuda")]
+            out.append((torch.empty_like(q), ws, up))
+        return out
+
+    def run(state, stream):
+        for (q, pool, table, lens, rows, d), (out, ws, up) in zip(jobs, state):
+            r = table.shape[0]
+            qsa.qsa_paged_attn(q, *pool, table, lens, out, ws, rows=rows, stream=stream)
+            qsa.qsa_page_update(table, i32([table.shape[1] * 32 - 32] * r), None, i32([1] * r), *pool, *up, stream=stream)
+
+    alone = state()
+    torch.cuda.synchronize()
+    run(alone, None)
+    torch.cuda.synchronize()
+    streams, both = [torch.cuda.Stream() for _ in range(2)], [state() for _ in range(2)]
+    for _ in range(5):
+        torch.cuda.synchronize()
+        for s, st in zip(streams, both):
+            with torch.cuda.stream(s):
+                run(st, s)
+        torch.cuda.synchronize()
+        for st in both:
+            for (out, _, up), (want, _, wup) in zip(st, alone):
+                assert torch.equal(out, want) and all(torch.equal(a, b) for a, b in zip(up[:5], wup[:5]))

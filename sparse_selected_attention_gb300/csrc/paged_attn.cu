@@ -184,7 +184,7 @@ __device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S>
         total_padded += sh.padded[w];
         groups += sh.together[w];
     }
-    if (block && take_groups(a, total, groups, true)) return false;
+    if (block && take_groups<S>(a, total, groups, true)) return false;
     before += s - mine;
     before_padded += sp - padded;
     const long long per = (total + ranges - 1) / ranges;
@@ -834,7 +834,7 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const bool whole = units <= WHOLE || resident == 1;
     const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups(a, units, group_block(per)) ? group_block(per) : 0;
+    const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
     const auto kernel = whole ? paged_attn_kernel<S, true> : paged_attn_kernel<S, false>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, block);

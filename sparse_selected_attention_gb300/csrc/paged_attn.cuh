@@ -73,22 +73,25 @@ __device__ __forceinline__ int units_of(int len) {  // one at least, so that an 
     return max((len + UNIT - 1) / UNIT, 1);
 }
 // alone: units of all rows; together: of the longest row of each group; longer:
-// some row has more than WHOLE.  A group costs what 3 to 3.6 rows cost, and some
-// microseconds more for a few long tiles than for many small units: groups where
-// they save 4096 units of a KV head (33 MB of codes).  One by one and by groups, us:
-//   48/4 heads of 256, 12 sequences: 3 rows of 6 K cells 103, 100; 4 131, 101; 8 241, 113
-//                                    4 rows of 1 K cells 44, 48; 8 69, 58
-//                      1 sequence:   8 rows of 1 K cells 23, 30; of 6 K 42, 35
-//   32/8 heads of 128, 12 sequences: 3 rows of 6 K cells 99, 117; 4 127, 120; 8 236, 120
-//                                    4 rows of 1 K cells 40, 44; 8 62, 46
-//                      1 sequence:   8 rows of 1 K cells 22, 22; of 6 K 36, 28
+// some row has more than WHOLE.  A group costs what 3 to 3.5 rows of 256 dims or
+// 4 of 128 cost, and some microseconds more for a few long tiles than for many
+// small units: groups where they save 4096 units of a KV head (33 MB of codes).
+// One by one and by groups, us:
+//   48/4 heads of 256, 12 sequences: 3 rows of 6 K cells 103, 103; 4 133, 104; 8 241, 115
+//                                    5 rows of 1 K cells 48, 51; 8 66, 58
+//                      1 sequence:   8 rows of 1 K cells 19, 26; of 6 K 38, 30
+//   32/8 heads of 128, 12 sequences: 4 rows of 6 K cells 124, 127; 5 150, 127; 8 231, 128
+//                                    5 rows of 1 K cells 42, 47; 8 57, 48
+//                      1 sequence:   8 rows of 1 K cells 18, 22; of 6 K 32, 27
+template <int S>
 __device__ __forceinline__ bool take_groups(const qsa_paged_attn_args &a, long long alone, long long together, bool longer) {
-    return longer && (2 * alone - 7 * together) * a.n_kv_heads > 2 * 4096;
+    return longer && (2 * alone - (S == 1 ? 8 : 7) * together) * a.n_kv_heads > 2 * 4096;
 }
 // Whether rows of up to `units` units could be: if not, the groups' launch is left out (2 us).
+template <int S>
 inline bool may_take_groups(const qsa_paged_attn_args &a, long long units, int block) {
     const long long groups = a.n_tokens < block ? 1 : a.n_tokens / block;
-    return a.rows && (2ll * a.n_tokens - 7 * groups) * units * a.n_kv_heads > 2 * 4096;
+    return a.rows && (2ll * a.n_tokens - (S == 1 ? 8 : 7) * groups) * units * a.n_kv_heads > 2 * 4096;
 }
 constexpr int GROUP_ROWS = 128;  // heads of a group, all its rows' (the M of its products)
 __host__ __device__ inline int group_block(int per) {

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             v.alone += __shfl_xor_sync(0xffffffffu, v.alone, o);
             v.together += __shfl_xor_sync(0xffffffffu, v.together, o);
         }
-        any = take_groups(a, v.alone, v.together, longer) && take_share(__shfl_sync(0xffffffffu, sum, 31));
+        any = take_groups<S>(a, v.alone, v.together, longer) && take_share(__shfl_sync(0xffffffffu, sum, 31));
         const long long x = (long long)share * range;
         const unsigned here = __ballot_sync(0xffffffffu, any && starts && x >= sum - v.tiles && x < sum);
         t = here ? __ffs(here) - 1 : 0;
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             alone += sums.alone;
             together += sums.together;
         }
-        any = take_groups(a, alone, together, __syncthreads_or(longer)) && take_share(total);
+        any = take_groups<S>(a, alone, together, __syncthreads_or(longer)) && take_share(total);
         const long long x = (long long)share * range;
         long long done = 0;
         for (int base = 0; any && base < a.n_tokens; base += CHUNK) {

@@ -384,11 +384,11 @@ def taken_together(rows, lens, hq, hkv, d):
             while end < len(rows) and end - t < block and rows[end] == rows[t] and (end == t or end % max(block, 64)):
                 end += 1
             together += max(units[t:end])
-    return max(units) > 16 and (2 * sum(units) - 7 * together) * hkv > 8192
+    return max(units) > 16 and (2 * sum(units) - (8 if d == 128 else 7) * together) * hkv > 8192
 
 
 @pytest.mark.parametrize("d,hq,hkv,page,windows,cells", [
-    (128, 8, 8, 64, [128], 600), (128, 12, 1, 64, [8], 30001), (256, 24, 2, 16, [8, 8, 1], 7900), (256, 16, 1, 256, [40], 2950),
+    (128, 8, 8, 64, [128], 600), (128, 12, 1, 64, [8], 33001), (256, 24, 2, 16, [8, 8, 1], 7900), (256, 16, 1, 256, [40], 2950),
     (128, 32, 8, 32, [4, 5, 7, 1, 8, 2, 6, 9, 5, 4, 3, 6], 2000), (256, 6, 3, 64, [67], 700), (128, 15, 3, 128, [90, 1, 30], 1300),
     (256, 8, 8, 32, [300, 210], 290), (128, 2, 2, 16, [512, 188], 1030)])
 def test_attn_rows_taken_together(cuda_device, d, hq, hkv, page, windows, cells):

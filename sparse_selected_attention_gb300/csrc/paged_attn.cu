@@ -55,10 +55,16 @@
 namespace qsa {
 namespace {
 
-constexpr int NW = 4;           // warps per CTA
+constexpr int NW = 4;           // warps per CTA, where a row's are not one
 constexpr int CTAS_PER_SM = 2;  // 255 registers a thread
 constexpr int MAX_CTAS = 152 * CTAS_PER_SM;
 static_assert(MAX_CTAS <= MAX_PARTS && WHOLE == 4 * NW, "shared with the join and the groups");
+// A warp per row, six to an SM, where the table holds up to SMALL units and there
+// are more rows and KV heads than CTAs of four warps; of more than two units,
+// twice as many.  Four warps and one, us: 156 rows, 48/8 heads of 128, one cell 24,
+// 16, 64 cells 28, 21, 128 cells 29, 29; 24/4 heads of 256, one cell 17, 11, 64 cells
+// 19, 17, but 80 rows of 64 cells 13, 15.
+constexpr int SMALL = 4, SMALL_PER_SM = 6;
 constexpr int TILE = 4096;      // a unit's K or V codes
 // Fewest units of a share, one per warp: finer ones would only add partials.
 constexpr int MIN_SHARE = NW;
@@ -107,19 +113,19 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool pr
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(dst), "l"(src), "r"(pred ? 8 : 0));
 }
 
-// Shared memory of a CTA.
-template <int S>
+// Shared memory of a CTA of W warps.
+template <int S, int W>
 struct Smem {
-    uint8_t tile[NW][2][2][TILE];                  // stage, K or V: [S][UNIT][128] codes; 1024-byte aligned
-    uint2 scale[NW][2][2][Shape<S>::UNIT];         // four fp16 per cell
+    uint8_t tile[W][2][2][TILE];                  // stage, K or V: [S][UNIT][128] codes; 1024-byte aligned
+    uint2 scale[W][2][2][Shape<S>::UNIT];         // four fp16 per cell
     uint4 q[8 * S][32];                            // Q fragments by k-step and lane
     float bias[4][8][4];                           // -1152 * sum of q over a scale group, as accumulators: heads g, g, g + 8, g + 8
     float qinv[16];                                // 2^-e of a head's scaled query
-    float o[NW][16][128];                          // 128 dims of the warps' values, at the end of a segment
-    float m[NW][16], l[NW][16], f[NW][16];
-    int v[NW];                                     // the warps' V exponents
-    uint64_t bar[NW][2];
-    long long together[NW], padded[NW], scan[NW];
+    float o[W][16][128];                          // 128 dims of the warps' values, at the end of a segment
+    float m[W][16], l[W][16], f[W][16];
+    int v[W];                                     // the warps' V exponents
+    uint64_t bar[W][2];
+    long long together[W], padded[W], scan[W];
     long long total, before;                       // units of all rows; of the rows before `row`
     int row, left;                                 // the share's units
 };
@@ -131,7 +137,7 @@ struct Smem {
 // 12 us; 23 us where a share took four of them, one after the other).  False: the
 // rows are taken by groups (block 0: there are none).
 template <int S>
-__device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S> &sh, int range, int ranges, int block, int &share) {
+__device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S, NW> &sh, int range, int ranges, int block, int &share) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (a.n_tokens + NW * 32 - 1) / (NW * 32);
     const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
@@ -221,18 +227,18 @@ __device__ __forceinline__ bool find_start(const qsa_paged_attn_args &a, Smem<S>
 // fp16, with the sums that undo the codes' 1152.  bf16 queries are scaled by
 // a power of two per head where they would leave the fp16 range; fp16 ones
 // are used as they are.  A negative softmax scale flips their sign.  A warp
-// takes every NW-th head; the loads are apart from the rest, so that a
+// takes every W-th head; the loads are apart from the rest, so that a
 // segment's can be in flight while the one before ends.
-template <int S>
+template <int S, int W>
 struct Query {
-    static constexpr int D = Shape<S>::D, N = D / 32, H = 16 / NW;
+    static constexpr int D = Shape<S>::D, N = D / 32, H = 16 / W;
     uint32_t raw[H][N / 2];
 
     __device__ __forceinline__ void load(const qsa_paged_attn_args &a, int t, int kvh, int per) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const int h = warp + i * NW;
+            const int h = warp + i * W;
             const size_t at = ((size_t)t * a.n_q_heads + (size_t)kvh * per + h) * D + lane * N;
 #pragma unroll
             for (int e = 0; e < N / 2; ++e) raw[i][e] = 0u;
@@ -246,11 +252,11 @@ struct Query {
         }
     }
 
-    __device__ __forceinline__ void store(const qsa_paged_attn_args &a, Smem<S> &sh) const {
+    __device__ __forceinline__ void store(const qsa_paged_attn_args &a, Smem<S, W> &sh) const {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
         for (int i = 0; i < H; ++i) {
-            const int h = warp + i * NW;
+            const int h = warp + i * W;
             float x[N], top = 0.0f;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
@@ -507,12 +513,12 @@ struct Feed {
 };
 
 // WHOLE_ROWS: no row is shared out.
-template <int S, bool WHOLE_ROWS>
-__global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
+template <int S, int W, bool WHOLE_ROWS>
+__global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
     paged_attn_kernel(const qsa_paged_attn_args a, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, int block) {
     extern __shared__ __align__(1024) uint8_t raw[];
-    Smem<S> &sh = *reinterpret_cast<Smem<S> *>(raw);
+    Smem<S, W> &sh = *reinterpret_cast<Smem<S, W> *>(raw);
     constexpr int D = Shape<S>::D, UNIT = Shape<S>::UNIT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, r = lane & 3;
     const int per = a.n_q_heads / a.n_kv_heads, page_shift = 31 - __clz(a.page_size);
@@ -528,7 +534,8 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     // This CTA's units: `left` of them from unit u0 of row t on, or of whole
     // rows every ranges-th from row `range`.
     int share = 0, t = range, u0 = 0, left = 0x7fffffff;
-    bool none = !WHOLE_ROWS && !find_start<S>(a, sh, range, ranges, block, share);
+    bool none = false;
+    if constexpr (!WHOLE_ROWS) none = !find_start<S>(a, sh, range, ranges, block, share);
     const int step = share ? 1 : ranges;
     if (share) {
         const long long x = (long long)share * range, total = sh.total;
@@ -623,12 +630,12 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
                 }
             }
         }
-        f.u += NW;
+        f.u += W;
         settle();
         return vmask;
     };
 
-    Query<S> q;
+    Query<S, W> q;
     q.load(a, t, kvh, per);
     peek();
     settle();
@@ -640,9 +647,9 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
     __syncthreads();  // the query fragments
 
     for (bool first = true;; first = false) {
-        // Segment: units u0 .. u1-1 of row t; this warp's are u0 + warp, + NW ...
+        // Segment: units u0 .. u1-1 of row t; this warp's are u0 + warp, + W ...
         const int u1 = min(nu, u0 + left), n_units = u1 - u0;
-        const int n = n_units > warp ? (n_units - warp + NW - 1) / NW : 0;
+        const int n = n_units > warp ? (n_units - warp + W - 1) / W : 0;
         // |scale| in base 2, floored at the smallest normal float: with scale
         // 0 the weights are uniform and a masked -inf stays -inf.
         const float sl2[2] = {fmaxf(fabsf(a.softmax_scale) * LOG2E * sh.qinv[g], 1.17549435e-38f),
@@ -714,17 +721,17 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
             __syncthreads();
             if (half == 0) {
                 if (tid < 16) {
-                    float M = -CUDART_INF_F, L = 0.0f, w[NW];
+                    float M = -CUDART_INF_F, L = 0.0f, w[W];
 #pragma unroll
-                    for (int p = 0; p < NW; ++p) M = fmaxf(M, sh.m[p][tid]);
+                    for (int p = 0; p < W; ++p) M = fmaxf(M, sh.m[p][tid]);
 #pragma unroll
-                    for (int p = 0; p < NW; ++p) {
+                    for (int p = 0; p < W; ++p) {
                         w[p] = sh.m[p][tid] == -CUDART_INF_F ? 0.0f : exp2f(sh.m[p][tid] - M);
                         L += w[p] * sh.l[p][tid];
                     }
                     const float inv = whole ? (M == -CUDART_INF_F ? 0.0f : 1.0f / L) : 1.0f;
 #pragma unroll
-                    for (int p = 0; p < NW; ++p) sh.f[p][tid] = w[p] == 0.0f ? 0.0f : w[p] * inv * exp2i(sh.v[p]);
+                    for (int p = 0; p < W; ++p) sh.f[p][tid] = w[p] == 0.0f ? 0.0f : w[p] * inv * exp2i(sh.v[p]);
                     if (tid < per) {
                         if (!whole)
                             *reinterpret_cast<float2 *>(work.ml + (at * per + tid) * 2) = make_float2(M, L);
@@ -734,39 +741,41 @@ __global__ void __launch_bounds__(NW * 32, CTAS_PER_SM)
                 }
                 __syncthreads();
             }
-            // A warp takes 64 dims of every other head, BATCH heads at a time
+            // A warp takes 64 dims of every ROWS-th head, BATCH heads at a time
             // with their gates on the way together.
-            constexpr int BATCH = 4;
-            const int d = 64 * (warp & 1) + 2 * lane, dd = 128 * half + d;
+            constexpr int BATCH = 4, COLS = W > 1 ? 2 : 1, ROWS = W / COLS;
             const size_t row0 = (size_t)t * a.n_q_heads + (size_t)kvh * per;
-            for (int h0 = warp >> 1; h0 < per; h0 += 2 * BATCH) {
-                float2 gate[BATCH], y[BATCH];
+            for (int dc = warp % COLS; dc < 2; dc += COLS) {
+                const int d = 64 * dc + 2 * lane, dd = 128 * half + d;
+                for (int h0 = warp / COLS; h0 < per; h0 += ROWS * BATCH) {
+                    float2 gate[BATCH], y[BATCH];
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int h = h0 + 2 * k;
-                    gate[k] = a.gate && whole && h < per && QSA_IN((row0 + h) * D + dd + 1, (size_t)a.n_tokens * a.n_q_heads * D)
-                                  ? __ldg(reinterpret_cast<const float2 *>(a.gate + (row0 + h) * D + dd))
-                                  : make_float2(0.0f, 0.0f);
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int h = min(h0 + 2 * k, per - 1), pd = d ^ (8 * (h & 3));
-                    y[k] = make_float2(0.0f, 0.0f);
-#pragma unroll
-                    for (int p = 0; p < NW; ++p) {
-                        const float w = sh.f[p][h];
-                        y[k] = __ffma2_rn(*reinterpret_cast<const float2 *>(&sh.o[p][h][pd]), make_float2(w, w), y[k]);
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int h = h0 + ROWS * k;
+                        gate[k] = a.gate && whole && h < per && QSA_IN((row0 + h) * D + dd + 1, (size_t)a.n_tokens * a.n_q_heads * D)
+                                      ? __ldg(reinterpret_cast<const float2 *>(a.gate + (row0 + h) * D + dd))
+                                      : make_float2(0.0f, 0.0f);
                     }
-                }
 #pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    const int h = h0 + 2 * k;
-                    if (h >= per) break;
-                    if (!whole) {
-                        *reinterpret_cast<float2 *>(work.o + (at * per + h) * D + dd) = y[k];
-                    } else if (QSA_IN((row0 + h) * D + dd + 1, (size_t)a.n_tokens * a.n_q_heads * D)) {
-                        if (a.gate) y[k] = make_float2(gated(y[k].x, gate[k].x), gated(y[k].y, gate[k].y));
-                        store_out(a, (row0 + h) * D + dd, y[k]);
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int h = min(h0 + ROWS * k, per - 1), pd = d ^ (8 * (h & 3));
+                        y[k] = make_float2(0.0f, 0.0f);
+#pragma unroll
+                        for (int p = 0; p < W; ++p) {
+                            const float w = sh.f[p][h];
+                            y[k] = __ffma2_rn(*reinterpret_cast<const float2 *>(&sh.o[p][h][pd]), make_float2(w, w), y[k]);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < BATCH; ++k) {
+                        const int h = h0 + ROWS * k;
+                        if (h >= per) break;
+                        if (!whole) {
+                            *reinterpret_cast<float2 *>(work.o + (at * per + h) * D + dd) = y[k];
+                        } else if (QSA_IN((row0 + h) * D + dd + 1, (size_t)a.n_tokens * a.n_q_heads * D)) {
+                            if (a.gate) y[k] = make_float2(gated(y[k].x, gate[k].x), gated(y[k].y, gate[k].y));
+                            store_out(a, (row0 + h) * D + dd, y[k]);
+                        }
                     }
                 }
             }
@@ -835,9 +844,16 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
-    const auto kernel = whole ? paged_attn_kernel<S, true> : paged_attn_kernel<S, false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S>));
-    if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S>), s, a, kmap, vmap, block);
+    if (whole && units <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
+        const int small = (int)std::min<long long>(a.n_tokens, std::max(152 * SMALL_PER_SM / a.n_kv_heads, 1));
+        e = cudaFuncSetAttribute(paged_attn_kernel<S, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, 1>));
+        return e != cudaSuccess ? e
+                                : launch_dependent(paged_attn_kernel<S, 1, true>, dim3(small * a.n_kv_heads), dim3(32), sizeof(Smem<S, 1>), s, a,
+                                                   kmap, vmap, 0);
+    }
+    const auto kernel = whole ? paged_attn_kernel<S, NW, true> : paged_attn_kernel<S, NW, false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, NW>));
+    if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S, NW>), s, a, kmap, vmap, block);
     if (e != cudaSuccess || whole) return e;
     const Joined one{a.workspace, MAX_CTAS, per, grid};
     Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};

@@ -294,6 +294,27 @@ def test_attn_split_lengths(cuda_device, rows_n, lo, hi, page):
     assert err == 0
 
 
+@pytest.mark.parametrize("d,hq,hkv,page,n,most", [
+    (128, 8, 8, 16, 40, 16), (128, 16, 1, 64, 320, 64), (128, 24, 4, 128, 160, 128), (256, 12, 4, 16, 90, 16), (256, 16, 2, 32, 170, 32),
+    (256, 10, 10, 64, 70, 64), (128, 320, 160, 16, 3, 16)])
+def test_attn_many_short_rows(cuda_device, d, hq, hkv, page, n, most):
+    """More short rows than blocks: a warp each, several rows to a warp, with
+    empty rows, bad pages and all head counts; gated and with lse."""
+    rng = np.random.default_rng(n)
+    lens = [int(v) for v in rng.integers(0, most + 1, n)]
+    lens[:3] = [most, 0, 1]
+    table, pages = shuffled_table(lens, page, 1, rng, wide=most // page)
+    pool = make_pool(pages, page, hkv, d, seed=40)
+    q = rng.standard_normal((n, hq, d)) * 2
+    gate = wl.gates_f32(n, seed=6, heads=hq, head_dim=d)
+    for otype in (F16, BF16):
+        _, err = check_attn(q, pool, table, lens, gate=gate, otype=otype)
+        assert err == 0
+    table[0, 0] = -7
+    out, err = check_attn(q, pool, table, lens, rows=list(range(n)))
+    assert err == qsa.QSA_DEVERR_BAD_ID and not out[1].any()
+
+
 def test_attn_draft_window_shares_a_sequence(cuda_device):
     """Eight rows of one sequence, each a cell longer, and the order of rows
     and columns unlike the table's; gated, wide heads."""

@@ -404,10 +404,11 @@ typedef struct {
  *   w_c = exp(s_c - max s);  O = sum w_c v_c / sum w_c,  v_c = vsc * vq
  *   out = O, or with a gate O / (1 + exp(-gate)), rounded to dtype
  *   lse[t,h] = max s + log(sum w_c)   (natural logarithm; lse may be NULL)
- * A row of length 0 gives out = +0 and lse = -inf.  A length below 0 or above
- * max_pages * page_size is cut to that range, a table row outside [0, n_rows)
- * counts as length 0, and a table entry outside the pool leaves its page's
- * cells out; each of these sets QSA_DEVERR_BAD_ID.
+ * A row of length 0 gives out = +0 and lse = -inf; a NaN among a head's scores
+ * gives NaN for both.  A length below 0 or above max_pages * page_size is cut
+ * to that range, a table row outside [0, n_rows) counts as length 0, and a
+ * table entry outside the pool leaves its page's cells out; each of these sets
+ * QSA_DEVERR_BAD_ID.
  *
  * q, out [n_tokens, n_q_heads, head_dim] in dtype (QSA_F16 or QSA_BF16); gate
  * NULL or fp32 of that shape; lse fp32 [n_tokens, n_q_heads]; seq_lens, rows

@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
                         if (!whole)
                             *reinterpret_cast<float2 *>(work.ml + (at * per + tid) * 2) = make_float2(M, L);
                         else if (a.lse)
-                            a.lse[(size_t)t * a.n_q_heads + kvh * per + tid] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+                            a.lse[(size_t)t * a.n_q_heads + kvh * per + tid] = lse_of(M, L);
                     }
                 }
                 __syncthreads();

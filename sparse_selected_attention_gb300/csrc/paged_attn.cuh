@@ -131,6 +131,9 @@ __device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i
     else
         *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(y.x, y.y);
 }
+// lse of a base-2 maximum and sum.  A row without cells has -inf and 0, which
+// gives -inf; one whose scores are all NaN has -inf and NaN, which gives NaN.
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * LN2; }
 // y / (1 + exp(-gate)); each step off by a few 2^-23, and a gate far below 0 gives 0.
 __device__ __forceinline__ float gated(float y, float gate) { return __fdividef(y, 1.0f + ex2(-gate * LOG2E)); }
 
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(JOIN_WARPS * 32)
         if (grp || h >= part.tokens * per) continue;
         const float inv = M == -CUDART_INF_F ? 0.0f : 1.0f / L;
         const size_t row = (size_t)(part.row + h / per) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + h % per;
-        if (dc == 0 && lane == 0 && a.lse) a.lse[row] = M == -CUDART_INF_F ? M : (M + log2f(L)) * LN2;
+        if (dc == 0 && lane == 0 && a.lse) a.lse[row] = lse_of(M, L);
         if (!QSA_IN(row * D + d + V - 1, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
 #pragma unroll
         for (int e = 0; e < V / 2; ++e) {

@@ -737,7 +737,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (!whole)
                         *reinterpret_cast<float2 *>(work.ml + (at * M + m) * 2) = make_float2(ref, l);
                     else if (a.lse)
-                        a.lse[head_row(m)] = none ? ref : (ref + log2f(l)) * LN2;
+                        a.lse[head_row(m)] = lse_of(ref, l);
                 }
                 fence_before();  // O is overwritten by the next segment
             }

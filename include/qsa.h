@@ -419,10 +419,13 @@ typedef struct {
  * concurrently (graphs that replay on different streams need one each).
  * The work is divided over the cached cells of all rows, so the last bits of
  * a row's results may depend on the other rows' lengths and on max_pages; the
- * same call gives the same bits.  Range: scores and sums are fp32; K scales of any fp16 value, V
- * scales below 2^15.
+ * same call gives the same bits.  Range: scores and sums are fp32; finite K
+ * scales of any size, V scales below 2^15.
  * An infinite or NaN V scale makes the dims it scales NaN or infinite in the
- * rows that attend to its cell, and in no other.
+ * rows that attend to its cell, and in no other.  An infinite or NaN K scale
+ * (qsa_paged_prep leaves one for a group with such a value) makes the cell's
+ * scores NaN, and with them out and lse of its KV head's query heads in the
+ * rows that attend to it, and in no other.
  * Supported: n_q_heads a multiple of n_kv_heads, 1..16 query heads per KV
  * head; max_pages * page_size up to 2^30.  q, out, kq, vq 16-byte aligned; ksc, vsc, gate 8-byte; the rest 4-byte.
  */

@@ -49,6 +49,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "paged_attn.cuh"
 
@@ -300,6 +301,7 @@ struct State {
     float o[16 * S][4];  // o[t][0..1]: head g, dims 8 t + 2 r, 8 t + 2 r + 1; o[t][2..3]: head g + 8
     float m[2], l[2];
     int v;  // values are in units of 2^v
+    uint32_t k;  // the largest |K scale| that this lane has seen, as bits, in two halves
 };
 
 // Folds one staged unit into the state.  vmask: the unit's valid cells.  EXACT:
@@ -325,6 +327,10 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     auto odd = [&](uint32_t w) { return h2u(__hsub2(u2h(odd_codes(w)), off)); };
     auto k_even = [&](uint32_t w) { return EXACT ? even(w) : even_codes(w); };
     auto k_odd = [&](uint32_t w) { return EXACT ? odd(w) : odd_codes(w); };
+
+    // A cell that is not there has scales of 0.
+    const uint2 kown = KS[lane % UNIT];
+    st.k = __vimax3_u16x2(st.k, kown.x & 0x7FFF7FFFu, kown.y & 0x7FFF7FFFu);
 
     // Scores: per scale group S 32-dim blocks of two k-steps from -1152 sum q,
     // then the scale.
@@ -660,6 +666,7 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
         st.m[0] = st.m[1] = -CUDART_INF_F;
         st.l[0] = st.l[1] = 0.0f;
         st.v = -64;  // below any scale's exponent: the first unit sets it
+        st.k = 0u;
         for (int i = 0; i < n; ++i) {
             if (!ahead) vmask = issue(stage);
             const unsigned vnext = issue(stage ^ 1);
@@ -688,6 +695,16 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
         for (int o = 1; o < 4; o <<= 1) {
             st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], o);
             st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], o);
+        }
+        // A cell with an infinite or NaN K scale scores NaN, and its row's heads
+        // are NaN: said here, once, since the scale times the codes' sum can be
+        // -inf, a cell left out.
+        if (__any_sync(0xffffffffu, max(st.k & 0xFFFFu, st.k >> 16) >= 0x7C00u)) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                st.m[e] = fmaxf(st.m[e], -FLT_MAX);
+                st.l[e] = CUDART_NAN_F;
+            }
         }
         left -= n_units;
         const int next = t + step;

@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     sh.vb[b][fcell] = sh.there[st][fcell] ? -(float)ev : -CUDART_INF_F;
                     sh.vw[b][fcell] = exp2i(ev);
                 }
+                // An infinite or NaN K scale: the low parts are NaN, and the cell's scores.
                 convert(0, k, h2u(scaled(ks, lane & 3, ek)));
                 mbar_arrive(smem_u32(&sh.k_full));
                 return true;

@@ -51,6 +51,12 @@ def attend(q, pool, table, lens, rows, otype):
     return out, lse
 
 
+def row_cells(table, lens, rows, t):
+    r = t if rows is None else rows[t]
+    c = np.arange(lens[t])
+    return table[r, c // 16], c % 16
+
+
 @pytest.mark.parametrize("otype", [F16, BF16])
 @pytest.mark.parametrize("d", [128, 256])
 @pytest.mark.parametrize("form", FORMS)
@@ -72,6 +78,36 @@ def test_all_scores_nan(cuda_device, form, d, otype):
     assert torch.equal(out[~nan], want[~nan]) and torch.equal(lse[~nan], wlse[~nan])
     empty = lens.index(0)
     assert not out[empty].any() and torch.isneginf(lse[empty]).all()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("codes", ["zero", "against", "along"])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("form", FORMS)
+def test_k_scale_not_finite(cuda_device, form, d, codes, value):
+    """A K scale that is infinite or NaN (as a quantised row with an infinite or
+    NaN value has it, its codes 0) makes its cell's scores NaN whatever their
+    sign would be: out and lse of its KV head are NaN in the rows that attend
+    to the cell, and nothing else changes."""
+    q, pool, table, lens, rows = batch(form, d)
+    otype, per, head = F16, 4, 2
+    t = 3 if form != "whole" else 0
+    page, at = (x[lens[t] - 1] for x in row_cells(table, lens, rows, t))
+    # Every row attends with one sign of q in the scale's dims, so that a score
+    # with this scale outside of the sum would be infinite of the other or the same sign.
+    q[..., d // 4:d // 2] = np.abs(q[..., d // 4:d // 2])
+    pool = [x.copy() for x in pool]
+    pool[0][page, at, head, d // 4:d // 2] = {"zero": 0, "against": -3, "along": 3}[codes]
+    want, wlse = attend(q, pool, table, lens, rows, otype)
+    pool[2][page, at, head, 1] = value
+    out, lse = attend(q, pool, table, lens, rows, otype)
+    nan = torch.zeros_like(lse, dtype=torch.bool)
+    for u, n in enumerate(lens):
+        p, a = row_cells(table, lens, rows, u)
+        if ((p == page) & (a == at)).any():
+            nan[u, head * per:(head + 1) * per] = True
+    assert nan.any() and torch.isnan(out[nan]).all() and torch.isnan(lse[nan]).all()
+    assert torch.equal(out[~nan], want[~nan]) and torch.equal(lse[~nan], wlse[~nan])
 
 
 @pytest.mark.parametrize("d", [128, 256])

@@ -16,7 +16,7 @@ built by build_all():
 and libqsa_l2probe.so, the benchmark's L2 gather-rate probe.
 
 _paged_binding.so, the paged calls' argument marshalling, is host code against
-the installed torch; it is given the library's entry points and links none.
+the installed torch (left out where there is none); it is given the library's entry points and links none.
 """
 from __future__ import annotations
 
@@ -76,8 +76,8 @@ def lib_path(variant: str = "release") -> str:
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, variant: str = "release") -> str:
-    """Compile and link one variant (with the release one, the binding);
-    returns the library path.  Rebuilds only stale parts."""
+    """Compile and link one variant (with the release one the binding, where
+    torch is installed); returns the library path.  Rebuilds only stale parts."""
     defines, libname = VARIANTS[variant]
     bdir = BUILD if variant == "release" else os.path.join(BUILD, variant)
     lib = os.path.join(PKG, libname)
@@ -97,15 +97,15 @@ def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, 
     with ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4)) + 1) as ex:
         binding = ex.submit(build_binding, verbose, force) if variant == "release" else None
         results = list(ex.map(lambda c: _run(c, verbose), jobs))
+        if ptxas_info:
+            for r in results:
+                sys.stdout.write(r.stderr)
+        if force or jobs or _stale(lib, objs):
+            tmp = lib + ".tmp"
+            _run([cc, *ARCH, "-shared", "-o", tmp, *objs], verbose)
+            os.replace(tmp, lib)
         if binding:
-            binding.result()
-    if ptxas_info:
-        for r in results:
-            sys.stdout.write(r.stderr)
-    if force or jobs or _stale(lib, objs):
-        tmp = lib + ".tmp"
-        _run([cc, *ARCH, "-shared", "-o", tmp, *objs], verbose)
-        os.replace(tmp, lib)
+            binding.result()  # the library is there, whatever comes of its Python binding
     return lib
 
 
@@ -135,14 +135,18 @@ def build_host_sanitized(verbose: bool = False) -> str:
 BINDING = os.path.join(PKG, "_paged_binding.so")
 
 
-def build_binding(verbose: bool = False, force: bool = False) -> str:
-    """_paged_binding.so, for this interpreter and its torch."""
+def build_binding(verbose: bool = False, force: bool = False) -> str | None:
+    """_paged_binding.so, for this interpreter and its torch; None without torch
+    (the library does without it, and the binding's tensors are torch's)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return None
     src = os.path.join(CSRC, "paged_binding.cpp")
     if force or _stale(BINDING, [src, os.path.join(INCLUDE, "qsa.h")]):
         gxx = shutil.which("g++")
         if not gxx:
             raise RuntimeError("g++ not found")
-        torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+        torch = os.path.dirname(spec.origin)
         cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
         includes = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                     sysconfig.get_paths()["include"], os.path.join(cuda_home, "include")]

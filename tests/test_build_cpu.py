@@ -1,0 +1,59 @@
+"""What the build makes, and from what, with the compilers replaced by a
+recorder that leaves an empty output file."""
+import importlib.util
+import os
+
+import pytest
+
+from sparse_selected_attention_gb300 import build
+
+
+@pytest.fixture
+def made(tmp_path, monkeypatch):
+    """The outputs of the commands that ran, in order; all files in a folder of the test's own."""
+    names = []
+
+    def run(cmd, verbose):
+        out = cmd[cmd.index("-o") + 1]
+        open(out, "w").close()
+        names.append(os.path.basename(out).removesuffix(".tmp"))
+
+        class Result:
+            stdout = stderr = ""
+        return Result
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "_build"))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_paged_binding.so"))
+    monkeypatch.setattr(build, "_run", run)
+    return names
+
+
+def without_torch(monkeypatch):
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+
+
+def test_the_library_builds_without_torch(made, tmp_path, monkeypatch):
+    without_torch(monkeypatch)
+    lib = build.build()
+    assert os.path.exists(lib) and made[-1] == "libqsa.so" and "_paged_binding.so" not in made
+    assert not (tmp_path / "_paged_binding.so").exists()
+
+
+def test_a_binding_that_does_not_build_leaves_the_library(made, tmp_path, monkeypatch):
+    def broken(*args):
+        raise RuntimeError("no headers")
+    monkeypatch.setattr(build, "build_binding", broken)
+    with pytest.raises(RuntimeError, match="no headers"):
+        build.build()
+    assert (tmp_path / "libqsa.so").exists()
+
+
+def test_the_library_and_its_binding(made, tmp_path):
+    build.build()
+    assert sorted(made) == sorted([s + ".o" for s in build.SOURCES] + ["libqsa.so", "_paged_binding.so"])
+    made.clear()
+    build.build()
+    assert made == []
+    build.build(variant="check")
+    assert "_paged_binding.so" not in made and made[-1] == "libqsa_check.so"

@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import runpy
 import shutil
 import subprocess
 import sys
@@ -135,26 +136,55 @@ def build_host_sanitized(verbose: bool = False) -> str:
 BINDING = os.path.join(PKG, "_paged_binding.so")
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else os.path.dirname(spec.origin)
+
+
+def torch_version() -> str:
+    """torch.__version__ of the installed torch, which is not imported for it."""
+    return runpy.run_path(os.path.join(_torch_dir(), "version.py"))["__version__"]
+
+
+def abi_tag() -> str:
+    return sysconfig.get_config_var("SOABI")
+
+
+def binding_stamp() -> str:
+    """The file that says which torch and interpreter the binding was built for."""
+    return os.path.join(BUILD, "_paged_binding.for")
+
+
 def build_binding(verbose: bool = False, force: bool = False) -> str | None:
     """_paged_binding.so, for this interpreter and its torch; None without torch
-    (the library does without it, and the binding's tensors are torch's)."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None:
+    (the library does without it, and the binding's tensors are torch's).  It
+    reads tensors by the layout in torch's headers, so it is rebuilt for another
+    torch, and carries the version, which paged.py compares."""
+    torch = _torch_dir()
+    if torch is None:
         return None
-    src = os.path.join(CSRC, "paged_binding.cpp")
+    src, stamp, made_for = os.path.join(CSRC, "paged_binding.cpp"), binding_stamp(), f"{torch_version()} {abi_tag()}"
+    if os.path.exists(stamp):
+        with open(stamp) as f:
+            force |= f.read() != made_for
+    else:
+        force = True
     if force or _stale(BINDING, [src, os.path.join(INCLUDE, "qsa.h")]):
         gxx = shutil.which("g++")
         if not gxx:
             raise RuntimeError("g++ not found")
-        torch = os.path.dirname(spec.origin)
         cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
         includes = [INCLUDE, os.path.join(torch, "include"), os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                     sysconfig.get_paths()["include"], os.path.join(cuda_home, "include")]
         lib = os.path.join(torch, "lib")
         tmp = BINDING + ".tmp"
-        _run([gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", *(x for i in includes for x in ("-I", i)), src, "-o", tmp,
+        _run([gxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f'-DQSA_TORCH_VERSION="{torch_version()}"',
+              f'-DQSA_ABI_TAG="{abi_tag()}"', *(x for i in includes for x in ("-I", i)), src, "-o", tmp,
               "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], verbose)
         os.replace(tmp, BINDING)
+        os.makedirs(BUILD, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(made_for)
     return BINDING
 
 

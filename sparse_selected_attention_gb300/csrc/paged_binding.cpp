@@ -268,4 +268,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_binding", nullptr, -1, meth
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged_binding() { return PyModule_Create(&module); }
+// With the torch and the interpreter that it was compiled for: tensors are read
+// by the layout in that torch's headers.
+PyMODINIT_FUNC PyInit__paged_binding() {
+    PyObject *m = PyModule_Create(&module);
+    if (m && (PyModule_AddStringConstant(m, "torch_version", QSA_TORCH_VERSION) < 0 ||
+              PyModule_AddStringConstant(m, "abi_tag", QSA_ABI_TAG) < 0))
+        Py_CLEAR(m);
+    return m;
+}

@@ -12,17 +12,28 @@ everything the kernels index by is a shape that was checked here.
 from __future__ import annotations
 
 import struct
+import sysconfig
 
 import torch
 
 from . import _abi
 
-try:
-    from . import _paged_binding as _native
-except ImportError as e:
-    raise RuntimeError("_paged_binding.so is missing or of another torch: build it with "
-                       "`python -m sparse_selected_attention_gb300.build --all`") from e
 
+def binding_of_this_torch():
+    """The compiled binding, if it was built for the torch and interpreter that run."""
+    how = "build it with `python -m sparse_selected_attention_gb300.build --all`"
+    try:
+        from . import _paged_binding as native
+    except ImportError as e:
+        raise RuntimeError(f"_paged_binding.so is missing or of another torch: {how}") from e
+    made_for = (getattr(native, "torch_version", None), getattr(native, "abi_tag", None))
+    here = (torch.__version__, sysconfig.get_config_var("SOABI"))
+    if made_for != here:
+        raise RuntimeError(f"_paged_binding.so is for torch {made_for[0]} ({made_for[1]}), this is {here[0]} ({here[1]}): {how}")
+    return native
+
+
+_native = binding_of_this_torch()
 F32, F16, BF16, I32, I8 = torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int8
 _CODE = {F32: _abi.QSA_F32, F16: _abi.QSA_F16, BF16: _abi.QSA_BF16}
 # The raw handle of the current stream and the current device's number: what

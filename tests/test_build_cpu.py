@@ -57,3 +57,42 @@ def test_the_library_and_its_binding(made, tmp_path):
     assert made == []
     build.build(variant="check")
     assert "_paged_binding.so" not in made and made[-1] == "libqsa_check.so"
+
+
+# ---------------------------------------------------------------- the binding's torch
+
+def test_a_binding_of_another_torch_is_rebuilt(made, tmp_path, monkeypatch):
+    build.build()
+    made.clear()
+    for name in ("torch_version", "abi_tag"):
+        with monkeypatch.context() as m:
+            m.setattr(build, name, lambda: "another")
+            build.build()
+            assert made == ["_paged_binding.so"], name
+            build.build()
+            assert made == ["_paged_binding.so"], name
+        made.clear()
+        build.build()
+        assert made == ["_paged_binding.so"], name  # and back
+        made.clear()
+    os.remove(build.binding_stamp())  # a file whose torch is not known
+    build.build()
+    assert made == ["_paged_binding.so"]
+
+
+def test_what_is_compiled_in_is_what_is_loaded():
+    import torch
+    build.build()
+    from sparse_selected_attention_gb300 import _paged_binding, paged
+    assert _paged_binding.torch_version == torch.__version__ == build.torch_version()
+    assert _paged_binding.abi_tag == build.abi_tag()
+    assert paged.binding_of_this_torch() is _paged_binding
+
+
+@pytest.mark.parametrize("name", ["torch_version", "abi_tag"])
+def test_a_binding_of_another_torch_is_refused(monkeypatch, name):
+    build.build()
+    from sparse_selected_attention_gb300 import _paged_binding, paged
+    monkeypatch.setattr(_paged_binding, name, "1.2.3")
+    with pytest.raises(RuntimeError, match="1.2.3.*sparse_selected_attention_gb300.build"):
+        paged.binding_of_this_torch()

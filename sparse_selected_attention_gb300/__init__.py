@@ -24,6 +24,7 @@ ksc, vsc [layers, pages, page, Hkv, 4], page_table [rows, max_pages], seq_lens
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 
 from . import _abi
@@ -32,10 +33,16 @@ from ._abi import (QSA_DEVERR_BAD_ID, QSA_DEVERR_NO_PAGES, QSA_DEVERR_TIMEOUT,  
 
 __all__ = ["qsa_prep", "qsa_score", "qsa_score_noalloc", "qsa_select", "qsa_attn", "qsa_score_workspace_bytes",
            "qsa_fill_ids_decode", "qsa_fill_ids_even", "qsa_abi_version",
-           "qsa_paged_prep", "qsa_paged_gather", "qsa_paged_attn", "qsa_paged_attn_workspace_bytes",
-           "qsa_page_update", "qsa_page_compact", "qsa_pages_workspace_bytes",
            "QSAError", "QSA_DEVERR_BAD_ID", "QSA_DEVERR_TIMEOUT", "QSA_DEVERR_NO_PAGES", "QSA_SCORE_NOALLOC_MAX_TOKENS",
            "QSA_SELECT_MAX_CELLS", "lib"]
+
+# The paged cache's calls, in paged.py; loaded at first use, since it imports
+# torch at its top and this package is also imported to build the library, also
+# where there is no torch.
+_PAGED = ("qsa_paged_prep", "qsa_paged_gather", "qsa_paged_attn", "qsa_paged_attn_workspace_bytes", "qsa_page_update",
+          "qsa_page_compact", "qsa_pages_workspace_bytes")
+if importlib.util.find_spec("torch") is not None:
+    __all__ += _PAGED
 
 
 def _ptr(t, name, dtype=None, optional=False):
@@ -195,12 +202,6 @@ def qsa_attn(q, kq, vq, ksc, vsc, ids, out, softmax_scale=None, part=None, err=N
                       err=_ptr(err, "err", torch.int32, optional=True),
                       gate=_ptr(gate, "gate", torch.float32, optional=True))
     _abi.check(lib().qsa_attn(ctypes.byref(a), _stream(stream)))
-
-
-# The paged cache's calls, in paged.py; loaded at first use, since it imports
-# torch at its top and this package is also imported to build the library.
-_PAGED = ("qsa_paged_prep", "qsa_paged_gather", "qsa_paged_attn", "qsa_paged_attn_workspace_bytes", "qsa_page_update",
-          "qsa_page_compact", "qsa_pages_workspace_bytes")
 
 
 def __getattr__(name):

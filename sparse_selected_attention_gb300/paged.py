@@ -33,12 +33,25 @@ def binding_of_this_torch():
     return native
 
 
-_native = binding_of_this_torch()
+class _NoBinding:
+    """In the binding's place where there is none: each paged call says why."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise RuntimeError(self._why)
+
+
+try:
+    _native = binding_of_this_torch()
+except RuntimeError as e:
+    _native = _NoBinding(str(e))
 F32, F16, BF16, I32, I8 = torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int8
 _CODE = {F32: _abi.QSA_F32, F16: _abi.QSA_F16, BF16: _abi.QSA_BF16}
 # The raw handle of the current stream and the current device's number: what
 # torch.cuda.current_stream() and current_device() wrap, without their objects.
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+_raw_stream, _current_device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
 
 
 def _formats():

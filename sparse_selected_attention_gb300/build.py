@@ -77,8 +77,8 @@ def lib_path(variant: str = "release") -> str:
 
 
 def build(verbose: bool = False, ptxas_info: bool = False, force: bool = False, variant: str = "release") -> str:
-    """Compile and link one variant (with the release one the binding, where
-    torch is installed); returns the library path.  Rebuilds only stale parts."""
+    """Compile and link one variant (with the release one the binding, where a
+    torch with CUDA is installed); returns the library path.  Rebuilds only stale parts."""
     defines, libname = VARIANTS[variant]
     bdir = BUILD if variant == "release" else os.path.join(BUILD, variant)
     lib = os.path.join(PKG, libname)
@@ -137,8 +137,10 @@ BINDING = os.path.join(PKG, "_paged_binding.so")
 
 
 def _torch_dir() -> str | None:
+    """The installed torch, if it is one with CUDA."""
     spec = importlib.util.find_spec("torch")
-    return None if spec is None else os.path.dirname(spec.origin)
+    torch = None if spec is None else os.path.dirname(spec.origin)
+    return torch if torch and os.path.exists(os.path.join(torch, "lib", "libc10_cuda.so")) else None
 
 
 def torch_version() -> str:
@@ -156,8 +158,8 @@ def binding_stamp() -> str:
 
 
 def build_binding(verbose: bool = False, force: bool = False) -> str | None:
-    """_paged_binding.so, for this interpreter and its torch; None without torch
-    (the library does without it, and the binding's tensors are torch's).  It
+    """_paged_binding.so, for this interpreter and its torch; None without one of
+    CUDA (the library does without it, and the binding's tensors are torch's).  It
     reads tensors by the layout in torch's headers, so it is rebuilt for another
     torch, and carries the version, which paged.py compares."""
     torch = _torch_dir()

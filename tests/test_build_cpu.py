@@ -1,5 +1,6 @@
 """What the build makes, and from what, with the compilers replaced by a
 recorder that leaves an empty output file."""
+import importlib.machinery
 import importlib.util
 import os
 
@@ -38,6 +39,15 @@ def test_the_library_builds_without_torch(made, tmp_path, monkeypatch):
     lib = build.build()
     assert os.path.exists(lib) and made[-1] == "libqsa.so" and "_paged_binding.so" not in made
     assert not (tmp_path / "_paged_binding.so").exists()
+
+
+def test_the_library_builds_beside_a_torch_without_cuda(made, tmp_path, monkeypatch):
+    spec = importlib.machinery.ModuleSpec("torch", None, origin=str(tmp_path / "torch" / "__init__.py"))
+    (tmp_path / "torch" / "lib").mkdir(parents=True)
+    (tmp_path / "torch" / "version.py").write_text("__version__ = '2.9.0+cpu'")
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: spec if name == "torch" else find(name, *a))
+    assert os.path.exists(build.build()) and "_paged_binding.so" not in made
 
 
 def test_a_binding_that_does_not_build_leaves_the_library(made, tmp_path, monkeypatch):

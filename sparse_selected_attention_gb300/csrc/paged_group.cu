@@ -102,10 +102,12 @@ struct GroupSmem {
 
 __device__ __forceinline__ uint32_t unit_off(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
-// -floor(log2) of the largest finite |scale| of a cell, 0 where that is 0.
+// -floor(log2) of the largest finite |scale| of a cell; of a cell whose scales are
+// 0, that of the least scale there is, so that what adds nothing to the values
+// never is their maximum.
 __device__ __forceinline__ int scale_exponent(uint2 sc) {
     const uint32_t m2 = __vmaxu2(finite2(sc.x) & 0x7FFF7FFFu, finite2(sc.y) & 0x7FFF7FFFu), m = max(m2 & 0xFFFFu, m2 >> 16);
-    if (m == 0u) return 0;
+    if (m == 0u) return 24;
     return 127 - (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) >> 23);
 }
 // Scale i of a cell times 2^e, in both halves.

@@ -419,8 +419,10 @@ typedef struct {
  * concurrently (graphs that replay on different streams need one each).
  * The work is divided over the cached cells of all rows, so the last bits of
  * a row's results may depend on the other rows' lengths and on max_pages; the
- * same call gives the same bits.  Range: scores and sums are fp32; finite K
- * scales of any size, V scales below 2^15.
+ * same call gives the same bits.  Range: scores and sums are fp32; finite
+ * scales of any size.  What a cell adds to a dim is kept to 2^-11 of itself (the
+ * product of weight and V scale is one fp16 value, or two) or to 2^-24 of |code|
+ * times the row's largest weight x V scale.
  * An infinite or NaN V scale makes the dims it scales NaN or infinite in the
  * rows that attend to its cell, and in no other.  An infinite or NaN K scale
  * (qsa_paged_prep leaves one for a group with such a value) makes the cell's

@@ -21,7 +21,7 @@
 // many.)  Consecutive rows of one sequence go to paged_group.cu where that saves
 // enough (take_groups).
 //
-// 61 rows of up to 32 K cells, 48/4 heads of 128, 1.1 GB: 197 us, 5.6 TB/s; the
+// 61 rows of up to 32 K cells, 48/4 heads of 128, 1.1 GB: 205 us, 5.4 TB/s; the
 // same launch without the arithmetic 176 us.  A row of 321 cells alone: 8 us,
 // all of it latency.
 //
@@ -44,8 +44,11 @@
 // multiplies in fp32 (compute_unit says when).  For V it is subtracted, and the
 // scales go to the weights, a set of fp16 weights per scale group (weight x
 // scale in fp32, rounded once: a first rounding of the weight alone would add as
-// much again, for 2 us of 196), under a power of two per warp that keeps small
-// scales out of the subnormals.
+// much again, for 2 us of 196).  So that the products use fp16's range whatever
+// the scales are, the running maximum is one of weight x scale, up to a power of
+// two per cell: m is the largest s_c log2e + e_c, e_c the exponent of cell c's
+// largest V scale.  (One exponent per unit where its cells' are alike, and this where
+// not: 204 us for the rows below, where this takes 205 by one path.)
 #include <cuda.h>
 
 #include <algorithm>
@@ -122,9 +125,9 @@ struct Smem {
     uint4 q[8 * S][32];                            // Q fragments by k-step and lane
     float bias[4][8][4];                           // -1152 * sum of q over a scale group, as accumulators: heads g, g, g + 8, g + 8
     float qinv[16];                                // 2^-e of a head's scaled query
+    alignas(16) float ve[W][Shape<S>::UNIT], vw[W][Shape<S>::UNIT];  // of the unit at hand, by cell: e_c and 2^-e_c
     float o[W][16][128];                          // 128 dims of the warps' values, at the end of a segment
     float m[W][16], l[W][16], f[W][16];
-    int v[W];                                     // the warps' V exponents
     uint64_t bar[W][2];
     long long together[W], padded[W], scan[W];
     long long total, before;                       // units of all rows; of the rows before `row`
@@ -300,7 +303,6 @@ template <int S>
 struct State {
     float o[16 * S][4];  // o[t][0..1]: head g, dims 8 t + 2 r, 8 t + 2 r + 1; o[t][2..3]: head g + 8
     float m[2], l[2];
-    int v;  // values are in units of 2^v
     uint32_t k;  // the largest |K scale| that this lane has seen, as bits, in two halves
 };
 
@@ -315,7 +317,8 @@ struct State {
 // goes with short tables.
 template <int S, bool EXACT>
 __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const uint2 *KS, const uint2 *VS, const uint4 (*q)[32],
-                                             const float (*bias)[8][4], unsigned vmask, State<S> &st, const float (&sl2)[2]) {
+                                             const float (*bias)[8][4], float *ve, float *vw, unsigned vmask, State<S> &st,
+                                             const float (&sl2)[2]) {
     constexpr int NJ = Shape<S>::NJ, NK = Shape<S>::NK, UNIT = Shape<S>::UNIT;
     const int lane = threadIdx.x & 31, g = lane >> 2, r = lane & 3;
     // Row 2 g of K with the swizzle of its first 16 bytes for this lane, and row 2 g + 1.
@@ -331,6 +334,10 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     // A cell that is not there has scales of 0.
     const uint2 kown = KS[lane % UNIT];
     st.k = __vimax3_u16x2(st.k, kown.x & 0x7FFF7FFFu, kown.y & 0x7FFF7FFFu);
+    const int own = scale_exponent(VS[lane % UNIT]);
+    ve[lane % UNIT] = (float)own;
+    vw[lane % UNIT] = exp2i(-own);
+    __syncwarp();
 
     // Scores: per scale group S 32-dim blocks of two k-steps from -1152 sum q,
     // then the scale.
@@ -386,18 +393,27 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
         }
     }
 
-    // The reference maximum moves only when a unit exceeds it by 2^SLACK, so
-    // the values are rarely rescaled.
-    float mx[2], al[2];
+    // In base 2, with the V exponents.  The reference maximum moves only when a
+    // unit exceeds it by 2^SLACK, so the values are rarely rescaled.  Weights
+    // 2^(s_c log2e - m), in fp32: weight times V scale is rounded to fp16, once (by
+    // at most 2^-11 of itself).  EXACT rounds a weight's argument at its own size,
+    // the others at that of score plus exponent (2^-21 of a weight where that is 8
+    // to 16).
+    const float2 f[2] = {make_float2(sl2[0], sl2[0]), make_float2(sl2[1], sl2[1])};
+    float2 w[NJ][2], sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    float mx[2] = {-CUDART_INF_F, -CUDART_INF_F}, al[2];
+    auto of_cells = [&](const float *x, int j) {  // of cells 4 r + j % 2 and two on
+        const float4 b = *reinterpret_cast<const float4 *>(x + 16 * (j >> 1) + 4 * r);
+        return (j & 1) ? make_float2(b.y, b.w) : make_float2(b.x, b.z);
+    };
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        mx[e] = max3(s[0][e].x, s[0][e].y, s[1][e].x);
-        mx[e] = fmaxf(mx[e], s[1][e].y);
-        if constexpr (NJ == 4) {
-            mx[e] = max3(mx[e], s[2][e].x, s[2][e].y);
-            mx[e] = max3(mx[e], s[3][e].x, s[3][e].y);
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float2 t = __ffma2_rn(s[j][e], f[e], of_cells(ve, j));
+            mx[e] = max3(mx[e], t.x, t.y);
+            if constexpr (!EXACT) s[j][e] = t;
         }
-    }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
@@ -405,41 +421,25 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        mx[e] *= sl2[e];
         const float mn = mx[e] > st.m[e] + SLACK ? mx[e] : st.m[e];
         al[e] = ex2(st.m[e] - mn);
         st.m[e] = mn;
     }
-    // Weights, in fp32: weight times V scale is rounded to fp16, once (by at
-    // most 2^-11 of itself).
-    float2 w[NJ][2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const float2 f = make_float2(sl2[e], sl2[e]), m = make_float2(-st.m[e], -st.m[e]);
-        float2 sum = make_float2(0.0f, 0.0f);
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            float2 p = __ffma2_rn(s[j][e], f, m);
-            p = make_float2(ex2(p.x), ex2(p.y));
-            sum = __fadd2_rn(sum, p);
-            w[j][e] = p;
+        for (int e = 0; e < 2; ++e) {
+            const float2 less = make_float2(-st.m[e], -st.m[e]);
+            float2 p;
+            if constexpr (EXACT)
+                p = __ffma2_rn(s[j][e], f[e], __fadd2_rn(of_cells(ve, j), less));
+            else
+                p = __fadd2_rn(s[j][e], less);
+            w[j][e] = __fmul2_rn(make_float2(ex2(p.x), ex2(p.y)), of_cells(vw, j));
+            sum[e] = __fadd2_rn(sum[e], w[j][e]);
         }
-        st.l[e] = fmaf(st.l[e], al[e], sum.x + sum.y);
-    }
-
-    // The values' power of two: the largest finite V scale of the first unit, raised
-    // when a later scale reaches 2^6 of it, so that weight (below 2^8) times
-    // scale stays in the fp16 range.
-    const uint2 own = VS[lane % UNIT];
-    uint32_t top = __vmaxu2(finite2(own.x) & 0x7FFF7FFFu, finite2(own.y) & 0x7FFF7FFFu);
-    top = __reduce_max_sync(0xffffffffu, max(top & 0xFFFFu, top >> 16));
-    const int ve = min(max((int)(top >> 10) - 15, -14), 15);
-    if (ve >= st.v + 6) {
-        const float down = exp2i(max(st.v - ve, -126));
-        st.v = ve;
-        al[0] *= down;
-        al[1] *= down;
-    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) st.l[e] = fmaf(st.l[e], al[e], sum[e].x + sum[e].y);
     if (__any_sync(0xffffffffu, al[0] != 1.0f || al[1] != 1.0f)) {
 #pragma unroll
         for (int i = 0; i < 16 * S; ++i) {
@@ -449,11 +449,6 @@ __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const
             st.o[i][3] *= al[1];
         }
     }
-    const float vf = exp2i(-max(st.v, -14));
-#pragma unroll
-    for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) w[j][e] = __fmul2_rn(w[j][e], make_float2(vf, vf));
 
     // This lane's row address of V's matrices: 128 dims, cells 0-31 by lane; or
     // cells 0-15 by lane % 16, lanes 16-31 sixteen dims on.
@@ -665,7 +660,6 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
         for (int i = 0; i < 16 * S; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.0f;
         st.m[0] = st.m[1] = -CUDART_INF_F;
         st.l[0] = st.l[1] = 0.0f;
-        st.v = -64;  // below any scale's exponent: the first unit sets it
         st.k = 0u;
         for (int i = 0; i < n; ++i) {
             if (!ahead) vmask = issue(stage);
@@ -684,8 +678,8 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
                 }
                 __syncwarp();
                 const uint8_t *k = sh.tile[warp][stage][0];
-                compute_unit<S, WHOLE_ROWS>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q, sh.bias, vmask, st,
-                                sl2);
+                compute_unit<S, WHOLE_ROWS>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q, sh.bias,
+                                            sh.ve[warp], sh.vw[warp], vmask, st, sl2);
             }
             __syncwarp();  // every lane has read the stage before it is filled again
             vmask = vnext;
@@ -718,7 +712,6 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
                 sh.l[warp][g + 8 * e] = st.l[e];
             }
         }
-        if (lane == 0) sh.v[warp] = st.v;
         if (more) q.store(a, sh);
         const bool whole = n_units == nu;
         const size_t at = (size_t)blockIdx.x * 2 + (first && u0 > 0 ? 0 : 1);
@@ -748,7 +741,7 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
                     }
                     const float inv = whole ? (M == -CUDART_INF_F ? 0.0f : 1.0f / L) : 1.0f;
 #pragma unroll
-                    for (int p = 0; p < W; ++p) sh.f[p][tid] = w[p] == 0.0f ? 0.0f : w[p] * inv * exp2i(sh.v[p]);
+                    for (int p = 0; p < W; ++p) sh.f[p][tid] = w[p] * inv;
                     if (tid < per) {
                         if (!whole)
                             *reinterpret_cast<float2 *>(work.ml + (at * per + tid) * 2) = make_float2(M, L);

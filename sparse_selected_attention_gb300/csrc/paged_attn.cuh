@@ -33,6 +33,20 @@ __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__
 // Two scales with an infinite or NaN one replaced by 0.
 __device__ __forceinline__ uint32_t finite2(uint32_t x) { return x & ~__vcmpgeu2(x & 0x7FFF7FFFu, 0x7C007C00u); }
 
+// floor(log2) of the largest finite |scale| of a cell; of a cell whose scales are
+// 0, below any other's, so that what adds nothing to the values never is their
+// maximum.
+constexpr int NO_SCALE = -25;
+__device__ __forceinline__ int scale_exponent(uint2 sc) {
+    auto largest = [](uint32_t x, uint32_t y) {
+        const uint32_t m = __vmaxu2(x & 0x7FFF7FFFu, y & 0x7FFF7FFFu);
+        return max(m & 0xFFFFu, m >> 16);
+    };
+    uint32_t m = largest(sc.x, sc.y);
+    if (m >= 0x7C00u) m = largest(finite2(sc.x), finite2(sc.y));
+    return max((int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) >> 23) - 127, NO_SCALE);
+}
+
 // The row of q (or, of a group, its first and the number of them) that starts in
 // a CTA's share and spans n CTAs of its KV head; row -1: none.
 struct Part {
@@ -131,9 +145,15 @@ __device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i
     else
         *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + i) = __floats2bfloat162_rn(y.x, y.y);
 }
-// lse of a base-2 maximum and sum.  A row without cells has -inf and 0, which
-// gives -inf; one whose scores are all NaN has -inf and NaN, which gives NaN.
-__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * LN2; }
+// lse of a base-2 maximum and sum.  The sum's exponent goes to the maximum first,
+// so that only the result's own size is rounded.  A row without cells has -inf
+// and 0, which gives -inf; one whose scores are all NaN has -inf and NaN, which
+// gives NaN.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    const int e = (int)(__float_as_uint(l) >> 23) - 127;
+    if (e <= -127 || e >= 128) return (m + log2f(l)) * LN2;  // 0, infinite or NaN
+    return (m + (float)e + log2f(__uint_as_float((__float_as_uint(l) & 0x007FFFFFu) | 0x3F800000u))) * LN2;
+}
 // y / (1 + exp(-gate)); each step off by a few 2^-23, and a gate far below 0 gives 0.
 __device__ __forceinline__ float gated(float y, float gate) { return __fdividef(y, 1.0f + ex2(-gate * LOG2E)); }
 

@@ -102,14 +102,6 @@ struct GroupSmem {
 
 __device__ __forceinline__ uint32_t unit_off(int r, int u) { return r * 128 + ((u ^ (r & 7)) << 4); }
 
-// -floor(log2) of the largest finite |scale| of a cell; of a cell whose scales are
-// 0, that of the least scale there is, so that what adds nothing to the values
-// never is their maximum.
-__device__ __forceinline__ int scale_exponent(uint2 sc) {
-    const uint32_t m2 = __vmaxu2(finite2(sc.x) & 0x7FFF7FFFu, finite2(sc.y) & 0x7FFF7FFFu), m = max(m2 & 0xFFFFu, m2 >> 16);
-    if (m == 0u) return 24;
-    return 127 - (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) >> 23);
-}
 // Scale i of a cell times 2^e, in both halves.
 __device__ __forceinline__ __half2 scaled(uint2 sc, int i, int e) {
     const uint32_t w = i >> 1 ? sc.y : sc.x;
@@ -469,7 +461,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (k > 0) good = good && mbar_wait_or_abort(smem_u32(&sh.s_full[(k - 1) & 1]), ((k - 1) >> 1) & 1, abort);
                 if (!__all_sync(0xffffffffu, good)) return false;
                 const uint2 ks = sh.scales[st][0][fcell], vs = sh.scales[st][1][fcell];
-                const int ek = scale_exponent(ks), ev = scale_exponent(vs);
+                const int ek = -scale_exponent(ks), ev = -scale_exponent(vs);
                 // A V scale that is infinite or NaN counts as 0 here: times a
                 // weight of 0 it would reach rows that end before its cell.
                 vnext = h2u(scaled(make_uint2(finite2(vs.x), finite2(vs.y)), lane & 3, ev));

@@ -84,5 +84,5 @@ def test_a_sum_over_shifted_codes_is_noticed(d):
                     a = np.nextafter(a, np.float32(0))
             s += float(a)
         want = float((q * code).sum())
-        off += abs(s - want) > 2.0 ** -21 * abs(want) + 2.0 ** -24 * 2.0 ** 19
+        off += abs(s - want) > 2.0 ** -21 * abs(want) + 2.0 ** -21 * 2.0 ** 19
     assert off > n // 10

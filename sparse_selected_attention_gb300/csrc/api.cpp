@@ -371,7 +371,7 @@ qsa_status qsa_paged_gather(const qsa_paged_gather_args *a, void *stream) {
     if (a->page_table) {
         if (!paged_page(a->page_size))
             return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_gather: page_size must be 16, 32, 64, 128 or 256");
-        if (a->n_rows < 1 || a->max_pages < 1 || (a->n_ids && !a->rows))
+        if (a->n_rows < (a->n_ids ? 1 : 0) || a->max_pages < 1 || (a->n_ids && !a->rows))
             return fail(QSA_ERR_INVALID_ARG, "qsa_paged_gather: a page table needs rows, n_rows and max_pages");
     }
     if ((long long)a->n_ids * a->n_kv_heads > (1ll << 40) / a->head_dim)
@@ -399,8 +399,9 @@ qsa_status qsa_paged_attn(const qsa_paged_attn_args *a, void *stream) {
         return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_attn: page_size must be 16, 32, 64, 128 or 256");
     if (a->dtype != QSA_F16 && a->dtype != QSA_BF16)
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: dtype must be QSA_F16 or QSA_BF16");
-    if (a->n_tokens < 0 || a->n_pages < 1 || a->n_rows < 1 || a->max_pages < 1)
-        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: negative n_tokens, or n_pages, n_rows or max_pages below 1");
+    if (a->n_tokens < 0 || a->n_pages < 1 || a->n_rows < (a->n_tokens ? 1 : 0) || a->max_pages < 1)
+        return fail(QSA_ERR_INVALID_ARG,
+                    "qsa_paged_attn: negative n_tokens, n_pages or max_pages below 1, or no n_rows for its tokens");
     if (!a->rows && a->n_rows < a->n_tokens)
         return fail(QSA_ERR_INVALID_ARG, "qsa_paged_attn: without rows the table needs a row per token");
     if ((long long)a->n_pages * a->page_size > kMaxInt || (long long)a->max_pages * a->page_size > kMaxInt)

@@ -63,12 +63,12 @@ constexpr int NW = 4;           // warps per CTA, where a row's are not one
 constexpr int CTAS_PER_SM = 2;  // 255 registers a thread
 constexpr int MAX_CTAS = 152 * CTAS_PER_SM;
 static_assert(MAX_CTAS <= MAX_PARTS && WHOLE == 4 * NW, "shared with the join and the groups");
-// A warp per row, six to an SM, where the table holds up to SMALL units and there
+// A warp per row, six to an SM, where the table holds up to SMALL cells and there
 // are more rows and KV heads than CTAs of four warps; of more than two units,
-// twice as many.  Four warps and one, us: 156 rows, 48/8 heads of 128, one cell 24,
-// 16, 64 cells 28, 21, 128 cells 29, 29; 24/4 heads of 256, one cell 17, 11, 64 cells
+// twice as many.  Four warps and one, us: 156 rows, 48/8 heads of 128, one cell 23,
+// 17, 64 cells 26, 21, 128 cells 27, 30; 24/4 heads of 256, one cell 17, 11, 64 cells
 // 19, 17, but 80 rows of 64 cells 13, 15.
-constexpr int SMALL = 4, SMALL_PER_SM = 6;
+constexpr int SMALL = 64, SMALL_PER_SM = 6;
 constexpr int TILE = 4096;      // a unit's K or V codes
 // Fewest units of a share, one per warp: finer ones would only add partials.
 constexpr int MIN_SHARE = NW;
@@ -311,10 +311,10 @@ struct State {
 // sixteen times the rounding, and the products weight x scale go in in two parts
 // of 11 bits, not in one.  Long rows average both (off by 2e-7 of lse, and by
 // 1.2 times the output's own rounding), and would pay 2.6 to 7% for exact codes
-// alone (61 rows, 48/4 heads of 128: 200 us, 195 us; 90 rows of 18 K cells, one
-// head of 256: 171 us, 159 us).  Of short ones, a few cells carry the result (1.2e-6
-// of lse, 1.5 times the output's rounding), and the time is latency: so EXACT
-// goes with short tables.
+// alone (61 rows of 48/4 heads of 128; 90 rows of 18 K cells, one head of 256).
+// Of short ones, a few cells carry the result (1.2e-6 of lse, 1.5 times the
+// output's rounding), and the time is latency: so EXACT goes with short tables
+// (short rows of a wide table go with the long ones).
 template <int S, bool EXACT>
 __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const uint2 *KS, const uint2 *VS, const uint4 (*q)[32],
                                              const float (*bias)[8][4], float *ve, float *vw, unsigned vmask, State<S> &st,
@@ -854,7 +854,7 @@ cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
     const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
-    if (whole && units <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
+    if (whole && units * UNIT <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
         const int small = (int)std::min<long long>(a.n_tokens, std::max(152 * SMALL_PER_SM / a.n_kv_heads, 1));
         e = cudaFuncSetAttribute(paged_attn_kernel<S, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, 1>));
         return e != cudaSuccess ? e

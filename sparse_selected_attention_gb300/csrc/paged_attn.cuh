@@ -91,12 +91,12 @@ __device__ __forceinline__ int units_of(int len) {  // one at least, so that an 
 // 4 of 128 cost, and some microseconds more for a few long tiles than for many
 // small units: groups where they save 4096 units of a KV head (33 MB of codes).
 // One by one and by groups, us:
-//   48/4 heads of 256, 12 sequences: 3 rows of 6 K cells 103, 103; 4 133, 104; 8 241, 115
-//                                    5 rows of 1 K cells 48, 51; 8 66, 58
-//                      1 sequence:   8 rows of 1 K cells 19, 26; of 6 K 38, 30
-//   32/8 heads of 128, 12 sequences: 4 rows of 6 K cells 124, 127; 5 150, 127; 8 231, 128
-//                                    5 rows of 1 K cells 42, 47; 8 57, 48
-//                      1 sequence:   8 rows of 1 K cells 18, 22; of 6 K 32, 27
+//   48/4 heads of 256, 12 sequences: 3 rows of 6 K cells 102, 103; 4 131, 104; 8 238, 114
+//                                    5 rows of 1 K cells 48, 51; 8 65, 58
+//                      1 sequence:   8 rows of 1 K cells 19, 26; of 6 K 38, 31
+//   32/8 heads of 128, 12 sequences: 4 rows of 6 K cells 127, 128; 5 152, 129; 8 234, 129
+//                                    5 rows of 1 K cells 42, 47; 8 58, 48
+//                      1 sequence:   8 rows of 1 K cells 18, 21; of 6 K 33, 27
 template <int S>
 __device__ __forceinline__ bool take_groups(const qsa_paged_attn_args &a, long long alone, long long together, bool longer) {
     return longer && (2 * alone - (S == 1 ? 8 : 7) * together) * a.n_kv_heads > 2 * 4096;

@@ -418,7 +418,8 @@ typedef struct {
  * 256-byte aligned, overwritten; two calls that share one must not run
  * concurrently (graphs that replay on different streams need one each).
  * The work is divided over the cached cells of all rows, so the last bits of
- * a row's results may depend on the other rows' lengths and on max_pages; the
+ * a row's results may depend on the other rows' lengths and on max_pages (tables
+ * of up to 512 cells of 128 dims or 256 of 256 are computed with more bits); the
  * same call gives the same bits.  Range: scores and sums are fp32; finite
  * scales of any size.  What a cell adds to a dim is kept to 2^-11 of itself (the
  * product of weight and V scale is one fp16 value, or two) or to 2^-24 of |code|

@@ -22,8 +22,8 @@
 // enough (take_groups).
 //
 // 61 rows of up to 32 K cells, 48/4 heads of 128, 1.1 GB: 205 us, 5.4 TB/s; the
-// same launch without the arithmetic 176 us.  A row of 321 cells alone: 8 us,
-// all of it latency.
+// same launch without the arithmetic 176 us.  A row of 321 cells alone: 8 us, all
+// of it latency (10.5 us in a table of 32 K cells, with the join's launch).
 //
 // A unit.  The query heads of one KV head are the M side (padded to 16) of
 // m16n8k16 products, cells are N of Q.K and the contraction of P.V.  (tcgen05

@@ -20,7 +20,11 @@
 // Tiles are shared out over the chip and joined as in paged_attn.cu.  A tile
 // takes 3.8 K cycles of the chain K converted - S - K converted, of which the
 // 32 products of S are 1.7 K; issue slots are used to a third and the tensor
-// pipe to a fifth, so the rest is the roles' latency.  (Dropped, each without
+// pipe to a fifth, so the rest is the roles' latency.  The seven tiles a CTA of
+// the rows above are 14 us so; what does not shrink with the tiles (the launch
+// of the kernel that takes rows one by one, the share, queries and first loads,
+// partials of up to 98 KB a CTA and the join of them) is as much again and more:
+// two tiles a CTA take 21 to 26 us.  (Dropped, each without
 // gain: K converted by halves of the dims beside the other half's products; TMA
 // boxes in place of cp.async; two warps each for the loads.  A bulk copy per
 // cell, 256 bytes each, took 70 cycles a copy: 53 us where cp.async took 35.)
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     allow_dependent_launch();
     const Work work(ws, MAX_GROUP_PARTS, M);
     // Results in fp16 take weights in two parts (22 bits); bf16's own rounding,
-    // 2^-9, hides one of 11 bits.
+    // up to 2^-8, hides one of 11 bits.
     const bool fine = a.dtype == QSA_F16;
     bool bad = false;
 

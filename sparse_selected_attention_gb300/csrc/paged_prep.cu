@@ -115,6 +115,10 @@ struct PrepPlan {
     int chunks, rows;  // runs per token, rows of a run (even)
 };
 
+// Seven blocks an SM: 72 registers.  Two-byte rows fit but for some 50 bytes of
+// halves of 256 dims; fp32 rows of 256 dims spill (halves 288 bytes stored and 576
+// loaded a thread, interleaved 104 and 172: 4096 tokens of 24/2 heads, 27 us for
+// their bytes, take 47 and 36 us).
 template <int D, bool INTER, class TI, class TO>
 __global__ void __launch_bounds__(PREP_WARPS * 32, 7) paged_prep_kernel(const qsa_paged_prep_args a, const PrepPlan plan) {
     constexpr int N = D / 32;  // elements per lane

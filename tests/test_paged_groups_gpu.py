@@ -36,31 +36,34 @@ def reference(q, pool, table, lens, rows, scale=None, gate=None):
     out, mag, flush = (torch.zeros(T, H, D, dtype=torch.float64, device=on) for _ in range(3))
     lse, qk = torch.full((T, H), -math.inf, dtype=torch.float64, device=on), torch.zeros(T, H, dtype=torch.float64, device=on)
     wide = lambda s: s.double().repeat_interleave(D // 4, -1)  # noqa: E731
-    kept = None
-    for t, (n, r) in enumerate(zip(lens, rows)):
-        n = min(max(n, 0), table.shape[1] * page) if 0 <= r < table.shape[0] else 0
-        if n == 0:
+    c = np.arange(table.shape[1] * page)
+    t0 = 0
+    while t0 < T:  # a run of rows of one sequence at a time
+        r, t1 = rows[t0], t0 + 1
+        while t1 < T and rows[t1] == r and t1 - t0 < 64:
+            t1 += 1
+        run, t0 = slice(t0, t1), t1
+        n = torch.tensor([min(max(v, 0), len(c)) if 0 <= r < table.shape[0] else 0 for v in lens[run]], device=on)
+        most = int(n.max())
+        if most == 0:
             continue
-        if kept is None or kept[0] != r:  # all of the sequence's cells
-            c = np.arange(table.shape[1] * page)
-            e = table[r, c // page].astype(np.int64)
-            ok = torch.from_numpy((e >= 0) & (e < pool[0].shape[0])).to(on)
-            at = torch.from_numpy(np.where((e >= 0) & (e < pool[0].shape[0]), e, 0) * page + c % page).to(on)
-            kept = (r, ok, kq[at].double() * wide(ksc[at]), vq[at].double(), wide(vsc[at]), ksc[at].double(), vsc[at].double().amax(-1))
-        _, ok, k, code, vs, ks, top = kept
-        ok, k, code, vs, ks, top = ok[:n], k[:n], code[:n], vs[:n], ks[:n], top[:n]
-        if not ok.any():
-            continue
-        x = q[t].double().view(hkv, per, D)
-        s = torch.einsum("hpd,chd->hpc", x, k) * scale
-        s = s.masked_fill(~ok, -math.inf)
-        w = torch.softmax(s, -1)
-        v = code * vs
-        out[t] = torch.einsum("hpc,chd->hpd", w, v).reshape(H, D)
-        lse[t] = torch.logsumexp(s, -1).flatten()
-        mag[t] = torch.einsum("hpc,chd->hpd", w, v.abs()).reshape(H, D)
-        flush[t] = ((w * top.T[:, None]).amax(-1)[..., None] * (code.abs() * ok[:, None, None]).sum(0)[:, None]).reshape(H, D)
-        qk[t] = (torch.einsum("cho,hpo->chp", ks, x.abs().unflatten(-1, (4, D // 4)).sum(-1)).amax(0) * abs(scale)).flatten()
+        e = table[r, c[:most] // page].astype(np.int64)
+        there = (e >= 0) & (e < pool[0].shape[0])
+        at = torch.from_numpy(np.where(there, e, 0) * page + c[:most] % page).to(on)
+        ok = (torch.arange(most, device=on) < n[:, None]) & torch.from_numpy(there).to(on)  # [t, c]
+        k, code, vs, ks = kq[at].double() * wide(ksc[at]), vq[at].double(), wide(vsc[at]), ksc[at].double()
+        top, v = vsc[at].double().amax(-1), code * vs
+        x = q[run].double().view(-1, hkv, per, D)
+        s = (torch.einsum("thpd,chd->thpc", x, k) * scale).masked_fill(~ok[:, None, None], -math.inf)
+        some = ok.any(-1)[:, None, None, None]
+        w = torch.where(some, torch.softmax(s, -1), 0.0)
+        shape = (-1, H, D)
+        out[run] = torch.einsum("thpc,chd->thpd", w, v).reshape(shape)
+        lse[run] = torch.logsumexp(s, -1).flatten(1)
+        mag[run] = torch.einsum("thpc,chd->thpd", w, v.abs()).reshape(shape)
+        flush[run] = ((w * top.T[None, :, None]).amax(-1)[..., None] * torch.einsum("tc,chd->thd", ok.double(), code.abs())[:, :, None]).reshape(shape)
+        each = torch.einsum("chg,thpg->tchp", ks, x.abs().unflatten(-1, (4, D // 4)).sum(-1))
+        qk[run] = ((each * ok[..., None, None]).amax(1) * abs(scale)).flatten(1)
     if gate is not None:
         sg = torch.sigmoid(gate.double())
         out, mag, flush = out * sg, mag * sg, flush * sg

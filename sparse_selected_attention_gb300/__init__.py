@@ -26,6 +26,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import math
+import sys
 
 from . import _abi
 from ._abi import (QSA_DEVERR_BAD_ID, QSA_DEVERR_NO_PAGES, QSA_DEVERR_TIMEOUT,  # noqa: F401
@@ -41,7 +42,7 @@ __all__ = ["qsa_prep", "qsa_score", "qsa_score_noalloc", "qsa_select", "qsa_attn
 # where there is no torch.
 _PAGED = ("qsa_paged_prep", "qsa_paged_gather", "qsa_paged_attn", "qsa_paged_attn_workspace_bytes", "qsa_page_update",
           "qsa_page_compact", "qsa_pages_workspace_bytes")
-if importlib.util.find_spec("torch") is not None:
+if sys.modules.get("torch") or importlib.util.find_spec("torch"):
     __all__ += _PAGED
 
 

@@ -58,6 +58,17 @@ assert callable(qsa_prep) and callable(qsa_paged_attn)
     assert r.returncode == 0, r.stderr
 
 
+def test_import_beside_a_stand_in_for_torch():
+    """A module put in torch's place, which the import system did not find."""
+    r = child(f"""
+import sys, types
+sys.modules["torch"] = types.ModuleType("torch")
+import {PKG} as p
+assert callable(p.qsa_prep) and "qsa_paged_attn" in p.__all__
+""")
+    assert r.returncode == 0, r.stderr
+
+
 def test_star_has_everything():
     r = child(f"""
 import {PKG} as p

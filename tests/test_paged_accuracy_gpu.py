@@ -17,17 +17,14 @@ that the roundings that a form does without would show.
                 of one product is exact; and of fp16 results the weights keep
                 22 bits: with V scales of a power of two `out` is off as above.
 
-test_the_bounds_notice plants the roundings in the definition, on the CPU.
+tests/test_paged_bounds_cpu.py plants the roundings in the definition.
 """
-import math
-
 import numpy as np
 import pytest
 import torch
 
-import sparse_selected_attention_gb300 as qsa
 from tests.test_paged_gpu import BF16, F16, HALF, TINY, dev, i32, make_pool, shuffled_table, taken_together
-from tests.test_paged_groups_gpu import bounds, check, queries, reference, run
+from tests.test_paged_groups_gpu import check, reference, run
 
 pytestmark = pytest.mark.gpu
 

@@ -519,11 +519,177 @@ typedef struct {
 /* Bytes of workspace qsa_page_update and qsa_page_compact need (0 on bad input). */
 size_t qsa_pages_workspace_bytes(int n_rows, int n_pages);
 
+/*
+ * Long sequences by their best pages.  For each page the cache keeps bounds of
+ * its keys; a cheap score ranks a sequence's pages for each token and KV head,
+ * and the attention goes over the chosen ones only:
+ *   qsa_page_bounds -> qsa_page_score -> qsa_page_select -> qsa_paged_sparse_attn
+ *
+ * qsa_page_bounds -- the bounds of the pages that rows' new tokens are in:
+ * for each KV head and dim d, hi and lo are the largest and smallest key
+ * ksc * kq over the page's filled cells, held in the cache's own format, rounded
+ * outwards per quarter of the dims:
+ *   hi_sc = the smallest fp16 s with 127 s >= max|hi|, hi_q = ceil(hi / s);
+ *   lo_sc = the smallest fp16 s with 127 s >= max|lo|, lo_q = floor(lo / s)
+ * (codes 0 where s is 0), so hi_sc * hi_q >= every key >= lo_sc * lo_q.  A
+ * quarter with an infinite or NaN K scale in a filled cell gets codes 0 and a
+ * NaN scale, so that the page scores NaN.  Bit-exact by definition.
+ * Row r's pages (seq_lens[r] - n_new[r]) / page_size .. the last are written,
+ * from all of their filled cells (cells below seq_lens[r]); with n_new NULL all
+ * of the row's pages are, and with n_new[r] = 0 none.  A page that several rows
+ * hold is written by each, so they must agree on its filled cells (forked rows
+ * do).  qsa_page_compact moves pages and not their bounds: call this with n_new
+ * NULL after it.
+ * A length outside [0, max_pages * page_size], an n_new outside [0, length] and
+ * a table entry outside the pool count as the nearest length, the nearest count
+ * and no page; each sets QSA_DEVERR_BAD_ID.
+ *
+ * page_table int32 [n_rows, max_pages], seq_lens, n_new int32 [n_rows]; kq, ksc
+ * one layer of the pool; hi_q, lo_q int8 [n_pages, n_kv_heads, head_dim], hi_sc,
+ * lo_sc fp16 [n_pages, n_kv_heads, 4]: a cache of one cell per page, which
+ * qsa_paged_gather reads back.  Codes 16-byte aligned, scales 8-byte.
+ */
+typedef struct {
+    int n_rows, max_pages, n_pages, page_size, n_kv_heads, head_dim, group;
+    const int32_t *page_table, *seq_lens, *n_new;
+    const int8_t *kq;
+    const uint16_t *ksc;
+    int8_t *hi_q, *lo_q;
+    uint16_t *hi_sc, *lo_sc;
+    unsigned int *err;
+} qsa_page_bounds_args;
+
+/*
+ * qsa_page_score -- for token t, KV head h and each page j of t's sequence
+ * (j < ceil(seq_lens[t] / page_size)), with p = page_table[rows[t], j] and the
+ * sums over the query heads of h:
+ *   scores[t, h, j] = sum_d hi[p,h,d] * (sum max(q[t,.,d], 0))
+ *                         + lo[p,h,d] * (sum min(q[t,.,d], 0))
+ * in fp32: the most that the heads' products with a key of the page can add up
+ * to.  Other elements of scores are left untouched.  rows as in qsa_paged_attn
+ * (consecutive tokens of one sequence share the reading of its bounds).  A
+ * table entry outside the pool scores -inf and sets QSA_DEVERR_BAD_ID; lengths
+ * and rows out of range are treated as in qsa_paged_attn.  Each q sum travels
+ * as two fp16 under a power of two per token and KV head, about 22 bits below
+ * the largest of its sums.
+ *
+ * q [n_tokens, n_q_heads, head_dim] in dtype (QSA_F16 or QSA_BF16); hi_q .. as
+ * written by qsa_page_bounds; scores fp32 [n_tokens, n_kv_heads, ld], ld >=
+ * max_pages.  Query heads as in qsa_paged_attn.  q and codes 16-byte aligned,
+ * scales 8-byte, the rest 4-byte.
+ */
+typedef struct {
+    int n_tokens, n_q_heads, n_kv_heads, head_dim, group, page_size, n_pages, n_rows, max_pages;
+    int dtype;
+    const void *q;
+    const int8_t *hi_q, *lo_q;
+    const uint16_t *hi_sc, *lo_sc;
+    const int32_t *page_table, *seq_lens, *rows;
+    float *scores;
+    int64_t ld;
+    unsigned int *err;
+} qsa_page_score_args;
+
+/*
+ * qsa_page_select -- qsa_select's rule for pages.  With n = ceil(seq_lens[t] /
+ * page_size) pages, pages[t, h, :] receives the first `sink` of them, the last
+ * `local`, and those of the others that score highest in scores[t, h, :], until
+ * min(n, budget) are chosen; ascending, then -1 up to width.  counts[t, h] =
+ * min(n, budget).  Equal scores (-0 and +0 are equal) rank the lower page first,
+ * a NaN below every number.  Deterministic and bit-exact.
+ * A length below 0 counts as 0, and one of more than ld pages as ld pages; each
+ * sets QSA_DEVERR_BAD_ID.
+ *
+ * scores fp32 [n_tokens, n_kv_heads, ld]; seq_lens int32 [n_tokens]; pages int32
+ * [n_tokens, n_kv_heads, width]; counts int32 [n_tokens, n_kv_heads].  All
+ * 4-byte aligned.  Requires 1 <= budget <= width, sink, local >= 0 and sink +
+ * local <= budget.  page_size 16, 32, 64, 128 or 256.
+ */
+typedef struct {
+    int n_tokens, n_kv_heads, page_size, width, budget, sink, local;
+    const float *scores;
+    int64_t ld;
+    const int32_t *seq_lens;
+    int32_t *pages, *counts;
+    unsigned int *err;
+} qsa_page_select_args;
+
+/*
+ * qsa_paged_sparse_attn -- qsa_paged_attn over listed pages: KV head h of row t
+ * attends to the cells below seq_lens[t] of pages pages[t, h, i], i <
+ * counts[t, h], of its sequence (page numbers as in scores and the table's
+ * columns, in any order).  -1 is padding; a page listed twice counts twice.
+ * Otherwise as qsa_paged_attn (out, gate, lse, rows, range of values, rows that
+ * see nothing).  A count outside [0, width] is cut to that range; a page number
+ * below -1 or from max_pages on is left out, as is a page whose table entry is
+ * outside the pool; each sets QSA_DEVERR_BAD_ID.
+ *
+ * pages int32 [n_tokens, n_kv_heads, width], counts int32 [n_tokens,
+ * n_kv_heads]; width * page_size up to 2^30.  workspace: at least
+ * qsa_paged_sparse_attn_workspace_bytes(), otherwise as there.
+ */
+typedef struct {
+    int n_tokens, n_q_heads, n_kv_heads, head_dim, group, page_size, n_pages, n_rows, max_pages, width;
+    int dtype;
+    const void *q;
+    const int8_t *kq, *vq;
+    const uint16_t *ksc, *vsc;
+    const int32_t *page_table, *seq_lens, *rows, *pages, *counts;
+    float softmax_scale;
+    const float *gate;
+    void *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    unsigned int *err;
+} qsa_paged_sparse_attn_args;
+
+/*
+ * qsa_paged_tree_attn -- qsa_paged_attn for drafted tokens that branch: row t
+ * attends to cells 0 .. prefix_lens[t]-1 of its sequence, and after them to cell
+ * prefix_lens[t] + b for each bit b that is set in its mask (bit b % 32 of
+ * mask[t, b / 32]).  For a tree whose node i is cached in cell prefix + i, a
+ * node's mask has the bits of itself and of the nodes that lead to it; a row
+ * that sees nothing (a padding token: prefix 0, mask 0) gives out = +0 and lse =
+ * -inf.  Consecutive rows of one sequence are read together where that saves
+ * time.  Otherwise as qsa_paged_attn; a bit at or past max_pages * page_size is
+ * left out and sets QSA_DEVERR_BAD_ID.
+ *
+ * prefix_lens int32 [n_tokens]; mask int32 [n_tokens, words], 1 <= words <=
+ * QSA_TREE_MAX_WORDS.  workspace: at least
+ * qsa_paged_tree_attn_workspace_bytes(), otherwise as there.
+ */
+#define QSA_TREE_MAX_WORDS 32
+typedef struct {
+    int n_tokens, n_q_heads, n_kv_heads, head_dim, group, page_size, n_pages, n_rows, max_pages, words;
+    int dtype;
+    const void *q;
+    const int8_t *kq, *vq;
+    const uint16_t *ksc, *vsc;
+    const int32_t *page_table, *prefix_lens, *rows, *mask;
+    float softmax_scale;
+    const float *gate;
+    void *out;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    unsigned int *err;
+} qsa_paged_tree_attn_args;
+
+/* Bytes of workspace (0 on a shape that is not supported). */
+size_t qsa_paged_sparse_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+size_t qsa_paged_tree_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+
 qsa_status qsa_paged_prep(const qsa_paged_prep_args *args, void *stream);
 qsa_status qsa_paged_gather(const qsa_paged_gather_args *args, void *stream);
 qsa_status qsa_paged_attn(const qsa_paged_attn_args *args, void *stream);
 qsa_status qsa_page_update(const qsa_page_update_args *args, void *stream);
 qsa_status qsa_page_compact(const qsa_page_compact_args *args, void *stream);
+qsa_status qsa_page_bounds(const qsa_page_bounds_args *args, void *stream);
+qsa_status qsa_page_score(const qsa_page_score_args *args, void *stream);
+qsa_status qsa_page_select(const qsa_page_select_args *args, void *stream);
+qsa_status qsa_paged_sparse_attn(const qsa_paged_sparse_attn_args *args, void *stream);
+qsa_status qsa_paged_tree_attn(const qsa_paged_tree_attn_args *args, void *stream);
 
 /*
  * qsa_check_word -- the pages have no counterpart to this call; it serves the

@@ -12,6 +12,13 @@ Pins (tests/test_paged_cpu.py):
   page_update   -- hand-built tables: growth, fork with a shared last page,
                    reorder, free, an exhausted pool; invariants on random ones.
   page_compact  -- a hand-built table; contents of every row kept.
+Pins (tests/test_paged_pick_cpu.py):
+  page_bounds   -- hand-built pages; every key between its page's bounds, which
+                   a code less or the next smaller scale would not hold.
+  page_score    -- brute force over the corners of the bounds.
+  page_select   -- the contiguous oracle's selection; hand-built ties and NaNs.
+  sparse_cells, tree_cells, attn_cells -- paged_attn with all pages listed, with
+                   a full mask, and a tree's branches as sequences of their own.
 """
 from __future__ import annotations
 
@@ -192,3 +199,168 @@ def page_compact(page_table, seq_lens, n_pages, page):
     for p, q in to.items():
         new_refs[q] = refs[p]
     return table, new_refs, page_map, live, list(zip(movers, holes)), err
+
+
+def _row_cells(page_table, seq_lens, rows, t, page, err):
+    """Table row and length of token t as they count, and whether they were in range."""
+    r = t if rows is None else int(rows[t])
+    n = int(seq_lens[t])
+    if not 0 <= r < page_table.shape[0]:
+        return 0, 0, BAD_ID
+    most = page_table.shape[1] * page
+    return r, min(max(n, 0), most), err | (0 if 0 <= n <= most else BAD_ID)
+
+
+def page_bounds(page_table, seq_lens, n_new, kq, ksc):
+    """{page: (hi_q, lo_q, hi_sc, lo_sc)} of the written pages ([Hkv, D] and [Hkv, 4]), and err."""
+    n_pages, page, hkv, d = kq.shape
+    most, out, err = page_table.shape[1] * page, {}, 0
+    for r in range(page_table.shape[0]):
+        n = min(max(int(seq_lens[r]), 0), most)
+        new = n if n_new is None else min(max(int(n_new[r]), 0), n)
+        err |= BAD_ID if n != int(seq_lens[r]) or (n_new is not None and new != int(n_new[r])) else 0
+        for j in range((n - new) // page, -(-n // page) if new else 0):
+            p = int(page_table[r, j])
+            if not 0 <= p < n_pages:
+                err |= BAD_ID
+                continue
+            filled = min(page, n - j * page)
+            sc = ksc[p, :filled].astype(np.float64)
+            with np.errstate(invalid="ignore"):
+                keys = (kq[p, :filled].astype(np.float64).reshape(filled, hkv, 4, d // 4) * sc[..., None])
+            bad = ~np.isfinite(sc).all(0)
+            keys = np.where(bad[None, ..., None], 0.0, keys)
+            res = []
+            for v, outwards in ((keys.max(0), np.ceil), (keys.min(0), np.floor)):
+                need = np.abs(v).max(-1) / 127.0
+                s16 = need.astype(np.float16)
+                s16 = np.where(s16.astype(np.float64) < need, np.nextafter(s16, np.float16(np.inf)), s16).astype(np.float16)
+                step = s16.astype(np.float64)[..., None]
+                code = outwards(np.divide(v, step, out=np.zeros_like(v), where=step > 0)).astype(np.int8)
+                res.append((code.reshape(hkv, d), np.where(bad, np.float16(np.nan), s16)))
+            out[p] = (res[0][0], res[1][0], res[0][1], res[1][1])
+    return out, err
+
+
+def page_score(q, hi_q, lo_q, hi_sc, lo_sc, page_table, seq_lens, page, rows=None):
+    """Per (token, KV head): the pages' scores, sum |terms| and sum |hi| + |lo|
+    (-inf, 0, 0 of a page outside the pool); the largest sum; and err."""
+    T, H, D = q.shape
+    hkv, err, out = hi_q.shape[1], 0, []
+    wide = lambda c, s: c.astype(np.float64) * np.repeat(s.astype(np.float64), D // 4, -1)  # noqa: E731
+    hi, lo = wide(hi_q, hi_sc), wide(lo_q, lo_sc)
+    for t in range(T):
+        r, n, err = _row_cells(page_table, seq_lens, rows, t, page, err)
+        x = q[t].astype(np.float64).reshape(hkv, -1, D)
+        up, down = np.maximum(x, 0).sum(1), np.minimum(x, 0).sum(1)
+        p = page_table[r, : -(-n // page)]
+        ok = (p >= 0) & (p < hi_q.shape[0])
+        err |= 0 if ok.all() else BAD_ID
+        per = []
+        for h in range(hkv):
+            a, b = hi[np.where(ok, p, 0), h], lo[np.where(ok, p, 0), h]
+            per.append((np.where(ok, a @ up[h] + b @ down[h], -np.inf), np.where(ok, np.abs(a) @ up[h] - np.abs(b) @ down[h], 0.0),
+                        np.where(ok, (np.abs(a) + np.abs(b)).sum(-1), 0.0), max(up[h].max(), -down[h].min())))
+        out.append(per)
+    return out, err
+
+
+def page_select(scores, seq_lens, page, budget, sink, local, width):
+    """pages [T, Hkv, width], counts [T, Hkv], err."""
+    T, hkv, ld = scores.shape
+    pages, counts, err = np.full((T, hkv, width), -1, np.int32), np.zeros((T, hkv), np.int32), 0
+    for t in range(T):
+        n = -(-int(seq_lens[t]) // page)
+        err |= BAD_ID if seq_lens[t] < 0 or n > ld else 0
+        n = min(max(n, 0), ld)
+        for h in range(hkv):
+            forced = [j for j in range(n) if j < sink or j >= n - local]
+            free = [j for j in range(n) if sink <= j < n - local]
+            rank = lambda j: (1, 0.0, j) if np.isnan(scores[t, h, j]) else (0, -float(scores[t, h, j]), j)  # noqa: E731
+            got = list(range(n)) if n <= budget else sorted(forced + sorted(free, key=rank)[: budget - len(forced)])
+            pages[t, h, : len(got)] = got
+            counts[t, h] = len(got)
+    return pages, counts, err
+
+
+def _pool_cells(page_table, r, cells, page, n_pages, err):
+    out = []
+    for c in cells:
+        p = int(page_table[r, c // page])
+        if 0 <= p < n_pages:
+            out.append(p * page + c % page)
+        else:
+            err |= BAD_ID
+    return out, err
+
+
+def sparse_cells(page_table, seq_lens, pages, counts, page, n_pages, rows=None):
+    """Pool cells that each (token, KV head) attends to, and err."""
+    T, hkv, width = pages.shape
+    out, err = [], 0
+    for t in range(T):
+        r, n, err = _row_cells(page_table, seq_lens, rows, t, page, err)
+        per = []
+        for h in range(hkv):
+            k = int(counts[t, h])
+            err |= 0 if 0 <= k <= width else BAD_ID
+            cells = []
+            for j in pages[t, h, : min(max(k, 0), width)] if n else []:
+                if j < -1 or j >= page_table.shape[1]:
+                    err |= BAD_ID
+                elif j >= 0:
+                    cells += [c for c in range(j * page, (j + 1) * page) if c < n]
+            cells, err = _pool_cells(page_table, r, cells, page, n_pages, err)
+            per.append(cells)
+        out.append(per)
+    return out, err
+
+
+def tree_cells(page_table, prefix_lens, mask, hkv, page, n_pages, rows=None):
+    """Pool cells that each (token, KV head) attends to, and err."""
+    out, err, most = [], 0, page_table.shape[1] * page
+    for t in range(len(prefix_lens)):
+        r = t if rows is None else int(rows[t])
+        if not 0 <= r < page_table.shape[0]:
+            out.append([[]] * hkv)
+            err |= BAD_ID
+            continue
+        n = min(max(int(prefix_lens[t]), 0), most)
+        err |= 0 if n == int(prefix_lens[t]) else BAD_ID
+        cells = list(range(n)) + [n + b for b in range(32 * mask.shape[1]) if int(mask[t, b // 32]) >> (b % 32) & 1]
+        err |= BAD_ID if cells and cells[-1] >= most else 0
+        cells, err = _pool_cells(page_table, r, [c for c in cells if c < most], page, n_pages, err)
+        out.append([cells] * hkv)
+    return out, err
+
+
+def attn_cells(q, kq, vq, ksc, vsc, cells, scale=None, gate=None):
+    """attn's numbers, of listed pool cells: cells[t][KV head]."""
+    T, H, D = q.shape
+    hkv = kq.shape[2]
+    per = H // hkv
+    scale = 1.0 / np.sqrt(D) if scale is None else scale
+    out, lse = np.zeros((T, H, D)), np.full((T, H), -np.inf)
+    mag, flush, qk = np.zeros((T, H, D)), np.zeros((T, H, D)), np.zeros((T, H))
+    flat = [x.reshape(-1, *x.shape[2:]) for x in (kq, vq, ksc, vsc)]
+    for t in range(T):
+        for k in range(hkv):
+            at = np.asarray(cells[t][k], dtype=np.int64)
+            if not len(at):
+                continue
+            codes, values, ks, vs = (x[at, k].astype(np.float64) for x in flat)
+            heads = slice(k * per, (k + 1) * per)
+            x = q[t, heads].astype(np.float64)
+            keys, v = codes * np.repeat(ks, D // 4, -1), values * np.repeat(vs, D // 4, -1)
+            s = x @ keys.T * scale
+            m = s.max(-1, keepdims=True)
+            w = np.exp(s - m)
+            L = w.sum(-1, keepdims=True)
+            out[t, heads], mag[t, heads] = w @ v / L, w @ np.abs(v) / L
+            lse[t, heads] = (m + np.log(L))[:, 0]
+            flush[t, heads] = np.abs(values).sum(0) * vs.max() / L
+            qk[t, heads] = abs(scale) * (np.abs(x).reshape(per, 4, -1).sum(-1) @ ks.T).max(-1)
+    if gate is not None:
+        sg = 1.0 / (1.0 + np.exp(-np.asarray(gate, dtype=np.float64)))
+        out, mag, flush = out * sg, mag * sg, flush * sg
+    return out, lse, mag, flush, qk

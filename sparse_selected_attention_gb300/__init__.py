@@ -20,6 +20,14 @@ ksc, vsc [layers, pages, page, Hkv, 4], page_table [rows, max_pages], seq_lens
     qsa_paged_attn   attention of one new token per row over its whole length
     qsa_paged_gather cached rows as fp16, bf16 or fp32 values
     qsa_page_compact held pages moved to the lowest numbers
+
+Long sequences by their best pages, and drafted tokens that branch:
+
+    qsa_page_bounds  the largest and smallest key of each page that new tokens are in
+    qsa_page_score   what each page's keys can reach at most, for a token and KV head
+    qsa_page_select  the first, the last and the best-scoring pages up to a budget
+    qsa_paged_sparse_attn  attention over the listed pages
+    qsa_paged_tree_attn    attention of drafted tokens over a prefix and, by bits, each other
 """
 from __future__ import annotations
 
@@ -30,18 +38,20 @@ import sys
 
 from . import _abi
 from ._abi import (QSA_DEVERR_BAD_ID, QSA_DEVERR_NO_PAGES, QSA_DEVERR_TIMEOUT,  # noqa: F401
-                   QSA_SCORE_NOALLOC_MAX_TOKENS, QSA_SELECT_MAX_CELLS, QSAError, lib)
+                   QSA_SCORE_NOALLOC_MAX_TOKENS, QSA_SELECT_MAX_CELLS, QSA_TREE_MAX_WORDS, QSAError, lib)
 
 __all__ = ["qsa_prep", "qsa_score", "qsa_score_noalloc", "qsa_select", "qsa_attn", "qsa_score_workspace_bytes",
            "qsa_fill_ids_decode", "qsa_fill_ids_even", "qsa_abi_version",
            "QSAError", "QSA_DEVERR_BAD_ID", "QSA_DEVERR_TIMEOUT", "QSA_DEVERR_NO_PAGES", "QSA_SCORE_NOALLOC_MAX_TOKENS",
-           "QSA_SELECT_MAX_CELLS", "lib"]
+           "QSA_SELECT_MAX_CELLS", "QSA_TREE_MAX_WORDS", "lib"]
 
 # The paged cache's calls, in paged.py; loaded at first use, since it imports
 # torch at its top and this package is also imported to build the library, also
 # where there is no torch.
 _PAGED = ("qsa_paged_prep", "qsa_paged_gather", "qsa_paged_attn", "qsa_paged_attn_workspace_bytes", "qsa_page_update",
-          "qsa_page_compact", "qsa_pages_workspace_bytes")
+          "qsa_page_compact", "qsa_pages_workspace_bytes", "qsa_page_bounds", "qsa_page_score", "qsa_page_select",
+          "qsa_paged_sparse_attn", "qsa_paged_sparse_attn_workspace_bytes", "qsa_paged_tree_attn",
+          "qsa_paged_tree_attn_workspace_bytes")
 if sys.modules.get("torch") or importlib.util.find_spec("torch"):
     __all__ += _PAGED
 

@@ -20,6 +20,7 @@ QSA_DEVERR_BAD_ID, QSA_DEVERR_TIMEOUT, QSA_DEVERR_NO_PAGES = 1, 2, 4
 QSA_F32, QSA_F16, QSA_BF16 = 0, 1, 2
 QSA_SCORE_NOALLOC_MAX_TOKENS = 8192
 QSA_SELECT_MAX_CELLS = 32768
+QSA_TREE_MAX_WORDS = 32
 
 _c_int, _c_float, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
 
@@ -93,6 +94,39 @@ class PageCompactArgs(ctypes.Structure):
                 + [("workspace_bytes", ctypes.c_size_t), ("err", _vp)])
 
 
+class PageBoundsArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_rows", "max_pages", "n_pages", "page_size", "n_kv_heads", "head_dim", "group")]
+                + [(n, _vp) for n in ("page_table", "seq_lens", "n_new", "kq", "ksc", "hi_q", "lo_q", "hi_sc", "lo_sc", "err")])
+
+
+class PageScoreArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "group", "page_size",
+                                       "n_pages", "n_rows", "max_pages", "dtype")]
+                + [(n, _vp) for n in ("q", "hi_q", "lo_q", "hi_sc", "lo_sc", "page_table", "seq_lens", "rows", "scores")]
+                + [("ld", ctypes.c_int64), ("err", _vp)])
+
+
+class PageSelectArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_tokens", "n_kv_heads", "page_size", "width", "budget", "sink", "local")]
+                + [("scores", _vp), ("ld", ctypes.c_int64)] + [(n, _vp) for n in ("seq_lens", "pages", "counts", "err")])
+
+
+class PagedSparseAttnArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "group", "page_size",
+                                       "n_pages", "n_rows", "max_pages", "width", "dtype")]
+                + [(n, _vp) for n in ("q", "kq", "vq", "ksc", "vsc", "page_table", "seq_lens", "rows", "pages", "counts")]
+                + [("softmax_scale", _c_float)] + [(n, _vp) for n in ("gate", "out", "lse", "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t), ("err", _vp)])
+
+
+class PagedTreeAttnArgs(ctypes.Structure):
+    _fields_ = ([(n, _c_int) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "group", "page_size",
+                                       "n_pages", "n_rows", "max_pages", "words", "dtype")]
+                + [(n, _vp) for n in ("q", "kq", "vq", "ksc", "vsc", "page_table", "prefix_lens", "rows", "mask")]
+                + [("softmax_scale", _c_float)] + [(n, _vp) for n in ("gate", "out", "lse", "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t), ("err", _vp)])
+
+
 class QSAError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"QSA status {status}: {message}")
@@ -163,7 +197,9 @@ def _declare(L: ctypes.CDLL, path: str) -> None:
                        ("qsa_score_noalloc", ScoreArgs), ("qsa_select", SelectArgs),
                        ("qsa_paged_prep", PagedPrepArgs), ("qsa_paged_gather", PagedGatherArgs),
                        ("qsa_paged_attn", PagedAttnArgs), ("qsa_page_update", PageUpdateArgs),
-                       ("qsa_page_compact", PageCompactArgs)):
+                       ("qsa_page_compact", PageCompactArgs), ("qsa_page_bounds", PageBoundsArgs),
+                       ("qsa_page_score", PageScoreArgs), ("qsa_page_select", PageSelectArgs),
+                       ("qsa_paged_sparse_attn", PagedSparseAttnArgs), ("qsa_paged_tree_attn", PagedTreeAttnArgs)):
         f = getattr(L, name)
         f.argtypes = [ctypes.POINTER(argt), _vp]
         f.restype = _c_int
@@ -175,8 +211,10 @@ def _declare(L: ctypes.CDLL, path: str) -> None:
     L.qsa_check_word.restype = _c_int
     L.qsa_score_workspace_bytes.argtypes = [_c_int, _c_int]
     L.qsa_score_workspace_bytes.restype = ctypes.c_size_t
-    L.qsa_paged_attn_workspace_bytes.argtypes = [_c_int, _c_int, _c_int]
-    L.qsa_paged_attn_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("qsa_paged_attn", "qsa_paged_sparse_attn", "qsa_paged_tree_attn"):
+        f = getattr(L, name + "_workspace_bytes")
+        f.argtypes = [_c_int, _c_int, _c_int]
+        f.restype = ctypes.c_size_t
     L.qsa_pages_workspace_bytes.argtypes = [_c_int, _c_int]
     L.qsa_pages_workspace_bytes.restype = ctypes.c_size_t
     L.qsa_status_str.argtypes = [_c_int]

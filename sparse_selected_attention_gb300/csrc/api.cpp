@@ -64,6 +64,40 @@ Fault check_pages(const A &a) {
     return kFine;
 }
 
+bool attn_heads(int n_q_heads, int n_kv_heads) {
+    return n_kv_heads >= 1 && n_kv_heads <= 65535 && n_q_heads >= 1 && n_q_heads % n_kv_heads == 0 && n_q_heads / n_kv_heads <= 16;
+}
+
+// The checks that the calls of tokens on a paged cache share: shapes, types, the
+// table; then, for the attention, its buffers.
+template <class A>
+Fault check_tokens(const A &a) {
+    if (!paged_shape(a.head_dim, a.group) || !attn_heads(a.n_q_heads, a.n_kv_heads))
+        return {QSA_ERR_UNSUPPORTED,
+                "supported shapes are (head_dim 128, group 32) or (head_dim 256, group 64), n_q_heads a multiple of "
+                "n_kv_heads with at most 16 query heads per KV head"};
+    if (!paged_page(a.page_size)) return {QSA_ERR_UNSUPPORTED, "page_size must be 16, 32, 64, 128 or 256"};
+    if (a.dtype != QSA_F16 && a.dtype != QSA_BF16) return {QSA_ERR_INVALID_ARG, "dtype must be QSA_F16 or QSA_BF16"};
+    if (a.n_tokens < 0 || a.n_pages < 1 || a.n_rows < (a.n_tokens ? 1 : 0) || a.max_pages < 1)
+        return {QSA_ERR_INVALID_ARG, "negative n_tokens, n_pages or max_pages below 1, or no n_rows for its tokens"};
+    if (!a.rows && a.n_rows < a.n_tokens) return {QSA_ERR_INVALID_ARG, "without rows the table needs a row per token"};
+    if ((long long)a.n_pages * a.page_size > kMaxInt || (long long)a.max_pages * a.page_size > kMaxInt)
+        return {QSA_ERR_INVALID_ARG, "n_pages * page_size or max_pages * page_size beyond int32"};
+    if ((long long)a.max_pages * a.page_size > 1ll << 30) return {QSA_ERR_UNSUPPORTED, "rows of more than 2^30 cells"};
+    if ((long long)a.n_tokens * a.n_kv_heads > kMaxInt) return {QSA_ERR_UNSUPPORTED, "n_tokens * n_kv_heads beyond int32"};
+    return kFine;
+}
+template <class A>
+Fault check_attn(const A &a, size_t workspace) {
+    if (!a.q || !a.kq || !a.vq || !a.ksc || !a.vsc || !a.page_table || !a.out || !a.workspace) return {QSA_ERR_INVALID_ARG, "NULL buffer"};
+    if (a.workspace_bytes < workspace) return {QSA_ERR_INVALID_ARG, "workspace smaller than its workspace_bytes()"};
+    if (!aligned(a.q, 16) || !aligned(a.kq, 16) || !aligned(a.vq, 16) || !aligned(a.ksc, 8) || !aligned(a.vsc, 8) ||
+        !aligned(a.page_table, 4) || !aligned(a.rows, 4) || !aligned(a.gate, 8) || !aligned(a.out, 16) || !aligned(a.lse, 4) ||
+        !aligned(a.workspace, 256) || !aligned(a.err, 4))
+        return {QSA_ERR_INVALID_ARG, "misaligned buffer"};
+    return kFine;
+}
+
 qsa_status fail_in(const char *where, const Fault &f) {
     std::snprintf(g_last_error, sizeof g_last_error, "%s: %s", where, f.what);
     return f.status;
@@ -264,7 +298,9 @@ qsa_status qsa_check_word(unsigned int *out) {
                                                       qsa::take_check_word_prep, qsa::take_check_word_select,
                                                       qsa::take_check_word_ids,  qsa::take_check_word_paged_prep,
                                                       qsa::take_check_word_paged_attn, qsa::take_check_word_paged_group,
-                                                      qsa::take_check_word_pages};
+                                                      qsa::take_check_word_pages, qsa::take_check_word_page_bounds,
+                                                      qsa::take_check_word_page_score, qsa::take_check_word_page_select,
+                                                      qsa::take_check_word_paged_sparse, qsa::take_check_word_paged_tree};
     for (auto rd : readers) {
         unsigned int v = 0u;
         const cudaError_t e = rd(&v);
@@ -463,6 +499,106 @@ qsa_status qsa_page_compact(const qsa_page_compact_args *a, void *stream) {
         return fail(QSA_ERR_INVALID_ARG, "qsa_page_compact: page_table_out overlaps page_table without being it");
     cudaError_t e = qsa::launch_page_compact(*a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_page_compact");
+}
+
+qsa_status qsa_page_bounds(const qsa_page_bounds_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_page_bounds: args is NULL");
+    if (!paged_shape(a->head_dim, a->group) || a->n_kv_heads < 1 || a->n_kv_heads > 65535 || !paged_page(a->page_size))
+        return fail(QSA_ERR_UNSUPPORTED,
+                    "qsa_page_bounds: supported pools are (head_dim 128, group 32) or (head_dim 256, group 64), 1..65535 KV "
+                    "heads and page_size 16, 32, 64, 128 or 256");
+    if (a->n_rows < 0 || a->max_pages < 1 || a->n_pages < 1)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_bounds: negative n_rows, or max_pages or n_pages below 1");
+    if ((long long)a->n_pages * a->page_size > kMaxInt || (long long)a->max_pages * a->page_size > kMaxInt)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_bounds: n_pages * page_size or max_pages * page_size beyond int32");
+    if (a->n_rows == 0) return QSA_OK;
+    if (!a->page_table || !a->seq_lens || !a->kq || !a->ksc || !a->hi_q || !a->lo_q || !a->hi_sc || !a->lo_sc)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_bounds: NULL buffer");
+    if (!aligned(a->page_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->n_new, 4) || !aligned(a->kq, 16) || !aligned(a->ksc, 8) ||
+        !aligned(a->hi_q, 16) || !aligned(a->lo_q, 16) || !aligned(a->hi_sc, 8) || !aligned(a->lo_sc, 8) || !aligned(a->err, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_bounds: misaligned buffer");
+    const cudaError_t e = qsa::launch_page_bounds(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_page_bounds");
+}
+
+qsa_status qsa_page_score(const qsa_page_score_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_page_score: args is NULL");
+    const Fault f = check_tokens(*a);
+    if (f.status != QSA_OK) return fail_in("qsa_page_score", f);
+    if (a->ld < a->max_pages) return fail(QSA_ERR_INVALID_ARG, "qsa_page_score: ld < max_pages");
+    if (a->n_tokens == 0) return QSA_OK;
+    if (!a->q || !a->hi_q || !a->lo_q || !a->hi_sc || !a->lo_sc || !a->page_table || !a->seq_lens || !a->scores)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_score: NULL buffer");
+    if (!aligned(a->q, 16) || !aligned(a->hi_q, 16) || !aligned(a->lo_q, 16) || !aligned(a->hi_sc, 8) || !aligned(a->lo_sc, 8) ||
+        !aligned(a->page_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->rows, 4) || !aligned(a->scores, 4) || !aligned(a->err, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_score: misaligned buffer");
+    const cudaError_t e = qsa::launch_page_score(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_page_score");
+}
+
+qsa_status qsa_page_select(const qsa_page_select_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_page_select: args is NULL");
+    if (!paged_page(a->page_size)) return fail(QSA_ERR_UNSUPPORTED, "qsa_page_select: page_size must be 16, 32, 64, 128 or 256");
+    if (a->n_tokens < 0 || a->n_kv_heads < 1 || a->ld < 1)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_select: negative n_tokens, or n_kv_heads or ld below 1");
+    if (a->budget < 1 || a->budget > a->width || a->sink < 0 || a->local < 0 || (long long)a->sink + a->local > a->budget)
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_select: requires 1 <= budget <= width, sink, local >= 0 and sink + local <= budget");
+    if ((long long)a->n_tokens * a->n_kv_heads > kMaxInt)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_page_select: n_tokens * n_kv_heads beyond int32");
+    if (a->n_tokens == 0) return QSA_OK;
+    if (!a->scores || !a->seq_lens || !a->pages || !a->counts) return fail(QSA_ERR_INVALID_ARG, "qsa_page_select: NULL buffer");
+    if (!aligned(a->scores, 4) || !aligned(a->seq_lens, 4) || !aligned(a->pages, 4) || !aligned(a->counts, 4) || !aligned(a->err, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_page_select: misaligned buffer");
+    const cudaError_t e = qsa::launch_page_select(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_page_select");
+}
+
+size_t qsa_paged_sparse_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
+    if ((head_dim != 128 && head_dim != 256) || !attn_heads(n_q_heads, n_kv_heads)) return 0;
+    return qsa::paged_sparse_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim);
+}
+
+qsa_status qsa_paged_sparse_attn(const qsa_paged_sparse_attn_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_sparse_attn: args is NULL");
+    Fault f = check_tokens(*a);
+    if (f.status != QSA_OK) return fail_in("qsa_paged_sparse_attn", f);
+    if (a->width < 1) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_sparse_attn: width below 1");
+    if ((long long)a->width * a->page_size > 1ll << 30)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_sparse_attn: lists of more than 2^30 cells");
+    if (!std::isfinite(a->softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_sparse_attn: softmax_scale not finite");
+    if (a->n_tokens == 0) return QSA_OK;
+    f = check_attn(*a, qsa_paged_sparse_attn_workspace_bytes(a->n_q_heads, a->n_kv_heads, a->head_dim));
+    if (f.status != QSA_OK) return fail_in("qsa_paged_sparse_attn", f);
+    if (!a->seq_lens || !a->pages || !a->counts) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_sparse_attn: NULL buffer");
+    if (!aligned(a->seq_lens, 4) || !aligned(a->pages, 4) || !aligned(a->counts, 4))
+        return fail(QSA_ERR_INVALID_ARG, "qsa_paged_sparse_attn: misaligned buffer");
+    const cudaError_t e = qsa::launch_paged_sparse_attn(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_paged_sparse_attn");
+}
+
+size_t qsa_paged_tree_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
+    return qsa_paged_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim);
+}
+
+qsa_status qsa_paged_tree_attn(const qsa_paged_tree_attn_args *a, void *stream) {
+    g_last_error[0] = 0;
+    if (!a) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_tree_attn: args is NULL");
+    Fault f = check_tokens(*a);
+    if (f.status != QSA_OK) return fail_in("qsa_paged_tree_attn", f);
+    if (a->words < 1 || a->words > QSA_TREE_MAX_WORDS)
+        return fail(QSA_ERR_UNSUPPORTED, "qsa_paged_tree_attn: a mask has 1 to 32 words (QSA_TREE_MAX_WORDS)");
+    if (!std::isfinite(a->softmax_scale)) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_tree_attn: softmax_scale not finite");
+    if (a->n_tokens == 0) return QSA_OK;
+    f = check_attn(*a, qsa_paged_tree_attn_workspace_bytes(a->n_q_heads, a->n_kv_heads, a->head_dim));
+    if (f.status != QSA_OK) return fail_in("qsa_paged_tree_attn", f);
+    if (!a->prefix_lens || !a->mask) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_tree_attn: NULL buffer");
+    if (!aligned(a->prefix_lens, 4) || !aligned(a->mask, 4)) return fail(QSA_ERR_INVALID_ARG, "qsa_paged_tree_attn: misaligned buffer");
+    const cudaError_t e = qsa::launch_paged_tree_attn(*a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? QSA_OK : cuda_fail(e, "qsa_paged_tree_attn");
 }
 
 }  // extern "C"

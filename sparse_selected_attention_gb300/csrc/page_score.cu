@@ -1,0 +1,325 @@
+// qsa_page_score: what the keys of each page of a sequence can reach at most, by
+// the page's bounds.
+//
+//   S = sum_d hi_d sum_heads max(q_d, 0) + lo_d sum_heads min(q_d, 0)
+//
+// The most that q . k can be for keys between lo and hi takes hi where q is
+// positive and lo where it is negative; over heads that is linear in the sums of
+// the positive and of the negative parts, so a page costs two rows of D codes and
+// not one per head.  It is bound by reading the bounds, 2 D + 16 bytes per page
+// and KV head, against 4 D flops per token.
+//
+// Pages are the M side (16 a warp) of m16n8k16 products, the sums of up to 4 NT
+// tokens of one sequence the N side, as two fp16 parts each under a power of two
+// per token (22 bits).  Codes go from memory to fragments: lane (g, r) holds codes
+// 8 S r .. 8 S r + 8 S - 1 of each quarter of pages g and g + 8, so that eight
+// bytes (or sixteen) are one load and a k-step's dims are of one quarter.  Its
+// products are summed per quarter, and the quarter's scale multiplies in fp32.
+//
+// The tiles of 16 pages of all sequences are shared out evenly (as the units of
+// paged_rows.cuh are); each CTA finds its place by itself.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "check.cuh"
+#include "qsa_internal.h"
+#include "tc_common.cuh"
+
+namespace qsa {
+namespace {
+
+constexpr int W = 4, THREADS = 32 * W;
+constexpr int TILE = 16;  // pages of a warp at a time
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2 *>(&u); }
+// Codes 0 and 2 (or 1 and 3) of w.
+__device__ __forceinline__ uint32_t pair(uint32_t w, bool odd) {
+    return h2u(__hsub2(u2h(tc::prmt(w ^ 0x80808080u, 0x64646464u, odd ? 0x4341 : 0x4240)), u2h(0x64806480u)));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint2 b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y));
+}
+
+// The power of two that puts a token's largest sum into [2^13, 2^14), as far as
+// it goes; 0 where that is 0, infinite or NaN.
+__device__ __forceinline__ int sum_exponent(float m) {
+    const uint32_t u = __float_as_uint(m);
+    if (u == 0u || u >= 0x7F800000u) return 0;
+    return min(max(13 - ((int)(u >> 23) - 127), -120), 120);
+}
+
+// The pages of token t's sequence.
+__device__ __forceinline__ int pages_of(const qsa_page_score_args &a, int t, int &row, bool &bad) {
+    row = a.rows ? __ldg(a.rows + t) : t;
+    const int len = __ldg(a.seq_lens + t), most = a.max_pages * a.page_size;
+    if (row < 0 || row >= a.n_rows) {
+        bad = true;
+        row = 0;
+        return 0;
+    }
+    bad |= len < 0 || len > most;
+    return (min(max(len, 0), most) + a.page_size - 1) >> (31 - __clz(a.page_size));
+}
+
+template <int S, int NT>
+struct Smem {
+    // The tokens' sums as B fragments: by bound, k-step, four tokens, lane.
+    uint2 b[2][8 * S][NT][32];
+    float unscale[4 * NT];      // 2^-e of a token
+    int pages[4 * NT];
+    uint32_t top[4 * NT];
+    long long scan[W];
+    long long total, before;
+    int t;
+};
+
+// S = head_dim / 128.  A group: up to 4 NT consecutive tokens of one sequence, not
+// across multiples of 4 NT; without rows, one token.
+template <int S, int NT>
+__global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_score_args a) {
+    constexpr int D = 128 * S, G = 4 * NT, Q = D / 4, KS = 2 * S;  // k-steps of a quarter
+    extern __shared__ __align__(16) uint8_t raw[];
+    Smem<S, NT> &sh = *reinterpret_cast<Smem<S, NT> *>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, r = lane & 3;
+    const int hkv = a.n_kv_heads, per = a.n_q_heads / hkv, kvh = blockIdx.x % hkv;
+    const int range = blockIdx.x / hkv, ranges = gridDim.x / hkv;
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    bool bad = false;
+    // Tokens of the group that starts at t (0: none does), and its tiles.
+    auto group_at = [&](int t, int &tiles) {
+        int row, most = pages_of(a, t, row, bad), n = 1;
+        tiles = 0;
+        if (a.rows) {
+            const int same = __ldg(a.rows + t);
+            if (t % G && __ldg(a.rows + t - 1) == same) return 0;
+            for (const int end = min(a.n_tokens, t / G * G + G); t + n < end && __ldg(a.rows + t + n) == same; ++n)
+                most = max(most, pages_of(a, t + n, row, bad));
+        }
+        tiles = (most + TILE - 1) / TILE;
+        return n;
+    };
+    // All tiles, and the group in which this CTA's share of them starts.
+    const int run = (a.n_tokens + THREADS - 1) / THREADS;
+    const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
+    long long mine = 0;
+    for (int t = t0; t < t1; ++t) {
+        int tiles;
+        group_at(t, tiles);
+        mine += tiles;
+    }
+    long long sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31) sh.scan[warp] = sum;
+    __syncthreads();
+    long long total = 0, before = sum - mine;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        before += w < warp ? sh.scan[w] : 0;
+        total += sh.scan[w];
+    }
+    const int share = (int)max((total + ranges - 1) / ranges, (long long)W);
+    const long long x0 = (long long)share * range;
+    if (x0 >= before && x0 < before + mine) {
+        for (int t = t0;; ++t) {
+            int tiles;
+            group_at(t, tiles);
+            if (x0 < before + tiles) {
+                sh.t = t;
+                sh.before = before;
+                break;
+            }
+            before += tiles;
+        }
+    }
+    __syncthreads();
+    int left = (int)max(min((long long)share, total - x0), 0ll);
+    int t = sh.t, i0 = left ? (int)(x0 - sh.before) : 0, tiles = 0;
+    while (left > 0) {
+        const int n = group_at(t, tiles);
+        const int i1 = min(tiles, i0 + left);
+        if (i1 > i0) {
+            // The tokens' sums: a thread takes two dims of a token.
+            __syncthreads();  // of the group before
+            if (tid < G) {
+                int row;
+                sh.top[tid] = 0u;
+                sh.pages[tid] = tid < n ? pages_of(a, t + tid, row, bad) : 0;
+            }
+            __syncthreads();
+            constexpr int PAIRS = D / 2, AT_ONCE = THREADS / PAIRS, ROUNDS = (G + AT_ONCE - 1) / AT_ONCE;
+            const int d = tid % PAIRS * 2, first = tid / PAIRS;
+            // Place of dims d, d + 1 (of different halves of a k-step) as codes of a quarter.
+            const int in = d % Q, rr = in / (8 * S), e = in % (8 * S), ks = d / Q * KS + e / 4;
+            float2 up[ROUNDS], down[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int k = first + i * AT_ONCE;
+                up[i] = down[i] = make_float2(0.0f, 0.0f);
+                if (k < n) {
+                    const size_t at = ((size_t)(t + k) * a.n_q_heads + (size_t)kvh * per) * D + d;
+                    for (int h = 0; h < per; ++h) {
+                        if (!QSA_IN(at + (size_t)h * D + 1, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
+                        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.q) + at + (size_t)h * D));
+                        const float2 v = a.dtype == QSA_F16 ? __half22float2(u2h(w))
+                                                            : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+                        up[i].x += fmaxf(v.x, 0.0f);
+                        up[i].y += fmaxf(v.y, 0.0f);
+                        down[i].x += fminf(v.x, 0.0f);
+                        down[i].y += fminf(v.y, 0.0f);
+                        // A NaN is lost in maximum and minimum.
+                        if (v.x != v.x) up[i].x = v.x;
+                        if (v.y != v.y) up[i].y = v.y;
+                    }
+                    const float m = fabsf(fmaxf(fmaxf(up[i].x, up[i].y), fmaxf(-down[i].x, -down[i].y)));
+                    atomicMax(&sh.top[k], __float_as_uint(m));  // not negative: bits order as values do
+                }
+            }
+            __syncthreads();
+            __half *frag = reinterpret_cast<__half *>(sh.b);
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int k = first + i * AT_ONCE;
+                if (k >= G) continue;
+                const int ex = sum_exponent(__uint_as_float(sh.top[k]));
+                const float f = exp2i(ex);
+                if (tid % PAIRS == 0) sh.unscale[k] = exp2i(-ex);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float2 v = b ? down[i] : up[i];
+#pragma unroll
+                    for (int odd = 0; odd < 2; ++odd) {
+                        const float x = (odd ? v.y : v.x) * f;
+                        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+                        // Column 2 (k % 4) + part, row: register `odd`, half by the pair.
+                        const size_t at = ((((size_t)b * 8 * S + ks) * NT + k / 4) * 32 + (2 * (k % 4)) * 4 + rr) * 4 + odd * 2 + (e % 4) / 2;
+                        frag[at] = hi;
+                        frag[at + 16] = lo;
+                    }
+                }
+            }
+            __syncthreads();
+            int row;
+            pages_of(a, t, row, bad);
+            const int most = tiles * TILE;  // pages of the longest token, or a few more
+            for (int i = i0 + warp; i < i1; i += W) {
+                size_t at[2];
+                bool there[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = i * TILE + g + 8 * e;
+                    const int page = j < a.max_pages && j < most ? __ldg(a.page_table + (size_t)row * a.max_pages + j) : -1;
+                    there[e] = page >= 0 && page < a.n_pages;
+                    at[e] = ((size_t)(there[e] ? page : 0) * hkv + kvh);
+                    there[e] = there[e] && QSA_IN(at[e], (size_t)a.n_pages * hkv);
+                }
+                float y[NT][4];
+#pragma unroll
+                for (int k = 0; k < NT; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int8_t *codes = b ? a.lo_q : a.hi_q;
+                    const uint16_t *scales = b ? a.lo_sc : a.hi_sc;
+                    uint32_t w[4][2][2 * S];
+                    uint2 sc[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        sc[e] = make_uint2(0u, 0u);
+                        if (there[e]) sc[e] = __ldg(reinterpret_cast<const uint2 *>(scales + at[e] * 4));
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int8_t *src = codes + at[e] * D + q * Q + 8 * S * r;
+#pragma unroll
+                            for (int c = 0; c < 2 * S; ++c) w[q][e][c] = 0u;
+                            if (there[e]) {
+                                if constexpr (S == 1)
+                                    *reinterpret_cast<uint2 *>(w[q][e]) = __ldg(reinterpret_cast<const uint2 *>(src));
+                                else
+                                    *reinterpret_cast<uint4 *>(w[q][e]) = __ldg(reinterpret_cast<const uint4 *>(src));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float s[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const __half2 h = u2h(q >> 1 ? sc[e].y : sc[e].x);
+                            s[e] = q & 1 ? __high2float(h) : __low2float(h);
+                        }
+                        uint32_t x[KS][4];
+#pragma unroll
+                        for (int c = 0; c < KS; ++c) {
+                            x[c][0] = pair(w[q][0][c], false);
+                            x[c][1] = pair(w[q][1][c], false);
+                            x[c][2] = pair(w[q][0][c], true);
+                            x[c][3] = pair(w[q][1][c], true);
+                        }
+#pragma unroll
+                        for (int k = 0; k < NT; ++k) {
+                            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int c = 0; c < KS; ++c) mma(acc, x[c], sh.b[b][q * KS + c][k][lane]);
+                            y[k][0] = fmaf(acc[0] + acc[1], s[0], y[k][0]);
+                            y[k][2] = fmaf(acc[2] + acc[3], s[1], y[k][2]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    const int token = 4 * k + r;
+                    if (token >= n) continue;
+                    const int count = sh.pages[token];
+                    const float f = sh.unscale[token];
+                    float *dst = a.scores + ((size_t)(t + token) * hkv + kvh) * a.ld;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = i * TILE + g + 8 * e;
+                        if (j >= count) continue;
+                        bad |= !there[e];
+                        if (QSA_IN(((size_t)(t + token) * hkv + kvh) * a.ld + j, (size_t)a.n_tokens * hkv * a.ld))
+                            dst[j] = there[e] ? y[k][2 * e] * f : -CUDART_INF_F;
+                    }
+                }
+            }
+        }
+        left -= i1 - i0;
+        i0 = 0;
+        t += max(n, 1);
+    }
+    if (__syncthreads_or(bad) && tid == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
+}
+
+template <int S, int NT>
+cudaError_t launch(const qsa_page_score_args &a, cudaStream_t s) {
+    constexpr int SMEM = (int)sizeof(Smem<S, NT>), CTAS_PER_SM = NT == 1 ? 6 : 3;
+    cudaError_t e = cudaFuncSetAttribute(page_score_kernel<S, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (a.max_pages + TILE - 1) / TILE, most = a.n_tokens * ((tiles + W - 1) / W);
+    const int resident = std::max(152 * CTAS_PER_SM / a.n_kv_heads, 1);
+    const int ranges = (int)std::min<long long>(most, resident);
+    return launch_dependent(page_score_kernel<S, NT>, dim3(ranges * a.n_kv_heads), dim3(THREADS), SMEM, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_page_score(const qsa_page_score_args &a, cudaStream_t s) {
+    const bool many = a.rows && a.n_tokens >= 256;
+    if (a.head_dim == 128) return many ? launch<1, 8>(a, s) : launch<1, 1>(a, s);
+    return many ? launch<2, 8>(a, s) : launch<2, 1>(a, s);
+}
+
+}  // namespace qsa
+
+QSA_DEFINE_CHECK_READER(take_check_word_page_score)

@@ -1,16 +1,30 @@
-// What the two kernels of qsa_paged_attn share: paged_attn.cu takes rows one by
-// one, paged_group.cu rows of q that read one sequence together.
+// What the kernels of attention over the paged cache share: paged_rows.cuh takes
+// rows one by one, paged_group.cu rows of q that read one sequence together.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include <type_traits>
+
 #include "check.cuh"
 #include "qsa_internal.h"
 #include "tc_common.cuh"
 
 namespace qsa {
+
+// What a row of q attends to.  qsa_paged_attn_args alone: all cells of its sequence
+// up to its length.
+struct ListedArgs : qsa_paged_attn_args {  // cells of listed pages, a list per KV head
+    const int32_t *lists, *counts;         // [n_tokens][n_kv_heads][width], [n_tokens][n_kv_heads]
+    int width;
+};
+struct TreeArgs : qsa_paged_attn_args {  // cells up to seq_lens, and those that bits say after them
+    const uint32_t *mask;                // [n_tokens][words]
+    int words;
+};
+
 namespace {
 
 constexpr float LN2 = 0.6931471805599453f;
@@ -76,7 +90,7 @@ struct Work {
 // Groups: every `block` rows, counted from its start, of a run of rows of q with
 // one table row (within aligned spans of group_span rows, which bound the search
 // for the start).  Either paged_group.cu takes all rows of a call, by groups, or
-// paged_attn.cu, one by one: one of them alone, as a few rows of a kind would
+// paged_rows.cuh, one by one: one of them alone, as a few rows of a kind would
 // still cost its whole latency (14 groups of four rows and three rows more, 2 K
 // cells, 8/2 heads of 256: 59 us by both, 44 us one by one).  Both decide it from
 // the lengths.
@@ -126,9 +140,14 @@ __device__ __forceinline__ int group_end(const qsa_paged_attn_args &a, int t, in
     return min(min(a.n_tokens, t + block), (t | (group_span(block) - 1)) + 1);
 }
 
-// Row t's length, cut to its range, and its table row (0 with length 0 if it
-// is out of range).
-__device__ __forceinline__ int row_len(const qsa_paged_attn_args &a, int t, int &row, bool &bad) {
+template <class A>
+constexpr bool LISTED = std::is_same<A, ListedArgs>::value;
+template <class A>
+constexpr bool TREE = std::is_same<A, TreeArgs>::value;
+
+// Row t's table row (0 if it is out of range) and seq_lens entry, cut to its range
+// (0 with a table row out of range).
+__device__ __forceinline__ int row_cells(const qsa_paged_attn_args &a, int t, int &row, bool &bad) {
     row = a.rows ? __ldg(a.rows + t) : t;
     const int len = __ldg(a.seq_lens + t), most = a.max_pages * a.page_size;
     if (row < 0 || row >= a.n_rows) {
@@ -138,6 +157,41 @@ __device__ __forceinline__ int row_len(const qsa_paged_attn_args &a, int t, int 
     }
     bad |= len < 0 || len > most;
     return min(max(len, 0), most);
+}
+// Cells of row t that a KV head goes through: of its sequence, or of its list one
+// after the other.  `sure`: the row's seq_lens entry; of a tree's row, the cells
+// that it sees for certain.
+template <class A>
+__device__ __forceinline__ int row_len(const A &a, int t, int kvh, int &row, int &sure, bool &bad) {
+    sure = row_cells(a, t, row, bad);
+    if constexpr (LISTED<A>) {
+        const int n = __ldg(a.counts + (size_t)t * a.n_kv_heads + kvh);
+        bad |= n < 0 || n > a.width;
+        return sure ? min(max(n, 0), a.width) * a.page_size : 0;
+    } else if constexpr (TREE<A>) {
+        if (a.rows ? __ldg(a.rows + t) != row : t != row) return 0;  // a table row out of range
+        int span = 0;
+        for (int w = 0; w < a.words; ++w) {
+            const uint32_t m = __ldg(a.mask + (size_t)t * a.words + w);
+            if (m) span = 32 * w + 32 - __clz(m);
+        }
+        const int most = a.max_pages * a.page_size;
+        bad |= span > most - sure;
+        return min(sure + span, most);
+    } else {
+        return sure;
+    }
+}
+template <class A>
+__device__ __forceinline__ int row_len(const A &a, int t, int kvh, int &row, bool &bad) {
+    int sure;
+    return row_len(a, t, kvh, row, sure, bad);
+}
+// Which of 32 cells from c on row t of a tree sees, of those below its length.
+__device__ __forceinline__ uint32_t tree_bits(const TreeArgs &a, int t, int c, int sure) {
+    const int off = c - sure, k = off >> 5;
+    auto word = [&](int i) { return i < 0 ? 0xffffffffu : i < a.words ? __ldg(a.mask + (size_t)t * a.words + i) : 0u; };
+    return __funnelshift_r(word(k), word(k + 1), off & 31);
 }
 __device__ __forceinline__ void store_out(const qsa_paged_attn_args &a, size_t i, float2 y) {
     if (a.dtype == QSA_F16)
@@ -311,5 +365,6 @@ size_t paged_group_workspace_bytes(int head_dim);
 // paged_group.cu: the groups, where a.rows is given.  ws as Work of GROUP_ROWS
 // rows; `ctas` receives how many leave partials there, to be joined.
 cudaError_t launch_paged_group(const qsa_paged_attn_args &a, void *ws, int &ctas, cudaStream_t s);
+cudaError_t launch_paged_group(const TreeArgs &a, void *ws, int &ctas, cudaStream_t s);
 
 }  // namespace qsa

@@ -250,6 +250,122 @@ int compact(PyObject *entry, Args o) {
     return run(entry, a, c.stream(o[12]));
 }
 
+// Page bounds: codes [pages, Hkv, D], scales [pages, Hkv, 4].
+template <class A>
+void bounds_of(A &a, const Call &c, Args o, int64_t pages, int64_t hkv, int64_t D) {
+    a.hi_q = c.in<int8_t>(o[0], at::kChar, {pages, hkv, D}), a.lo_q = c.in<int8_t>(o[1], at::kChar, {pages, hkv, D});
+    a.hi_sc = c.in<uint16_t>(o[2], at::kHalf, {pages, hkv, 4}), a.lo_sc = c.in<uint16_t>(o[3], at::kHalf, {pages, hkv, 4});
+}
+int whole(PyObject *o) {
+    const long long v = PyLong_AsLongLong(o);
+    want(!(v == -1 && PyErr_Occurred()) && v >= INT_MIN && v <= INT_MAX);
+    return (int)v;
+}
+
+// page_table seq_lens kq ksc hi_q lo_q hi_sc lo_sc n_new err stream
+int bounds(PyObject *entry, Args o) {
+    const at::Tensor &table = tensor(o[0]), &kq = tensor(o[2]);
+    const Call c(kq);
+    want(kq.dim() == 4 && table.dim() == 2);
+    const int64_t pages = kq.size(0), page = kq.size(1), hkv = kq.size(2), D = kq.size(3), rows = table.size(0);
+    qsa_page_bounds_args a{};
+    a.n_rows = small(rows), a.max_pages = small(table.size(1)), a.n_pages = small(pages), a.page_size = small(page);
+    a.n_kv_heads = small(hkv), a.head_dim = small(D), a.group = a.head_dim / 4;
+    a.page_table = static_cast<const int32_t *>(c.in(table, at::kInt, table.sizes()));
+    a.seq_lens = c.in<int32_t>(o[1], at::kInt, {rows}), a.n_new = c.opt<int32_t>(o[8], at::kInt, {rows});
+    a.kq = static_cast<const int8_t *>(c.in(kq, at::kChar, kq.sizes()));
+    a.ksc = c.in<uint16_t>(o[3], at::kHalf, {pages, page, hkv, 4});
+    bounds_of(a, c, o + 4, pages, hkv, D);
+    a.err = c.err(o[9]);
+    return run(entry, a, c.stream(o[10]));
+}
+
+// q hi_q lo_q hi_sc lo_sc page_table seq_lens scores page_size rows err stream
+int score(PyObject *entry, Args o) {
+    const at::Tensor &q = tensor(o[0]), &hi = tensor(o[1]), &table = tensor(o[5]), &scores = tensor(o[7]);
+    const Call c(q);
+    want(q.dim() == 3 && hi.dim() == 3 && table.dim() == 2 && scores.dim() == 3);
+    const int64_t T = q.size(0), H = q.size(1), D = q.size(2), hkv = hi.size(1);
+    want(hi.size(2) == D && (q.scalar_type() == at::kHalf || q.scalar_type() == at::kBFloat16));
+    qsa_page_score_args a{};
+    a.n_tokens = small(T), a.n_q_heads = small(H), a.n_kv_heads = small(hkv), a.head_dim = small(D), a.group = a.head_dim / 4;
+    a.page_size = whole(o[8]), a.n_pages = small(hi.size(0)), a.n_rows = small(table.size(0)), a.max_pages = small(table.size(1));
+    a.dtype = dtype_code(q.scalar_type());
+    a.q = c.in(q, q.scalar_type(), {T, H, D});
+    bounds_of(a, c, o + 1, hi.size(0), hkv, D);
+    a.page_table = static_cast<const int32_t *>(c.in(table, at::kInt, table.sizes()));
+    a.seq_lens = c.in<int32_t>(o[6], at::kInt, {T}), a.rows = c.opt<int32_t>(o[9], at::kInt, {T});
+    a.scores = static_cast<float *>(c.in(scores, at::kFloat, {T, hkv, scores.size(2)})), a.ld = scores.size(2);
+    a.err = c.err(o[10]);
+    return run(entry, a, c.stream(o[11]));
+}
+
+// scores seq_lens pages counts page_size budget sink local err stream
+int select(PyObject *entry, Args o) {
+    const at::Tensor &scores = tensor(o[0]), &pages = tensor(o[2]);
+    const Call c(scores);
+    want(scores.dim() == 3 && pages.dim() == 3);
+    const int64_t T = scores.size(0), hkv = scores.size(1), w = pages.size(2);
+    qsa_page_select_args a{};
+    a.n_tokens = small(T), a.n_kv_heads = small(hkv), a.page_size = whole(o[4]), a.width = small(w);
+    a.budget = whole(o[5]), a.sink = whole(o[6]), a.local = whole(o[7]);
+    a.scores = static_cast<const float *>(c.in(scores, at::kFloat, scores.sizes())), a.ld = scores.size(2);
+    a.seq_lens = c.in<int32_t>(o[1], at::kInt, {T});
+    a.pages = static_cast<int32_t *>(c.in(pages, at::kInt, {T, hkv, w})), a.counts = c.in<int32_t>(o[3], at::kInt, {T, hkv});
+    a.err = c.err(o[8]);
+    return run(entry, a, c.stream(o[9]));
+}
+
+// What the two calls below have in common: q kq vq ksc vsc page_table; out
+// workspace rows softmax_scale gate lse err
+template <class A>
+Call attn_parts(A &a, Args first, Args last) {
+    const at::Tensor &q = tensor(first[0]), &kq = tensor(first[1]), &table = tensor(first[5]);
+    const Call c(q);
+    want(q.dim() == 3 && kq.dim() == 4 && table.dim() == 2);
+    const int64_t T = q.size(0), H = q.size(1), D = q.size(2);
+    want(kq.size(3) == D && (q.scalar_type() == at::kHalf || q.scalar_type() == at::kBFloat16));
+    a.n_tokens = small(T), a.n_q_heads = small(H), a.n_kv_heads = small(kq.size(2)), a.head_dim = small(D), a.group = a.head_dim / 4;
+    a.page_size = small(kq.size(1)), a.n_pages = small(kq.size(0)), a.n_rows = small(table.size(0)), a.max_pages = small(table.size(1));
+    a.dtype = dtype_code(q.scalar_type());
+    c.cache(a, first + 1);
+    a.q = c.in(q, q.scalar_type(), {T, H, D});
+    a.page_table = static_cast<const int32_t *>(c.in(table, at::kInt, table.sizes()));
+    a.out = c.in<void>(last[0], q.scalar_type(), {T, H, D});
+    a.workspace = c.scratch(last[1], a.workspace_bytes);
+    a.rows = c.opt<int32_t>(last[2], at::kInt, {T});
+    a.softmax_scale = last[3] == Py_None ? (float)std::pow((double)D, -0.5) : number(last[3]);
+    a.gate = c.opt<float>(last[4], at::kFloat, {T, H, D}), a.lse = c.opt<float>(last[5], at::kFloat, {T, H});
+    a.err = c.err(last[6]);
+    return c;
+}
+
+// q kq vq ksc vsc page_table seq_lens pages counts out workspace rows softmax_scale gate lse err stream
+int sparse_attn(PyObject *entry, Args o) {
+    qsa_paged_sparse_attn_args a{};
+    const Call c = attn_parts(a, o, o + 9);
+    const at::Tensor &pages = tensor(o[7]);
+    want(pages.dim() == 3);
+    const int64_t T = a.n_tokens, hkv = a.n_kv_heads;
+    a.width = small(pages.size(2));
+    a.seq_lens = c.in<int32_t>(o[6], at::kInt, {T});
+    a.pages = static_cast<const int32_t *>(c.in(pages, at::kInt, {T, hkv, pages.size(2)}));
+    a.counts = c.in<int32_t>(o[8], at::kInt, {T, hkv});
+    return run(entry, a, c.stream(o[16]));
+}
+
+// q kq vq ksc vsc page_table prefix_lens mask out workspace rows softmax_scale gate lse err stream
+int tree_attn(PyObject *entry, Args o) {
+    qsa_paged_tree_attn_args a{};
+    const Call c = attn_parts(a, o, o + 8);
+    const at::Tensor &mask = tensor(o[7]);
+    want(mask.dim() == 2);
+    a.words = small(mask.size(1));
+    a.prefix_lens = c.in<int32_t>(o[6], at::kInt, {a.n_tokens});
+    a.mask = static_cast<const int32_t *>(c.in(mask, at::kInt, {a.n_tokens, mask.size(1)}));
+    return run(entry, a, c.stream(o[15]));
+}
+
 // What is thrown here is said again by Python.
 template <int (*F)(PyObject *, Args), int N>
 PyObject *entry(PyObject *, Args o, Py_ssize_t n) {
@@ -263,7 +379,9 @@ PyObject *entry(PyObject *, Args o, Py_ssize_t n) {
 }
 #define QSA_METHOD(name, n) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(entry<name, n>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {QSA_METHOD(prep, 18),   QSA_METHOD(gather, 11),  QSA_METHOD(attn, 15),
-                         QSA_METHOD(update, 16), QSA_METHOD(compact, 13), {nullptr, nullptr, 0, nullptr}};
+                         QSA_METHOD(update, 16), QSA_METHOD(compact, 13), QSA_METHOD(bounds, 11),
+                         QSA_METHOD(score, 12),  QSA_METHOD(select, 10),  QSA_METHOD(sparse_attn, 17),
+                         QSA_METHOD(tree_attn, 16), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

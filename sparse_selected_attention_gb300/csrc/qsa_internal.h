@@ -143,6 +143,12 @@ cudaError_t launch_paged_gather(const qsa_paged_gather_args &a, cudaStream_t s);
 cudaError_t launch_paged_attn(const qsa_paged_attn_args &a, cudaStream_t s);
 cudaError_t launch_page_update(const qsa_page_update_args &a, cudaStream_t s);
 cudaError_t launch_page_compact(const qsa_page_compact_args &a, cudaStream_t s);
+cudaError_t launch_page_bounds(const qsa_page_bounds_args &a, cudaStream_t s);
+cudaError_t launch_page_score(const qsa_page_score_args &a, cudaStream_t s);
+cudaError_t launch_page_select(const qsa_page_select_args &a, cudaStream_t s);
+cudaError_t launch_paged_sparse_attn(const qsa_paged_sparse_attn_args &a, cudaStream_t s);
+cudaError_t launch_paged_tree_attn(const qsa_paged_tree_attn_args &a, cudaStream_t s);
+size_t paged_sparse_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 size_t paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 size_t pages_workspace_bytes(int n_rows, int n_pages);
 
@@ -157,6 +163,11 @@ cudaError_t take_check_word_paged_prep(unsigned int *out);
 cudaError_t take_check_word_paged_attn(unsigned int *out);
 cudaError_t take_check_word_paged_group(unsigned int *out);
 cudaError_t take_check_word_pages(unsigned int *out);
+cudaError_t take_check_word_page_bounds(unsigned int *out);
+cudaError_t take_check_word_page_score(unsigned int *out);
+cudaError_t take_check_word_page_select(unsigned int *out);
+cudaError_t take_check_word_paged_sparse(unsigned int *out);
+cudaError_t take_check_word_paged_tree(unsigned int *out);
 #endif
 
 }  // namespace qsa

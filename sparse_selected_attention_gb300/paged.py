@@ -58,11 +58,13 @@ def _formats():
     """struct formats of the argument structs, from their ctypes mirrors."""
     letter = {_abi._c_int: "i", _abi._c_float: "f", _abi._vp: "P", _abi.ctypes.c_int64: "q", _abi.ctypes.c_size_t: "N"}
     return {cls: struct.Struct("@" + "".join(letter[t] for _, t in cls._fields_))
-            for cls in (_abi.PagedPrepArgs, _abi.PagedGatherArgs, _abi.PagedAttnArgs, _abi.PageUpdateArgs, _abi.PageCompactArgs)}
+            for cls in (_abi.PagedPrepArgs, _abi.PagedGatherArgs, _abi.PagedAttnArgs, _abi.PageUpdateArgs, _abi.PageCompactArgs,
+                        _abi.PageBoundsArgs, _abi.PageScoreArgs, _abi.PageSelectArgs, _abi.PagedSparseAttnArgs,
+                        _abi.PagedTreeAttnArgs)}
 
 
 _FORMAT = _formats()
-_PREP, _GATHER, _ATTN, _UPDATE, _COMPACT = (_FORMAT[c].pack for c in _FORMAT)
+_PREP, _GATHER, _ATTN, _UPDATE, _COMPACT, _BOUNDS, _SCORE, _SELECT, _SPARSE, _TREE = (_FORMAT[c].pack for c in _FORMAT)
 
 
 def _bad(t, name, dtype, shape, dev):
@@ -351,3 +353,180 @@ def _checked_compact(page_table, seq_lens, kq, vq, ksc, vsc, page_table_out, ref
         _in(seq_lens, "seq_lens", I32, (rows,), dev), *kv, _in(page_table_out, "page_table_out", I32, table, dev),
         _in(refs, "refs", I32, (pages,), dev), _in(page_map, "page_map", I32, (pages,), dev),
         _in(n_live, "n_live", I32, (1,), dev), ws, ws_bytes, _err(err, dev)), dev, stream)
+
+
+def qsa_page_bounds(page_table, seq_lens, kq, ksc, hi_q, lo_q, hi_sc, lo_sc, n_new=None, err=None, stream=None):
+    """Bounds of the keys in each page that rows' new tokens are in: hi_q, lo_q
+    [pages, Hkv, D] int8 and hi_sc, lo_sc [pages, Hkv, 4] fp16 <- the largest and
+    smallest key per dim of the page's filled cells, rounded outwards, by kq
+    [pages, page, Hkv, D] and ksc [pages, page, Hkv, 4] (one layer of the pool).
+    seq_lens [R] int32 are the rows' lengths with the new tokens, n_new [R] int32
+    how many of them are new (None: all).  A cache of one cell per page, which
+    qsa_paged_gather reads back."""
+    status = _native.bounds(_abi.entry("qsa_page_bounds"), page_table, seq_lens, kq, ksc, hi_q, lo_q, hi_sc, lo_sc, n_new, err,
+                            stream)
+    if status:
+        _again(status, _checked_bounds, page_table, seq_lens, kq, ksc, hi_q, lo_q, hi_sc, lo_sc, n_new, err, stream)
+
+
+def _page_bounds(hi_q, lo_q, hi_sc, lo_sc, shape, dev):
+    scales = (*shape[:-1], 4)
+    return (_in(hi_q, "hi_q", I8, shape, dev), _in(lo_q, "lo_q", I8, shape, dev), _in(hi_sc, "hi_sc", F16, scales, dev),
+            _in(lo_sc, "lo_sc", F16, scales, dev))
+
+
+def _checked_bounds(page_table, seq_lens, kq, ksc, hi_q, lo_q, hi_sc, lo_sc, n_new, err, stream):
+    dev = kq.get_device()
+    if dev < 0:
+        raise ValueError("kq must be a CUDA tensor (the QSA path runs only on the GPU)")
+    if kq.dim() != 4 or page_table.dim() != 2:
+        raise ValueError(f"kq must be [pages, page, Hkv, D] and page_table [R, max_pages], got {tuple(kq.shape)}, {tuple(page_table.shape)}")
+    pages, page, hkv, d = kq.shape
+    rows, wide = table = page_table.shape
+    _call("qsa_page_bounds", _BOUNDS(
+        rows, wide, pages, page, hkv, d, d // 4, _in(page_table, "page_table", I32, table, dev),
+        _in(seq_lens, "seq_lens", I32, (rows,), dev), _opt(n_new, "n_new", I32, (rows,), dev), _in(kq, "kq", I8, kq.shape, dev),
+        _in(ksc, "ksc", F16, (pages, page, hkv, 4), dev), *_page_bounds(hi_q, lo_q, hi_sc, lo_sc, (pages, hkv, d), dev),
+        _err(err, dev)), dev, stream)
+
+
+def qsa_page_score(q, hi_q, lo_q, hi_sc, lo_sc, page_table, seq_lens, scores, page_size, rows=None, err=None, stream=None):
+    """scores [T, Hkv, ld] fp32 (ld >= the table's columns): element [t, h, j] <-
+    the most that the products of q [T, Hq, D]'s query heads of KV head h (fp16 or
+    bf16) with a key of page j can add up to, by the bounds of qsa_page_bounds,
+    for each page j of the sequence rows[t] (t itself when rows is None) with
+    seq_lens[t] cells; the others are left untouched."""
+    status = _native.score(_abi.entry("qsa_page_score"), q, hi_q, lo_q, hi_sc, lo_sc, page_table, seq_lens, scores, page_size, rows,
+                           err, stream)
+    if status:
+        _again(status, _checked_score, q, hi_q, lo_q, hi_sc, lo_sc, page_table, seq_lens, scores, page_size, rows, err, stream)
+
+
+def _tokens(q, page_table):
+    """T, H, D, device and type of the queries of a call on a paged cache."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [T, Hq, D], got {tuple(q.shape)}")
+    dev, dtype = q.get_device(), q.dtype
+    if dev < 0:
+        raise ValueError("q must be a CUDA tensor (the QSA path runs only on the GPU)")
+    if dtype is not F16 and dtype is not BF16:
+        raise ValueError(f"q must be float16 or bfloat16, got {dtype}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [R, max_pages]")
+    return *q.shape, dev, dtype
+
+
+def _checked_score(q, hi_q, lo_q, hi_sc, lo_sc, page_table, seq_lens, scores, page_size, rows, err, stream):
+    T, H, D, dev, dtype = _tokens(q, page_table)
+    if hi_q.dim() != 3 or hi_q.shape[2] != D:
+        raise ValueError(f"hi_q must be [pages, Hkv, {D}], got {tuple(hi_q.shape)}")
+    pages, hkv, _ = hi_q.shape
+    if scores.dim() != 3:
+        raise ValueError(f"scores must be [{T}, {hkv}, ld], got {tuple(scores.shape)}")
+    table, ld = page_table.shape, scores.shape[2]
+    _call("qsa_page_score", _SCORE(
+        T, H, hkv, D, D // 4, page_size, pages, table[0], table[1], _CODE[dtype], _in(q, "q", dtype, (T, H, D), dev),
+        *_page_bounds(hi_q, lo_q, hi_sc, lo_sc, hi_q.shape, dev), _in(page_table, "page_table", I32, table, dev),
+        _in(seq_lens, "seq_lens", I32, (T,), dev), _opt(rows, "rows", I32, (T,), dev), _in(scores, "scores", F32, (T, hkv, ld), dev), ld,
+        _err(err, dev)), dev, stream)
+
+
+def qsa_page_select(scores, seq_lens, pages, counts, page_size, budget, sink=1, local=1, err=None, stream=None):
+    """pages [T, Hkv, W] int32 <- the first `sink` pages of a sequence of
+    seq_lens[t] cells, its last `local` and the best of the others by scores [T,
+    Hkv, ld] fp32 (ties to the lower page), `budget` in all, ascending, -1 padded;
+    counts [T, Hkv] int32 <- how many."""
+    status = _native.select(_abi.entry("qsa_page_select"), scores, seq_lens, pages, counts, page_size, budget, sink, local, err,
+                            stream)
+    if status:
+        _again(status, _checked_select, scores, seq_lens, pages, counts, page_size, budget, sink, local, err, stream)
+
+
+def _checked_select(scores, seq_lens, pages, counts, page_size, budget, sink, local, err, stream):
+    dev = scores.get_device()
+    if dev < 0:
+        raise ValueError("scores must be a CUDA tensor (the QSA path runs only on the GPU)")
+    if scores.dim() != 3 or pages.dim() != 3:
+        raise ValueError(f"scores must be [T, Hkv, ld] and pages [T, Hkv, W], got {tuple(scores.shape)}, {tuple(pages.shape)}")
+    T, hkv, ld = scores.shape
+    w = pages.shape[2]
+    _call("qsa_page_select", _SELECT(
+        T, hkv, page_size, w, budget, sink, local, _in(scores, "scores", F32, (T, hkv, ld), dev), ld,
+        _in(seq_lens, "seq_lens", I32, (T,), dev), _in(pages, "pages", I32, (T, hkv, w), dev), _in(counts, "counts", I32, (T, hkv), dev),
+        _err(err, dev)), dev, stream)
+
+
+def qsa_paged_sparse_attn_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int = 128) -> int:
+    return int(_abi.lib().qsa_paged_sparse_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim))
+
+
+def qsa_paged_sparse_attn(q, kq, vq, ksc, vsc, page_table, seq_lens, pages, counts, out, workspace, rows=None, softmax_scale=None,
+                          gate=None, lse=None, err=None, stream=None):
+    """qsa_paged_attn over listed pages: KV head h of row t attends to the cells
+    below seq_lens[t] of the first counts[t, h] pages of pages [T, Hkv, W] int32
+    (page numbers of the sequence, -1 is padding), as qsa_page_select writes them.
+    workspace is a uint8 CUDA tensor of at least
+    qsa_paged_sparse_attn_workspace_bytes(Hq, Hkv, D) bytes."""
+    status = _native.sparse_attn(_abi.entry("qsa_paged_sparse_attn"), q, kq, vq, ksc, vsc, page_table, seq_lens, pages, counts, out,
+                                 workspace, rows, softmax_scale, gate, lse, err, stream)
+    if status:
+        _again(status, _checked_sparse, q, kq, vq, ksc, vsc, page_table, seq_lens, pages, counts, out, workspace, rows, softmax_scale,
+               gate, lse, err, stream)
+
+
+def _attn_parts(T, H, D, dev, dtype, q, kq, vq, ksc, vsc, page_table, out, gate, lse, rows):
+    """What the two calls below check alike: the sizes, and addresses by name."""
+    if kq.dim() != 4 or kq.shape[3] != D:
+        raise ValueError(f"kq must be [pages, page, Hkv, {D}], got {tuple(kq.shape)}")
+    pages, page, hkv, _ = kq.shape
+    table, heads = page_table.shape, (T, H, D)
+    kv = _cache(kq, vq, ksc, vsc, dev)
+    return ((T, H, hkv, D, D // 4, page, pages, table[0], table[1]), (_in(q, "q", dtype, heads, dev), *kv,
+            _in(page_table, "page_table", I32, table, dev)), _opt(rows, "rows", I32, (T,), dev),
+            (_opt(gate, "gate", F32, heads, dev), _in(out, "out", dtype, heads, dev), _opt(lse, "lse", F32, (T, H), dev)))
+
+
+def _checked_sparse(q, kq, vq, ksc, vsc, page_table, seq_lens, pages, counts, out, workspace, rows, softmax_scale, gate, lse, err,
+                    stream):
+    T, H, D, dev, dtype = _tokens(q, page_table)
+    sizes, first, rows, last = _attn_parts(T, H, D, dev, dtype, q, kq, vq, ksc, vsc, page_table, out, gate, lse, rows)
+    hkv = sizes[2]
+    if pages.dim() != 3:
+        raise ValueError(f"pages must be [{T}, {hkv}, W], got {tuple(pages.shape)}")
+    w = pages.shape[2]
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("qsa_paged_sparse_attn", _SPARSE(
+        *sizes, w, _CODE[dtype], *first, _in(seq_lens, "seq_lens", I32, (T,), dev), rows, _in(pages, "pages", I32, (T, hkv, w), dev),
+        _in(counts, "counts", I32, (T, hkv), dev), D ** -0.5 if softmax_scale is None else softmax_scale, *last, ws, ws_bytes,
+        _err(err, dev)), dev, stream)
+
+
+def qsa_paged_tree_attn_workspace_bytes(n_q_heads: int, n_kv_heads: int, head_dim: int = 128) -> int:
+    return int(_abi.lib().qsa_paged_tree_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim))
+
+
+def qsa_paged_tree_attn(q, kq, vq, ksc, vsc, page_table, prefix_lens, mask, out, workspace, rows=None, softmax_scale=None, gate=None,
+                        lse=None, err=None, stream=None):
+    """qsa_paged_attn for drafted tokens that branch: row t attends to cells 0 ..
+    prefix_lens[t]-1 of its sequence and to cell prefix_lens[t] + b for each bit b
+    of mask [T, words] int32 (bit b % 32 of word b / 32; up to QSA_TREE_MAX_WORDS
+    words): of a tree whose node i is cached in cell prefix + i, the node itself
+    and those that lead to it.  workspace is a uint8 CUDA tensor of at least
+    qsa_paged_tree_attn_workspace_bytes(Hq, Hkv, D) bytes."""
+    status = _native.tree_attn(_abi.entry("qsa_paged_tree_attn"), q, kq, vq, ksc, vsc, page_table, prefix_lens, mask, out, workspace,
+                               rows, softmax_scale, gate, lse, err, stream)
+    if status:
+        _again(status, _checked_tree, q, kq, vq, ksc, vsc, page_table, prefix_lens, mask, out, workspace, rows, softmax_scale, gate, lse,
+               err, stream)
+
+
+def _checked_tree(q, kq, vq, ksc, vsc, page_table, prefix_lens, mask, out, workspace, rows, softmax_scale, gate, lse, err, stream):
+    T, H, D, dev, dtype = _tokens(q, page_table)
+    sizes, first, rows, last = _attn_parts(T, H, D, dev, dtype, q, kq, vq, ksc, vsc, page_table, out, gate, lse, rows)
+    if mask.dim() != 2:
+        raise ValueError(f"mask must be [{T}, words], got {tuple(mask.shape)}")
+    words = mask.shape[1]
+    ws, ws_bytes = _scratch(workspace, dev)
+    _call("qsa_paged_tree_attn", _TREE(
+        *sizes, words, _CODE[dtype], *first, _in(prefix_lens, "prefix_lens", I32, (T,), dev), rows, _in(mask, "mask", I32, (T, words), dev),
+        D ** -0.5 if softmax_scale is None else softmax_scale, *last, ws, ws_bytes, _err(err, dev)), dev, stream)

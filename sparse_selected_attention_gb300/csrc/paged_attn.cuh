@@ -365,6 +365,5 @@ size_t paged_group_workspace_bytes(int head_dim);
 // paged_group.cu: the groups, where a.rows is given.  ws as Work of GROUP_ROWS
 // rows; `ctas` receives how many leave partials there, to be joined.
 cudaError_t launch_paged_group(const qsa_paged_attn_args &a, void *ws, int &ctas, cudaStream_t s);
-cudaError_t launch_paged_group(const TreeArgs &a, void *ws, int &ctas, cudaStream_t s);
 
 }  // namespace qsa

@@ -1,5 +1,5 @@
-// Rows that read one sequence together: the consecutive tokens of a draft window, of
-// a chunk or of a tree of drafts, each with its own length or bits.
+// qsa_paged_attn, rows that read one sequence together: the consecutive tokens
+// of a draft window or of a chunk, each with its own length.
 //
 // Their heads, up to 128, are the M side of tcgen05 products over one pass of
 // the cache, so a cell's codes are read and converted once for all of them.
@@ -76,7 +76,7 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0u;
 }
 // The group that starts at a row t: its rows (0: none starts), and the shortest
-// and longest length (of a tree: the fewest cells that a row sees for certain).
+// and longest length.
 struct Group {
     int rows, least, most, trow;
     __device__ __forceinline__ int tiles() const { return rows ? max((most + N - 1) / N, 1) : 0; }
@@ -113,8 +113,7 @@ __device__ __forceinline__ __half2 scaled(uint2 sc, int i, int e) {
     return __float2half2_rn(f * exp2i(e));
 }
 // Looked up by a warp.
-template <class A>
-__device__ __forceinline__ Group group_at(const A &a, int t, int block, bool &bad) {
+__device__ __forceinline__ Group group_at(const qsa_paged_attn_args &a, int t, int block, bool &bad) {
     const int lane = threadIdx.x & 31, row = __ldg(a.rows + t);
     Group g{0, 0x7fffffff, 0, 0};
     if (group_start(a.rows, t, block) != t) return g;
@@ -122,13 +121,13 @@ __device__ __forceinline__ Group group_at(const A &a, int t, int block, bool &ba
     int n = 0, least = 0x7fffffff, most = 0;
     for (bool more = true; more && t + n < end;) {
         const int u = t + n + lane;
-        int trow, len = 0, sure = 0;
+        int trow, len = 0;
         const bool same = u < end && __ldg(a.rows + u) == row;
-        if (u < end) len = row_len(a, u, 0, trow, sure, bad);
+        if (u < end) len = row_cells(a, u, trow, bad);
         const unsigned m = __ballot_sync(0xffffffffu, same);
         const int k = m == 0xffffffffu ? 32 : __ffs(~m) - 1;  // rows that go on with the run
         if (lane < k) {
-            least = min(least, sure);
+            least = min(least, len);
             most = max(most, len);
         }
         n += k;
@@ -141,9 +140,9 @@ __device__ __forceinline__ Group group_at(const A &a, int t, int block, bool &ba
     return g;
 }
 
-template <int S, class A>
+template <int S>
 __global__ void __launch_bounds__(THREADS, 1)
-    paged_group_kernel(const A a, void *ws, int block) {
+    paged_group_kernel(const qsa_paged_attn_args a, void *ws, int block) {
     using G = GroupShape<S>;
     constexpr int D = G::D;
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -194,10 +193,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // Few rows: each warp works it out for itself, a lane per row (2 us
         // less than by the block).
         const bool in = lane < a.n_tokens;
-        int row = -1, len = 0, sure = 0, trow = 0;
+        int row = -1, len = 0, trow = 0;
         if (in) {
             row = __ldg(a.rows + lane);
-            len = row_len(a, lane, 0, trow, sure, bad);
+            len = row_cells(a, lane, trow, bad);
         }
         const int prev = __shfl_up_sync(0xffffffffu, row, 1);
         const unsigned upto = 0xffffffffu >> (31 - lane), runs = __ballot_sync(0xffffffffu, in && (lane == 0 || prev != row));
@@ -205,7 +204,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool starts = in && ((lane - run) & (block - 1)) == 0;
         const unsigned groups = __ballot_sync(0xffffffffu, starts), after = groups & ~upto;
         const int id = __popc(groups & upto);
-        Group g{(after ? __ffs(after) - 1 : a.n_tokens) - lane, sure, len, trow};
+        Group g{(after ? __ffs(after) - 1 : a.n_tokens) - lane, len, len, trow};
         struct {
             long long tiles, alone, together;
         } v{0, in ? units_of<S>(len) : 0, 0};
@@ -243,14 +242,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         // time, and the thread of a row in which a group starts adds it up there.
         constexpr int CHUNK = 512;  // a multiple of any block
         static_assert(CHUNK <= THREADS && CHUNK % M == 0, "a thread per row");
-        int *srow = reinterpret_cast<int *>(sh.k), *slen = srow + CHUNK, *ssure = slen + CHUNK;
+        int *srow = reinterpret_cast<int *>(sh.k), *slen = srow + CHUNK;
         auto group_from = [&](int base) -> Group {  // that starts in row base + tid
             const int t = base + tid;
             __syncthreads();
             if (tid < CHUNK && t < a.n_tokens) {
                 int trow;
                 srow[tid] = __ldg(a.rows + t);
-                slen[tid] = row_len(a, t, 0, trow, ssure[tid], bad);
+                slen[tid] = row_cells(a, t, trow, bad);
             }
             __syncthreads();
             Group g{0, 0x7fffffff, 0, 0};
@@ -262,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int end = min(group_end(a, t, block) - base, CHUNK);
             u = tid;
             for (; u < end && srow[u] == row; ++u) {
-                g.least = min(g.least, ssure[u]);
+                g.least = min(g.least, slen[u]);
                 g.most = max(g.most, slen[u]);
             }
             g.rows = u - tid;
@@ -554,9 +553,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int m = tid & (M - 1), half = tid / M, j0 = half * NH;
             const bool mine = m < rows;
             const uint32_t lane_base = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-            int len = 0, sure = 0, tr;
-            const int token = t + (int)((uint32_t)m * per_inv >> 16);  // if it is mine
-            if (mine) len = row_len(a, token, 0, tr, sure, bad);
+            int len = 0, tr;
+            if (mine) len = row_cells(a, t + (int)((uint32_t)m * per_inv >> 16), tr, bad);
             // Of the two warps that share their head rows.  Both come here once a
             // tile whatever they waited for, and go on or stop together.
             auto both = [&](bool good) {
@@ -637,19 +635,13 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int w = 0; w < CONVERTERS / 32; ++w)
                         for (uint32_t bits = sh.poison[k % 3][w]; bits; bits &= bits - 1) {
                             const int b = __ffs(bits) - 1;
-                            const int c = i * N + factor_cell(w, b);
-                            bool in = c < len;
-                            if constexpr (TREE<A>) in = in && (tree_bits(a, token, c, sure) & 1u);
-                            if (in) poison |= 1u << (b & 3);
+                            if (i * N + factor_cell(w, b) < len) poison |= 1u << (b & 3);
                         }
                 }
-                if (i * N > least - N) {  // some row ends in this tile, or sees by its bits
-                    const int c0 = i * N + j0;
-                    uint32_t bits = 0xffffffffu;
-                    if constexpr (TREE<A>) bits = c0 < len ? tree_bits(a, token, c0, sure) : 0u;
+                if (i * N > least - N) {  // some row ends in this tile
 #pragma unroll
                     for (int j = 0; j < NH; ++j)
-                        if (c0 + j >= len || (TREE<A> && !(bits >> j & 1u))) y[j] = -CUDART_INF_F;
+                        if (i * N + j0 + j >= len) y[j] = -CUDART_INF_F;
                 }
                 float top = -CUDART_INF_F;
 #pragma unroll
@@ -811,12 +803,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
-template <int S, class A>
-cudaError_t launch(const A &a, void *ws, int &ctas, cudaStream_t s) {
+template <int S>
+cudaError_t launch(const qsa_paged_attn_args &a, void *ws, int &ctas, cudaStream_t s) {
     const int per = a.n_q_heads / a.n_kv_heads, smem = (int)sizeof(GroupSmem<S>);
     ctas = (MAX_GROUP_PARTS / a.n_kv_heads > 1 ? MAX_GROUP_PARTS / a.n_kv_heads : 1) * a.n_kv_heads;
-    const cudaError_t e = cudaFuncSetAttribute(paged_group_kernel<S, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e != cudaSuccess ? e : launch_dependent(paged_group_kernel<S, A>, dim3(ctas), dim3(THREADS), smem, s, a, ws, group_block(per));
+    const cudaError_t e = cudaFuncSetAttribute(paged_group_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : launch_dependent(paged_group_kernel<S>, dim3(ctas), dim3(THREADS), smem, s, a, ws, group_block(per));
 }
 
 }  // namespace
@@ -824,10 +816,6 @@ cudaError_t launch(const A &a, void *ws, int &ctas, cudaStream_t s) {
 size_t paged_group_workspace_bytes(int head_dim) { return Work::bytes(MAX_GROUP_PARTS, M, head_dim); }
 
 cudaError_t launch_paged_group(const qsa_paged_attn_args &a, void *ws, int &ctas, cudaStream_t s) {
-    return a.head_dim == 128 ? launch<1>(a, ws, ctas, s) : launch<2>(a, ws, ctas, s);
-}
-
-cudaError_t launch_paged_group(const TreeArgs &a, void *ws, int &ctas, cudaStream_t s) {
     return a.head_dim == 128 ? launch<1>(a, ws, ctas, s) : launch<2>(a, ws, ctas, s);
 }
 

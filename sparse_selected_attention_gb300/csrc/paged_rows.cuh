@@ -822,7 +822,7 @@ using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, vo
                               const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-EncodeFn encode_fn() {
+inline EncodeFn encode_fn() {
     static const EncodeFn fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -834,54 +834,23 @@ EncodeFn encode_fn() {
     return fn;
 }
 
-// Codes [cells, heads, D] in boxes of a unit's cells (or a page's, if fewer) x
-// one head x 128 dims.
-template <int S>
-cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t *codes) {
+// Codes [cells, heads, D] in boxes of `cells` cells x one head x 128 dims.
+inline cudaError_t encode_boxes(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t *codes, int cells) {
     const EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads, (cuuint64_t)a.n_pages * a.page_size};
     const cuuint64_t strides[2] = {(cuuint64_t)a.head_dim, (cuuint64_t)a.n_kv_heads * a.head_dim};
-    const cuuint32_t box[3] = {128, 1, (cuuint32_t)std::min(a.page_size, Shape<S>::UNIT)}, ones[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {128, 1, (cuuint32_t)cells}, ones[3] = {1, 1, 1};
     const CUresult e = fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<int8_t *>(codes), dims, strides, box, ones,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return e == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Boxes of a unit's cells, or a page's, if fewer.
 template <int S>
-cudaError_t launch(const qsa_paged_attn_args &a, cudaStream_t s) {
-    constexpr int UNIT = Shape<S>::UNIT;
-    CUtensorMap kmap, vmap;
-    cudaError_t e = encode<S>(kmap, a, a.kq);
-    if (e == cudaSuccess) e = encode<S>(vmap, a, a.vq);
-    if (e != cudaSuccess) return e;
-    // A share per resident CTA.  Whole rows, and no join, where the table
-    // cannot hold longer ones than WHOLE units, or where there are as many KV
-    // heads as CTAs (then there may also be more CTAs than the workspace has
-    // places for).
-    const long long units = ((long long)a.max_pages * a.page_size + UNIT - 1) / UNIT;
-    const int resident = std::max(MAX_CTAS / a.n_kv_heads, 1);
-    const bool whole = units <= WHOLE || resident == 1;
-    const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
-    const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, block = !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
-    if (whole && units * UNIT <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
-        const int small = (int)std::min<long long>(a.n_tokens, std::max(152 * SMALL_PER_SM / a.n_kv_heads, 1));
-        e = cudaFuncSetAttribute(paged_attn_kernel<S, 1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, 1>));
-        return e != cudaSuccess ? e
-                                : launch_dependent(paged_attn_kernel<S, 1, true>, dim3(small * a.n_kv_heads), dim3(32), sizeof(Smem<S, 1>), s, a,
-                                                   kmap, vmap, 0);
-    }
-    const auto kernel = whole ? paged_attn_kernel<S, NW, true> : paged_attn_kernel<S, NW, false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, NW>));
-    if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S, NW>), s, a, kmap, vmap, block);
-    if (e != cudaSuccess || whole) return e;
-    const Joined one{a.workspace, MAX_CTAS, per, grid};
-    Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};
-    if (block && (e = launch_paged_group(a, two.ws, two.ctas, s)) != cudaSuccess) return e;
-    if (!block) two.rows = 0;
-    return launch_join<S>(a, one, two, s);
+cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t *codes) {
+    return encode_boxes(map, a, codes, std::min(a.page_size, Shape<S>::UNIT));
 }
 
 // A call.  cells: the most that a row can go through.
@@ -901,7 +870,7 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     const bool whole = units <= WHOLE || resident == 1;
     const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, block = !LISTED<A> && !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
+    const int per = a.n_q_heads / a.n_kv_heads, block = !LISTED<A> && !TREE<A> && !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
     if (whole && units * UNIT <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
         const int small = (int)std::min<long long>(a.n_tokens, std::max(152 * SMALL_PER_SM / a.n_kv_heads, 1));
         e = cudaFuncSetAttribute(paged_attn_kernel<S, 1, true, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, 1>));
@@ -915,7 +884,7 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     if (e != cudaSuccess || whole) return e;
     const Joined one{a.workspace, MAX_CTAS, per, grid};
     Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};
-    if constexpr (!LISTED<A>)
+    if constexpr (!LISTED<A> && !TREE<A>)
         if (block && (e = launch_paged_group(a, two.ws, two.ctas, s)) != cudaSuccess) return e;
     if (!block) two.rows = 0;
     return launch_join<S>(a, one, two, s);

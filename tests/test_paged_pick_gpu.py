@@ -17,7 +17,7 @@ import torch
 
 import sparse_selected_attention_gb300 as qsa
 from oracle import paged_oracle as po
-from tests.test_paged_gpu import BF16, F16, HALF, TINY, dev, err_word, host, i32, make_pool, shuffled_table, taken_together
+from tests.test_paged_gpu import BF16, F16, HALF, TINY, dev, err_word, host, i32, make_pool, shuffled_table
 from tests.test_paged_pick_cpu import random_tree
 
 pytestmark = pytest.mark.gpu
@@ -446,13 +446,9 @@ def trees(rng, prefix, nodes, page, hkv, d, seed, extra=2):
     return pool, table, [prefix[s] for s in rows], mask, rows
 
 
-def spans(prefix, mask):
-    """Lengths up to the last cell that a row sees."""
-    out = []
-    for p, m in zip(prefix, mask):
-        bits = [b for b in range(32 * len(m)) if int(m[b // 32]) >> (b % 32) & 1]
-        out.append(p + (bits[-1] + 1 if bits else 0))
-    return out
+def read_together(table, page, d, rows):
+    """Whether the call reads the tokens of one sequence together: sixteen units of 32 (of 256 dims 16) cells are few."""
+    return rows is not None and len(rows) > 1 and table.shape[1] * page > 16 * (32 if d == 128 else 16)
 
 
 @pytest.mark.parametrize("otype", [F16, BF16])
@@ -472,7 +468,7 @@ def test_tree_shapes(cuda_device, d, hq, hkv, page, otype):
 def test_trees_taken_together(cuda_device, d, hq, hkv, page, prefix, nodes, otype):
     rng = np.random.default_rng(hq)
     pool, table, pre, mask, rows = trees(rng, prefix, nodes, page, hkv, d, 32)
-    assert taken_together(rows, spans(pre, mask), hq, hkv, d)
+    assert read_together(table, page, d, rows)
     gate = rng.standard_normal((len(rows), hq, d)).astype(np.float32) * 2
     q = rng.standard_normal((len(rows), hq, d)) * 2
     check_tree(q, pool, table, pre, mask, rows=rows, otype=otype, gate=gate)
@@ -483,10 +479,10 @@ def test_tree_any_masks(cuda_device, together):
     """Bits at random, none, all; rows that see nothing; prefixes of their own."""
     rng = np.random.default_rng(33)
     n, hkv = (96, 8) if together else (20, 2)
-    table, pages = shuffled_table([1100, 200], 32, 3, rng)
+    table, pages = shuffled_table([1100, 200] if together else [500, 200], 32, 3, rng)
     pool = make_pool(pages, 32, hkv, 128, seed=33)
     rows = [0] * (n - 4) + [1] * 4
-    prefix = [int(v) for v in rng.integers(600, 900, n - 4)] + [0, 0, 100, 7]
+    prefix = [int(v) for v in rng.integers(*((600, 900) if together else (0, 300)), n - 4)] + [0, 0, 100, 7]
     mask = rng.integers(-2 ** 31, 2 ** 31, (n, 6), dtype=np.int64).astype(np.int32)
     mask[3], mask[4], mask[5, 1:], mask[6, :5] = 0, -1, 0, 0
     mask[n - 4:] = 0
@@ -495,7 +491,7 @@ def test_tree_any_masks(cuda_device, together):
     prefix[7], mask[7] = 0, 0
     prefix[8], mask[8] = 0, 0
     mask[8, 0] = 1
-    assert taken_together(rows, spans(prefix, mask), 16 if together else 4, hkv, 128) == together
+    assert read_together(table, 32, 128, rows) == together
     out, lse = check_tree(rng.standard_normal((n, (16 if together else 4), 128)), pool, table, prefix, mask, rows=rows)
     assert not out[7].any() and torch.isneginf(lse[7]).all() and not out[n - 4].any()
 
@@ -530,7 +526,7 @@ def test_nan_and_inf_scales_reach_only_rows_that_see_them(cuda_device, together)
     hkv, d, hq = (8, 128, 16) if together else (2, 128, 8)
     nodes, pre = (64, 700) if together else (9, 300)
     pool, table, prefix, mask, rows = trees(rng, [pre], [nodes], 32, hkv, d, 35)
-    assert taken_together(rows, spans(prefix, mask), hq, hkv, d) == together
+    assert read_together(table, 32, d, rows) == together
     sees = np.array([[int(m[b // 32]) >> (b % 32) & 1 for b in range(nodes)] for m in mask], bool)
     q = dev(rng.standard_normal((nodes, hq, d)).astype(np.float16))
     ws = torch.empty(qsa.qsa_paged_tree_attn_workspace_bytes(hq, hkv, d), dtype=torch.uint8, device="cuda")

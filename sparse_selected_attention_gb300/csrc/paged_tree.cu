@@ -41,7 +41,8 @@ constexpr int STAGES = 2;  // tiles of codes on their way
 constexpr int INFOS = 4;   // tiles of factors
 constexpr int SPREAD = 6, K_SPREAD = 16;
 constexpr int LIFT = 6;    // weights are 2^LIFT times those of the reference maximum
-constexpr int CHUNK = 512; // tokens that are looked up at once; groups end where one ends
+constexpr int CHUNK = 1024;  // tokens that are looked up at once, one a thread; groups end where one ends
+static_assert(CHUNK == THREADS, "a thread per token");
 
 template <int S>
 struct TreeShape {
@@ -78,7 +79,7 @@ template <int S>
 struct TreeSmem {
     using G = TreeShape<S>;
     static constexpr int N = G::N;
-    uint8_t k[2][2][S][N * 128];         // halves of the dims, high and low part; from here on also the values at the end of a segment, fp32 [M][D]
+    uint8_t k[2][2][S][N * 128];         // halves of the dims, high and low part
     uint8_t v[2][G::BLOCKS][N * 128];
     uint8_t codes[2][STAGES][S][N * 128];  // K's and V's as they come, by 128 dims
     Info<N> info[INFOS];
@@ -90,7 +91,8 @@ struct TreeSmem {
     uint64_t k_full[2], k_empty[2], v_full[2], s_full[2], p_full[2], pv_full[2], ref_full[2];
     uint64_t q_full, drain;
     long long scan[WARPS];
-    int starts[CHUNK / 32];
+    unsigned starts[CHUNK / 32];
+    TreeGroup<S> next;
     long long before;
     int t;
     TreeGroup<S> grp;
@@ -123,6 +125,17 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[16]
 // The rest of a wait whose first look did not see the phase completed; in one
 // place, since every line of the roles' loops counts in the instruction cache.
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int *abort) { return mbar_wait_or_abort(bar, parity, abort); }
+// Two values of the output, gated, as they are stored.
+template <bool FINE>
+__device__ __forceinline__ uint32_t tree_value(const TreeArgs &a, size_t at, float2 y) {
+    if (a.gate) {
+        const float2 g = __ldg(reinterpret_cast<const float2 *>(a.gate + at));
+        y = make_float2(gated(y.x, g.x), gated(y.y, g.y));
+    }
+    if constexpr (FINE) return h2u(__floats2half2_rn(y.x, y.y));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(y.x, y.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
 // The group that starts at t, looked up by a warp.
@@ -201,88 +214,85 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool bad = false;
 
     // The groups' tiles, and the group in which this CTA's share of them starts.
+    // Loops, as all of this kernel that runs once or rarely: an instruction's first
+    // fetch costs more than its execution (unrolled, this took 9 us of 63 tokens').
     int share = 0, left = 0, t = 0;
     TreeGroup<S> grp;
     {
         int *srow = reinterpret_cast<int *>(sh.k), *most = srow + CHUNK, *least = most + CHUNK, *size = least + CHUNK;
-        auto groups_from = [&](int base) -> TreeGroup<S> {  // the one that starts in token base + tid
-            const int u = base + tid;
-            const bool in = tid < CHUNK && u < a.n_tokens;
-            int row = 0, trow = 0, len = 0, sure = 0;
-            __syncthreads();
-            if (in) {
-                row = __ldg(a.rows + u);
-                len = row_len(a, u, 0, trow, sure, bad);
+        long long total = 0, x = 0, done = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {  // the tiles; then where the share starts
+#pragma unroll 1
+            for (int base = 0; base < a.n_tokens; base += CHUNK) {
+                if (pass && a.n_tokens <= CHUNK) break;  // found already
+                const int u = base + tid;
+                const bool in = u < a.n_tokens;
+                int row = 0, trow = 0, len = 0, sure = 0;
+                if (in) {
+                    row = __ldg(a.rows + u);
+                    len = row_len(a, u, 0, trow, sure, bad);
+                }
+                __syncthreads();  // of the chunk before
                 srow[tid] = row;
                 most[tid] = 0;
                 least[tid] = 0x7fffffff;
                 size[tid] = 0;
+                __syncthreads();
+                // Where the token's run of one sequence starts: in its warp, or before.
+                const unsigned starts = __ballot_sync(0xffffffffu, in && (tid == 0 || srow[tid - 1] != row));
+                if (lane == 0) sh.starts[warp] = starts;
+                __syncthreads();
+                unsigned mine = starts & (0xffffffffu >> (31 - lane));
+                int w = warp;
+                while (!mine && w > 0) mine = sh.starts[--w];
+                const int start = w * 32 + 31 - __clz(mine), lead = tid - (tid - start) % in_group;
+                if (in) {
+                    atomicMax(most + lead, len);
+                    atomicMin(least + lead, sure);
+                    atomicAdd(size + lead, 1);
+                }
+                __syncthreads();
+                const TreeGroup<S> g{in && lead == tid ? size[tid] : 0, least[tid], most[tid], trow};
+                const int tiles = g.tiles();
+                long long sum = tiles;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, sum, o);
+                    if (lane >= o) sum += v;
+                }
+                if (lane == 31) sh.scan[warp] = sum;
+                __syncthreads();
+                long long before = done + sum - tiles, all = sh.scan[lane];
+                if (lane >= warp) all = 0;  // of the warps before
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+                before += all;
+                const long long chunk = sh.scan[lane];
+                all = chunk;
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+                if (!pass) total += all;
+                done += all;
+                if (pass || a.n_tokens <= CHUNK) {
+                    if (!pass) {
+                        share = (int)max((total + ranges - 1) / ranges, (long long)S);
+                        x = (long long)share * range;
+                    }
+                    if (tiles && x >= before && x < before + tiles) {
+                        sh.t = u;
+                        sh.before = before;
+                        sh.grp = g;
+                    }
+                }
             }
-            __syncthreads();
-            // Where the token's run starts.
-            int start = in && (tid == 0 || srow[tid - 1] != row) ? tid : -1;
-            start = max(start, -1);
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, start, o);
-                if (lane >= o) start = max(start, v);
+            if (!pass) {
+                share = (int)max((total + ranges - 1) / ranges, (long long)S);
+                x = (long long)share * range;
+                done = 0;
             }
-            if (warp < CHUNK / 32 && lane == 31) sh.starts[warp] = start;
-            __syncthreads();
-            for (int w = min(warp, CHUNK / 32) - 1; w >= 0 && start < 0; --w) start = sh.starts[w];
-            const int lead = tid - (tid - start) % in_group;
-            if (in) {
-                atomicMax(most + lead, len);
-                atomicMin(least + lead, sure);
-                atomicAdd(size + lead, 1);
-            }
-            __syncthreads();
-            if (!in || lead != tid) return TreeGroup<S>{0, 0, 0, 0};
-            return TreeGroup<S>{size[tid], least[tid], most[tid], trow};
-        };
-        auto block_sum = [&](long long v, long long &before) -> long long {
-            long long sum = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += u;
-            }
-            __syncthreads();
-            if (lane == 31) sh.scan[warp] = sum;
-            __syncthreads();
-            long long total = 0;
-            before = sum - v;
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                if (w < warp) before += sh.scan[w];
-                total += sh.scan[w];
-            }
-            return total;
-        };
-        TreeGroup<S> g{0, 0, 0, 0};
-        long long total = 0, before = 0;
-        for (int base = 0; base < a.n_tokens; base += CHUNK) {
-            g = groups_from(base);
-            total += block_sum(g.tiles(), before);
         }
-        share = (int)max((total + ranges - 1) / ranges, (long long)S);
-        const long long x = (long long)share * range;
         left = (int)max(min((long long)share, total - x), 0ll);
-        long long done = 0;
-        for (int base = 0; left > 0 && base < a.n_tokens; base += CHUNK) {
-            long long sum = total;  // of one chunk, g and before are at hand
-            if (a.n_tokens > CHUNK) {
-                g = groups_from(base);
-                sum = block_sum(g.tiles(), before);
-            }
-            if (x >= done + before && x < done + before + g.tiles()) {
-                sh.t = base + tid;
-                sh.before = done + before;
-                sh.grp = g;
-            }
-            done += sum;
-            if (x < done) break;
-        }
     }
     fence_before();
     __syncthreads();
@@ -305,7 +315,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int tiles = grp.tiles(), i1 = min(tiles, i0 + left), n = i1 - i0, rows = grp.tokens * per;
         const bool whole = n == tiles;
         const size_t at = (size_t)blockIdx.x * 2 + (first && i0 > 0 ? 0 : 1);
-        float *values = reinterpret_cast<float *>(sh.k);
         auto head_row = [&](int m) -> size_t {  // of q: token t + m / per, head kvh per + m % per
             const int i = (int)((uint32_t)m * per_inv >> 16);  // m / per, m < 128
             return (size_t)(t + i) * a.n_q_heads + (size_t)kvh * per + (m - i * per);
@@ -343,6 +352,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
                 if (!good) break;
+            }
+            if (left > n) {  // the next group, for all
+                const TreeGroup<S> g = tree_group_at<S>(a, t + grp.tokens, in_group, bad);
+                if (lane == 0) sh.next = g;
             }
         } else if (warp >= SCALER) {
             // ---- factors: 32 cells of each tile ----
@@ -589,40 +602,30 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const size_t from = head_row(mine ? m : 0) * D + wg * DQ;
                 const bool in = mine && QSA_IN(from + DQ - 1, (size_t)a.n_tokens * a.n_q_heads * D);
                 const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q) + (in ? from : 0));
-                auto load = [&](int c, uint32_t (&x)[16]) {  // 32 dims
+                uint32_t x[DQ / 32][16];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4 *>(&x[4 * j]) = in ? __ldg(src + 4 * c + j) : make_uint4(0u, 0u, 0u, 0u);
-                };
-                float f = 1.0f;
-                if (a.dtype != QSA_F16) {
+                for (int j = 0; j < DQ / 8; ++j) *reinterpret_cast<uint4 *>(&x[j / 4][j % 4 * 4]) = in ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (!FINE) {  // bf16
                     uint32_t top = 0u;
 #pragma unroll
-                    for (int c = 0; c < DQ / 32; ++c) {
-                        uint32_t x[16];
-                        load(c, x);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) top = __vmaxu2(top, x[j] & 0x7FFF7FFFu);
-                    }
+                    for (int j = 0; j < DQ / 2; ++j) top = __vmaxu2(top, x[j / 16][j % 16] & 0x7FFF7FFFu);
                     sh.poison[wg][m] = max(top & 0xFFFFu, top >> 16);
                     softmax_sync();
-                    top = 0u;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) top = max(top, sh.poison[w][m]);
+                    top = max(max(sh.poison[0][m], sh.poison[1][m]), max(sh.poison[2][m], sh.poison[3][m]));
                     const int ex = head_sum_exponent(__uint_as_float(top << 16));
-                    f = exp2i(ex);
+                    const float f = flip ? -exp2i(ex) : exp2i(ex);
                     sl2 *= exp2i(-ex);
-                }
-#pragma unroll 1
-                for (int c = 0; c < DQ / 32; ++c) {
-                    uint32_t x[16];
-                    load(c, x);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (a.dtype != QSA_F16) x[j] = h2u(__floats2half2_rn(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xFFFF0000u) * f));
-                        x[j] ^= flip ? 0x80008000u : 0u;
+                    for (int j = 0; j < DQ / 2; ++j) {
+                        const uint32_t v = x[j / 16][j % 16];
+                        x[j / 16][j % 16] = h2u(__floats2half2_rn(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f));
                     }
-                    tmem_st16(lane_base + G::Q_COL + wg * (DQ / 2) + 16 * c, x);
+                } else if (flip) {
+#pragma unroll
+                    for (int j = 0; j < DQ / 2; ++j) x[j / 16][j % 16] ^= 0x80008000u;
                 }
+#pragma unroll
+                for (int c = 0; c < DQ / 32; ++c) tmem_st16(lane_base + G::Q_COL + wg * (DQ / 2) + 16 * c, x[c]);
                 tmem_wait_st();
                 fence_before();
                 mbar_arrive(smem_u32(&sh.q_full));
@@ -787,41 +790,50 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             softmax_sync();
             if (good) {
-                // The values to shared memory, in place of the tiles (whose
-                // products are done): 16-byte unit c of row m at c ^ (m % 8).
                 fence_after();
                 float ref = -CUDART_INF_F;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) ref = fmaxf(ref, sh.lref[w][m]);
                 l = 0.0f;
                 poison = 0u;
-#pragma unroll
+#pragma unroll 1
+                for (int w = 0; w < 4; ++w) ref = fmaxf(ref, sh.lref[w][m]);
+#pragma unroll 1
                 for (int w = 0; w < 4; ++w) {
                     l += sh.l[w][m] * (sh.lref[w][m] == ref ? 1.0f : ex2(sh.lref[w][m] - ref));
                     poison |= sh.poison[w][m];
                 }
-                const bool none = ref == -CUDART_INF_F;
-                const float scale = whole ? (none ? 0.0f : 1.0f / l) : 1.0f;
+                float scale = whole ? (ref == -CUDART_INF_F ? 0.0f : 1.0f / l) : 1.0f;
+                if (poison >> wg & 1u) scale = CUDART_NAN_F;  // a quarter of the dims has a V scale of its own
+                const size_t row = head_row(mine ? m : 0), d0 = row * D + wg * DQ;
+                float *part_o = work.o + at * M * D + (size_t)(wg * DQ) * M + m;  // [D][M]: a warp's lanes next to one another
+                const bool in = mine && QSA_IN(d0 + DQ - 1, (size_t)a.n_tokens * a.n_q_heads * D);
 #pragma unroll 1
-                for (int c = 0; c < DQ / 16; ++c) {
+                for (int c = 0; c < DQ; c += 16) {
                     uint32_t v[16];
-                    tmem_ld16(lane_base + G::O_COL + wg * DQ + 16 * c, v);
+                    tmem_ld16(lane_base + G::O_COL + wg * DQ + c, v);
                     tmem_wait_ld();
-                    const float w = poison >> wg & 1u ? CUDART_NAN_F : scale;  // a quarter of the dims has a V scale of its own
+                    if (!whole) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 16; ++j) {
+                            asm volatile("" : "+r"(v[j]));
+                            part_o[(size_t)(c + j) * M] = __uint_as_float(v[j]) * scale;
+                        }
+                    } else if (in) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) asm volatile("" : "+r"(v[4 * j + e]));
-                        float *dst = values + m * D + 4 * ((wg * (DQ / 4) + 4 * c + j) ^ (m & 7));
-                        *reinterpret_cast<float4 *>(dst) = make_float4(__uint_as_float(v[4 * j]) * w, __uint_as_float(v[4 * j + 1]) * w,
-                                                                       __uint_as_float(v[4 * j + 2]) * w, __uint_as_float(v[4 * j + 3]) * w);
+                        for (int j = 0; j < 16; j += 2) {
+                            asm volatile("" : "+r"(v[j]), "+r"(v[j + 1]));
+                            w[j / 2] = tree_value<FINE>(a, d0 + c + j, make_float2(__uint_as_float(v[j]) * scale, __uint_as_float(v[j + 1]) * scale));
+                        }
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + d0 + c);
+                        dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
                     }
                 }
                 if (mine && wg == 0) {
                     if (!whole)
                         *reinterpret_cast<float2 *>(work.ml + (at * M + m) * 2) = make_float2(ref - LIFT, l);
                     else if (a.lse)
-                        a.lse[head_row(m)] = lse_of(ref - LIFT, l);
+                        a.lse[row] = lse_of(ref - LIFT, l);
                 }
                 fence_before();  // O is overwritten by the next segment
             }
@@ -831,33 +843,13 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = false;
             break;
         }
-        // All threads write the values out, whole rows at a time.
-        for (int u = tid; u < rows * (D / 4); u += THREADS) {
-            const int m = u / (D / 4), c = u % (D / 4);
-            const float4 y = *reinterpret_cast<const float4 *>(values + m * D + 4 * (c ^ (m & 7)));
-            if (!whole) {
-                *reinterpret_cast<float4 *>(work.o + (at * M + m) * D + 4 * c) = y;
-                continue;
-            }
-            const size_t oi = head_row(m) * D + 4 * c;
-            if (!QSA_IN(oi + 3, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
-            float2 y0 = make_float2(y.x, y.y), y1 = make_float2(y.z, y.w);
-            if (a.gate) {
-                const float2 g0 = __ldg(reinterpret_cast<const float2 *>(a.gate + oi));
-                const float2 g1 = __ldg(reinterpret_cast<const float2 *>(a.gate + oi + 2));
-                y0 = make_float2(gated(y0.x, g0.x), gated(y0.y, g0.y));
-                y1 = make_float2(gated(y1.x, g1.x), gated(y1.y, g1.y));
-            }
-            store_out(a, oi, y0);
-            store_out(a, oi + 2, y1);
-        }
         if (!whole && i0 == 0) part = Part{t, 1 + (tiles - i1 + share - 1) / share, grp.tokens, 0};
         left -= n;
         if (left <= 0) break;
         i0 = 0;
         t += grp.tokens;
-        grp = tree_group_at<S>(a, t, in_group, bad);
-        __syncthreads();  // the values have been read; the tiles take their place again
+        grp = sh.next;
+        __syncthreads();  // the next is written over
     }
 
     // After a time-out: copies on their way land before the block ends, and
@@ -884,6 +876,45 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
+// Joins the partials of a group that spans CTAs: part p of the one that starts in
+// CTA x is slot 1 of that CTA, then slot 0 of the next ones of its KV head, values as
+// [D][M].  A block takes COLS dims of all head rows, a thread each.
+constexpr int COLS = 8;
+template <int S, bool FINE>
+__global__ void __launch_bounds__(M) paged_tree_join_kernel(const TreeArgs a, void *ws) {
+    constexpr int D = 128 * S;
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    const Work work(ws, MAX_GROUP_PARTS, M);
+    const int x = blockIdx.y, m = threadIdx.x, per = a.n_q_heads / a.n_kv_heads, d0 = blockIdx.x * COLS;
+    const Part part = work.part[x];
+    if (part.row < 0 || m >= part.tokens * per) return;
+    auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * M; };
+    float top = -CUDART_INF_F, l = 0.0f;
+    float2 o[COLS / 2];
+#pragma unroll
+    for (int j = 0; j < COLS / 2; ++j) o[j] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = 0; p < part.n; ++p) top = fmaxf(top, work.ml[(slot(p) + m) * 2]);
+#pragma unroll 2
+    for (int p = 0; p < part.n; ++p) {
+        const float2 ml = reinterpret_cast<const float2 *>(work.ml)[slot(p) + m];
+        const float w = ml.x == -CUDART_INF_F ? 0.0f : exp2f(ml.x - top), *src = work.o + slot(p) * D + (size_t)d0 * M + m;
+        l = fmaf(w, ml.y, l);
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j) o[j] = __ffma2_rn(make_float2(w, w), make_float2(src[2 * j * M], src[(2 * j + 1) * M]), o[j]);
+    }
+    const float inv = top == -CUDART_INF_F ? 0.0f : 1.0f / l;
+    const int i = m / per;
+    const size_t row = (size_t)(part.row + i) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + (m - i * per);
+    if (d0 == 0 && a.lse) a.lse[row] = lse_of(top, l);
+    if (!QSA_IN(row * D + d0 + COLS - 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
+    uint32_t y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = tree_value<FINE>(a, row * D + d0 + 2 * j, make_float2(o[j].x * inv, o[j].y * inv));
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * D + d0) = make_uint4(y[0], y[1], y[2], y[3]);
+}
+
 // Codes [cells, heads, D] in boxes of a tile's cells (or a page's, if fewer) x one
 // head x 128 dims.
 template <int S>
@@ -903,7 +934,7 @@ cudaError_t launch_tree(const TreeArgs &a, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TreeSmem<S>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TreeSmem<S>), s, a, kmap, vmap, ws);
     if (e != cudaSuccess || ranges == 1) return e;
-    return launch_join<S>(a, Joined{a.workspace, MAX_CTAS, per, 0}, Joined{ws, MAX_GROUP_PARTS, M, ctas}, s);
+    return launch_dependent(a.dtype == QSA_F16 ? paged_tree_join_kernel<S, true> : paged_tree_join_kernel<S, false>, dim3(a.head_dim / COLS, ctas), dim3(M), 0, s, a, ws);
 }
 
 template <int S>

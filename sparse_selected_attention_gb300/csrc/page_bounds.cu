@@ -20,8 +20,19 @@
 namespace qsa {
 namespace {
 
-constexpr int WARPS = 4, THREADS = 32 * WARPS, CTAS_PER_SM = 4;
-constexpr int BATCH = 8;  // loads of a lane on their way
+constexpr int WARPS = 4, THREADS = 32 * WARPS, CTAS_PER_SM = 5;
+constexpr int BATCH = 4;  // loads of a lane on their way, twice
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // The pages of row r that are to be written: n from `first` on.
 struct Span {
@@ -129,32 +140,44 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) page_bounds_kernel(const
                     lo[i] = CUDART_INF_F;
                 }
                 bool nan = false;
-                for (int c0 = 0; c0 < filled; c0 += CELLS * BATCH) {
-                    uint4 w[BATCH] = {};
-                    uint16_t sc[BATCH] = {};
+                uint4 w[2][BATCH] = {};
+                uint16_t sc[2][BATCH] = {};
+                auto load = [&](int buf, int c0) {
 #pragma unroll
                     for (int i = 0; i < BATCH; ++i) {
                         // Cells behind the last stand for it: twice counts once.
                         const size_t row = row0 + (size_t)min(c0 + i * CELLS + sub, filled - 1) * hkv;
                         if (QSA_IN(row, (size_t)a.n_pages * a.page_size * hkv)) {
-                            w[i] = __ldg(reinterpret_cast<const uint4 *>(a.kq + row * D) + c16);
-                            sc[i] = __ldg(a.ksc + row * 4 + quarter);
+                            w[buf][i] = __ldg(reinterpret_cast<const uint4 *>(a.kq + row * D) + c16);
+                            sc[buf][i] = __ldg(a.ksc + row * 4 + quarter);
                         }
                     }
+                };
+                auto fold = [&](int buf) {  // two cells' values of a dim at a time
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        nan |= (sc[i] & 0x7C00u) == 0x7C00u;
-                        const float f = __half2float(__ushort_as_half(sc[i]));
-                        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    for (int i = 0; i < BATCH; i += 2) {
+                        nan |= (sc[buf][i] & 0x7C00u) == 0x7C00u || (sc[buf][i + 1] & 0x7C00u) == 0x7C00u;
+                        const float f0 = __half2float(__ushort_as_half(sc[buf][i])), f1 = __half2float(__ushort_as_half(sc[buf][i + 1]));
+                        const uint32_t x0[4] = {w[buf][i].x, w[buf][i].y, w[buf][i].z, w[buf][i].w};
+                        const uint32_t x1[4] = {w[buf][i + 1].x, w[buf][i + 1].y, w[buf][i + 1].z, w[buf][i + 1].w};
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
-                            const float2 v = __fmul2_rn(codes2(x[e / 2], e & 1), make_float2(f, f));
-                            hi[2 * e] = fmaxf(hi[2 * e], v.x);
-                            hi[2 * e + 1] = fmaxf(hi[2 * e + 1], v.y);
-                            lo[2 * e] = fminf(lo[2 * e], v.x);
-                            lo[2 * e + 1] = fminf(lo[2 * e + 1], v.y);
+                            const float2 v0 = __fmul2_rn(codes2(x0[e / 2], e & 1), make_float2(f0, f0));
+                            const float2 v1 = __fmul2_rn(codes2(x1[e / 2], e & 1), make_float2(f1, f1));
+                            hi[2 * e] = max3(hi[2 * e], v0.x, v1.x);
+                            hi[2 * e + 1] = max3(hi[2 * e + 1], v0.y, v1.y);
+                            lo[2 * e] = min3(lo[2 * e], v0.x, v1.x);
+                            lo[2 * e + 1] = min3(lo[2 * e + 1], v0.y, v1.y);
                         }
                     }
+                };
+                load(0, 0);
+                for (int c0 = 0; c0 < filled; c0 += 2 * CELLS * BATCH) {
+                    if (c0 + CELLS * BATCH < filled) load(1, c0 + CELLS * BATCH);
+                    fold(0);
+                    if (c0 + CELLS * BATCH >= filled) break;
+                    if (c0 + 2 * CELLS * BATCH < filled) load(0, c0 + 2 * CELLS * BATCH);
+                    fold(1);
                 }
                 // Across the lanes of other cells: each step a lane keeps half of its dims.
                 constexpr int K = 4 * S;

@@ -158,6 +158,7 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                 sh.pages[tid] = tid < n ? pages_of(a, t + tid, row, bad) : 0;
             }
             __syncthreads();
+            constexpr int AT_A_TIME = NT == 1 ? 8 : 4;  // heads whose loads are on their way together
             constexpr int PAIRS = D / 2, AT_ONCE = THREADS / PAIRS, ROUNDS = (G + AT_ONCE - 1) / AT_ONCE;
             const int d = tid % PAIRS * 2, first = tid / PAIRS;
             // Place of dims d, d + 1 (of different halves of a k-step) as codes of a quarter.
@@ -169,18 +170,26 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                 up[i] = down[i] = make_float2(0.0f, 0.0f);
                 if (k < n) {
                     const size_t at = ((size_t)(t + k) * a.n_q_heads + (size_t)kvh * per) * D + d;
-                    for (int h = 0; h < per; ++h) {
-                        if (!QSA_IN(at + (size_t)h * D + 1, (size_t)a.n_tokens * a.n_q_heads * D)) continue;
-                        const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.q) + at + (size_t)h * D));
-                        const float2 v = a.dtype == QSA_F16 ? __half22float2(u2h(w))
-                                                            : make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-                        up[i].x += fmaxf(v.x, 0.0f);
-                        up[i].y += fmaxf(v.y, 0.0f);
-                        down[i].x += fminf(v.x, 0.0f);
-                        down[i].y += fminf(v.y, 0.0f);
-                        // A NaN is lost in maximum and minimum.
-                        if (v.x != v.x) up[i].x = v.x;
-                        if (v.y != v.y) up[i].y = v.y;
+#pragma unroll 1
+                    for (int h = 0; h < per; h += AT_A_TIME) {
+                        uint32_t w[AT_A_TIME];
+#pragma unroll
+                        for (int e = 0; e < AT_A_TIME; ++e)
+                            w[e] = h + e < per && QSA_IN(at + (size_t)(h + e) * D + 1, (size_t)a.n_tokens * a.n_q_heads * D)
+                                       ? __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.q) + at + (size_t)(h + e) * D))
+                                       : 0u;
+#pragma unroll
+                        for (int e = 0; e < AT_A_TIME; ++e) {
+                            const float2 v = a.dtype == QSA_F16 ? __half22float2(u2h(w[e]))
+                                                                : make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+                            up[i].x += fmaxf(v.x, 0.0f);
+                            up[i].y += fmaxf(v.y, 0.0f);
+                            down[i].x += fminf(v.x, 0.0f);
+                            down[i].y += fminf(v.y, 0.0f);
+                            // A NaN is lost in maximum and minimum.
+                            if (v.x != v.x) up[i].x = v.x;
+                            if (v.y != v.y) up[i].y = v.y;
+                        }
                     }
                     const float m = fabsf(fmaxf(fmaxf(up[i].x, up[i].y), fmaxf(-down[i].x, -down[i].y)));
                     atomicMax(&sh.top[k], __float_as_uint(m));  // not negative: bits order as values do
@@ -213,43 +222,56 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
             int row;
             pages_of(a, t, row, bad);
             const int most = tiles * TILE;  // pages of the longest token, or a few more
+            int page[2];
+            auto look = [&](int i) {  // up a tile's pages
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int j = i * TILE + g + 8 * e;
+                    page[e] = i < i1 && j < a.max_pages && j < most ? __ldg(a.page_table + (size_t)row * a.max_pages + j) : -1;
+                }
+            };
+            look(i0 + warp);
             for (int i = i0 + warp; i < i1; i += W) {
                 size_t at[2];
                 bool there[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int j = i * TILE + g + 8 * e;
-                    const int page = j < a.max_pages && j < most ? __ldg(a.page_table + (size_t)row * a.max_pages + j) : -1;
-                    there[e] = page >= 0 && page < a.n_pages;
-                    at[e] = ((size_t)(there[e] ? page : 0) * hkv + kvh);
+                    there[e] = page[e] >= 0 && page[e] < a.n_pages;
+                    at[e] = ((size_t)(there[e] ? page[e] : 0) * hkv + kvh);
                     there[e] = there[e] && QSA_IN(at[e], (size_t)a.n_pages * hkv);
                 }
+                look(i + W);
                 float y[NT][4];
 #pragma unroll
                 for (int k = 0; k < NT; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int8_t *codes = b ? a.lo_q : a.hi_q;
-                    const uint16_t *scales = b ? a.lo_sc : a.hi_sc;
-                    uint32_t w[4][2][2 * S];
-                    uint2 sc[2];
+                uint32_t codes[2][4][2][2 * S];
+                uint2 scales[2][2];
+                auto load = [&](int b) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        sc[e] = make_uint2(0u, 0u);
-                        if (there[e]) sc[e] = __ldg(reinterpret_cast<const uint2 *>(scales + at[e] * 4));
+                        scales[b][e] = make_uint2(0u, 0u);
+                        if (there[e]) scales[b][e] = __ldg(reinterpret_cast<const uint2 *>((b ? a.lo_sc : a.hi_sc) + at[e] * 4));
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            const int8_t *src = codes + at[e] * D + q * Q + 8 * S * r;
+                            const int8_t *src = (b ? a.lo_q : a.hi_q) + at[e] * D + q * Q + 8 * S * r;
 #pragma unroll
-                            for (int c = 0; c < 2 * S; ++c) w[q][e][c] = 0u;
+                            for (int c = 0; c < 2 * S; ++c) codes[b][q][e][c] = 0u;
                             if (there[e]) {
                                 if constexpr (S == 1)
-                                    *reinterpret_cast<uint2 *>(w[q][e]) = __ldg(reinterpret_cast<const uint2 *>(src));
+                                    *reinterpret_cast<uint2 *>(codes[b][q][e]) = __ldg(reinterpret_cast<const uint2 *>(src));
                                 else
-                                    *reinterpret_cast<uint4 *>(w[q][e]) = __ldg(reinterpret_cast<const uint4 *>(src));
+                                    *reinterpret_cast<uint4 *>(codes[b][q][e]) = __ldg(reinterpret_cast<const uint4 *>(src));
                             }
                         }
                     }
+                };
+                load(0);
+                if constexpr (NT == 1) load(1);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    if (NT > 1 && b) load(1);
+                    const auto &w = codes[b];
+                    const auto &sc = scales[b];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float s[2];

@@ -4,16 +4,17 @@
 //   hi_d = max_c s_c k_cd,  scale = roundup16(max_d |hi_d| / 127),  code = ceil(hi_d / scale)
 //
 // A key s_c k_cd has 19 bits and is exact in fp32; a division rounded up to fp32
-// and then to fp16 (or to a whole number) gives the value rounded up once, as the
-// coarser numbers are fp32 numbers too.  So the results are exact by definition.
+// and then to fp16 gives the value rounded up once, as the coarser numbers are fp32
+// numbers too.  So the results are exact by definition.
 //
 // It is bound by reading the keys.  A warp takes a page of one KV head: 16 codes a
 // lane, four cells (of 128 dims) or two at a time, maxima and minima in registers,
-// exchanged across the lanes of other cells by halves.  The pages that the rows'
-// new tokens are in, counted by each warp for itself, are shared out evenly.
+// exchanged across the lanes of other cells by halves.  The pages that the rows' new
+// tokens are in are shared out evenly.
 #include <math_constants.h>
 
 #include "check.cuh"
+#include "page_share.cuh"
 #include "qsa_internal.h"
 #include "tc_common.cuh"
 
@@ -64,18 +65,21 @@ __device__ __forceinline__ float2 codes2(uint32_t w, bool high) {
     return __fadd2_rn(f, make_float2(-8388736.0f, -8388736.0f));
 }
 
-// The dims' bounds of one page and head: v [K dims of a lane], their quarter's
-// largest |v| among the lanes of `mask` bits, codes and scale out.  sign 1: upwards.
+// One bound of a page and head: v [K dims of a lane], top the largest |v| of their
+// quarter.  x / s rounded upwards to a whole number c is where c s >= x > (c - 1) s;
+// both products have 18 bits, so the reciprocal's rounding is put right exactly.
 template <int K>
 __device__ __forceinline__ void write_bound(const float (&v)[K], float top, bool nan, bool up, int8_t *q, uint16_t *sc, bool one) {
     const __half scale = nan ? __ushort_as_half(0x7E00) : __float2half_ru(__fdiv_ru(top, 127.0f));
-    const float s = __half2float(scale);
+    const float s = __half2float(scale), inv = __frcp_rn(s);
     uint32_t w[K / 4];
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-        const float x = up ? ceilf(__fdiv_ru(v[i], s)) : floorf(__fdiv_rd(v[i], s));
-        const uint32_t c = s > 0.0f ? (uint32_t)(int)x & 0xFFu : 0u;
-        w[i / 4] = i % 4 ? w[i / 4] | c << (8 * (i % 4)) : c;
+        const float x = up ? v[i] : -v[i];  // floor(x / s) = -ceil(-x / s)
+        float c = ceilf(x * inv);
+        c += c * s < x ? 1.0f : (c - 1.0f) * s >= x ? -1.0f : 0.0f;
+        const uint32_t code = s > 0.0f ? (uint32_t)(int)(up ? c : -c) & 0xFFu : 0u;
+        w[i / 4] = i % 4 ? w[i / 4] | code << (8 * (i % 4)) : code;
     }
     if constexpr (K == 4)
         *reinterpret_cast<uint32_t *>(q) = w[0];
@@ -89,43 +93,24 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) page_bounds_kernel(const
     constexpr int D = 128 * S, LANES = 8 * S, CELLS = 32 / LANES;  // lanes of a cell's row, cells at a time
     const int lane = threadIdx.x & 31, c16 = lane % LANES, sub = lane / LANES;
     const int quarter = c16 / (2 * S), page_shift = 31 - __clz(a.page_size), hkv = a.n_kv_heads;
-    const long long warps = (long long)gridDim.x * WARPS, me = (long long)blockIdx.x * WARPS + (threadIdx.x >> 5);
+    __shared__ ShareSmem<WARPS> found;
     wait_for_previous_grid();
     allow_dependent_launch();
     bool bad = false;
-    // All rows' pages; then the row that holds this warp's first item (a page and a head).
-    long long total = 0;
-    for (int r0 = 0; r0 < a.n_rows; r0 += 32) total += r0 + lane < a.n_rows ? span_of(a, r0 + lane, bad).n : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total *= hkv;
-    const long long share = (total + warps - 1) / warps;
-    long long at = share * me;
-    int left = (int)max(min(share, total - at), 0ll);
+    // This block's pages, of all heads; its warps take the (page, head) pairs in turn.
+    int r, at, pages;
+    find_share(found, a.n_rows, blockIdx.x, gridDim.x, 1, [&](int i) { return span_of(a, i, bad).n; }, r, at, pages);
+    int left = pages * hkv - (threadIdx.x >> 5);  // pairs from this warp's first on
     if (left > 0) {
-        long long before = 0;
-        int r = 0, j = 0, head = 0;
-        Span s{0, 0, 0};
-        for (int r0 = 0; r0 < a.n_rows; r0 += 32) {
-            const Span mine = r0 + lane < a.n_rows ? span_of(a, r0 + lane, bad) : Span{0, 0, 0};
-            long long sum = (long long)mine.n * hkv;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += u;
+        Span s = span_of(a, r, bad);
+        int j = at, head = threadIdx.x >> 5;
+        auto settle = [&] {
+            while (head >= hkv) {
+                head -= hkv;
+                for (++j; j == s.n; j = 0) s = span_of(a, ++r, bad);  // there is a next row with pages
             }
-            const unsigned past = __ballot_sync(0xffffffffu, before + sum > at);
-            if (past) {
-                const int k = __ffs(past) - 1;
-                const long long in = at - before - __shfl_sync(0xffffffffu, sum - (long long)mine.n * hkv, k);
-                r = r0 + k;
-                s = Span{__shfl_sync(0xffffffffu, mine.first, k), __shfl_sync(0xffffffffu, mine.n, k), __shfl_sync(0xffffffffu, mine.len, k)};
-                j = (int)(in / hkv);
-                head = (int)(in % hkv);
-                break;
-            }
-            before += __shfl_sync(0xffffffffu, sum, 31);
-        }
+        };
+        settle();
         for (;;) {
             const int lp = s.first + j, page = __ldg(a.page_table + (size_t)r * a.max_pages + lp);
             const int filled = min(a.page_size, s.len - (lp << page_shift));
@@ -230,15 +215,9 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) page_bounds_kernel(const
                     write_bound<K>(vl, tl, n, false, a.lo_q + out * D + d0, a.lo_sc + out * 4 + quarter, one);
                 }
             }
-            if (--left == 0) break;
-            if (++head == hkv) {
-                head = 0;
-                ++j;
-            }
-            while (j == s.n) {  // there is a next row with pages
-                s = span_of(a, ++r, bad);
-                j = 0;
-            }
+            if ((left -= WARPS) <= 0) break;
+            head += WARPS;
+            settle();
         }
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
@@ -246,8 +225,8 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) page_bounds_kernel(const
 
 template <int S>
 cudaError_t launch(const qsa_page_bounds_args &a, cudaStream_t s) {
-    const long long most = (long long)a.n_rows * a.max_pages * a.n_kv_heads, ctas = (most + WARPS - 1) / WARPS;
-    const int grid = (int)(ctas < 152 * CTAS_PER_SM ? ctas : 152 * CTAS_PER_SM);
+    const long long most = (long long)a.n_rows * a.max_pages;
+    const int grid = (int)(most < 152 * CTAS_PER_SM ? most : 152 * CTAS_PER_SM);
     return launch_dependent(page_bounds_kernel<S>, dim3(grid), dim3(THREADS), 0, s, a);
 }
 

@@ -16,8 +16,10 @@
 // bytes (or sixteen) are one load and a k-step's dims are of one quarter.  Its
 // products are summed per quarter, and the quarter's scale multiplies in fp32.
 //
-// The tiles of 16 pages of all sequences are shared out evenly (as the units of
-// paged_rows.cuh are); each CTA finds its place by itself.
+// The tiles of 16 pages of all sequences are shared out evenly over the blocks.
+// Chunks of many tokens go to a grid of 32 tokens by tiles instead: there, one
+// sequence's tokens have pages enough for all, and looking up thousands of tokens
+// would cost more than it evens out.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
@@ -25,6 +27,7 @@
 #include <algorithm>
 
 #include "check.cuh"
+#include "page_share.cuh"
 #include "qsa_internal.h"
 #include "tc_common.cuh"
 
@@ -75,9 +78,7 @@ struct Smem {
     float unscale[4 * NT];      // 2^-e of a token
     int pages[4 * NT];
     uint32_t top[4 * NT];
-    long long scan[W];
-    long long total, before;
-    int t;
+    ShareSmem<W> found;
 };
 
 // S = head_dim / 128.  A group: up to 4 NT consecutive tokens of one sequence, not
@@ -93,63 +94,41 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
     wait_for_previous_grid();
     allow_dependent_launch();
     bool bad = false;
-    // Tokens of the group that starts at t (0: none does), and its tiles.
-    auto group_at = [&](int t, int &tiles) {
-        int row, most = pages_of(a, t, row, bad), n = 1;
-        tiles = 0;
-        if (a.rows) {
-            const int same = __ldg(a.rows + t);
-            if (t % G && __ldg(a.rows + t - 1) == same) return 0;
-            for (const int end = min(a.n_tokens, t / G * G + G); t + n < end && __ldg(a.rows + t + n) == same; ++n)
-                most = max(most, pages_of(a, t + n, row, bad));
-        }
-        tiles = (most + TILE - 1) / TILE;
+    auto group_of = [&](int t, int &tiles) {  // by a warp: the group that starts at t, where one does
+        const int u = t + lane;
+        const bool same = u < min(a.n_tokens, t / G * G + G) && (lane == 0 || (a.rows && __ldg(a.rows + u) == __ldg(a.rows + t)));
+        const unsigned m = __ballot_sync(0xffffffffu, same);
+        const int n = m == 0xffffffffu ? 32 : __ffs(~m) - 1;
+        int row;
+        tiles = (__reduce_max_sync(0xffffffffu, lane < n ? pages_of(a, u, row, bad) : 0) + TILE - 1) / TILE;
         return n;
     };
-    // All tiles, and the group in which this CTA's share of them starts.
-    const int run = (a.n_tokens + THREADS - 1) / THREADS;
-    const int t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
-    long long mine = 0;
-    for (int t = t0; t < t1; ++t) {
-        int tiles;
-        group_at(t, tiles);
-        mine += tiles;
-    }
-    long long sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += u;
-    }
-    if (lane == 31) sh.scan[warp] = sum;
-    __syncthreads();
-    long long total = 0, before = sum - mine;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-        before += w < warp ? sh.scan[w] : 0;
-        total += sh.scan[w];
-    }
-    const int share = (int)max((total + ranges - 1) / ranges, (long long)W);
-    const long long x0 = (long long)share * range;
-    if (x0 >= before && x0 < before + mine) {
-        for (int t = t0;; ++t) {
-            int tiles;
-            group_at(t, tiles);
-            if (x0 < before + tiles) {
-                sh.t = t;
-                sh.before = before;
-                break;
+    int t, i0, left, step = 1;  // tiles i0, i0 + step, .. are this block's
+    if constexpr (NT == 1) {
+        auto tiles_of = [&](int t) {  // of the group that starts at t; 0 where none does
+            int row, most = pages_of(a, t, row, bad);
+            if (a.rows) {
+                const int same = __ldg(a.rows + t);
+                if (t % G && __ldg(a.rows + t - 1) == same) return 0;
+#pragma unroll 1
+                for (int u = t + 1; u < min(a.n_tokens, t / G * G + G) && __ldg(a.rows + u) == same; ++u) most = max(most, pages_of(a, u, row, bad));
             }
-            before += tiles;
-        }
+            return (most + TILE - 1) / TILE;
+        };
+        find_share(sh.found, a.n_tokens, range, ranges, W, tiles_of, t, i0, left);
+    } else {
+        // Block x of those that take the 32 tokens' groups.
+        const int blocks = (a.n_tokens + G - 1) / G;
+        step = ranges / blocks;
+        t = range % blocks * G;
+        left = min(a.n_tokens - t, G);  // tokens
+        i0 = range / blocks;
     }
-    __syncthreads();
-    int left = (int)max(min((long long)share, total - x0), 0ll);
-    int t = sh.t, i0 = left ? (int)(x0 - sh.before) : 0, tiles = 0;
     while (left > 0) {
-        const int n = group_at(t, tiles);
-        const int i1 = min(tiles, i0 + left);
-        if (i1 > i0) {
+        int tiles;
+        const int n = group_of(t, tiles), from = i0;
+        const int i1 = NT == 1 ? min(tiles, i0 + left) : tiles;
+        if (i1 > from) {
             // The tokens' sums: a thread takes two dims of a token.
             __syncthreads();  // of the group before
             if (tid < G) {
@@ -230,8 +209,8 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                     page[e] = i < i1 && j < a.max_pages && j < most ? __ldg(a.page_table + (size_t)row * a.max_pages + j) : -1;
                 }
             };
-            look(i0 + warp);
-            for (int i = i0 + warp; i < i1; i += W) {
+            look(from + warp * step);
+            for (int i = from + warp * step; i < i1; i += W * step) {
                 size_t at[2];
                 bool there[2];
 #pragma unroll
@@ -240,7 +219,7 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                     at[e] = ((size_t)(there[e] ? page[e] : 0) * hkv + kvh);
                     there[e] = there[e] && QSA_IN(at[e], (size_t)a.n_pages * hkv);
                 }
-                look(i + W);
+                look(i + W * step);
                 float y[NT][4];
 #pragma unroll
                 for (int k = 0; k < NT; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
@@ -316,8 +295,12 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                 }
             }
         }
-        left -= i1 - i0;
-        i0 = 0;
+        if constexpr (NT == 1) {
+            left -= i1 - i0;
+            i0 = 0;
+        } else {
+            left -= n;
+        }
         t += max(n, 1);
     }
     if (__syncthreads_or(bad) && tid == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
@@ -325,12 +308,18 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
 
 template <int S, int NT>
 cudaError_t launch(const qsa_page_score_args &a, cudaStream_t s) {
-    constexpr int SMEM = (int)sizeof(Smem<S, NT>), CTAS_PER_SM = NT == 1 ? 6 : 3;
+    constexpr int SMEM = (int)sizeof(Smem<S, NT>), CTAS_PER_SM = NT == 1 ? 5 : 3;
     cudaError_t e = cudaFuncSetAttribute(page_score_kernel<S, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    const long long tiles = (a.max_pages + TILE - 1) / TILE, most = a.n_tokens * ((tiles + W - 1) / W);
+    const long long tiles = (a.max_pages + TILE - 1) / TILE;
     const int resident = std::max(152 * CTAS_PER_SM / a.n_kv_heads, 1);
-    const int ranges = (int)std::min<long long>(most, resident);
+    int ranges;
+    if (NT == 1) {
+        ranges = (int)std::min<long long>(a.n_tokens * ((tiles + W - 1) / W), resident);
+    } else {
+        const long long blocks = (a.n_tokens + 4 * NT - 1) / (4 * NT);
+        ranges = (int)(blocks * std::max<long long>(std::min<long long>(resident / blocks, (tiles + W - 1) / W), 1));
+    }
     return launch_dependent(page_score_kernel<S, NT>, dim3(ranges * a.n_kv_heads), dim3(THREADS), SMEM, s, a);
 }
 

@@ -11,10 +11,12 @@
 //
 // Pages are the M side (16 a warp) of m16n8k16 products, the sums of up to 4 NT
 // tokens of one sequence the N side, as two fp16 parts each under a power of two
-// per token (22 bits).  Codes go from memory to fragments: lane (g, r) holds codes
-// 8 S r .. 8 S r + 8 S - 1 of each quarter of pages g and g + 8, so that eight
-// bytes (or sixteen) are one load and a k-step's dims are of one quarter.  Its
-// products are summed per quarter, and the quarter's scale multiplies in fp32.
+// per token (22 bits).  Codes go through shared memory (read straight to fragments,
+// 32 bytes of a row at a time, the loads' tags took half of the time), a tile ahead.
+// Lane (g, r) holds codes 8 S r .. 8 S r + 8 S - 1 of each quarter of pages g and g + 8,
+// so that eight bytes (or sixteen) are one read and a k-step's dims are of one
+// quarter; its products are summed per quarter, and the quarter's scale multiplies in
+// fp32.
 //
 // The tiles of 16 pages of all sequences are shared out evenly over the blocks.
 // Chunks of many tokens go to a grid of 32 tokens by tiles instead: there, one
@@ -79,7 +81,26 @@ struct Smem {
     int pages[4 * NT];
     uint32_t top[4 * NT];
     ShareSmem<W> found;
+    // A warp's tiles: upper and lower bounds of sixteen pages.  Of many tokens one at a
+    // time: their products hide the other warps' copies, and more blocks fit.
+    static constexpr int STAGES = NT == 1 ? 2 : 1;
+    alignas(16) uint8_t codes[W][STAGES][2][TILE * 128 * S];
+    uint2 scales[W][STAGES][2][TILE];
 };
+// Place of 16-byte unit u of row r of a tile: the reads of a fragment meet a bank once.
+template <int S>
+__device__ __forceinline__ int unit_at(int r, int u) {
+    return r * 128 * S + 16 * (S == 1 ? u ^ 2 * (r & 3) : u ^ 4 * (r & 1));
+}
+// Zeros where not `have`.
+template <int BYTES>
+__device__ __forceinline__ void cp_async(void *dst, const void *src, bool have) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(tc::smem_u32(dst)), "l"(src), "r"(have ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(tc::smem_u32(dst)), "l"(src), "n"(BYTES), "r"(have ? BYTES : 0)
+                     : "memory");
+}
 
 // S = head_dim / 128.  A group: up to 4 NT consecutive tokens of one sequence, not
 // across multiples of 4 NT; without rows, one token.
@@ -115,7 +136,7 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
             }
             return (most + TILE - 1) / TILE;
         };
-        find_share(sh.found, a.n_tokens, range, ranges, W, tiles_of, t, i0, left);
+        find_share(sh.found, a.n_tokens, range, ranges, 1, tiles_of, t, i0, left);
     } else {
         // Block x of those that take the 32 tokens' groups.
         const int blocks = (a.n_tokens + G - 1) / G;
@@ -201,56 +222,56 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
             int row;
             pages_of(a, t, row, bad);
             const int most = tiles * TILE;  // pages of the longest token, or a few more
-            int page[2];
-            auto look = [&](int i) {  // up a tile's pages
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int j = i * TILE + g + 8 * e;
-                    page[e] = i < i1 && j < a.max_pages && j < most ? __ldg(a.page_table + (size_t)row * a.max_pages + j) : -1;
-                }
+            // The warp's tiles, one ahead of the products and its pages one more: 16-byte
+            // units of a page's row next to one another, eight lanes (or sixteen) a row.
+            int page = -1;  // of row lane % 16
+            auto look = [&](int i) {
+                const int j = i * TILE + (lane & 15);
+                page = i < i1 && j < a.max_pages && j < most ? __ldg(a.page_table + (size_t)row * a.max_pages + j) : -1;
             };
-            look(from + warp * step);
-            for (int i = from + warp * step; i < i1; i += W * step) {
-                size_t at[2];
-                bool there[2];
+            unsigned held = 0u;  // rows that are there: sixteen of the tile at hand, sixteen of the next
+            auto copy = [&](int st) {
+                bool there = page >= 0 && page < a.n_pages;
+                const size_t at = (size_t)(there ? page : 0) * hkv + kvh;
+                there = there && QSA_IN(at, (size_t)a.n_pages * hkv);
+                const unsigned m = __ballot_sync(0xffffffffu, there);
+                held = held >> 16 | m << 16;
+                cp_async<8>(&sh.scales[warp][st][lane >> 4][lane & 15], (lane >> 4 ? a.lo_sc : a.hi_sc) + at * 4, there);
+                constexpr int UNITS = 8 * S, ROWS = 32 / UNITS;  // of a row; rows at a time
+                const int u = lane % UNITS;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    there[e] = page[e] >= 0 && page[e] < a.n_pages;
-                    at[e] = ((size_t)(there[e] ? page[e] : 0) * hkv + kvh);
-                    there[e] = there[e] && QSA_IN(at[e], (size_t)a.n_pages * hkv);
+                for (int x = 0; x < TILE / ROWS; ++x) {
+                    const int r16 = x * ROWS + lane / UNITS;
+                    const size_t from = (size_t)__shfl_sync(0xffffffffu, (unsigned long long)at, r16) * D + 16 * u;
+                    uint8_t *to = sh.codes[warp][st][0] + unit_at<S>(r16, u);
+                    cp_async<16>(to, a.hi_q + from, m >> r16 & 1u);
+                    cp_async<16>(to + TILE * D, a.lo_q + from, m >> r16 & 1u);
                 }
-                look(i + W * step);
+                asm volatile("cp.async.commit_group;\n" ::);
+            };
+            constexpr int STAGES = Smem<S, NT>::STAGES;
+            int st = 0;
+            look(from + warp * step);
+            copy(0);
+            look(from + (warp + W) * step);
+            for (int i = from + warp * step; i < i1; i += W * step, st ^= STAGES - 1) {
+                if constexpr (STAGES == 2) {
+                    copy(st ^ 1);
+                    look(i + 2 * W * step);
+                    asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+                } else {
+                    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+                }
+                __syncwarp();
+                const unsigned held_now = STAGES == 2 ? held : held >> 16;
+                const bool there[2] = {(held_now >> g & 1u) != 0u, (held_now >> (g + 8) & 1u) != 0u};
                 float y[NT][4];
 #pragma unroll
                 for (int k = 0; k < NT; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
-                uint32_t codes[2][4][2][2 * S];
-                uint2 scales[2][2];
-                auto load = [&](int b) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        scales[b][e] = make_uint2(0u, 0u);
-                        if (there[e]) scales[b][e] = __ldg(reinterpret_cast<const uint2 *>((b ? a.lo_sc : a.hi_sc) + at[e] * 4));
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int8_t *src = (b ? a.lo_q : a.hi_q) + at[e] * D + q * Q + 8 * S * r;
-#pragma unroll
-                            for (int c = 0; c < 2 * S; ++c) codes[b][q][e][c] = 0u;
-                            if (there[e]) {
-                                if constexpr (S == 1)
-                                    *reinterpret_cast<uint2 *>(codes[b][q][e]) = __ldg(reinterpret_cast<const uint2 *>(src));
-                                else
-                                    *reinterpret_cast<uint4 *>(codes[b][q][e]) = __ldg(reinterpret_cast<const uint4 *>(src));
-                            }
-                        }
-                    }
-                };
-                load(0);
-                if constexpr (NT == 1) load(1);
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    if (NT > 1 && b) load(1);
-                    const auto &w = codes[b];
-                    const auto &sc = scales[b];
+                    const uint2 sc[2] = {sh.scales[warp][st][b][g], sh.scales[warp][st][b][g + 8]};
+                    const uint8_t *codes = sh.codes[warp][st][b];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         float s[2];
@@ -259,13 +280,21 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                             const __half2 h = u2h(q >> 1 ? sc[e].y : sc[e].x);
                             s[e] = q & 1 ? __high2float(h) : __low2float(h);
                         }
+                        uint32_t w[2][2 * S];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if constexpr (S == 1)
+                                *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(codes + unit_at<S>(g + 8 * e, 2 * q + (r >> 1)) + 8 * (r & 1));
+                            else
+                                *reinterpret_cast<uint4 *>(w[e]) = *reinterpret_cast<const uint4 *>(codes + unit_at<S>(g + 8 * e, 4 * q + r));
+                        }
                         uint32_t x[KS][4];
 #pragma unroll
                         for (int c = 0; c < KS; ++c) {
-                            x[c][0] = pair(w[q][0][c], false);
-                            x[c][1] = pair(w[q][1][c], false);
-                            x[c][2] = pair(w[q][0][c], true);
-                            x[c][3] = pair(w[q][1][c], true);
+                            x[c][0] = pair(w[0][c], false);
+                            x[c][1] = pair(w[1][c], false);
+                            x[c][2] = pair(w[0][c], true);
+                            x[c][3] = pair(w[1][c], true);
                         }
 #pragma unroll
                         for (int k = 0; k < NT; ++k) {
@@ -276,6 +305,11 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                             y[k][2] = fmaf(acc[2] + acc[3], s[1], y[k][2]);
                         }
                     }
+                }
+                __syncwarp();  // the tile has been read
+                if constexpr (STAGES == 1) {
+                    copy(0);
+                    look(i + 2 * W * step);
                 }
 #pragma unroll
                 for (int k = 0; k < NT; ++k) {
@@ -295,6 +329,8 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                 }
             }
         }
+        asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+        __syncwarp();
         if constexpr (NT == 1) {
             left -= i1 - i0;
             i0 = 0;
@@ -308,14 +344,14 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
 
 template <int S, int NT>
 cudaError_t launch(const qsa_page_score_args &a, cudaStream_t s) {
-    constexpr int SMEM = (int)sizeof(Smem<S, NT>), CTAS_PER_SM = NT == 1 ? 5 : 3;
+    constexpr int SMEM = (int)sizeof(Smem<S, NT>), CTAS_PER_SM = S == 1 ? (NT == 1 ? 5 : 3) : NT == 1 ? 3 : 2;  // by shared memory
     cudaError_t e = cudaFuncSetAttribute(page_score_kernel<S, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     const long long tiles = (a.max_pages + TILE - 1) / TILE;
     const int resident = std::max(152 * CTAS_PER_SM / a.n_kv_heads, 1);
     int ranges;
     if (NT == 1) {
-        ranges = (int)std::min<long long>(a.n_tokens * ((tiles + W - 1) / W), resident);
+        ranges = (int)std::min<long long>(a.n_tokens * tiles, resident);
     } else {
         const long long blocks = (a.n_tokens + 4 * NT - 1) / (4 * NT);
         ranges = (int)(blocks * std::max<long long>(std::min<long long>(resident / blocks, (tiles + W - 1) / W), 1));

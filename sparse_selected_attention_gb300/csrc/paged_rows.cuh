@@ -514,6 +514,7 @@ struct Feed {
     int next_trow, next_len, next_sure;
     int slot;                        // this lane's page of the sequence for unit u
     int page;                        // and its table entry
+    int ahead, ahead_t, ahead_u;     // of a list: the entry for the unit after, if it is unit ahead_u of row ahead_t
 };
 
 // WHOLE_ROWS: no row is shared out.
@@ -567,6 +568,7 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
     f.left = left - (f.end - u0);
     f.u = u0 + warp;
     f.next_len = f.next_trow = f.next_sure = 0;
+    f.ahead_t = -1;
     auto peek = [&] {
         if (f.left > 0 && f.t + step < a.n_tokens) f.next_len = row_len(a, f.t + step, kvh, f.next_trow, f.next_sure, bad);
     };
@@ -584,9 +586,20 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
         }
         int j = (f.u * UNIT + lane % UNIT) >> page_shift;
         if constexpr (LISTED<A>) {
-            j = f.u < f.end && j < a.width ? __ldg(a.lists + ((size_t)f.t * a.n_kv_heads + kvh) * a.width + j) : -1;
+            // The list's entry and then the table's are two loads one after the other;
+            // the first of them is made a unit before.
+            auto entry = [&](int t, int u) {
+                const int i = (u * UNIT + lane % UNIT) >> page_shift;
+                return i < a.width ? __ldg(a.lists + ((size_t)t * a.n_kv_heads + kvh) * a.width + i) : -1;
+            };
+            const bool known = f.ahead_t == f.t && f.ahead_u == f.u;
+            j = f.u >= f.end ? -1 : known ? f.ahead : entry(f.t, f.u);
             bad |= j < -1 || j >= a.max_pages;
             f.slot = j < a.max_pages ? j : -1;
+            const bool same = f.u + W < f.end;
+            f.ahead_t = same ? f.t : f.t + step;
+            f.ahead_u = same ? f.u + W : warp;
+            if (same || (f.left > 0 && f.ahead_t < a.n_tokens)) f.ahead = entry(f.ahead_t, f.ahead_u);
         }
         f.page = f.u < f.end && j >= 0 && j < a.max_pages ? __ldg(a.page_table + (size_t)f.trow * a.max_pages + j) : -1;
     };
@@ -853,6 +866,63 @@ cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t 
     return encode_boxes(map, a, codes, std::min(a.page_size, Shape<S>::UNIT));
 }
 
+// Joins the partials of a row that spans CTAs, where there are no groups: part p of the
+// one that starts in CTA x is slot 1 of that CTA, then slot 0 of the next ones of its
+// KV head.  A block takes one head of it; few rows have many parts, which G sets of
+// threads share.  (A list of the CTAs in which such rows start, and blocks that go
+// round over it, took 11 us where this takes 5: 244 rows of 2 K cells.)
+template <int S, int G>
+__global__ void __launch_bounds__(64 * S * G) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
+    constexpr int D = 128 * S, LANES = D / 2;
+    __shared__ float2 so[G][LANES];
+    __shared__ float sl[G];
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    const Work work(from.ws, from.cap, from.rows);
+    const int x = blockIdx.x, h = blockIdx.y, d = threadIdx.x % LANES * 2, set = threadIdx.x / LANES;
+    const Part part = work.part[x];
+    if (part.row < 0) return;
+    auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * from.rows + h; };
+    float top = -CUDART_INF_F, l = 0.0f;
+#pragma unroll 4
+    for (int p = 0; p < part.n; ++p) top = fmaxf(top, work.ml[slot(p) * 2]);
+    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+    for (int p = set; p < part.n; p += G) {
+        const float2 ml = reinterpret_cast<const float2 *>(work.ml)[slot(p)];
+        const float w = ml.x == -CUDART_INF_F ? 0.0f : exp2f(ml.x - top);
+        l = fmaf(w, ml.y, l);
+        o = __ffma2_rn(make_float2(w, w), *reinterpret_cast<const float2 *>(work.o + slot(p) * D + d), o);
+    }
+    if constexpr (G > 1) {
+        so[set][d / 2] = o;
+        if (d == 0) sl[set] = l;
+        __syncthreads();
+        if (set) return;
+#pragma unroll
+        for (int i = 1; i < G; ++i) {
+            o = __fadd2_rn(o, so[i][d / 2]);
+            l += sl[i];
+        }
+    }
+    const float inv = top == -CUDART_INF_F ? 0.0f : 1.0f / l;
+    const size_t row = (size_t)part.row * a.n_q_heads + (size_t)(x % a.n_kv_heads) * from.rows + h;
+    if (d == 0 && a.lse) a.lse[row] = lse_of(top, l);
+    if (!QSA_IN(row * D + d + 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
+    float2 y = make_float2(o.x * inv, o.y * inv);
+    if (a.gate) {
+        const float2 gate = __ldg(reinterpret_cast<const float2 *>(a.gate + row * D + d));
+        y = make_float2(gated(y.x, gate.x), gated(y.y, gate.y));
+    }
+    store_out(a, row * D + d, y);
+}
+template <int S>
+cudaError_t launch_rows_join(const qsa_paged_attn_args &a, const Joined &from, cudaStream_t s) {
+    const dim3 grid(from.ctas, from.rows);
+    return (long long)a.n_tokens * a.n_kv_heads < 76 ? launch_dependent(paged_rows_join_kernel<S, 4>, grid, dim3(256 * S), 0, s, a, from)
+                                                     : launch_dependent(paged_rows_join_kernel<S, 1>, grid, dim3(64 * S), 0, s, a, from);
+}
+
 // A call.  cells: the most that a row can go through.
 template <int S, class A>
 cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
@@ -882,6 +952,7 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, NW>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S, NW>), s, a, kmap, vmap, block);
     if (e != cudaSuccess || whole) return e;
+    if constexpr (LISTED<A> || TREE<A>) return launch_rows_join<S>(a, Joined{a.workspace, MAX_CTAS, per, grid}, s);
     const Joined one{a.workspace, MAX_CTAS, per, grid};
     Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};
     if constexpr (!LISTED<A> && !TREE<A>)

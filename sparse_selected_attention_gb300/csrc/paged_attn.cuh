@@ -16,9 +16,17 @@ namespace qsa {
 
 // What a row of q attends to.  qsa_paged_attn_args alone: all cells of its sequence
 // up to its length.
+// What a group of listed rows goes through: the pages that any of them lists, in order.
+// By KV head and the group's first row.
+struct Union {
+    uint2 *unit;  // [n_kv_heads][n_tokens][width]: a page of the sequence, and by bit the rows that list it; null: no groups
+    int *page;    // its place in the pool, -1 outside
+    int *size;    // [n_kv_heads][n_tokens]: rows << SIZE_BITS | pages (SIZE_MASK: not to be taken), or 0: no group starts
+};
 struct ListedArgs : qsa_paged_attn_args {  // cells of listed pages, a list per KV head
     const int32_t *lists, *counts;         // [n_tokens][n_kv_heads][width], [n_tokens][n_kv_heads]
     int width;
+    Union shared;
 };
 struct TreeArgs : qsa_paged_attn_args {  // cells up to seq_lens, and those that bits say after them
     const uint32_t *mask;                // [n_tokens][words]
@@ -144,6 +152,26 @@ template <class A>
 constexpr bool LISTED = std::is_same<A, ListedArgs>::value;
 template <class A>
 constexpr bool TREE = std::is_same<A, TreeArgs>::value;
+
+// Groups of listed rows: those of one sequence of every group_tokens rows.  As with
+// whole sequences, a KV head's rows are taken all by groups or all one by one.
+constexpr int SIZE_BITS = 20, SIZE_MASK = (1 << SIZE_BITS) - 1;
+template <class A>
+__host__ __device__ constexpr int group_tokens(int per) {
+    return LISTED<A> && GROUP_ROWS / per > 32 ? 32 : GROUP_ROWS / per;
+}
+// What the group that starts at row t saves, in tenths of a unit, if each row's units
+// are counted as they are met.
+constexpr int TILE_COST = 83, GROUP_COST = 270, CALL_COST = 44000;
+template <int S>
+__device__ __forceinline__ long long saved_by(const ListedArgs &a, int kvh, int t, int units) {
+    const int size = __ldcg(a.shared.size + (size_t)kvh * a.n_tokens + t), pages = size & SIZE_MASK;
+    if (!size) return 10ll * units;
+    if (pages == SIZE_MASK) return -(1ll << 40);
+    constexpr int N = 128 / S;
+    return 10ll * units - GROUP_COST - (long long)TILE_COST * max((pages * a.page_size + N - 1) / N, 1);
+}
+__device__ __forceinline__ bool saves_enough(const ListedArgs &a, long long saved) { return saved * a.n_kv_heads > CALL_COST; }
 
 // Row t's table row (0 if it is out of range) and seq_lens entry, cut to its range
 // (0 with a table row out of range).

@@ -157,7 +157,9 @@ __device__ __forceinline__ bool find_start(const A &a, Smem<S, NW> &sh, int kvh,
         mine += u;
         padded += pad(u);
         most = max(most, u);
-        if (block && group_start(a.rows, t, block) == t) {
+        if constexpr (LISTED<A>) {
+            if (block) together += saved_by<S>(a, kvh, t, u);
+        } else if (block && group_start(a.rows, t, block) == t) {
             int longest = u;
             const int end = group_end(a, t, block), same = __ldg(a.rows + t);
             for (int i = t + 1; i < end && __ldg(a.rows + i) == same; ++i) longest = max(longest, units_of<S>(row_len(a, i, kvh, row, bad)));
@@ -196,7 +198,11 @@ __device__ __forceinline__ bool find_start(const A &a, Smem<S, NW> &sh, int kvh,
         total_padded += sh.padded[w];
         groups += sh.together[w];
     }
-    if (block && take_groups<S>(a, total, groups, true)) return false;
+    if constexpr (LISTED<A>) {
+        if (block && saves_enough(a, groups)) return false;
+    } else if (block && take_groups<S>(a, total, groups, true)) {
+        return false;
+    }
     before += s - mine;
     before_padded += sp - padded;
     const long long per = (total + ranges - 1) / ranges;
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
                 return i < a.width ? __ldg(a.lists + ((size_t)t * a.n_kv_heads + kvh) * a.width + i) : -1;
             };
             const bool known = f.ahead_t == f.t && f.ahead_u == f.u;
-            j = f.u >= f.end ? -1 : known ? f.ahead : entry(f.t, f.u);
+            j = f.u >= f.end || f.u * UNIT + lane % UNIT >= f.len ? -1 : known ? f.ahead : entry(f.t, f.u);
             bad |= j < -1 || j >= a.max_pages;
             f.slot = j < a.max_pages ? j : -1;
             const bool same = f.u + W < f.end;
@@ -923,6 +929,14 @@ cudaError_t launch_rows_join(const qsa_paged_attn_args &a, const Joined &from, c
                                                      : launch_dependent(paged_rows_join_kernel<S, 1>, grid, dim3(64 * S), 0, s, a, from);
 }
 
+// Whether rows of up to `cells` cells are shared out over CTAs, not taken whole: if the
+// table can hold longer ones than WHOLE units, and there are fewer KV heads than CTAs
+// (else there may also be more CTAs than the workspace has places for).
+template <int S>
+bool shared_out(const qsa_paged_attn_args &a, long long cells) {
+    return cells > WHOLE * Shape<S>::UNIT && MAX_CTAS / a.n_kv_heads > 1;
+}
+
 // A call.  cells: the most that a row can go through.
 template <int S, class A>
 cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
@@ -931,16 +945,18 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     cudaError_t e = encode<S>(kmap, a, a.kq);
     if (e == cudaSuccess) e = encode<S>(vmap, a, a.vq);
     if (e != cudaSuccess) return e;
-    // A share per resident CTA.  Whole rows, and no join, where the table
-    // cannot hold longer ones than WHOLE units, or where there are as many KV
-    // heads as CTAs (then there may also be more CTAs than the workspace has
-    // places for).
+    // A share per resident CTA; whole rows, and no join, where they are not shared out.
     const long long units = (cells + UNIT - 1) / UNIT;
     const int resident = std::max(MAX_CTAS / a.n_kv_heads, 1);
-    const bool whole = units <= WHOLE || resident == 1;
+    const bool whole = !shared_out<S>(a, cells);
     const long long most = whole ? a.n_tokens : a.n_tokens * ((units + MIN_SHARE - 1) / MIN_SHARE);
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, block = !LISTED<A> && !TREE<A> && !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
+    const int per = a.n_q_heads / a.n_kv_heads;
+    int block = 0;
+    if constexpr (LISTED<A>)
+        block = a.shared.unit ? group_tokens<A>(per) : 0;
+    else if constexpr (!TREE<A>)
+        block = !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
     if (whole && units * UNIT <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
         const int small = (int)std::min<long long>(a.n_tokens, std::max(152 * SMALL_PER_SM / a.n_kv_heads, 1));
         e = cudaFuncSetAttribute(paged_attn_kernel<S, 1, true, A>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, 1>));

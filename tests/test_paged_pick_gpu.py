@@ -426,6 +426,165 @@ def test_sparse_bad_inputs(cuda_device):
     assert both(rows=[0, 4, -1, 3]) == po.BAD_ID
 
 
+def alike_lists(rng, lens, rows, hkv, page, width, most, spread=0.3):
+    """Lists of up to `most` pages by scores that the tokens of a sequence mostly share, the first and the last page among them."""
+    have = -(-max(lens) // page)
+    base = rng.standard_normal((max(rows) + 1, hkv, have))
+    pages, counts = np.full((len(lens), hkv, width), -1, np.int32), np.zeros((len(lens), hkv), np.int32)
+    for t, (n, r) in enumerate(zip(lens, rows)):
+        own = -(-n // page)
+        for h in range(hkv):
+            x = (base[r, h] + spread * rng.standard_normal(have))[:own]
+            if own:
+                x[[0, -1]] = 99.0
+            k = min(own, most)
+            pages[t, h, :k], counts[t, h] = np.sort(np.argsort(-x)[:k]), k
+    return pages, counts
+
+
+def alike(rng, runs, base, page, hkv, d, width, most, seed, spread=0.3):
+    """Pool, table, lengths, rows and lists: runs[s] tokens of sequence s, of base cells and on."""
+    rows = [s for s, n in enumerate(runs) for _ in range(n)]
+    lens = [base + 37 * s + i for s, n in enumerate(runs) for i in range(n)]
+    table, pages = shuffled_table([base + 37 * s + n for s, n in enumerate(runs)], page, 3, rng)
+    lists, counts = alike_lists(rng, lens, rows, hkv, page, width, most, spread)
+    return make_pool(pages, page, hkv, d, seed=seed), table, lens, rows, lists, counts
+
+
+def sparse_workspace(hq, hkv, d):
+    return torch.full((qsa.qsa_paged_sparse_attn_workspace_bytes(hq, hkv, d),), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def taken_together(ws):
+    """Whether a call on long rows took them by groups: then no row is shared out one by one."""
+    return not bool((ws[: 304 * 16].view(torch.int32)[::4] >= 0).any())
+
+
+@pytest.mark.parametrize("otype", [F16, BF16])
+@pytest.mark.parametrize("d,hq,hkv,page,runs,base,most", [
+    (128, 12, 1, 64, [130], 9000, 40), (128, 12, 1, 64, [77, 40, 1, 9, 60], 5000, 33), (128, 32, 8, 32, [70], 2500, 40),
+    (128, 16, 2, 16, [100, 95], 4000, 100), (128, 2, 2, 256, [61], 9000, 30), (256, 24, 2, 16, [80], 4000, 100),
+    (256, 16, 1, 128, [90, 33], 9000, 30), (256, 5, 5, 64, [75], 3000, 21), (128, 8, 1, 128, [200], 300, 3), (128, 12, 1, 64, [190], 3, 99)])
+def test_sparse_alike_lists_taken_together(cuda_device, d, hq, hkv, page, runs, base, most, otype):
+    rng = np.random.default_rng(most)
+    pool, table, lens, rows, lists, counts = alike(rng, runs, base, page, hkv, d, most + 4, most, 37)
+    ws = sparse_workspace(hq, hkv, d)
+    gate = rng.standard_normal((len(rows), hq, d)).astype(np.float32) if otype == F16 else None
+    check_sparse(rng.standard_normal((len(rows), hq, d)), pool, table, lens, lists, counts, rows=rows, otype=otype, gate=gate, ws=ws)
+    assert taken_together(ws)  # or rows so short that none is shared out
+
+
+@pytest.mark.parametrize("d,hq,hkv,page", [(128, 12, 1, 64), (256, 24, 2, 16)])
+def test_sparse_groups_with_gaps_ends_and_bad_inputs(cuda_device, d, hq, hkv, page):
+    """Rows that see nothing, lists in any order with gaps, counts of junk, tables and rows out of range, in groups."""
+    rng = np.random.default_rng(38)
+    n, most = 190, 2048 // page
+    pool, table, lens, rows, lists, counts = alike(rng, [n], 4000, page, hkv, d, most + 3, most, 38)
+    lists[:, :, most:] = 10 ** 6  # past the counts
+    for t in range(n):
+        if t % 3 == 0:
+            lists[t, :, :most] = lists[t, :, rng.permutation(most)].T
+        if t % 4 == 1:
+            lists[t, :, rng.integers(0, most, 5)] = -1
+    lens[3], lens[20], lens[21], lens[40], lens[41] = 0, 1, page, 17, 1000
+    counts[5], counts[6], counts[7, 0] = 0, 1, 3
+    q = rng.standard_normal((n, hq, d))
+
+    def run(want_err, lists=lists, counts=counts, table=table, lens=lens, rows=rows, together=True, **kw):
+        ws = sparse_workspace(hq, hkv, d)
+        check_sparse(q, pool, table, lens, lists, counts, rows=rows, ws=ws, **kw)
+        assert po.sparse_cells(table, lens, lists, counts, page, pool[0].shape[0], rows)[1] == want_err
+        assert taken_together(ws) == together
+
+    run(0)
+    run(0, scale=-0.15)
+    run(0, scale=0.0, otype=BF16)
+    x = lists.copy()
+    x[9, 0, 2], x[10, hkv - 1, 0], x[11, 0, 1], x[12, 0, 4] = table.shape[1], -2, 2 ** 31 - 1, -2 ** 31
+    run(po.BAD_ID, lists=x)
+    x = counts.copy()
+    x[30], x[31] = -1, 0
+    run(po.BAD_ID, counts=x)
+    x = table.copy()
+    x[0, lists[50, 0, 3]], x[0, 0] = pool[0].shape[0], -1
+    run(po.BAD_ID, table=x)
+    x = list(lens)
+    x[60] = -5
+    run(po.BAD_ID, lens=x)
+    x = list(rows)
+    x[70], x[80] = 1, -1
+    run(po.BAD_ID, rows=x)
+    # A page that a list holds twice counts twice: then rows go one by one, all of that KV head's.
+    x = lists.copy()
+    x[2, :, 1] = x[2, :, 0]
+    run(0, lists=x, together=False)
+
+
+def test_sparse_groups_are_left_where_they_save_nothing(cuda_device):
+    rng = np.random.default_rng(39)
+    pool, table, lens, rows, lists, counts = alike(rng, [100], 30000, 64, 1, 128, 32, 32, 39, spread=50.0)
+    ws = sparse_workspace(12, 1, 128)
+    check_sparse(rng.standard_normal((100, 12, 128)), pool, table, lens, lists, counts, rows=rows, ws=ws)
+    assert not taken_together(ws)
+    rows = [i % 10 for i in range(100)]
+    table = np.repeat(table, 10, 0)
+    ws = sparse_workspace(12, 1, 128)
+    check_sparse(rng.standard_normal((100, 12, 128)), pool, table, lens, lists, counts, rows=rows, ws=ws)
+    assert not taken_together(ws)
+
+
+def test_sparse_junk_past_the_counts(cuda_device):
+    rng = np.random.default_rng(40)
+    lens = [3000, 20, 700]
+    table, pages = shuffled_table(lens, 16, 3, rng)
+    pool = make_pool(pages, 16, 1, 128, seed=40)
+    lists, counts = random_lists(rng, lens, 1, 16, 80, 71)
+    for t in range(3):
+        lists[t, 0, counts[t, 0]:] = 10 ** 6 if t else -9
+    check_sparse(rng.standard_normal((3, 12, 128)), pool, table, lens, lists, counts)
+
+
+@pytest.mark.parametrize("d,page,otype", [(128, 64, F16), (128, 16, BF16), (256, 32, F16)])
+def test_sparse_groups_nan_scales_and_queries_reach_only_rows_that_see_them(cuda_device, d, page, otype):
+    rng = np.random.default_rng(41)
+    n, hq, hkv, most = 96, 24, 2, 2560 // page
+    pool, table, lens, rows, lists, counts = alike(rng, [n], 6000, page, hkv, d, most, most, 41)
+    counts[17] = 0
+    q = rng.standard_normal((n, hq, d)).astype(np.float32)
+
+    def run(p, q=q):
+        ws = sparse_workspace(hq, hkv, d)
+        qd = dev(q).to(otype)
+        out, lse, err = torch.empty_like(qd), torch.empty(n, hq, device="cuda"), err_word()
+        qsa.qsa_paged_sparse_attn(qd, *[dev(x) for x in p], dev(table), i32(lens), dev(lists), dev(counts), out, ws, rows=i32(rows), lse=lse,
+                                  err=err)
+        assert taken_together(ws) and not int(err.item())
+        return out, lse
+
+    want = run(pool)
+    lists_some = [j for j in range(lens[0] // page) if 3 < sum(j in lists[t, 1, :counts[t, 1]] for t in range(n)) < n - 10]
+    heads = torch.arange(hq, device="cuda") // (hq // hkv) == 1
+    for j, part, value in ((lists_some[0], 2, np.inf), (lists_some[1], 3, np.nan), (lists_some[-1], 3, np.inf), (lists_some[-2], 2, np.nan)):
+        p = [x.copy() for x in pool]
+        p[part][table[0, j], 5, 1, 1] = value
+        out, lse = run(p)
+        hit = torch.tensor([j in lists[t, 1, :counts[t, 1]] for t in range(n)], device="cuda")
+        assert hit.any() and not hit.all()
+        assert torch.equal(out[:, ~heads], want[0][:, ~heads])
+        # Their tile's powers of two may be others without that scale.
+        torch.testing.assert_close(out[~hit].float(), want[0][~hit].float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+        torch.testing.assert_close(lse[~hit], want[1][~hit], rtol=2.0 ** -18, atol=2.0 ** -16)
+        got = out[hit][:, heads]
+        assert not torch.isfinite(got if part == 2 else got[..., d // 4:d // 2]).any()
+    x = q.copy()
+    x[17], x[40, 3] = np.nan, np.inf
+    out, lse = run(pool, x)
+    assert not out[17].any() and torch.isneginf(lse[17]).all() and not torch.isfinite(out[40, 3]).any()
+    rest = torch.ones(n, hq, dtype=torch.bool, device="cuda")
+    rest[17], rest[40, 3] = False, False
+    assert torch.equal(out[rest], want[0][rest]) and torch.equal(lse[rest], want[1][rest])
+
+
 def check_tree(q, pool, table, prefix, mask, **kw):
     cells, werr = po.tree_cells(table, prefix, mask, pool[0].shape[2], pool[0].shape[1], pool[0].shape[0], kw.get("rows"))
     return check_cells("qsa_paged_tree_attn", q, pool, (dev(table), i32(prefix), dev(mask)), cells, werr, **kw)
@@ -552,6 +711,33 @@ def test_nan_and_inf_scales_reach_only_rows_that_see_them(cuda_device, together)
             rest = torch.ones(d, dtype=torch.bool, device="cuda")
             rest[d // 4:d // 2] = False
             assert torch.isfinite(got[..., rest]).all()
+
+
+@pytest.mark.parametrize("d,hq,hkv", [(128, 16, 4), (256, 16, 2)])
+def test_tree_of_many_infinite_and_nan_v_scales(cuda_device, d, hq, hkv):
+    """One half of a tile's cells is then slower than the other, over many tiles in a row."""
+    rng = np.random.default_rng(42)
+    pool, table, prefix, mask, rows = trees(rng, [9000], [24], 64, hkv, d, 42)
+    q = dev(rng.standard_normal((24, hq, d)).astype(np.float16))
+
+    def run(p):
+        ws = torch.empty(qsa.qsa_paged_tree_attn_workspace_bytes(hq, hkv, d), dtype=torch.uint8, device="cuda")
+        out, lse, err = torch.empty_like(q), torch.empty(24, hq, device="cuda"), err_word()
+        qsa.qsa_paged_tree_attn(q, *[dev(x) for x in p], dev(table), i32(prefix), dev(mask), out, ws, rows=i32(rows), lse=lse, err=err)
+        assert int(err.item()) == 0
+        return out, lse
+
+    want, wlse = run(pool)
+    for offset in (0, 40, 64, 100):
+        p = [x.copy() for x in pool]
+        for c in range(offset, 9000, 128):
+            p[3][table[0, c // 64], c % 64, :, 2] = (np.nan, np.inf, -np.inf)[c // 128 % 3]
+        out, lse = run(p)
+        quarter = slice(d // 2, 3 * d // 4)
+        assert torch.isnan(out[..., quarter]).all()
+        out[..., quarter] = want[..., quarter]
+        torch.testing.assert_close(out.float(), want.float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+        torch.testing.assert_close(lse, wlse, rtol=2.0 ** -18, atol=2.0 ** -16)
 
 
 def test_sparse_nan_scales_reach_only_their_lists(cuda_device):

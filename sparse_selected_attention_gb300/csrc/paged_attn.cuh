@@ -22,6 +22,7 @@ struct Union {
     uint2 *unit;  // [n_kv_heads][n_tokens][width]: a page of the sequence, and by bit the rows that list it; null: no groups
     int *page;    // its place in the pool, -1 outside
     int *size;    // [n_kv_heads][n_tokens]: rows << SIZE_BITS | pages (SIZE_MASK: not to be taken), or 0: no group starts
+    int *taken;   // [n_kv_heads]: whether groups are taken, as the kernel that takes them found
 };
 struct ListedArgs : qsa_paged_attn_args {  // cells of listed pages, a list per KV head
     const int32_t *lists, *counts;         // [n_tokens][n_kv_heads][width], [n_tokens][n_kv_heads]

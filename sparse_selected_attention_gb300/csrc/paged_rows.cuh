@@ -157,9 +157,7 @@ __device__ __forceinline__ bool find_start(const A &a, Smem<S, NW> &sh, int kvh,
         mine += u;
         padded += pad(u);
         most = max(most, u);
-        if constexpr (LISTED<A>) {
-            if (block) together += saved_by<S>(a, kvh, t, u);
-        } else if (block && group_start(a.rows, t, block) == t) {
+        if (block && group_start(a.rows, t, block) == t) {
             int longest = u;
             const int end = group_end(a, t, block), same = __ldg(a.rows + t);
             for (int i = t + 1; i < end && __ldg(a.rows + i) == same; ++i) longest = max(longest, units_of<S>(row_len(a, i, kvh, row, bad)));
@@ -198,11 +196,7 @@ __device__ __forceinline__ bool find_start(const A &a, Smem<S, NW> &sh, int kvh,
         total_padded += sh.padded[w];
         groups += sh.together[w];
     }
-    if constexpr (LISTED<A>) {
-        if (block && saves_enough(a, groups)) return false;
-    } else if (block && take_groups<S>(a, total, groups, true)) {
-        return false;
-    }
+    if (block && take_groups<S>(a, total, groups, true)) return false;
     before += s - mine;
     before_padded += sp - padded;
     const long long per = (total + ranges - 1) / ranges;
@@ -546,7 +540,8 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
     // rows every ranges-th from row `range`.
     int share = 0, t = range, u0 = 0, left = 0x7fffffff;
     bool none = false;
-    if constexpr (!WHOLE_ROWS) none = !find_start<S>(a, sh, kvh, range, ranges, block, share);
+    if constexpr (LISTED<A> && !WHOLE_ROWS) none = a.shared.taken && __ldcg(a.shared.taken + kvh);
+    if constexpr (!WHOLE_ROWS) none = none || !find_start<S>(a, sh, kvh, range, ranges, block, share);
     const int step = share ? 1 : ranges;
     if (share) {
         const long long x = (long long)share * range, total = sh.total;
@@ -878,14 +873,12 @@ cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t 
 // threads share.  (A list of the CTAs in which such rows start, and blocks that go
 // round over it, took 11 us where this takes 5: 244 rows of 2 K cells.)
 template <int S, int G>
-__global__ void __launch_bounds__(64 * S * G) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
+__device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Joined &from, int x, int h) {
     constexpr int D = 128 * S, LANES = D / 2;
     __shared__ float2 so[G][LANES];
     __shared__ float sl[G];
-    wait_for_previous_grid();
-    allow_dependent_launch();
     const Work work(from.ws, from.cap, from.rows);
-    const int x = blockIdx.x, h = blockIdx.y, d = threadIdx.x % LANES * 2, set = threadIdx.x / LANES;
+    const int d = threadIdx.x % LANES * 2, set = threadIdx.x / LANES;
     const Part part = work.part[x];
     if (part.row < 0) return;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * from.rows + h; };
@@ -922,6 +915,12 @@ __global__ void __launch_bounds__(64 * S * G) paged_rows_join_kernel(const qsa_p
     }
     store_out(a, row * D + d, y);
 }
+template <int S, int G>
+__global__ void __launch_bounds__(64 * S * G) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    rows_join<S, G>(a, from, blockIdx.x, blockIdx.y);
+}
 template <int S>
 cudaError_t launch_rows_join(const qsa_paged_attn_args &a, const Joined &from, cudaStream_t s) {
     const dim3 grid(from.ctas, from.rows);
@@ -953,9 +952,7 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     const int ranges = (int)std::min<long long>(most, resident), grid = ranges * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads;
     int block = 0;
-    if constexpr (LISTED<A>)
-        block = a.shared.unit ? group_tokens<A>(per) : 0;
-    else if constexpr (!TREE<A>)
+    if constexpr (!LISTED<A> && !TREE<A>)
         block = !whole && may_take_groups<S>(a, units, group_block(per)) ? group_block(per) : 0;
     if (whole && units * UNIT <= SMALL && (long long)a.n_tokens * a.n_kv_heads > (units > 2 ? 2 : 1) * MAX_CTAS) {
         const int small = (int)std::min<long long>(a.n_tokens, std::max(152 * SMALL_PER_SM / a.n_kv_heads, 1));
@@ -968,6 +965,8 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, NW>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S, NW>), s, a, kmap, vmap, block);
     if (e != cudaSuccess || whole) return e;
+    if constexpr (LISTED<A>)
+        if (a.shared.taken) return cudaSuccess;  // joined with the groups'
     if constexpr (LISTED<A> || TREE<A>) return launch_rows_join<S>(a, Joined{a.workspace, MAX_CTAS, per, grid}, s);
     const Joined one{a.workspace, MAX_CTAS, per, grid};
     Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};

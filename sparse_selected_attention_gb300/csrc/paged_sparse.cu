@@ -99,6 +99,19 @@ __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const Li
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
 }
 
+// Joins the partials of both kinds: blocks for the groups', then for the rows'.
+template <int S, bool FINE>
+__global__ void __launch_bounds__(M) listed_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
+    constexpr int CHUNKS = 128 * S / COLS;
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    const int x = blockIdx.x, y = x - ctas * CHUNKS;
+    if (y < 0)
+        tiles_join<S, FINE>(a, ws, x / CHUNKS, x % CHUNKS * COLS);
+    else
+        rows_join<S, 2 / S>(a, rows, y % rows.ctas, y / rows.ctas);
+}
+
 size_t rows_bytes(int per, int head_dim) { return (Work::bytes(MAX_CTAS, per, head_dim) + 255) / 256 * 256; }
 size_t tiles_bytes(int head_dim) { return (Work::bytes(MAX_GROUP_PARTS, GROUP_ROWS, head_dim) + 255) / 256 * 256; }
 
@@ -112,19 +125,27 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
                      heads * a.width <= ENTRIES && bytes <= UNION_BYTES && heads * (cells / Shape<S>::UNIT) * 10 > 2 * CALL_COST;
     if (!may) return launch_rows<S>(a, cells, s);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + rows_bytes(per, a.head_dim), *u = ws + tiles_bytes(a.head_dim);
-    a.shared = Union{reinterpret_cast<uint2 *>(u), reinterpret_cast<int *>(u + ENTRIES * sizeof(uint2)),
-                     reinterpret_cast<int *>(u + ENTRIES * (sizeof(uint2) + sizeof(int)))};
+    int *const ints = reinterpret_cast<int *>(u + ENTRIES * sizeof(uint2));
+    a.shared = Union{reinterpret_cast<uint2 *>(u), ints, ints + ENTRIES, ints + 2 * ENTRIES};
     cudaError_t e = cudaFuncSetAttribute(listed_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, UNION_BYTES);
     if (e == cudaSuccess)
         e = launch_dependent(listed_union_kernel, dim3((a.n_tokens + tokens - 1) / tokens, a.n_kv_heads), dim3(32 * UNION_WARPS), bytes, s, a, tokens, words);
     if (e == cudaSuccess) e = launch_tiles<S>(a, ws, s);
-    return e == cudaSuccess ? launch_rows<S>(a, cells, s) : e;
+    if (e == cudaSuccess) e = launch_rows<S>(a, cells, s);
+    if (e != cudaSuccess) return e;
+    const int ctas = tiles_ctas(a.n_kv_heads);
+    // The rows' kernel has all the CTAs that fit: there is more than enough for them.
+    const Joined rows{a.workspace, MAX_CTAS, per, MAX_CTAS / a.n_kv_heads * a.n_kv_heads};
+    return launch_dependent(a.dtype == QSA_F16 ? listed_join_kernel<S, true> : listed_join_kernel<S, false>,
+                            dim3(ctas * (a.head_dim / COLS) + rows.ctas * per), dim3(M), 0, s, static_cast<const qsa_paged_attn_args &>(a),
+                            static_cast<void *>(ws), ctas, rows);
 }
 
 }  // namespace
 
 size_t paged_sparse_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
-    return rows_bytes(n_q_heads / n_kv_heads, head_dim) + tiles_bytes(head_dim) + ENTRIES * (sizeof(uint2) + 2 * sizeof(int));
+    return rows_bytes(n_q_heads / n_kv_heads, head_dim) + tiles_bytes(head_dim) + ENTRIES * (sizeof(uint2) + 2 * sizeof(int)) +
+           sizeof(int) * MAX_GROUP_PARTS;
 }
 
 cudaError_t launch_paged_sparse_attn(const qsa_paged_sparse_attn_args &x, cudaStream_t s) {

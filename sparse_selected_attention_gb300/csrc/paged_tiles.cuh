@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     int share = 0, left = 0, t = 0;
     TileGroup<S> grp;
     if constexpr (LISTED<A>) {
-        // The groups are there already; whether they are taken is for all of a KV head's
-        // CTAs, here and in the kernel for rows one by one, the same.
+        // The groups are there already; whether they are taken is the same for all of a
+        // KV head's CTAs, and for the kernel of rows one by one, which reads it.
         const int run = (a.n_tokens + THREADS - 1) / THREADS, t0 = min(tid * run, a.n_tokens), t1 = min(t0 + run, a.n_tokens);
         long long tiles = 0, saved = 0;
         int trow, most = 0;
@@ -262,7 +262,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             total += __shfl_xor_sync(0xffffffffu, total, o);
             saved += __shfl_xor_sync(0xffffffffu, saved, o);
         }
-        if (longer && saves_enough(a, saved)) {
+        const bool taken = longer && saves_enough(a, saved);
+        if (range == 0 && tid == 0) a.shared.taken[kvh] = taken;
+        if (taken) {
             share = (int)max((total + ranges - 1) / ranges, 1ll);
             const long long x = (long long)share * range;
             left = (int)max(min((long long)share, total - x), 0ll);
@@ -1018,12 +1020,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 // [D][M].  A block takes COLS dims of all head rows, a thread each.
 constexpr int COLS = 8;
 template <int S, bool FINE>
-__global__ void __launch_bounds__(M) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws) {
+__device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *ws, int x, int d0) {
     constexpr int D = 128 * S;
-    wait_for_previous_grid();
-    allow_dependent_launch();
     const Work work(ws, MAX_GROUP_PARTS, M);
-    const int x = blockIdx.y, m = threadIdx.x, per = a.n_q_heads / a.n_kv_heads, d0 = blockIdx.x * COLS;
+    const int m = threadIdx.x, per = a.n_q_heads / a.n_kv_heads;
     const Part part = work.part[x];
     if (part.row < 0 || m >= part.tokens * per) return;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * M; };
@@ -1052,6 +1052,14 @@ __global__ void __launch_bounds__(M) paged_tiles_join_kernel(const qsa_paged_att
     *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * D + d0) = make_uint4(y[0], y[1], y[2], y[3]);
 }
 
+template <int S, bool FINE>
+__global__ void __launch_bounds__(M) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws) {
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    tiles_join<S, FINE>(a, ws, blockIdx.y, blockIdx.x * COLS);
+}
+inline int tiles_ctas(int n_kv_heads) { return std::max(MAX_GROUP_PARTS / n_kv_heads, 1) * n_kv_heads; }
+
 // Codes [cells, heads, D] in boxes of a tile's cells (or a page's, if fewer) x one
 // head x 128 dims.
 template <int S>
@@ -1059,18 +1067,18 @@ cudaError_t encode_tiles(CUtensorMap &map, const qsa_paged_attn_args &a, const i
     return encode_boxes(map, a, codes, std::min(a.page_size, TileShape<S>::N));
 }
 
-// ws: where the partials go, Work of M rows.
+// ws: where the partials go, Work of M rows.  Those of listed rows are left to be joined.
 template <int S, class A>
 cudaError_t launch_tiles(const A &a, void *ws, cudaStream_t s) {
     CUtensorMap kmap, vmap;
     cudaError_t e = encode_tiles<S>(kmap, a, a.kq);
     if (e == cudaSuccess) e = encode_tiles<S>(vmap, a, a.vq);
     if (e != cudaSuccess) return e;
-    const int ranges = std::max(MAX_GROUP_PARTS / a.n_kv_heads, 1), ctas = ranges * a.n_kv_heads;
+    const int ctas = tiles_ctas(a.n_kv_heads);
     const auto kernel = a.dtype == QSA_F16 ? paged_tiles_kernel<S, true, A> : paged_tiles_kernel<S, false, A>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TileSmem<S>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TileSmem<S>), s, a, kmap, vmap, ws);
-    if (e != cudaSuccess || ranges == 1) return e;
+    if (LISTED<A> || e != cudaSuccess || ctas == a.n_kv_heads) return e;
     return launch_dependent(a.dtype == QSA_F16 ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>, dim3(a.head_dim / COLS, ctas), dim3(M), 0, s,
                             static_cast<const qsa_paged_attn_args &>(a), ws);
 }

@@ -162,8 +162,17 @@ __host__ __device__ constexpr int group_tokens(int per) {
     return LISTED<A> && GROUP_ROWS / per > 32 ? 32 : GROUP_ROWS / per;
 }
 // What the group that starts at row t saves, in tenths of a unit, if each row's units
-// are counted as they are met.
-constexpr int TILE_COST = 83, GROUP_COST = 270, CALL_COST = 44000;
+// are counted as they are met.  A unit costs 1.8 ns, a tile what 8 units cost, a group
+// 45, and the groups' kernels 13,000 more than one launch.  All rows of a KV head list 2 K
+// of 16 K cells; us one by one, and by groups of lists that are more and less alike:
+//   12/1 heads of 128, 256 rows:  16 K units 40;  576 tiles 43, 988 50, 1583 59
+//                     1024 rows:  66 K units 125;  2298 tiles 70, 3941 92, 6329 128
+//   48/4 heads of 128, 256 rows:  66 K units 128;  2152 tiles 72, 3596 92, 6063 125
+//   32/8 heads of 128, 64 rows:   33 K units 68;  352 tiles 40, 687 48, 1312 58, 1908 68
+//                      256 rows:  131 K units 234;  1419 tiles 58, 2778 81, 7648 151
+//   16/1 heads of 256, 256 rows:  33 K units 72;  1189 tiles 55, 1989 67, 3407 84
+//                     1024 rows:  131 K units 241;  4731 tiles 104, 7862 144, 13505 218
+constexpr int TILE_COST = 80, GROUP_COST = 450, CALL_COST = 130000;
 template <int S>
 __device__ __forceinline__ long long saved_by(const ListedArgs &a, int kvh, int t, int units) {
     const int size = __ldcg(a.shared.size + (size_t)kvh * a.n_tokens + t), pages = size & SIZE_MASK;

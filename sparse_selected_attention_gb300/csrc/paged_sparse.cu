@@ -120,9 +120,10 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
     const long long cells = (long long)a.width * a.page_size, heads = (long long)a.n_tokens * a.n_kv_heads;
     const int per = a.n_q_heads / a.n_kv_heads, tokens = group_tokens<ListedArgs>(per), words = (a.max_pages + 31) / 32;
     const size_t bytes = sizeof(unsigned) * tokens * (size_t)(words | 1);
-    // Groups, where they can be had and there is enough to save.
+    // Groups, where they can be had and like lists would save enough: a tile then does
+    // for four units of each of a group's rows.
     const bool may = a.rows && a.n_tokens >= 4 && tokens >= 4 && shared_out<S>(a, cells) && a.n_kv_heads <= MAX_GROUP_PARTS / 2 &&
-                     heads * a.width <= ENTRIES && bytes <= UNION_BYTES && heads * (cells / Shape<S>::UNIT) * 10 > 2 * CALL_COST;
+                     heads * a.width <= ENTRIES && bytes <= UNION_BYTES && heads * (cells / Shape<S>::UNIT) * (tokens - 2) * 10 > (long long)CALL_COST * tokens;
     if (!may) return launch_rows<S>(a, cells, s);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + rows_bytes(per, a.head_dim), *u = ws + tiles_bytes(a.head_dim);
     int *const ints = reinterpret_cast<int *>(u + ENTRIES * sizeof(uint2));

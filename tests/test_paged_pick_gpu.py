@@ -462,9 +462,9 @@ def taken_together(ws):
 
 @pytest.mark.parametrize("otype", [F16, BF16])
 @pytest.mark.parametrize("d,hq,hkv,page,runs,base,most", [
-    (128, 12, 1, 64, [130], 9000, 40), (128, 12, 1, 64, [77, 40, 1, 9, 60], 5000, 33), (128, 32, 8, 32, [70], 2500, 40),
-    (128, 16, 2, 16, [100, 95], 4000, 100), (128, 2, 2, 256, [61], 9000, 30), (256, 24, 2, 16, [80], 4000, 100),
-    (256, 16, 1, 128, [90, 33], 9000, 30), (256, 5, 5, 64, [75], 3000, 21), (128, 8, 1, 128, [200], 300, 3), (128, 12, 1, 64, [190], 3, 99)])
+    (128, 12, 1, 64, [340], 9000, 40), (128, 12, 1, 64, [177, 140, 1, 9, 60], 5000, 40), (128, 32, 8, 32, [90], 2500, 50),
+    (128, 16, 2, 16, [180, 175], 4000, 100), (128, 2, 2, 256, [71], 9000, 30), (256, 24, 2, 16, [130], 4000, 110),
+    (256, 16, 1, 128, [190, 63], 9000, 30), (256, 5, 5, 64, [75], 3000, 40), (128, 8, 1, 128, [200], 300, 3), (128, 12, 1, 64, [190], 3, 99)])
 def test_sparse_alike_lists_taken_together(cuda_device, d, hq, hkv, page, runs, base, most, otype):
     rng = np.random.default_rng(most)
     pool, table, lens, rows, lists, counts = alike(rng, runs, base, page, hkv, d, most + 4, most, 37)
@@ -478,7 +478,7 @@ def test_sparse_alike_lists_taken_together(cuda_device, d, hq, hkv, page, runs, 
 def test_sparse_groups_with_gaps_ends_and_bad_inputs(cuda_device, d, hq, hkv, page):
     """Rows that see nothing, lists in any order with gaps, counts of junk, tables and rows out of range, in groups."""
     rng = np.random.default_rng(38)
-    n, most = 190, 2048 // page
+    n, most = 190 if hkv == 2 else 420, 2048 // page
     pool, table, lens, rows, lists, counts = alike(rng, [n], 4000, page, hkv, d, most + 3, most, 38)
     lists[:, :, most:] = 10 ** 6  # past the counts
     for t in range(n):
@@ -547,7 +547,7 @@ def test_sparse_junk_past_the_counts(cuda_device):
 @pytest.mark.parametrize("d,page,otype", [(128, 64, F16), (128, 16, BF16), (256, 32, F16)])
 def test_sparse_groups_nan_scales_and_queries_reach_only_rows_that_see_them(cuda_device, d, page, otype):
     rng = np.random.default_rng(41)
-    n, hq, hkv, most = 96, 24, 2, 2560 // page
+    n, hq, hkv, most = 200, 24, 2, 2560 // page
     pool, table, lens, rows, lists, counts = alike(rng, [n], 6000, page, hkv, d, most, most, 41)
     counts[17] = 0
     q = rng.standard_normal((n, hq, d)).astype(np.float32)

@@ -734,8 +734,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int kk = k + i, c0 = (i0 + i) * N + half * H;
                 const uint32_t s_col = lane_base + set * N + half * H;
                 wait(sh.info_full[kk % INFOS], kk / INFOS);
-                wait(sh.s_full[set], kk >> 1);
-                fence_after();
                 const Info<N> &f = sh.info[kk % INFOS];
                 constexpr int MY = H / 32;  // parts of the half
                 int flags = 0;
@@ -769,6 +767,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if constexpr (TREE<A>) bits &= tree_bits(a, token, from, sure);
                     return len - from < 32 ? bits & ((1u << (len - from)) - 1) : bits;
                 };
+                wait(sh.s_full[set], kk >> 1);
+                fence_after();
                 // There, -inf takes the place of the scores that it does not see, and
                 // of a marked tile's the scores with their cells' powers of two.
                 if (edge || (flags & MARKED)) {

@@ -70,10 +70,11 @@ __device__ __forceinline__ int scale_exponent(uint2 sc) {
     return max((int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)m))) >> 23) - 127, NO_SCALE);
 }
 
-// The row of q (or, of a group, its first and the number of them) that starts in
-// a CTA's share and spans n CTAs of its KV head; row -1: none.
+// The row of q (or, of a group, its first and the number of them; of a group of
+// head rows their number, from head `head` on) that starts in a CTA's share and
+// spans n CTAs of its KV head; row -1: none.
 struct Part {
-    int row, n, tokens, pad;
+    int row, n, tokens, head;
 };
 
 // Workspace of one kernel: partials of up to `ctas` CTAs, two each (of the row
@@ -157,10 +158,7 @@ constexpr bool TREE = std::is_same<A, TreeArgs>::value;
 // Groups of listed rows: those of one sequence of every group_tokens rows.  As with
 // whole sequences, a KV head's rows are taken all by groups or all one by one.
 constexpr int SIZE_BITS = 20, SIZE_MASK = (1 << SIZE_BITS) - 1;
-template <class A>
-__host__ __device__ constexpr int group_tokens(int per) {
-    return LISTED<A> && GROUP_ROWS / per > 32 ? 32 : GROUP_ROWS / per;
-}
+__host__ __device__ constexpr int group_tokens(int per) { return GROUP_ROWS / per > 32 ? 32 : GROUP_ROWS / per; }
 // What the group that starts at row t saves, in tenths of a unit, if each row's units
 // are counted as they are met.  A unit costs 1.8 ns, a tile what 8 units cost, a group
 // 45, and the groups' kernels 13,000 more than one launch.  All rows of a KV head list 2 K

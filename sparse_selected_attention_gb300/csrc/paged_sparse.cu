@@ -118,7 +118,7 @@ size_t tiles_bytes(int head_dim) { return (Work::bytes(MAX_GROUP_PARTS, GROUP_RO
 template <int S>
 cudaError_t launch(ListedArgs a, cudaStream_t s) {
     const long long cells = (long long)a.width * a.page_size, heads = (long long)a.n_tokens * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, tokens = group_tokens<ListedArgs>(per), words = (a.max_pages + 31) / 32;
+    const int per = a.n_q_heads / a.n_kv_heads, tokens = group_tokens(per), words = (a.max_pages + 31) / 32;
     const size_t bytes = sizeof(unsigned) * tokens * (size_t)(words | 1);
     // Groups, where they can be had and like lists would save enough: a tile then does
     // for four units of each of a group's rows.

@@ -57,14 +57,17 @@ struct TileShape {
     static_assert(O_COL + D <= TMEM_COLS, "tensor memory");
     static constexpr uint32_t IDESC_S = idesc_f16(M, N, false, false), IDESC_O = idesc_f16(M, D, false, true);
 };
-// The group that starts at a token: its tokens (0: none starts), the fewest cells
-// that one sees for certain and the most that one goes through.
+// The group that starts at a token: its head rows (0: none starts), from head `head` of
+// the token on, the fewest cells that a token of it sees for certain and the most that
+// one goes through.  A tree's head rows fill groups one after the other, whatever tokens
+// they are of (63 tokens of 12 heads: six groups; seven of ten whole tokens); a group of
+// listed rows has whole tokens.
 template <int S>
 struct TileGroup {
-    int tokens, least, most, trow;
+    int rows, least, most, trow, head;
     __device__ __forceinline__ int tiles() const {
         constexpr int N = TileShape<S>::N;
-        return tokens ? max((most + N - 1) / N, 1) : 0;
+        return rows ? max((most + N - 1) / N, 1) : 0;
     }
 };
 
@@ -144,18 +147,19 @@ __device__ __forceinline__ uint32_t tile_value(const qsa_paged_attn_args &a, siz
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
-// The group that starts at t, looked up by a warp.
+// The group that starts at head `head` of t, looked up by a warp.
 template <int S, class A>
-__device__ __forceinline__ TileGroup<S> group_at(const A &a, int kvh, int t, int tokens, bool &bad) {
+__device__ __forceinline__ TileGroup<S> group_at(const A &a, int kvh, int t, int head, int per, bool &bad) {
     if constexpr (LISTED<A>) {
         const int size = __ldcg(a.shared.size + (size_t)kvh * a.n_tokens + t);
-        return TileGroup<S>{size >> SIZE_BITS, 0, (size & SIZE_MASK) * a.page_size, 0};
+        return TileGroup<S>{(size >> SIZE_BITS) * per, 0, (size & SIZE_MASK) * a.page_size, 0, 0};
     }
     const int lane = threadIdx.x & 31, row = __ldg(a.rows + t);
-    const int end = min(min(a.n_tokens, t + tokens), (t | (CHUNK - 1)) + 1);
-    TileGroup<S> g{0, 0x7fffffff, 0, row >= 0 && row < a.n_rows ? row : 0};
-    for (bool more = true; more && t + g.tokens < end;) {
-        const int u = t + g.tokens + lane;
+    const int end = min(min(a.n_tokens, t + (head + M + per - 1) / per), (t | (CHUNK - 1)) + 1);
+    TileGroup<S> g{0, 0x7fffffff, 0, row >= 0 && row < a.n_rows ? row : 0, head};
+    int tokens = 0;
+    for (bool more = true; more && t + tokens < end;) {
+        const int u = t + tokens + lane;
         int trow, len = 0, sure = 0;
         const bool same = u < end && __ldg(a.rows + u) == row;
         if (same) len = row_len(a, u, 0, trow, sure, bad);
@@ -165,9 +169,10 @@ __device__ __forceinline__ TileGroup<S> group_at(const A &a, int kvh, int t, int
             g.least = min(g.least, sure);
             g.most = max(g.most, len);
         }
-        g.tokens += k;
+        tokens += k;
         more = k == 32;
     }
+    g.rows = min(tokens * per - head, M);
     g.least = __reduce_min_sync(0xffffffffu, g.least);
     g.most = __reduce_max_sync(0xffffffffu, g.most);
     return g;
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ __align__(1024) uint8_t raw[];
     TileSmem<S> &sh = *reinterpret_cast<TileSmem<S> *>(raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = a.n_q_heads / a.n_kv_heads, page_shift = 31 - __clz(a.page_size), in_group = group_tokens<A>(per);
+    const int per = a.n_q_heads / a.n_kv_heads, page_shift = 31 - __clz(a.page_size);
     const uint32_t per_inv = 65536u / per + 1;
     const int kvh = blockIdx.x % a.n_kv_heads, range = blockIdx.x / a.n_kv_heads, ranges = gridDim.x / a.n_kv_heads;
     volatile int *abort = &sh.abort;
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int trow, most = 0;
 #pragma unroll 1
         for (int u = t0; u < t1; ++u) {
-            const TileGroup<S> g = group_at<S>(a, kvh, u, 0, bad);
+            const TileGroup<S> g = group_at<S>(a, kvh, u, 0, per, bad);
             const int units = units_of<S>(row_len(a, u, kvh, trow, bad));
             most = max(most, units);
             tiles += g.tiles();
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (x >= before && x < before + tiles) {
 #pragma unroll 1
                 for (int u = t0; u < t1; ++u) {
-                    const TileGroup<S> g = group_at<S>(a, kvh, u, 0, bad);
+                    const TileGroup<S> g = group_at<S>(a, kvh, u, 0, per, bad);
                     if (x < before + g.tiles()) {
                         sh.t = u;
                         sh.before = before;
@@ -311,14 +316,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 unsigned mine = starts & (0xffffffffu >> (31 - lane));
                 int w = warp;
                 while (!mine && w > 0) mine = sh.starts[--w];
-                const int start = w * 32 + 31 - __clz(mine), lead = tid - (tid - start) % in_group;
-                if (in) {
+                // The groups of its head rows, one or two, and the tokens that those start at.
+                const int start = w * 32 + 31 - __clz(mine), from = (tid - start) * per, to = from + per;
+                for (int i = from / M; in && i * M < to; ++i) {
+                    const int lead = start + i * M / per;
                     atomicMax(most + lead, len);
                     atomicMin(least + lead, sure);
-                    atomicAdd(size + lead, 1);
+                    atomicAdd(size + lead, min(to, i * M + M) - max(from, i * M));
                 }
                 __syncthreads();
-                const TileGroup<S> g{in && lead == tid ? size[tid] : 0, least[tid], most[tid], trow};
+                const int own = (from + M - 1) / M * M;  // where a group starts, if before `to`
+                const TileGroup<S> g{in && own < to ? size[tid] : 0, least[tid], most[tid], trow, own - from};
                 const int tiles = g.tiles();
                 long long sum = tiles;
 #pragma unroll 1
@@ -377,12 +385,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     for (bool first = true; left > 0; first = false, ++segment) {
         // Segment: tiles i0 .. i1-1 of the group at t.
-        const int tiles = grp.tiles(), i1 = min(tiles, i0 + left), n = i1 - i0, rows = grp.tokens * per;
+        const int tiles = grp.tiles(), i1 = min(tiles, i0 + left), n = i1 - i0, rows = grp.rows;
         const bool whole = n == tiles;
         const size_t at = (size_t)blockIdx.x * 2 + (first && i0 > 0 ? 0 : 1);
-        auto head_row = [&](int m) -> size_t {  // of q: token t + m / per, head kvh per + m % per
-            const int i = (int)((uint32_t)m * per_inv >> 16);  // m / per, m < 128
-            return (size_t)(t + i) * a.n_q_heads + (size_t)kvh * per + (m - i * per);
+        const int head = LISTED<A> ? 0 : grp.head;
+        auto token_of = [&](int m) { return t + (int)((uint32_t)(head + m) * per_inv >> 16); };  // (head + m) / per, below 144
+        auto head_row = [&](int m) -> size_t {  // of q
+            const int u = token_of(m);
+            return (size_t)u * a.n_q_heads + (size_t)kvh * per + (head + m - (u - t) * per);
         };
         const int32_t *tab = a.page_table + (size_t)grp.trow * a.max_pages;
         const int *pages = nullptr;  // of a union, and what tokens see of them
@@ -429,7 +439,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (!good) break;
             }
             if (left > n) {  // the next group, for all
-                const TileGroup<S> g = group_at<S>(a, kvh, t + grp.tokens, in_group, bad);
+                const int end = head + rows;
+                const TileGroup<S> g = group_at<S>(a, kvh, t + end / per, end % per, per, bad);
                 if (lane == 0) sh.next = g;
             }
         } else if (warp >= SCALER) {
@@ -672,7 +683,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int m = tid & (M - 1), wg = tid / M, set = wg >> 1, half = wg & 1;
             const bool mine = m < rows;
             const uint32_t lane_base = tmem + ((uint32_t)(warp % 4 * 32) << 16);
-            const int token = t + (int)((uint32_t)m * per_inv >> 16);
+            const int token = token_of(m);
             int len = 0, sure = 0, tr;
             if (mine) {
                 if constexpr (LISTED<A>)
@@ -982,11 +993,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             ok = false;
             break;
         }
-        if (!whole && i0 == 0) part = Part{t, 1 + (tiles - i1 + share - 1) / share, grp.tokens, 0};
+        if (!whole && i0 == 0) part = Part{t, 1 + (tiles - i1 + share - 1) / share, rows, head};
         left -= n;
         if (left <= 0) break;
         i0 = 0;
-        t += grp.tokens;
+        t += (head + rows) / per;
         grp = sh.next;
         __syncthreads();  // the next is written over
     }
@@ -1025,7 +1036,7 @@ __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *w
     const Work work(ws, MAX_GROUP_PARTS, M);
     const int m = threadIdx.x, per = a.n_q_heads / a.n_kv_heads;
     const Part part = work.part[x];
-    if (part.row < 0 || m >= part.tokens * per) return;
+    if (part.row < 0 || m >= part.tokens) return;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * M; };
     float top = -CUDART_INF_F, l = 0.0f;
     float2 o[COLS / 2];
@@ -1042,8 +1053,8 @@ __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *w
         for (int j = 0; j < COLS / 2; ++j) o[j] = __ffma2_rn(make_float2(w, w), make_float2(src[2 * j * M], src[(2 * j + 1) * M]), o[j]);
     }
     const float inv = top == -CUDART_INF_F ? 0.0f : 1.0f / l;
-    const int i = m / per;
-    const size_t row = (size_t)(part.row + i) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + (m - i * per);
+    const int i = (part.head + m) / per;
+    const size_t row = (size_t)(part.row + i) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + (part.head + m - i * per);
     if (d0 == 0 && a.lse) a.lse[row] = lse_of(top, l);
     if (!QSA_IN(row * D + d0 + COLS - 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
     uint32_t y[4];

@@ -102,12 +102,12 @@ __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const Li
 // Joins the partials of both kinds: blocks for the groups', then for the rows'.
 template <int S, bool FINE>
 __global__ void __launch_bounds__(M) listed_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
-    constexpr int CHUNKS = 128 * S / COLS;
+    constexpr int CHUNKS = 128 * S / COLS<S>;
     wait_for_previous_grid();
     allow_dependent_launch();
     const int x = blockIdx.x, y = x - ctas * CHUNKS;
     if (y < 0)
-        tiles_join<S, FINE>(a, ws, x / CHUNKS, x % CHUNKS * COLS);
+        tiles_join<S, FINE>(a, ws, x / CHUNKS, x % CHUNKS * COLS<S>);
     else
         rows_join<S, 2 / S>(a, rows, y % rows.ctas, y / rows.ctas);
 }
@@ -138,7 +138,7 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
     // The rows' kernel has all the CTAs that fit: there is more than enough for them.
     const Joined rows{a.workspace, MAX_CTAS, per, MAX_CTAS / a.n_kv_heads * a.n_kv_heads};
     return launch_dependent(a.dtype == QSA_F16 ? listed_join_kernel<S, true> : listed_join_kernel<S, false>,
-                            dim3(ctas * (a.head_dim / COLS) + rows.ctas * per), dim3(M), 0, s, static_cast<const qsa_paged_attn_args &>(a),
+                            dim3(ctas * (a.head_dim / COLS<S>) + rows.ctas * per), dim3(M), 0, s, static_cast<const qsa_paged_attn_args &>(a),
                             static_cast<void *>(ws), ctas, rows);
 }
 

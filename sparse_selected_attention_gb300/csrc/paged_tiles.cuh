@@ -1028,11 +1028,14 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // Joins the partials of a group that spans CTAs: part p of the one that starts in
 // CTA x is slot 1 of that CTA, then slot 0 of the next ones of its KV head, values as
-// [D][M].  A block takes COLS dims of all head rows, a thread each.
-constexpr int COLS = 8;
+// [D][M].  A block takes COLS dims of all head rows, a thread each
+// (four of 256: 128 head rows' partials by 64 blocks; by 32, a row of 30 K cells took 5
+// us more).
+template <int S>
+constexpr int COLS = 8 / S;
 template <int S, bool FINE>
 __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *ws, int x, int d0) {
-    constexpr int D = 128 * S;
+    constexpr int D = 128 * S, COLS = qsa::COLS<S>;
     const Work work(ws, MAX_GROUP_PARTS, M);
     const int m = threadIdx.x, per = a.n_q_heads / a.n_kv_heads;
     const Part part = work.part[x];
@@ -1044,7 +1047,7 @@ __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *w
     for (int j = 0; j < COLS / 2; ++j) o[j] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
     for (int p = 0; p < part.n; ++p) top = fmaxf(top, work.ml[(slot(p) + m) * 2]);
-#pragma unroll 2
+#pragma unroll 1
     for (int p = 0; p < part.n; ++p) {
         const float2 ml = reinterpret_cast<const float2 *>(work.ml)[slot(p) + m];
         const float w = ml.x == -CUDART_INF_F ? 0.0f : exp2f(ml.x - top), *src = work.o + slot(p) * D + (size_t)d0 * M + m;
@@ -1057,17 +1060,21 @@ __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *w
     const size_t row = (size_t)(part.row + i) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + (part.head + m - i * per);
     if (d0 == 0 && a.lse) a.lse[row] = lse_of(top, l);
     if (!QSA_IN(row * D + d0 + COLS - 1, (size_t)a.n_tokens * a.n_q_heads * D)) return;
-    uint32_t y[4];
+    uint32_t y[COLS / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = tile_value<FINE>(a, row * D + d0 + 2 * j, make_float2(o[j].x * inv, o[j].y * inv));
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + row * D + d0) = make_uint4(y[0], y[1], y[2], y[3]);
+    for (int j = 0; j < COLS / 2; ++j) y[j] = tile_value<FINE>(a, row * D + d0 + 2 * j, make_float2(o[j].x * inv, o[j].y * inv));
+    uint16_t *dst = static_cast<uint16_t *>(a.out) + row * D + d0;
+    if constexpr (S == 1)
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+    else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(y[0], y[1]);
 }
 
 template <int S, bool FINE>
 __global__ void __launch_bounds__(M) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws) {
     wait_for_previous_grid();
     allow_dependent_launch();
-    tiles_join<S, FINE>(a, ws, blockIdx.y, blockIdx.x * COLS);
+    tiles_join<S, FINE>(a, ws, blockIdx.y, blockIdx.x * COLS<S>);
 }
 inline int tiles_ctas(int n_kv_heads) { return std::max(MAX_GROUP_PARTS / n_kv_heads, 1) * n_kv_heads; }
 
@@ -1090,7 +1097,7 @@ cudaError_t launch_tiles(const A &a, void *ws, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TileSmem<S>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TileSmem<S>), s, a, kmap, vmap, ws);
     if (LISTED<A> || e != cudaSuccess || ctas == a.n_kv_heads) return e;
-    return launch_dependent(a.dtype == QSA_F16 ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>, dim3(a.head_dim / COLS, ctas), dim3(M), 0, s,
+    return launch_dependent(a.dtype == QSA_F16 ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>, dim3(a.head_dim / COLS<S>, ctas), dim3(M), 0, s,
                             static_cast<const qsa_paged_attn_args &>(a), ws);
 }
 

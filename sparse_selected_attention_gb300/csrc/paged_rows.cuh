@@ -869,18 +869,18 @@ cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t 
 
 // Joins the partials of a row that spans CTAs, where there are no groups: part p of the
 // one that starts in CTA x is slot 1 of that CTA, then slot 0 of the next ones of its
-// KV head.  A block takes one head of it; few rows have many parts, which G sets of
-// threads share.  (A list of the CTAs in which such rows start, and blocks that go
-// round over it, took 11 us where this takes 5: 244 rows of 2 K cells.)
+// KV head.  A block takes its heads, as many as fit; few rows have many parts, which G
+// sets of threads share, and a block for each head.  (Of 244 rows of 2 K cells, cold,
+// blocks that go round over a list of the CTAs in which rows start took 12 us, this 7.)
 template <int S, int G>
-__device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Joined &from, int x, int h) {
+__device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Joined &from, int x, int h, int tid) {
     constexpr int D = 128 * S, LANES = D / 2;
     __shared__ float2 so[G][LANES];
     __shared__ float sl[G];
     const Work work(from.ws, from.cap, from.rows);
-    const int d = threadIdx.x % LANES * 2, set = threadIdx.x / LANES;
+    const int d = tid % LANES * 2, set = tid / LANES;
     const Part part = work.part[x];
-    if (part.row < 0) return;
+    if (part.row < 0 || h >= from.rows) return;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * from.rows + h; };
     float top = -CUDART_INF_F, l = 0.0f;
 #pragma unroll 4
@@ -915,17 +915,21 @@ __device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Jo
     }
     store_out(a, row * D + d, y);
 }
+template <int S>
+constexpr int JOIN_HEADS = 16 / S;  // of a block of 1024 threads
 template <int S, int G>
-__global__ void __launch_bounds__(64 * S * G) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
+__global__ void __launch_bounds__(G == 1 ? 1024 : 64 * S * G) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
     wait_for_previous_grid();
     allow_dependent_launch();
-    rows_join<S, G>(a, from, blockIdx.x, blockIdx.y);
+    const int heads = blockDim.x / (64 * S * G);
+    rows_join<S, G>(a, from, blockIdx.x, blockIdx.y * heads + threadIdx.x / (64 * S * G), threadIdx.x % (64 * S * G));
 }
 template <int S>
 cudaError_t launch_rows_join(const qsa_paged_attn_args &a, const Joined &from, cudaStream_t s) {
-    const dim3 grid(from.ctas, from.rows);
-    return (long long)a.n_tokens * a.n_kv_heads < 76 ? launch_dependent(paged_rows_join_kernel<S, 4>, grid, dim3(256 * S), 0, s, a, from)
-                                                     : launch_dependent(paged_rows_join_kernel<S, 1>, grid, dim3(64 * S), 0, s, a, from);
+    if ((long long)a.n_tokens * a.n_kv_heads < 76)
+        return launch_dependent(paged_rows_join_kernel<S, 4>, dim3(from.ctas, from.rows), dim3(256 * S), 0, s, a, from);
+    const int heads = std::min(from.rows, JOIN_HEADS<S>);
+    return launch_dependent(paged_rows_join_kernel<S, 1>, dim3(from.ctas, (from.rows + heads - 1) / heads), dim3(64 * S * heads), 0, s, a, from);
 }
 
 // Whether rows of up to `cells` cells are shared out over CTAs, not taken whole: if the

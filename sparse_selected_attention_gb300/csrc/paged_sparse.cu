@@ -4,7 +4,12 @@
 // ten of them list a fifth of what they count).  Where that saves enough, rows are
 // taken by groups over the pages that any of a group's rows lists (paged_tiles.cuh),
 // else one by one (paged_rows.cuh).  What the groups go through is found by a kernel
-// before; both kinds then start, and one of them finds that it has nothing to do.
+// before; both kinds then start, and one of them finds that it has nothing to do.  Those
+// tokens, 12/1 heads of 128: 141 us by groups (cold: union 8, groups 132, join 12), 229
+// one by one.  Lists that turn out not to be alike pay 12 us for the attempt.
+//
+// Rows one by one: 61 rows of 2 K cells, 48/4 heads of 128, 146 MB: 46.4 us, 3.1 TB/s,
+// thirteen units a warp between some 20 us of launch, first loads and ends of rows.
 #include "paged_tiles.cuh"
 
 namespace qsa {
@@ -101,15 +106,15 @@ __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const Li
 
 // Joins the partials of both kinds: blocks for the groups', then for the rows'.
 template <int S, bool FINE>
-__global__ void __launch_bounds__(M) listed_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
-    constexpr int CHUNKS = 128 * S / COLS<S>;
+__global__ void __launch_bounds__(M *SLICES) listed_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
+    constexpr int CHUNKS = 128 * S / (COLS<S> * SLICES);
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int x = blockIdx.x, y = x - ctas * CHUNKS;
+    const int x = blockIdx.x, y = x - ctas * CHUNKS, tid = threadIdx.x;
     if (y < 0)
-        tiles_join<S, FINE>(a, ws, x / CHUNKS, x % CHUNKS * COLS<S>);
+        tiles_join<S, FINE>(a, ws, x / CHUNKS, (x % CHUNKS * SLICES + tid / M) * COLS<S>, tid % M);
     else
-        rows_join<S, 2 / S>(a, rows, y % rows.ctas, y / rows.ctas);
+        rows_join<S, 1>(a, rows, y % rows.ctas, y / rows.ctas * JOIN_HEADS<S> + tid / (64 * S), tid % (64 * S));
 }
 
 size_t rows_bytes(int per, int head_dim) { return (Work::bytes(MAX_CTAS, per, head_dim) + 255) / 256 * 256; }
@@ -138,7 +143,7 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
     // The rows' kernel has all the CTAs that fit: there is more than enough for them.
     const Joined rows{a.workspace, MAX_CTAS, per, MAX_CTAS / a.n_kv_heads * a.n_kv_heads};
     return launch_dependent(a.dtype == QSA_F16 ? listed_join_kernel<S, true> : listed_join_kernel<S, false>,
-                            dim3(ctas * (a.head_dim / COLS<S>) + rows.ctas * per), dim3(M), 0, s, static_cast<const qsa_paged_attn_args &>(a),
+                            dim3(ctas * (a.head_dim / (COLS<S> * SLICES)) + rows.ctas * ((per + JOIN_HEADS<S> - 1) / JOIN_HEADS<S>)), dim3(M * SLICES), 0, s, static_cast<const qsa_paged_attn_args &>(a),
                             static_cast<void *>(ws), ctas, rows);
 }
 

@@ -28,6 +28,18 @@
 // scale had set the maximum, where the tile's V scales lie within 2^SPREAD of one
 // another.  Tiles whose scales do not (or K's not within 2^16: rare, by a few odd
 // cells) are marked, and take a power of two per cell.
+//
+// What bounds it.  24 trees of 16 to 32 tokens over up to 8 K cells, 32/8 heads of 128: 127 us,
+// 370 TFLOP/s; 63 tokens over 30 K cells, 24/2 of 256: 101 us, 460 TFLOP/s; 1984 tokens
+// over 2 K listed cells each, 12/1 of 128: 141 us.  Tensor pipe 39 to 42 % busy, issue
+// slots 67 %: a tile of 128 cells takes 4.1 K cycles, of which its products take 2.1 K, the
+// conversion of K 3 K, the softmax of one set 5 K of 8.2 K.  Each role is near its own
+// latency, so that more of one thing brings little.  In the cases' order: 64-cell tiles by
+// four sets 192, 114 and 213 us where two sets took 129, 114 and 149; two warps for the two
+// products 140, 140 and 148; roles that go on to the next segment by themselves 133, 116 and
+// 149; all softmax warps on one tile 125, 117 and 140 where this took 128, 112 and 139 then;
+// unrolled conversion 131, 114 and 145 (129, 112 and 143).  Beginning and end of a share
+// cost 12 us of 100, mostly first fetches of instructions.
 #pragma once
 
 #include "paged_rows.cuh"
@@ -1033,11 +1045,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 // us more).
 template <int S>
 constexpr int COLS = 8 / S;
+constexpr int SLICES = 8;  // of a block
 template <int S, bool FINE>
-__device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *ws, int x, int d0) {
+__device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *ws, int x, int d0, int m) {
     constexpr int D = 128 * S, COLS = qsa::COLS<S>;
     const Work work(ws, MAX_GROUP_PARTS, M);
-    const int m = threadIdx.x, per = a.n_q_heads / a.n_kv_heads;
+    const int per = a.n_q_heads / a.n_kv_heads;
     const Part part = work.part[x];
     if (part.row < 0 || m >= part.tokens) return;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * M; };
@@ -1071,10 +1084,10 @@ __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *w
 }
 
 template <int S, bool FINE>
-__global__ void __launch_bounds__(M) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws) {
+__global__ void __launch_bounds__(M *SLICES) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws) {
     wait_for_previous_grid();
     allow_dependent_launch();
-    tiles_join<S, FINE>(a, ws, blockIdx.y, blockIdx.x * COLS<S>);
+    tiles_join<S, FINE>(a, ws, blockIdx.y, (blockIdx.x * SLICES + threadIdx.x / M) * COLS<S>, threadIdx.x % M);
 }
 inline int tiles_ctas(int n_kv_heads) { return std::max(MAX_GROUP_PARTS / n_kv_heads, 1) * n_kv_heads; }
 
@@ -1097,7 +1110,7 @@ cudaError_t launch_tiles(const A &a, void *ws, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TileSmem<S>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TileSmem<S>), s, a, kmap, vmap, ws);
     if (LISTED<A> || e != cudaSuccess || ctas == a.n_kv_heads) return e;
-    return launch_dependent(a.dtype == QSA_F16 ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>, dim3(a.head_dim / COLS<S>, ctas), dim3(M), 0, s,
+    return launch_dependent(a.dtype == QSA_F16 ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>, dim3(a.head_dim / (COLS<S> * SLICES), ctas), dim3(M * SLICES), 0, s,
                             static_cast<const qsa_paged_attn_args &>(a), ws);
 }
 

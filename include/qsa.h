@@ -654,7 +654,8 @@ typedef struct {
  * node's mask has the bits of itself and of the nodes that lead to it; a row
  * that sees nothing (a padding token: prefix 0, mask 0) gives out = +0 and lse =
  * -inf.  Consecutive rows of one sequence are read together where that saves
- * time.  Otherwise as qsa_paged_attn; a bit at or past max_pages * page_size is
+ * time; without rows each goes by itself (the form for single tokens).
+ * Otherwise as qsa_paged_attn; a bit at or past max_pages * page_size is
  * left out and sets QSA_DEVERR_BAD_ID.
  *
  * prefix_lens int32 [n_tokens]; mask int32 [n_tokens, words], 1 <= words <=

@@ -581,7 +581,8 @@ qsa_status qsa_paged_sparse_attn(const qsa_paged_sparse_attn_args *a, void *stre
 }
 
 size_t qsa_paged_tree_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
-    return qsa_paged_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim);
+    if ((head_dim != 128 && head_dim != 256) || !attn_heads(n_q_heads, n_kv_heads)) return 0;
+    return qsa::paged_tree_attn_workspace_bytes(n_q_heads, n_kv_heads, head_dim);
 }
 
 qsa_status qsa_paged_tree_attn(const qsa_paged_tree_attn_args *a, void *stream) {

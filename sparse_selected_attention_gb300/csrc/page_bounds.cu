@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM) page_bounds_kernel(const
     // This block's pages, of all heads; its warps take the (page, head) pairs in turn.
     int r, at, pages;
     find_share(found, a.n_rows, blockIdx.x, gridDim.x, 1, [&](int i) { return span_of(a, i, bad).n; }, r, at, pages);
-    int left = pages * hkv - (threadIdx.x >> 5);  // pairs from this warp's first on
+    long long left = (long long)pages * hkv - (threadIdx.x >> 5);  // pairs from this warp's first on
     if (left > 0) {
         Span s = span_of(a, r, bad);
         int j = at, head = threadIdx.x >> 5;

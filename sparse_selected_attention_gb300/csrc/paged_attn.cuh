@@ -22,16 +22,17 @@ struct Union {
     uint2 *unit;  // [n_kv_heads][n_tokens][width]: a page of the sequence, and by bit the rows that list it; null: no groups
     int *page;    // its place in the pool, -1 outside
     int *size;    // [n_kv_heads][n_tokens]: rows << SIZE_BITS | pages (SIZE_MASK: not to be taken), or 0: no group starts
-    int *taken;   // [n_kv_heads]: whether groups are taken, as the kernel that takes them found
 };
 struct ListedArgs : qsa_paged_attn_args {  // cells of listed pages, a list per KV head
     const int32_t *lists, *counts;         // [n_tokens][n_kv_heads][width], [n_tokens][n_kv_heads]
     int width;
     Union shared;
+    int *taken;  // [n_kv_heads]: whether groups are taken, as the kernel that takes them found; null: none are
 };
 struct TreeArgs : qsa_paged_attn_args {  // cells up to seq_lens, and those that bits say after them
     const uint32_t *mask;                // [n_tokens][words]
     int words;
+    int *taken;                          // [n_kv_heads], as above
 };
 
 namespace {
@@ -156,11 +157,11 @@ template <class A>
 constexpr bool TREE = std::is_same<A, TreeArgs>::value;
 
 // Groups of listed rows: those of one sequence of every group_tokens rows.  As with
-// whole sequences, a KV head's rows are taken all by groups or all one by one.
+// whole sequences, a KV head's rows are taken all by groups or all one by one, and so
+// are trees'.
 constexpr int SIZE_BITS = 20, SIZE_MASK = (1 << SIZE_BITS) - 1;
 __host__ __device__ constexpr int group_tokens(int per) { return GROUP_ROWS / per > 32 ? 32 : GROUP_ROWS / per; }
-// What the group that starts at row t saves, in tenths of a unit, if each row's units
-// are counted as they are met.  A unit costs 1.8 ns, a tile what 8 units cost, a group
+// What groups save, in tenths of a unit.  A unit costs 1.8 ns, a tile what 8 units cost, a group
 // 45, and the groups' kernels 13,000 more than one launch.  All rows of a KV head list 2 K
 // of 16 K cells; us one by one, and by groups of lists that are more and less alike:
 //   12/1 heads of 128, 256 rows:  16 K units 40;  576 tiles 43, 988 50, 1583 59
@@ -170,16 +171,17 @@ __host__ __device__ constexpr int group_tokens(int per) { return GROUP_ROWS / pe
 //                      256 rows:  131 K units 234;  1419 tiles 58, 2778 81, 7648 151
 //   16/1 heads of 256, 256 rows:  33 K units 72;  1189 tiles 55, 1989 67, 3407 84
 //                     1024 rows:  131 K units 241;  4731 tiles 104, 7862 144, 13505 218
+// Trees of as many tokens in each of so many sequences, us one by one, and together:
+//   12/1 heads of 128, 4 K cells:   61 of 1 29, 52;  61 of 4 51, 53;  61 of 8 89, 54
+//   32/8 heads of 128, 8 K cells:   8 of 1 42, 80;  8 of 4 90, 80;  8 of 8 171, 80
+//                      4 K cells:   61 of 1 114, 252;  61 of 4 305, 253
+//   24/2 heads of 256, 30 K cells:  1 of 2 41, 53;  1 of 8 67, 41;  1 of 16 109, 63
 constexpr int TILE_COST = 80, GROUP_COST = 450, CALL_COST = 130000;
-template <int S>
-__device__ __forceinline__ long long saved_by(const ListedArgs &a, int kvh, int t, int units) {
-    const int size = __ldcg(a.shared.size + (size_t)kvh * a.n_tokens + t), pages = size & SIZE_MASK;
-    if (!size) return 10ll * units;
-    if (pages == SIZE_MASK) return -(1ll << 40);
-    constexpr int N = 128 / S;
-    return 10ll * units - GROUP_COST - (long long)TILE_COST * max((pages * a.page_size + N - 1) / N, 1);
+// Of a row's units and the tiles of the group that starts with it (0: none does).
+__device__ __forceinline__ long long saved_by(int units, int tiles) {
+    return 10ll * units - (tiles ? GROUP_COST + (long long)TILE_COST * tiles : 0ll);
 }
-__device__ __forceinline__ bool saves_enough(const ListedArgs &a, long long saved) { return saved * a.n_kv_heads > CALL_COST; }
+__device__ __forceinline__ bool saves_enough(const qsa_paged_attn_args &a, long long saved) { return saved * a.n_kv_heads > CALL_COST; }
 
 // Row t's table row (0 if it is out of range) and seq_lens entry, cut to its range
 // (0 with a table row out of range).

@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
     // rows every ranges-th from row `range`.
     int share = 0, t = range, u0 = 0, left = 0x7fffffff;
     bool none = false;
-    if constexpr (LISTED<A> && !WHOLE_ROWS) none = a.shared.taken && __ldcg(a.shared.taken + kvh);
+    if constexpr ((LISTED<A> || TREE<A>) && !WHOLE_ROWS) none = a.taken && __ldcg(a.taken + kvh);
     if constexpr (!WHOLE_ROWS) none = none || !find_start<S>(a, sh, kvh, range, ranges, block, share);
     const int step = share ? 1 : ranges;
     if (share) {
@@ -872,38 +872,43 @@ cudaError_t encode(CUtensorMap &map, const qsa_paged_attn_args &a, const int8_t 
 // KV head.  A block takes its heads, as many as fit; few rows have many parts, which G
 // sets of threads share, and a block for each head.  (Of 244 rows of 2 K cells, cold,
 // blocks that go round over a list of the CTAs in which rows start took 12 us, this 7.)
+constexpr int JOIN_THREADS = 1024;
 template <int S, int G>
-__device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Joined &from, int x, int h, int tid) {
+constexpr int JOIN_HEADS = JOIN_THREADS / (64 * S * G);  // of a block, at most
+template <int S, int G>
+__device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Joined &from, int x, int h0) {
     constexpr int D = 128 * S, LANES = D / 2;
-    __shared__ float2 so[G][LANES];
-    __shared__ float sl[G];
+    __shared__ float2 so[G > 1 ? JOIN_HEADS<S, G> : 1][G][LANES];
+    __shared__ float sl[G > 1 ? JOIN_HEADS<S, G> : 1][G];
     const Work work(from.ws, from.cap, from.rows);
-    const int d = tid % LANES * 2, set = tid / LANES;
+    const int tid = threadIdx.x, d = tid % LANES * 2, set = tid / LANES % G, in_block = tid / (LANES * G), h = h0 + in_block;
     const Part part = work.part[x];
-    if (part.row < 0 || h >= from.rows) return;
+    if (part.row < 0) return;
+    const int n = h < from.rows ? part.n : 0;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * from.rows + h; };
     float top = -CUDART_INF_F, l = 0.0f;
 #pragma unroll 4
-    for (int p = 0; p < part.n; ++p) top = fmaxf(top, work.ml[slot(p) * 2]);
+    for (int p = 0; p < n; ++p) top = fmaxf(top, work.ml[slot(p) * 2]);
     float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-    for (int p = set; p < part.n; p += G) {
+    for (int p = set; p < n; p += G) {
         const float2 ml = reinterpret_cast<const float2 *>(work.ml)[slot(p)];
         const float w = ml.x == -CUDART_INF_F ? 0.0f : exp2f(ml.x - top);
         l = fmaf(w, ml.y, l);
         o = __ffma2_rn(make_float2(w, w), *reinterpret_cast<const float2 *>(work.o + slot(p) * D + d), o);
     }
     if constexpr (G > 1) {
-        so[set][d / 2] = o;
-        if (d == 0) sl[set] = l;
+        so[in_block][set][d / 2] = o;
+        if (d == 0) sl[in_block][set] = l;
         __syncthreads();
         if (set) return;
 #pragma unroll
         for (int i = 1; i < G; ++i) {
-            o = __fadd2_rn(o, so[i][d / 2]);
-            l += sl[i];
+            o = __fadd2_rn(o, so[in_block][i][d / 2]);
+            l += sl[in_block][i];
         }
     }
+    if (!n) return;
     const float inv = top == -CUDART_INF_F ? 0.0f : 1.0f / l;
     const size_t row = (size_t)part.row * a.n_q_heads + (size_t)(x % a.n_kv_heads) * from.rows + h;
     if (d == 0 && a.lse) a.lse[row] = lse_of(top, l);
@@ -915,20 +920,17 @@ __device__ __forceinline__ void rows_join(const qsa_paged_attn_args &a, const Jo
     }
     store_out(a, row * D + d, y);
 }
-template <int S>
-constexpr int JOIN_HEADS = 16 / S;  // of a block of 1024 threads
 template <int S, int G>
-__global__ void __launch_bounds__(G == 1 ? 1024 : 64 * S * G) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
+__global__ void __launch_bounds__(JOIN_THREADS) paged_rows_join_kernel(const qsa_paged_attn_args a, const Joined from) {
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int heads = blockDim.x / (64 * S * G);
-    rows_join<S, G>(a, from, blockIdx.x, blockIdx.y * heads + threadIdx.x / (64 * S * G), threadIdx.x % (64 * S * G));
+    rows_join<S, G>(a, from, blockIdx.x, blockIdx.y * (blockDim.x / (64 * S * G)));
 }
 template <int S>
 cudaError_t launch_rows_join(const qsa_paged_attn_args &a, const Joined &from, cudaStream_t s) {
     if ((long long)a.n_tokens * a.n_kv_heads < 76)
         return launch_dependent(paged_rows_join_kernel<S, 4>, dim3(from.ctas, from.rows), dim3(256 * S), 0, s, a, from);
-    const int heads = std::min(from.rows, JOIN_HEADS<S>);
+    const int heads = std::min(from.rows, JOIN_HEADS<S, 1>);
     return launch_dependent(paged_rows_join_kernel<S, 1>, dim3(from.ctas, (from.rows + heads - 1) / heads), dim3(64 * S * heads), 0, s, a, from);
 }
 
@@ -969,8 +971,8 @@ cudaError_t launch_rows(const A &a, long long cells, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem<S, NW>));
     if (e == cudaSuccess) e = launch_dependent(kernel, dim3(grid), dim3(NW * 32), sizeof(Smem<S, NW>), s, a, kmap, vmap, block);
     if (e != cudaSuccess || whole) return e;
-    if constexpr (LISTED<A>)
-        if (a.shared.taken) return cudaSuccess;  // joined with the groups'
+    if constexpr (LISTED<A> || TREE<A>)
+        if (a.taken) return cudaSuccess;  // joined with the groups'
     if constexpr (LISTED<A> || TREE<A>) return launch_rows_join<S>(a, Joined{a.workspace, MAX_CTAS, per, grid}, s);
     const Joined one{a.workspace, MAX_CTAS, per, grid};
     Joined two{static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, per, a.head_dim), MAX_GROUP_PARTS, GROUP_ROWS, 0};

@@ -5,7 +5,7 @@
 // taken by groups over the pages that any of a group's rows lists (paged_tiles.cuh),
 // else one by one (paged_rows.cuh).  What the groups go through is found by a kernel
 // before; both kinds then start, and one of them finds that it has nothing to do.  Those
-// tokens, 12/1 heads of 128: 141 us by groups (cold: union 8, groups 132, join 12), 229
+// tokens, 12/1 heads of 128: 138 us by groups (cold: union 8, groups 132, join 12), 229
 // one by one.  Lists that turn out not to be alike pay 12 us for the attempt.
 //
 // Rows one by one: 61 rows of 2 K cells, 48/4 heads of 128, 146 MB: 46.4 us, 3.1 TB/s,
@@ -104,19 +104,6 @@ __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const Li
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
 }
 
-// Joins the partials of both kinds: blocks for the groups', then for the rows'.
-template <int S, bool FINE>
-__global__ void __launch_bounds__(M *SLICES) listed_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
-    constexpr int CHUNKS = 128 * S / (COLS<S> * SLICES);
-    wait_for_previous_grid();
-    allow_dependent_launch();
-    const int x = blockIdx.x, y = x - ctas * CHUNKS, tid = threadIdx.x;
-    if (y < 0)
-        tiles_join<S, FINE>(a, ws, x / CHUNKS, (x % CHUNKS * SLICES + tid / M) * COLS<S>, tid % M);
-    else
-        rows_join<S, 1>(a, rows, y % rows.ctas, y / rows.ctas * JOIN_HEADS<S> + tid / (64 * S), tid % (64 * S));
-}
-
 size_t rows_bytes(int per, int head_dim) { return (Work::bytes(MAX_CTAS, per, head_dim) + 255) / 256 * 256; }
 size_t tiles_bytes(int head_dim) { return (Work::bytes(MAX_GROUP_PARTS, GROUP_ROWS, head_dim) + 255) / 256 * 256; }
 
@@ -132,19 +119,14 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
     if (!may) return launch_rows<S>(a, cells, s);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + rows_bytes(per, a.head_dim), *u = ws + tiles_bytes(a.head_dim);
     int *const ints = reinterpret_cast<int *>(u + ENTRIES * sizeof(uint2));
-    a.shared = Union{reinterpret_cast<uint2 *>(u), ints, ints + ENTRIES, ints + 2 * ENTRIES};
+    a.shared = Union{reinterpret_cast<uint2 *>(u), ints, ints + ENTRIES};
+    a.taken = ints + 2 * ENTRIES;
     cudaError_t e = cudaFuncSetAttribute(listed_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, UNION_BYTES);
     if (e == cudaSuccess)
         e = launch_dependent(listed_union_kernel, dim3((a.n_tokens + tokens - 1) / tokens, a.n_kv_heads), dim3(32 * UNION_WARPS), bytes, s, a, tokens, words);
     if (e == cudaSuccess) e = launch_tiles<S>(a, ws, s);
     if (e == cudaSuccess) e = launch_rows<S>(a, cells, s);
-    if (e != cudaSuccess) return e;
-    const int ctas = tiles_ctas(a.n_kv_heads);
-    // The rows' kernel has all the CTAs that fit: there is more than enough for them.
-    const Joined rows{a.workspace, MAX_CTAS, per, MAX_CTAS / a.n_kv_heads * a.n_kv_heads};
-    return launch_dependent(a.dtype == QSA_F16 ? listed_join_kernel<S, true> : listed_join_kernel<S, false>,
-                            dim3(ctas * (a.head_dim / (COLS<S> * SLICES)) + rows.ctas * ((per + JOIN_HEADS<S> - 1) / JOIN_HEADS<S>)), dim3(M * SLICES), 0, s, static_cast<const qsa_paged_attn_args &>(a),
-                            static_cast<void *>(ws), ctas, rows);
+    return e == cudaSuccess ? launch_tiles_join<S>(a, ws, true, s) : e;
 }
 
 }  // namespace

@@ -30,8 +30,8 @@
 // cells) are marked, and take a power of two per cell.
 //
 // What bounds it.  24 trees of 16 to 32 tokens over up to 8 K cells, 32/8 heads of 128: 127 us,
-// 370 TFLOP/s; 63 tokens over 30 K cells, 24/2 of 256: 101 us, 460 TFLOP/s; 1984 tokens
-// over 2 K listed cells each, 12/1 of 128: 141 us.  Tensor pipe 39 to 42 % busy, issue
+// 370 TFLOP/s; 63 tokens over 30 K cells, 24/2 of 256: 97 us, 480 TFLOP/s; 1984 tokens
+// over 2 K listed cells each, 12/1 of 128: 138 us.  Tensor pipe 39 to 42 % busy, issue
 // slots 67 %: a tile of 128 cells takes 4.1 K cycles, of which its products take 2.1 K, the
 // conversion of K 3 K, the softmax of one set 5 K of 8.2 K.  Each role is near its own
 // latency, so that more of one thing brings little.  In the cases' order: 64-cell tiles by
@@ -257,7 +257,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int units = units_of<S>(row_len(a, u, kvh, trow, bad));
             most = max(most, units);
             tiles += g.tiles();
-            saved += saved_by<S>(a, kvh, u, units);
+            saved += saved_by(units, g.tiles());
+            if (g.most == SIZE_MASK * a.page_size) saved -= 1ll << 40;
         }
         long long sum = tiles;
 #pragma unroll 1
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             saved += __shfl_xor_sync(0xffffffffu, saved, o);
         }
         const bool taken = longer && saves_enough(a, saved);
-        if (range == 0 && tid == 0) a.shared.taken[kvh] = taken;
+        if (range == 0 && tid == 0) a.taken[kvh] = taken;
         if (taken) {
             share = (int)max((total + ranges - 1) / ranges, 1ll);
             const long long x = (long long)share * range;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
     } else {
         int *srow = reinterpret_cast<int *>(sh.k), *most = srow + CHUNK, *least = most + CHUNK, *size = least + CHUNK;
-        long long total = 0, x = 0, done = 0;
+        long long total = 0, x = 0, done = 0, saved = 0;
 #pragma unroll 1
         for (int pass = 0; pass < 2; ++pass) {  // the tiles; then where the share starts
 #pragma unroll 1
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int own = (from + M - 1) / M * M;  // where a group starts, if before `to`
                 const TileGroup<S> g{in && own < to ? size[tid] : 0, least[tid], most[tid], trow, own - from};
                 const int tiles = g.tiles();
+                if (!pass && in) saved += saved_by(units_of<S>(len), tiles);
                 long long sum = tiles;
 #pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
@@ -378,6 +380,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
         }
         left = (int)max(min((long long)share, total - x), 0ll);
+        if constexpr (TREE<A>) {
+            if (a.taken) {  // else there is no other way
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
+                if (lane == 0) sh.saved[warp] = saved;
+                __syncthreads();
+                saved = sh.saved[lane];
+#pragma unroll 1
+                for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
+                const bool taken = saves_enough(a, saved);
+                if (range == 0 && tid == 0) a.taken[kvh] = taken;
+                if (!taken) left = 0;
+            }
+        }
     }
     fence_before();
     __syncthreads();
@@ -1043,31 +1059,51 @@ __global__ void __launch_bounds__(THREADS, 1)
 // [D][M].  A block takes COLS dims of all head rows, a thread each
 // (four of 256: 128 head rows' partials by 64 blocks; by 32, a row of 30 K cells took 5
 // us more).
+// SETS: sets of threads that share the parts of a group, where these are many; else a
+// block takes as many slices of the dims.
 template <int S>
 constexpr int COLS = 8 / S;
-constexpr int SLICES = 8;  // of a block
-template <int S, bool FINE>
-__device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *ws, int x, int d0, int m) {
+constexpr int SLICES = JOIN_THREADS / M;
+template <int S, bool FINE, int SETS>
+__device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *ws, int x, int block) {
     constexpr int D = 128 * S, COLS = qsa::COLS<S>;
+    __shared__ float2 so[SETS > 1 ? SETS : 1][COLS / 2][SETS > 1 ? M : 1];
+    __shared__ float sl[SETS > 1 ? SETS : 1][SETS > 1 ? M : 1];
     const Work work(ws, MAX_GROUP_PARTS, M);
+    const int m = threadIdx.x % M, k = threadIdx.x / M, set = SETS > 1 ? k : 0, d0 = (SETS > 1 ? block : block * SLICES + k) * COLS;
     const int per = a.n_q_heads / a.n_kv_heads;
     const Part part = work.part[x];
-    if (part.row < 0 || m >= part.tokens) return;
+    if (part.row < 0) return;
+    const int n = m < part.tokens ? part.n : 0;
     auto slot = [&](int p) { return ((size_t)(x + p * a.n_kv_heads) * 2 + (p == 0 ? 1 : 0)) * M; };
     float top = -CUDART_INF_F, l = 0.0f;
     float2 o[COLS / 2];
 #pragma unroll
     for (int j = 0; j < COLS / 2; ++j) o[j] = make_float2(0.0f, 0.0f);
 #pragma unroll 4
-    for (int p = 0; p < part.n; ++p) top = fmaxf(top, work.ml[(slot(p) + m) * 2]);
+    for (int p = 0; p < n; ++p) top = fmaxf(top, work.ml[(slot(p) + m) * 2]);
 #pragma unroll 1
-    for (int p = 0; p < part.n; ++p) {
+    for (int p = set; p < n; p += SETS) {
         const float2 ml = reinterpret_cast<const float2 *>(work.ml)[slot(p) + m];
         const float w = ml.x == -CUDART_INF_F ? 0.0f : exp2f(ml.x - top), *src = work.o + slot(p) * D + (size_t)d0 * M + m;
         l = fmaf(w, ml.y, l);
 #pragma unroll
         for (int j = 0; j < COLS / 2; ++j) o[j] = __ffma2_rn(make_float2(w, w), make_float2(src[2 * j * M], src[(2 * j + 1) * M]), o[j]);
     }
+    if constexpr (SETS > 1) {
+#pragma unroll
+        for (int j = 0; j < COLS / 2; ++j) so[set][j][m] = o[j];
+        sl[set][m] = l;
+        __syncthreads();
+        if (set) return;
+#pragma unroll 1
+        for (int i = 1; i < SETS; ++i) {
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j) o[j] = __fadd2_rn(o[j], so[i][j][m]);
+            l += sl[i][m];
+        }
+    }
+    if (!n) return;
     const float inv = top == -CUDART_INF_F ? 0.0f : 1.0f / l;
     const int i = (part.head + m) / per;
     const size_t row = (size_t)(part.row + i) * a.n_q_heads + (size_t)(x % a.n_kv_heads) * per + (part.head + m - i * per);
@@ -1082,12 +1118,60 @@ __device__ __forceinline__ void tiles_join(const qsa_paged_attn_args &a, void *w
     else
         *reinterpret_cast<uint2 *>(dst) = make_uint2(y[0], y[1]);
 }
-
+// The groups' partials, then those of rows one by one (none: no CTAs).  Blocks list the
+// CTAs in which a group or a row that spans CTAs starts, and go round over these.
 template <int S, bool FINE>
-__global__ void __launch_bounds__(M *SLICES) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws) {
+__global__ void __launch_bounds__(JOIN_THREADS) paged_tiles_join_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
+    __shared__ int at[JOIN_THREADS], found[32];
+    static_assert(MAX_CTAS <= JOIN_THREADS / 2 && MAX_GROUP_PARTS <= JOIN_THREADS / 2, "a thread per CTA");
     wait_for_previous_grid();
     allow_dependent_launch();
-    tiles_join<S, FINE>(a, ws, blockIdx.y, (blockIdx.x * SLICES + threadIdx.x / M) * COLS<S>, threadIdx.x % M);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, x = tid % (JOIN_THREADS / 2);
+    const bool group = tid < JOIN_THREADS / 2;
+    const bool starts = group ? x < ctas && Work(ws, MAX_GROUP_PARTS, M).part[x].row >= 0
+                              : x < rows.ctas && Work(rows.ws, rows.cap, rows.rows).part[x].row >= 0;
+    const unsigned m = __ballot_sync(0xffffffffu, starts);
+    if (lane == 0) found[warp] = __popc(m);
+    __syncthreads();
+    const int mine = found[lane];
+    const int groups = __reduce_add_sync(0xffffffffu, lane < 16 ? mine : 0), others = __reduce_add_sync(0xffffffffu, lane < 16 ? 0 : mine);
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? mine : 0);
+    if (starts) at[before + __popc(m & ((1u << lane) - 1))] = x;
+    __syncthreads();
+    // Few of a kind have many parts each, which sets of threads share: where blocks need
+    // not go round for it.
+    const bool few_groups = groups * (128 * S / COLS<S>) <= gridDim.x;
+    const bool few_rows = others * ((rows.rows + JOIN_HEADS<S, 4> - 1) / JOIN_HEADS<S, 4>) <= gridDim.x;
+    const int slices = 128 * S / COLS<S> / (few_groups ? 1 : SLICES), heads = few_rows ? JOIN_HEADS<S, 4> : JOIN_HEADS<S, 1>;
+    const int chunks = (rows.rows + heads - 1) / heads;
+    for (int it = blockIdx.x; it < groups * slices + others * chunks; it += gridDim.x) {
+        const int k = it - groups * slices;
+        if (k < 0) {
+            if (few_groups)
+                tiles_join<S, FINE, SLICES>(a, ws, at[it / slices], it % slices);
+            else
+                tiles_join<S, FINE, 1>(a, ws, at[it / slices], it % slices);
+        } else {
+            if (few_rows)
+                rows_join<S, 4>(a, rows, at[groups + k / chunks], k % chunks * heads);
+            else
+                rows_join<S, 1>(a, rows, at[groups + k / chunks], k % chunks * heads);
+        }
+        __syncthreads();  // what they share is written over
+    }
+}
+// The same where most CTAs of 128 dims have a part that starts there: a block for each
+// (1984 listed tokens 139 us in all, 143 by the list; of 256 dims, fewer blocks are more).
+template <int S, bool FINE>
+__global__ void __launch_bounds__(JOIN_THREADS) paged_tiles_join_all_kernel(const qsa_paged_attn_args a, void *ws, int ctas, const Joined rows) {
+    constexpr int BLOCKS = 128 * S / (COLS<S> * SLICES);
+    wait_for_previous_grid();
+    allow_dependent_launch();
+    const int x = blockIdx.x, y = x - ctas * BLOCKS;
+    if (y < 0)
+        tiles_join<S, FINE, 1>(a, ws, x / BLOCKS, x % BLOCKS);
+    else
+        rows_join<S, 1>(a, rows, y % rows.ctas, y / rows.ctas * JOIN_HEADS<S, 1>);
 }
 inline int tiles_ctas(int n_kv_heads) { return std::max(MAX_GROUP_PARTS / n_kv_heads, 1) * n_kv_heads; }
 
@@ -1098,7 +1182,7 @@ cudaError_t encode_tiles(CUtensorMap &map, const qsa_paged_attn_args &a, const i
     return encode_boxes(map, a, codes, std::min(a.page_size, TileShape<S>::N));
 }
 
-// ws: where the partials go, Work of M rows.  Those of listed rows are left to be joined.
+// ws: where the partials go, Work of M rows.
 template <int S, class A>
 cudaError_t launch_tiles(const A &a, void *ws, cudaStream_t s) {
     CUtensorMap kmap, vmap;
@@ -1108,10 +1192,19 @@ cudaError_t launch_tiles(const A &a, void *ws, cudaStream_t s) {
     const int ctas = tiles_ctas(a.n_kv_heads);
     const auto kernel = a.dtype == QSA_F16 ? paged_tiles_kernel<S, true, A> : paged_tiles_kernel<S, false, A>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TileSmem<S>));
-    if (e == cudaSuccess) e = launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TileSmem<S>), s, a, kmap, vmap, ws);
-    if (LISTED<A> || e != cudaSuccess || ctas == a.n_kv_heads) return e;
-    return launch_dependent(a.dtype == QSA_F16 ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>, dim3(a.head_dim / (COLS<S> * SLICES), ctas), dim3(M * SLICES), 0, s,
-                            static_cast<const qsa_paged_attn_args &>(a), ws);
+    return e == cudaSuccess ? launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TileSmem<S>), s, a, kmap, vmap, ws) : e;
+}
+// Joins what both kinds of kernels left.  both: rows one by one may have been taken.
+template <int S, class A>
+cudaError_t launch_tiles_join(const A &a, void *ws, bool both, cudaStream_t s) {
+    // The rows' kernel has all the CTAs that fit: there is more than enough for them.
+    const Joined rows{a.workspace, MAX_CTAS, a.n_q_heads / a.n_kv_heads, both ? MAX_CTAS / a.n_kv_heads * a.n_kv_heads : 0};
+    const int ctas = tiles_ctas(a.n_kv_heads);
+    const bool fine = a.dtype == QSA_F16, all = S == 1 && ((long long)a.n_tokens * rows.rows / M + 1) * a.n_kv_heads > MAX_GROUP_PARTS / 2;
+    const auto kernel = all ? (fine ? paged_tiles_join_all_kernel<S, true> : paged_tiles_join_all_kernel<S, false>)
+                            : (fine ? paged_tiles_join_kernel<S, true> : paged_tiles_join_kernel<S, false>);
+    const int grid = all ? ctas * (128 * S / (COLS<S> * SLICES)) + rows.ctas * ((rows.rows + JOIN_HEADS<S, 1> - 1) / JOIN_HEADS<S, 1>) : MAX_CTAS;
+    return launch_dependent(kernel, dim3(grid), dim3(JOIN_THREADS), 0, s, static_cast<const qsa_paged_attn_args &>(a), ws, ctas, rows);
 }
 
 }  // namespace

@@ -1,21 +1,45 @@
 // qsa_paged_tree_attn: drafted tokens over a prefix and, by bits, each other.
 //
 // Tokens of one sequence (rows of q that follow one another) read it together
-// (paged_tiles.cuh); rows without such company, and short tables, go row by row
-// (paged_rows.cuh).
+// (paged_tiles.cuh), where that saves enough; else, and where tables are short, they go
+// one by one (paged_rows.cuh).  As with listed rows, both kinds start, and one of them
+// finds that it has nothing to do.
 #include "paged_tiles.cuh"
 
 namespace qsa {
 namespace {
 
+// The rows' partials, the groups', and a word for each KV head.
+size_t rows_and_tiles_bytes(int per, int head_dim) {
+    return (Work::bytes(MAX_CTAS, per, head_dim) + 255) / 256 * 256 + (Work::bytes(MAX_GROUP_PARTS, M, head_dim) + 255) / 256 * 256;
+}
+
 template <int S>
-cudaError_t launch(const TreeArgs &a, cudaStream_t s) {
+cudaError_t launch(TreeArgs a, cudaStream_t s) {
     const long long cells = (long long)a.max_pages * a.page_size;
-    if (!a.rows || a.n_tokens < 2 || cells <= WHOLE * Shape<S>::UNIT) return launch_rows<S>(a, cells, s);
-    return launch_tiles<S>(a, static_cast<uint8_t *>(a.workspace) + Work::bytes(MAX_CTAS, a.n_q_heads / a.n_kv_heads, a.head_dim), s);
+    const int per = a.n_q_heads / a.n_kv_heads;
+    // Tenths of a unit, if all rows are as long as the table is wide.
+    const long long most = (long long)a.n_tokens * a.n_kv_heads * (cells / Shape<S>::UNIT) * 10;
+    const bool shared = a.n_kv_heads <= MAX_GROUP_PARTS / 2;  // else no kind has more than one CTA for a head
+    if (!a.rows || a.n_tokens < 2 || cells <= WHOLE * Shape<S>::UNIT || (shared && most <= CALL_COST)) return launch_rows<S>(a, cells, s);
+    // With eight tokens for each row of the table they are taken together unseen (a
+    // second kind's launch costs 24 trees of 32 tokens 9 us of 128); with fewer, by what
+    // the lengths say.
+    const bool both = shared && (a.n_tokens < 8ll * a.n_rows || most <= 2 * CALL_COST);
+    uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+    if (both) a.taken = reinterpret_cast<int *>(ws + rows_and_tiles_bytes(per, a.head_dim));
+    ws += (Work::bytes(MAX_CTAS, per, a.head_dim) + 255) / 256 * 256;
+    cudaError_t e = launch_tiles<S>(a, ws, s);
+    if (e == cudaSuccess && both) e = launch_rows<S>(a, cells, s);
+    if (e != cudaSuccess || tiles_ctas(a.n_kv_heads) == a.n_kv_heads) return e;
+    return launch_tiles_join<S>(a, ws, both, s);
 }
 
 }  // namespace
+
+size_t paged_tree_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim) {
+    return rows_and_tiles_bytes(n_q_heads / n_kv_heads, head_dim) + sizeof(int) * MAX_GROUP_PARTS;
+}
 
 cudaError_t launch_paged_tree_attn(const qsa_paged_tree_attn_args &x, cudaStream_t s) {
     TreeArgs a{};

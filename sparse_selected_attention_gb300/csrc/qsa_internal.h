@@ -149,6 +149,7 @@ cudaError_t launch_page_select(const qsa_page_select_args &a, cudaStream_t s);
 cudaError_t launch_paged_sparse_attn(const qsa_paged_sparse_attn_args &a, cudaStream_t s);
 cudaError_t launch_paged_tree_attn(const qsa_paged_tree_attn_args &a, cudaStream_t s);
 size_t paged_sparse_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
+size_t paged_tree_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 size_t paged_attn_workspace_bytes(int n_q_heads, int n_kv_heads, int head_dim);
 size_t pages_workspace_bytes(int n_rows, int n_pages);
 

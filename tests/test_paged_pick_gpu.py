@@ -605,9 +605,17 @@ def trees(rng, prefix, nodes, page, hkv, d, seed, extra=2):
     return pool, table, [prefix[s] for s in rows], mask, rows
 
 
-def read_together(table, page, d, rows):
-    """Whether the call reads the tokens of one sequence together: sixteen units of 32 (of 256 dims 16) cells are few."""
-    return rows is not None and len(rows) > 1 and table.shape[1] * page > 16 * (32 if d == 128 else 16)
+def tree_workspace(hq, hkv, d):
+    return torch.full((qsa.qsa_paged_tree_attn_workspace_bytes(hq, hkv, d),), 0xA5, dtype=torch.uint8, device="cuda")
+
+
+def read_together(ws, rows, n_rows, cells, hkv, d):
+    """Whether a call on rows of a table of n_rows by `cells` took the tokens of one sequence together: where
+    there are eight and more for each row of the table, unasked; else the call leaves a word for each KV head."""
+    most = len(rows) * hkv * (cells // (32 if d == 128 else 16)) * 10
+    if cells <= 512 or most <= 130000:
+        return False
+    return len(rows) >= 8 * n_rows and most > 260000 or bool((ws[-608:].view(torch.int32)[:hkv] == 1).all())
 
 
 @pytest.mark.parametrize("otype", [F16, BF16])
@@ -622,22 +630,34 @@ def test_tree_shapes(cuda_device, d, hq, hkv, page, otype):
 
 @pytest.mark.parametrize("otype", [F16, BF16])
 @pytest.mark.parametrize("d,hq,hkv,page,prefix,nodes", [
-    (128, 12, 1, 64, [9001], [40]), (256, 24, 2, 16, [3001, 2500], [63, 30]), (128, 32, 8, 64, [700, 630, 1400], [32, 17, 60]),
-    (128, 16, 8, 128, [577], [130]), (256, 8, 4, 32, [1000, 515, 2000], [31, 33, 90]), (128, 8, 8, 16, [560], [256])])
+    (128, 12, 1, 64, [17001], [70]), (256, 24, 2, 16, [3001, 2500], [63, 30]), (128, 32, 8, 64, [900, 1630, 1400], [32, 17, 60]),
+    (128, 16, 8, 128, [577], [130]), (256, 8, 4, 32, [1000, 515, 2000], [31, 33, 90]), (128, 8, 8, 16, [560], [256]),
+    (128, 16, 8, 32, [6000, 5000, 4000, 900], [7, 7, 7, 2]), (256, 24, 2, 64, [12000, 9000, 100], [9, 7, 1]), (128, 12, 4, 64, [30000], [7])])
 def test_trees_taken_together(cuda_device, d, hq, hkv, page, prefix, nodes, otype):
     rng = np.random.default_rng(hq)
     pool, table, pre, mask, rows = trees(rng, prefix, nodes, page, hkv, d, 32)
-    assert read_together(table, page, d, rows)
     gate = rng.standard_normal((len(rows), hq, d)).astype(np.float32) * 2
     q = rng.standard_normal((len(rows), hq, d)) * 2
-    check_tree(q, pool, table, pre, mask, rows=rows, otype=otype, gate=gate)
+    ws = tree_workspace(hq, hkv, d)
+    check_tree(q, pool, table, pre, mask, rows=rows, otype=otype, gate=gate, ws=ws)
+    assert read_together(ws, rows, len(prefix), table.shape[1] * page, hkv, d)
+
+
+@pytest.mark.parametrize("d,hq,hkv,page,prefix,nodes", [(128, 12, 2, 64, [3000] * 40, [1] * 40), (256, 24, 2, 16, [2500, 3000] * 6, [2, 1] * 6),
+                                                        (128, 32, 8, 32, [900] * 30, [1, 2, 3] * 10)])
+def test_trees_of_few_tokens_go_one_by_one(cuda_device, d, hq, hkv, page, prefix, nodes):
+    rng = np.random.default_rng(hq)
+    pool, table, pre, mask, rows = trees(rng, prefix, nodes, page, hkv, d, 43)
+    ws = tree_workspace(hq, hkv, d)
+    check_tree(rng.standard_normal((len(rows), hq, d)), pool, table, pre, mask, rows=rows, ws=ws)
+    assert not read_together(ws, rows, len(prefix), table.shape[1] * page, hkv, d)
 
 
 @pytest.mark.parametrize("together", [False, True])
 def test_tree_any_masks(cuda_device, together):
     """Bits at random, none, all; rows that see nothing; prefixes of their own."""
     rng = np.random.default_rng(33)
-    n, hkv = (96, 8) if together else (20, 2)
+    n, hkv = (130, 8) if together else (20, 2)
     table, pages = shuffled_table([1100, 200] if together else [500, 200], 32, 3, rng)
     pool = make_pool(pages, 32, hkv, 128, seed=33)
     rows = [0] * (n - 4) + [1] * 4
@@ -650,8 +670,9 @@ def test_tree_any_masks(cuda_device, together):
     prefix[7], mask[7] = 0, 0
     prefix[8], mask[8] = 0, 0
     mask[8, 0] = 1
-    assert read_together(table, 32, 128, rows) == together
-    out, lse = check_tree(rng.standard_normal((n, (16 if together else 4), 128)), pool, table, prefix, mask, rows=rows)
+    ws = tree_workspace(16 if together else 4, hkv, 128)
+    out, lse = check_tree(rng.standard_normal((n, (16 if together else 4), 128)), pool, table, prefix, mask, rows=rows, ws=ws)
+    assert read_together(ws, rows, 2, table.shape[1] * 32, hkv, 128) == together
     assert not out[7].any() and torch.isneginf(lse[7]).all() and not out[n - 4].any()
 
 
@@ -683,9 +704,8 @@ def test_tree_bad_inputs(cuda_device):
 def test_nan_and_inf_scales_reach_only_rows_that_see_them(cuda_device, together):
     rng = np.random.default_rng(35)
     hkv, d, hq = (8, 128, 16) if together else (2, 128, 8)
-    nodes, pre = (64, 700) if together else (9, 300)
+    nodes, pre = (130, 900) if together else (9, 300)
     pool, table, prefix, mask, rows = trees(rng, [pre], [nodes], 32, hkv, d, 35)
-    assert read_together(table, 32, d, rows) == together
     sees = np.array([[int(m[b // 32]) >> (b % 32) & 1 for b in range(nodes)] for m in mask], bool)
     q = dev(rng.standard_normal((nodes, hq, d)).astype(np.float16))
     ws = torch.empty(qsa.qsa_paged_tree_attn_workspace_bytes(hq, hkv, d), dtype=torch.uint8, device="cuda")
@@ -696,6 +716,7 @@ def test_nan_and_inf_scales_reach_only_rows_that_see_them(cuda_device, together)
         return out, lse
 
     want = run(pool)
+    assert read_together(ws, rows, 1, table.shape[1] * 32, hkv, d) == together
     for node, part, value in ((2, 2, np.inf), (5, 3, np.nan), (nodes - 1, 3, np.inf), (3, 2, np.nan)):
         p = [x.copy() for x in pool]
         c = pre + node

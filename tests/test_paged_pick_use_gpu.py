@@ -15,7 +15,7 @@ import sparse_selected_attention_gb300 as qsa
 from oracle import paged_oracle as po
 from tests.test_paged_gpu import BF16, F16, F32, HALF, TINY, Serving, dev, err_word, i32, make_pool, shuffled_table
 from tests.test_paged_groups_gpu import reference
-from tests.test_paged_pick_gpu import alike, check_sparse, check_tree, sparse_workspace, taken_together, trees
+from tests.test_paged_pick_gpu import alike, check_sparse, check_tree, read_together, sparse_workspace, taken_together, tree_workspace, trees
 from tests.test_paged_variants_gpu import use_library, word  # noqa: F401
 from tests.test_paged_vscales_gpu import scales
 
@@ -24,10 +24,6 @@ pytestmark = pytest.mark.gpu
 
 def zeros(*s, t=torch.int32):
     return torch.zeros(s, dtype=t, device="cuda")
-
-
-def tree_workspace(hq, hkv, d):
-    return torch.full((qsa.qsa_paged_tree_attn_workspace_bytes(hq, hkv, d),), 0xA5, dtype=torch.uint8, device="cuda")
 
 
 def chain(n, words=None):
@@ -291,7 +287,7 @@ def test_tree_softmax_scales(cuda_device, scale):
 def one_sequence(form, d, seed):
     """Tokens of one sequence, all of whose pages are seen: pool, table, lengths, rows and the call."""
     rng = np.random.default_rng(seed)
-    n, cells, page, hkv, hq = 48, 1700, 32, 8, 16
+    n, cells, page, hkv, hq = 72, 1700, 32, 8, 16
     table, pages = shuffled_table([cells], page, 1, rng)
     pool = [dev(x) for x in make_pool(pages, page, hkv, d, seed=seed)]
     lens, rows = [cells - n + i + 1 for i in range(n)], [0] * n
@@ -299,8 +295,9 @@ def one_sequence(form, d, seed):
     def call(q, pool, **kw):
         out, lse, err = torch.empty_like(q), zeros(n, hq, t=F32), err_word()
         if form == "tree":
-            qsa.qsa_paged_tree_attn(q, *pool, dev(table), i32([cells - n] * n), dev(chain(n)), out, tree_workspace(hq, hkv, d), rows=i32(rows),
-                                    lse=lse, err=err, **kw)
+            ws = tree_workspace(hq, hkv, d)
+            qsa.qsa_paged_tree_attn(q, *pool, dev(table), i32([cells - n] * n), dev(chain(n)), out, ws, rows=i32(rows), lse=lse, err=err, **kw)
+            assert read_together(ws, rows, 1, table.shape[1] * page, hkv, d)
         else:
             wide = table.shape[1]
             lists = torch.arange(wide, dtype=torch.int32, device="cuda").expand(n, hkv, wide).contiguous()

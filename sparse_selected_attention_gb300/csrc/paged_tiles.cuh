@@ -448,7 +448,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                 else if (want && j < a.max_pages)
                     page = __ldg(tab + j);
                 const bool there = page >= 0 && page < a.n_pages;
-                if constexpr (!LISTED<A>) bad |= want && !there;
                 const int cell = (page << page_shift) + (c & (a.page_size - 1));
                 const unsigned m = __ballot_sync(0xffffffffu, there);
 #pragma unroll
@@ -802,9 +801,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if constexpr (LISTED<A>) return c ? sees[MY - 1] : sees[0];
                     const int from = c0 + 32 * c;
                     if (from >= len) return 0u;
-                    uint32_t bits = f.there[half * MY + c];
-                    if constexpr (TREE<A>) bits &= tree_bits(a, token, from, sure);
-                    return len - from < 32 ? bits & ((1u << (len - from)) - 1) : bits;
+                    uint32_t bits = 0xffffffffu;
+                    if constexpr (TREE<A>) bits = tree_bits(a, token, from, sure);
+                    if (len - from < 32) bits &= (1u << (len - from)) - 1;
+                    const uint32_t there = f.there[half * MY + c];
+                    bad |= good && (bits & ~there);  // a page that no row attends to may be missing
+                    return bits & there;
                 };
                 wait(sh.s_full[set], kk >> 1);
                 fence_after();

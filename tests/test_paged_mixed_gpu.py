@@ -1,0 +1,80 @@
+"""Calls on the paged cache whose tokens are of several kinds: what each way of
+taking rows reports, that rows of one kind leave others their way, and that a
+call's size, order or neighbours do not change how its tokens are taken.
+
+Tolerances as tests/test_paged_pick_gpu.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged_oracle as po
+from tests.test_paged_gpu import BF16, F16, make_pool, shuffled_table
+from tests.test_paged_pick_gpu import check_tree, tree_workspace
+
+pytestmark = pytest.mark.gpu
+
+
+def tile_parts(ws, hq, hkv, d):
+    """What the groups' CTAs left to be joined, a first row (or -1) for each, by the workspace's layout."""
+    up = lambda n: -(-n // 256) * 256  # noqa: E731
+    rows, ctas = hq // hkv, 304
+    at = up(up(ctas * 16) + up(ctas * 2 * rows * 8) + ctas * 2 * rows * d * 4)
+    return ws[at:at + 152 // hkv * hkv * 16].view(torch.int32)[::4]
+
+
+def by_groups(ws, hq, hkv, d):
+    """Whether groups went through tiles of the cache (of calls whose groups are cut over CTAs): there is a part of one."""
+    return bool((tile_parts(ws, hq, hkv, d) >= 0).any())
+
+
+def one_by_one(ws):
+    """Whether rows went one by one (of calls whose rows are cut over CTAs): there is a part of one."""
+    return bool((ws[: 304 * 16].view(torch.int32)[::4] >= 0).any())
+
+
+# ---------------------------------------------------------------- what trees report
+
+@pytest.mark.parametrize("otype", [F16, BF16])
+@pytest.mark.parametrize("n,hq,hkv,d", [(72, 16, 8, 128), (64, 16, 4, 256), (3, 4, 2, 128)])
+def test_tree_reports_what_its_tokens_attend_to(cuda_device, n, hq, hkv, d, otype):
+    """Pages that no mask reaches may be missing, whichever way rows are taken; those that one token attends to may not."""
+    rng = np.random.default_rng(n)
+    page, prefix, together = 16, 2000, n > 3
+    table, pages = shuffled_table([prefix + 256], page, 0, rng)
+    pool = make_pool(pages, page, hkv, d, seed=n)
+    q = rng.standard_normal((n, hq, d))
+    sees = np.zeros((n, 256), bool)
+    sees[:, :16] = rng.random((n, 16)) < 0.6
+    sees[:, 200:208] = rng.random((n, 8)) < 0.6
+    pre, rows = [prefix - 5 * (i % 3) for i in range(n)], [0] * n
+
+    def error(sees=sees, pre=pre, table=table, rows=rows):
+        mask = np.packbits(sees, axis=1, bitorder="little").view(np.int32)
+        ws = tree_workspace(hq, hkv, d)
+        check_tree(q, pool, table, pre, mask, rows=rows, otype=otype, ws=ws)
+        assert by_groups(ws, hq, hkv, d) == together
+        return po.tree_cells(table, pre, mask, hkv, page, pages, rows)[1]
+
+    gone = table.copy()
+    gone[0, 128:136], gone[0, 130] = -1, pages  # cells 2048 .. 2175: bits 48 and more of the longest prefix, to 185 of the shortest
+    assert error(table=gone) == 0
+    one = sees.copy()
+    one[n // 2, 70] = True
+    assert error(sees=one, table=gone) == po.BAD_ID
+    assert error(sees=one) == 0
+    hole = table.copy()
+    hole[0, 7] = -1
+    assert error(table=hole) == po.BAD_ID
+    # A page behind all prefixes but one, whose token's bits end before the table does.
+    x, few = list(pre), sees.copy()
+    x[n - 1], few[n - 1, 16:] = prefix + 70, False
+    assert error(sees=few, pre=x) == 0
+    assert error(sees=few, pre=x, table=gone) == po.BAD_ID
+    for bad in (-4, 10 ** 9, table.shape[1] * page - 100):
+        x = list(pre)
+        x[1] = bad
+        assert error(pre=x) == po.BAD_ID
+    x = list(rows)
+    x[n - 1] = 1
+    assert error(rows=x) == po.BAD_ID

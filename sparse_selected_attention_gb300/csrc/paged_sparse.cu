@@ -126,7 +126,7 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
         e = launch_dependent(listed_union_kernel, dim3((a.n_tokens + tokens - 1) / tokens, a.n_kv_heads), dim3(32 * UNION_WARPS), bytes, s, a, tokens, words);
     if (e == cudaSuccess) e = launch_tiles<S>(a, ws, s);
     if (e == cudaSuccess) e = launch_rows<S>(a, cells, s);
-    return e == cudaSuccess ? launch_tiles_join<S>(a, ws, true, s) : e;
+    return e == cudaSuccess ? launch_tiles_join<S>(a, ws, s) : e;
 }
 
 }  // namespace

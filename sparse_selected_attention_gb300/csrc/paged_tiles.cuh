@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         left = (int)max(min((long long)share, total - x), 0ll);
         if constexpr (TREE<A>) {
-            if (a.taken) {  // else there is no other way
+            if (a.taken) {  // else they are taken whatever it saves
 #pragma unroll 1
                 for (int o = 16; o > 0; o >>= 1) saved += __shfl_xor_sync(0xffffffffu, saved, o);
                 if (lane == 0) sh.saved[warp] = saved;
@@ -1048,7 +1048,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
     if (tid == 0) {
         if (!ok && a.err) atomicOr(a.err, QSA_DEVERR_TIMEOUT);
-        if (ranges > 1) work.part[blockIdx.x] = ok ? part : Part{-1, 0, 0, 0};
+        if (gridDim.x <= MAX_GROUP_PARTS) work.part[blockIdx.x] = ok ? part : Part{-1, 0, 0, 0};
     }
     if (warp == PRODUCTS) {
         fence_after();
@@ -1196,11 +1196,11 @@ cudaError_t launch_tiles(const A &a, void *ws, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(TileSmem<S>));
     return e == cudaSuccess ? launch_dependent(kernel, dim3(ctas), dim3(THREADS), sizeof(TileSmem<S>), s, a, kmap, vmap, ws) : e;
 }
-// Joins what both kinds of kernels left.  both: rows one by one may have been taken.
+// Joins what both kinds of kernels left, one of which has had the rows.
 template <int S, class A>
-cudaError_t launch_tiles_join(const A &a, void *ws, bool both, cudaStream_t s) {
+cudaError_t launch_tiles_join(const A &a, void *ws, cudaStream_t s) {
     // The rows' kernel has all the CTAs that fit: there is more than enough for them.
-    const Joined rows{a.workspace, MAX_CTAS, a.n_q_heads / a.n_kv_heads, both ? MAX_CTAS / a.n_kv_heads * a.n_kv_heads : 0};
+    const Joined rows{a.workspace, MAX_CTAS, a.n_q_heads / a.n_kv_heads, MAX_CTAS / a.n_kv_heads * a.n_kv_heads};
     const int ctas = tiles_ctas(a.n_kv_heads);
     const bool fine = a.dtype == QSA_F16, all = S == 1 && ((long long)a.n_tokens * rows.rows / M + 1) * a.n_kv_heads > MAX_GROUP_PARTS / 2;
     const auto kernel = all ? (fine ? paged_tiles_join_all_kernel<S, true> : paged_tiles_join_all_kernel<S, false>)

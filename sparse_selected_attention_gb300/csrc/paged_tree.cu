@@ -20,19 +20,19 @@ cudaError_t launch(TreeArgs a, cudaStream_t s) {
     const int per = a.n_q_heads / a.n_kv_heads;
     // Tenths of a unit, if all rows are as long as the table is wide.
     const long long most = (long long)a.n_tokens * a.n_kv_heads * (cells / Shape<S>::UNIT) * 10;
-    const bool shared = a.n_kv_heads <= MAX_GROUP_PARTS / 2;  // else no kind has more than one CTA for a head
-    if (!a.rows || a.n_tokens < 2 || cells <= WHOLE * Shape<S>::UNIT || (shared && most <= CALL_COST)) return launch_rows<S>(a, cells, s);
-    // With eight tokens for each row of the table they are taken together unseen (a
-    // second kind's launch costs 24 trees of 32 tokens 9 us of 128); with fewer, by what
-    // the lengths say.
-    const bool both = shared && (a.n_tokens < 8ll * a.n_rows || most <= 2 * CALL_COST);
+    // The lengths and the order of the tokens say which kind is taken, and those only the
+    // device knows.  (Together unseen, 24 trees of 16 to 32 tokens, 32/8 heads, would take
+    // 127 us, not 131, but given level by level, rows 0, 1, 2, .., 0, 1, 2, .., 2600, where
+    // one by one they take 1150.)  With more KV heads than there are places for partials,
+    // no kind has more than one CTA for a head, and all go together.
+    const bool both = a.n_kv_heads <= MAX_GROUP_PARTS;
+    if (!a.rows || a.n_tokens < 2 || cells <= WHOLE * Shape<S>::UNIT || (both && most <= CALL_COST)) return launch_rows<S>(a, cells, s);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace);
     if (both) a.taken = reinterpret_cast<int *>(ws + rows_and_tiles_bytes(per, a.head_dim));
     ws += (Work::bytes(MAX_CTAS, per, a.head_dim) + 255) / 256 * 256;
     cudaError_t e = launch_tiles<S>(a, ws, s);
     if (e == cudaSuccess && both) e = launch_rows<S>(a, cells, s);
-    if (e != cudaSuccess || tiles_ctas(a.n_kv_heads) == a.n_kv_heads) return e;
-    return launch_tiles_join<S>(a, ws, both, s);
+    return e == cudaSuccess && both ? launch_tiles_join<S>(a, ws, s) : e;
 }
 
 }  // namespace

@@ -10,7 +10,7 @@ import torch
 
 from oracle import paged_oracle as po
 from tests.test_paged_gpu import BF16, F16, make_pool, shuffled_table
-from tests.test_paged_pick_gpu import check_tree, tree_workspace
+from tests.test_paged_pick_gpu import check_tree, tree_workspace, trees
 
 pytestmark = pytest.mark.gpu
 
@@ -28,9 +28,9 @@ def by_groups(ws, hq, hkv, d):
     return bool((tile_parts(ws, hq, hkv, d) >= 0).any())
 
 
-def one_by_one(ws):
-    """Whether rows went one by one (of calls whose rows are cut over CTAs): there is a part of one."""
-    return bool((ws[: 304 * 16].view(torch.int32)[::4] >= 0).any())
+def decided(ws, hkv):
+    """What the device decided, a word for each KV head at the workspace's end: 1 by groups, 0 one by one."""
+    return ws[-152 * 4:].view(torch.int32)[:hkv].tolist()
 
 
 # ---------------------------------------------------------------- what trees report
@@ -78,3 +78,23 @@ def test_tree_reports_what_its_tokens_attend_to(cuda_device, n, hq, hkv, d, otyp
     x = list(rows)
     x[n - 1] = 1
     assert error(rows=x) == po.BAD_ID
+
+
+# ---------------------------------------------------------------- trees in any order
+
+@pytest.mark.parametrize("d,hq,hkv,page,seqs,nodes,prefix", [(128, 32, 8, 64, 6, 16, 1500), (256, 24, 2, 16, 4, 60, 2500), (128, 100, 100, 32, 3, 40, 600),
+                                                            (128, 154, 77, 128, 2, 9, 900)])
+def test_tree_order_decides_how_tokens_are_taken(cuda_device, d, hq, hkv, page, seqs, nodes, prefix):
+    """Neighbours of one sequence go together; given level by level, they have none and go one by one, however many there are."""
+    rng = np.random.default_rng(seqs)
+    pool, table, pre, mask, rows = trees(rng, [prefix + 31 * s for s in range(seqs)], [nodes] * seqs, page, hkv, d, 70)
+    q = rng.standard_normal((len(rows), hq, d))
+    order = np.arange(len(rows)).reshape(seqs, nodes).T.reshape(-1)
+    res = []
+    for o in (np.arange(len(rows)), order):
+        ws = tree_workspace(hq, hkv, d)
+        out, lse = check_tree(q[o], pool, table, [pre[i] for i in o], mask[o], rows=[rows[i] for i in o], ws=ws)
+        res.append((out[np.argsort(o)], lse[np.argsort(o)], decided(ws, hkv)))
+    assert [x[2] for x in res] == [[1] * hkv, [0] * hkv]
+    torch.testing.assert_close(res[0][0].float(), res[1][0].float(), rtol=2.0 ** -8, atol=2.0 ** -9)
+    torch.testing.assert_close(res[0][1], res[1][1], rtol=2.0 ** -18, atol=2.0 ** -14)

@@ -6,7 +6,7 @@
 // else one by one (paged_rows.cuh).  What the groups go through is found by a kernel
 // before; both kinds then start, and one of them finds that it has nothing to do.  Those
 // tokens, 12/1 heads of 128: 138 us by groups (cold: union 8, groups 132, join 12), 229
-// one by one.  Lists that turn out not to be alike pay 12 us for the attempt.
+// one by one.  Lists that turn out not to be alike pay 11 to 14 us for the attempt.
 //
 // Rows one by one: 61 rows of 2 K cells, 48/4 heads of 128, 146 MB: 46.4 us, 3.1 TB/s,
 // thirteen units a warp between some 20 us of launch, first loads and ends of rows.
@@ -18,21 +18,19 @@ namespace {
 // Entries of all unions, and groups' first rows, that the workspace has room for; and
 // the rows' bits of pages that a block holds.
 constexpr long long ENTRIES = 1 << 20;
-constexpr int UNION_WARPS = 8, UNION_BYTES = 96 * 1024;
-// Sequences that a block's rows may belong to; with more, there is little to share.
-constexpr int MOST_RUNS = 4;
+constexpr int UNION_WARPS = 32, UNION_BYTES = 96 * 1024, BATCH = 4;  // warps at most; BATCH: loads of a lane on their way
 
 // The unions of the groups among `tokens` rows: a bit for each row and page, and the
-// pages of 32 at once from these.
+// pages of 32 at once from these.  A row without neighbours of its sequence is a group
+// by itself, which costs what its own tiles cost and leaves the others theirs.
 __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const ListedArgs a, int tokens, int words) {
     extern __shared__ unsigned bits[];  // [tokens][words | 1]
-    __shared__ int row[32], sure[32], count[32], sums[UNION_WARPS], twice;
-    __shared__ unsigned starts;
+    __shared__ int row[32], sure[32], count[32], sums[32][UNION_WARPS];
+    __shared__ unsigned starts, twice;
     wait_for_previous_grid();
     allow_dependent_launch();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, kvh = blockIdx.y, page_shift = 31 - __clz(a.page_size);
+    const int tid = threadIdx.x, warps = blockDim.x >> 5, lane = tid & 31, warp = tid >> 5, kvh = blockIdx.y, page_shift = 31 - __clz(a.page_size);
     const int t0 = blockIdx.x * tokens, n = min(tokens, a.n_tokens - t0), pitch = words | 1;
-    int *size = a.shared.size + (size_t)kvh * a.n_tokens + t0;
     bool bad = false;
     if (warp == 0) {
         int trow = 0, known = 0, raw = 0;
@@ -44,63 +42,113 @@ __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const Li
         }
         const int before = __shfl_up_sync(0xffffffffu, raw, 1);
         const unsigned m = __ballot_sync(0xffffffffu, lane < n && (lane == 0 || raw != before));
-        if (lane == 0) starts = m;
+        if (lane == 0) {
+            starts = m;
+            twice = 0u;
+        }
     }
+    for (int i = tid; i < n * pitch; i += 32 * warps) bits[i] = 0u;
     __syncthreads();
-    const unsigned m = starts;
-    if (__popc(m) > MOST_RUNS) {
-        if (tid < n) size[tid] = tid ? 0 : n << SIZE_BITS | SIZE_MASK;
+    const unsigned single = starts & (starts >> 1 | 1u << (n - 1));  // rows that are a group by themselves
+    for (int i = warp; i < n; i += warps) {
+        const int32_t *list = a.lists + ((size_t)(t0 + i) * a.n_kv_heads + kvh) * a.width;
+        const bool alone = single >> i & 1u;  // then its list is the union, whatever its order
+        const size_t base = ((size_t)kvh * a.n_tokens + t0 + i) * a.width;
+        int total = 0;
+        for (int x0 = 0; x0 < count[i]; x0 += 32 * BATCH) {
+            int j[BATCH], page[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                const int x = x0 + 32 * k + lane;
+                j[k] = x < count[i] ? __ldg(list + x) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                bad |= j[k] < -1 || j[k] >= a.max_pages;
+                if (j[k] >= a.max_pages || (j[k] >= 0 && j[k] << page_shift >= sure[i])) j[k] = -1;
+                page[k] = alone && j[k] >= 0 ? __ldg(a.page_table + (size_t)row[i] * a.max_pages + j[k]) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) {
+                if (alone) {
+                    const unsigned in = __ballot_sync(0xffffffffu, j[k] >= 0);
+                    if (j[k] >= 0) {
+                        const size_t to = base + total + __popc(in & ((1u << lane) - 1));
+                        const bool held = page[k] >= 0 && page[k] < a.n_pages;
+                        bad |= !held;
+                        a.shared.unit[to] = make_uint2(j[k], 1u);
+                        a.shared.page[to] = held ? page[k] : -1;
+                    }
+                    total += __popc(in);
+                } else if (j[k] >= 0) {
+                    const unsigned bit = 1u << (j[k] & 31);
+                    if (atomicOr(&bits[i * pitch + (j[k] >> 5)], bit) & bit) atomicOr(&twice, 1u << i);
+                }
+            }
+        }
+        if (alone && lane == 0) a.shared.size[(size_t)kvh * a.n_tokens + t0 + i] = 1 << SIZE_BITS | total;
+    }
+    if (single == starts) {  // the same in all threads
+        if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
         return;
     }
-    for (int s = 0; s < n;) {
-        const unsigned later = m & (0xfffffffeu << s);
-        const int e = later ? __ffs(later) - 1 : n;
-        for (int i = tid; i < (e - s) * pitch; i += 32 * UNION_WARPS) bits[i] = 0u;
-        if (tid == 0) twice = 0;
-        __syncthreads();
-        for (int i = s + warp; i < e; i += UNION_WARPS) {
-            const int32_t *list = a.lists + ((size_t)(t0 + i) * a.n_kv_heads + kvh) * a.width;
-            for (int x = lane; x < count[i]; x += 32) {
-                const int j = __ldg(list + x);
-                bad |= j < -1 || j >= a.max_pages;
-                if (j < 0 || j >= a.max_pages || j << page_shift >= sure[i]) continue;
-                const unsigned bit = 1u << (j & 31);
-                if (atomicOr(&bits[(i - s) * pitch + (j >> 5)], bit) & bit) twice = 1;
+    __syncthreads();
+    // The other groups: rows s .. e - 1.  Of each, a warp takes a run of the words: it counts its
+    // pages, and writes them behind those of the warps before.
+    const int run = (words + warps - 1) / warps, w0 = min(warp * run, words), w1 = min(w0 + run, words);
+    auto each_group = [&](auto &&f) {
+        for (unsigned left = starts & ~single; left; left &= left - 1) {
+            const int s = __ffs(left) - 1;
+            const unsigned later = starts & (0xfffffffeu << s);
+            f(s, later ? __ffs(later) - 1 : n);
+        }
+    };
+    auto any_of = [&](int s, int e, int w) {
+        unsigned any = 0u;
+        for (int i = s; i < e; ++i) any |= w < w1 ? bits[i * pitch + w] : 0u;
+        return any;
+    };
+    each_group([&](int s, int e) {
+        int pages = 0;
+        for (int w = w0; w < w1; w += 32) pages += __popc(any_of(s, e, w + lane));
+        pages = __reduce_add_sync(0xffffffffu, pages);
+        if (lane == 0) sums[s][warp] = pages;
+    });
+    __syncthreads();
+    each_group([&](int s, int e) {
+        size_t to = ((size_t)kvh * a.n_tokens + t0 + s) * a.width;
+        for (int w = 0; w < warp; ++w) to += sums[s][w];
+        for (int base = w0; base < w1; base += 32) {
+            const unsigned any = any_of(s, e, base + lane);
+            for (unsigned left = __ballot_sync(0xffffffffu, any != 0u); left; left &= left - 1) {
+                const int in = __ffs(left) - 1;
+                const unsigned all = __shfl_sync(0xffffffffu, any, in), mine = lane < e - s ? bits[(s + lane) * pitch + base + in] : 0u;
+                unsigned who = 0u;
+                for (int i = 0; i < e - s; ++i) who |= (__shfl_sync(0xffffffffu, mine, i) >> lane & 1u) << i;
+                if (who) a.shared.unit[to + __popc(all & ((1u << lane) - 1))] = make_uint2(32 * (base + in) + lane, who);
+                to += __popc(all);
             }
         }
-        __syncthreads();
-        // A warp takes a run of the words.
-        const int run = (words + UNION_WARPS - 1) / UNION_WARPS, w0 = min(warp * run, words), w1 = min(w0 + run, words);
-        int at = 0;
-        for (int w = w0; w < w1; ++w) at += __popc(__reduce_or_sync(0xffffffffu, lane < e - s ? bits[lane * pitch + w] : 0u));
-        if (lane == 0) sums[warp] = at;
-        __syncthreads();
+    });
+    __syncthreads();
+    // Their places in the pool, 32 at a time by the warps in turn.
+    int turn = 0;
+    each_group([&](int s, int e) {
         int total = 0;
-        at = 0;
-        for (int w = 0; w < UNION_WARPS; ++w) {
-            at += w < warp ? sums[w] : 0;
-            total += sums[w];
+        for (int w = 0; w < warps; ++w) total += sums[s][w];
+        const size_t to = ((size_t)kvh * a.n_tokens + t0 + s) * a.width;
+        for (int x = lane; x - lane < total; x += 32, ++turn) {
+            if (turn % warps != warp || x >= total) continue;
+            const int page = __ldg(a.page_table + (size_t)row[s] * a.max_pages + a.shared.unit[to + x].x);
+            const bool held = page >= 0 && page < a.n_pages;
+            bad |= !held;
+            a.shared.page[to + x] = held ? page : -1;
         }
-        const size_t base = ((size_t)kvh * a.n_tokens + t0 + s) * a.width;
-        for (int w = w0; w < w1; ++w) {
-            const unsigned mine = lane < e - s ? bits[lane * pitch + w] : 0u, any = __reduce_or_sync(0xffffffffu, mine);
-            if (!any) continue;
-            unsigned who = 0u;
-            for (int i = 0; i < e - s; ++i) who |= (__shfl_sync(0xffffffffu, mine, i) >> lane & 1u) << i;
-            if (who) {
-                const size_t to = base + at + __popc(any & ((1u << lane) - 1));
-                const int j = 32 * w + lane, page = __ldg(a.page_table + (size_t)row[s] * a.max_pages + j);
-                const bool held = page >= 0 && page < a.n_pages;
-                bad |= !held;
-                a.shared.unit[to] = make_uint2(j, who);
-                a.shared.page[to] = held ? page : -1;
-            }
-            at += __popc(any);
+        if (tid >= s && tid < e) {
+            const unsigned own = (e - s == 32 ? 0xffffffffu : (1u << (e - s)) - 1) << s;
+            a.shared.size[(size_t)kvh * a.n_tokens + t0 + tid] = tid > s ? 0 : (e - s) << SIZE_BITS | (twice & own ? SIZE_MASK : total);
         }
-        for (int i = s + tid; i < e; i += 32 * UNION_WARPS) size[i] = i > s ? 0 : (e - s) << SIZE_BITS | (twice ? SIZE_MASK : total);
-        __syncthreads();  // before the words and `twice` are written again
-        s = e;
-    }
+    });
     if (__any_sync(0xffffffffu, bad) && lane == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
 }
 
@@ -122,8 +170,11 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
     a.shared = Union{reinterpret_cast<uint2 *>(u), ints, ints + ENTRIES};
     a.taken = ints + 2 * ENTRIES;
     cudaError_t e = cudaFuncSetAttribute(listed_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, UNION_BYTES);
-    if (e == cudaSuccess)
-        e = launch_dependent(listed_union_kernel, dim3((a.n_tokens + tokens - 1) / tokens, a.n_kv_heads), dim3(32 * UNION_WARPS), bytes, s, a, tokens, words);
+    // Blocks of eight warps go round sooner, few blocks end sooner with all the warps that
+    // fit: 1984 tokens of 12/1 heads (199 blocks) 139 us in all, 143; 61 rows of 32/8 (16) 86, 81.
+    const dim3 grid((a.n_tokens + tokens - 1) / tokens, a.n_kv_heads);
+    const int warps = grid.x * grid.y > 152 ? 8 : UNION_WARPS;
+    if (e == cudaSuccess) e = launch_dependent(listed_union_kernel, grid, dim3(32 * warps), bytes, s, a, tokens, words);
     if (e == cudaSuccess) e = launch_tiles<S>(a, ws, s);
     if (e == cudaSuccess) e = launch_rows<S>(a, cells, s);
     return e == cudaSuccess ? launch_tiles_join<S>(a, ws, s) : e;

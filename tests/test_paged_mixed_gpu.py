@@ -10,7 +10,7 @@ import torch
 
 from oracle import paged_oracle as po
 from tests.test_paged_gpu import BF16, F16, make_pool, shuffled_table
-from tests.test_paged_pick_gpu import check_tree, tree_workspace, trees
+from tests.test_paged_pick_gpu import alike, check_sparse, check_tree, sparse_workspace, tree_workspace, trees
 
 pytestmark = pytest.mark.gpu
 
@@ -98,3 +98,47 @@ def test_tree_order_decides_how_tokens_are_taken(cuda_device, d, hq, hkv, page, 
     assert [x[2] for x in res] == [[1] * hkv, [0] * hkv]
     torch.testing.assert_close(res[0][0].float(), res[1][0].float(), rtol=2.0 ** -8, atol=2.0 ** -9)
     torch.testing.assert_close(res[0][1], res[1][1], rtol=2.0 ** -18, atol=2.0 ** -14)
+
+
+# ---------------------------------------------------------------- listed rows of several kinds
+
+@pytest.mark.parametrize("otype", [F16, BF16])
+@pytest.mark.parametrize("d,hq,hkv,page,runs,base,most,together", [
+    (128, 8, 2, 64, [300] + [1] * 40, 5000, 40, 1), (128, 12, 1, 64, [1] * 17 + [500] + [1] * 8, 6000, 40, 1),
+    (128, 8, 2, 64, [9] * 34, 5000, 40, 1), (256, 24, 2, 32, [1, 2, 1, 3] + [170] + [1] * 23, 4000, 60, 1), (128, 16, 1, 16, [5, 3] * 60, 4000, 99, 0),
+    (128, 32, 8, 32, [1] * 70, 2000, 50, 0)])
+def test_listed_rows_beside_a_chunk_leave_it_together(cuda_device, d, hq, hkv, page, runs, base, most, together, otype):
+    """Rows without neighbours, in whole blocks of them, do not keep others from their groups; without others they go one by one."""
+    rng = np.random.default_rng(len(runs))
+    pool, table, lens, rows, lists, counts = alike(rng, runs, base, page, hkv, d, most + 2, most, 71)
+    n = len(rows)
+    counts[rng.integers(0, n, 4)] = 0
+    lens[n // 3] = 0
+    q, gate = rng.standard_normal((n, hq, d)), rng.standard_normal((n, hq, d)).astype(np.float32)
+
+    def run(want_err, lists=lists, table=table, rows=rows):
+        ws = sparse_workspace(hq, hkv, d)
+        check_sparse(q, pool, table, lens, lists, counts, rows=rows, otype=otype, gate=gate, ws=ws)
+        assert po.sparse_cells(table, lens, lists, counts, page, pool[0].shape[0], rows)[1] == want_err
+        assert decided(ws, hkv) == [together] * hkv
+
+    run(0)
+    if otype is F16:
+        return
+    # What a row by itself reports.
+    t = next(i for i in range(n - 1, -1, -1) if counts[i, 0] > 3 and lens[i])
+    x = lists.copy()
+    x[t, 0, 2] = table.shape[1]
+    run(po.BAD_ID, lists=x)
+    x = table.copy()
+    x[rows[t], lists[t, 0, 1]] = -1
+    run(po.BAD_ID, table=x)
+    x = list(rows)
+    x[t] = len(table)
+    run(po.BAD_ID, rows=x)
+    # A page twice in the list of a row without neighbours: it counts twice there, and says nothing about others.
+    t = next((i for i in range(n) if rows.count(rows[i]) == 1 and counts[i, 0] > 3 and lens[i]), None)
+    if t is not None:
+        x = lists.copy()
+        x[t, 0, 1] = x[t, 0, 2]
+        run(0, lists=x)

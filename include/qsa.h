@@ -620,7 +620,10 @@ typedef struct {
  * counts[t, h], of its sequence (page numbers as in scores and the table's
  * columns, in any order).  -1 is padding; a page listed twice counts twice.
  * Consecutive rows of one sequence whose lists are alike go together over the
- * pages that any of them lists, where that saves time.  Otherwise as
+ * pages that any of them lists, where that saves time.  (Not where n_kv_heads *
+ * width is above 8192, of a call with n_tokens * n_kv_heads * width above 2^20,
+ * nor beyond some 24,000 to 98,000 max_pages: a row's bits of pages times the
+ * rows of a group have 96 KB.)  Otherwise as
  * qsa_paged_attn (out, gate, lse, rows, range of values, rows that see
  * nothing).  A count outside [0, width] is cut to that range; a page number
  * below -1 or from max_pages on is left out, as is a page whose table entry is

@@ -155,15 +155,17 @@ __global__ void __launch_bounds__(32 * UNION_WARPS) listed_union_kernel(const Li
 size_t rows_bytes(int per, int head_dim) { return (Work::bytes(MAX_CTAS, per, head_dim) + 255) / 256 * 256; }
 size_t tiles_bytes(int head_dim) { return (Work::bytes(MAX_GROUP_PARTS, GROUP_ROWS, head_dim) + 255) / 256 * 256; }
 
+// Words of a row's bits of pages.
+int bit_words(const ListedArgs &a) { return (a.max_pages + 31) / 32; }
+
+// a: rows that groups may be taken of, with no more list entries than ENTRIES.
 template <int S>
-cudaError_t launch(ListedArgs a, cudaStream_t s) {
+cudaError_t launch_slice(ListedArgs a, cudaStream_t s) {
     const long long cells = (long long)a.width * a.page_size, heads = (long long)a.n_tokens * a.n_kv_heads;
-    const int per = a.n_q_heads / a.n_kv_heads, tokens = group_tokens(per), words = (a.max_pages + 31) / 32;
-    const size_t bytes = sizeof(unsigned) * tokens * (size_t)(words | 1);
-    // Groups, where they can be had and like lists would save enough: a tile then does
-    // for four units of each of a group's rows.
-    const bool may = a.rows && a.n_tokens >= 4 && tokens >= 4 && shared_out<S>(a, cells) && a.n_kv_heads <= MAX_GROUP_PARTS / 2 &&
-                     heads * a.width <= ENTRIES && bytes <= UNION_BYTES && heads * (cells / Shape<S>::UNIT) * (tokens - 2) * 10 > (long long)CALL_COST * tokens;
+    const int per = a.n_q_heads / a.n_kv_heads, tokens = group_tokens(per), words = bit_words(a);
+    // Groups, where like lists would save enough: a tile then does for four units of each
+    // of a group's rows.
+    const bool may = a.n_tokens >= 4 && heads * (cells / Shape<S>::UNIT) * (tokens - 2) * 10 > (long long)CALL_COST * tokens;
     if (!may) return launch_rows<S>(a, cells, s);
     uint8_t *ws = static_cast<uint8_t *>(a.workspace) + rows_bytes(per, a.head_dim), *u = ws + tiles_bytes(a.head_dim);
     int *const ints = reinterpret_cast<int *>(u + ENTRIES * sizeof(uint2));
@@ -174,10 +176,45 @@ cudaError_t launch(ListedArgs a, cudaStream_t s) {
     // fit: 1984 tokens of 12/1 heads (199 blocks) 139 us in all, 143; 61 rows of 32/8 (16) 86, 81.
     const dim3 grid((a.n_tokens + tokens - 1) / tokens, a.n_kv_heads);
     const int warps = grid.x * grid.y > 152 ? 8 : UNION_WARPS;
-    if (e == cudaSuccess) e = launch_dependent(listed_union_kernel, grid, dim3(32 * warps), bytes, s, a, tokens, words);
+    if (e == cudaSuccess)
+        e = launch_dependent(listed_union_kernel, grid, dim3(32 * warps), sizeof(unsigned) * tokens * (size_t)(words | 1), s, a, tokens, words);
     if (e == cudaSuccess) e = launch_tiles<S>(a, ws, s);
     if (e == cudaSuccess) e = launch_rows<S>(a, cells, s);
     return e == cudaSuccess ? launch_tiles_join<S>(a, ws, s) : e;
+}
+
+// A call, in slices of tokens whose lists the workspace has room for, one after the other
+// in the same workspace; they end where groups do.  1984 tokens of 32/8 heads, 128 pages of
+// 16: 480 us in two slices, one by one 1805; in lists of 1024, 872 in sixteen.  Slices of
+// fewer than MIN_SLICE tokens could cost more in launches than their groups save (256 rows
+// without neighbours, 32 pages in lists of 1024: 123 us in two slices, one by one 85).
+constexpr long long MIN_SLICE = 128;
+template <int S>
+cudaError_t launch(const ListedArgs &a, cudaStream_t s) {
+    const int tokens = group_tokens(a.n_q_heads / a.n_kv_heads);
+    const long long cells = (long long)a.width * a.page_size, most = ENTRIES / ((long long)a.n_kv_heads * a.width) / tokens * tokens;
+    const bool all = (long long)a.n_tokens * a.n_kv_heads * a.width <= ENTRIES;
+    const bool groups = a.rows && shared_out<S>(a, cells) && a.n_kv_heads <= MAX_GROUP_PARTS / 2 &&
+                        sizeof(unsigned) * tokens * (size_t)(bit_words(a) | 1) <= UNION_BYTES;
+    if (!groups || (!all && most < MIN_SLICE)) return launch_rows<S>(a, cells, s);
+    if (all) return launch_slice<S>(a, s);
+    const long long slices = (a.n_tokens + most - 1) / most, each = ((a.n_tokens + slices - 1) / slices + tokens - 1) / tokens * tokens;
+    cudaError_t e = cudaSuccess;
+    for (long long t = 0; t < a.n_tokens && e == cudaSuccess; t += each) {
+        const size_t head = (size_t)t * a.n_q_heads, list = (size_t)t * a.n_kv_heads, at = head * a.head_dim;
+        ListedArgs x = a;
+        x.n_tokens = (int)std::min(each, a.n_tokens - t);
+        x.q = static_cast<const uint16_t *>(a.q) + at;
+        x.out = static_cast<uint16_t *>(a.out) + at;
+        x.gate = a.gate ? a.gate + at : nullptr;
+        x.lse = a.lse ? a.lse + head : nullptr;
+        x.seq_lens = a.seq_lens + t;
+        x.rows = a.rows + t;
+        x.lists = a.lists + list * a.width;
+        x.counts = a.counts + list;
+        e = launch_slice<S>(x, s);
+    }
+    return e;
 }
 
 }  // namespace

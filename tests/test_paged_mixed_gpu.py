@@ -142,3 +142,40 @@ def test_listed_rows_beside_a_chunk_leave_it_together(cuda_device, d, hq, hkv, p
         x = lists.copy()
         x[t, 0, 1] = x[t, 0, 2]
         run(0, lists=x)
+
+
+@pytest.mark.parametrize("d,hq,hkv,page,runs,base,most,width,otype,last", [
+    (128, 16, 8, 16, [150, 90, 60], 1800, 90, 500, F16, 1), (256, 24, 2, 32, [300], 2500, 60, 2000, BF16, 1),
+    (128, 12, 1, 64, [200, 1, 1, 1, 1, 1, 60], 4000, 40, 7777, F16, 0)])
+def test_listed_calls_of_more_entries_than_the_workspace_holds(cuda_device, d, hq, hkv, page, runs, base, most, width, otype, last):
+    """They go in slices of tokens, each by groups where that saves enough in it (not in the last 85 rows of 80 units of a KV
+    head: 10 * 85 * 80 is less than a call's cost)."""
+    rng = np.random.default_rng(width)
+    pool, table, lens, rows, lists, counts = alike(rng, runs, base, page, hkv, d, width, most, 72)
+    n = len(rows)
+    assert n * hkv * width > 1 << 20
+    q, gate = rng.standard_normal((n, hq, d)), rng.standard_normal((n, hq, d)).astype(np.float32)
+
+    def run(want_err, lists=lists, counts=counts):
+        ws = sparse_workspace(hq, hkv, d)
+        check_sparse(q, pool, table, lens, lists, counts, rows=rows, otype=otype, gate=gate, ws=ws)
+        assert po.sparse_cells(table, lens, lists, counts, page, pool[0].shape[0], rows)[1] == want_err
+        assert decided(ws, hkv) == [last] * hkv  # of the last slice
+
+    run(0)
+    for t in (3, n - 2):  # of the first slice, of the last one
+        x = lists.copy()
+        x[t, hkv - 1, 1] = table.shape[1]
+        run(po.BAD_ID, lists=x)
+    x = counts.copy()
+    x[0], x[n - 1] = 0, 0
+    run(0, counts=x)
+
+
+def test_listed_calls_too_wide_for_groups(cuda_device):
+    """Lists so wide that few rows' fill the workspace: one by one."""
+    rng = np.random.default_rng(9)
+    pool, table, lens, rows, lists, counts = alike(rng, [150], 3000, 16, 4, 128, 2300, 120, 73)
+    ws = sparse_workspace(16, 4, 128)
+    check_sparse(rng.standard_normal((150, 16, 128)), pool, table, lens, lists, counts, rows=rows, ws=ws)
+    assert not by_groups(ws, 16, 4, 128)

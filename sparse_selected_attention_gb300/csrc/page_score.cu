@@ -18,19 +18,24 @@
 // quarter; its products are summed per quarter, and the quarter's scale multiplies in
 // fp32.
 //
-// The tiles of 16 pages of all sequences are shared out evenly over the blocks.
-// Chunks of many tokens go to a grid of 32 tokens by tiles instead: there, one
-// sequence's tokens have pages enough for all, and looking up thousands of tokens
-// would cost more than it evens out.
+// The tiles of 16 pages of all sequences are shared out evenly over the blocks.  From
+// 256 tokens on, where table rows are given, groups hold up to 32 tokens of one sequence,
+// and a tile weighs what its group's tokens make it cost; by 32 tokens whatever they
+// belong to, as a grid of tokens and tiles, 256 rows of one token took 207 us and 1984
+// tokens of a prompt beside 60 such rows 514 where these take 38 and 69 (12 and 57 by
+// themselves).  In us, 48/4 heads of 128, pages of 16, sequences of up to 32 K cells (of one
+// token 8 K; without rows 24): 256 x 1 38, 64 x 4 31, 64 x 8 43, 32 x 16 28, 16 x 32 31.
 //
 // 61 tokens of 4 heads of 128 over pages of 16 of up to 32.7 K cells, 69 MB of bounds:
-// 22.1 us, 3.1 TB/s (15.4 us from L2): issue 47 %, DRAM 37 %, latency of a warp's two
-// tiles on their way.  One token over 469 pages: 4.1 us.
+// 22.4 us, 3.1 TB/s (15.4 us from L2): issue 47 %, DRAM 37 %, latency of a warp's two
+// tiles on their way.  One token over 469 pages: 4.1 us.  1984 tokens over 2 K pages of 16,
+// 12/2 heads of 128: 57 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "check.cuh"
 #include "page_share.cuh"
@@ -63,6 +68,9 @@ __device__ __forceinline__ int sum_exponent(float m) {
     if (u == 0u || u >= 0x7F800000u) return 0;
     return min(max(13 - ((int)(u >> 23) - 127), -120), 120);
 }
+
+// What a tile of a group of n tokens costs: its codes' way to fragments, and products.
+__device__ __forceinline__ int weight_of(int n) { return 4 + (n + 3) / 4; }
 
 // The pages of token t's sequence.
 __device__ __forceinline__ int pages_of(const qsa_page_score_args &a, int t, int &row, bool &bad) {
@@ -106,10 +114,13 @@ __device__ __forceinline__ void cp_async(void *dst, const void *src, bool have) 
                      : "memory");
 }
 
+template <int S, int NT>
+constexpr int CTAS_PER_SM = S == 1 ? (NT == 1 ? 5 : 3) : NT == 1 ? 3 : 2;  // by shared memory
+
 // S = head_dim / 128.  A group: up to 4 NT consecutive tokens of one sequence, not
 // across multiples of 4 NT; without rows, one token.
 template <int S, int NT>
-__global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_score_args a) {
+__global__ void __launch_bounds__(THREADS, CTAS_PER_SM<S, NT>) page_score_kernel(const qsa_page_score_args a) {
     constexpr int D = 128 * S, G = 4 * NT, Q = D / 4, KS = 2 * S;  // k-steps of a quarter
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<S, NT> &sh = *reinterpret_cast<Smem<S, NT> *>(raw);
@@ -128,7 +139,19 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
         tiles = (__reduce_max_sync(0xffffffffu, lane < n ? pages_of(a, u, row, bad) : 0) + TILE - 1) / TILE;
         return n;
     };
-    int t, i0, left, step = 1;  // tiles i0, i0 + step, .. are this block's
+    // This block's: tiles from i0 of the group that starts at t on; one token's, `left` in
+    // all; else those up to the next share's, weights counted from the first token's.
+    int t, i0, left = 0;
+    long long total = 0, share = 0, pos = 0;  // all weights, a share's, those before t
+    // The tile of the group of n tokens at `pos` with which share r starts, which starts in
+    // it: the one whose weight does; a group whose sums cost more than its tiles weigh is
+    // shared out evenly among as many shares as start in it, from its first tile on.
+    auto split = [&](int r, int n, int tiles) {
+        const long long w = weight_of(n), x = share * r;
+        if (n <= 8) return (int)((x - pos + w - 1) / w);
+        const int first = (int)((pos + share - 1) / share), m = (int)((pos + tiles * w + share - 1) / share) - first;
+        return (int)((long long)(r - first) * tiles / m);
+    };
     if constexpr (NT == 1) {
         auto tiles_of = [&](int t) {  // of the group that starts at t; 0 where none does
             int row, most = pages_of(a, t, row, bad);
@@ -142,83 +165,199 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
         };
         find_share(sh.found, a.n_tokens, range, ranges, 1, tiles_of, t, i0, left);
     } else {
-        // Block x of those that take the 32 tokens' groups.
-        const int blocks = (a.n_tokens + G - 1) / G;
-        step = ranges / blocks;
-        t = range % blocks * G;
-        left = min(a.n_tokens - t, G);  // tokens
-        i0 = range / blocks;
+        // Spans of 32 tokens, a quarter of them by each warp, a lane a token: the group that
+        // starts there, if one does, weighs its tiles' weight.  All of them; then where the
+        // share starts, by the warp that has it.  Not unrolled: it runs once.
+        const int spans = (a.n_tokens + 31) / 32, run = (spans + W - 1) / W, s0 = min(warp * run, spans), s1 = min(s0 + run, spans);
+        long long mine = 0, at = 0, x = 0;
+#pragma unroll 1
+        for (int pass = 0; pass < 2; ++pass) {
+            if (pass) {
+                if (lane == 0) sh.found.part[warp] = mine;
+                __syncthreads();
+#pragma unroll 1
+                for (int w = 0; w < W; ++w) {
+                    at += w < warp ? sh.found.part[w] : 0;
+                    total += sh.found.part[w];
+                }
+                share = max((total + ranges - 1) / ranges, 1ll);
+                x = share * range;
+                if (x < at || x >= at + mine) break;
+            }
+            int next_row = 0, next_pages = 0;
+            auto load = [&](int s) {
+                const int u = 32 * s + lane;
+                next_row = next_pages = 0;
+                if (s < s1 && u < a.n_tokens) {
+                    int row;
+                    next_row = __ldg(a.rows + u);
+                    next_pages = pages_of(a, u, row, bad);
+                }
+            };
+            load(s0);
+#pragma unroll 1
+            for (int s = s0; s < s1; ++s) {
+                const int own = next_row, n = min(a.n_tokens - 32 * s, 32), before = __shfl_up_sync(0xffffffffu, own, 1);
+                int most = next_pages, end = n;  // of the tokens from this one on; where its group ends
+                load(s + 1);
+                const unsigned starts = __ballot_sync(0xffffffffu, lane < n && (lane == 0 || own != before));
+                if (starts == 1u) {
+                    most = __reduce_max_sync(0xffffffffu, most);
+                } else {
+                    const unsigned later = starts & (0xfffffffeu << lane);
+                    if (later) end = __ffs(later) - 1;
+#pragma unroll 1
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int v = __shfl_down_sync(0xffffffffu, most, o);
+                        if (lane + o < end) most = max(most, v);
+                    }
+                }
+                const int w = starts >> lane & 1u ? (most + TILE - 1) / TILE * weight_of(end - lane) : 0;
+                const int all = __reduce_add_sync(0xffffffffu, w);
+                if (!pass || x >= at + all) {
+                    (pass ? at : mine) += all;
+                    continue;
+                }
+                int upto = w;
+#pragma unroll 1
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += v;
+                }
+                if (x >= at + upto - w && x < at + upto) {
+                    sh.found.item = 32 * s + lane;
+                    sh.found.before = at + upto - w;
+                }
+                break;
+            }
+        }
+        __syncthreads();
+        t = i0 = 0;
+        pos = total;
+        if (x < total) {
+            t = sh.found.item;
+            pos = sh.found.before;
+            int tiles;
+            const int n = group_of(t, tiles);
+            i0 = split(range, n, tiles);
+        }
     }
-    while (left > 0) {
+    while (NT == 1 ? left > 0 : pos < total) {
         int tiles;
         const int n = group_of(t, tiles), from = i0;
-        const int i1 = NT == 1 ? min(tiles, i0 + left) : tiles;
+        const bool last = NT > 1 && share * (range + 1) < pos + (long long)tiles * weight_of(n);  // the share ends in this group
+        const int i1 = NT == 1 ? min(tiles, i0 + left) : last ? split(range + 1, n, tiles) : tiles;
         if (i1 > from) {
-            // The tokens' sums: a thread takes two dims of a token.
+            // The tokens' sums: a thread takes V dims of a token, of 32 tokens eight, so that a
+            // token's are in one warp and the loads of all tokens are on their way together.
+            constexpr int V = NT == 1 ? 2 : 8, LANES = D / V, AT_ONCE = THREADS / LANES, ROUNDS = (G + AT_ONCE - 1) / AT_ONCE;
+            constexpr int AT_A_TIME = NT == 1 ? 8 : 8 / ROUNDS;  // heads whose loads are on their way together
+            using Word = std::conditional_t<NT == 1, uint32_t, uint4>;
             __syncthreads();  // of the group before
             if (tid < G) {
                 int row;
                 sh.top[tid] = 0u;
                 sh.pages[tid] = tid < n ? pages_of(a, t + tid, row, bad) : 0;
             }
-            __syncthreads();
-            constexpr int AT_A_TIME = NT == 1 ? 8 : 4;  // heads whose loads are on their way together
-            constexpr int PAIRS = D / 2, AT_ONCE = THREADS / PAIRS, ROUNDS = (G + AT_ONCE - 1) / AT_ONCE;
-            const int d = tid % PAIRS * 2, first = tid / PAIRS;
-            // Place of dims d, d + 1 (of different halves of a k-step) as codes of a quarter.
-            const int in = d % Q, rr = in / (8 * S), e = in % (8 * S), ks = d / Q * KS + e / 4;
-            float2 up[ROUNDS], down[ROUNDS];
+            if constexpr (NT == 1) __syncthreads();
+            const int d = tid % LANES * V, first = tid / LANES;
+            float2 up[ROUNDS][V / 2], down[ROUNDS][V / 2];
 #pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int k = first + i * AT_ONCE;
-                up[i] = down[i] = make_float2(0.0f, 0.0f);
-                if (k < n) {
-                    const size_t at = ((size_t)(t + k) * a.n_q_heads + (size_t)kvh * per) * D + d;
+            for (int i = 0; i < ROUNDS; ++i)
+#pragma unroll
+                for (int p = 0; p < V / 2; ++p) up[i][p] = down[i][p] = make_float2(0.0f, 0.0f);
+            const size_t at = ((size_t)(t + first) * a.n_q_heads + (size_t)kvh * per) * D + d, next = (size_t)AT_ONCE * a.n_q_heads * D;
+            auto load = [&](int i, int h) {
+                const size_t from = at + i * next + (size_t)h * D;
+                return first + i * AT_ONCE < n && h < per && QSA_IN(from + V - 1, (size_t)a.n_tokens * a.n_q_heads * D)
+                           ? __ldg(reinterpret_cast<const Word *>(static_cast<const uint16_t *>(a.q) + from))
+                           : Word{};
+            };
+            auto add = [&](int i, const Word &w) {
+#pragma unroll
+                for (int p = 0; p < V / 2; ++p) {
+                    const uint32_t x = reinterpret_cast<const uint32_t *>(&w)[p];
+                    const float2 v = a.dtype == QSA_F16 ? __half22float2(u2h(x))
+                                                        : make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u));
+                    up[i][p].x += fmaxf(v.x, 0.0f);
+                    up[i][p].y += fmaxf(v.y, 0.0f);
+                    down[i][p].x += fminf(v.x, 0.0f);
+                    down[i][p].y += fminf(v.y, 0.0f);
+                    // A NaN is lost in maximum and minimum.
+                    if (v.x != v.x) up[i][p].x = v.x;
+                    if (v.y != v.y) up[i][p].y = v.y;
+                }
+            };
+            auto top_of = [&](int i) {
+                float m = 0.0f;
+#pragma unroll
+                for (int p = 0; p < V / 2; ++p)
+                    m = fmaxf(m, fmaxf(fmaxf(up[i][p].x, up[i][p].y), fmaxf(-down[i][p].x, -down[i][p].y)));
+                return __float_as_uint(fabsf(m));  // not negative: bits order as values do
+            };
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int i = 0; i < ROUNDS; ++i) {
+                    if (first + i * AT_ONCE >= n) continue;
 #pragma unroll 1
                     for (int h = 0; h < per; h += AT_A_TIME) {
-                        uint32_t w[AT_A_TIME];
+                        Word w[AT_A_TIME];
 #pragma unroll
-                        for (int e = 0; e < AT_A_TIME; ++e)
-                            w[e] = h + e < per && QSA_IN(at + (size_t)(h + e) * D + 1, (size_t)a.n_tokens * a.n_q_heads * D)
-                                       ? __ldg(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.q) + at + (size_t)(h + e) * D))
-                                       : 0u;
+                        for (int e = 0; e < AT_A_TIME; ++e) w[e] = load(i, h + e);
 #pragma unroll
-                        for (int e = 0; e < AT_A_TIME; ++e) {
-                            const float2 v = a.dtype == QSA_F16 ? __half22float2(u2h(w[e]))
-                                                                : make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-                            up[i].x += fmaxf(v.x, 0.0f);
-                            up[i].y += fmaxf(v.y, 0.0f);
-                            down[i].x += fminf(v.x, 0.0f);
-                            down[i].y += fminf(v.y, 0.0f);
-                            // A NaN is lost in maximum and minimum.
-                            if (v.x != v.x) up[i].x = v.x;
-                            if (v.y != v.y) up[i].y = v.y;
-                        }
+                        for (int e = 0; e < AT_A_TIME; ++e) add(i, w[e]);
                     }
-                    const float m = fabsf(fmaxf(fmaxf(up[i].x, up[i].y), fmaxf(-down[i].x, -down[i].y)));
-                    atomicMax(&sh.top[k], __float_as_uint(m));  // not negative: bits order as values do
+                    atomicMax(&sh.top[first + i * AT_ONCE], top_of(i));
+                }
+                __syncthreads();
+            } else {
+#pragma unroll 1
+                for (int h = 0; h < per; h += AT_A_TIME) {
+                    Word w[AT_A_TIME][ROUNDS];
+#pragma unroll
+                    for (int e = 0; e < AT_A_TIME; ++e)
+#pragma unroll
+                        for (int i = 0; i < ROUNDS; ++i) w[e][i] = load(i, h + e);
+#pragma unroll
+                    for (int i = 0; i < ROUNDS; ++i) {
+                        if (i * AT_ONCE >= n) break;
+#pragma unroll
+                        for (int e = 0; e < AT_A_TIME; ++e) add(i, w[e][i]);
+                    }
                 }
             }
-            __syncthreads();
             __half *frag = reinterpret_cast<__half *>(sh.b);
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
                 const int k = first + i * AT_ONCE;
-                if (k >= G) continue;
-                const int ex = sum_exponent(__uint_as_float(sh.top[k]));
+                uint32_t top;
+                if constexpr (NT == 1) {
+                    top = sh.top[k];
+                } else {
+                    top = top_of(i);
+#pragma unroll
+                    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                }
+                if (k >= (n + 3) / 4 * 4) continue;  // no product takes them
+                const int ex = sum_exponent(__uint_as_float(top));
                 const float f = exp2i(ex);
-                if (tid % PAIRS == 0) sh.unscale[k] = exp2i(-ex);
+                if (tid % LANES == 0) sh.unscale[k] = exp2i(-ex);
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float2 v = b ? down[i] : up[i];
+                for (int p = 0; p < V / 2; ++p) {
+                    // Place of dims d + 2 p and the next (of different halves of a k-step) as codes of a quarter.
+                    const int in = (d + 2 * p) % Q, rr = in / (8 * S), e = in % (8 * S), ks = d / Q * KS + e / 4;
 #pragma unroll
-                    for (int odd = 0; odd < 2; ++odd) {
-                        const float x = (odd ? v.y : v.x) * f;
-                        const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
-                        // Column 2 (k % 4) + part, row: register `odd`, half by the pair.
-                        const size_t at = ((((size_t)b * 8 * S + ks) * NT + k / 4) * 32 + (2 * (k % 4)) * 4 + rr) * 4 + odd * 2 + (e % 4) / 2;
-                        frag[at] = hi;
-                        frag[at + 16] = lo;
+                    for (int b = 0; b < 2; ++b) {
+                        const float2 v = b ? down[i][p] : up[i][p];
+#pragma unroll
+                        for (int odd = 0; odd < 2; ++odd) {
+                            const float x = (odd ? v.y : v.x) * f;
+                            const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+                            // Column 2 (k % 4) + part, row: register `odd`, half by the pair.
+                            const size_t at = ((((size_t)b * 8 * S + ks) * NT + k / 4) * 32 + (2 * (k % 4)) * 4 + rr) * 4 + odd * 2 + (e % 4) / 2;
+                            frag[at] = hi;
+                            frag[at + 16] = lo;
+                        }
                     }
                 }
             }
@@ -255,13 +394,13 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
             };
             constexpr int STAGES = Smem<S, NT>::STAGES;
             int st = 0;
-            look(from + warp * step);
+            look(from + warp);
             copy(0);
-            look(from + (warp + W) * step);
-            for (int i = from + warp * step; i < i1; i += W * step, st ^= STAGES - 1) {
+            look(from + warp + W);
+            for (int i = from + warp; i < i1; i += W, st ^= STAGES - 1) {
                 if constexpr (STAGES == 2) {
                     copy(st ^ 1);
-                    look(i + 2 * W * step);
+                    look(i + 2 * W);
                     asm volatile("cp.async.wait_group 1;\n" ::: "memory");
                 } else {
                     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
@@ -269,78 +408,85 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
                 __syncwarp();
                 const unsigned held_now = STAGES == 2 ? held : held >> 16;
                 const bool there[2] = {(held_now >> g & 1u) != 0u, (held_now >> (g + 8) & 1u) != 0u};
-                float y[NT][4];
+                auto products = [&](auto columns) {  // with the sums of the first 4 K tokens
+                    constexpr int K = decltype(columns)::value;
+                    float y[K][4];
 #pragma unroll
-                for (int k = 0; k < NT; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
+                    for (int k = 0; k < K; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint2 sc[2] = {sh.scales[warp][st][b][g], sh.scales[warp][st][b][g + 8]};
-                    const uint8_t *codes = sh.codes[warp][st][b];
+                    for (int b = 0; b < 2; ++b) {
+                        const uint2 sc[2] = {sh.scales[warp][st][b][g], sh.scales[warp][st][b][g + 8]};
+                        const uint8_t *codes = sh.codes[warp][st][b];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float s[2];
+                        for (int q = 0; q < 4; ++q) {
+                            float s[2];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const __half2 h = u2h(q >> 1 ? sc[e].y : sc[e].x);
-                            s[e] = q & 1 ? __high2float(h) : __low2float(h);
-                        }
-                        uint32_t w[2][2 * S];
+                            for (int e = 0; e < 2; ++e) {
+                                const __half2 h = u2h(q >> 1 ? sc[e].y : sc[e].x);
+                                s[e] = q & 1 ? __high2float(h) : __low2float(h);
+                            }
+                            uint32_t w[2][2 * S];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if constexpr (S == 1)
-                                *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(codes + unit_at<S>(g + 8 * e, 2 * q + (r >> 1)) + 8 * (r & 1));
-                            else
-                                *reinterpret_cast<uint4 *>(w[e]) = *reinterpret_cast<const uint4 *>(codes + unit_at<S>(g + 8 * e, 4 * q + r));
-                        }
-                        uint32_t x[KS][4];
+                            for (int e = 0; e < 2; ++e) {
+                                if constexpr (S == 1)
+                                    *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(codes + unit_at<S>(g + 8 * e, 2 * q + (r >> 1)) + 8 * (r & 1));
+                                else
+                                    *reinterpret_cast<uint4 *>(w[e]) = *reinterpret_cast<const uint4 *>(codes + unit_at<S>(g + 8 * e, 4 * q + r));
+                            }
+                            uint32_t x[KS][4];
 #pragma unroll
-                        for (int c = 0; c < KS; ++c) {
-                            x[c][0] = pair(w[0][c], false);
-                            x[c][1] = pair(w[1][c], false);
-                            x[c][2] = pair(w[0][c], true);
-                            x[c][3] = pair(w[1][c], true);
-                        }
+                            for (int c = 0; c < KS; ++c) {
+                                x[c][0] = pair(w[0][c], false);
+                                x[c][1] = pair(w[1][c], false);
+                                x[c][2] = pair(w[0][c], true);
+                                x[c][3] = pair(w[1][c], true);
+                            }
 #pragma unroll
-                        for (int k = 0; k < NT; ++k) {
-                            float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                            for (int k = 0; k < K; ++k) {
+                                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                            for (int c = 0; c < KS; ++c) mma(acc, x[c], sh.b[b][q * KS + c][k][lane]);
-                            y[k][0] = fmaf(acc[0] + acc[1], s[0], y[k][0]);
-                            y[k][2] = fmaf(acc[2] + acc[3], s[1], y[k][2]);
+                                for (int c = 0; c < KS; ++c) mma(acc, x[c], sh.b[b][q * KS + c][k][lane]);
+                                y[k][0] = fmaf(acc[0] + acc[1], s[0], y[k][0]);
+                                y[k][2] = fmaf(acc[2] + acc[3], s[1], y[k][2]);
+                            }
                         }
                     }
-                }
-                __syncwarp();  // the tile has been read
-                if constexpr (STAGES == 1) {
-                    copy(0);
-                    look(i + 2 * W * step);
-                }
-#pragma unroll
-                for (int k = 0; k < NT; ++k) {
-                    const int token = 4 * k + r;
-                    if (token >= n) continue;
-                    const int count = sh.pages[token];
-                    const float f = sh.unscale[token];
-                    float *dst = a.scores + ((size_t)(t + token) * hkv + kvh) * a.ld;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = i * TILE + g + 8 * e;
-                        if (j >= count) continue;
-                        bad |= !there[e];
-                        if (QSA_IN(((size_t)(t + token) * hkv + kvh) * a.ld + j, (size_t)a.n_tokens * hkv * a.ld))
-                            dst[j] = there[e] ? y[k][2 * e] * f : -CUDART_INF_F;
+                    __syncwarp();  // the tile has been read
+                    if constexpr (STAGES == 1) {
+                        copy(0);
+                        look(i + 2 * W);
                     }
-                }
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        const int token = 4 * k + r;
+                        if (token >= n) continue;
+                        const int count = sh.pages[token];
+                        const float f = sh.unscale[token];
+                        float *dst = a.scores + ((size_t)(t + token) * hkv + kvh) * a.ld;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = i * TILE + g + 8 * e;
+                            if (j >= count) continue;
+                            bad |= !there[e];
+                            if (QSA_IN(((size_t)(t + token) * hkv + kvh) * a.ld + j, (size_t)a.n_tokens * hkv * a.ld))
+                                dst[j] = there[e] ? y[k][2 * e] * f : -CUDART_INF_F;
+                        }
+                    }
+                };
+                if (NT == 1 || n <= 4)
+                    products(std::integral_constant<int, 1>{});
+                else if (n <= 16)
+                    products(std::integral_constant<int, NT == 1 ? 1 : 4>{});
+                else
+                    products(std::integral_constant<int, NT>{});
             }
         }
         asm volatile("cp.async.wait_group 0;\n" ::: "memory");
         __syncwarp();
-        if constexpr (NT == 1) {
-            left -= i1 - i0;
-            i0 = 0;
-        } else {
-            left -= n;
-        }
+        if (last) break;
+        if constexpr (NT == 1) left -= i1 - from;
+        pos += (long long)tiles * weight_of(n);
+        i0 = 0;
         t += max(n, 1);
     }
     if (__syncthreads_or(bad) && tid == 0 && a.err) atomicOr(a.err, QSA_DEVERR_BAD_ID);
@@ -348,18 +494,11 @@ __global__ void __launch_bounds__(THREADS) page_score_kernel(const qsa_page_scor
 
 template <int S, int NT>
 cudaError_t launch(const qsa_page_score_args &a, cudaStream_t s) {
-    constexpr int SMEM = (int)sizeof(Smem<S, NT>), CTAS_PER_SM = S == 1 ? (NT == 1 ? 5 : 3) : NT == 1 ? 3 : 2;  // by shared memory
+    constexpr int SMEM = (int)sizeof(Smem<S, NT>);
     cudaError_t e = cudaFuncSetAttribute(page_score_kernel<S, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
     const long long tiles = (a.max_pages + TILE - 1) / TILE;
-    const int resident = std::max(152 * CTAS_PER_SM / a.n_kv_heads, 1);
-    int ranges;
-    if (NT == 1) {
-        ranges = (int)std::min<long long>(a.n_tokens * tiles, resident);
-    } else {
-        const long long blocks = (a.n_tokens + 4 * NT - 1) / (4 * NT);
-        ranges = (int)(blocks * std::max<long long>(std::min<long long>(resident / blocks, (tiles + W - 1) / W), 1));
-    }
+    const int ranges = (int)std::min<long long>(a.n_tokens * tiles, std::max(152 * CTAS_PER_SM<S, NT> / a.n_kv_heads, 1));
     return launch_dependent(page_score_kernel<S, NT>, dim3(ranges * a.n_kv_heads), dim3(THREADS), SMEM, s, a);
 }
 

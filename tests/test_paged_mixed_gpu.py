@@ -8,9 +8,11 @@ import numpy as np
 import pytest
 import torch
 
+import sparse_selected_attention_gb300 as qsa
 from oracle import paged_oracle as po
-from tests.test_paged_gpu import BF16, F16, make_pool, shuffled_table
-from tests.test_paged_pick_gpu import alike, check_sparse, check_tree, sparse_workspace, tree_workspace, trees
+from tests.test_paged_gpu import BF16, F16, dev, i32, make_pool, shuffled_table
+from tests.test_paged_pick_gpu import (alike, check_score, check_sparse, check_tree, make_bounds, sparse_workspace, tree_workspace,
+                                       trees)
 
 pytestmark = pytest.mark.gpu
 
@@ -179,3 +181,69 @@ def test_listed_calls_too_wide_for_groups(cuda_device):
     ws = sparse_workspace(16, 4, 128)
     check_sparse(rng.standard_normal((150, 16, 128)), pool, table, lens, lists, counts, rows=rows, ws=ws)
     assert not by_groups(ws, 16, 4, 128)
+
+
+# ---------------------------------------------------------------- scores
+
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("runs,lo,hi,hkv", [
+    ([1] * 300, 1, 4000, 2), ([300] + [1] * 60, 2000, 6000, 1), ([1, 2, 3, 5, 8, 13, 21, 34, 55, 89, 144], 0, 3000, 4), ([9] * 40, 1, 9000, 1),
+    ([40, 1, 33, 1, 31, 32, 7] * 3, 500, 800, 8), ([1] * 2500, 1, 200, 1), ([700, 1500, 3, 60], 30, 900, 2), ([17, 260], 12, 12, 3)])
+def test_score_of_many_tokens_of_all_kinds(cuda_device, d, runs, lo, hi, hkv):
+    """Every page of every token once, however its tokens are shared out; the others keep what they hold."""
+    rng = np.random.default_rng(len(runs))
+    base = [int(v) for v in rng.integers(lo, hi + 1, len(runs))]
+    lens = [b + i for b, k in zip(base, runs) for i in range(k)]
+    lens[len(lens) // 2], lens[-1] = 0, 1
+    rows = [s for s, k in enumerate(runs) for _ in range(k)]
+    table, pages = shuffled_table([b + k for b, k in zip(base, runs)], 16, 2, rng)
+    order = rng.permutation(len(runs))  # of the sequences' rows in the table
+    table, rows = table[np.argsort(order)], [int(order[r]) for r in rows]
+    bounds = make_bounds(pages, hkv, d, 5)
+    assert check_score(rng.standard_normal((len(lens), 2 * hkv, d)), bounds, table, lens, 16, rows=rows, ld=table.shape[1] + 1) == 0
+    table[rows[0], 0] = pages
+    rows[7] = len(runs)
+    assert check_score(rng.standard_normal((len(lens), 2 * hkv, d)), bounds, table, lens, 16, rows=rows, otype=BF16) == po.BAD_ID
+
+
+def fastest(calls, reps=10, rounds=7):
+    """The least time of each call, captured `reps` times; taken in turn."""
+    graphs, best = [], [float("inf")] * len(calls)
+    for f in calls:
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            for _ in range(reps):
+                f()
+        graphs.append(g)
+    for _ in range(rounds):
+        for i, g in enumerate(graphs):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            torch.cuda.synchronize()
+            best[i] = min(best[i], a.elapsed_time(b))
+    return best
+
+
+def test_score_takes_no_longer_for_neighbours_of_other_kinds(cuda_device):
+    """Rows of one token each, with and without a table row each said, and beside a prompt's chunk: in the time that they take
+    by themselves, a few times over at most (eight and seven times, where tokens were shared out by their number alone)."""
+    rng = np.random.default_rng(77)
+    page, hkv, hq, d = 16, 2, 12, 128
+    lens = [int(v) for v in rng.integers(1, 30000, 256)]
+    table, pages = shuffled_table([31984] + lens, page, 0, rng)
+    bounds = [dev(x) for x in make_bounds(pages, hkv, d, 78)]
+    n = 1024
+    q, t = torch.randn(n + 256, hq, d, device="cuda").half(), dev(table)
+    held = i32([31984 - n + 1 + i for i in range(n)] + lens)
+    rows = i32([0] * n + list(range(1, 257)))
+    scores = torch.zeros(n + 256, hkv, table.shape[1], device="cuda")
+
+    def call(a, b, rows, table=t):
+        return lambda: qsa.qsa_page_score(q[a:b], *bounds, table, held[a:b], scores[a:b], page, rows=rows)
+
+    own = t[1:].contiguous()
+    chunk, single, given, both = fastest([call(0, n, rows[:n]), call(n, n + 256, None, own), call(n, n + 256, rows[n:]), call(0, n + 256, rows)])
+    assert given < 4 * single and both < 2 * (chunk + given), (chunk, single, given, both)

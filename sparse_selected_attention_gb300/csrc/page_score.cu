@@ -351,8 +351,11 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM<S, NT>) page_score_kernel
                         const float2 v = b ? down[i][p] : up[i][p];
 #pragma unroll
                         for (int odd = 0; odd < 2; ++odd) {
-                            const float x = (odd ? v.y : v.x) * f;
-                            const __half hi = __float2half_rn(x), lo = __float2half_rn(x - __half2float(hi));
+                            // Beside an infinite sum the finite ones, which have no power of two
+                            // then, count for nothing.
+                            float x = (odd ? v.y : v.x) * f;
+                            if (top >= 0x7F800000u && fabsf(x) < CUDART_INF_F) x = 0.0f;
+                            const __half hi = __float2half_rn(x), lo = fabsf(x) < CUDART_INF_F ? __float2half_rn(x - __half2float(hi)) : __half(0.0f);
                             // Column 2 (k % 4) + part, row: register `odd`, half by the pair.
                             const size_t at = ((((size_t)b * 8 * S + ks) * NT + k / 4) * 32 + (2 * (k % 4)) * 4 + rr) * 4 + odd * 2 + (e % 4) / 2;
                             frag[at] = hi;

@@ -206,6 +206,34 @@ def test_score_of_many_tokens_of_all_kinds(cuda_device, d, runs, lo, hi, hkv):
     assert check_score(rng.standard_normal((len(lens), 2 * hkv, d)), bounds, table, lens, 16, rows=rows, otype=BF16) == po.BAD_ID
 
 
+@pytest.mark.parametrize("otype", [F16, BF16])
+@pytest.mark.parametrize("d,n", [(128, 5), (256, 5), (128, 300), (256, 300)])
+def test_score_of_infinite_queries(cuda_device, d, n, otype):
+    """An infinite query scores what its products are: infinite by its bound's sign, NaN where that is 0, whatever its other dims hold."""
+    rng = np.random.default_rng(n)
+    table, pages = shuffled_table([900] * 2, 16, 0, rng)
+    b = make_bounds(pages, 2, d, 79)
+    b[0][::3, :, 17] = 0
+    b[1][:, 0, 40] = -np.abs(b[1][:, 0, 40]) - 1
+    q = (rng.standard_normal((n, 8, d)) * 300).astype(np.float32)
+    q[1, 5, 17], q[2, 0, 40], q[3, 2, 9], q[3, 3, 9] = np.inf, -np.inf, np.inf, -np.inf
+    q[4, 6, 17], q[4, 7, 100] = np.inf, np.nan
+    rows = [i % 2 if n < 256 else int(i > n // 2) for i in range(n)]
+    qd, scores = dev(q).to(otype), torch.zeros(n, 2, table.shape[1], device="cuda")
+    qsa.qsa_page_score(qd, *[dev(x) for x in b], dev(table), i32([900] * n), scores, 16, rows=i32(rows))
+    with np.errstate(invalid="ignore"):
+        want, _ = po.page_score(qd.float().cpu().numpy(), *b, table, [900] * n, 16, rows)
+    wild = 0
+    for t in range(n):
+        for h in range(2):
+            s, a, w, m = want[t][h]
+            x, fin = scores[t, h, : len(s)].cpu().numpy().astype(np.float64), np.isfinite(s)
+            np.testing.assert_array_equal(x[~fin], s[~fin])
+            assert (np.abs(x - s)[fin] <= (2.0 ** -19 * a + 2.0 ** -22 * m * w)[fin]).all()
+            wild += int((~fin).any())
+    assert wild == 4
+
+
 def fastest(calls, reps=10, rounds=7):
     """The least time of each call, captured `reps` times; taken in turn."""
     graphs, best = [], [float("inf")] * len(calls)

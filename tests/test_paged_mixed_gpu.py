@@ -37,8 +37,7 @@ def decided(ws, hkv):
 
 # ---------------------------------------------------------------- what trees report
 
-@pytest.mark.parametrize("otype", [F16, BF16])
-@pytest.mark.parametrize("n,hq,hkv,d", [(72, 16, 8, 128), (64, 16, 4, 256), (3, 4, 2, 128)])
+@pytest.mark.parametrize("n,hq,hkv,d,otype", [(72, 16, 8, 128, F16), (64, 16, 4, 256, BF16), (3, 4, 2, 128, F16)])
 def test_tree_reports_what_its_tokens_attend_to(cuda_device, n, hq, hkv, d, otype):
     """Pages that no mask reaches may be missing, whichever way rows are taken; those that one token attends to may not."""
     rng = np.random.default_rng(n)
@@ -125,7 +124,7 @@ def test_listed_rows_beside_a_chunk_leave_it_together(cuda_device, d, hq, hkv, p
         assert decided(ws, hkv) == [together] * hkv
 
     run(0)
-    if otype is F16:
+    if n > 200 or otype is F16:
         return
     # What a row by itself reports.
     t = next(i for i in range(n - 1, -1, -1) if counts[i, 0] > 3 and lens[i])
@@ -165,13 +164,10 @@ def test_listed_calls_of_more_entries_than_the_workspace_holds(cuda_device, d, h
         assert decided(ws, hkv) == [last] * hkv  # of the last slice
 
     run(0)
-    for t in (3, n - 2):  # of the first slice, of the last one
-        x = lists.copy()
-        x[t, hkv - 1, 1] = table.shape[1]
-        run(po.BAD_ID, lists=x)
-    x = counts.copy()
-    x[0], x[n - 1] = 0, 0
-    run(0, counts=x)
+    x, y = lists.copy(), counts.copy()
+    x[3 if d == 128 else n - 2, hkv - 1, 1] = table.shape[1]  # of the first slice, or the last one
+    y[0], y[n - 1] = 0, 0
+    run(po.BAD_ID, lists=x, counts=y)
 
 
 def test_listed_calls_too_wide_for_groups(cuda_device):
@@ -275,3 +271,31 @@ def test_score_takes_no_longer_for_neighbours_of_other_kinds(cuda_device):
     own = t[1:].contiguous()
     chunk, single, given, both = fastest([call(0, n, rows[:n]), call(n, n + 256, None, own), call(n, n + 256, rows[n:]), call(0, n + 256, rows)])
     assert given < 4 * single and both < 2 * (chunk + given), (chunk, single, given, both)
+
+
+# ---------------------------------------------------------------- which kernels ran
+
+@pytest.mark.parametrize("form,otype", [("tree", F16), ("listed", BF16)])
+@pytest.mark.parametrize("d,hq,hkv,page,n,cells,together", [
+    (128, 16, 8, 32, 72, 1700, 1), (256, 16, 8, 32, 72, 1700, 1), (128, 12, 1, 64, 340, 2600, 1), (256, 24, 2, 16, 130, 1800, 1), (128, 32, 8, 32, 90, 1600, 1),
+    (128, 8, 1, 128, 200, 500, 0), (128, 12, 1, 64, 190, 190, 0), (128, 12, 1, 64, 40, 2000, 0), (256, 8, 8, 64, 3, 900, 0)])
+def test_groups_are_taken_where_they_save_time(cuda_device, form, d, hq, hkv, page, n, cells, together, otype):
+    """Tokens of one sequence, all of whose pages they see: by the partials that each kind leaves and by what the device wrote down."""
+    rng = np.random.default_rng(n)
+    table, pages = shuffled_table([cells], page, 1, rng)
+    pool = make_pool(pages, page, hkv, d, seed=80)
+    lens, rows, wide = [cells - n + i + 1 for i in range(n)], [0] * n, table.shape[1]
+    q = rng.standard_normal((n, hq, d))
+    if form == "tree":
+        ws = tree_workspace(hq, hkv, d)
+        mask = np.packbits(np.tril(np.ones((n, -(-n // 32) * 32), bool)), axis=1, bitorder="little").view(np.int32)
+        check_tree(q, pool, table, [cells - n] * n, mask, rows=rows, otype=otype, ws=ws)
+    else:
+        ws = sparse_workspace(hq, hkv, d)
+        lists = np.broadcast_to(np.arange(wide, dtype=np.int32), (n, hkv, wide)).copy()
+        check_sparse(q, pool, table, lens, lists, np.full((n, hkv), wide, np.int32), rows=rows, otype=otype, ws=ws)
+    assert by_groups(ws, hq, hkv, d) == bool(together)
+    if together:  # then the kernel of rows one by one has none
+        assert decided(ws, hkv) == [1] * hkv and bool((ws[: 304 // hkv * hkv * 16].view(torch.int32)[::4] == -1).all())
+    else:
+        assert 1 not in decided(ws, hkv)

@@ -316,7 +316,8 @@ struct State {
 // alone (61 rows of 48/4 heads of 128; 90 rows of 18 K cells, one head of 256).
 // Of short ones, a few cells carry the result (1.2e-6 of lse, 1.5 times the
 // output's rounding), and the time is latency: so EXACT goes with short tables
-// (short rows of a wide table go with the long ones).
+// (short rows of a wide table go with the long ones), and of listed rows and drafts
+// with rows of up to WHOLE units (61 listed rows of up to 2 K cells 48 us, 47 without).
 template <int S, bool EXACT>
 __device__ __forceinline__ void compute_unit(const uint8_t *K, uint32_t V, const uint2 *KS, const uint2 *VS, const uint4 (*q)[32],
                                              const float (*bias)[8][4], float *ve, float *vw, unsigned vmask, State<S> &st,
@@ -704,8 +705,18 @@ __global__ void __launch_bounds__(W * 32, W == 1 ? SMALL_PER_SM : CTAS_PER_SM)
                 }
                 __syncwarp();
                 const uint8_t *k = sh.tile[warp][stage][0];
-                compute_unit<S, WHOLE_ROWS>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q, sh.bias,
-                                            sh.ve[warp], sh.vw[warp], vmask, st, sl2);
+                auto compute = [&](auto exact) {
+                    compute_unit<S, decltype(exact)::value>(k, tc::smem_u32(k) + TILE, sh.scale[warp][stage][0], sh.scale[warp][stage][1], sh.q,
+                                                            sh.bias, sh.ve[warp], sh.vw[warp], vmask, st, sl2);
+                };
+                if constexpr ((LISTED<A> || TREE<A>) && !WHOLE_ROWS) {
+                    if (nu <= WHOLE)
+                        compute(std::true_type{});
+                    else
+                        compute(std::false_type{});
+                } else {
+                    compute(std::integral_constant<bool, WHOLE_ROWS>{});
+                }
             }
             __syncwarp();  // every lane has read the stage before it is filled again
             vmask = vnext;

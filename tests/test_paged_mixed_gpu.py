@@ -299,3 +299,36 @@ def test_groups_are_taken_where_they_save_time(cuda_device, form, d, hq, hkv, pa
         assert decided(ws, hkv) == [1] * hkv and bool((ws[: 304 // hkv * hkv * 16].view(torch.int32)[::4] == -1).all())
     else:
         assert 1 not in decided(ws, hkv)
+
+
+# ---------------------------------------------------------------- digits
+
+@pytest.mark.parametrize("form", ["listed", "tree"])
+@pytest.mark.parametrize("d,hq,hkv,n", [(128, 12, 2, 5), (256, 6, 2, 5), (128, 16, 1, 200), (256, 6, 2, 90)])
+def test_short_rows_have_exact_scores_behind_wide_lists_and_long_rows(cuda_device, form, d, hq, hkv, n):
+    """As tests/test_paged_accuracy_gpu.py derives for short tables: whole-number scores have no rounding but the scale's.
+    A row of one cell has them whatever its list's width, its table's and its neighbours' lengths are."""
+    rng = np.random.default_rng(81)
+    long = 1200
+    table, pages = shuffled_table([long] + [1] * (n - 1), 16, 1, rng)
+    pool = make_pool(pages, 16, hkv, d, seed=82)
+    pool[2][:] = 2.0 ** -7
+    q = rng.integers(0, 2048, (n, hq, d)).astype(np.float64)
+    scale, per = 2.0 ** -12, hq // hkv
+    prod = q * np.repeat(pool[0][table[:, 0], 0].astype(np.float64), per, 1)
+    assert np.abs(prod.reshape(n, hq, 4, -1)).sum(-1).max() < 2 ** 24 and np.abs(np.cumsum(prod, -1)).max() < 2 ** 24
+    s = torch.from_numpy(prod.sum(-1) * 2.0 ** -19).cuda()[1:]
+    qd = dev(q.astype(np.float16))
+    out, lse = torch.empty_like(qd), torch.empty(n, hq, device="cuda")
+    args = [qd, *[dev(x) for x in pool], dev(table)]
+    if form == "listed":
+        lists = np.full((n, hkv, table.shape[1]), -1, np.int32)
+        lists[:, :, 0], lists[0] = 0, np.arange(table.shape[1])
+        counts = np.ones((n, hkv), np.int32)
+        counts[0] = -(-long // 16)
+        qsa.qsa_paged_sparse_attn(*args, i32([long] + [1] * (n - 1)), dev(lists), dev(counts), out, sparse_workspace(hq, hkv, d), lse=lse,
+                                  softmax_scale=scale)
+    else:
+        qsa.qsa_paged_tree_attn(*args, i32([long - 1] + [0] * (n - 1)), dev(np.ones((n, 1), np.int32)), out, tree_workspace(hq, hkv, d), lse=lse,
+                                softmax_scale=scale)
+    assert ((lse[1:].double() - s).abs() <= 2.0 ** -21 * s.abs() + 2.0 ** -21).all(), ((lse[1:].double() - s).abs() / s.abs()).max()

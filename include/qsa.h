@@ -657,9 +657,16 @@ typedef struct {
  * node's mask has the bits of itself and of the nodes that lead to it; a row
  * that sees nothing (a padding token: prefix 0, mask 0) gives out = +0 and lse =
  * -inf.  Consecutive rows of one sequence are read together where that saves
- * time; without rows each goes by itself (the form for single tokens).
- * Otherwise as qsa_paged_attn; a bit at or past max_pages * page_size is
- * left out and sets QSA_DEVERR_BAD_ID.
+ * time (so a sequence's tokens are best given one after the other); without rows
+ * each goes by itself (the form for single tokens).  Otherwise as
+ * qsa_paged_attn; a bit at or past max_pages * page_size is left out and sets
+ * QSA_DEVERR_BAD_ID.
+ * An accepted path goes on in cells prefix, prefix + 1, ..: the caller copies the
+ * rows of kq, vq, ksc and vsc (of all layers) there from its nodes' cells, from
+ * the first on (a node's number is not below its depth, and its key holds the
+ * rotation of the position that it was prepared with), sets the length to
+ * prefix + accepted, and calls qsa_page_bounds for the pages from the prefix's
+ * last on, whose bounds may still be those of cells that are gone.
  *
  * prefix_lens int32 [n_tokens]; mask int32 [n_tokens, words], 1 <= words <=
  * QSA_TREE_MAX_WORDS.  workspace: at least

@@ -27,7 +27,7 @@
 // token 8 K; without rows 24): 256 x 1 38, 64 x 4 31, 64 x 8 43, 32 x 16 28, 16 x 32 31.
 //
 // 61 tokens of 4 heads of 128 over pages of 16 of up to 32.7 K cells, 69 MB of bounds:
-// 22.4 us, 3.1 TB/s (15.4 us from L2): issue 47 %, DRAM 37 %, latency of a warp's two
+// 22.5 us, 3.1 TB/s (15.4 us from L2): issue 47 %, DRAM 37 %, latency of a warp's two
 // tiles on their way.  One token over 469 pages: 4.1 us.  1984 tokens over 2 K pages of 16,
 // 12/2 heads of 128: 57 us.
 #include <cuda_bf16.h>

@@ -14,8 +14,6 @@
 
 namespace qsa {
 
-// What a row of q attends to.  qsa_paged_attn_args alone: all cells of its sequence
-// up to its length.
 // What a group of listed rows goes through: the pages that any of them lists, in order.
 // By KV head and the group's first row.
 struct Union {
@@ -23,6 +21,8 @@ struct Union {
     int *page;    // its place in the pool, -1 outside
     int *size;    // [n_kv_heads][n_tokens]: rows << SIZE_BITS | pages (SIZE_MASK: not to be taken), or 0: no group starts
 };
+// What a row of q attends to.  qsa_paged_attn_args alone: all cells of its sequence
+// up to its length.
 struct ListedArgs : qsa_paged_attn_args {  // cells of listed pages, a list per KV head
     const int32_t *lists, *counts;         // [n_tokens][n_kv_heads][width], [n_tokens][n_kv_heads]
     int width;

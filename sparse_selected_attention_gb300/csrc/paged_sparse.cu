@@ -8,7 +8,7 @@
 // tokens, 12/1 heads of 128: 138 us by groups (cold: union 8, groups 132, join 12), 229
 // one by one.  Lists that turn out not to be alike pay 11 to 14 us for the attempt.
 //
-// Rows one by one: 61 rows of 2 K cells, 48/4 heads of 128, 146 MB: 46.4 us, 3.1 TB/s,
+// Rows one by one: 61 rows of 2 K cells, 48/4 heads of 128, 146 MB: 47.8 us, 3.1 TB/s,
 // thirteen units a warp between some 20 us of launch, first loads and ends of rows.
 #include "paged_tiles.cuh"
 

@@ -29,8 +29,8 @@
 // another.  Tiles whose scales do not (or K's not within 2^16: rare, by a few odd
 // cells) are marked, and take a power of two per cell.
 //
-// What bounds it.  24 trees of 16 to 32 tokens over up to 8 K cells, 32/8 heads of 128: 127 us,
-// 370 TFLOP/s; 63 tokens over 30 K cells, 24/2 of 256: 97 us, 480 TFLOP/s; 1984 tokens
+// What bounds it.  24 trees of 16 to 32 tokens over up to 8 K cells, 32/8 heads of 128: 132 us,
+// 355 TFLOP/s; 63 tokens over 30 K cells, 24/2 of 256: 100 us, 465 TFLOP/s; 1984 tokens
 // over 2 K listed cells each, 12/1 of 128: 138 us.  Tensor pipe 39 to 42 % busy, issue
 // slots 67 %: a tile of 128 cells takes 4.1 K cycles, of which its products take 2.1 K, the
 // conversion of K 3 K, the softmax of one set 5 K of 8.2 K.  Each role is near its own

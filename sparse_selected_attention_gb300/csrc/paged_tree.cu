@@ -22,7 +22,7 @@ cudaError_t launch(TreeArgs a, cudaStream_t s) {
     const long long most = (long long)a.n_tokens * a.n_kv_heads * (cells / Shape<S>::UNIT) * 10;
     // The lengths and the order of the tokens say which kind is taken, and those only the
     // device knows.  (Together unseen, 24 trees of 16 to 32 tokens, 32/8 heads, would take
-    // 127 us, not 131, but given level by level, rows 0, 1, 2, .., 0, 1, 2, .., 2600, where
+    // 127 us, not 132, but given level by level, rows 0, 1, 2, .., 0, 1, 2, .., 2600, where
     // one by one they take 1150.)  With more KV heads than there are places for partials,
     // no kind has more than one CTA for a head, and all go together.
     const bool both = a.n_kv_heads <= MAX_GROUP_PARTS;

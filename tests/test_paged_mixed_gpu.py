@@ -10,7 +10,7 @@ import torch
 
 import sparse_selected_attention_gb300 as qsa
 from oracle import paged_oracle as po
-from tests.test_paged_gpu import BF16, F16, dev, i32, make_pool, shuffled_table
+from tests.test_paged_gpu import BF16, F16, Serving, dev, i32, make_pool, shuffled_table
 from tests.test_paged_pick_gpu import (alike, check_score, check_sparse, check_tree, make_bounds, sparse_workspace, tree_workspace,
                                        trees)
 
@@ -332,3 +332,60 @@ def test_short_rows_have_exact_scores_behind_wide_lists_and_long_rows(cuda_devic
         qsa.qsa_paged_tree_attn(*args, i32([long - 1] + [0] * (n - 1)), dev(np.ones((n, 1), np.int32)), out, tree_workspace(hq, hkv, d), lse=lse,
                                 softmax_scale=scale)
     assert ((lse[1:].double() - s).abs() <= 2.0 ** -21 * s.abs() + 2.0 ** -21).all(), ((lse[1:].double() - s).abs() / s.abs()).max()
+
+
+# ---------------------------------------------------------------- after a tree
+
+def test_an_accepted_path_is_moved_behind_its_prefix(cuda_device):
+    """A tree's cells lie as its nodes were numbered.  Copied one after the other behind the prefix, the accepted ones are
+    what the same tokens make when they are appended, and the sequence goes on from there."""
+    make = lambda: Serving(2, hq=12, hkv=2, page=16, pages=40, wide=16)  # noqa: E731
+    a, b = make(), make()
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    rand = lambda n: torch.randn(n, 16, 128, generator=gen, device="cuda").half()  # noqa: E731
+    empty = lambda n: torch.empty(n, 12, 128, dtype=F16, device="cuda")  # noqa: E731
+    prompts = rand(37 + 46)
+    for s in (a, b):
+        s.update(None, i32(37, 46))
+        s.write(prompts, empty(len(prompts)))
+    parent, path = [-1, 0, 0, 1, 2, 2, 5, -1, 7, 6], [0, 2, 5, 6, 9]
+    depth, sees = [], np.zeros((len(parent), 32), bool)
+    for i, p in enumerate(parent):
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+        sees[i] = sees[p] if p >= 0 else False
+        sees[i, i] = True
+    x, n = rand(len(parent)), len(parent)
+    a.update(None, i32(0, n))
+    q, out, err = empty(n), empty(n), a.err
+    qsa.qsa_paged_prep(x[:, :12], x[:, 12:14], x[:, 14:], i32([46 + k for k in depth]), a.slots[:n], *a.layer(), q, q_norm_w=a.w, k_norm_w=a.w,
+                       inv_freq=a.freq, err=err)
+    mask = dev(np.packbits(sees, axis=1, bitorder="little").view(np.int32))
+    qsa.qsa_paged_tree_attn(q, *a.layer(), a.table, i32([46] * n), mask, out, tree_workspace(12, 2, 128), rows=i32([1] * n), err=err)
+
+    def cells(c):
+        c = torch.as_tensor(c, device="cuda")
+        return a.table[1].long()[c // 16] * 16 + c % 16
+
+    src, dst = cells([46 + i for i in path]), cells([46 + k for k in range(len(path))])
+    for t in a.pool:
+        rows = t.flatten(1, 2)
+        rows[:, dst] = rows[:, src]
+    a.lens[1] = 46 + len(path)
+    # The same tokens appended, each attending to what is before it.
+    b.update(None, i32(0, len(path)))
+    qb, ob = empty(len(path)), empty(len(path))
+    b.write(x[path], qb)
+    qsa.qsa_paged_attn(qb, *b.layer(), b.table, i32([47 + k for k in range(len(path))]), ob, b.aws, rows=i32([1] * len(path)), err=b.err)
+    assert torch.equal(q[path], qb)
+    torch.testing.assert_close(out[path].float(), ob.float(), rtol=2.0 ** -9, atol=2.0 ** -10)
+    for _ in range(3):
+        for r in range(2):
+            assert all(torch.equal(y, z) for y, z in zip(a.kv(r), b.kv(r)))
+        y = rand(2)
+        for s in (a, b):
+            s.update(None, i32(1, 1))
+            s.q, s.o = empty(2), empty(2)
+            s.write(y, s.q)
+            s.attend(s.q, s.o)
+        assert torch.equal(a.o, b.o) and a.lens.tolist() == b.lens.tolist()
+    assert int(a.err.item()) == 0 and int(b.err.item()) == 0

@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(THREADS, CTAS_PER_SM<S, NT>) page_score_kernel
             i0 = split(range, n, tiles);
         }
     }
-    while (NT == 1 ? left > 0 : pos < total) {
+    while (t < a.n_tokens && (NT == 1 ? left > 0 : pos < total)) {
         int tiles;
         const int n = group_of(t, tiles), from = i0;
         const bool last = NT > 1 && share * (range + 1) < pos + (long long)tiles * weight_of(n);  // the share ends in this group

@@ -5,7 +5,7 @@
 // taken by groups over the pages that any of a group's rows lists (paged_tiles.cuh),
 // else one by one (paged_rows.cuh).  What the groups go through is found by a kernel
 // before; both kinds then start, and one of them finds that it has nothing to do.  Those
-// tokens, 12/1 heads of 128: 138 us by groups (cold: union 8, groups 132, join 12), 229
+// tokens, 12/1 heads of 128: 138 us by groups (cold: union 10, groups 132, join 12), 229
 // one by one.  Lists that turn out not to be alike pay 11 to 14 us for the attempt.
 //
 // Rows one by one: 61 rows of 2 K cells, 48/4 heads of 128, 146 MB: 47.8 us, 3.1 TB/s,
@@ -185,18 +185,18 @@ cudaError_t launch_slice(ListedArgs a, cudaStream_t s) {
 
 // A call, in slices of tokens whose lists the workspace has room for, one after the other
 // in the same workspace; they end where groups do.  1984 tokens of 32/8 heads, 128 pages of
-// 16: 480 us in two slices, one by one 1805; in lists of 1024, 872 in sixteen.  Slices of
-// fewer than MIN_SLICE tokens could cost more in launches than their groups save (256 rows
+// 16: 480 us in two slices, one by one 1805; in lists of 1024, 872 in sixteen.  Slices of not
+// even MIN_SLICE tokens could cost more in launches than their groups save (256 rows
 // without neighbours, 32 pages in lists of 1024: 123 us in two slices, one by one 85).
 constexpr long long MIN_SLICE = 128;
 template <int S>
 cudaError_t launch(const ListedArgs &a, cudaStream_t s) {
     const int tokens = group_tokens(a.n_q_heads / a.n_kv_heads);
-    const long long cells = (long long)a.width * a.page_size, most = ENTRIES / ((long long)a.n_kv_heads * a.width) / tokens * tokens;
+    const long long cells = (long long)a.width * a.page_size, fit = ENTRIES / ((long long)a.n_kv_heads * a.width), most = fit / tokens * tokens;
     const bool all = (long long)a.n_tokens * a.n_kv_heads * a.width <= ENTRIES;
     const bool groups = a.rows && shared_out<S>(a, cells) && a.n_kv_heads <= MAX_GROUP_PARTS / 2 &&
                         sizeof(unsigned) * tokens * (size_t)(bit_words(a) | 1) <= UNION_BYTES;
-    if (!groups || (!all && most < MIN_SLICE)) return launch_rows<S>(a, cells, s);
+    if (!groups || (!all && fit < MIN_SLICE)) return launch_rows<S>(a, cells, s);
     if (all) return launch_slice<S>(a, s);
     const long long slices = (a.n_tokens + most - 1) / most, each = ((a.n_tokens + slices - 1) / slices + tokens - 1) / tokens * tokens;
     cudaError_t e = cudaSuccess;

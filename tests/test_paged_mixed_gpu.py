@@ -170,13 +170,14 @@ def test_listed_calls_of_more_entries_than_the_workspace_holds(cuda_device, d, h
     run(po.BAD_ID, lists=x, counts=y)
 
 
-def test_listed_calls_too_wide_for_groups(cuda_device):
-    """Lists so wide that few rows' fill the workspace: one by one."""
+@pytest.mark.parametrize("hq,hkv,width,tried", [(16, 4, 2300, False), (24, 2, 4097, False), (24, 2, 4096, True)])
+def test_listed_calls_too_wide_for_groups(cuda_device, hq, hkv, width, tried):
+    """Lists so wide that few rows' fill the workspace: one by one, and groups are not even looked for."""
     rng = np.random.default_rng(9)
-    pool, table, lens, rows, lists, counts = alike(rng, [150], 3000, 16, 4, 128, 2300, 120, 73)
-    ws = sparse_workspace(16, 4, 128)
-    check_sparse(rng.standard_normal((150, 16, 128)), pool, table, lens, lists, counts, rows=rows, ws=ws)
-    assert not by_groups(ws, 16, 4, 128)
+    pool, table, lens, rows, lists, counts = alike(rng, [150], 3000, 16, hkv, 128, width, 40, 73)
+    ws = sparse_workspace(hq, hkv, 128)
+    check_sparse(rng.standard_normal((150, hq, 128)), pool, table, lens, lists, counts, rows=rows, ws=ws)
+    assert not by_groups(ws, hq, hkv, 128) and (decided(ws, hkv) == [0] * hkv) == tried
 
 
 # ---------------------------------------------------------------- scores
